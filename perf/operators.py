@@ -302,14 +302,14 @@ def run(st):
     case, op, out = st["case"], st["case"]["op"], st["out"]
     if op == "linear":
         q, s = moe.quantize_rows(st["x"])
-        return moe.gemm_i8(q, s, st["packed"], st["ws"], out=out)
+        return moe.gemm_quantized(q, s, st["packed"], st["ws"], out=out)
     p = moe.Spec(case["T"], case["d"], case["E"], case["k"], case.get("f", 8), 0, case["n"],
                  case.get("dtype", "bf16"))
     if op == "combine":
         return moe.combine_backward(p, st["dy"], st["yp"], st["inv"], st["w"], out=out)
     if op == "experts":
-        return moe.expert_gemm_i8(p, st["x"], st["offsets"], st["p1"], st["s1"], st["p3"], st["s3"],
-                                  st["p2"], st["s2"], out=out)
+        return moe.expert_gemm_quantized(p, st["x"], st["offsets"], st["p1"], st["s1"], st["p3"],
+                                         st["s3"], st["p2"], st["s2"], out=out)
     if op == "train":
         return moe.expert_gemm_train(p, st["x"], st["offsets"], st["w1"], st["w3"], st["w2"], out=out)
     return moe.expert_gemm_backward(p, st["x"], st["offsets"], st["w1"], st["w3"], st["w2"], st["g"],
