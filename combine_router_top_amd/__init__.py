@@ -17,6 +17,14 @@ Functions (same names as the C calls):
     layer_ws_offset(p, MOE_WS_H | MOE_WS_Y_PACKED) -> byte offset in the layer workspace
     dispatch_padded(p, capacity, topk_idx, x) -> dict(counts_all, offsets, perm, inv, x_packed)
     expert_gemm_padded(p, capacity, x_packed, offsets, w1, w3, w2) -> (h, y_packed)
+    expert_gemm_train(p, x_packed, offsets, w1, w3, w2) -> (g, u, h, y_packed)
+    expert_gemm_backward(p, x_packed, offsets, w1, w3, w2, g, u, h, dy_packed)
+        -> (dx_packed, dw1, dw3, dw2)
+    combine_backward(p, dy, y_packed, inv, topk_w) -> (dy_packed, dtopk_w)
+    quantize_rows(x) -> (q, scale)
+    pack_weights(w) -> packed;  quantize_weights(w) -> (packed, scale)   (w [n,K,N] or [K,N])
+    gemm_quantized(a, a_scale, packed, b_scale) -> C
+    expert_gemm_quantized(p, x_packed, offsets, w1, s1, w3, s3, w2, s2) -> (h, y_packed)
     gemm_signal(A, B, flags, epoch) -> C          (C = rnd(A B), a flag per 256 x 256 tile)
     tile_forward(C, dst, flags, epoch, spin_limit, timeouts, workgroups)
 """
@@ -36,12 +44,16 @@ MOE_F_WRITE_LOGITS, MOE_F_OVERLAP, MOE_F_FOLD_WEIGHT = 1, 2, 4
 MOE_WS_H, MOE_WS_Y_PACKED = 0, 1
 MOE_CALL_ROUTE, MOE_CALL_DISPATCH, MOE_CALL_EXPERT_GEMM, MOE_CALL_COMBINE, MOE_CALL_LAYER = range(5)
 MOE_CALL_DISPATCH_PADDED, MOE_CALL_EXPERT_GEMM_PADDED = 5, 6
+MOE_CALL_EXPERT_GEMM_TRAIN, MOE_CALL_EXPERT_GEMM_BACKWARD, MOE_CALL_EXPERT_GEMM_QUANTIZED = 7, 8, 9
 MOE_SCOPE_AGENT, MOE_SCOPE_SYSTEM = 0, 1
 
 EXPORTED = ["moe_last_error", "moe_version", "moe_workspace_bytes", "moe_route", "moe_dispatch",
             "moe_expert_gemm", "moe_combine", "moe_layer", "moe_dispatch_padded",
             "moe_expert_gemm_padded", "moe_gemm_signal_tiles", "moe_gemm_signal", "moe_tile_forward",
-            "moe_dispatch_noalloc", "moe_layer_ws_offset", "moe_layer_set_gemm_events"]
+            "moe_dispatch_noalloc", "moe_layer_ws_offset", "moe_layer_set_gemm_events",
+            "moe_expert_gemm_train", "moe_expert_gemm_backward", "moe_combine_backward",
+            "moe_quantize_rows", "moe_packed_weights_bytes", "moe_pack_weights",
+            "moe_quantize_weights", "moe_gemm_quantized", "moe_expert_gemm_quantized"]
 
 
 class MoeError(RuntimeError):
@@ -94,6 +106,21 @@ def lib() -> ctypes.CDLL:
         u32 = ctypes.c_uint32
         L.moe_gemm_signal.argtypes = [i32, i32, i32, vp, vp, vp, vp, u32, i32, vp]
         L.moe_tile_forward.argtypes = [i32, i32, vp, vp, vp, u32, u32, i32, vp, i32, vp]
+        i64 = ctypes.c_int64
+        L.moe_expert_gemm_train.argtypes = [P] + [vp] * 10 + [sz, vp]
+        L.moe_expert_gemm_backward.argtypes = [P] + [vp] * 14 + [sz, vp]
+        L.moe_combine_backward.argtypes = [P] + [vp] * 7
+        L.moe_quantize_rows.argtypes = [i64, i32, i32, vp, vp, vp, vp]
+        L.moe_packed_weights_bytes.argtypes = [i32, i32, i32]
+        L.moe_packed_weights_bytes.restype = sz
+        L.moe_pack_weights.argtypes = [i32, i32, i32, vp, vp, vp]
+        L.moe_quantize_weights.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_gemm_quantized.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i32, vp]
+        L.moe_expert_gemm_quantized.argtypes = [P] + [vp] * 11 + [sz, vp]
+        for n in ("moe_expert_gemm_train", "moe_expert_gemm_backward", "moe_combine_backward",
+                  "moe_quantize_rows", "moe_pack_weights", "moe_quantize_weights",
+                  "moe_gemm_quantized", "moe_expert_gemm_quantized"):
+            getattr(L, n).restype = i32
         for n in ("moe_route", "moe_dispatch", "moe_expert_gemm", "moe_combine", "moe_layer",
                   "moe_dispatch_padded", "moe_expert_gemm_padded", "moe_gemm_signal",
                   "moe_tile_forward", "moe_dispatch_noalloc"):
@@ -344,6 +371,208 @@ def expert_gemm_padded(p: Spec, capacity: int, x_packed, offsets, w1, w3, w2, wo
                                         _ptr(offsets), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(h),
                                         _ptr(yp), _ptr(ws), 0 if ws is None else ws.numel(),
                                         _stream(stream)))
+    return h, yp
+
+
+# ---------------------------------------------------------------------------
+# training
+# ---------------------------------------------------------------------------
+def expert_gemm_train(p: Spec, x_packed, offsets, w1, w3, w2, workspace=None, stream=None, out=None):
+    """``expert_gemm`` that also returns the unactivated products the backward
+    pass reads: (g, u, h, y_packed).  ``out``: these four, written in place."""
+    torch = _torch()
+    dt = _dt(p)
+    _need(x_packed, (p.rows_max, p.d), dt, "x_packed")
+    _need(offsets, (p.n_local + 1,), torch.int32, "offsets")
+    _need(w1, (p.n_local, p.d, p.f), dt, "w1")
+    _need(w3, (p.n_local, p.d, p.f), dt, "w3")
+    _need(w2, (p.n_local, p.f, p.d), dt, "w2")
+    dev = x_packed.device
+    if out is None:
+        out = tuple(torch.zeros((p.rows_max, n), dtype=dt, device=dev) for n in (p.f, p.f, p.f, p.d))
+    g, u, h, yp = out
+    for t, n, name in ((g, p.f, "g"), (u, p.f, "u"), (h, p.f, "h"), (yp, p.d, "y_packed")):
+        _need(t, (p.rows_max, n), dt, name)
+    ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_TRAIN, dev)
+    pc = p.c()
+    _check(lib().moe_expert_gemm_train(ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1),
+                                       _ptr(w3), _ptr(w2), _ptr(g), _ptr(u), _ptr(h), _ptr(yp),
+                                       _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    return g, u, h, yp
+
+
+def expert_gemm_backward(p: Spec, x_packed, offsets, w1, w3, w2, g, u, h, dy_packed, workspace=None,
+                         stream=None, out=None):
+    """Gradients (dx_packed, dw1, dw3, dw2) of ``expert_gemm_train``.  ``out``:
+    these four, written in place; a None among them is not computed."""
+    torch = _torch()
+    dt = _dt(p)
+    for t, n, name in ((x_packed, p.d, "x_packed"), (g, p.f, "g"), (u, p.f, "u"), (h, p.f, "h"),
+                       (dy_packed, p.d, "dy_packed")):
+        _need(t, (p.rows_max, n), dt, name)
+    _need(offsets, (p.n_local + 1,), torch.int32, "offsets")
+    _need(w1, (p.n_local, p.d, p.f), dt, "w1")
+    _need(w3, (p.n_local, p.d, p.f), dt, "w3")
+    _need(w2, (p.n_local, p.f, p.d), dt, "w2")
+    dev = x_packed.device
+    if out is None:
+        out = (torch.zeros((p.rows_max, p.d), dtype=dt, device=dev), torch.empty_like(w1),
+               torch.empty_like(w3), torch.empty_like(w2))
+    dx, dw1, dw3, dw2 = out
+    for t, shape, name in ((dx, (p.rows_max, p.d), "dx_packed"), (dw1, (p.n_local, p.d, p.f), "dw1"),
+                           (dw3, (p.n_local, p.d, p.f), "dw3"), (dw2, (p.n_local, p.f, p.d), "dw2")):
+        if t is not None:
+            _need(t, shape, dt, name)
+    ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_BACKWARD, dev)
+    pc = p.c()
+    _check(lib().moe_expert_gemm_backward(
+        ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(g), _ptr(u),
+        _ptr(h), _ptr(dy_packed), _ptr(dx), _ptr(dw1), _ptr(dw3), _ptr(dw2), _ptr(ws),
+        0 if ws is None else ws.numel(), _stream(stream)))
+    return dx, dw1, dw3, dw2
+
+
+def combine_backward(p: Spec, dy, y_packed, inv, topk_w, stream=None, out=None,
+                     rows: Optional[int] = None):
+    """Gradients (dy_packed, dtopk_w) of ``combine``.  ``rows`` as there;
+    ``topk_w=None``: unit weights.  ``out``: the two, written in place; with
+    dtopk_w None it is not computed and ``y_packed`` may be None."""
+    torch = _torch()
+    dt = _dt(p)
+    n = p.rows_max if rows is None else rows
+    _need(dy, (p.T, p.d), dt, "dy")
+    _need(inv, (p.T * p.k,), torch.int32, "inv")
+    if topk_w is not None:
+        _need(topk_w, (p.T, p.k), torch.float32, "topk_w")
+    if out is None:
+        out = (torch.zeros((n, p.d), dtype=dt, device=dy.device),
+               torch.empty((p.T, p.k), dtype=torch.float32, device=dy.device))
+    dyp, dw = out
+    _need(dyp, (n, p.d), dt, "dy_packed")
+    if dw is not None:
+        _need(dw, (p.T, p.k), torch.float32, "dtopk_w")
+    if dw is not None or y_packed is not None:
+        _need(y_packed, (n, p.d), dt, "y_packed")
+    pc = p.c()
+    _check(lib().moe_combine_backward(ctypes.byref(pc), _ptr(dy), _ptr(y_packed), _ptr(inv),
+                                      _ptr(topk_w), _ptr(dyp), _ptr(dw), _stream(stream)))
+    return dyp, dw
+
+
+# ---------------------------------------------------------------------------
+# 8-bit weights and activations
+# ---------------------------------------------------------------------------
+def _dtype_code(t, name):
+    torch = _torch()
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+    return MOE_DTYPE_BF16 if t.dtype == torch.bfloat16 else MOE_DTYPE_F32
+
+
+def quantize_rows(x, stream=None, out=None):
+    """(q int8, scale fp32) of the rows of x [rows, K] (bf16 or fp32):
+    scale = max|x| / 127, q = rint(x * (127 * (1 / max|x|)))."""
+    torch = _torch()
+    code = _dtype_code(x, "x")
+    rows, K = x.shape
+    _need(x, (rows, K), x.dtype, "x")
+    q, s = out if out is not None else (torch.empty((rows, K), dtype=torch.int8, device=x.device),
+                                        torch.empty(rows, dtype=torch.float32, device=x.device))
+    _need(q, (rows, K), torch.int8, "q")
+    _need(s, (rows,), torch.float32, "scale")
+    _check(lib().moe_quantize_rows(rows, K, code, _ptr(x), _ptr(q), _ptr(s), _stream(stream)))
+    return q, s
+
+
+def packed_weights_shape(K: int, N: int):
+    """Shape of one packed [K, N] matrix: (N/16, K/64, 4, 16, 16), rounded up."""
+    return (-(-N // 16), -(-K // 64), 4, 16, 16)
+
+
+def packed_weights_bytes(n: int, K: int, N: int) -> int:
+    b = int(lib().moe_packed_weights_bytes(int(n), int(K), int(N)))
+    if b == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, lib().moe_last_error().decode())
+    return b
+
+
+def _packed_out(w, out):
+    torch = _torch()
+    lead, K, N = tuple(w.shape[:-2]), w.shape[-2], w.shape[-1]
+    if len(lead) > 1:
+        raise ValueError(f"w: expected [n, K, N] or [K, N], got {tuple(w.shape)}")
+    n = lead[0] if lead else 1
+    packed_weights_bytes(n, K, N)
+    shape = lead + packed_weights_shape(K, N)
+    packed = torch.empty(shape, dtype=torch.int8, device=w.device) if out is None else out
+    return n, K, N, lead, _need(packed, shape, torch.int8, "packed")
+
+
+def pack_weights(w, stream=None, out=None):
+    """int8 weights [n, K, N] or [K, N] in the order the 8-bit products read."""
+    torch = _torch()
+    n, K, N, _, packed = _packed_out(w, out)
+    _need(w, tuple(w.shape), torch.int8, "w")
+    _check(lib().moe_pack_weights(n, K, N, _ptr(w), _ptr(packed), _stream(stream)))
+    return packed
+
+
+def quantize_weights(w, stream=None, out=None):
+    """(packed, scale) of bf16 or fp32 weights [n, K, N] or [K, N], one scale
+    per output channel."""
+    torch = _torch()
+    code = _dtype_code(w, "w")
+    n, K, N, lead, packed = _packed_out(w, None if out is None else out[0])
+    _need(w, tuple(w.shape), w.dtype, "w")
+    s = torch.empty(lead + (N,), dtype=torch.float32, device=w.device) if out is None else out[1]
+    _need(s, lead + (N,), torch.float32, "scale")
+    _check(lib().moe_quantize_weights(n, K, N, code, _ptr(w), _ptr(packed), _ptr(s), _stream(stream)))
+    return packed, s
+
+
+def gemm_quantized(a, a_scale, packed, b_scale, dtype=None, stream=None, out=None):
+    """C = rnd((a b) a_scale b_scale): int8 a [M, K], packed weights of one
+    [K, N] matrix, a scale per row and per output channel; ``dtype`` (default
+    torch.bfloat16, or that of ``out``) is C's."""
+    torch = _torch()
+    M, K = a.shape
+    N = b_scale.shape[0]
+    _need(a, (M, K), torch.int8, "a")
+    _need(a_scale, (M,), torch.float32, "a_scale")
+    _need(packed, packed_weights_shape(K, N), torch.int8, "packed")
+    _need(b_scale, (N,), torch.float32, "b_scale")
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
+    _need(out, (M, N), dtype or out.dtype, "out")
+    _check(lib().moe_gemm_quantized(M, N, K, _ptr(a), _ptr(a_scale), _ptr(packed), _ptr(b_scale),
+                                    _ptr(out), _dtype_code(out, "out"), _stream(stream)))
+    return out
+
+
+def expert_gemm_quantized(p: Spec, x_packed, offsets, w1, s1, w3, s3, w2, s2, workspace=None,
+                          stream=None, out=None):
+    """``expert_gemm`` with packed 8-bit weights [n_local, ...] and their channel
+    scales, and rows quantised on the way: (h, y_packed)."""
+    torch = _torch()
+    dt = _dt(p)
+    _need(x_packed, (p.rows_max, p.d), dt, "x_packed")
+    _need(offsets, (p.n_local + 1,), torch.int32, "offsets")
+    for w, s, K, N, name in ((w1, s1, p.d, p.f, "1"), (w3, s3, p.d, p.f, "3"), (w2, s2, p.f, p.d, "2")):
+        _need(w, (p.n_local,) + packed_weights_shape(K, N), torch.int8, "w" + name)
+        _need(s, (p.n_local, N), torch.float32, "s" + name)
+    dev = x_packed.device
+    if out is None:
+        out = (torch.zeros((p.rows_max, p.f), dtype=dt, device=dev),
+               torch.zeros((p.rows_max, p.d), dtype=dt, device=dev))
+    h, yp = out
+    _need(h, (p.rows_max, p.f), dt, "h")
+    _need(yp, (p.rows_max, p.d), dt, "y_packed")
+    ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_QUANTIZED, dev)
+    pc = p.c()
+    _check(lib().moe_expert_gemm_quantized(
+        ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1), _ptr(s1), _ptr(w3), _ptr(s3),
+        _ptr(w2), _ptr(s2), _ptr(h), _ptr(yp), _ptr(ws), 0 if ws is None else ws.numel(),
+        _stream(stream)))
     return h, yp
 
 

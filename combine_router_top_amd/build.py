@@ -21,7 +21,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 ARCH = "gfx950"
 
-SOURCES = ["route.hip", "dispatch.hip", "expert_gemm.hip", "combine.hip", "tile_forward.hip", "moe_api.cpp"]
+SOURCES = ["route.hip", "dispatch.hip", "expert_gemm.hip", "combine.hip", "tile_forward.hip",
+           "expert_backward.hip", "expert_i8.hip", "moe_api.cpp"]
 # measurement-only streaming-read probe, linked into a library of its own
 PROBE_SOURCE = "hbm_read_probe.hip"
 PROBE_LIB = os.path.join(PKG, "libhbm_probe.so")

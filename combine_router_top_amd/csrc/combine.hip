@@ -120,4 +120,122 @@ hipError_t launch_combine(const Prob& p, const void* y_packed, const int32_t* in
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Backward pass of combine: for every local slot a = t k + j with row p = inv[a],
+//   dy_packed[p] = rnd(w[a] dy[t])      dw[a] = <dy[t], y_packed[p]>
+// and dw[a] = 0 for the others.  The inner product is summed in fp32: pairwise
+// over the lanes of a wave, in a fixed order over waves and chunks.
+//
+// One workgroup per token holds a chunk of dy[t] (up to CBB_U 16-byte pieces
+// per thread) in registers and walks the token's local slots: each row of
+// y_packed is read once, each row of dy_packed written once, dy[t] read once;
+// a token without local slots reads nothing.  Bound by those bytes, and by
+// latency for a few tokens.
+// ---------------------------------------------------------------------------
+constexpr int CBB_U = 4;
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const u32x4* __restrict__ dy,
+                                                               const u32x4* __restrict__ yp,
+                                                               const int32_t* __restrict__ inv,
+                                                               const float* __restrict__ w,
+                                                               u32x4* __restrict__ dyp, float* __restrict__ dw, int k,
+                                                               int nvec) {
+  __shared__ int s_row[32], s_slot[32];
+  __shared__ float s_w[32], s_dot[4][32];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  if (wave == 0) {
+    int row = -1;
+    float wt = 0.f;
+    if (lane < k) {
+      row = inv[t * k + lane];
+      wt = w ? w[t * k + lane] : 1.0f;
+      if (dw && row < 0) dw[t * k + lane] = 0.f;
+    }
+    const uint64_t valid = __ballot(row >= 0);
+    if (row >= 0) {
+      const int at = __popcll(valid & lanemask_lt());
+      s_row[at] = row;
+      s_w[at] = wt;
+      s_slot[at] = lane;
+    }
+    if (lane < 32) {
+      s_dot[0][lane] = s_dot[1][lane] = s_dot[2][lane] = s_dot[3][lane] = 0.f;
+      if (lane >= __popcll(valid)) s_row[lane] = -1;
+    }
+  }
+  __syncthreads();
+  constexpr int NQ = BF16 ? 8 : 4;
+  for (int c0 = 0; c0 < nvec; c0 += 256 * CBB_U) {
+    if (s_row[0] < 0) return;   // no local slot (uniform)
+    float g[CBB_U][NQ];
+#pragma unroll
+    for (int u = 0; u < CBB_U; ++u) {
+      const int v = c0 + threadIdx.x + 256 * u;
+      const u32x4 x = v < nvec ? dy[t * nvec + v] : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (BF16) {
+          g[u][2 * q] = bf16_lo(x[q]);
+          g[u][2 * q + 1] = bf16_hi(x[q]);
+        } else {
+          g[u][q] = __uint_as_float(x[q]);
+        }
+      }
+    }
+    for (int j = 0; j < k; ++j) {
+      const int64_t row = s_row[j];
+      if (row < 0) break;
+      const float wt = s_w[j];
+      u32x4 val[CBB_U];
+#pragma unroll
+      for (int u = 0; u < CBB_U; ++u) {
+        const int v = c0 + threadIdx.x + 256 * u;
+        val[u] = dw && v < nvec ? yp[row * nvec + v] : u32x4{0u, 0u, 0u, 0u};
+      }
+      float dot = 0.f;
+#pragma unroll
+      for (int u = 0; u < CBB_U; ++u) {
+        const int v = c0 + threadIdx.x + 256 * u;
+        u32x4 o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (BF16) {
+            dot = fmaf(g[u][2 * q], bf16_lo(val[u][q]), dot);
+            dot = fmaf(g[u][2 * q + 1], bf16_hi(val[u][q]), dot);
+            o[q] = pack_bf16x2(wt * g[u][2 * q], wt * g[u][2 * q + 1]);
+          } else {
+            dot = fmaf(g[u][q], __uint_as_float(val[u][q]), dot);
+            o[q] = __float_as_uint(wt * g[u][q]);
+          }
+        }
+        if (v < nvec) dyp[row * nvec + v] = o;
+      }
+      if (dw) {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
+        if (lane == 0) s_dot[wave][j] += dot;
+      }
+    }
+  }
+  if (!dw) return;
+  __syncthreads();
+  if (threadIdx.x < 32 && s_row[threadIdx.x] >= 0)
+    dw[t * k + s_slot[threadIdx.x]] =
+        (s_dot[0][threadIdx.x] + s_dot[1][threadIdx.x]) + (s_dot[2][threadIdx.x] + s_dot[3][threadIdx.x]);
+}
+
+hipError_t launch_combine_backward(const Prob& p, const void* dy, const void* y_packed, const int32_t* inv,
+                                   const float* w, void* dy_packed, float* dw, hipStream_t st) {
+  const int nvec = (int)((int64_t)p.d * p.elem() / 16);
+  if (p.dtype == 1)
+    hipLaunchKernelGGL(combine_backward_kernel<true>, dim3((unsigned)p.T), dim3(256), 0, st, (const u32x4*)dy,
+                       (const u32x4*)y_packed, inv, w, (u32x4*)dy_packed, dw, p.k, nvec);
+  else
+    hipLaunchKernelGGL(combine_backward_kernel<false>, dim3((unsigned)p.T), dim3(256), 0, st, (const u32x4*)dy,
+                       (const u32x4*)y_packed, inv, w, (u32x4*)dy_packed, dw, p.k, nvec);
+  return hipGetLastError();
+}
+
 }  // namespace moe

@@ -1,0 +1,466 @@
+// Backward pass of the SwiGLU expert FFNs over expert-contiguous segments.  For
+// the rows R of expert e, with g = x W1, u = x W3, h = SiLU(g) u as the forward
+// pass kept them and s = 1 / (1 + exp(-g)):
+//
+//   dh    = dy W2^T                           (fp32, never stored)
+//   dg    = rnd(dh u s (1 + g (1 - s)))       du = rnd(dh g s)
+//   dx    = rnd(dg W1^T + du W3^T)            (one fp32 sum over both products)
+//   dW1_e = rnd(x^T dg), dW3_e = rnd(x^T du), dW2_e = rnd(h^T dy)
+//
+// Three launches: the gate gradient (dh with its epilogue), the input gradient,
+// and all weight gradients.  The one rounding inside is that of dg and du to
+// the storage type, which the matrix cores need of their operands: it costs
+// 2^-9 relative once per value, as the rounding of h does in the forward pass.
+// Every other sum stays in fp32.
+//
+// bf16: tiles of seg_tile.h.  The first two products contract over a dimension
+// that both operands hold contiguously (dy and rows of W2; dg and rows of W1),
+// the weight gradients over a segment's rows, which neither does: there both
+// operands are read as panels and transposed by the LDS read.  No operand is
+// ever transposed in memory.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "common.h"
+#include "kernels.h"
+#include "seg_tile.h"
+
+namespace moe {
+
+// d/dg and d/du of SiLU(g) u, times dh.  The hardware exponential and
+// reciprocal as in silu_mul; both limits of g are exact (s = 0 or 1).
+__device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& dg, float& du) {
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
+  dg = dh * u * (s * fmaf(g, 1.0f - s, 1.0f));
+  du = dh * (g * s);
+}
+
+__device__ __forceinline__ u32x2 pack_bf16x4(float a, float b, float c, float d) {
+  return u32x2{pack_bf16x2(a, b), pack_bf16x2(c, d)};
+}
+
+template <int MT, bool KT>
+using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, KT>;
+template <int MT, bool KT>
+using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, KT>;
+using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, false>;
+
+// dh tiles: rows of dy against rows of W2 (its f rows are the output columns).
+template <int MT, bool KT>
+__global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restrict__ dy,
+                                                           const int32_t* __restrict__ offsets, int n,
+                                                           const bf16_t* __restrict__ w2,
+                                                           const bf16_t* __restrict__ g,
+                                                           const bf16_t* __restrict__ u,
+                                                           bf16_t* __restrict__ dg, bf16_t* __restrict__ du,
+                                                           int d, int f, int ntn) {
+  using Cfg = GateCfg<MT, KT>;
+  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
+  __shared__ int pre[ST_MAXN + 1];
+  const int total = st_prefix(offsets, n, Cfg::BM, pre) * ntn;
+  const StRange rg = st_range(total, blockIdx.x, gridDim.x);
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 3, wn = wave >> 2;
+  for (int L = rg.begin; L < rg.end; L += rg.step) {
+    const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+    StCtx<Cfg> c;
+    st_setup(c, ring);
+    st_rows<Cfg::BM>(c.a[0], dy + (int64_t)t.r0 * d, (uint32_t)d * 2, t.R, (uint32_t)d * 2);
+    st_rows<ST_BN>(c.b[0], w2 + ((int64_t)t.e * f + 256 * t.nt) * d, (uint32_t)d * 2,
+                   min(ST_BN, f - 256 * t.nt), (uint32_t)d * 2);
+    c.nst = c.nst1 = (d + 31) / 32;
+    c.kvals = d;
+    f32x4 acc[MT][8];
+    st_clear<Cfg>(acc);
+    st_accum(c, ring, acc);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int row = 16 * MT * wm + 16 * mt + i;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int col = 256 * t.nt + 128 * wn + 16 * k + 4 * q;
+        if (row < t.R && col < f) {
+          const int64_t at = (int64_t)(t.r0 + row) * f + col;
+          const u32x2 gv = *reinterpret_cast<const u32x2*>(g + at);
+          const u32x2 uv = *reinterpret_cast<const u32x2*>(u + at);
+          float og[4], ou[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float gf = r & 1 ? bf16_hi(gv[r >> 1]) : bf16_lo(gv[r >> 1]);
+            const float uf = r & 1 ? bf16_hi(uv[r >> 1]) : bf16_lo(uv[r >> 1]);
+            swiglu_grad(acc[mt][k][r], gf, uf, og[r], ou[r]);
+          }
+          *reinterpret_cast<u32x2*>(dg + at) = pack_bf16x4(og[0], og[1], og[2], og[3]);
+          *reinterpret_cast<u32x2*>(du + at) = pack_bf16x4(ou[0], ou[1], ou[2], ou[3]);
+        }
+      }
+    }
+    // the next tile's copies are counted together with these stores, and its
+    // first copies overwrite slots that other waves may still read
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  }
+}
+
+// dx tiles: [dg | du] against rows of W1, then of W3, in one accumulator.
+template <int MT, bool KT>
+__global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __restrict__ dg,
+                                                            const bf16_t* __restrict__ du,
+                                                            const int32_t* __restrict__ offsets, int n,
+                                                            const bf16_t* __restrict__ w1,
+                                                            const bf16_t* __restrict__ w3,
+                                                            bf16_t* __restrict__ dx, int d, int f, int ntn) {
+  using Cfg = InputCfg<MT, KT>;
+  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
+  __shared__ int pre[ST_MAXN + 1];
+  const int total = st_prefix(offsets, n, Cfg::BM, pre) * ntn;
+  const StRange rg = st_range(total, blockIdx.x, gridDim.x);
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 3, wn = wave >> 2;
+  for (int L = rg.begin; L < rg.end; L += rg.step) {
+    const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+    StCtx<Cfg> c;
+    st_setup(c, ring);
+    const uint32_t ld = (uint32_t)f * 2;
+    const int64_t arow = (int64_t)t.r0 * f, brow = ((int64_t)t.e * d + 256 * t.nt) * f;
+    const int cols = min(ST_BN, d - 256 * t.nt);
+    st_rows<Cfg::BM>(c.a[0], dg + arow, ld, t.R, ld);
+    st_rows<Cfg::BM>(c.a[1], du + arow, ld, t.R, ld);
+    st_rows<ST_BN>(c.b[0], w1 + brow, ld, cols, ld);
+    st_rows<ST_BN>(c.b[1], w3 + brow, ld, cols, ld);
+    c.nst1 = (f + 31) / 32;
+    c.nst = 2 * c.nst1;
+    c.kvals = f;
+    f32x4 acc[MT][8];
+    st_clear<Cfg>(acc);
+    st_accum(c, ring, acc);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int row = 16 * MT * wm + 16 * mt + i;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int col = 256 * t.nt + 128 * wn + 16 * k + 4 * q;
+        if (row < t.R && col < d)
+          *reinterpret_cast<u32x2*>(dx + (int64_t)(t.r0 + row) * d + col) =
+              pack_bf16x4(acc[mt][k][0], acc[mt][k][1], acc[mt][k][2], acc[mt][k][3]);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  }
+}
+
+// One weight gradient C_e [M][N] = P^T Q over the segment's rows, P [rows][M],
+// Q [rows][N]; C NULL: not wanted.
+struct WeightGrad {
+  const bf16_t* P;
+  const bf16_t* Q;
+  bf16_t* C;
+  int M, N;
+};
+struct WeightGrads {
+  WeightGrad m[3];
+};
+
+// All tiles of all wanted weight gradients, expert by expert; a segment without
+// rows gives zeros.
+__global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int nm,
+                                                             const int32_t* __restrict__ offsets, int n) {
+  using Cfg = WeightCfg;
+  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
+  int tiles[3], per = 0;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    tiles[k] = k < nm ? ((w.m[k].M + 255) / 256) * ((w.m[k].N + 255) / 256) : 0;
+    per += tiles[k];
+  }
+  const StRange rg = st_range(n * per, blockIdx.x, gridDim.x);
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 3, wn = wave >> 2;
+  for (int L = rg.begin; L < rg.end; L += rg.step) {
+    const int e = L / per;
+    int at = L - e * per;
+    WeightGrad m = w.m[0];
+    if (at >= tiles[0]) {
+      at -= tiles[0];
+      m = w.m[1];
+      if (at >= tiles[1]) {
+        at -= tiles[1];
+        m = w.m[2];
+      }
+    }
+    // groups of 8 row tiles run through the column tiles together
+    const int nmt = (m.M + 255) / 256, nnt = (m.N + 255) / 256;
+    const int mg = at / (ST_GM * nnt), rem = at - mg * ST_GM * nnt;
+    const int gsz = min(ST_GM, nmt - mg * ST_GM);
+    const int tn = rem / gsz, tm = mg * ST_GM + (rem - tn * gsz);
+    const int o = offsets[e], cnt = offsets[e + 1] - o;
+    f32x4 acc[4][8];
+    st_clear<Cfg>(acc);
+    const uint32_t la = (uint32_t)m.M * 2, lb = (uint32_t)m.N * 2;
+    // 32-bit descriptors: rows in chunks of at most 2 GiB of the wider operand
+    const int chunk = (int)min((uint32_t)cnt, (0x7FFFFFFFu / max(la, lb)) & ~31u);
+    for (int k0 = 0; k0 < cnt; k0 += chunk) {
+      StCtx<Cfg> c;
+      st_setup(c, ring);
+      const int rows = min(chunk, cnt - k0);
+      st_panel<256>(c.a[0], m.P + (int64_t)(o + k0) * m.M, la, rows, 256 * tm, m.M);
+      st_panel<256>(c.b[0], m.Q + (int64_t)(o + k0) * m.N, lb, rows, 256 * tn, m.N);
+      c.nst = c.nst1 = (rows + 31) / 32;
+      c.kvals = rows;
+      st_accum(c, ring, acc);
+      __syncthreads();
+    }
+    bf16_t* C = m.C + (int64_t)e * m.M * m.N;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      const int row = 256 * tm + 64 * wm + 16 * mt + i;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int col = 256 * tn + 128 * wn + 16 * k + 4 * q;
+        if (row < m.M && col < m.N)
+          *reinterpret_cast<u32x2*>(C + (int64_t)row * m.N + col) =
+              pack_bf16x4(acc[mt][k][0], acc[mt][k][1], acc[mt][k][2], acc[mt][k][3]);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32: 64 x 64 tiles of 256 threads, 4 x 4 values each, K in steps of 16
+// through LDS, the next step's operands loaded while one is multiplied.  For
+// the small fp32 problems only.
+// ---------------------------------------------------------------------------
+constexpr int F_K = 16, F_LD = 68;
+
+// acc[a][b] += sum_k A(k, 4 ty + a) B(k, 4 tx + b) over k < K; A and B give 0
+// outside their operand and are called with tile indices 0 .. 63.
+template <class FA, class FB>
+__device__ __forceinline__ void f32_tile(const FA& A, bool a_kfast, const FB& B, bool b_kfast, int K, float* sa,
+                                         float* sb, float (&acc)[4][4]) {
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  float ra[4], rb[4];
+  // element v of a thread: (k, j) with the operand's contiguous index fastest over threads
+  auto ka = [&](int v) { return a_kfast ? tid & 15 : (tid >> 6) + 4 * v; };
+  auto ja = [&](int v) { return a_kfast ? (tid >> 4) + 16 * v : tid & 63; };
+  auto kb = [&](int v) { return b_kfast ? tid & 15 : (tid >> 6) + 4 * v; };
+  auto jb = [&](int v) { return b_kfast ? (tid >> 4) + 16 * v : tid & 63; };
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      ra[v] = k0 + ka(v) < K ? A(k0 + ka(v), ja(v)) : 0.f;
+      rb[v] = k0 + kb(v) < K ? B(k0 + kb(v), jb(v)) : 0.f;
+    }
+  };
+  load(0);
+  for (int k0 = 0; k0 < K; k0 += F_K) {
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      sa[ka(v) * F_LD + ja(v)] = ra[v];
+      sb[kb(v) * F_LD + jb(v)] = rb[v];
+    }
+    __syncthreads();
+    if (k0 + F_K < K) load(k0 + F_K);
+#pragma unroll
+    for (int k = 0; k < F_K; ++k) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(sa + k * F_LD + 4 * ty);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(sb + k * F_LD + 4 * tx);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[p][r] = fmaf(a[p], b[r], acc[p][r]);
+    }
+  }
+}
+
+// Row block of a 64-row tile grid: block b of the prefix over ceil(rows / 64).
+__device__ __forceinline__ bool f32_row_block(const int32_t* offsets, int n, int b, int* pre, StTile& t) {
+  const int total = st_prefix(offsets, n, 64, pre);
+  if (b >= total) return false;
+  t = st_tile_at(b, offsets, n, 1, 64, pre);
+  return true;
+}
+
+__global__ __launch_bounds__(256) void gate_grad_f32(const float* __restrict__ dy, const int32_t* __restrict__ offsets,
+                                                     int n, const float* __restrict__ w2, const float* __restrict__ g,
+                                                     const float* __restrict__ u, float* __restrict__ dg,
+                                                     float* __restrict__ du, int d, int f) {
+  __shared__ __attribute__((aligned(16))) float sa[F_K * F_LD], sb[F_K * F_LD];
+  __shared__ int pre[ST_MAXN + 1];
+  StTile t;
+  if (!f32_row_block(offsets, n, blockIdx.x, pre, t)) return;
+  const int c0 = blockIdx.y * 64;
+  const float* a = dy + (int64_t)t.r0 * d;
+  const float* b = w2 + (int64_t)t.e * f * d;
+  float acc[4][4] = {};
+  f32_tile([&](int k, int j) { return j < t.R ? a[(int64_t)j * d + k] : 0.f; }, true,
+           [&](int k, int j) { return c0 + j < f ? b[(int64_t)(c0 + j) * d + k] : 0.f; }, true, d, sa, sb, acc);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  for (int p = 0; p < 4; ++p)
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * ty + p, col = c0 + 4 * tx + r;
+      if (row >= t.R || col >= f) continue;
+      const int64_t at = (int64_t)(t.r0 + row) * f + col;
+      const float gv = g[at], s = 1.0f / (1.0f + expf(-gv));
+      dg[at] = acc[p][r] * u[at] * (s * (1.0f + gv * (1.0f - s)));
+      du[at] = acc[p][r] * (gv * s);
+    }
+}
+
+__global__ __launch_bounds__(256) void input_grad_f32(const float* __restrict__ dg, const float* __restrict__ du,
+                                                      const int32_t* __restrict__ offsets, int n,
+                                                      const float* __restrict__ w1, const float* __restrict__ w3,
+                                                      float* __restrict__ dx, int d, int f) {
+  __shared__ __attribute__((aligned(16))) float sa[F_K * F_LD], sb[F_K * F_LD];
+  __shared__ int pre[ST_MAXN + 1];
+  StTile t;
+  if (!f32_row_block(offsets, n, blockIdx.x, pre, t)) return;
+  const int c0 = blockIdx.y * 64;
+  float acc[4][4] = {};
+  for (int half = 0; half < 2; ++half) {
+    const float* a = (half ? du : dg) + (int64_t)t.r0 * f;
+    const float* b = (half ? w3 : w1) + (int64_t)t.e * d * f;
+    f32_tile([&](int k, int j) { return j < t.R ? a[(int64_t)j * f + k] : 0.f; }, true,
+             [&](int k, int j) { return c0 + j < d ? b[(int64_t)(c0 + j) * f + k] : 0.f; }, true, f, sa, sb, acc);
+  }
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  for (int p = 0; p < 4; ++p)
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * ty + p, col = c0 + 4 * tx + r;
+      if (row < t.R && col < d) dx[(int64_t)(t.r0 + row) * d + col] = acc[p][r];
+    }
+}
+
+// C_e [M][N] = P^T Q over the segment's rows; blockIdx.z is the expert.
+__global__ __launch_bounds__(256) void weight_grad_f32(const float* __restrict__ P, const float* __restrict__ Q,
+                                                       float* __restrict__ C, int M, int N,
+                                                       const int32_t* __restrict__ offsets) {
+  __shared__ __attribute__((aligned(16))) float sa[F_K * F_LD], sb[F_K * F_LD];
+  const int e = blockIdx.z, o = offsets[e], cnt = offsets[e + 1] - o;
+  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
+  const float* a = P + (int64_t)o * M;
+  const float* b = Q + (int64_t)o * N;
+  float acc[4][4] = {};
+  if (cnt > 0)
+    f32_tile([&](int k, int j) { return m0 + j < M ? a[(int64_t)k * M + m0 + j] : 0.f; }, false,
+             [&](int k, int j) { return n0 + j < N ? b[(int64_t)k * N + n0 + j] : 0.f; }, false, cnt, sa, sb, acc);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  for (int p = 0; p < 4; ++p)
+    for (int r = 0; r < 4; ++r) {
+      const int row = m0 + 4 * ty + p, col = n0 + 4 * tx + r;
+      if (row < M && col < N) C[((int64_t)e * M + row) * N + col] = acc[p][r];
+    }
+}
+
+// Zeros (the weight gradients of an empty batch): a kernel, so that a captured
+// call holds no memset node.
+__global__ __launch_bounds__(256) void fill_zero(u32x4* __restrict__ p, int64_t n16) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256)
+    p[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+size_t expert_backward_ws_bytes(const Prob& p) {
+  // dg and du, [rows_max, f] each
+  return 2 * (((size_t)p.rows_max * p.f * p.elem() + 255) / 256 * 256);
+}
+
+hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* offsets, const void* w1,
+                                  const void* w3, const void* w2, const void* g, const void* u, const void* h,
+                                  const void* dy, void* dx, void* dw1, void* dw3, void* dw2, void* ws,
+                                  hipStream_t st) {
+  hipError_t e;
+  if (p.T == 0) {
+    const int64_t n16 = (int64_t)p.n * p.d * p.f * p.elem() / 16;
+    for (void* w : {dw1, dw3, dw2}) {
+      if (!w) continue;
+      hipLaunchKernelGGL(fill_zero, dim3((unsigned)std::min<int64_t>((n16 + 255) / 256, 2048)), dim3(256), 0, st,
+                         (u32x4*)w, n16);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  char* dgp = (char*)ws;
+  char* dup = dgp + expert_backward_ws_bytes(p) / 2;
+  const bool gate = dx || dw1 || dw3;
+  if (p.dtype != 1) {
+    const unsigned rb = (unsigned)std::min<int64_t>((p.rows_max + 63) / 64 + p.n, p.rows_max);
+    const unsigned cf = (unsigned)((p.f + 63) / 64), cd = (unsigned)((p.d + 63) / 64);
+    if (gate) {
+      hipLaunchKernelGGL(gate_grad_f32, dim3(rb, cf), dim3(256), 0, st, (const float*)dy, offsets, p.n,
+                         (const float*)w2, (const float*)g, (const float*)u, (float*)dgp, (float*)dup, p.d, p.f);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (dx) {
+      hipLaunchKernelGGL(input_grad_f32, dim3(rb, cd), dim3(256), 0, st, (const float*)dgp, (const float*)dup, offsets,
+                         p.n, (const float*)w1, (const float*)w3, (float*)dx, p.d, p.f);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const struct { const void *P, *Q; void* C; int M, N; } m[3] = {
+        {x, dgp, dw1, p.d, p.f}, {x, dup, dw3, p.d, p.f}, {h, dy, dw2, p.f, p.d}};
+    for (const auto& k : m) {
+      if (!k.C) continue;
+      hipLaunchKernelGGL(weight_grad_f32, dim3((k.M + 63) / 64, (k.N + 63) / 64, p.n), dim3(256), 0, st,
+                         (const float*)k.P, (const float*)k.Q, (float*)k.C, k.M, k.N, offsets);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  // one workgroup per compute unit walks its share of the tiles
+  const int cus = device_cus();
+  auto row_grid = [&](int bm, int ntn) {
+    const int64_t blocks = std::min<int64_t>(p.rows_max / bm + std::min<int64_t>(p.n, p.rows_max), p.rows_max);
+    return dim3((unsigned)std::min<int64_t>(blocks * ntn, cus));
+  };
+  // 256-row tiles where the mean segment fills them, else 128-row tiles
+  const bool tall = p.tk() / p.E >= 192;
+  const bf16_t* DG = (const bf16_t*)dgp;
+  const bf16_t* DU = (const bf16_t*)dup;
+  if (gate) {
+    const int ntn = (p.f + 255) / 256;
+    auto go = [&](auto kernel, int bm) {
+      hipLaunchKernelGGL(kernel, row_grid(bm, ntn), dim3(ST_NT), 0, st, (const bf16_t*)dy, offsets, p.n,
+                         (const bf16_t*)w2, (const bf16_t*)g, (const bf16_t*)u, (bf16_t*)dgp, (bf16_t*)dup, p.d, p.f,
+                         ntn);
+      return hipGetLastError();
+    };
+    if (p.d % 32 == 0) e = tall ? go(gate_grad_bf16<4, false>, 256) : go(gate_grad_bf16<2, false>, 128);
+    else e = tall ? go(gate_grad_bf16<4, true>, 256) : go(gate_grad_bf16<2, true>, 128);
+    if (e != hipSuccess) return e;
+  }
+  if (dx) {
+    const int ntn = (p.d + 255) / 256;
+    auto go = [&](auto kernel, int bm) {
+      hipLaunchKernelGGL(kernel, row_grid(bm, ntn), dim3(ST_NT), 0, st, DG, DU, offsets, p.n, (const bf16_t*)w1,
+                         (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn);
+      return hipGetLastError();
+    };
+    if (p.f % 32 == 0) e = tall ? go(input_grad_bf16<4, false>, 256) : go(input_grad_bf16<2, false>, 128);
+    else e = tall ? go(input_grad_bf16<4, true>, 256) : go(input_grad_bf16<2, true>, 128);
+    if (e != hipSuccess) return e;
+  }
+  WeightGrads w{};
+  int nm = 0;
+  int64_t tiles = 0;
+  auto want = [&](const void* P, const void* Q, void* C, int M, int N) {
+    if (!C) return;
+    w.m[nm++] = WeightGrad{(const bf16_t*)P, (const bf16_t*)Q, (bf16_t*)C, M, N};
+    tiles += (int64_t)((M + 255) / 256) * ((N + 255) / 256) * p.n;
+  };
+  want(h, dy, dw2, p.f, p.d);
+  want(x, DG, dw1, p.d, p.f);
+  want(x, DU, dw3, p.d, p.f);
+  if (nm) {
+    hipLaunchKernelGGL(weight_grad_bf16, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(ST_NT), 0, st, w, nm, offsets,
+                       p.n);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

@@ -58,6 +58,10 @@ hipError_t launch_expert_gemm(const Prob& p, const void* x_packed, const int32_t
                               const void* w1, const void* w3, const void* w2, void* h,
                               void* y_packed, void* ws, int e_begin, int e_end, hipStream_t st,
                               const int32_t* perm = nullptr, const float* rscale = nullptr);
+// The same, keeping g = rnd(x W1) and u = rnd(x W3) for the backward pass.
+hipError_t launch_expert_gemm_train(const Prob& p, const void* x_packed, const int32_t* offsets,
+                                    const void* w1, const void* w3, const void* w2, void* g, void* u,
+                                    void* h, void* y_packed, void* ws, hipStream_t st);
 
 // expert_gemm.hip: GEMM C = rnd(A B) with a release flag per 256 x 256 tile
 int64_t gemm_signal_tiles(int M, int N);
@@ -71,5 +75,35 @@ hipError_t launch_tile_forward(int M, int N, const void* C, void* dst, const uin
 // combine.hip
 hipError_t launch_combine(const Prob& p, const void* y_packed, const int32_t* inv,
                           const float* w, void* y, hipStream_t st);
+
+// Backward pass of combine; w NULL: unit weights, dw NULL: not wanted (then
+// y_packed is not read).
+hipError_t launch_combine_backward(const Prob& p, const void* dy, const void* y_packed, const int32_t* inv,
+                                   const float* w, void* dy_packed, float* dw, hipStream_t st);
+
+// Compute units of the current device.
+int device_cus();
+
+// expert_backward.hip: gradients of the expert FFNs (any output may be NULL).
+// T = 0 writes zeros to the wanted weight gradients.
+size_t expert_backward_ws_bytes(const Prob& p);
+hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* offsets, const void* w1,
+                                  const void* w3, const void* w2, const void* g, const void* u, const void* h,
+                                  const void* dy, void* dx, void* dw1, void* dw3, void* dw2, void* ws, hipStream_t st);
+
+// expert_i8.hip: 8-bit products.  Rows of x (dtype 0 fp32, 1 bf16) to int8 rows
+// of ldq bytes and a scale each; limit (or NULL): device row count.
+hipError_t launch_quantize_rows(const void* x, int dtype, int64_t rows, int K, int64_t ldq, void* q, float* s,
+                                const int32_t* limit, hipStream_t st);
+size_t packed_i8_bytes(int n, int K, int N);
+hipError_t launch_pack_i8(int n, int K, int N, const void* w, void* packed, hipStream_t st);
+hipError_t launch_quantize_weights(int n, int K, int N, int dtype, const void* w, void* packed, float* s,
+                                   hipStream_t st);
+hipError_t launch_gemm_i8(int M, int N, int K, const void* a, const float* sa, const void* packed, const float* sb,
+                          void* c, int out_dtype, hipStream_t st);
+size_t expert_i8_ws_bytes(const Prob& p);
+hipError_t launch_expert_i8(const Prob& p, const void* x, const int32_t* offsets, const void* q1, const float* s1,
+                            const void* q3, const float* s3, const void* q2, const float* s2, void* h, void* y,
+                            void* ws, hipStream_t st);
 
 }  // namespace moe

@@ -121,7 +121,10 @@ size_t call_ws_bytes(const moe::Prob& p, int32_t call) {
     case MOE_CALL_COMBINE: return 0;
     case MOE_CALL_LAYER: return layer_ws(p).total;
     case MOE_CALL_DISPATCH_PADDED: return moe::dispatch_padded_ws_bytes(p);
-    case MOE_CALL_EXPERT_GEMM_PADDED: return moe::expert_gemm_ws_bytes(p);
+    case MOE_CALL_EXPERT_GEMM_PADDED:
+    case MOE_CALL_EXPERT_GEMM_TRAIN: return moe::expert_gemm_ws_bytes(p);
+    case MOE_CALL_EXPERT_GEMM_BACKWARD: return moe::expert_backward_ws_bytes(p);
+    case MOE_CALL_EXPERT_GEMM_QUANTIZED: return moe::expert_i8_ws_bytes(p);
     default: return 0;
   }
 }
@@ -160,6 +163,36 @@ moe_status_t check_signal_shape(int32_t M, int32_t N, int32_t K) {
   if ((int64_t)K * N * 2 >= ((int64_t)1 << 31) || (int64_t)256 * K * 2 >= ((int64_t)1 << 32) ||
       (int64_t)M * N >= ((int64_t)1 << 40))
     return fail(MOE_ERR_UNSUPPORTED, "GEMM too large (M=%d N=%d K=%d)", M, N, K);
+  return MOE_OK;
+}
+
+// The backward pass addresses up to 256 rows of d or f elements, and a 2 GiB
+// run of rows in steps of 32, with 32-bit offsets.
+moe_status_t check_backward_widths(const moe::Prob& q) {
+  const int32_t lim = 1 << 21;
+  if (q.d > lim || q.f > lim)
+    return fail(MOE_ERR_UNSUPPORTED, "d=%d and f=%d must be at most %d", q.d, q.f, lim);
+  return MOE_OK;
+}
+
+// Widths of the 8-bit products: K below 131072 keeps every int32 sum exact
+// (131071 products of at most 128 * 128).
+constexpr int32_t kMaxQuantK = 131072;
+
+moe_status_t check_packed(int32_t n, int32_t K, int32_t N) {
+  if (n <= 0 || K <= 0 || N <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "n=%d K=%d N=%d must be positive", n, K, N);
+  if (n > 1024) return fail(MOE_ERR_UNSUPPORTED, "n=%d > 1024 not supported", n);
+  if (K >= kMaxQuantK) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be below %d", K, kMaxQuantK);
+  if (N % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "N=%d must be a multiple of 8", N);
+  if ((int64_t)K * N >= ((int64_t)1 << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "a weight matrix exceeds 2 GiB (K=%d N=%d)", K, N);
+  return MOE_OK;
+}
+
+moe_status_t check_dtype(int32_t dtype) {
+  if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "dtype %d not supported", dtype);
   return MOE_OK;
 }
 
@@ -226,7 +259,7 @@ size_t moe_layer_ws_offset(const moe_problem_t* p, int32_t what) {
 size_t moe_workspace_bytes(const moe_problem_t* p, int32_t call) {
   moe::Prob q;
   if (check_problem(p, &q) != MOE_OK) return 0;
-  if (call < MOE_CALL_ROUTE || call > MOE_CALL_EXPERT_GEMM_PADDED) {
+  if (call < MOE_CALL_ROUTE || call > MOE_CALL_EXPERT_GEMM_QUANTIZED) {
     fail(MOE_ERR_INVALID_ARG, "unknown call %d", call);
     return 0;
   }
@@ -400,6 +433,198 @@ moe_status_t moe_expert_gemm_padded(const moe_problem_t* p, int32_t capacity, co
                     "moe_expert_gemm_padded");
 }
 
+moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
+                                   const int32_t* offsets, const void* w1, const void* w3,
+                                   const void* w2, void* g, void* u, void* h, void* y_packed,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  moe::Prob q;
+  moe_status_t st = check_problem(p, &q);
+  if (st != MOE_OK) return st;
+  NEED_PTR(offsets);
+  NEED_PTR(w1);
+  NEED_PTR(w3);
+  NEED_PTR(w2);
+  NEED_ALIGNED(w1);
+  NEED_ALIGNED(w3);
+  NEED_ALIGNED(w2);
+  if (q.T == 0) return ok();  // empty batch: no rows
+  NEED_PTR(x_packed);
+  NEED_PTR(g);
+  NEED_PTR(u);
+  NEED_PTR(h);
+  NEED_PTR(y_packed);
+  NEED_ALIGNED(x_packed);
+  NEED_ALIGNED(g);
+  NEED_ALIGNED(u);
+  NEED_ALIGNED(h);
+  NEED_ALIGNED(y_packed);
+  if ((st = check_ws(q, MOE_CALL_EXPERT_GEMM_TRAIN, workspace, workspace_bytes)) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(moe::launch_expert_gemm_train(q, x_packed, offsets, w1, w3, w2, g, u, h, y_packed,
+                                                  workspace, (hipStream_t)stream),
+                    "moe_expert_gemm_train");
+}
+
+moe_status_t moe_expert_gemm_backward(const moe_problem_t* p, const void* x_packed,
+                                      const int32_t* offsets, const void* w1, const void* w3,
+                                      const void* w2, const void* g, const void* u, const void* h,
+                                      const void* dy_packed, void* dx_packed, void* dw1, void* dw3,
+                                      void* dw2, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  moe::Prob q;
+  moe_status_t st = check_problem(p, &q);
+  if (st != MOE_OK) return st;
+  if ((st = check_backward_widths(q)) != MOE_OK) return st;
+  NEED_PTR(offsets);
+  NEED_PTR(w1);
+  NEED_PTR(w3);
+  NEED_PTR(w2);
+  NEED_ALIGNED(w1);
+  NEED_ALIGNED(w3);
+  NEED_ALIGNED(w2);
+  if (!dx_packed && !dw1 && !dw3 && !dw2)
+    return fail(MOE_ERR_INVALID_ARG, "dx_packed, dw1, dw3 and dw2 are all NULL");
+  NEED_ALIGNED(dw1);
+  NEED_ALIGNED(dw3);
+  NEED_ALIGNED(dw2);
+  if (q.T > 0) {  // an empty batch only zeroes the weight gradients
+    NEED_PTR(x_packed);
+    NEED_PTR(g);
+    NEED_PTR(u);
+    NEED_PTR(h);
+    NEED_PTR(dy_packed);
+    NEED_ALIGNED(x_packed);
+    NEED_ALIGNED(g);
+    NEED_ALIGNED(u);
+    NEED_ALIGNED(h);
+    NEED_ALIGNED(dy_packed);
+    NEED_ALIGNED(dx_packed);
+  }
+  if ((st = check_ws(q, MOE_CALL_EXPERT_GEMM_BACKWARD, workspace, workspace_bytes)) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(moe::launch_expert_backward(q, x_packed, offsets, w1, w3, w2, g, u, h, dy_packed,
+                                                dx_packed, dw1, dw3, dw2, workspace,
+                                                (hipStream_t)stream),
+                    "moe_expert_gemm_backward");
+}
+
+moe_status_t moe_quantize_rows(int64_t rows, int32_t K, int32_t dtype, const void* x, int8_t* q,
+                               float* scale, void* stream) {
+  moe_status_t st;
+  if (rows < 0 || K <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "rows=%lld must be >= 0 and K=%d positive", (long long)rows, K);
+  if (K % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 8", K);
+  if (rows >= ((int64_t)1 << 40) / K)
+    return fail(MOE_ERR_UNSUPPORTED, "rows=%lld x K=%d too large", (long long)rows, K);
+  if ((st = check_dtype(dtype)) != MOE_OK) return st;
+  if (rows == 0) return ok();
+  NEED_PTR(x);
+  NEED_PTR(q);
+  NEED_PTR(scale);
+  NEED_ALIGNED(x);
+  if ((reinterpret_cast<uintptr_t>(q) & 7u) != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "q is not 8-byte aligned");
+  (void)hipGetLastError();
+  return hip_status(moe::launch_quantize_rows(x, dtype, rows, K, K, q, scale, nullptr,
+                                              (hipStream_t)stream),
+                    "moe_quantize_rows");
+}
+
+size_t moe_packed_weights_bytes(int32_t n, int32_t K, int32_t N) {
+  if (check_packed(n, K, N) != MOE_OK) return 0;
+  ok();
+  return moe::packed_i8_bytes(n, K, N);
+}
+
+moe_status_t moe_pack_weights(int32_t n, int32_t K, int32_t N, const int8_t* w, void* packed,
+                              void* stream) {
+  moe_status_t st;
+  if ((st = check_packed(n, K, N)) != MOE_OK) return st;
+  NEED_PTR(w);
+  NEED_PTR(packed);
+  NEED_ALIGNED(packed);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_pack_i8(n, K, N, w, packed, (hipStream_t)stream), "moe_pack_weights");
+}
+
+moe_status_t moe_quantize_weights(int32_t n, int32_t K, int32_t N, int32_t dtype, const void* w,
+                                  void* packed, float* scale, void* stream) {
+  moe_status_t st;
+  if ((st = check_packed(n, K, N)) != MOE_OK) return st;
+  if ((st = check_dtype(dtype)) != MOE_OK) return st;
+  NEED_PTR(w);
+  NEED_PTR(packed);
+  NEED_PTR(scale);
+  NEED_ALIGNED(w);
+  NEED_ALIGNED(packed);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_quantize_weights(n, K, N, dtype, w, packed, scale, (hipStream_t)stream),
+                    "moe_quantize_weights");
+}
+
+moe_status_t moe_gemm_quantized(int32_t M, int32_t N, int32_t K, const int8_t* A,
+                                const float* a_scale, const void* packed, const float* b_scale,
+                                void* C, int32_t out_dtype, void* stream) {
+  moe_status_t st;
+  if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M=%d must be >= 0", M);
+  if ((st = check_packed(1, K, N)) != MOE_OK) return st;
+  if (K % 16 != 0) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 16", K);
+  if ((st = check_dtype(out_dtype)) != MOE_OK) return st;
+  NEED_PTR(packed);
+  NEED_PTR(b_scale);
+  NEED_ALIGNED(packed);
+  NEED_ALIGNED(b_scale);
+  if (M == 0) return ok();
+  NEED_PTR(A);
+  NEED_PTR(a_scale);
+  NEED_PTR(C);
+  NEED_ALIGNED(A);
+  NEED_ALIGNED(C);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_gemm_i8(M, N, K, A, a_scale, packed, b_scale, C, out_dtype,
+                                        (hipStream_t)stream),
+                    "moe_gemm_quantized");
+}
+
+moe_status_t moe_expert_gemm_quantized(const moe_problem_t* p, const void* x_packed,
+                                       const int32_t* offsets, const void* w1, const float* s1,
+                                       const void* w3, const float* s3, const void* w2,
+                                       const float* s2, void* h, void* y_packed, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  moe::Prob q;
+  moe_status_t st = check_problem(p, &q);
+  if (st != MOE_OK) return st;
+  if (q.dtype != MOE_DTYPE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "8-bit experts take bf16 rows (dtype %d)", q.dtype);
+  if (q.d >= kMaxQuantK || q.f >= kMaxQuantK)
+    return fail(MOE_ERR_UNSUPPORTED, "d=%d and f=%d must be below %d", q.d, q.f, kMaxQuantK);
+  NEED_PTR(offsets);
+  NEED_PTR(w1);
+  NEED_PTR(s1);
+  NEED_PTR(w3);
+  NEED_PTR(s3);
+  NEED_PTR(w2);
+  NEED_PTR(s2);
+  NEED_ALIGNED(w1);
+  NEED_ALIGNED(s1);
+  NEED_ALIGNED(w3);
+  NEED_ALIGNED(s3);
+  NEED_ALIGNED(w2);
+  NEED_ALIGNED(s2);
+  if (q.T == 0) return ok();  // empty batch: no rows
+  NEED_PTR(x_packed);
+  NEED_PTR(h);
+  NEED_PTR(y_packed);
+  NEED_ALIGNED(x_packed);
+  NEED_ALIGNED(h);
+  NEED_ALIGNED(y_packed);
+  if ((st = check_ws(q, MOE_CALL_EXPERT_GEMM_QUANTIZED, workspace, workspace_bytes)) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(moe::launch_expert_i8(q, x_packed, offsets, w1, s1, w3, s3, w2, s2, h, y_packed,
+                                          workspace, (hipStream_t)stream),
+                    "moe_expert_gemm_quantized");
+}
+
 int64_t moe_gemm_signal_tiles(int32_t M, int32_t N) {
   if (M <= 0 || N <= 0) {
     fail(MOE_ERR_INVALID_ARG, "M=%d and N=%d must be positive", M, N);
@@ -465,6 +690,26 @@ moe_status_t moe_combine(const moe_problem_t* p, const void* y_packed, const int
   (void)hipGetLastError();
   return hip_status(moe::launch_combine(q, y_packed, inv, topk_w, y, (hipStream_t)stream),
                     "moe_combine");
+}
+
+moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dy, const void* y_packed,
+                                  const int32_t* inv, const float* topk_w, void* dy_packed,
+                                  float* dtopk_w, void* stream) {
+  moe::Prob q;
+  moe_status_t st = check_problem(p, &q);
+  if (st != MOE_OK) return st;
+  if (q.T == 0) return ok();  // empty batch: no rows
+  NEED_PTR(dy);
+  NEED_PTR(inv);
+  NEED_PTR(dy_packed);
+  if (dtopk_w) NEED_PTR(y_packed);
+  NEED_ALIGNED(dy);
+  NEED_ALIGNED(y_packed);
+  NEED_ALIGNED(dy_packed);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_combine_backward(q, dy, y_packed, inv, topk_w, dy_packed, dtopk_w,
+                                                 (hipStream_t)stream),
+                    "moe_combine_backward");
 }
 
 moe_status_t moe_layer(const moe_problem_t* p, const void* x, const void* w_gate,

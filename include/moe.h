@@ -17,6 +17,12 @@
  *   moe_layer        all of the above, stream-ordered
  *   moe_dispatch_padded, moe_expert_gemm_padded
  *                    the padded fixed-capacity layout, as an A/B
+ *   moe_expert_gemm_train, moe_expert_gemm_backward, moe_combine_backward
+ *                    the experts in training: the forward pass that keeps what
+ *                    the gradients need, and the gradients
+ *   moe_quantize_rows, moe_quantize_weights, moe_pack_weights,
+ *   moe_gemm_quantized, moe_expert_gemm_quantized
+ *                    the experts served with 8-bit weights and activations
  *   moe_gemm_signal, moe_tile_forward
  *                    GEMM with per-tile completion flags and their consumer
  *                    (the local half of the pages' GEMM + AllGather)
@@ -87,7 +93,10 @@ enum {
   MOE_CALL_COMBINE = 3,
   MOE_CALL_LAYER = 4,
   MOE_CALL_DISPATCH_PADDED = 5,
-  MOE_CALL_EXPERT_GEMM_PADDED = 6
+  MOE_CALL_EXPERT_GEMM_PADDED = 6,
+  MOE_CALL_EXPERT_GEMM_TRAIN = 7,
+  MOE_CALL_EXPERT_GEMM_BACKWARD = 8,
+  MOE_CALL_EXPERT_GEMM_QUANTIZED = 9
 };
 
 /*
@@ -257,6 +266,125 @@ moe_status_t moe_expert_gemm_padded(const moe_problem_t* p, int32_t capacity, co
                                     const int32_t* offsets, const void* w1, const void* w3,
                                     const void* w2, void* h, void* y_packed, void* workspace,
                                     size_t workspace_bytes, void* stream);
+
+/*
+ * Training forward of the local experts: moe_expert_gemm that also keeps the
+ * two unactivated products for the backward pass.  For each local expert e and
+ * its rows R:
+ *   g[R] = rnd(x_packed[R] w1[e]),  u[R] = rnd(x_packed[R] w3[e])
+ * and h, y_packed as moe_expert_gemm writes them (h from the unrounded
+ * products).
+ *   g, u [rows_max,f]  dtype output (rows >= A untouched)
+ *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_TRAIN) bytes
+ * A dense gated block is the problem with E = k = n_local = 1 and offsets
+ * {0, T}.
+ */
+moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
+                                   const int32_t* offsets, const void* w1, const void* w3,
+                                   const void* w2, void* g, void* u, void* h, void* y_packed,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Backward pass of the local experts.  With the g, u, h that
+ * moe_expert_gemm_train kept and s = 1 / (1 + exp(-g)), for each local expert
+ * e and its rows R:
+ *   dh           = dy_packed[R] w2[e]^T                      (fp32, not stored)
+ *   dg           = rnd(dh u s (1 + g (1 - s))),  du = rnd(dh g s)
+ *   dx_packed[R] = rnd(dg w1[e]^T + du w3[e]^T)
+ *   dw1[e] = rnd(x_packed[R]^T dg), dw3[e] = rnd(x_packed[R]^T du),
+ *   dw2[e] = rnd(h[R]^T dy_packed[R])
+ * with fp32 accumulation.  An expert without rows gets zero weight gradients;
+ * every element of dw1, dw3 and dw2 is written (zeros for T = 0 too).
+ *   dy_packed [rows_max,d]              dtype
+ *   dx_packed [rows_max,d]              dtype output (rows >= A untouched), or NULL
+ *   dw1, dw3  [n_local,d,f]             dtype outputs, each may be NULL
+ *   dw2       [n_local,f,d]             dtype output, or NULL
+ * A NULL output is not computed; at least one must be given.  Outputs must not
+ * overlap inputs.  d and f at most 2^21.
+ *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_BACKWARD) bytes
+ * moe_combine(p, dx_packed, inv, NULL, dx) sums dx_packed back to token order
+ * (the backward pass of dispatch's row gather).
+ */
+moe_status_t moe_expert_gemm_backward(const moe_problem_t* p, const void* x_packed,
+                                      const int32_t* offsets, const void* w1, const void* w3,
+                                      const void* w2, const void* g, const void* u, const void* h,
+                                      const void* dy_packed, void* dx_packed, void* dw1, void* dw3,
+                                      void* dw2, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * Backward pass of moe_combine (unpadded or padded layout).  For every slot a
+ * = t*k + j with row p = inv[a] >= 0:
+ *   dy_packed[p] = rnd(topk_w[a] * dy[t]),  dtopk_w[a] = sum_i dy[t,i] y_packed[p,i]
+ * and dtopk_w[a] = 0 where inv[a] < 0.  Rows of dy_packed that inv does not
+ * name are left untouched; the entries of inv must be distinct where not
+ * negative.  topk_w = NULL: unit weights.
+ *   dy       [T,d] dtype;  y_packed as moe_combine read it (may be NULL with dtopk_w NULL)
+ *   dy_packed      dtype output, as many rows as y_packed
+ *   dtopk_w  [T,k] fp32 output, or NULL
+ */
+moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dy, const void* y_packed,
+                                  const int32_t* inv, const float* topk_w, void* dy_packed,
+                                  float* dtopk_w, void* stream);
+
+/*
+ * Rows to 8 bits, one scale each: with m = max_k |x[r,k]|
+ *   scale[r] = m / 127,  q[r,k] = rint(x[r,k] * (127 * (1 / m)))   (ties to even)
+ * in fp32 arithmetic, each operation rounded; a row with m < 2^-119 (zeros
+ * among them) gets scale 0 and zeros.
+ *   x [rows,K] of dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32;  q [rows,K] int8
+ * K a multiple of 8, x 16-byte and q 8-byte aligned; rows >= 0.
+ */
+moe_status_t moe_quantize_rows(int64_t rows, int32_t K, int32_t dtype, const void* x, int8_t* q,
+                               float* scale, void* stream);
+
+/*
+ * Packed 8-bit weights: n matrices [K,N] in the order the matrix cores read
+ * them.  Element (k, j) of matrix e is byte
+ *   ((((e * ceil(N/16) + j/16) * ceil(K/64) + k/64) * 4 + k%64/16) * 16 + j%16) * 16 + k%16
+ * (integer divisions); elements past K and N are zero.
+ * moe_packed_weights_bytes(n, K, N): its size, 0 for invalid sizes.
+ * moe_pack_weights:      packs int8 w [n,K,N].
+ * moe_quantize_weights:  quantises w [n,K,N] of `dtype` per output channel
+ *   (scale[e,j] = max_k |w[e,k,j]| / 127, values as moe_quantize_rows) and packs.
+ * n 1..1024, K < 131072, N a multiple of 8; packed 16-byte aligned.
+ */
+size_t moe_packed_weights_bytes(int32_t n, int32_t K, int32_t N);
+moe_status_t moe_pack_weights(int32_t n, int32_t K, int32_t N, const int8_t* w, void* packed,
+                              void* stream);
+moe_status_t moe_quantize_weights(int32_t n, int32_t K, int32_t N, int32_t dtype, const void* w,
+                                  void* packed, float* scale, void* stream);
+
+/*
+ * 8-bit product with a scale for each row and each output channel:
+ *   C[m,j] = rnd(float(sum_k A[m,k] B[k,j]) * a_scale[m] * b_scale[j])
+ * The sum is exact in int32 (K < 131072); rnd rounds to out_dtype
+ * (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
+ *   A [M,K] int8 row-major, K a multiple of 16;  packed: one matrix [K,N] of
+ *   moe_pack_weights or moe_quantize_weights;  C [M,N], N a multiple of 8.
+ * A, packed, b_scale and C 16-byte aligned.  M = 0 launches nothing.
+ */
+moe_status_t moe_gemm_quantized(int32_t M, int32_t N, int32_t K, const int8_t* A,
+                                const float* a_scale, const void* packed, const float* b_scale,
+                                void* C, int32_t out_dtype, void* stream);
+
+/*
+ * moe_expert_gemm with 8-bit weights and activations.  For each local expert e
+ * and its rows R, with (xq, sx) the rows of x_packed and (hq, sh) those of h
+ * quantised as moe_quantize_rows does:
+ *   h[R]        = rnd(SiLU(xq w1 sx s1[e]) * (xq w3 sx s3[e]))
+ *   y_packed[R] = rnd(hq w2 sh s2[e])
+ * The products sum exactly in int32.  bf16 only (dtype of x_packed, h, y_packed).
+ *   w1, w3 packed [n_local][d,f], w2 packed [n_local][f,d] (moe_pack_weights);
+ *   s1, s3 [n_local,f], s2 [n_local,d] fp32 channel scales;  d, f < 131072
+ *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_QUANTIZED) bytes
+ * Rows >= A of x_packed are not read, those of h and y_packed are left untouched.
+ */
+moe_status_t moe_expert_gemm_quantized(const moe_problem_t* p, const void* x_packed,
+                                       const int32_t* offsets, const void* w1, const float* s1,
+                                       const void* w3, const float* s3, const void* w2,
+                                       const float* s2, void* h, void* y_packed, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 /*
  * GEMM with per-tile completion signals: the local compute half of the pages'

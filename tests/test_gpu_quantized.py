@@ -1,0 +1,195 @@
+"""8-bit rows, weights and products.
+
+The integer sums are exact, so a product is checked through its formula: the
+int64 sum rounded to fp32 (one rounding), two fp32 products (two more) and the
+store.  fp32 outputs with unit scales must equal the rounded sum itself.
+"""
+import numpy as np
+import pytest
+import torch
+
+import combine_router_top_amd as M
+from tests.segments import HALF, Rows, assert_within, offsets_of, spec
+
+pytestmark = pytest.mark.gpu
+
+
+def _quant(x):
+    """The quantiser's definition in single precision (numpy)."""
+    x = np.asarray(x, dtype=np.float32)
+    top = np.abs(x).max(axis=1) if x.shape[1] else np.zeros(x.shape[0], np.float32)
+    live = top >= np.float32(2.0 ** -119)
+    with np.errstate(divide="ignore", over="ignore"):
+        inv = np.where(live, np.float32(127) * (np.float32(1) / top), np.float32(0)).astype(np.float32)
+    return (np.rint(x * inv[:, None]).astype(np.int8),
+            np.where(live, top / np.float32(127), np.float32(0)).astype(np.float32))
+
+
+@pytest.mark.parametrize("rows,K", [(1, 8), (3, 16), (5, 264), (2, 8192), (3, 8200), (2, 40960), (700, 72), (5000, 8)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_rows(rows, K, dtype):
+    g = torch.Generator().manual_seed(rows + K)
+    x = (torch.randn((rows, K), generator=g) * torch.rand((rows, 1), generator=g) * 10).to(dtype)
+    x[0] = 0                       # scale 0, zeros
+    if rows > 1:
+        x[1, 1:] = 0               # one value: 127 or -127
+    if rows > 3:
+        x[3] = x[3].sign() * 2.0 ** -120   # counts as zeros
+        x[4] = x[4].sign() * 2.0 ** -119
+    if rows > 2:
+        x[2, :4] = torch.tensor([2.0, 1.0, -1.0, 0.5]).to(dtype)
+    q, s = M.quantize_rows(x.cuda())
+    rq, rs = _quant(x.float().numpy())
+    assert np.array_equal(s.cpu().numpy(), rs)
+    assert np.array_equal(q.cpu().numpy(), rq)
+
+
+@pytest.mark.parametrize("lead,K,N", [((), 8, 8), ((), 64, 16), ((3,), 72, 40), ((2,), 200, 136), ((), 1, 8), ((1,), 130, 24)])
+def test_packed_weights(lead, K, N):
+    g = torch.Generator().manual_seed(K * N)
+    w = torch.randint(-128, 128, lead + (K, N), generator=g, dtype=torch.int8)
+    packed = M.pack_weights(w.cuda()).cpu()
+    kp, np_ = -(-K // 64) * 64, -(-N // 16) * 16
+    full = torch.zeros(lead + (kp, np_), dtype=torch.int8)
+    full[..., :K, :N] = w
+    ref = full.view(*lead, kp // 64, 4, 16, np_ // 16, 16).movedim((-2, -5, -4, -1, -3), (-5, -4, -3, -2, -1))
+    assert torch.equal(packed, ref)
+    assert M.packed_weights_bytes(lead[0] if lead else 1, K, N) == packed.numel()
+    for dtype in (torch.bfloat16, torch.float32):
+        wf = torch.randn(lead + (K, N), generator=g).to(dtype)
+        wf[..., 0] = 0             # a channel of zeros
+        qp, s = M.quantize_weights(wf.cuda())
+        cols = wf.float().movedim(-1, -2).reshape(-1, K).numpy()
+        rq, rs = _quant(cols)
+        assert np.array_equal(s.cpu().numpy().ravel(), rs)
+        rw = torch.from_numpy(rq).view(*lead, N, K).movedim(-1, -2).contiguous()
+        assert torch.equal(qp.cpu(), M.pack_weights(rw.cuda()).cpu())
+
+
+SIZES = [(1, 8, 16), (1, 2048, 7168), (2, 24, 48), (15, 136, 64), (16, 512, 80), (17, 40, 1040), (31, 264, 256),
+         (32, 4096, 128), (33, 264, 144), (64, 72, 320), (129, 520, 592), (300, 264, 1040), (257, 1000, 128), (1, 20000, 64),
+         (20, 20000, 192), (3, 8, 8192)]
+
+
+@pytest.mark.parametrize("Mr,N,K", SIZES)
+def test_product_is_exact(Mr, N, K):
+    g = torch.Generator().manual_seed(Mr + N + K)
+    a = torch.randint(-128, 128, (Mr, K), generator=g, dtype=torch.int8)
+    b = torch.randint(-128, 128, (K, N), generator=g, dtype=torch.int8)
+    a[0] = -128
+    b[:, 0] = -128                 # the largest sum
+    packed = M.pack_weights(b.cuda())
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    got = M.gemm_quantized(a.cuda(), one(Mr), packed, one(N), dtype=torch.float32)
+    ref = (a.double() @ b.double())          # exact: below 2^53
+    assert torch.equal(got.cpu(), ref.float())
+    # scales, and bf16 output: three fp32 roundings and half a step
+    sa, sb = torch.rand(Mr, generator=g) + 0.01, torch.rand(N, generator=g) + 0.01
+    got = M.gemm_quantized(a.cuda(), sa.cuda(), packed, sb.cuda())
+    ref = ref * sa.double()[:, None] * sb.double()
+    assert_within(got, ref, (HALF["bf16"] + 4 * HALF["f32"]) * ref.abs(), "C")
+
+
+def test_product_extreme_depth():
+    """The deepest K: 131056 products of 16384 stay inside int32."""
+    K, N = 131056, 8
+    for Mr in (2, 40):
+        a = torch.full((Mr, K), -128, dtype=torch.int8, device="cuda")
+        a[1] = 127
+        packed = M.pack_weights(torch.full((K, N), -128, dtype=torch.int8, device="cuda"))
+        got = M.gemm_quantized(a, torch.ones(Mr, device="cuda"), packed, torch.ones(N, device="cuda"), dtype=torch.float32)
+        assert bool((got[0] == float(np.float32(K * 16384))).all()) and bool((got[1] == float(np.float32(-K * 127 * 128))).all())
+
+
+CASES = {
+    "one_row": ([1], 64, 64, {}),
+    "narrow": ([3, 0, 2], 8, 8, {}),
+    "streams": ([0, 5, 16, 1, 17, 32], 264, 200, {}),
+    "streams_16": ([4, 0, 16, 1], 1032, 328, dict(T=16, k=4)),
+    "mixed": ([0, 5, 33, 130, 1, 257], 264, 200, dict(T=257, k=2, E=48)),   # streams and tiles in one call
+    "tiles": ([100, 70, 0, 150], 328, 264, {}),
+    "tall_tiles": ([700, 0, 300], 136, 72, {}),
+    "wide": ([3] * 40, 64, 1032, dict(T=20)),
+    "no_rows": ([0, 0, 0], 64, 72, dict(T=5, k=2)),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_expert_gemm_quantized(name):
+    counts, d, f, kw = CASES[name]
+    p = spec(counts, d, f, "bf16", **kw)
+    r = Rows(p, counts, seed=d + f)
+    n = len(counts)
+    g = torch.Generator().manual_seed(d * f)
+    x = r.draw(r.A, d)
+    w = {k: torch.randint(-127, 128, (n, K, N), generator=g, dtype=torch.int8) for k, K, N in (("1", d, f), ("3", d, f), ("2", f, d))}
+    s = {k: (torch.rand((n, N), generator=g) + 0.5) / (70.0 * K ** 0.5) for k, K, N in (("1", d, f), ("3", d, f), ("2", f, d))}
+    h, y = M.expert_gemm_quantized(p, r.packed(x), offsets_of(counts), *(t for k in "132" for t in (M.pack_weights(w[k].cuda()), s[k].cuda())),
+                                   out=(r.out(f), r.out(d)))
+    torch.cuda.synchronize()
+    r.check_tail(h, y)
+    for e, seg in r.segments():
+        if seg.start == seg.stop:
+            continue
+        q, sx = _quant(x[seg].numpy())
+        q, sx = torch.from_numpy(q).double(), torch.from_numpy(sx).double()[:, None]
+        a = q @ w["1"][e].double() * sx * s["1"][e].double()
+        b = q @ w["3"][e].double() * sx * s["3"][e].double()
+        ref = a * torch.sigmoid(a) * b
+        # the two products carry three fp32 roundings each, the activation a few
+        # ulp that grow with |a| where it decays exponentially (d log SiLU <= 1 + |a|)
+        tol = (HALF["bf16"] + (2.0 ** -20) * (1 + a.abs())) * ref.abs()
+        assert_within(h[seg], ref, tol, "h")
+        # the down projection from the h that was stored
+        q, sh = _quant(h[seg].float().cpu().numpy())
+        ref = torch.from_numpy(q).double() @ w["2"][e].double() * torch.from_numpy(sh).double()[:, None] * s["2"][e].double()
+        assert_within(y[seg], ref, (HALF["bf16"] + 4 * HALF["f32"]) * ref.abs(), "y")
+
+
+def test_expert_gemm_quantized_near_bf16():
+    """Quantised from the same weights: near the bf16 experts (a sanity check of
+    scales and layout on real weights; 8-bit steps of a normal row are about 1%)."""
+    counts, d, f = [20, 0, 90], 512, 256
+    p = spec(counts, d, f, "bf16")
+    r = Rows(p, counts, seed=3)
+    w = [r.dev(r.draw(3, *s, scale=s[0] ** -0.5)) for s in ((d, f), (d, f), (f, d))]
+    x, off = r.packed(r.draw(r.A, d)), offsets_of(counts)
+    _, y = M.expert_gemm(p, x, off, *w)
+    packed = [t for v in w for t in M.quantize_weights(v)]
+    _, yq = M.expert_gemm_quantized(p, x, off, *packed)
+    a, b = y[: r.A].double(), yq[: r.A].double()
+    # a step is max / 127 and max of ~500 normal values about 3.3 sigma, so each
+    # quantised operand is off by 3.3 / 127 / sqrt(12) = 0.75% (h: larger
+    # maxima, about 2%); five of them in quadrature stay below 4%
+    assert float((a - b).norm() / a.norm()) < 0.04
+
+
+def test_quantized_captured():
+    """Replays follow new inputs, with eager calls between them."""
+    counts, d, f = [0, 5, 33, 130], 264, 200
+    p = spec(counts, d, f, "bf16", T=130, k=2, E=16)
+    r = Rows(p, counts, seed=9)
+    w = [t for s in ((d, f), (d, f), (f, d)) for t in M.quantize_weights(r.dev(r.draw(4, *s, scale=s[0] ** -0.5)))]
+    x, off = r.packed(r.draw(r.A, d)), offsets_of(counts)
+    ws = M.alloc_workspace(p, M.MOE_CALL_EXPERT_GEMM_QUANTIZED)
+    out = (r.out(f), r.out(d))
+
+    def step():
+        M.expert_gemm_quantized(p, x, off, *w, workspace=ws, out=out)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        x[: r.A] = r.dev(r.draw(r.A, d))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in out]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, out))

@@ -1,0 +1,343 @@
+"""The experts in training: kept forward pass, gradients, combine's gradient,
+and the whole layer's gradient through dispatch and combine.
+
+References are the formulas in 64 bits.  Tolerances per element:
+  half a step of the output type (2^-8 bf16, 2^-24 fp32) of the value, plus
+  half a step for each rounded operand times the sum of absolute products, plus
+  K 2^-23 times that sum for the fp32 additions (segments.dot_slack).
+The exponential and reciprocal of the activations are good to a few fp32 ulp:
+2^-20 relative is allowed for an activation or its derivative.
+"""
+import numpy as np
+import pytest
+import torch
+
+import combine_router_top_amd as M
+from tests.segments import HALF, SENTINEL, Rows, assert_within, dot_slack, offsets_of, spec
+
+pytestmark = pytest.mark.gpu
+
+ACT = 2.0 ** -20
+
+CASES = {
+    # name: (counts, d, f, dtype, spec arguments)
+    "one_row": ([1], 64, 64, "bf16", {}),
+    "narrow": ([3, 0, 2], 8, 8, "bf16", {}),
+    "ragged": ([0, 5, 130, 1, 0, 257], 264, 200, "bf16", {}),        # K tails in every product
+    "ragged_whole_k": ([31, 32, 33, 127, 128, 129], 256, 320, "bf16", {}),
+    "long": ([700, 0, 300], 136, 72, "bf16", {}),                    # 256-row tiles, K tails
+    "long_whole_k": ([513, 255, 256], 288, 544, "bf16", {}),
+    "one_long": ([1100], 520, 264, "bf16", {}),
+    "mid_k": ([70, 64], 96, 416, "bf16", {}),                        # 3 and 13 stages of K
+    "many_experts": ([(7 * e) % 5 for e in range(150)], 40, 48, "bf16", dict(T=40, k=8)),
+    "no_rows": ([0, 0, 0], 64, 72, "bf16", dict(T=5, k=2)),
+    "part_of_experts": ([9, 40, 0, 3], 72, 136, "bf16", dict(T=64, k=2, E=16)),
+    "f32_one_row": ([1], 8, 8, "f32", {}),
+    "f32_ragged": ([0, 5, 130, 1, 65], 72, 136, "f32", {}),
+    "f32_no_rows": ([0, 0], 16, 24, "f32", dict(T=3, k=1)),
+}
+
+
+def _case(name):
+    counts, d, f, dtype, kw = CASES[name]
+    p = spec(counts, d, f, dtype, **kw)
+    r = Rows(p, counts, seed=sum(map(ord, name)))
+    n = len(counts)
+    v = dict(x=r.draw(r.A, d), w1=r.draw(n, d, f, scale=d ** -0.5), w3=r.draw(n, d, f, scale=d ** -0.5),
+             w2=r.draw(n, f, d, scale=f ** -0.5))
+    return p, r, v
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_train_forward(name):
+    p, r, v = _case(name)
+    half = HALF[p.dtype]
+    outs = (r.out(p.f), r.out(p.f), r.out(p.f), r.out(p.d))
+    got = M.expert_gemm_train(p, r.packed(v["x"]), offsets_of(r.counts), r.dev(v["w1"]), r.dev(v["w3"]),
+                              r.dev(v["w2"]), out=outs)
+    torch.cuda.synchronize()
+    r.check_tail(*got)
+    for e, s in r.segments():
+        x = v["x"][s]
+        a, b = x @ v["w1"][e], x @ v["w3"][e]
+        ea, eb = dot_slack(x, v["w1"][e]), dot_slack(x, v["w3"][e])
+        assert_within(got[0][s], a, half * a.abs() + 2 * ea, "g")
+        assert_within(got[1][s], b, half * b.abs() + 2 * eb, "u")
+        sig = torch.sigmoid(a)
+        act = a * sig
+        h = act * b
+        # |SiLU'| <= 1.1
+        eh = 1.1 * ea * b.abs() + act.abs() * eb + 1.1 * ea * eb + ACT * h.abs()
+        assert_within(got[2][s], h, (half + 2 * ACT) * h.abs() + 2 * eh, "h")
+        # the down projection from the h that was stored
+        hs = got[2][s].cpu().double()
+        y = hs @ v["w2"][e]
+        assert_within(got[3][s], y, half * y.abs() + 2 * dot_slack(hs, v["w2"][e]), "y")
+
+
+def test_train_forward_is_expert_gemm():
+    """h and y bit for bit those of expert_gemm, in every tile class."""
+    for name in ("ragged", "long", "one_row", "f32_ragged"):
+        p, r, v = _case(name)
+        args = (r.packed(v["x"]), offsets_of(r.counts), r.dev(v["w1"]), r.dev(v["w3"]), r.dev(v["w2"]))
+        h, y = M.expert_gemm(p, *args)
+        _, _, h2, y2 = M.expert_gemm_train(p, *args)
+        assert torch.equal(h[: r.A], h2[: r.A]) and torch.equal(y[: r.A], y2[: r.A]), name
+
+
+def _backward_inputs(r, v, p):
+    g, u = r.draw(r.A, p.f), r.draw(r.A, p.f)
+    h = (g * torch.sigmoid(g) * u).to(r.dt).double()
+    return g, u, h, r.draw(r.A, p.d)
+
+
+def _check_backward(p, r, v, g, u, h, dy, got):
+    half = HALF[p.dtype]
+    # dg and du are rounded to the storage type; fp32 keeps them as computed
+    for e, s in r.segments():
+        w1, w3, w2 = v["w1"][e], v["w3"][e], v["w2"][e]
+        dh, edh = dy[s] @ w2.T, dot_slack(dy[s], w2.T)
+        sig = torch.sigmoid(g[s])
+        fg, fu = u[s] * sig * (1 + g[s] * (1 - sig)), g[s] * sig
+        dg, du = dh * fg, dh * fu
+        # 1 - s loses relative but not absolute precision: its error is 2^-23 g u s dh at most
+        eg = half * dg.abs() + 2 * edh * fg.abs() + ACT * (dh * u[s] * sig).abs() * (1 + g[s].abs())
+        eu = half * du.abs() + 2 * edh * fu.abs() + ACT * du.abs()
+        dx = dg @ w1.T + du @ w3.T
+        if got[0] is not None:
+            tol = (half * dx.abs() + (1 + half) * (eg @ w1.T.abs() + eu @ w3.T.abs())
+                   + 2 * (dot_slack(dg, w1.T) + dot_slack(du, w3.T)) + p.f * 2.0 ** -23 * dx.abs())
+            assert_within(got[0][s], dx, tol, "dx")
+        x = v["x"][s]
+        for k, (left, right, er, what) in enumerate(((x, dg, eg, "dw1"), (x, du, eu, "dw3"), (h[s], dy[s], None, "dw2"))):
+            if got[k + 1] is None:
+                continue
+            ref = left.T @ right
+            tol = half * ref.abs() + 2 * dot_slack(left.T, right)
+            if er is not None:
+                tol = tol + (1 + half) * (left.T.abs() @ er)
+            assert_within(got[k + 1][e], ref, tol, what)
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_backward(name):
+    p, r, v = _case(name)
+    g, u, h, dy = _backward_inputs(r, v, p)
+    n = len(r.counts)
+    outs = (r.out(p.d),) + tuple(torch.full(s, float("nan"), dtype=r.dt, device="cuda")
+                                 for s in ((n, p.d, p.f), (n, p.d, p.f), (n, p.f, p.d)))
+    got = M.expert_gemm_backward(p, r.packed(v["x"]), offsets_of(r.counts), r.dev(v["w1"]), r.dev(v["w3"]),
+                                 r.dev(v["w2"]), r.packed(g), r.packed(u), r.packed(h), r.packed(dy), out=outs)
+    torch.cuda.synchronize()
+    r.check_tail(got[0])
+    _check_backward(p, r, v, g, u, h, dy, got)
+
+
+@pytest.mark.parametrize("name", ["ragged", "f32_ragged"])
+@pytest.mark.parametrize("wanted", [(1, 0, 0, 0), (0, 1, 0, 0), (0, 0, 1, 0), (0, 0, 0, 1), (1, 0, 1, 1)])
+def test_backward_some_outputs(name, wanted):
+    p, r, v = _case(name)
+    g, u, h, dy = _backward_inputs(r, v, p)
+    n = len(r.counts)
+    shapes = (None, (n, p.d, p.f), (n, p.d, p.f), (n, p.f, p.d))
+    outs = tuple(None if not w else r.out(p.d) if i == 0 else torch.full(shapes[i], float("nan"), dtype=r.dt, device="cuda")
+                 for i, w in enumerate(wanted))
+    got = M.expert_gemm_backward(p, r.packed(v["x"]), offsets_of(r.counts), r.dev(v["w1"]), r.dev(v["w3"]),
+                                 r.dev(v["w2"]), r.packed(g), r.packed(u), r.packed(h), r.packed(dy), out=outs)
+    torch.cuda.synchronize()
+    _check_backward(p, r, v, g, u, h, dy, got)
+
+
+@pytest.mark.parametrize("name", ["ragged", "f32_ragged"])
+def test_backward_extreme_gates(name):
+    """Gates far out on both sides: s is 0 or 1 there and nothing turns into NaN."""
+    p, r, v = _case(name)
+    g, u, h, dy = _backward_inputs(r, v, p)
+    far = torch.tensor([-3e38, -1e4, -200.0, -90.0, 90.0, 200.0, 1e4, 3e38], dtype=torch.float64).to(r.dt).double()
+    g[:, : far.numel()] = far
+    u[:, : far.numel()] = u[:, : far.numel()].sign()
+    got = M.expert_gemm_backward(p, r.packed(v["x"]), offsets_of(r.counts), r.dev(v["w1"]), r.dev(v["w3"]),
+                                 r.dev(v["w2"]), r.packed(g), r.packed(u), r.packed(h), r.packed(dy),
+                                 out=(None, *(torch.empty((len(r.counts), p.d, p.f), dtype=r.dt, device="cuda")
+                                              for _ in range(1)), None, None))
+    torch.cuda.synchronize()
+    s = torch.sigmoid(g)
+    for e, seg in r.segments():
+        dg = (dy[seg] @ v["w2"][e].T) * u[seg] * s[seg] * (1 + g[seg] * (1 - s[seg]))
+        dg[:, : far.numel()] = (dy[seg] @ v["w2"][e].T)[:, : far.numel()] * u[seg][:, : far.numel()] * (far > 0)
+        ref = v["x"][seg].T @ dg
+        tol = (HALF[p.dtype] * (ref.abs() + 1.1 * (v["x"][seg].T.abs() @ dg.abs()))
+               + 3 * dot_slack(v["x"][seg].T, dg) + 1e-3 * (p.dtype == "bf16") * 0
+               + v["x"][seg].T.abs() @ (2 * dot_slack(dy[seg], v["w2"][e].T) * (1 + u[seg].abs()) * 1.1
+                                        + ACT * (1 + g[seg].abs().clamp(max=100)) * dg.abs().clamp(min=1e-6)
+                                        + ACT * ((dy[seg] @ v["w2"][e].T) * u[seg]).abs()))
+        assert_within(got[1][e], ref, tol, "dw1")
+
+
+def test_backward_empty_batch():
+    for dtype in ("bf16", "f32"):
+        p = M.Spec(0, 64, 4, 2, 40, 0, 3, dtype)
+        dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+        z = lambda *s: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+        outs = (z(0, 64), *(torch.full(s, float("nan"), dtype=dt, device="cuda")
+                            for s in ((3, 64, 40), (3, 64, 40), (3, 40, 64))))
+        M.expert_gemm_backward(p, z(0, 64), torch.zeros(4, dtype=torch.int32, device="cuda"), z(3, 64, 40),
+                               z(3, 64, 40), z(3, 40, 64), z(0, 40), z(0, 40), z(0, 40), z(0, 64), out=outs)
+        torch.cuda.synchronize()
+        assert all(bool((o == 0).all()) for o in outs[1:])
+
+
+def _slots(T, k, n, E, seed):
+    rng = np.random.default_rng(seed)
+    inv = np.full((T, k), -1, dtype=np.int32)
+    for t in range(T):
+        c = rng.choice(E, k, replace=False)
+        inv[t][c < n] = 0
+    at = np.argwhere(inv.ravel() == 0).ravel()
+    flat = inv.ravel()
+    flat[at] = rng.permutation(len(at)).astype(np.int32)
+    return flat, len(at)
+
+
+@pytest.mark.parametrize("T,k,n,E,d,dtype", [
+    (1, 1, 1, 1, 8, "bf16"), (7, 4, 3, 12, 264, "bf16"), (64, 2, 8, 8, 4096, "bf16"), (33, 32, 64, 64, 72, "bf16"),
+    (5, 8, 32, 256, 7168, "bf16"), (9, 3, 2, 5, 8200, "bf16"), (6, 2, 2, 4, 24584, "bf16"),
+    (11, 4, 3, 6, 136, "f32"), (3, 2, 2, 2, 4104, "f32"), (40, 1, 1, 16, 64, "bf16")])
+def test_combine_backward(T, k, n, E, d, dtype):
+    inv, A = _slots(T, k, n, E, seed=T + d)
+    p = M.Spec(T, d, E, k, 8, 0, n, dtype)
+    r = Rows(p, [A], seed=d)
+    r.A = A
+    dy, yp = r.draw(T, d), r.draw(A, d)
+    w = torch.rand((T, k), generator=r.gen)
+    di = torch.from_numpy(inv).cuda()
+    dyp, dw = M.combine_backward(p, r.dev(dy), r.packed(yp), di, w.cuda(), out=(r.out(d), torch.full((T, k), 9.0, device="cuda")))
+    torch.cuda.synchronize()
+    r.check_tail(dyp)
+    iv = torch.from_numpy(inv).long().view(T, k)
+    for t in range(T):
+        for j in range(k):
+            row = int(iv[t, j])
+            if row < 0:
+                assert float(dw[t, j]) == 0.0
+                continue
+            ref = w[t, j].double() * dy[t]
+            # the fp32 product and its rounding
+            assert_within(dyp[row], ref, (HALF[dtype] + 2.0 ** -23) * ref.abs(), "dy_packed")
+            dot = (dy[t] * yp[row]).sum()
+            tol = d * 2.0 ** -23 * (dy[t] * yp[row]).abs().sum()
+            assert abs(float(dw[t, j]) - dot) <= tol, (t, j)
+    # unit weights, and the rows alone
+    one, none = M.combine_backward(p, r.dev(dy), None, di, None, out=(r.out(d), None))
+    torch.cuda.synchronize()
+    assert none is None
+    for t in range(T):
+        for j in range(k):
+            if iv[t, j] >= 0:
+                assert torch.equal(one[int(iv[t, j])].cpu(), dy[t].to(r.dt))
+
+
+def _layer64(x, w1, w3, w2, idx, w, lo, n):
+    """y of the MoE layer with fixed routing, float64, autograd on."""
+    y = torch.zeros_like(x)
+    for e in range(n):
+        t, j = torch.nonzero(idx == lo + e, as_tuple=True)
+        if t.numel():
+            xe = x[t]
+            a = xe @ w1[e]
+            out = (a * torch.sigmoid(a) * (xe @ w3[e])) @ w2[e]
+            y = y.index_add(0, t, w[t, j][:, None] * out)
+    return y
+
+
+@pytest.mark.parametrize("dtype,T,d,f", [("f32", 50, 72, 56), ("bf16", 300, 136, 200)])
+def test_layer_training_step(dtype, T, d, f):
+    """dispatch, experts, combine and their gradients together, against autograd
+    in 64 bits and against differences of the layer in 64 bits."""
+    E, k, lo, n = 8, 3, 2, 5
+    p = M.Spec(T, d, E, k, f, lo, n, dtype)
+    r = Rows(p, [0], seed=T)
+    x = r.draw(T, d)
+    w1, w3, w2 = r.draw(n, d, f, scale=d ** -0.5), r.draw(n, d, f, scale=d ** -0.5), r.draw(n, f, d, scale=f ** -0.5)
+    wg = r.draw(d, E, scale=d ** -0.5)
+    dy = r.draw(T, d)
+    idx, wt = M.route(p, r.dev(x), r.dev(wg))
+    D = M.dispatch(p, idx, r.dev(x))
+    W = (r.dev(w1), r.dev(w3), r.dev(w2))
+    g, u, h, yp = M.expert_gemm_train(p, D["x_packed"], D["offsets"], *W)
+    y = M.combine(p, yp, D["inv"], wt)
+    dyp, dwt = M.combine_backward(p, r.dev(dy), yp, D["inv"], wt)
+    dxp, dw1, dw3, dw2 = M.expert_gemm_backward(p, D["x_packed"], D["offsets"], *W, g, u, h, dyp)
+    dx = M.combine(p, dxp, D["inv"], None)
+    torch.cuda.synchronize()
+    leaves = [t.clone().requires_grad_(True) for t in (x, w1, w3, w2, wt.cpu().double())]
+    ref = _layer64(*leaves[:4], idx.cpu().long(), leaves[4], lo, n)
+    ref.backward(dy)
+    # Every value passes at most six roundings to the storage type on its way
+    # (x W1, h, y or w dy, dg, dx_packed, the output), each half a step, that
+    # add like independent errors of the tensor's norm: 6 half steps bound the
+    # relative 2-norm, with the fp32 sums' K 2^-23 on top.
+    bound = 6 * HALF[dtype] + (d + f) * 2.0 ** -23
+    names = ("y", "dx", "dw1", "dw3", "dw2", "dtopk_w")
+    for name, a, b in zip(names, (y, dx, dw1, dw3, dw2, dwt), (ref, *(t.grad for t in leaves))):
+        rel = float((a.cpu().double() - b.detach()).norm() / b.detach().norm())
+        assert rel <= bound, (name, rel, bound)
+    # along a random direction: the loss's central difference in 64 bits
+    for i, got in ((0, dx), (1, dw1), (2, dw3), (3, dw2), (4, dwt)):
+        with torch.no_grad():
+            dirn = torch.randn(leaves[i].shape, generator=r.gen, dtype=torch.float64)
+            step = 1e-5
+            vals = []
+            for sgn in (1, -1):
+                moved = [t.detach() + (sgn * step * dirn if j == i else 0) for j, t in enumerate(leaves)]
+                vals.append(float((_layer64(*moved[:4], idx.cpu().long(), moved[4], lo, n) * dy).sum()))
+            diff = (vals[0] - vals[1]) / (2 * step)
+            mine = float((got.cpu().double() * dirn).sum())
+            scale = float(leaves[i].grad.norm() * dirn.norm())
+            assert abs(mine - diff) <= (bound + 1e-7) * scale, (names[i + 1], mine, diff)
+
+
+def test_backward_captured():
+    """A captured training step replays with new inputs, on a stream of its own."""
+    p, r, v = _case("ragged")
+    g, u, h, dy = _backward_inputs(r, v, p)
+    off = offsets_of(r.counts)
+    W = [r.dev(v[k]) for k in ("w1", "w3", "w2")]
+    x, dyd = r.packed(v["x"]), r.packed(dy)
+    n = len(r.counts)
+    ws = M.alloc_workspace(p, M.MOE_CALL_EXPERT_GEMM_BACKWARD)
+    ws2 = M.alloc_workspace(p, M.MOE_CALL_EXPERT_GEMM_TRAIN)
+    fw = tuple(r.out(w) for w in (p.f, p.f, p.f, p.d))
+    bw = (r.out(p.d), *(torch.empty(s, dtype=r.dt, device="cuda") for s in ((n, p.d, p.f), (n, p.d, p.f), (n, p.f, p.d))))
+
+    def step():
+        M.expert_gemm_train(p, x, off, *W, workspace=ws2, out=fw)
+        M.expert_gemm_backward(p, x, off, *W, *fw[:3], dyd, workspace=ws, out=bw)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for k in range(3):
+        x[: r.A] = r.dev(r.draw(r.A, p.d))
+        dyd[: r.A] = r.dev(r.draw(r.A, p.d))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in (*fw, *bw)]
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(kept, (*fw, *bw)):
+            assert torch.equal(a, b), k
+
+
+def test_backward_is_reproducible():
+    p, r, v = _case("long")
+    g, u, h, dy = _backward_inputs(r, v, p)
+    args = (r.packed(v["x"]), offsets_of(r.counts), r.dev(v["w1"]), r.dev(v["w3"]), r.dev(v["w2"]), r.packed(g),
+            r.packed(u), r.packed(h), r.packed(dy))
+    a, b = M.expert_gemm_backward(p, *args), M.expert_gemm_backward(p, *args)
+    assert all(torch.equal(s[: r.A] if i == 0 else s, t[: r.A] if i == 0 else t) for i, (s, t) in enumerate(zip(a, b)))
