@@ -36,15 +36,11 @@ __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& d
   du = dh * (g * s);
 }
 
-__device__ __forceinline__ u32x2 pack_bf16x4(float a, float b, float c, float d) {
-  return u32x2{pack_bf16x2(a, b), pack_bf16x2(c, d)};
-}
-
 template <int MT, bool KT>
-using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, KT>;
+using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, KT, 8 * MT>;
 template <int MT, bool KT>
-using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, KT>;
-using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, false>;
+using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, KT, 4 * MT>;
+using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, false, 16>;
 
 // dh tiles: rows of dy against rows of W2 (its f rows are the output columns).
 template <int MT, bool KT>
@@ -59,49 +55,77 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
   __shared__ int pre[ST_MAXN + 1];
   const int total = st_prefix(offsets, n, Cfg::BM, pre) * ntn;
-  const StRange rg = st_range(total, blockIdx.x, gridDim.x);
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 3, wn = wave >> 2;
-  for (int L = rg.begin; L < rg.end; L += rg.step) {
-    const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
-    StCtx<Cfg> c;
-    st_setup(c, ring);
-    st_rows<Cfg::BM>(c.a[0], dy + (int64_t)t.r0 * d, (uint32_t)d * 2, t.R, (uint32_t)d * 2);
-    st_rows<ST_BN>(c.b[0], w2 + ((int64_t)t.e * f + 256 * t.nt) * d, (uint32_t)d * 2,
-                   min(ST_BN, f - 256 * t.nt), (uint32_t)d * 2);
-    c.nst = c.nst1 = (d + 31) / 32;
-    c.kvals = d;
-    f32x4 acc[MT][8];
-    st_clear<Cfg>(acc);
-    st_accum(c, ring, acc);
+  st_run<Cfg>(
+      total, ring,
+      [&](int L, StCtx<Cfg>& c) {
+        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+        const uint32_t ld = (uint32_t)d * 2;
+        st_rows<Cfg::BM>(c.a[0], dy + (int64_t)t.r0 * d, ld, t.R, ld);
+        st_rows<ST_BN>(c.b[0], w2 + ((int64_t)t.e * f + 256 * t.nt) * d, ld, min(ST_BN, f - 256 * t.nt), ld);
+        c.nst = c.nst1 = (d + 63) / 64;
+        c.kvals = d;
+      },
+      [&](int L, f32x4 (&acc)[MT][8]) {
+        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+        const int64_t first = (int64_t)t.r0 * f;
+        const int64_t ld = (int64_t)f * 2;
+        const StOut og = st_out(dg + first, ld, t.R), ou = st_out(du + first, ld, t.R);
+        const __amdgpu_buffer_rsrc_t rg = gc_rsrc(g + first, (uint32_t)t.R * (uint32_t)ld);
+        const __amdgpu_buffer_rsrc_t ru = gc_rsrc(u + first, (uint32_t)t.R * (uint32_t)ld);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int row = 16 * MT * wm + 16 * mt + i;
+        for (int mt = 0; mt < MT; ++mt) {
+          const int row = 16 * MT * wm + 16 * mt + i;
+          u32x4 gv[4], uv[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int col = 256 * t.nt + 128 * wn + 16 * k + 4 * q;
-        if (row < t.R && col < f) {
-          const int64_t at = (int64_t)(t.r0 + row) * f + col;
-          const u32x2 gv = *reinterpret_cast<const u32x2*>(g + at);
-          const u32x2 uv = *reinterpret_cast<const u32x2*>(u + at);
-          float og[4], ou[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float gf = r & 1 ? bf16_hi(gv[r >> 1]) : bf16_lo(gv[r >> 1]);
-            const float uf = r & 1 ? bf16_hi(uv[r >> 1]) : bf16_lo(uv[r >> 1]);
-            swiglu_grad(acc[mt][k][r], gf, uf, og[r], ou[r]);
+          for (int k = 0; k < 4; ++k) {
+            const int col = 256 * t.nt + 128 * wn + 32 * k + 8 * q;
+            const uint32_t at = col < f ? (uint32_t)row * (uint32_t)ld + 2u * (uint32_t)col : 0xFFFFFFF0u;
+            gv[k] = __builtin_amdgcn_raw_buffer_load_b128(rg, at, 0, 0);
+            uv[k] = __builtin_amdgcn_raw_buffer_load_b128(ru, at, 0, 0);
           }
-          *reinterpret_cast<u32x2*>(dg + at) = pack_bf16x4(og[0], og[1], og[2], og[3]);
-          *reinterpret_cast<u32x2*>(du + at) = pack_bf16x4(ou[0], ou[1], ou[2], ou[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int col = 256 * t.nt + 128 * wn + 32 * k + 8 * q;
+            float x[4], y[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              x[r] = acc[mt][2 * k][r];
+              y[r] = acc[mt][2 * k + 1][r];
+              st_swap_pair(x[r], y[r]);   // x: columns 8 q + r, y: 8 q + 4 + r
+            }
+            u32x4 vg, vu;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const float* dh = h < 2 ? x + 2 * h : y + 2 * (h - 2);
+              float a0, a1, b0, b1;
+              swiglu_grad(dh[0], bf16_lo(gv[k][h]), bf16_lo(uv[k][h]), a0, b0);
+              swiglu_grad(dh[1], bf16_hi(gv[k][h]), bf16_hi(uv[k][h]), a1, b1);
+              vg[h] = pack_bf16x2(a0, a1);
+              vu[h] = pack_bf16x2(b0, b1);
+            }
+            st_put(og, row, 2u * (uint32_t)col, col < f, vg);
+            st_put(ou, row, 2u * (uint32_t)col, col < f, vu);
+          }
         }
-      }
+      });
+}
+
+// bf16 rows of a finished tile: columns col0 + 128 wn .. of N.
+template <int MT>
+__device__ __forceinline__ void store_tile(const StOut& o, const f32x4 (&acc)[MT][8], int col0, int N) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int col = col0 + 128 * (wave >> 2) + 32 * k + 8 * q;
+      st_put(o, 16 * MT * (wave & 3) + 16 * mt + i, 2u * (uint32_t)col, col < N,
+             st_pack8(acc[mt][2 * k], acc[mt][2 * k + 1]));
     }
-    // the next tile's copies are counted together with these stores, and its
-    // first copies overwrite slots that other waves may still read
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-  }
 }
 
 // dx tiles: [dg | du] against rows of W1, then of W3, in one accumulator.
@@ -116,45 +140,29 @@ __global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __rest
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
   __shared__ int pre[ST_MAXN + 1];
   const int total = st_prefix(offsets, n, Cfg::BM, pre) * ntn;
-  const StRange rg = st_range(total, blockIdx.x, gridDim.x);
-  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave & 3, wn = wave >> 2;
-  for (int L = rg.begin; L < rg.end; L += rg.step) {
-    const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
-    StCtx<Cfg> c;
-    st_setup(c, ring);
-    const uint32_t ld = (uint32_t)f * 2;
-    const int64_t arow = (int64_t)t.r0 * f, brow = ((int64_t)t.e * d + 256 * t.nt) * f;
-    const int cols = min(ST_BN, d - 256 * t.nt);
-    st_rows<Cfg::BM>(c.a[0], dg + arow, ld, t.R, ld);
-    st_rows<Cfg::BM>(c.a[1], du + arow, ld, t.R, ld);
-    st_rows<ST_BN>(c.b[0], w1 + brow, ld, cols, ld);
-    st_rows<ST_BN>(c.b[1], w3 + brow, ld, cols, ld);
-    c.nst1 = (f + 31) / 32;
-    c.nst = 2 * c.nst1;
-    c.kvals = f;
-    f32x4 acc[MT][8];
-    st_clear<Cfg>(acc);
-    st_accum(c, ring, acc);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int row = 16 * MT * wm + 16 * mt + i;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int col = 256 * t.nt + 128 * wn + 16 * k + 4 * q;
-        if (row < t.R && col < d)
-          *reinterpret_cast<u32x2*>(dx + (int64_t)(t.r0 + row) * d + col) =
-              pack_bf16x4(acc[mt][k][0], acc[mt][k][1], acc[mt][k][2], acc[mt][k][3]);
-      }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-  }
+  st_run<Cfg>(
+      total, ring,
+      [&](int L, StCtx<Cfg>& c) {
+        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+        const uint32_t ld = (uint32_t)f * 2;
+        const int64_t arow = (int64_t)t.r0 * f, brow = ((int64_t)t.e * d + 256 * t.nt) * f;
+        const int cols = min(ST_BN, d - 256 * t.nt);
+        st_rows<Cfg::BM>(c.a[0], dg + arow, ld, t.R, ld);
+        st_rows<Cfg::BM>(c.a[1], du + arow, ld, t.R, ld);
+        st_rows<ST_BN>(c.b[0], w1 + brow, ld, cols, ld);
+        st_rows<ST_BN>(c.b[1], w3 + brow, ld, cols, ld);
+        c.nst1 = (f + 63) / 64;
+        c.nst = 2 * c.nst1;
+        c.kvals = f;
+      },
+      [&](int L, f32x4 (&acc)[MT][8]) {
+        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+        store_tile<MT>(st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R), acc, 256 * t.nt, d);
+      });
 }
 
 // One weight gradient C_e [M][N] = P^T Q over the segment's rows, P [rows][M],
-// Q [rows][N]; C NULL: not wanted.
+// Q [rows][N].
 struct WeightGrad {
   const bf16_t* P;
   const bf16_t* Q;
@@ -177,58 +185,47 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
     tiles[k] = k < nm ? ((w.m[k].M + 255) / 256) * ((w.m[k].N + 255) / 256) : 0;
     per += tiles[k];
   }
-  const StRange rg = st_range(n * per, blockIdx.x, gridDim.x);
-  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave & 3, wn = wave >> 2;
-  for (int L = rg.begin; L < rg.end; L += rg.step) {
-    const int e = L / per;
-    int at = L - e * per;
-    WeightGrad m = w.m[0];
+  struct Where {
+    WeightGrad m;
+    int e, tm, tn;
+  };
+  auto where = [&](int L) {
+    Where r;
+    r.e = L / per;
+    int at = L - r.e * per;
+    r.m = w.m[0];
     if (at >= tiles[0]) {
       at -= tiles[0];
-      m = w.m[1];
+      r.m = w.m[1];
       if (at >= tiles[1]) {
         at -= tiles[1];
-        m = w.m[2];
+        r.m = w.m[2];
       }
     }
     // groups of 8 row tiles run through the column tiles together
-    const int nmt = (m.M + 255) / 256, nnt = (m.N + 255) / 256;
+    const int nmt = (r.m.M + 255) / 256, nnt = (r.m.N + 255) / 256;
     const int mg = at / (ST_GM * nnt), rem = at - mg * ST_GM * nnt;
     const int gsz = min(ST_GM, nmt - mg * ST_GM);
-    const int tn = rem / gsz, tm = mg * ST_GM + (rem - tn * gsz);
-    const int o = offsets[e], cnt = offsets[e + 1] - o;
-    f32x4 acc[4][8];
-    st_clear<Cfg>(acc);
-    const uint32_t la = (uint32_t)m.M * 2, lb = (uint32_t)m.N * 2;
-    // 32-bit descriptors: rows in chunks of at most 2 GiB of the wider operand
-    const int chunk = (int)min((uint32_t)cnt, (0x7FFFFFFFu / max(la, lb)) & ~31u);
-    for (int k0 = 0; k0 < cnt; k0 += chunk) {
-      StCtx<Cfg> c;
-      st_setup(c, ring);
-      const int rows = min(chunk, cnt - k0);
-      st_panel<256>(c.a[0], m.P + (int64_t)(o + k0) * m.M, la, rows, 256 * tm, m.M);
-      st_panel<256>(c.b[0], m.Q + (int64_t)(o + k0) * m.N, lb, rows, 256 * tn, m.N);
-      c.nst = c.nst1 = (rows + 31) / 32;
-      c.kvals = rows;
-      st_accum(c, ring, acc);
-      __syncthreads();
-    }
-    bf16_t* C = m.C + (int64_t)e * m.M * m.N;
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const int row = 256 * tm + 64 * wm + 16 * mt + i;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int col = 256 * tn + 128 * wn + 16 * k + 4 * q;
-        if (row < m.M && col < m.N)
-          *reinterpret_cast<u32x2*>(C + (int64_t)row * m.N + col) =
-              pack_bf16x4(acc[mt][k][0], acc[mt][k][1], acc[mt][k][2], acc[mt][k][3]);
-      }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  }
+    r.tn = rem / gsz;
+    r.tm = mg * ST_GM + (rem - r.tn * gsz);
+    return r;
+  };
+  st_run<Cfg>(
+      n * per, ring,
+      [&](int L, StCtx<Cfg>& c) {
+        const Where r = where(L);
+        const int o = __builtin_amdgcn_readfirstlane(offsets[r.e]);
+        const int cnt = __builtin_amdgcn_readfirstlane(offsets[r.e + 1]) - o;
+        st_panel<256>(c.a[0], r.m.P + (int64_t)o * r.m.M, (uint32_t)r.m.M * 2, cnt, 256 * r.tm, r.m.M);
+        st_panel<256>(c.b[0], r.m.Q + (int64_t)o * r.m.N, (uint32_t)r.m.N * 2, cnt, 256 * r.tn, r.m.N);
+        c.nst = c.nst1 = (cnt + 63) / 64;
+        c.kvals = cnt;
+      },
+      [&](int L, f32x4 (&acc)[4][8]) {
+        const Where r = where(L);
+        bf16_t* C = r.m.C + ((int64_t)r.e * r.m.M + 256 * r.tm) * r.m.N;
+        store_tile<4>(st_out(C, (int64_t)r.m.N * 2, min(256, r.m.M - 256 * r.tm)), acc, 256 * r.tn, r.m.N);
+      });
 }
 
 // ---------------------------------------------------------------------------
@@ -411,14 +408,15 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
     }
     return hipSuccess;
   }
-  // one workgroup per compute unit walks its share of the tiles
-  const int cus = device_cus();
   auto row_grid = [&](int bm, int ntn) {
     const int64_t blocks = std::min<int64_t>(p.rows_max / bm + std::min<int64_t>(p.n, p.rows_max), p.rows_max);
-    return dim3((unsigned)std::min<int64_t>(blocks * ntn, cus));
+    return dim3(st_grid(blocks * ntn));
   };
-  // 256-row tiles where the mean segment fills them, else 128-row tiles
-  const bool tall = p.tk() / p.E >= 192;
+  // Tile height from the expected segment: 256 rows where it fills them; below,
+  // the weights' stream bounds the product, and a height that holds a whole
+  // segment reads them once: 192 rows around a mean of 128.
+  const int64_t mean = p.tk() / p.E;
+  const int mt = mean >= 256 ? 4 : mean > 96 ? 3 : 2;
   const bf16_t* DG = (const bf16_t*)dgp;
   const bf16_t* DU = (const bf16_t*)dup;
   if (gate) {
@@ -429,8 +427,12 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
                          ntn);
       return hipGetLastError();
     };
-    if (p.d % 32 == 0) e = tall ? go(gate_grad_bf16<4, false>, 256) : go(gate_grad_bf16<2, false>, 128);
-    else e = tall ? go(gate_grad_bf16<4, true>, 256) : go(gate_grad_bf16<2, true>, 128);
+    if (p.d % 64 == 0)
+      e = mt == 4 ? go(gate_grad_bf16<4, false>, 256)
+                  : mt == 3 ? go(gate_grad_bf16<3, false>, 192) : go(gate_grad_bf16<2, false>, 128);
+    else
+      e = mt == 4 ? go(gate_grad_bf16<4, true>, 256)
+                  : mt == 3 ? go(gate_grad_bf16<3, true>, 192) : go(gate_grad_bf16<2, true>, 128);
     if (e != hipSuccess) return e;
   }
   if (dx) {
@@ -440,8 +442,12 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
                          (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn);
       return hipGetLastError();
     };
-    if (p.f % 32 == 0) e = tall ? go(input_grad_bf16<4, false>, 256) : go(input_grad_bf16<2, false>, 128);
-    else e = tall ? go(input_grad_bf16<4, true>, 256) : go(input_grad_bf16<2, true>, 128);
+    if (p.f % 64 == 0)
+      e = mt == 4 ? go(input_grad_bf16<4, false>, 256)
+                  : mt == 3 ? go(input_grad_bf16<3, false>, 192) : go(input_grad_bf16<2, false>, 128);
+    else
+      e = mt == 4 ? go(input_grad_bf16<4, true>, 256)
+                  : mt == 3 ? go(input_grad_bf16<3, true>, 192) : go(input_grad_bf16<2, true>, 128);
     if (e != hipSuccess) return e;
   }
   WeightGrads w{};
@@ -456,7 +462,7 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
   want(x, DG, dw1, p.d, p.f);
   want(x, DU, dw3, p.d, p.f);
   if (nm) {
-    hipLaunchKernelGGL(weight_grad_bf16, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(ST_NT), 0, st, w, nm, offsets,
+    hipLaunchKernelGGL(weight_grad_bf16, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, offsets,
                        p.n);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }

@@ -240,12 +240,12 @@ __device__ __forceinline__ void i8_values(const i32x4& p1, const i32x4& p3, floa
 
 // Tiles of 64 MT rows x 256 weight columns (GATED: 128 output columns of both
 // matrices) for segments of more than `lo` rows.
-template <int MT, bool GATED>
-using I8Cfg = StCfg<MT, ST_ROWS, ST_PACK, i32x4, 1, GATED, false>;
+template <int MT, bool GATED, bool F32OUT>
+using I8Cfg = StCfg<MT, ST_ROWS, ST_PACK, i32x4, 1, GATED, false, MT * (F32OUT ? 8 : 4) / (GATED ? 2 : 1)>;
 
 template <int MT, bool GATED, bool F32OUT>
 __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
-  using Cfg = I8Cfg<MT, GATED>;
+  using Cfg = I8Cfg<MT, GATED, F32OUT>;
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
   __shared__ int pre[ST_MAXN + 1];
   __shared__ int32_t whole[2];
@@ -253,52 +253,63 @@ __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
   __syncthreads();
   const int32_t* offsets = p.offsets ? p.offsets : whole;
   const int total = st_prefix(offsets, p.n, Cfg::BM, pre, p.lo) * ntn;
-  const StRange rg = st_range(total, blockIdx.x, gridDim.x);
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 3, wn = wave >> 2;
   const uint32_t run = (uint32_t)p.kt * 1024u;
-  for (int L = rg.begin; L < rg.end; L += rg.step) {
-    const StTile t = st_tile_at(L, offsets, p.n, ntn, Cfg::BM, pre);
-    StCtx<Cfg> c;
-    st_setup(c, ring);
-    st_rows<Cfg::BM>(c.a[0], p.a + (int64_t)t.r0 * p.lda, (uint32_t)p.lda, t.R, (uint32_t)p.K);
-    const int64_t eo = (int64_t)t.e * p.ntiles * run;
-    if (GATED) {
-      st_pack(c.b[0], 0, p.b1 + eo, 8 * t.nt, p.ntiles, run);
-      st_pack(c.b[0], 1, p.b3 + eo, 8 * t.nt, p.ntiles, run);
-    } else {
-      st_pack(c.b[0], 0, p.b1 + eo, 16 * t.nt, p.ntiles, run);
-      st_pack(c.b[0], 1, p.b1 + eo, 16 * t.nt + 8, p.ntiles, run);
-    }
-    c.nst = c.nst1 = p.kt;
-    c.kvals = 0;
-    i32x4 acc[MT][8];
-    st_clear<Cfg>(acc);
-    st_accum(c, ring, acc);
-    float sr[MT];
+  st_run<Cfg>(
+      total, ring,
+      [&](int L, StCtx<Cfg>& c) {
+        const StTile t = st_tile_at(L, offsets, p.n, ntn, Cfg::BM, pre);
+        st_rows<Cfg::BM>(c.a[0], p.a + (int64_t)t.r0 * p.lda, (uint32_t)p.lda, t.R, (uint32_t)p.K);
+        const int64_t eo = (int64_t)t.e * p.ntiles * run;
+        if (GATED) {
+          st_pack(c.b[0], 0, p.b1 + eo, 8 * t.nt, p.ntiles, run);
+          st_pack(c.b[0], 1, p.b3 + eo, 8 * t.nt, p.ntiles, run);
+        } else {
+          st_pack(c.b[0], 0, p.b1 + eo, 16 * t.nt, p.ntiles, run);
+          st_pack(c.b[0], 1, p.b1 + eo, 16 * t.nt + 8, p.ntiles, run);
+        }
+        c.nst = c.nst1 = (p.kt + 1) / 2;   // an odd last block meets zeros past its run
+        c.kvals = 0;
+      },
+      [&](int L, i32x4 (&acc)[MT][8]) {
+        const StTile t = st_tile_at(L, offsets, p.n, ntn, Cfg::BM, pre);
+        constexpr int ES = F32OUT ? 4 : 2;
+        const StOut out = st_out((char*)p.c + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
+        float sr[MT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) sr[mt] = p.sa[t.r0 + min(16 * MT * wm + 16 * mt + i, t.R - 1)];
-    const float* s1 = p.s1 + (int64_t)t.e * p.N;
-    const float* s3 = GATED ? p.s3 + (int64_t)t.e * p.N : nullptr;
+        for (int mt = 0; mt < MT; ++mt) sr[mt] = p.sa[t.r0 + min(16 * MT * wm + 16 * mt + i, t.R - 1)];
+        const float* s1 = p.s1 + (int64_t)t.e * p.N;
+        const float* s3 = GATED ? p.s3 + (int64_t)t.e * p.N : nullptr;
+        const int col0 = GATED ? 128 * t.nt + 64 * wn : 256 * t.nt + 128 * wn;
 #pragma unroll
-    for (int k = 0; k < (GATED ? 4 : 8); ++k) {
-      const int col = (GATED ? 128 * t.nt + 64 * wn : 256 * t.nt + 128 * wn) + 16 * k + 4 * q;
-      if (col >= p.N) continue;
-      const f32x4 c1 = *reinterpret_cast<const f32x4*>(s1 + col);
-      const f32x4 c3 = GATED ? *reinterpret_cast<const f32x4*>(s3 + col) : c1;
+        for (int k = 0; k < (GATED ? 4 : 8); k += 2) {
+          f32x4 c1[2], c3[2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int row = 16 * MT * wm + 16 * mt + i;
-        if (row >= t.R) continue;
-        float o[4];
-        i8_values<GATED>(acc[mt][k], acc[mt][GATED ? k + 4 : k], sr[mt], c1, c3, o);
-        i8_store<F32OUT>(p.c, (int64_t)(t.r0 + row) * p.N + col, o);
-      }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-  }
+          for (int h = 0; h < 2; ++h) {
+            const int col = min(col0 + 16 * (k + h) + 4 * q, p.N - 4);
+            c1[h] = *reinterpret_cast<const f32x4*>(s1 + col);
+            c3[h] = GATED ? *reinterpret_cast<const f32x4*>(s3 + col) : c1[h];
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int row = 16 * MT * wm + 16 * mt + i;
+            float x[4], y[4];
+            i8_values<GATED>(acc[mt][k], acc[mt][GATED ? k + 4 : k], sr[mt], c1[0], c3[0], x);
+            i8_values<GATED>(acc[mt][k + 1], acc[mt][GATED ? k + 5 : k + 1], sr[mt], c1[1], c3[1], y);
+            if (F32OUT) {
+              const int at = col0 + 16 * k + 4 * q;
+              st_put(out, row, 4u * (uint32_t)at, at < p.N, __builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]}));
+              st_put(out, row, 4u * (uint32_t)(at + 16), at + 16 < p.N,
+                     __builtin_bit_cast(u32x4, f32x4{y[0], y[1], y[2], y[3]}));
+            } else {
+              const int at = col0 + 16 * k + 8 * q;
+              st_put(out, row, 2u * (uint32_t)at, at < p.N, st_pack8(x, y));
+            }
+          }
+        }
+      });
 }
 
 // Segments of at most 16 MT rows: a stream of the packed weights.  Workgroup
@@ -405,7 +416,6 @@ constexpr int I8_THIN_MEAN = 64;   // expected rows from which every segment tak
 // mean: expected rows of a segment; most: bound of one segment's rows.
 template <bool GATED, bool F32OUT>
 static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t rows_max, hipStream_t st) {
-  const int cus = device_cus();
   hipError_t e;
   const bool stream = mean <= I8_THIN_MEAN;
   if (stream) {
@@ -414,7 +424,7 @@ static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t r
     const bool one = most <= 16;   // 16-row tiles alone
     // four tiles of 16 columns a workgroup where that still makes a workgroup
     // per compute unit, else one (gated: one of each matrix)
-    const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= cus;
+    const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
     auto go = [&](auto kernel, int cols, int ks) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n), dim3(64 * ks), 0, st, p);
       return hipGetLastError();
@@ -433,10 +443,12 @@ static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t r
   const int ntn = (p.N + cols - 1) / cols;
   auto go = [&](auto kernel, int bm) {
     const int64_t blocks = std::min<int64_t>(rows_max / bm + std::min<int64_t>(p.n, rows_max), rows_max);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(blocks * ntn, cus)), dim3(ST_NT), 0, st, p, ntn);
+    hipLaunchKernelGGL(kernel, dim3(st_grid(blocks * ntn)), dim3(ST_NT), 0, st, p, ntn);
     return hipGetLastError();
   };
-  return mean >= 192 ? go(i8_tile<4, GATED, F32OUT>, 256) : go(i8_tile<2, GATED, F32OUT>, 128);
+  // tile height from the expected segment, as in the backward pass
+  if (mean >= 256) return go(i8_tile<4, GATED, F32OUT>, 256);
+  return mean > 96 ? go(i8_tile<3, GATED, F32OUT>, 192) : go(i8_tile<2, GATED, F32OUT>, 128);
 }
 
 hipError_t launch_quantize_rows(const void* x, int dtype, int64_t rows, int K, int64_t ldq, void* q, float* s,

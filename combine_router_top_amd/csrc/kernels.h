@@ -81,8 +81,14 @@ hipError_t launch_combine(const Prob& p, const void* y_packed, const int32_t* in
 hipError_t launch_combine_backward(const Prob& p, const void* dy, const void* y_packed, const int32_t* inv,
                                    const float* w, void* dy_packed, float* dw, hipStream_t st);
 
-// Compute units of the current device.
+// Compute units of the current device, and the grid of a persistent kernel over
+// `tiles` tiles: a multiple of 8 (one share per XCD) of at most that many.
 int device_cus();
+inline unsigned st_grid(int64_t tiles) {
+  const int64_t most = device_cus() >= 8 ? device_cus() / 8 * 8 : 8;
+  const int64_t want = (tiles + 7) / 8 * 8;
+  return (unsigned)(want < most ? (want < 8 ? 8 : want) : most);
+}
 
 // expert_backward.hip: gradients of the expert FFNs (any output may be NULL).
 // T = 0 writes zeros to the wanted weight gradients.

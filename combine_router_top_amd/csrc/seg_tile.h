@@ -2,31 +2,47 @@
 // in any of three ways (gfx950): the products of the experts' backward pass
 // (bf16) and of the 8-bit experts (int8) share this core.
 //
-// A workgroup of 8 waves computes a (64 MT) x 256 tile, MT = 2 or 4, in stages
-// of 64 bytes of K (32 bf16 or 64 int8 values, one 16x16 MFMA k-step).  Wave
-// (wm, wn) = (w & 3, w >> 2) multiplies 16 MT tile rows by 128 tile columns.
-// Both operands of a stage are copied from memory straight into a slot of an
-// LDS ring (16 bytes per lane and instruction); a wave holds the fragments of
-// the stage it multiplies in registers, so all other slots are in flight or
-// wait.  A stage is released by an explicit wait for the wave's own copies and
-// one barrier, which also frees the slot that every wave has read.
+// A workgroup of 8 waves computes (64 MT) x 256 tiles, MT = 2, 3 or 4, in
+// stages of 128 bytes of K (64 bf16 or 128 int8 values, two 16x16 MFMA
+// k-steps).  Wave (wm, wn) = (w & 3, w >> 2) multiplies 16 MT tile rows by 128
+// tile columns.  Both operands of a stage are copied from memory straight into
+// LDS (16 bytes per lane and instruction), the rows into a ring of NA slots and
+// the columns into one of NB.  While a wave multiplies one k-step from
+// registers it reads the fragments of the next.  A stage costs one barrier, in
+// its middle: by then every wave holds the stage's second half in registers,
+// so its slots may be refilled, and the wait before it has seen the next
+// stage's copies arrive.
+//
+// Why stages of 128 bytes: an operand whose rows are contiguous along K is read
+// in pieces of one stage, and the address unit of a compute unit spends about
+// 44 cycles on an instruction of sixteen 64-byte pieces against 22 on one of
+// eight 128-byte pieces (whole cache lines, half the requests to L2).  With
+// 64-byte stages that unit was busy 77% of the time and bounded the kernel.
 //
 // Operand layouts in memory and in a slot (W tile rows or columns):
-//   ST_ROWS   row r of the operand is contiguous along K: 64-byte rows, 16-byte
-//             piece q kept at q ^ dt_swa(r); a fragment is one 16-byte read.
+//   ST_ROWS   row r of the operand is contiguous along K: 128-byte rows, 16-byte
+//             piece q kept at q ^ ((r >> 1) & 7), so that every pass of a
+//             fragment read (8 rows of one piece and 8 of its neighbour, see
+//             dma_tile.h) meets 16 distinct bank groups.
 //   ST_PANEL  row-major [K][ld], the operand's index contiguous (the products
-//             that sum over a segment's rows): half-panels of 32 K-rows x 128
-//             columns, piece q of row j kept at q ^ 2 sigma(j); a fragment is
-//             two transposing 8-byte reads.  bf16 only.
+//             that sum over a segment's rows): half-panels of 64 K-rows x 128
+//             columns, piece q of row j kept at q ^ 2 sigma(j) as in dma_big.h;
+//             a fragment is two transposing 8-byte reads.  bf16 only.
 //   ST_PACK   int8 weights in MFMA operand order, 1 KB per 16 columns x 64 K:
 //             copied and read linearly, without bank conflicts.
-// Both swizzles are those of dma_tile.h and dma_big.h, applied by the lane's
-// choice of the source piece.
 //
 // The MFMA takes the column operand first, so a product lane holds 4
 // consecutive columns of one row: lane (i, g) = (l % 16, l / 16) of wave
 // (wm, wn) holds in acc[mt][t] row 16 MT wm + 16 mt + i, columns 128 wn + 16 t
-// + 4 g .. + 3.
+// + 4 g .. + 3.  st_swap_pair exchanges two column tiles between lane groups so
+// that a lane holds 8 consecutive columns: 16-byte stores, whole 64-byte
+// sectors per row.
+//
+// Workgroups are persistent (one per compute unit).  The first stages of the
+// next tile are copied before the epilogue of this one, and its first waits
+// count the epilogue's stores as outstanding (loads and stores retire in
+// order), so that the stores of a tile drain while the next is loaded and
+// multiplied.
 #pragma once
 
 #include "common.h"
@@ -41,60 +57,57 @@ enum { ST_ROWS = 0, ST_PANEL = 1, ST_PACK = 2 };
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int ST_BN = 256;     // tile columns
-constexpr int ST_KB = 64;      // bytes of K per stage
+constexpr int ST_KB = 128;     // bytes of K per stage
 constexpr int ST_NT = 512;     // threads
 
-// One operand of W tile rows (or columns): per-thread state of its copies.
+// One operand of W tile rows (or columns): state of its copies.
 template <int L, int W>
 struct StOp {
-  static_assert(W == 256 || W == 128, "tile sides of 128 or 256");
-  static constexpr int C = W / 128;              // copies per wave per stage
+  static constexpr int C = W / 64;               // copies per wave per stage
   static constexpr int BYTES = W * ST_KB;        // bytes of a stage
-  __amdgpu_buffer_rsrc_t r[L == ST_PACK ? C : 1];
-  uint32_t v[L == ST_PANEL ? 1 : C];             // lane source offsets at stage 0
-  uint32_t step;                                 // source bytes per stage
-  uint32_t sub;                                  // ST_PANEL: bytes of 4 K-rows
-  int dst;                                       // this wave's first destination in the region
+  const char* base[L == ST_PACK ? 2 : 1];        // wave-uniform
+  uint32_t v[L == ST_PANEL ? 2 : 1];             // lane source offsets at stage 0
+  uint32_t ld;                                   // bytes between rows (ST_ROWS) or K-rows (ST_PANEL)
+  uint32_t size;                                 // descriptor bytes (ST_ROWS, ST_PACK)
+  int krows;                                     // ST_PANEL: valid K-rows
 };
 
-// ST_ROWS: `rows` valid rows (>= 1) of `ld` bytes from base; K bytes per row.
-// Rows past the last valid one repeat it.
+// ST_ROWS: `rows` valid rows (>= 1) of `ld` bytes from base, kbytes of each
+// read.  Rows past the last valid one lie outside the descriptor and read zeros.
 template <int W>
 __device__ __forceinline__ void st_rows(StOp<ST_ROWS, W>& o, const void* base, uint32_t ld, int rows,
                                         uint32_t kbytes) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  o.r[0] = gc_rsrc(base, (uint32_t)(min(rows, W) - 1) * ld + kbytes);
-#pragma unroll
-  for (int c = 0; c < W / 128; ++c) {
-    const int r = 16 * (wave + 8 * c) + (lane >> 2);
-    o.v[c] = (uint32_t)min(r, rows - 1) * ld + 16u * (uint32_t)((lane & 3) ^ dt_swa(r));
-  }
-  o.step = ST_KB;
-  o.sub = 0;
-  o.dst = 1024 * wave;
+  // copy c of wave w: rows 64 c + 8 w .. + 7 (the swizzle does not depend on c)
+  const int r = 8 * wave + (lane >> 3);
+  o.base[0] = (const char*)base;
+  o.v[0] = (uint32_t)r * ld + 16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
+  o.ld = ld;
+  o.size = (uint32_t)(min(rows, W) - 1) * ld + kbytes;
 }
 
 // ST_PANEL: K-rows [0, krows) of ld2 bytes from base, columns col0 .. col0 + W
-// - 1 of which those below ncols are read; K-rows past krows read zeros (the
-// descriptor ends there).  krows * ld2 < 2^32.
+// - 1 of which those below ncols are read; K-rows past krows read zeros.
 template <int W>
 __device__ __forceinline__ void st_panel(StOp<ST_PANEL, W>& o, const void* base, uint32_t ld2,
                                          int krows, int col0, int ncols) {
+  static_assert(W == 256, "two half-panels");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // W = 256: wave w copies K-rows 8 (w % 4) .. + 7 of half-panel w / 4 in two
-  // copies; W = 128: K-rows 4 w .. + 3 of the one half-panel
-  const int hp = W == 256 ? wave >> 2 : 0;
-  const int j0 = W == 256 ? 8 * (wave & 3) : 4 * wave;
-  const int j = j0 + (lane >> 4);
-  const int sig = (j & 3) | (((j >> 3) & 1) << 2);
-  const int col = col0 + 128 * hp + 8 * ((lane & 15) ^ (2 * sig));
-  o.r[0] = gc_rsrc(base, (uint32_t)krows * ld2);
-  o.v[0] = col < ncols ? (uint32_t)j * ld2 + 2u * (uint32_t)col : GC_OOR;
-  o.step = 32 * ld2;
-  o.sub = 4 * ld2;
-  o.dst = hp * BD_HP + j0 * BD_HPROW;
+  // copy c of wave w: K-rows 16 (w % 4) + 4 c .. + 3 of half-panel w / 4;
+  // sigma depends on c through c / 2
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int sig = ((lane >> 4) & 3) | (h << 2);
+    const int col = col0 + 128 * (wave >> 2) + 8 * ((lane & 15) ^ (2 * sig));
+    const int j = 16 * (wave & 3) + 8 * h + (lane >> 4);
+    o.v[h] = col < ncols ? (uint32_t)j * ld2 + 2u * (uint32_t)col : GC_OOR;
+  }
+  o.base[0] = (const char*)base;
+  o.ld = ld2;
+  o.krows = krows;
+  o.size = 0;
 }
 
 // ST_PACK, one 128-column half c: 16-column tiles nt0 .. nt0 + 7 of a packed
@@ -103,52 +116,63 @@ __device__ __forceinline__ void st_panel(StOp<ST_PANEL, W>& o, const void* base,
 template <int W>
 __device__ __forceinline__ void st_pack(StOp<ST_PACK, W>& o, int c, const void* base, int nt0, int ntiles,
                                         uint32_t run) {
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // the descriptor starts at this wave's tile, so that its offsets stay below one run
   const int nt = min(nt0 + wave, ntiles - 1);
-  o.r[c] = gc_rsrc((const char*)base + (int64_t)nt * run, run);
-  o.v[c] = 16u * (uint32_t)lane;
-  o.step = 1024;
-  o.sub = 0;
-  o.dst = 1024 * wave;
+  o.base[c] = (const char*)base + (int64_t)nt * run;
+  o.v[0] = 16u * (uint32_t)(threadIdx.x & 63);
+  o.ld = 0;
+  o.size = run;
 }
 
-// The copies of stage st of one operand into its region at LDS address lds.
+// The copies of stage st of one operand into its slot at LDS address lds.
 template <int L, int W>
-__device__ __forceinline__ void st_issue(const StOp<L, W>& o, uint32_t lds, uint32_t st) {
-  const uint32_t so = st * o.step;
+__device__ __forceinline__ void st_issue(const StOp<L, W>& o, uint32_t lds, int st) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if constexpr (L == ST_ROWS) {
+    const __amdgpu_buffer_rsrc_t r = gc_rsrc(o.base[0], o.size);
 #pragma unroll
-  for (int c = 0; c < W / 128; ++c) {
-    if constexpr (L == ST_PANEL) bd_copy16(o.r[0], lds + o.dst + 1024 * c, o.v[0], so + c * o.sub);
-    else if constexpr (L == ST_ROWS) bd_copy16(o.r[0], lds + o.dst + 8192 * c, o.v[c], so);
-    else bd_copy16(o.r[c], lds + o.dst + 8192 * c, o.v[c], so);
+    for (int c = 0; c < W / 64; ++c)
+      bd_copy16(r, lds + 1024 * wave + 8192 * c, o.v[0], (uint32_t)st * ST_KB + (uint32_t)(64 * c) * o.ld);
+  } else if constexpr (L == ST_PANEL) {
+    // a descriptor per stage: a segment may span more than 32 bits
+    const __amdgpu_buffer_rsrc_t r =
+        gc_rsrc(o.base[0] + (int64_t)st * 64 * o.ld, (uint32_t)min(64, o.krows - 64 * st) * o.ld);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      bd_copy16(r, lds + 16384 * (wave >> 2) + 4096 * (wave & 3) + 1024 * c, o.v[c >> 1], (uint32_t)(4 * (c & 1)) * o.ld);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      bd_copy16(gc_rsrc(o.base[c >> 1], o.size), lds + 2048 * (wave + 8 * (c >> 1)) + 1024 * (c & 1), o.v[0],
+                (uint32_t)st * 2048u + 1024u * (c & 1));
   }
 }
 
-// Lane offset, inside the operand's region, of the fragment of 16-row tile 0
-// of a wave that starts at tile t0.
+// Lane offset, inside the operand's slot, of the fragment of a wave's first
+// 16-wide tile t0 for k-step 0.
 template <int L>
 __device__ __forceinline__ int st_lane(int t0) {
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  if constexpr (L == ST_ROWS) return (16 * t0 + i) * ST_KB + 16 * (g ^ dt_swa(i));
-  if constexpr (L == ST_PACK) return 1024 * t0 + 16 * lane;
+  if constexpr (L == ST_ROWS) return (16 * t0 + i) * ST_KB + 16 * (g ^ ((i >> 1) & 7));
+  if constexpr (L == ST_PACK) return 2048 * t0 + 16 * lane;
   const int sig = (i >> 2) | ((g & 1) << 2);
   const int base = (8 * g + (i >> 2)) * BD_HPROW + 32 * sig + 8 * (i & 3);
-  return (t0 >> 3) * BD_HP + (base ^ (32 * (t0 & 7)));
+  return (t0 >> 3) * 16384 + (base ^ (32 * (t0 & 7)));
 }
 
-// Fragment of the wave's tile t (16 bytes).  ST_PANEL tiles of a wave lie in
-// one half-panel and t0 is a multiple of the wave's tile count, so the tile
-// index enters by XOR.
+// Fragment (16 bytes) of the wave's tile t and k-step ks.  ST_PANEL tiles of a
+// wave lie in one half-panel and t0 is a multiple of the wave's tile count, so
+// the tile index enters by XOR, as does the k-step of ST_ROWS.
 template <int L>
-__device__ __forceinline__ u32x4 st_frag(const char* region, int lane_off, int t) {
+__device__ __forceinline__ u32x4 st_frag(const char* slot, int lane_off, int ks, int t) {
   if constexpr (L == ST_PANEL) {
-    const char* p = region + (lane_off ^ (32 * t));
+    const char* p = slot + (lane_off ^ (32 * t)) + 8192 * ks;
     const s16x4 lo = dt_tr16(p), hi = dt_tr16(p + 4 * BD_HPROW);
     return __builtin_bit_cast(u32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  } else if constexpr (L == ST_ROWS) {
+    return *reinterpret_cast<const u32x4*>(slot + (lane_off ^ (64 * ks)) + 2048 * t);
   } else {
-    return *reinterpret_cast<const u32x4*>(region + lane_off + 1024 * t);
+    return *reinterpret_cast<const u32x4*>(slot + lane_off + 1024 * ks + 2048 * t);
   }
 }
 
@@ -161,36 +185,37 @@ __device__ __forceinline__ i32x4 st_mfma(const u32x4& a, const u32x4& b, const i
 }
 
 // Tile configuration.  NP phases of operands follow one another along K (the
-// input gradient sums two products).  SPLIT: the 256 columns are 128 of one
-// packed matrix and the same 128 of a second (gate and up products of one h
-// column meet in one lane: acc[mt][t] and acc[mt][t + 4]).  KT: K is not a
-// multiple of a stage; the fragments of a phase's last stage are zeroed past
-// its end (ST_ROWS reads there what follows the row).
-template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, bool KT_>
+// input gradient sums two products); all have the same shape.  SPLIT: the 256
+// columns are 128 of one packed matrix and the same 128 of a second (gate and
+// up products of one h column meet in one lane: acc[mt][t] and acc[mt][t + 4]).
+// KT: K is not a multiple of a stage; the fragments past its end are zeroed
+// (ST_ROWS reads there what follows the row).  STORES: store instructions of a
+// wave's epilogue, every one of them unconditional.
+template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, bool KT_, int STORES_>
 struct StCfg {
-  static constexpr int MT = MT_, LA = LA_, LB = LB_, NP = NP_;
+  static constexpr int MT = MT_, LA = LA_, LB = LB_, NP = NP_, STORES = STORES_;
   static constexpr bool SPLIT = SPLIT_, KT = KT_;
   typedef AccT_ Acc;
   static constexpr int BM = 64 * MT;
   typedef StOp<LA, BM> A;
   typedef StOp<LB, ST_BN> B;
-  static constexpr int AB = A::BYTES, SLOT = AB + B::BYTES;   // columns follow the rows in a slot
-  static constexpr int NS = MT == 4 ? 4 : 6;                   // ring slots (128 / 144 KB)
-  static constexpr int LDS = NS * SLOT;
-  static constexpr int CNT = A::C + B::C;                      // copies per wave per stage
-  static_assert(MT == 2 || MT == 4, "128- or 256-row tiles");
-  static_assert(NS % 2 == 0, "fragments alternate between two register sets");
+  // slots: the columns (weights, from HBM) three deep where LDS allows
+  static constexpr int NA = MT == 2 ? 3 : 2, NB = MT == 4 ? 2 : 3;
+  static constexpr int AREG = NA * A::BYTES;                   // the column slots follow the row slots
+  static constexpr int LDS = AREG + NB * B::BYTES;             // 144, 144, 128 KB
+  static constexpr int CA = A::C, CB = B::C;                   // copies per wave per stage
+  // copies issued after those of stage s + 1 when stage s reaches its middle
+  static constexpr int LATER = (NB > NA ? CB : 0) + (NA - 2) * (CA + CB);
+  static_assert(NB == NA || NB == NA + 1, "issue order");
 };
 
 template <class Cfg>
 struct StCtx {
   typename Cfg::A a[Cfg::NP];
   typename Cfg::B b[Cfg::NP];
-  int nst1;          // stages of a phase (all phases have the same K)
+  int nst1;          // stages of a phase
   int nst;           // stages in all
-  int kvals;         // K of a phase in elements of 2 bytes (KT only)
-  uint32_t lbase;
-  int ao, bo;        // lane fragment offsets
+  int kvals;         // K of a phase in bf16 elements (KT only)
 };
 
 template <class Cfg>
@@ -198,81 +223,78 @@ struct StFrag {
   u32x4 x[Cfg::MT], w[8];
 };
 
+// The copies of stage st into the slot at LDS address `at`.
 template <class Cfg>
-__device__ __forceinline__ void st_issue_all(const StCtx<Cfg>& c, int slot, int st) {
-  uint32_t base = c.lbase;
-  asm volatile("" : "+s"(base));   // one base, so that no address per slot stays in registers
-  base += (uint32_t)(slot * Cfg::SLOT);
-  if constexpr (Cfg::NP == 1) {
-    st_issue(c.a[0], base, (uint32_t)st);
-    st_issue(c.b[0], base + Cfg::AB, (uint32_t)st);
-  } else {
-    const bool second = st >= c.nst1;
-    if (second) {
-      st_issue(c.a[1], base, (uint32_t)(st - c.nst1));
-      st_issue(c.b[1], base + Cfg::AB, (uint32_t)(st - c.nst1));
-    } else {
-      st_issue(c.a[0], base, (uint32_t)st);
-      st_issue(c.b[0], base + Cfg::AB, (uint32_t)st);
-    }
-  }
+__device__ __forceinline__ void st_issue_a(const StCtx<Cfg>& c, uint32_t at, int st) {
+  if (Cfg::NP > 1 && st >= c.nst1) st_issue(c.a[Cfg::NP - 1], at, st - c.nst1);
+  else st_issue(c.a[0], at, st);
+}
+template <class Cfg>
+__device__ __forceinline__ void st_issue_b(const StCtx<Cfg>& c, uint32_t at, int st) {
+  if (Cfg::NP > 1 && st >= c.nst1) st_issue(c.b[Cfg::NP - 1], at, st - c.nst1);
+  else st_issue(c.b[0], at, st);
 }
 
-// Whether this lane's k (8 bf16 from 8 g) lie past the end of stage st's phase.
+// Whether this lane's k (8 bf16 from 8 g) of k-step ks lie past the end of
+// stage st's phase.
 template <class Cfg>
-__device__ __forceinline__ bool st_past(const StCtx<Cfg>& c, int st) {
+__device__ __forceinline__ bool st_past(const StCtx<Cfg>& c, int st, int ks) {
   if constexpr (!Cfg::KT) return false;
   const int s = Cfg::NP > 1 && st >= c.nst1 ? st - c.nst1 : st;
-  return 32 * s + 8 * (int)((threadIdx.x & 63) >> 4) >= c.kvals;
+  return 64 * s + 32 * ks + 8 * (int)((threadIdx.x & 63) >> 4) >= c.kvals;
+}
+
+// Wait until at most N of this wave's copies and stores are outstanding and its
+// LDS reads have completed, then barrier.
+template <int N>
+__device__ __forceinline__ void st_sync() {
+  static_assert(N < 64, "vmcnt holds six bits");
+  bd_sync<N>();
 }
 
 template <class Cfg>
-__device__ __forceinline__ void st_read_x(const StCtx<Cfg>& c, const char* slot, bool zero, StFrag<Cfg>& f) {
-#pragma unroll
-  for (int mt = 0; mt < Cfg::MT; ++mt) {
-    f.x[mt] = st_frag<Cfg::LA>(slot, c.ao, mt);
-    if (Cfg::KT && zero) f.x[mt] = u32x4{0u, 0u, 0u, 0u};
-  }
-}
+struct StLane {
+  int ao, bo;        // lane fragment offsets in a slot
+  uint32_t lbase;    // LDS address of the ring
+};
+
 template <class Cfg>
-__device__ __forceinline__ void st_read_w(const StCtx<Cfg>& c, const char* slot, bool zero, int t,
-                                          StFrag<Cfg>& f) {
-  const int tt = Cfg::SPLIT ? (t & 3) + 8 * (t >> 2) : t;
-  f.w[t] = st_frag<Cfg::LB>(slot + Cfg::AB, c.bo, tt);
-  if (Cfg::KT && zero) f.w[t] = u32x4{0u, 0u, 0u, 0u};
+__device__ __forceinline__ StLane<Cfg> st_lanes(char* ring) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  StLane<Cfg> l;
+  l.lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
+  l.ao = st_lane<Cfg::LA>(Cfg::MT * (wave & 3));
+  l.bo = st_lane<Cfg::LB>(Cfg::SPLIT ? 4 * (wave >> 2) : 8 * (wave >> 2));
+  return l;
 }
 
-template <int CNT>
-__device__ __forceinline__ void st_sync_n(int n) {
-  if (n >= 5) bd_sync<5 * CNT>();
-  else bd_sync_n<CNT>(n);
-}
-
-// Step st (slot J): F holds its fragments.  Wait for stage st + 1 and meet the
-// other waves (all have read slot J), refill slot J with stage st + NS, then
-// read stage st + 1 into G while F is multiplied.
-template <int J, bool GUARD, class Cfg>
-__device__ __forceinline__ void st_step(const StCtx<Cfg>& c, char* ring, int st, StFrag<Cfg>& F, StFrag<Cfg>& G,
-                                        typename Cfg::Acc (&acc)[Cfg::MT][8]) {
-  constexpr int NS = Cfg::NS, MT = Cfg::MT;
-  if (GUARD && st >= c.nst) return;
-  const bool next = !GUARD || st + 1 < c.nst;
-  if (next) {
-    if (!GUARD) bd_sync<(NS - 2) * Cfg::CNT>();
-    else st_sync_n<Cfg::CNT>(min(c.nst - 2 - st, NS - 2));
-    if (!GUARD || st + NS < c.nst) st_issue_all(c, J % NS, st + NS);
-  }
+// Multiply F; with READ, read k-step ks of stage st into G meanwhile, from the
+// slots at as and bs.
+template <bool READ, class Cfg>
+__device__ __forceinline__ void st_kstep(const StCtx<Cfg>& c, const StLane<Cfg>& l, const char* as, const char* bs,
+                                         int st, int ks, const StFrag<Cfg>& F, StFrag<Cfg>& G,
+                                         typename Cfg::Acc (&acc)[Cfg::MT][8]) {
+  constexpr int MT = Cfg::MT;
+  const bool zero = READ && st_past(c, st, ks);
   __builtin_amdgcn_sched_barrier(0);
-  const char* slot = ring + ((J + 1) % NS) * Cfg::SLOT;
-  const bool zero = st_past(c, st + 1);
-  if (next) st_read_x(c, slot, zero, G);
+  if (READ) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      G.x[mt] = st_frag<Cfg::LA>(as, l.ao, ks, mt);
+      if (Cfg::KT && zero) G.x[mt] = u32x4{0u, 0u, 0u, 0u};
+    }
+  }
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[mt][t] = st_mfma(F.w[t], F.x[mt], acc[mt][t]);
-    if (next) st_read_w(c, slot, zero, t, G);
+    if (READ) {
+      const int tt = Cfg::SPLIT ? (t & 3) + 8 * (t >> 2) : t;
+      G.w[t] = st_frag<Cfg::LB>(bs, l.bo, ks, tt);
+      if (Cfg::KT && zero) G.w[t] = u32x4{0u, 0u, 0u, 0u};
+    }
   }
-  if (next && !Cfg::KT) {
+  if (READ && !Cfg::KT) {
     __builtin_amdgcn_sched_group_barrier(0x100, Cfg::LA == ST_PANEL ? 2 * MT : MT, 0);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
@@ -283,23 +305,6 @@ __device__ __forceinline__ void st_step(const StCtx<Cfg>& c, char* ring, int st,
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int J, bool GUARD, class Cfg>
-__device__ __forceinline__ void st_trip(const StCtx<Cfg>& c, char* ring, int st, StFrag<Cfg>& F, StFrag<Cfg>& G,
-                                        typename Cfg::Acc (&acc)[Cfg::MT][8]) {
-  st_step<J, GUARD>(c, ring, st + J, F, G, acc);
-  if constexpr (J + 1 < Cfg::NS) st_trip<J + 1, GUARD>(c, ring, st, G, F, acc);
-}
-
-// The wave's fragment offsets and the ring's address (operands and stage
-// counts are the caller's).
-template <class Cfg>
-__device__ __forceinline__ void st_setup(StCtx<Cfg>& c, char* ring) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  c.lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
-  c.ao = st_lane<Cfg::LA>(Cfg::MT * (wave & 3));
-  c.bo = st_lane<Cfg::LB>(Cfg::SPLIT ? 4 * (wave >> 2) : 8 * (wave >> 2));
-}
-
 template <class Cfg>
 __device__ __forceinline__ void st_clear(typename Cfg::Acc (&acc)[Cfg::MT][8]) {
 #pragma unroll
@@ -308,24 +313,124 @@ __device__ __forceinline__ void st_clear(typename Cfg::Acc (&acc)[Cfg::MT][8]) {
     for (int t = 0; t < 8; ++t) acc[a][t] = typename Cfg::Acc{};
 }
 
-// acc += the product over c.nst stages.  No copy of this wave may be
-// outstanding and every wave must be done with the ring.
+// The copies of a tile's first stages, in the order A0 B0 A1 B1 (A2) (B2).
+// Every wave must be done with the ring.
 template <class Cfg>
-__device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, char* ring, typename Cfg::Acc (&acc)[Cfg::MT][8]) {
-  constexpr int NS = Cfg::NS;
-  if (c.nst <= 0) return;
-  for (int j = 0; j < NS; ++j)
-    if (j < c.nst) st_issue_all(c, j, j);
-  st_sync_n<Cfg::CNT>(min(c.nst - 1, NS - 1));
-  StFrag<Cfg> F, G;
-  const bool zero = st_past(c, 0);
-  st_read_x(c, ring, zero, F);
+__device__ __forceinline__ void st_prologue(const StCtx<Cfg>& c, const StLane<Cfg>& l) {
 #pragma unroll
-  for (int t = 0; t < 8; ++t) st_read_w(c, ring, zero, t, F);
-  int st = 0;
-  for (; st + 2 * NS <= c.nst; st += NS) st_trip<0, false>(c, ring, st, F, G, acc);
-  st_trip<0, true>(c, ring, st, F, G, acc);
-  st_trip<0, true>(c, ring, st + NS, F, G, acc);
+  for (int s = 0; s < 3; ++s) {
+    if (s < Cfg::NA && s < c.nst) st_issue_a(c, l.lbase + s * Cfg::A::BYTES, s);
+    if (s < Cfg::NB && s < c.nst) st_issue_b(c, l.lbase + Cfg::AREG + s * Cfg::B::BYTES, s);
+  }
+}
+
+// Wait for stage s (0 or 1) of the prologue with S later stores outstanding.
+template <int S, class Cfg>
+__device__ __forceinline__ void st_wait_first(int s, int nst) {
+  constexpr int ST = Cfg::CA + Cfg::CB;                                       // a whole stage
+  constexpr int THIRD = (Cfg::NA > 2 ? Cfg::CA : 0) + (Cfg::NB > 2 ? Cfg::CB : 0);
+  if (s == 0) {
+    if (nst >= 3) st_sync<ST + THIRD + S>();
+    else if (nst == 2) st_sync<ST + S>();
+    else st_sync<S>();
+  } else {
+    if (nst >= 3) st_sync<THIRD + S>();
+    else st_sync<S>();
+  }
+}
+
+// acc = the product over c.nst stages (>= 1) whose prologue has been issued,
+// followed by `stores` (0 or Cfg::STORES) stores of the epilogue before.  At
+// the end no copy is outstanding and every wave is done with the ring.
+template <class Cfg>
+__device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, const StLane<Cfg>& l, const char* ring, bool stores,
+                                         typename Cfg::Acc (&acc)[Cfg::MT][8]) {
+  st_clear<Cfg>(acc);
+  if (stores) st_wait_first<Cfg::STORES, Cfg>(0, c.nst);
+  else st_wait_first<0, Cfg>(0, c.nst);
+  StFrag<Cfg> F, G;
+  {
+    const bool zero = st_past(c, 0, 0);
+#pragma unroll
+    for (int mt = 0; mt < Cfg::MT; ++mt) {
+      F.x[mt] = st_frag<Cfg::LA>(ring, l.ao, 0, mt);
+      if (Cfg::KT && zero) F.x[mt] = u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      F.w[t] = st_frag<Cfg::LB>(ring + Cfg::AREG, l.bo, 0, Cfg::SPLIT ? (t & 3) + 8 * (t >> 2) : t);
+      if (Cfg::KT && zero) F.w[t] = u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+  // slot offsets of stage s; stage s + NA (NB) takes the slot of stage s
+  uint32_t as = 0, bs = Cfg::AREG;
+  int s = 0;
+  for (; s + 1 < c.nst; ++s) {
+    st_kstep<true>(c, l, ring + as, ring + bs, s, 1, F, G, acc);
+    if (s == 0) {
+      if (stores) st_wait_first<Cfg::STORES, Cfg>(1, c.nst);
+      else st_wait_first<0, Cfg>(1, c.nst);
+    } else if (s + 2 < c.nst) {
+      st_sync<Cfg::LATER>();
+    } else {
+      st_sync<0>();
+    }
+    if (s + Cfg::NA < c.nst) st_issue_a(c, l.lbase + as, s + Cfg::NA);
+    if (s + Cfg::NB < c.nst) st_issue_b(c, l.lbase + bs, s + Cfg::NB);
+    as = as == (Cfg::NA - 1) * Cfg::A::BYTES ? 0 : as + Cfg::A::BYTES;
+    bs = bs == Cfg::AREG + (Cfg::NB - 1) * Cfg::B::BYTES ? Cfg::AREG : bs + Cfg::B::BYTES;
+    st_kstep<true>(c, l, ring + as, ring + bs, s + 1, 0, G, F, acc);
+  }
+  st_kstep<true>(c, l, ring + as, ring + bs, s, 1, F, G, acc);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  st_kstep<false>(c, l, ring, ring, s, 0, G, F, acc);
+}
+
+// ---------------------------------------------------------------------------
+// epilogues
+// ---------------------------------------------------------------------------
+// Column tiles t (x) and t + 1 (y) of one row tile, one word of 2 packed or 1
+// plain column per lane and register: afterwards lane group g holds, in (x, y)
+// order, what groups 2 (g % 2) and 2 (g % 2) + 1 held of tile t + g / 2.
+__device__ __forceinline__ void st_swap_pair(uint32_t& x, uint32_t& y) {
+  const auto a = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[1], false, false);
+  x = b[0];
+  y = b[1];
+}
+__device__ __forceinline__ void st_swap_pair(float& x, float& y) {
+  uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  st_swap_pair(a, b);
+  x = __uint_as_float(a);
+  y = __uint_as_float(b);
+}
+
+// Values of column tiles t and t + 1 as bf16: 8 consecutive columns per lane,
+// 16 t + 8 g .. + 7 (g the lane group).
+__device__ __forceinline__ u32x4 st_pack8(const float (&x)[4], const float (&y)[4]) {
+  uint32_t x0 = pack_bf16x2(x[0], x[1]), x1 = pack_bf16x2(x[2], x[3]);
+  uint32_t y0 = pack_bf16x2(y[0], y[1]), y1 = pack_bf16x2(y[2], y[3]);
+  st_swap_pair(x0, y0);
+  st_swap_pair(x1, y1);
+  return u32x4{x0, x1, y0, y1};
+}
+__device__ __forceinline__ u32x4 st_pack8(const f32x4& x, const f32x4& y) {
+  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {y[0], y[1], y[2], y[3]};
+  return st_pack8(a, b);
+}
+
+// Output rows of a tile: stores outside its rows or columns leave the
+// descriptor, so that every store is issued and none needs a branch.
+struct StOut {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t ld;   // bytes per row
+};
+__device__ __forceinline__ StOut st_out(void* base, int64_t ld, int rows) {
+  return StOut{gc_rsrc(base, (uint32_t)rows * (uint32_t)ld), (uint32_t)ld};
+}
+// 16 bytes at (row, byte column), or nothing where !ok.
+__device__ __forceinline__ void st_put(const StOut& o, int row, uint32_t byte, bool ok, const u32x4& v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, o.r, ok ? (uint32_t)row * o.ld + byte : 0xFFFFFFF0u, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -391,16 +496,44 @@ __device__ __forceinline__ StTile st_tile_at(int L, const int32_t* __restrict__ 
   return t;
 }
 
-// The tiles [begin, end) of `total` that workgroup b of G takes, every `step`-th:
-// each XCD (workgroup id mod 8 on this part) gets one contiguous range.
-struct StRange {
-  int begin, end, step;
-};
-__device__ __forceinline__ StRange st_range(int total, int b, int G) {
-  if (G & 7) return StRange{b, total, G};
-  const int x = b & 7, per = total >> 3, more = total & 7;
-  const int first = x * per + min(x, more);
-  return StRange{first + (b >> 3), first + per + (x < more ? 1 : 0), G >> 3};
+// Walk of the G persistent workgroups (G a multiple of 8) over `total` tiles:
+// in every round each XCD (workgroup id mod 8 on this part) takes one run of
+// G / 8 consecutive tiles, so that neighbouring tiles share an L2, and tiles of
+// unequal length (experts of unequal row counts) spread over all XCDs.
+__device__ __forceinline__ int st_first_tile() {
+  return (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
+}
+
+// The persistent loop.  setup(L, ctx) describes tile L, fill(L, acc, stored)
+// finishes it with exactly Cfg::STORES stores per wave.  setup may leave ctx.nst
+// = 0 (a tile of zeros).
+template <class Cfg, class Setup, class Finish>
+__device__ __forceinline__ void st_run(int total, char* ring, const Setup& setup, const Finish& finish) {
+  const StLane<Cfg> l = st_lanes<Cfg>(ring);
+  int L = st_first_tile();
+  if (L >= total) return;
+  StCtx<Cfg> c;
+  setup(L, c);
+  st_prologue(c, l);
+  bool stores = false;
+  for (;;) {
+    typename Cfg::Acc acc[Cfg::MT][8];
+    if (c.nst > 0) st_accum(c, l, ring, stores, acc);
+    else st_clear<Cfg>(acc);
+    const int next = L + (int)gridDim.x;
+    const bool more = next < total;
+    if (more) {
+      setup(next, c);
+      st_prologue(c, l);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    finish(L, acc);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    if (!more) return;
+    L = next;
+    stores = true;
+  }
 }
 
 }  // namespace moe
