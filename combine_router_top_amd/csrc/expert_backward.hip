@@ -40,7 +40,8 @@ template <int MT, bool KT>
 using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, KT, 8 * MT>;
 template <int MT, bool KT>
 using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, KT, 4 * MT>;
-using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, false, 16>;
+template <bool SHORT>
+using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, false, 16, SHORT>;
 
 // dh tiles: rows of dy against rows of W2 (its f rows are the output columns).
 template <int MT, bool KT>
@@ -53,23 +54,22 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
                                                            int d, int f, int ntn) {
   using Cfg = GateCfg<MT, KT>;
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
-  __shared__ int pre[ST_MAXN + 1];
-  const int total = st_prefix(offsets, n, Cfg::BM, pre) * ntn;
+  const int total = st_row_blocks(offsets, n, Cfg::BM) * ntn;
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 3, wn = wave >> 2;
   st_run<Cfg>(
       total, ring,
       [&](int L, StCtx<Cfg>& c) {
-        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM);
         const uint32_t ld = (uint32_t)d * 2;
-        st_rows<Cfg::BM>(c.a[0], dy + (int64_t)t.r0 * d, ld, t.R, ld);
-        st_rows<ST_BN>(c.b[0], w2 + ((int64_t)t.e * f + 256 * t.nt) * d, ld, min(ST_BN, f - 256 * t.nt), ld);
+        st_rows(c.a[0], dy + (int64_t)t.r0 * d, ld, t.R, ld);
+        st_rows(c.b[0], w2 + ((int64_t)t.e * f + 256 * t.nt) * d, ld, min(ST_BN, f - 256 * t.nt), ld);
         c.nst = c.nst1 = (d + 63) / 64;
         c.kvals = d;
+        return t;
       },
-      [&](int L, f32x4 (&acc)[MT][8]) {
-        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+      [&](const StTile& t, f32x4 (&acc)[MT][8]) {
         const int64_t first = (int64_t)t.r0 * f;
         const int64_t ld = (int64_t)f * 2;
         const StOut og = st_out(dg + first, ld, t.R), ou = st_out(du + first, ld, t.R);
@@ -103,8 +103,8 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
               float a0, a1, b0, b1;
               swiglu_grad(dh[0], bf16_lo(gv[k][h]), bf16_lo(uv[k][h]), a0, b0);
               swiglu_grad(dh[1], bf16_hi(gv[k][h]), bf16_hi(uv[k][h]), a1, b1);
-              vg[h] = pack_bf16x2(a0, a1);
-              vu[h] = pack_bf16x2(b0, b1);
+              vg[h] = cvt_bf16x2(a0, a1);
+              vu[h] = cvt_bf16x2(b0, b1);
             }
             st_put(og, row, 2u * (uint32_t)col, col < f, vg);
             st_put(ou, row, 2u * (uint32_t)col, col < f, vu);
@@ -128,6 +128,32 @@ __device__ __forceinline__ void store_tile(const StOut& o, const f32x4 (&acc)[MT
     }
 }
 
+// The same through a 4 KB staging area of this wave: a store then writes four
+// rows of 256 bytes instead of sixteen pieces of 64, which cost the address
+// unit about 100 cycles an instruction and bounded tiles that mostly store.
+// Staged rows keep their 32-byte chunk c at c ^ (row & 7).
+__device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&acc)[4][8], int col0, int N, char* stage) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char* stg = stage + 4096 * wave;
+  const int p = lane & 15, col = col0 + 128 * (wave >> 2) + 8 * p;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const f32x4 v = acc[mt][t];
+      *reinterpret_cast<u32x2*>(stg + i * 256 + 32 * (t ^ (i & 7)) + 8 * q) =
+          u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 4 * k + q;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * 256 + 32 * ((p >> 1) ^ (row & 7)) + 16 * (p & 1));
+      st_put<true>(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
+    }
+  }
+}
+
 // dx tiles: [dg | du] against rows of W1, then of W3, in one accumulator.
 template <int MT, bool KT>
 __global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __restrict__ dg,
@@ -138,26 +164,25 @@ __global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __rest
                                                             bf16_t* __restrict__ dx, int d, int f, int ntn) {
   using Cfg = InputCfg<MT, KT>;
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
-  __shared__ int pre[ST_MAXN + 1];
-  const int total = st_prefix(offsets, n, Cfg::BM, pre) * ntn;
+  const int total = st_row_blocks(offsets, n, Cfg::BM) * ntn;
   st_run<Cfg>(
       total, ring,
       [&](int L, StCtx<Cfg>& c) {
-        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
+        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM);
         const uint32_t ld = (uint32_t)f * 2;
         const int64_t arow = (int64_t)t.r0 * f, brow = ((int64_t)t.e * d + 256 * t.nt) * f;
         const int cols = min(ST_BN, d - 256 * t.nt);
-        st_rows<Cfg::BM>(c.a[0], dg + arow, ld, t.R, ld);
-        st_rows<Cfg::BM>(c.a[1], du + arow, ld, t.R, ld);
-        st_rows<ST_BN>(c.b[0], w1 + brow, ld, cols, ld);
-        st_rows<ST_BN>(c.b[1], w3 + brow, ld, cols, ld);
+        st_rows(c.a[0], dg + arow, ld, t.R, ld);
+        st_rows(c.a[1], du + arow, ld, t.R, ld);
+        st_rows(c.b[0], w1 + brow, ld, cols, ld);
+        st_rows(c.b[1], w3 + brow, ld, cols, ld);
         c.nst1 = (f + 63) / 64;
         c.nst = 2 * c.nst1;
         c.kvals = f;
+        return t;
       },
-      [&](int L, f32x4 (&acc)[MT][8]) {
-        const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM, pre);
-        store_tile<MT>(st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R), acc, 256 * t.nt, d);
+      [&](const StTile& t, f32x4 (&acc)[MT][8]) {
+        store_tile(st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R), acc, 256 * t.nt, d);
       });
 }
 
@@ -174,58 +199,94 @@ struct WeightGrads {
 };
 
 // All tiles of all wanted weight gradients, expert by expert; a segment without
-// rows gives zeros.
-__global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int nm,
+// rows gives zeros.  SHORT: st_run_short over units of at most glen row blocks.
+template <bool SHORT>
+__global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int nm, int glen,
                                                              const int32_t* __restrict__ offsets, int n) {
-  using Cfg = WeightCfg;
-  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
-  int tiles[3], per = 0;
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    tiles[k] = k < nm ? ((w.m[k].M + 255) / 256) * ((w.m[k].N + 255) / 256) : 0;
-    per += tiles[k];
-  }
-  struct Where {
-    WeightGrad m;
-    int e, tm, tn;
+  using Cfg = WeightCfg<SHORT>;
+  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS + (SHORT ? 8 * 4096 : 0)];
+  // the table as values: a choice between its addresses would put it in scratch,
+  // and what is read from there into vector registers
+  auto held = [&](WeightGrad m) {
+    asm volatile("" : "+s"(m.P), "+s"(m.Q), "+s"(m.C), "+s"(m.M), "+s"(m.N));
+    return m;
   };
-  auto where = [&](int L) {
-    Where r;
-    r.e = L / per;
+  const WeightGrad m0 = held(w.m[0]), m1 = held(w.m[1]), m2 = held(w.m[2]);
+  // column blocks, runs of row blocks and their length, and the tiles (SHORT:
+  // units) of each matrix
+  auto runs_of = [&](int M) { return SHORT ? st_div((M + 255) / 256 + glen - 1, glen) : (M + 255) / 256; };
+  auto len_of = [&](int M, int runs) { return st_div((M + 255) / 256 + runs - 1, runs); };
+  const int r0 = runs_of(m0.M), r1 = runs_of(m1.M), r2 = runs_of(m2.M);
+  const int l0 = len_of(m0.M, r0), l1 = len_of(m1.M, r1), l2 = len_of(m2.M, r2);
+  const int n0 = (m0.N + 255) / 256, n1 = (m1.N + 255) / 256, n2 = (m2.N + 255) / 256;
+  const int c0 = n0 * r0, c1 = nm > 1 ? n1 * r1 : 0, c2 = nm > 2 ? n2 * r2 : 0;
+  const int per = c0 + c1 + c2;
+  struct Unit {
+    WeightGrad m;
+    int e, tm, tn, tiles;   // row blocks tm .. tm + tiles - 1
+    int o, cnt, nst;
+  };
+  auto unit = [&](int L) __attribute__((always_inline)) {
+    Unit r;
+    r.e = st_div(L, per);
     int at = L - r.e * per;
-    r.m = w.m[0];
-    if (at >= tiles[0]) {
-      at -= tiles[0];
-      r.m = w.m[1];
-      if (at >= tiles[1]) {
-        at -= tiles[1];
-        r.m = w.m[2];
-      }
+    const bool b1 = at >= c0, b2 = at >= c0 + c1;
+    auto pick = [&](auto v0, auto v1, auto v2) { return b2 ? v2 : b1 ? v1 : v0; };
+    at -= pick(0, c0, c0 + c1);
+    r.m.P = pick(m0.P, m1.P, m2.P);
+    r.m.Q = pick(m0.Q, m1.Q, m2.Q);
+    r.m.C = pick(m0.C, m1.C, m2.C);
+    r.m.M = pick(m0.M, m1.M, m2.M);
+    r.m.N = pick(m0.N, m1.N, m2.N);
+    const int nnt = pick(n0, n1, n2);
+    if (SHORT) {
+      // the column blocks of the same rows run together, so that whole rows of
+      // the gradient are written at a time
+      const int q = st_div(at, nnt), ln = pick(l0, l1, l2);
+      r.tn = at - q * nnt;
+      r.tm = q * ln;
+      r.tiles = min(ln, (r.m.M + 255) / 256 - r.tm);
+    } else {
+      // groups of 8 row blocks run through the columns together
+      const int mg = st_div(at, ST_GM * nnt), rem = at - mg * ST_GM * nnt;
+      const int gsz = min(ST_GM, (r.m.M + 255) / 256 - mg * ST_GM);
+      r.tn = st_div(rem, gsz);
+      r.tm = mg * ST_GM + (rem - r.tn * gsz);
+      r.tiles = 1;
     }
-    // groups of 8 row tiles run through the column tiles together
-    const int nmt = (r.m.M + 255) / 256, nnt = (r.m.N + 255) / 256;
-    const int mg = at / (ST_GM * nnt), rem = at - mg * ST_GM * nnt;
-    const int gsz = min(ST_GM, nmt - mg * ST_GM);
-    r.tn = rem / gsz;
-    r.tm = mg * ST_GM + (rem - r.tn * gsz);
+    r.o = __builtin_amdgcn_readfirstlane(offsets[r.e]);
+    r.cnt = __builtin_amdgcn_readfirstlane(offsets[r.e + 1]) - r.o;
+    r.nst = (r.cnt + 63) / 64;
+    if (SHORT && r.nst == 1) r.nst = 2;
     return r;
   };
-  st_run<Cfg>(
-      n * per, ring,
-      [&](int L, StCtx<Cfg>& c) {
-        const Where r = where(L);
-        const int o = __builtin_amdgcn_readfirstlane(offsets[r.e]);
-        const int cnt = __builtin_amdgcn_readfirstlane(offsets[r.e + 1]) - o;
-        st_panel<256>(c.a[0], r.m.P + (int64_t)o * r.m.M, (uint32_t)r.m.M * 2, cnt, 256 * r.tm, r.m.M);
-        st_panel<256>(c.b[0], r.m.Q + (int64_t)o * r.m.N, (uint32_t)r.m.N * 2, cnt, 256 * r.tn, r.m.N);
-        c.nst = c.nst1 = (cnt + 63) / 64;
-        c.kvals = cnt;
-      },
-      [&](int L, f32x4 (&acc)[4][8]) {
-        const Where r = where(L);
-        bf16_t* C = r.m.C + ((int64_t)r.e * r.m.M + 256 * r.tm) * r.m.N;
-        store_tile<4>(st_out(C, (int64_t)r.m.N * 2, min(256, r.m.M - 256 * r.tm)), acc, 256 * r.tn, r.m.N);
-      });
+  auto cols = [&](const Unit& r, StCtx<Cfg>& c) __attribute__((always_inline)) {
+    st_panel(c.b[0], r.m.Q + (int64_t)r.o * r.m.N, (uint32_t)r.m.N * 2, r.cnt, 256 * r.tn, r.m.N);
+    c.nst = c.nst1 = r.nst;
+    c.kvals = 0;
+  };
+  auto rows = [&](const Unit& r, int j, StCtx<Cfg>& c) __attribute__((always_inline)) {
+    st_panel(c.a[0], r.m.P + (int64_t)r.o * r.m.M, (uint32_t)r.m.M * 2, r.cnt, 256 * (r.tm + j), r.m.M);
+  };
+  auto out = [&](const Unit& r, int j) {
+    const int row = 256 * (r.tm + j);
+    return st_out(r.m.C + ((int64_t)r.e * r.m.M + row) * r.m.N, (int64_t)r.m.N * 2, min(256, r.m.M - row));
+  };
+  if constexpr (SHORT) {
+    st_run_short<Cfg>(n * per, ring, unit, cols, rows, [&](const Unit& r, int j, f32x4 (&acc)[4][8]) {
+      store_tile_rows(out(r, j), acc, 256 * r.tn, r.m.N, ring + Cfg::LDS);
+    });
+  } else {
+    st_run<Cfg>(
+        n * per, ring,
+        [&](int L, StCtx<Cfg>& c) {
+          const Unit r = unit(L);
+          cols(r, c);
+          rows(r, 0, c);
+          return r;
+        },
+        [&](const Unit& r, f32x4 (&acc)[4][8]) { store_tile(out(r, 0), acc, 256 * r.tn, r.m.N); });
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -276,12 +337,10 @@ __device__ __forceinline__ void f32_tile(const FA& A, bool a_kfast, const FB& B,
   }
 }
 
-// Row block of a 64-row tile grid: block b of the prefix over ceil(rows / 64).
-__device__ __forceinline__ bool f32_row_block(const int32_t* offsets, int n, int b, int* pre, StTile& t) {
-  const int total = st_prefix(offsets, n, 64, pre);
-  if (b >= total) return false;
-  t = st_tile_at(b, offsets, n, 1, 64, pre);
-  return true;
+// Row block b of 64 rows, counted over all segments; false past the last.
+__device__ __forceinline__ bool f32_row_block(const int32_t* offsets, int n, int b, StTile& t) {
+  t = st_tile_at(b, offsets, n, 1, 64);
+  return t.R > 0;
 }
 
 __global__ __launch_bounds__(256) void gate_grad_f32(const float* __restrict__ dy, const int32_t* __restrict__ offsets,
@@ -289,9 +348,8 @@ __global__ __launch_bounds__(256) void gate_grad_f32(const float* __restrict__ d
                                                      const float* __restrict__ u, float* __restrict__ dg,
                                                      float* __restrict__ du, int d, int f) {
   __shared__ __attribute__((aligned(16))) float sa[F_K * F_LD], sb[F_K * F_LD];
-  __shared__ int pre[ST_MAXN + 1];
   StTile t;
-  if (!f32_row_block(offsets, n, blockIdx.x, pre, t)) return;
+  if (!f32_row_block(offsets, n, blockIdx.x, t)) return;
   const int c0 = blockIdx.y * 64;
   const float* a = dy + (int64_t)t.r0 * d;
   const float* b = w2 + (int64_t)t.e * f * d;
@@ -315,9 +373,8 @@ __global__ __launch_bounds__(256) void input_grad_f32(const float* __restrict__ 
                                                       const float* __restrict__ w1, const float* __restrict__ w3,
                                                       float* __restrict__ dx, int d, int f) {
   __shared__ __attribute__((aligned(16))) float sa[F_K * F_LD], sb[F_K * F_LD];
-  __shared__ int pre[ST_MAXN + 1];
   StTile t;
-  if (!f32_row_block(offsets, n, blockIdx.x, pre, t)) return;
+  if (!f32_row_block(offsets, n, blockIdx.x, t)) return;
   const int c0 = blockIdx.y * 64;
   float acc[4][4] = {};
   for (int half = 0; half < 2; ++half) {
@@ -361,6 +418,8 @@ __global__ __launch_bounds__(256) void fill_zero(u32x4* __restrict__ p, int64_t 
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n16; i += (int64_t)gridDim.x * 256)
     p[i] = u32x4{0u, 0u, 0u, 0u};
 }
+
+constexpr int WG_SHORT = 512;   // expected rows up to which the weight gradients take st_run_short
 
 size_t expert_backward_ws_bytes(const Prob& p) {
   // dg and du, [rows_max, f] each
@@ -462,8 +521,14 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
   want(x, DG, dw1, p.d, p.f);
   want(x, DU, dw3, p.d, p.f);
   if (nm) {
-    hipLaunchKernelGGL(weight_grad_bf16, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, offsets,
-                       p.n);
+    // runs of row blocks that share their columns: up to 4 (8, 2 and 1 measured
+    // 864, 813 and 839 us against 808 on 32 experts of about 128 rows), fewer where that
+    // would leave less than four units for each compute unit
+    const int glen = (int)std::min<int64_t>(4, std::max<int64_t>(1, tiles / (4 * (int64_t)device_cus())));
+    if (mean <= WG_SHORT)
+      hipLaunchKernelGGL(weight_grad_bf16<true>, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, glen, offsets, p.n);
+    else
+      hipLaunchKernelGGL(weight_grad_bf16<false>, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, 1, offsets, p.n);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;

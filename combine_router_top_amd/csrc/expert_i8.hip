@@ -247,12 +247,8 @@ template <int MT, bool GATED, bool F32OUT>
 __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
   using Cfg = I8Cfg<MT, GATED, F32OUT>;
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
-  __shared__ int pre[ST_MAXN + 1];
-  __shared__ int32_t whole[2];
-  if (threadIdx.x < 2) whole[threadIdx.x] = threadIdx.x ? p.M : 0;   // without offsets: one segment
-  __syncthreads();
-  const int32_t* offsets = p.offsets ? p.offsets : whole;
-  const int total = st_prefix(offsets, p.n, Cfg::BM, pre, p.lo) * ntn;
+  // without offsets: one segment of M rows, ntn column blocks
+  const int total = (p.offsets ? st_row_blocks(p.offsets, p.n, Cfg::BM, p.lo) : (p.M + Cfg::BM - 1) / Cfg::BM) * ntn;
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 3, wn = wave >> 2;
@@ -260,8 +256,9 @@ __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
   st_run<Cfg>(
       total, ring,
       [&](int L, StCtx<Cfg>& c) {
-        const StTile t = st_tile_at(L, offsets, p.n, ntn, Cfg::BM, pre);
-        st_rows<Cfg::BM>(c.a[0], p.a + (int64_t)t.r0 * p.lda, (uint32_t)p.lda, t.R, (uint32_t)p.K);
+        const StTile t = p.offsets ? st_tile_at(L, p.offsets, p.n, ntn, Cfg::BM, p.lo)
+                                   : st_tile_of(L, 0, p.M, (p.M + Cfg::BM - 1) / Cfg::BM, ntn, Cfg::BM);
+        st_rows(c.a[0], p.a + (int64_t)t.r0 * p.lda, (uint32_t)p.lda, t.R, (uint32_t)p.K);
         const int64_t eo = (int64_t)t.e * p.ntiles * run;
         if (GATED) {
           st_pack(c.b[0], 0, p.b1 + eo, 8 * t.nt, p.ntiles, run);
@@ -272,9 +269,9 @@ __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
         }
         c.nst = c.nst1 = (p.kt + 1) / 2;   // an odd last block meets zeros past its run
         c.kvals = 0;
+        return t;
       },
-      [&](int L, i32x4 (&acc)[MT][8]) {
-        const StTile t = st_tile_at(L, offsets, p.n, ntn, Cfg::BM, pre);
+      [&](const StTile& t, i32x4 (&acc)[MT][8]) {
         constexpr int ES = F32OUT ? 4 : 2;
         const StOut out = st_out((char*)p.c + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
         float sr[MT];

@@ -110,39 +110,45 @@ __device__ __forceinline__ void st_panel(StOp<ST_PANEL, W>& o, const void* base,
   o.size = 0;
 }
 
-// ST_PACK, one 128-column half c: 16-column tiles nt0 .. nt0 + 7 of a packed
-// matrix of `ntiles` of them, each a run of `run` bytes (1 KB per 64 K); tiles
-// past the last repeat it (their columns are never stored).
+// ST_PACK, the 128-column half `half`: 16-column tiles nt0 .. nt0 + 7 of a
+// packed matrix of `ntiles` of them, each a run of `run` bytes (1 KB per 64 K);
+// tiles past the last repeat it (their columns are never stored).
 template <int W>
-__device__ __forceinline__ void st_pack(StOp<ST_PACK, W>& o, int c, const void* base, int nt0, int ntiles,
+__device__ __forceinline__ void st_pack(StOp<ST_PACK, W>& o, int half, const void* base, int nt0, int ntiles,
                                         uint32_t run) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nt = min(nt0 + wave, ntiles - 1);
-  o.base[c] = (const char*)base + (int64_t)nt * run;
+  o.base[half] = (const char*)base + (int64_t)min(nt0 + wave, ntiles - 1) * run;
   o.v[0] = 16u * (uint32_t)(threadIdx.x & 63);
   o.ld = 0;
   o.size = run;
 }
 
+// A wave-uniform quotient in a scalar register: the division runs on the vector
+// unit, and what is derived from it (descriptors, offsets) has to be scalar.
+__device__ __forceinline__ int st_div(int a, int b) { return __builtin_amdgcn_readfirstlane(a / b); }
+
 // The copies of stage st of one operand into its slot at LDS address lds.
 template <int L, int W>
 __device__ __forceinline__ void st_issue(const StOp<L, W>& o, uint32_t lds, int st) {
+  constexpr int C = StOp<L, W>::C;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if constexpr (L == ST_ROWS) {
     const __amdgpu_buffer_rsrc_t r = gc_rsrc(o.base[0], o.size);
 #pragma unroll
-    for (int c = 0; c < W / 64; ++c)
-      bd_copy16(r, lds + 1024 * wave + 8192 * c, o.v[0], (uint32_t)st * ST_KB + (uint32_t)(64 * c) * o.ld);
+    for (int c = 0; c < C; ++c)
+      bd_copy16(r, lds + 1024 * (wave + 8 * c), o.v[0], (uint32_t)st * ST_KB + (uint32_t)(64 * c) * o.ld);
   } else if constexpr (L == ST_PANEL) {
     // a descriptor per stage: a segment may span more than 32 bits
-    const __amdgpu_buffer_rsrc_t r =
-        gc_rsrc(o.base[0] + (int64_t)st * 64 * o.ld, (uint32_t)min(64, o.krows - 64 * st) * o.ld);
+    // (the saturated row count is formed on the vector unit; the descriptor is scalar)
+    const int rows = __builtin_amdgcn_readfirstlane(max(0, min(64, o.krows - 64 * st)));
+    const __amdgpu_buffer_rsrc_t r = gc_rsrc(o.base[0] + (int64_t)st * 64 * o.ld, (uint32_t)rows * o.ld);
+    const uint32_t at = lds + 16384 * (wave >> 2) + 4096 * (wave & 3);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      bd_copy16(r, lds + 16384 * (wave >> 2) + 4096 * (wave & 3) + 1024 * c, o.v[c >> 1], (uint32_t)(4 * (c & 1)) * o.ld);
+    for (int c = 0; c < C; ++c)
+      bd_copy16(r, at + 1024 * c, o.v[c >> 1], (uint32_t)(4 * (c & 1)) * o.ld);
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < C; ++c)
       bd_copy16(gc_rsrc(o.base[c >> 1], o.size), lds + 2048 * (wave + 8 * (c >> 1)) + 1024 * (c & 1), o.v[0],
                 (uint32_t)st * 2048u + 1024u * (c & 1));
   }
@@ -157,7 +163,7 @@ __device__ __forceinline__ int st_lane(int t0) {
   if constexpr (L == ST_PACK) return 2048 * t0 + 16 * lane;
   const int sig = (i >> 2) | ((g & 1) << 2);
   const int base = (8 * g + (i >> 2)) * BD_HPROW + 32 * sig + 8 * (i & 3);
-  return (t0 >> 3) * 16384 + (base ^ (32 * (t0 & 7)));
+  return (t0 >> 3) * 16384 + (base ^ (32 * (t0 & 7)));   // t0 & 7 = 0 or 4
 }
 
 // Fragment (16 bytes) of the wave's tile t and k-step ks.  ST_PANEL tiles of a
@@ -190,8 +196,9 @@ __device__ __forceinline__ i32x4 st_mfma(const u32x4& a, const u32x4& b, const i
 // up products of one h column meet in one lane: acc[mt][t] and acc[mt][t + 4]).
 // KT: K is not a multiple of a stage; the fragments past its end are zeroed
 // (ST_ROWS reads there what follows the row).  STORES: store instructions of a
-// wave's epilogue, every one of them unconditional.
-template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, bool KT_, int STORES_>
+// wave's epilogue, every one of them unconditional.  SHORT: two slots for each
+// operand, for st_run_short.
+template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, bool KT_, int STORES_, bool SHORT_ = false>
 struct StCfg {
   static constexpr int MT = MT_, LA = LA_, LB = LB_, NP = NP_, STORES = STORES_;
   static constexpr bool SPLIT = SPLIT_, KT = KT_;
@@ -200,9 +207,9 @@ struct StCfg {
   typedef StOp<LA, BM> A;
   typedef StOp<LB, ST_BN> B;
   // slots: the columns (weights, from HBM) three deep where LDS allows
-  static constexpr int NA = MT == 2 ? 3 : 2, NB = MT == 4 ? 2 : 3;
+  static constexpr int NA = BM == 128 && !SHORT_ ? 3 : 2, NB = SHORT_ ? 2 : 3;
   static constexpr int AREG = NA * A::BYTES;                   // the column slots follow the row slots
-  static constexpr int LDS = AREG + NB * B::BYTES;             // 144, 144, 128 KB
+  static constexpr int LDS = AREG + NB * B::BYTES;             // 128 to 160 KB (all there is)
   static constexpr int CA = A::C, CB = B::C;                   // copies per wave per stage
   // copies issued after those of stage s + 1 when stage s reaches its middle
   static constexpr int LATER = (NB > NA ? CB : 0) + (NA - 2) * (CA + CB);
@@ -248,8 +255,7 @@ __device__ __forceinline__ bool st_past(const StCtx<Cfg>& c, int st, int ks) {
 // LDS reads have completed, then barrier.
 template <int N>
 __device__ __forceinline__ void st_sync() {
-  static_assert(N < 64, "vmcnt holds six bits");
-  bd_sync<N>();
+  bd_sync<(N < 63 ? N : 63)>();   // the counter's six bits; a smaller count waits for more
 }
 
 template <class Cfg>
@@ -264,12 +270,16 @@ __device__ __forceinline__ StLane<Cfg> st_lanes(char* ring) {
   StLane<Cfg> l;
   l.lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
   l.ao = st_lane<Cfg::LA>(Cfg::MT * (wave & 3));
-  l.bo = st_lane<Cfg::LB>(Cfg::SPLIT ? 4 * (wave >> 2) : 8 * (wave >> 2));
+  l.bo = st_lane<Cfg::LB>((Cfg::SPLIT ? 4 : 8) * (wave >> 2));
   return l;
 }
 
 // Multiply F; with READ, read k-step ks of stage st into G meanwhile, from the
-// slots at as and bs.
+// slots at as and bs.  Once a wave has its first products under way it takes
+// priority over the other wave of its SIMD, which then waits, copies or reads
+// LDS beside them instead of both multiplying in step (dense 8-expert backward
+// pass 19.6 -> 18.7 ms, 4096 x 14336 x 4096 int8 product 241 -> 222 us; the
+// order of reads and products inside a k-step is left to the compiler).
 template <bool READ, class Cfg>
 __device__ __forceinline__ void st_kstep(const StCtx<Cfg>& c, const StLane<Cfg>& l, const char* as, const char* bs,
                                          int st, int ks, const StFrag<Cfg>& F, StFrag<Cfg>& G,
@@ -288,20 +298,14 @@ __device__ __forceinline__ void st_kstep(const StCtx<Cfg>& c, const StLane<Cfg>&
   for (int t = 0; t < 8; ++t) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[mt][t] = st_mfma(F.w[t], F.x[mt], acc[mt][t]);
+    if (t == 0) __builtin_amdgcn_s_setprio(1);
     if (READ) {
       const int tt = Cfg::SPLIT ? (t & 3) + 8 * (t >> 2) : t;
       G.w[t] = st_frag<Cfg::LB>(bs, l.bo, ks, tt);
       if (Cfg::KT && zero) G.w[t] = u32x4{0u, 0u, 0u, 0u};
     }
   }
-  if (READ && !Cfg::KT) {
-    __builtin_amdgcn_sched_group_barrier(0x100, Cfg::LA == ST_PANEL ? 2 * MT : MT, 0);
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      __builtin_amdgcn_sched_group_barrier(0x008, MT, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, Cfg::LB == ST_PANEL ? 2 : 1, 0);
-    }
-  }
+  __builtin_amdgcn_s_setprio(0);
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -376,10 +380,12 @@ __device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, const StLane<Cfg>&
       st_sync<0>();
     }
     if (s + Cfg::NA < c.nst) st_issue_a(c, l.lbase + as, s + Cfg::NA);
-    if (s + Cfg::NB < c.nst) st_issue_b(c, l.lbase + bs, s + Cfg::NB);
+    const uint32_t free_b = bs;
     as = as == (Cfg::NA - 1) * Cfg::A::BYTES ? 0 : as + Cfg::A::BYTES;
     bs = bs == Cfg::AREG + (Cfg::NB - 1) * Cfg::B::BYTES ? Cfg::AREG : bs + Cfg::B::BYTES;
     st_kstep<true>(c, l, ring + as, ring + bs, s + 1, 0, G, F, acc);
+    // half a stage after the rows' copies, which spreads the requests
+    if (s + Cfg::NB < c.nst) st_issue_b(c, l.lbase + free_b, s + Cfg::NB);
   }
   st_kstep<true>(c, l, ring + as, ring + bs, s, 1, F, G, acc);
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -408,8 +414,8 @@ __device__ __forceinline__ void st_swap_pair(float& x, float& y) {
 // Values of column tiles t and t + 1 as bf16: 8 consecutive columns per lane,
 // 16 t + 8 g .. + 7 (g the lane group).
 __device__ __forceinline__ u32x4 st_pack8(const float (&x)[4], const float (&y)[4]) {
-  uint32_t x0 = pack_bf16x2(x[0], x[1]), x1 = pack_bf16x2(x[2], x[3]);
-  uint32_t y0 = pack_bf16x2(y[0], y[1]), y1 = pack_bf16x2(y[2], y[3]);
+  uint32_t x0 = cvt_bf16x2(x[0], x[1]), x1 = cvt_bf16x2(x[2], x[3]);
+  uint32_t y0 = cvt_bf16x2(y[0], y[1]), y1 = cvt_bf16x2(y[2], y[3]);
   st_swap_pair(x0, y0);
   st_swap_pair(x1, y1);
   return u32x4{x0, x1, y0, y1};
@@ -428,71 +434,77 @@ struct StOut {
 __device__ __forceinline__ StOut st_out(void* base, int64_t ld, int rows) {
   return StOut{gc_rsrc(base, (uint32_t)rows * (uint32_t)ld), (uint32_t)ld};
 }
-// 16 bytes at (row, byte column), or nothing where !ok.
+// 16 bytes at (row, byte column), or nothing where !ok.  NT: non-temporal.
+template <bool NT = false>
 __device__ __forceinline__ void st_put(const StOut& o, int row, uint32_t byte, bool ok, const u32x4& v) {
-  __builtin_amdgcn_raw_buffer_store_b128(v, o.r, ok ? (uint32_t)row * o.ld + byte : 0xFFFFFFF0u, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(v, o.r, ok ? (uint32_t)row * o.ld + byte : 0xFFFFFFF0u, 0, NT ? 2 : 0);
 }
 
 // ---------------------------------------------------------------------------
 // row blocks of expert segments
 // ---------------------------------------------------------------------------
-constexpr int ST_MAXN = 1024;   // experts at most
 constexpr int ST_GM = 8;        // row blocks of one expert that run together
 
 struct StTile {
   int e, r0, R, nt;   // expert, first row, valid rows, column block
 };
 
-// pre[j] = row blocks of experts 0 .. j, bm rows each (segments of at most lo
-// rows have none); returns their total.
-// All threads call; the caller separates the next use of pre by a barrier.
-__device__ __forceinline__ int st_prefix(const int32_t* __restrict__ offsets, int n, int bm, int* pre, int lo = 0) {
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    int carry = 0;
-    for (int j0 = 0; j0 < n; j0 += 64) {
-      const int j = j0 + lane;
-      const int cnt = j < n ? offsets[j + 1] - offsets[j] : 0;
-      int x = cnt > lo ? (cnt + bm - 1) / bm : 0;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(x, off);
-        if (lane >= off) x += y;
-      }
-      if (j < n) pre[j] = carry + x;
-      carry += __shfl(x, 63);
-    }
-    if (lane == 0) pre[ST_MAXN] = carry;
+// Row blocks of bm rows of all n segments (those of at most lo rows have none).
+// Every wave computes it by itself.
+__device__ __forceinline__ int st_row_blocks(const int32_t* __restrict__ offsets, int n, int bm, int lo = 0) {
+  const int lane = threadIdx.x & 63;
+  int x = 0;
+  for (int j = lane; j < n; j += 64) {
+    const int cnt = offsets[j + 1] - offsets[j];
+    x += cnt > lo ? (cnt + bm - 1) / bm : 0;
   }
-  __syncthreads();
-  return pre[ST_MAXN];
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+  return __builtin_amdgcn_readfirstlane(x);
 }
 
-// Tile L of (row blocks) * ntn: an expert's tiles follow one another, in groups
-// of ST_GM row blocks that run through the column blocks together, so that
+// Tile `local` of one segment of `rows` rows from row o, `blocks` row blocks:
+// groups of ST_GM row blocks run through the column blocks together, so that
 // neighbouring tiles share weight columns and an expert's rows in an L2.
-__device__ __forceinline__ StTile st_tile_at(int L, const int32_t* __restrict__ offsets, int n, int ntn, int bm,
-                                             const int* pre) {
-  int lo = 0, hi = n - 1;
-  const int q = L / ntn;   // first e with pre[e] > q
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] > q) hi = mid; else lo = mid + 1;
-  }
-  const int first = lo ? pre[lo - 1] : 0;
-  const int nrb = pre[lo] - first;
-  const int local = L - first * ntn;
-  const int mg = local / (ST_GM * ntn);
+__device__ __forceinline__ StTile st_tile_of(int local, int o, int rows, int blocks, int ntn, int bm) {
+  const int mg = st_div(local, ST_GM * ntn);
   const int rem = local - mg * ST_GM * ntn;
-  const int gsz = min(ST_GM, nrb - mg * ST_GM);
-  const int nt = rem / gsz;
+  const int gsz = min(ST_GM, blocks - mg * ST_GM);
+  const int nt = st_div(rem, gsz);
   const int mb = mg * ST_GM + (rem - nt * gsz);
-  const int o = offsets[lo];
-  StTile t;
-  t.e = __builtin_amdgcn_readfirstlane(lo);
-  t.r0 = __builtin_amdgcn_readfirstlane(o + mb * bm);
-  t.R = __builtin_amdgcn_readfirstlane(min(bm, offsets[lo + 1] - o - mb * bm));
-  t.nt = __builtin_amdgcn_readfirstlane(nt);
+  return StTile{0, __builtin_amdgcn_readfirstlane(o + mb * bm),
+                __builtin_amdgcn_readfirstlane(min(bm, rows - mb * bm)), __builtin_amdgcn_readfirstlane(nt)};
+}
+
+// Tile L of (row blocks) * ntn, expert by expert.  Every wave searches by
+// itself (64 experts a step), which leaves all of LDS to the rings.
+__device__ __forceinline__ StTile st_tile_at(int L, const int32_t* __restrict__ offsets, int n, int ntn, int bm,
+                                             int lo = 0) {
+  const int lane = threadIdx.x & 63;
+  const int q = st_div(L, ntn);   // the row block, counted over all experts
+  StTile t{0, 0, 0, 0};
+  for (int j0 = 0, before = 0; j0 < n; j0 += 64) {
+    const int j = j0 + lane;
+    const int o = j < n ? offsets[j] : 0;
+    const int cnt = j < n ? offsets[j + 1] - o : 0;
+    const int nrb = cnt > lo ? (cnt + bm - 1) / bm : 0;
+    int x = nrb;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(x, off);
+      if (lane >= off) x += y;
+    }
+    const uint64_t hit = __ballot(before + x > q);
+    if (hit) {
+      const int at = __ffsll((unsigned long long)hit) - 1;
+      const int blocks = __shfl(nrb, at), first = before + __shfl(x, at) - blocks;
+      const int o0 = __shfl(o, at), rows = __shfl(cnt, at);
+      t = st_tile_of(L - first * ntn, o0, rows, blocks, ntn, bm);
+      t.e = __builtin_amdgcn_readfirstlane(j0 + at);
+      return t;
+    }
+    before += __shfl(x, 63);
+  }
   return t;
 }
 
@@ -504,16 +516,16 @@ __device__ __forceinline__ int st_first_tile() {
   return (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
 }
 
-// The persistent loop.  setup(L, ctx) describes tile L, fill(L, acc, stored)
-// finishes it with exactly Cfg::STORES stores per wave.  setup may leave ctx.nst
-// = 0 (a tile of zeros).
+// The persistent loop.  setup(L, ctx) describes tile L and returns what
+// finish(tile, acc) needs to store it, with exactly Cfg::STORES stores per wave.
+// setup may leave ctx.nst = 0 (a tile of zeros).
 template <class Cfg, class Setup, class Finish>
 __device__ __forceinline__ void st_run(int total, char* ring, const Setup& setup, const Finish& finish) {
   const StLane<Cfg> l = st_lanes<Cfg>(ring);
   int L = st_first_tile();
   if (L >= total) return;
   StCtx<Cfg> c;
-  setup(L, c);
+  auto tile = setup(L, c);
   st_prologue(c, l);
   bool stores = false;
   for (;;) {
@@ -522,17 +534,122 @@ __device__ __forceinline__ void st_run(int total, char* ring, const Setup& setup
     else st_clear<Cfg>(acc);
     const int next = L + (int)gridDim.x;
     const bool more = next < total;
+    const auto done = tile;
     if (more) {
-      setup(next, c);
+      tile = setup(next, c);
       st_prologue(c, l);
     }
     __builtin_amdgcn_sched_barrier(0);
-    finish(L, acc);
+    finish(done, acc);
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
     if (!more) return;
     L = next;
     stores = true;
+  }
+}
+
+// The persistent loop for tiles of few stages (segments of a few hundred rows,
+// where a tile is mostly loading and storing).  A workgroup takes units: runs of
+// row blocks of one block of columns.  Two things differ from st_run:
+//   - the copies run ahead of the products across tiles and units: the stages
+//     form one sequence, and as soon as a stage's slots are free the next but
+//     one is copied, so that a tile's operands arrive while its predecessor is
+//     multiplied and stored;
+//   - a unit of two stages (up to 128 K-rows; one is padded to two with zeros)
+//     copies its columns once: stages alternate between the two slots, so the
+//     columns of stage s stay in theirs from tile to tile.
+// unit(U) gives a Unit with nst (stages, 0 or >= 2) and tiles; cols(unit, ctx)
+// and rows(unit, j, ctx) describe its operands for row block j; finish(unit, j,
+// acc) stores with exactly Cfg::STORES stores per wave.
+template <class Cfg, class UnitOf, class Cols, class Rows, class Finish>
+__device__ __forceinline__ void st_run_short(int total, char* ring, const UnitOf& unit, const Cols& cols,
+                                             const Rows& rows, const Finish& finish) {
+  static_assert(Cfg::NA == 2 && Cfg::NB == 2 && Cfg::NP == 1, "two slots, one phase");
+  constexpr int CA = Cfg::CA, S = Cfg::STORES;
+  const StLane<Cfg> l = st_lanes<Cfg>(ring);
+  const int G = (int)gridDim.x;
+  const int first = st_first_tile();
+  if (first >= total) return;
+  // the copies' place: unit Up, its row block jp, that block's next stage sp
+  int Up = first - G, jp = 0, sp = 0;
+  int ahead = 0;   // stages copied or on their way, not yet multiplied
+  StCtx<Cfg> p;
+  auto up = unit(first);
+  up.tiles = 0;   // before the first unit
+  auto copy_next = [&](int slot) __attribute__((always_inline)) {
+    while (up.nst == 0 || jp >= up.tiles) {
+      Up += G;
+      if (Up >= total) {
+        Up = total;   // nothing left: stay here
+        return;
+      }
+      up = unit(Up);
+      jp = sp = 0;
+      if (up.nst > 0) {
+        cols(up, p);
+        rows(up, 0, p);
+      }
+    }
+    if (jp == 0 || up.nst > 2) st_issue_b(p, l.lbase + Cfg::AREG + slot * Cfg::B::BYTES, sp);
+    st_issue_a(p, l.lbase + slot * Cfg::A::BYTES, sp);
+    ++ahead;
+    if (++sp == up.nst) {
+      sp = 0;
+      if (++jp < up.tiles) rows(up, jp, p);
+    }
+  };
+  copy_next(0);
+  copy_next(1);
+  int slot = 0;
+  bool stores = false;   // the last finish's stores may be outstanding
+  for (int U = first; U < total; U += G) {
+    const auto u = unit(U);
+    for (int j = 0; j < u.tiles; ++j) {
+      typename Cfg::Acc acc[Cfg::MT][8];
+      st_clear<Cfg>(acc);
+      if (u.nst > 0) {
+        // this stage's copies; after them came the next stage's (at least its
+        // rows) and the last tile's stores
+        if (ahead > 1) {
+          if (stores) st_sync<CA + S>();
+          else st_sync<CA>();
+        } else {
+          if (stores) st_sync<S>();
+          else st_sync<0>();
+        }
+        StFrag<Cfg> F, F1;
+        const char* as = ring + slot * Cfg::A::BYTES;
+        const char* bs = ring + Cfg::AREG + slot * Cfg::B::BYTES;
+#pragma unroll
+        for (int mt = 0; mt < Cfg::MT; ++mt) F.x[mt] = st_frag<Cfg::LA>(as, l.ao, 0, mt);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) F.w[t] = st_frag<Cfg::LB>(bs, l.bo, 0, t);
+        int s = 0;
+        for (; s + 1 < u.nst; ++s) {
+          st_kstep<true>(p, l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, s, 1, F, F1, acc);
+          // the next stage was copied before the stores only if this is the first
+          if (s == 0 && stores) st_sync<S>();
+          else st_sync<0>();
+          --ahead;
+          copy_next(slot);
+          slot ^= 1;
+          st_kstep<true>(p, l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, s + 1, 0, F1, F,
+                         acc);
+        }
+        st_kstep<true>(p, l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, s, 1, F, F1, acc);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        --ahead;
+        copy_next(slot);
+        slot ^= 1;
+        st_kstep<false>(p, l, ring, ring, s, 0, F1, F, acc);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      finish(u, j, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      stores = true;
+    }
   }
 }
 
