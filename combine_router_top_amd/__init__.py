@@ -152,8 +152,13 @@ class Spec:
         return self.T * min(self.k, self.n_local)
 
     def c(self) -> Problem:
-        return Problem(self.T, self.d, self.E, self.k, self.f, self.expert_lo, self.n_local,
-                       MOE_DTYPE_BF16 if self.dtype == "bf16" else MOE_DTYPE_F32, self.flags)
+        """The C structure (made once: the fields of a Spec do not change)."""
+        pc = self.__dict__.get("_c")
+        if pc is None:
+            pc = Problem(self.T, self.d, self.E, self.k, self.f, self.expert_lo, self.n_local,
+                         MOE_DTYPE_BF16 if self.dtype == "bf16" else MOE_DTYPE_F32, self.flags)
+            object.__setattr__(self, "_c", pc)
+        return pc
 
     @staticmethod
     def of(w, flags: int = 0) -> "Spec":
@@ -172,9 +177,15 @@ def workspace_bytes(p: Spec, call: int = MOE_CALL_LAYER) -> int:
 # ---------------------------------------------------------------------------
 # torch helpers (device memory and streams only)
 # ---------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dt(p: Spec):
@@ -187,20 +198,31 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream=None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
     t = _torch()
-    s = stream if stream is not None else t.cuda.current_stream()
-    return s.cuda_stream
+    # what torch.cuda.current_stream().cuda_stream gives, without the Stream object
+    return t._C._cuda_getCurrentRawStream(t._C._cuda_getDevice())
 
 
 def _need(t, shape, dtype, name):
     torch = _torch()
     if t is None:
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape and tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous device tensor")
     return t
+
+
+def _here(*named):
+    """Refuses tensors of another device than the current one, on whose stream
+    the call would run: (tensor or None, name) pairs."""
+    cur = _torch()._C._cuda_getDevice()
+    for t, name in named:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"{name} is on device {t.get_device()}, the current device is {cur}")
 
 
 def alloc_workspace(p: Spec, call: int = MOE_CALL_LAYER, device="cuda"):
@@ -394,6 +416,8 @@ def expert_gemm_train(p: Spec, x_packed, offsets, w1, w3, w2, workspace=None, st
     for t, n, name in ((g, p.f, "g"), (u, p.f, "u"), (h, p.f, "h"), (yp, p.d, "y_packed")):
         _need(t, (p.rows_max, n), dt, name)
     ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_TRAIN, dev)
+    _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (w3, "w3"), (w2, "w2"), (g, "g"),
+          (u, "u"), (h, "h"), (yp, "y_packed"), (ws, "workspace"))
     pc = p.c()
     _check(lib().moe_expert_gemm_train(ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1),
                                        _ptr(w3), _ptr(w2), _ptr(g), _ptr(u), _ptr(h), _ptr(yp),
@@ -424,6 +448,9 @@ def expert_gemm_backward(p: Spec, x_packed, offsets, w1, w3, w2, g, u, h, dy_pac
         if t is not None:
             _need(t, shape, dt, name)
     ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_BACKWARD, dev)
+    _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (w3, "w3"), (w2, "w2"), (g, "g"),
+          (u, "u"), (h, "h"), (dy_packed, "dy_packed"), (dx, "dx_packed"), (dw1, "dw1"), (dw3, "dw3"),
+          (dw2, "dw2"), (ws, "workspace"))
     pc = p.c()
     _check(lib().moe_expert_gemm_backward(
         ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(g), _ptr(u),
@@ -453,6 +480,8 @@ def combine_backward(p: Spec, dy, y_packed, inv, topk_w, stream=None, out=None,
         _need(dw, (p.T, p.k), torch.float32, "dtopk_w")
     if dw is not None or y_packed is not None:
         _need(y_packed, (n, p.d), dt, "y_packed")
+    _here((dy, "dy"), (y_packed, "y_packed"), (inv, "inv"), (topk_w, "topk_w"), (dyp, "dy_packed"),
+          (dw, "dtopk_w"))
     pc = p.c()
     _check(lib().moe_combine_backward(ctypes.byref(pc), _ptr(dy), _ptr(y_packed), _ptr(inv),
                                       _ptr(topk_w), _ptr(dyp), _ptr(dw), _stream(stream)))
@@ -480,6 +509,7 @@ def quantize_rows(x, stream=None, out=None):
                                         torch.empty(rows, dtype=torch.float32, device=x.device))
     _need(q, (rows, K), torch.int8, "q")
     _need(s, (rows,), torch.float32, "scale")
+    _here((x, "x"), (q, "q"), (s, "scale"))
     _check(lib().moe_quantize_rows(rows, K, code, _ptr(x), _ptr(q), _ptr(s), _stream(stream)))
     return q, s
 
@@ -512,7 +542,8 @@ def pack_weights(w, stream=None, out=None):
     """int8 weights [n, K, N] or [K, N] in the order the 8-bit products read."""
     torch = _torch()
     n, K, N, _, packed = _packed_out(w, out)
-    _need(w, tuple(w.shape), torch.int8, "w")
+    _need(w, w.shape, torch.int8, "w")
+    _here((w, "w"), (packed, "packed"))
     _check(lib().moe_pack_weights(n, K, N, _ptr(w), _ptr(packed), _stream(stream)))
     return packed
 
@@ -523,9 +554,10 @@ def quantize_weights(w, stream=None, out=None):
     torch = _torch()
     code = _dtype_code(w, "w")
     n, K, N, lead, packed = _packed_out(w, None if out is None else out[0])
-    _need(w, tuple(w.shape), w.dtype, "w")
+    _need(w, w.shape, w.dtype, "w")
     s = torch.empty(lead + (N,), dtype=torch.float32, device=w.device) if out is None else out[1]
     _need(s, lead + (N,), torch.float32, "scale")
+    _here((w, "w"), (packed, "packed"), (s, "scale"))
     _check(lib().moe_quantize_weights(n, K, N, code, _ptr(w), _ptr(packed), _ptr(s), _stream(stream)))
     return packed, s
 
@@ -544,6 +576,7 @@ def gemm_quantized(a, a_scale, packed, b_scale, dtype=None, stream=None, out=Non
     if out is None:
         out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
     _need(out, (M, N), dtype or out.dtype, "out")
+    _here((a, "a"), (a_scale, "a_scale"), (packed, "packed"), (b_scale, "b_scale"), (out, "out"))
     _check(lib().moe_gemm_quantized(M, N, K, _ptr(a), _ptr(a_scale), _ptr(packed), _ptr(b_scale),
                                     _ptr(out), _dtype_code(out, "out"), _stream(stream)))
     return out
@@ -568,6 +601,8 @@ def expert_gemm_quantized(p: Spec, x_packed, offsets, w1, s1, w3, s3, w2, s2, wo
     _need(h, (p.rows_max, p.f), dt, "h")
     _need(yp, (p.rows_max, p.d), dt, "y_packed")
     ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_QUANTIZED, dev)
+    _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (s1, "s1"), (w3, "w3"), (s3, "s3"),
+          (w2, "w2"), (s2, "s2"), (h, "h"), (yp, "y_packed"), (ws, "workspace"))
     pc = p.c()
     _check(lib().moe_expert_gemm_quantized(
         ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1), _ptr(s1), _ptr(w3), _ptr(s3),
