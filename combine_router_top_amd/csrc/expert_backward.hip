@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "kernels.h"
@@ -37,9 +38,9 @@ __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& d
 }
 
 template <int MT, bool KT>
-using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, KT, 8 * MT>;
+using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, KT, (MT == 1 ? 4 : 8) * MT>;
 template <int MT, bool KT>
-using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, KT, 4 * MT>;
+using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, KT, (MT == 1 ? 2 : 4) * MT>;
 template <bool SHORT>
 using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, false, 16, SHORT>;
 
@@ -64,12 +65,12 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
         const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM);
         const uint32_t ld = (uint32_t)d * 2;
         st_rows(c.a[0], dy + (int64_t)t.r0 * d, ld, t.R, ld);
-        st_rows(c.b[0], w2 + ((int64_t)t.e * f + 256 * t.nt) * d, ld, min(ST_BN, f - 256 * t.nt), ld);
+        st_rows(c.b[0], w2 + ((int64_t)t.e * f + Cfg::BN * t.nt) * d, ld, min(Cfg::BN, f - Cfg::BN * t.nt), ld);
         c.nst = c.nst1 = (d + 63) / 64;
         c.kvals = d;
         return t;
       },
-      [&](const StTile& t, f32x4 (&acc)[MT][8]) {
+      [&](const StTile& t, typename Cfg::Acc& acc) {
         const int64_t first = (int64_t)t.r0 * f;
         const int64_t ld = (int64_t)f * 2;
         const StOut og = st_out(dg + first, ld, t.R), ou = st_out(du + first, ld, t.R);
@@ -78,17 +79,17 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const int row = 16 * MT * wm + 16 * mt + i;
-          u32x4 gv[4], uv[4];
+          u32x4 gv[Cfg::NT / 2], uv[Cfg::NT / 2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int col = 256 * t.nt + 128 * wn + 32 * k + 8 * q;
+          for (int k = 0; k < Cfg::NT / 2; ++k) {
+            const int col = Cfg::BN * t.nt + Cfg::WN * wn + 32 * k + 8 * q;
             const uint32_t at = col < f ? (uint32_t)row * (uint32_t)ld + 2u * (uint32_t)col : 0xFFFFFFF0u;
             gv[k] = __builtin_amdgcn_raw_buffer_load_b128(rg, at, 0, 0);
             uv[k] = __builtin_amdgcn_raw_buffer_load_b128(ru, at, 0, 0);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int col = 256 * t.nt + 128 * wn + 32 * k + 8 * q;
+          for (int k = 0; k < Cfg::NT / 2; ++k) {
+            const int col = Cfg::BN * t.nt + Cfg::WN * wn + 32 * k + 8 * q;
             float x[4], y[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -113,16 +114,16 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
       });
 }
 
-// bf16 rows of a finished tile: columns col0 + 128 wn .. of N.
-template <int MT>
-__device__ __forceinline__ void store_tile(const StOut& o, const f32x4 (&acc)[MT][8], int col0, int N) {
+// bf16 rows of a finished tile: its columns from col0, those below N.
+template <int MT, int NT>
+__device__ __forceinline__ void store_tile(const StOut& o, const f32x4 (&acc)[MT][NT], int col0, int N) {
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int col = col0 + 128 * (wave >> 2) + 32 * k + 8 * q;
+    for (int k = 0; k < NT / 2; ++k) {
+      const int col = col0 + 16 * NT * (wave >> 2) + 32 * k + 8 * q;
       st_put(o, 16 * MT * (wave & 3) + 16 * mt + i, 2u * (uint32_t)col, col < N,
              st_pack8(acc[mt][2 * k], acc[mt][2 * k + 1]));
     }
@@ -170,8 +171,8 @@ __global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __rest
       [&](int L, StCtx<Cfg>& c) {
         const StTile t = st_tile_at(L, offsets, n, ntn, Cfg::BM);
         const uint32_t ld = (uint32_t)f * 2;
-        const int64_t arow = (int64_t)t.r0 * f, brow = ((int64_t)t.e * d + 256 * t.nt) * f;
-        const int cols = min(ST_BN, d - 256 * t.nt);
+        const int64_t arow = (int64_t)t.r0 * f, brow = ((int64_t)t.e * d + Cfg::BN * t.nt) * f;
+        const int cols = min(Cfg::BN, d - Cfg::BN * t.nt);
         st_rows(c.a[0], dg + arow, ld, t.R, ld);
         st_rows(c.a[1], du + arow, ld, t.R, ld);
         st_rows(c.b[0], w1 + brow, ld, cols, ld);
@@ -181,8 +182,8 @@ __global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __rest
         c.kvals = f;
         return t;
       },
-      [&](const StTile& t, f32x4 (&acc)[MT][8]) {
-        store_tile(st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R), acc, 256 * t.nt, d);
+      [&](const StTile& t, typename Cfg::Acc& acc) {
+        store_tile(st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R), acc, Cfg::BN * t.nt, d);
       });
 }
 
@@ -478,35 +479,35 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
   const int mt = mean >= 256 ? 4 : mean > 96 ? 3 : 2;
   const bf16_t* DG = (const bf16_t*)dgp;
   const bf16_t* DU = (const bf16_t*)dup;
-  if (gate) {
-    const int ntn = (p.f + 255) / 256;
-    auto go = [&](auto kernel, int bm) {
-      hipLaunchKernelGGL(kernel, row_grid(bm, ntn), dim3(ST_NT), 0, st, (const bf16_t*)dy, offsets, p.n,
-                         (const bf16_t*)w2, (const bf16_t*)g, (const bf16_t*)u, (bf16_t*)dgp, (bf16_t*)dup, p.d, p.f,
-                         ntn);
+  // the kernel of this product's tile and K tail
+  auto launch = [&](auto pick, int K, int N, auto... args) {
+    // 64 x 128 tiles where those make at most two rounds of workgroups: larger
+    // ones would leave most compute units idle
+    const int64_t small = (int64_t)p.n * std::max<int64_t>(1, (mean + 63) / 64) * ((N + 127) / 128);
+    const int h = small <= 2 * device_cus() ? 1 : mt;
+    const int bn = h == 1 ? 128 : 256, ntn = (N + bn - 1) / bn;
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, row_grid(64 * h, ntn), dim3(ST_NT), 0, st, args..., ntn);
       return hipGetLastError();
     };
-    if (p.d % 64 == 0)
-      e = mt == 4 ? go(gate_grad_bf16<4, false>, 256)
-                  : mt == 3 ? go(gate_grad_bf16<3, false>, 192) : go(gate_grad_bf16<2, false>, 128);
-    else
-      e = mt == 4 ? go(gate_grad_bf16<4, true>, 256)
-                  : mt == 3 ? go(gate_grad_bf16<3, true>, 192) : go(gate_grad_bf16<2, true>, 128);
+    auto tail = [&](auto height) {
+      return K % 64 == 0 ? go(pick(height, std::false_type{})) : go(pick(height, std::true_type{}));
+    };
+    switch (h) {
+      case 1: return tail(std::integral_constant<int, 1>{});
+      case 2: return tail(std::integral_constant<int, 2>{});
+      case 3: return tail(std::integral_constant<int, 3>{});
+      default: return tail(std::integral_constant<int, 4>{});
+    }
+  };
+  if (gate) {
+    e = launch([](auto h, auto kt) { return gate_grad_bf16<h(), kt()>; }, p.d, p.f, (const bf16_t*)dy, offsets, p.n,
+               (const bf16_t*)w2, (const bf16_t*)g, (const bf16_t*)u, (bf16_t*)dgp, (bf16_t*)dup, p.d, p.f);
     if (e != hipSuccess) return e;
   }
   if (dx) {
-    const int ntn = (p.d + 255) / 256;
-    auto go = [&](auto kernel, int bm) {
-      hipLaunchKernelGGL(kernel, row_grid(bm, ntn), dim3(ST_NT), 0, st, DG, DU, offsets, p.n, (const bf16_t*)w1,
-                         (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn);
-      return hipGetLastError();
-    };
-    if (p.f % 64 == 0)
-      e = mt == 4 ? go(input_grad_bf16<4, false>, 256)
-                  : mt == 3 ? go(input_grad_bf16<3, false>, 192) : go(input_grad_bf16<2, false>, 128);
-    else
-      e = mt == 4 ? go(input_grad_bf16<4, true>, 256)
-                  : mt == 3 ? go(input_grad_bf16<3, true>, 192) : go(input_grad_bf16<2, true>, 128);
+    e = launch([](auto h, auto kt) { return input_grad_bf16<h(), kt()>; }, p.f, p.d, DG, DU, offsets, p.n,
+               (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f);
     if (e != hipSuccess) return e;
   }
   WeightGrads w{};

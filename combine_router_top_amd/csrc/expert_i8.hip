@@ -238,10 +238,11 @@ __device__ __forceinline__ void i8_values(const i32x4& p1, const i32x4& p3, floa
   }
 }
 
-// Tiles of 64 MT rows x 256 weight columns (GATED: 128 output columns of both
-// matrices) for segments of more than `lo` rows.
+// Tiles of 64 MT rows x 256 weight columns, or 64 x 128 (GATED: half as many
+// output columns, of both matrices), for segments of more than `lo` rows.
 template <int MT, bool GATED, bool F32OUT>
-using I8Cfg = StCfg<MT, ST_ROWS, ST_PACK, i32x4, 1, GATED, false, MT * (F32OUT ? 8 : 4) / (GATED ? 2 : 1)>;
+using I8Cfg = StCfg<MT, ST_ROWS, ST_PACK, i32x4, 1, GATED, false,
+                    MT * (MT == 1 ? 1 : 2) * (F32OUT ? 4 : 2) / (GATED ? 2 : 1)>;
 
 template <int MT, bool GATED, bool F32OUT>
 __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
@@ -260,18 +261,13 @@ __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
                                    : st_tile_of(L, 0, p.M, (p.M + Cfg::BM - 1) / Cfg::BM, ntn, Cfg::BM);
         st_rows(c.a[0], p.a + (int64_t)t.r0 * p.lda, (uint32_t)p.lda, t.R, (uint32_t)p.K);
         const int64_t eo = (int64_t)t.e * p.ntiles * run;
-        if (GATED) {
-          st_pack(c.b[0], 0, p.b1 + eo, 8 * t.nt, p.ntiles, run);
-          st_pack(c.b[0], 1, p.b3 + eo, 8 * t.nt, p.ntiles, run);
-        } else {
-          st_pack(c.b[0], 0, p.b1 + eo, 16 * t.nt, p.ntiles, run);
-          st_pack(c.b[0], 1, p.b1 + eo, 16 * t.nt + 8, p.ntiles, run);
-        }
+        st_pack<GATED>(c.b[0], p.b1 + eo, GATED ? p.b3 + eo : nullptr, (GATED ? Cfg::BN / 32 : Cfg::BN / 16) * t.nt,
+                       p.ntiles, run);
         c.nst = c.nst1 = (p.kt + 1) / 2;   // an odd last block meets zeros past its run
         c.kvals = 0;
         return t;
       },
-      [&](const StTile& t, i32x4 (&acc)[MT][8]) {
+      [&](const StTile& t, typename Cfg::Acc& acc) {
         constexpr int ES = F32OUT ? 4 : 2;
         const StOut out = st_out((char*)p.c + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
         float sr[MT];
@@ -279,9 +275,10 @@ __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
         for (int mt = 0; mt < MT; ++mt) sr[mt] = p.sa[t.r0 + min(16 * MT * wm + 16 * mt + i, t.R - 1)];
         const float* s1 = p.s1 + (int64_t)t.e * p.N;
         const float* s3 = GATED ? p.s3 + (int64_t)t.e * p.N : nullptr;
-        const int col0 = GATED ? 128 * t.nt + 64 * wn : 256 * t.nt + 128 * wn;
+        const int col0 = (GATED ? Cfg::BN / 2 * t.nt + Cfg::WN / 2 * wn : Cfg::BN * t.nt + Cfg::WN * wn);
+        constexpr int OT = GATED ? Cfg::NT / 2 : Cfg::NT;   // column tiles of output
 #pragma unroll
-        for (int k = 0; k < (GATED ? 4 : 8); k += 2) {
+        for (int k = 0; k < OT; k += 2) {
           f32x4 c1[2], c3[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -293,8 +290,8 @@ __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
           for (int mt = 0; mt < MT; ++mt) {
             const int row = 16 * MT * wm + 16 * mt + i;
             float x[4], y[4];
-            i8_values<GATED>(acc[mt][k], acc[mt][GATED ? k + 4 : k], sr[mt], c1[0], c3[0], x);
-            i8_values<GATED>(acc[mt][k + 1], acc[mt][GATED ? k + 5 : k + 1], sr[mt], c1[1], c3[1], y);
+            i8_values<GATED>(acc[mt][k], acc[mt][GATED ? k + OT : k], sr[mt], c1[0], c3[0], x);
+            i8_values<GATED>(acc[mt][k + 1], acc[mt][GATED ? k + OT + 1 : k + 1], sr[mt], c1[1], c3[1], y);
             if (F32OUT) {
               const int at = col0 + 16 * k + 4 * q;
               st_put(out, row, 4u * (uint32_t)at, at < p.N, __builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]}));
@@ -436,16 +433,24 @@ static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t r
     if (e != hipSuccess || most <= I8_THIN) return e;
   }
   p.lo = stream ? I8_THIN : 0;
-  const int cols = GATED ? 128 : 256;
+  // tile height from the expected segment, and small tiles, as in the backward pass
+  const int64_t small =
+      (int64_t)p.n * std::max<int64_t>(1, (mean + 63) / 64) * ((p.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
+  const int mt = small <= 2 * device_cus() ? 1 : mean >= 256 ? 4 : mean > 96 ? 3 : 2;
+  const int cols = (mt == 1 ? 128 : 256) / (GATED ? 2 : 1);
   const int ntn = (p.N + cols - 1) / cols;
-  auto go = [&](auto kernel, int bm) {
+  auto go = [&](auto kernel) {
+    const int bm = 64 * mt;
     const int64_t blocks = std::min<int64_t>(rows_max / bm + std::min<int64_t>(p.n, rows_max), rows_max);
     hipLaunchKernelGGL(kernel, dim3(st_grid(blocks * ntn)), dim3(ST_NT), 0, st, p, ntn);
     return hipGetLastError();
   };
-  // tile height from the expected segment, as in the backward pass
-  if (mean >= 256) return go(i8_tile<4, GATED, F32OUT>, 256);
-  return mean > 96 ? go(i8_tile<3, GATED, F32OUT>, 192) : go(i8_tile<2, GATED, F32OUT>, 128);
+  switch (mt) {
+    case 1: return go(i8_tile<1, GATED, F32OUT>);
+    case 2: return go(i8_tile<2, GATED, F32OUT>);
+    case 3: return go(i8_tile<3, GATED, F32OUT>);
+    default: return go(i8_tile<4, GATED, F32OUT>);
+  }
 }
 
 hipError_t launch_quantize_rows(const void* x, int dtype, int64_t rows, int K, int64_t ldq, void* q, float* s,

@@ -2,10 +2,10 @@
 // in any of three ways (gfx950): the products of the experts' backward pass
 // (bf16) and of the 8-bit experts (int8) share this core.
 //
-// A workgroup of 8 waves computes (64 MT) x 256 tiles, MT = 2, 3 or 4, in
-// stages of 128 bytes of K (64 bf16 or 128 int8 values, two 16x16 MFMA
-// k-steps).  Wave (wm, wn) = (w & 3, w >> 2) multiplies 16 MT tile rows by 128
-// tile columns.  Both operands of a stage are copied from memory straight into
+// A workgroup of 8 waves computes (64 MT) x 256 tiles, MT = 2, 3 or 4, or, for
+// small problems, 64 x 128 tiles, in stages of 128 bytes of K (64 bf16 or 128
+// int8 values, two 16x16 MFMA k-steps).  Wave (wm, wn) = (w & 3, w >> 2)
+// multiplies 16 MT tile rows by half of the tile's columns.  Both operands of a stage are copied from memory straight into
 // LDS (16 bytes per lane and instruction), the rows into a ring of NA slots and
 // the columns into one of NB.  While a wave multiplies one k-step from
 // registers it reads the fragments of the next.  A stage costs one barrier, in
@@ -33,8 +33,8 @@
 //
 // The MFMA takes the column operand first, so a product lane holds 4
 // consecutive columns of one row: lane (i, g) = (l % 16, l / 16) of wave
-// (wm, wn) holds in acc[mt][t] row 16 MT wm + 16 mt + i, columns 128 wn + 16 t
-// + 4 g .. + 3.  st_swap_pair exchanges two column tiles between lane groups so
+// (wm, wn) holds in acc[mt][t] row 16 MT wm + 16 mt + i, columns WN wn + 16 t
+// + 4 g .. + 3 (WN: the columns of a wave).  st_swap_pair exchanges two column tiles between lane groups so
 // that a lane holds 8 consecutive columns: 16-byte stores, whole 64-byte
 // sectors per row.
 //
@@ -56,7 +56,6 @@ enum { ST_ROWS = 0, ST_PANEL = 1, ST_PACK = 2 };
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int ST_BN = 256;     // tile columns
 constexpr int ST_KB = 128;     // bytes of K per stage
 constexpr int ST_NT = 512;     // threads
 
@@ -65,7 +64,7 @@ template <int L, int W>
 struct StOp {
   static constexpr int C = W / 64;               // copies per wave per stage
   static constexpr int BYTES = W * ST_KB;        // bytes of a stage
-  const char* base[L == ST_PACK ? 2 : 1];        // wave-uniform
+  const char* base[L == ST_PACK ? C / 2 : 1];    // wave-uniform
   uint32_t v[L == ST_PANEL ? 2 : 1];             // lane source offsets at stage 0
   uint32_t ld;                                   // bytes between rows (ST_ROWS) or K-rows (ST_PANEL)
   uint32_t size;                                 // descriptor bytes (ST_ROWS, ST_PACK)
@@ -110,14 +109,21 @@ __device__ __forceinline__ void st_panel(StOp<ST_PANEL, W>& o, const void* base,
   o.size = 0;
 }
 
-// ST_PACK, the 128-column half `half`: 16-column tiles nt0 .. nt0 + 7 of a
-// packed matrix of `ntiles` of them, each a run of `run` bytes (1 KB per 64 K);
-// tiles past the last repeat it (their columns are never stored).
-template <int W>
-__device__ __forceinline__ void st_pack(StOp<ST_PACK, W>& o, int half, const void* base, int nt0, int ntiles,
+// ST_PACK: 16-column tiles nt0, nt0 + 1, .. of the packed matrix b1 of `ntiles`
+// of them, each a run of `run` bytes (1 KB per 64 K); SPLIT: the first half of
+// the columns from b1, the second, the same tiles, from b3.  Tiles past the last
+// repeat it (their columns are never stored).
+template <bool SPLIT, int W>
+__device__ __forceinline__ void st_pack(StOp<ST_PACK, W>& o, const char* b1, const char* b3, int nt0, int ntiles,
                                         uint32_t run) {
+  constexpr int H = W / 32;   // tiles of one half
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  o.base[half] = (const char*)base + (int64_t)min(nt0 + wave, ntiles - 1) * run;
+#pragma unroll
+  for (int c = 0; c < W / 128; ++c) {
+    const int t = wave + 8 * c;
+    const char* b = SPLIT && t >= H ? b3 : b1;
+    o.base[c] = b + (int64_t)min(nt0 + (SPLIT && t >= H ? t - H : t), ntiles - 1) * run;
+  }
   o.v[0] = 16u * (uint32_t)(threadIdx.x & 63);
   o.ld = 0;
   o.size = run;
@@ -190,24 +196,27 @@ __device__ __forceinline__ i32x4 st_mfma(const u32x4& a, const u32x4& b, const i
                                                0, 0, 0);
 }
 
-// Tile configuration.  NP phases of operands follow one another along K (the
-// input gradient sums two products); all have the same shape.  SPLIT: the 256
-// columns are 128 of one packed matrix and the same 128 of a second (gate and
-// up products of one h column meet in one lane: acc[mt][t] and acc[mt][t + 4]).
-// KT: K is not a multiple of a stage; the fragments past its end are zeroed
-// (ST_ROWS reads there what follows the row).  STORES: store instructions of a
-// wave's epilogue, every one of them unconditional.  SHORT: two slots for each
-// operand, for st_run_short.
+// Tile configuration.  MT = 1: the 64 x 128 tile.  NP phases of operands follow
+// one another along K (the input gradient sums two products); all have the same
+// shape.  SPLIT: half of the columns are of one packed matrix, the others the
+// same columns of a second (gate and up products of one h column meet in one
+// lane: acc[mt][t] and acc[mt][t + NT / 2]).  KT: K is not a multiple of a stage;
+// the fragments past its end are zeroed (ST_ROWS reads there what follows the
+// row).  STORES: store instructions of a wave's epilogue, every one of them
+// unconditional.  SHORT: two slots for each operand, for st_run_short.
 template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, bool KT_, int STORES_, bool SHORT_ = false>
 struct StCfg {
   static constexpr int MT = MT_, LA = LA_, LB = LB_, NP = NP_, STORES = STORES_;
   static constexpr bool SPLIT = SPLIT_, KT = KT_;
-  typedef AccT_ Acc;
-  static constexpr int BM = 64 * MT;
+  static constexpr int BM = 64 * MT, BN = MT == 1 ? 128 : 256;
+  static constexpr int NT = BN / 32, WN = BN / 2;              // a wave's column tiles and columns
+  typedef AccT_ Acc[MT][NT];
   typedef StOp<LA, BM> A;
-  typedef StOp<LB, ST_BN> B;
-  // slots: the columns (weights, from HBM) three deep where LDS allows
-  static constexpr int NA = BM == 128 && !SHORT_ ? 3 : 2, NB = SHORT_ ? 2 : 3;
+  typedef StOp<LB, BN> B;
+  // slots: the columns (weights, from HBM) three deep where LDS allows; small
+  // tiles, of which a compute unit may have one alone, six deep, since nothing
+  // else hides the latency of their loads
+  static constexpr int NA = MT == 1 ? 6 : BM == 128 && !SHORT_ ? 3 : 2, NB = MT == 1 ? 6 : SHORT_ ? 2 : 3;
   static constexpr int AREG = NA * A::BYTES;                   // the column slots follow the row slots
   static constexpr int LDS = AREG + NB * B::BYTES;             // 128 to 160 KB (all there is)
   static constexpr int CA = A::C, CB = B::C;                   // copies per wave per stage
@@ -227,7 +236,7 @@ struct StCtx {
 
 template <class Cfg>
 struct StFrag {
-  u32x4 x[Cfg::MT], w[8];
+  u32x4 x[Cfg::MT], w[Cfg::NT];
 };
 
 // The copies of stage st into the slot at LDS address `at`.
@@ -270,8 +279,15 @@ __device__ __forceinline__ StLane<Cfg> st_lanes(char* ring) {
   StLane<Cfg> l;
   l.lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
   l.ao = st_lane<Cfg::LA>(Cfg::MT * (wave & 3));
-  l.bo = st_lane<Cfg::LB>((Cfg::SPLIT ? 4 : 8) * (wave >> 2));
+  l.bo = st_lane<Cfg::LB>((Cfg::SPLIT ? Cfg::NT / 2 : Cfg::NT) * (wave >> 2));
   return l;
+}
+
+// Where a wave's column tile t lies in a slot, from its first.
+template <class Cfg>
+__device__ __forceinline__ constexpr int st_slot_tile(int t) {
+  constexpr int H = Cfg::NT / 2;
+  return Cfg::SPLIT ? t % H + 2 * H * (t / H) : t;
 }
 
 // Multiply F; with READ, read k-step ks of stage st into G meanwhile, from the
@@ -283,7 +299,7 @@ __device__ __forceinline__ StLane<Cfg> st_lanes(char* ring) {
 template <bool READ, class Cfg>
 __device__ __forceinline__ void st_kstep(const StCtx<Cfg>& c, const StLane<Cfg>& l, const char* as, const char* bs,
                                          int st, int ks, const StFrag<Cfg>& F, StFrag<Cfg>& G,
-                                         typename Cfg::Acc (&acc)[Cfg::MT][8]) {
+                                         typename Cfg::Acc& acc) {
   constexpr int MT = Cfg::MT;
   const bool zero = READ && st_past(c, st, ks);
   __builtin_amdgcn_sched_barrier(0);
@@ -295,13 +311,12 @@ __device__ __forceinline__ void st_kstep(const StCtx<Cfg>& c, const StLane<Cfg>&
     }
   }
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
+  for (int t = 0; t < Cfg::NT; ++t) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[mt][t] = st_mfma(F.w[t], F.x[mt], acc[mt][t]);
     if (t == 0) __builtin_amdgcn_s_setprio(1);
     if (READ) {
-      const int tt = Cfg::SPLIT ? (t & 3) + 8 * (t >> 2) : t;
-      G.w[t] = st_frag<Cfg::LB>(bs, l.bo, ks, tt);
+      G.w[t] = st_frag<Cfg::LB>(bs, l.bo, ks, st_slot_tile<Cfg>(t));
       if (Cfg::KT && zero) G.w[t] = u32x4{0u, 0u, 0u, 0u};
     }
   }
@@ -310,27 +325,43 @@ __device__ __forceinline__ void st_kstep(const StCtx<Cfg>& c, const StLane<Cfg>&
 }
 
 template <class Cfg>
-__device__ __forceinline__ void st_clear(typename Cfg::Acc (&acc)[Cfg::MT][8]) {
+__device__ __forceinline__ void st_clear(typename Cfg::Acc& acc) {
 #pragma unroll
   for (int a = 0; a < Cfg::MT; ++a)
 #pragma unroll
-    for (int t = 0; t < 8; ++t) acc[a][t] = typename Cfg::Acc{};
+    for (int t = 0; t < Cfg::NT; ++t) acc[a][t] = {};
 }
 
-// The copies of a tile's first stages, in the order A0 B0 A1 B1 (A2) (B2).
+// The copies of a tile's first stages, in the order A0 B0 A1 B1 (A2) (B2) ..
 // Every wave must be done with the ring.
 template <class Cfg>
 __device__ __forceinline__ void st_prologue(const StCtx<Cfg>& c, const StLane<Cfg>& l) {
 #pragma unroll
-  for (int s = 0; s < 3; ++s) {
+  for (int s = 0; s < Cfg::NB; ++s) {
     if (s < Cfg::NA && s < c.nst) st_issue_a(c, l.lbase + s * Cfg::A::BYTES, s);
     if (s < Cfg::NB && s < c.nst) st_issue_b(c, l.lbase + Cfg::AREG + s * Cfg::B::BYTES, s);
   }
 }
 
+// Wait until n (0 .. 5) newer stages of CNT copies may be outstanding.
+template <int CNT>
+__device__ __forceinline__ void st_sync_n(int n) {
+  if (n >= 5) st_sync<5 * CNT>();
+  else if (n == 4) st_sync<4 * CNT>();
+  else if (n == 3) st_sync<3 * CNT>();
+  else if (n == 2) st_sync<2 * CNT>();
+  else if (n == 1) st_sync<CNT>();
+  else st_sync<0>();
+}
+
 // Wait for stage s (0 or 1) of the prologue with S later stores outstanding.
+// Small tiles wait for the stores as well: a workgroup has few of them.
 template <int S, class Cfg>
 __device__ __forceinline__ void st_wait_first(int s, int nst) {
+  if constexpr (Cfg::MT == 1) {
+    st_sync_n<Cfg::CA + Cfg::CB>(min(nst, Cfg::NA) - 1 - s);
+    return;
+  }
   constexpr int ST = Cfg::CA + Cfg::CB;                                       // a whole stage
   constexpr int THIRD = (Cfg::NA > 2 ? Cfg::CA : 0) + (Cfg::NB > 2 ? Cfg::CB : 0);
   if (s == 0) {
@@ -348,7 +379,7 @@ __device__ __forceinline__ void st_wait_first(int s, int nst) {
 // the end no copy is outstanding and every wave is done with the ring.
 template <class Cfg>
 __device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, const StLane<Cfg>& l, const char* ring, bool stores,
-                                         typename Cfg::Acc (&acc)[Cfg::MT][8]) {
+                                         typename Cfg::Acc& acc) {
   st_clear<Cfg>(acc);
   if (stores) st_wait_first<Cfg::STORES, Cfg>(0, c.nst);
   else st_wait_first<0, Cfg>(0, c.nst);
@@ -361,8 +392,8 @@ __device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, const StLane<Cfg>&
       if (Cfg::KT && zero) F.x[mt] = u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      F.w[t] = st_frag<Cfg::LB>(ring + Cfg::AREG, l.bo, 0, Cfg::SPLIT ? (t & 3) + 8 * (t >> 2) : t);
+    for (int t = 0; t < Cfg::NT; ++t) {
+      F.w[t] = st_frag<Cfg::LB>(ring + Cfg::AREG, l.bo, 0, st_slot_tile<Cfg>(t));
       if (Cfg::KT && zero) F.w[t] = u32x4{0u, 0u, 0u, 0u};
     }
   }
@@ -374,6 +405,9 @@ __device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, const StLane<Cfg>&
     if (s == 0) {
       if (stores) st_wait_first<Cfg::STORES, Cfg>(1, c.nst);
       else st_wait_first<0, Cfg>(1, c.nst);
+    } else if (Cfg::MT == 1) {
+      // stages s + 2 .. s + NA - 1, those of them that exist
+      st_sync_n<Cfg::CA + Cfg::CB>(min(c.nst - 2 - s, Cfg::NA - 2));
     } else if (s + 2 < c.nst) {
       st_sync<Cfg::LATER>();
     } else {
@@ -381,11 +415,12 @@ __device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, const StLane<Cfg>&
     }
     if (s + Cfg::NA < c.nst) st_issue_a(c, l.lbase + as, s + Cfg::NA);
     const uint32_t free_b = bs;
+    if (Cfg::MT == 1 && s + Cfg::NB < c.nst) st_issue_b(c, l.lbase + free_b, s + Cfg::NB);
     as = as == (Cfg::NA - 1) * Cfg::A::BYTES ? 0 : as + Cfg::A::BYTES;
     bs = bs == Cfg::AREG + (Cfg::NB - 1) * Cfg::B::BYTES ? Cfg::AREG : bs + Cfg::B::BYTES;
     st_kstep<true>(c, l, ring + as, ring + bs, s + 1, 0, G, F, acc);
     // half a stage after the rows' copies, which spreads the requests
-    if (s + Cfg::NB < c.nst) st_issue_b(c, l.lbase + free_b, s + Cfg::NB);
+    if (Cfg::MT != 1 && s + Cfg::NB < c.nst) st_issue_b(c, l.lbase + free_b, s + Cfg::NB);
   }
   st_kstep<true>(c, l, ring + as, ring + bs, s, 1, F, G, acc);
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -529,7 +564,7 @@ __device__ __forceinline__ void st_run(int total, char* ring, const Setup& setup
   st_prologue(c, l);
   bool stores = false;
   for (;;) {
-    typename Cfg::Acc acc[Cfg::MT][8];
+    typename Cfg::Acc acc;
     if (c.nst > 0) st_accum(c, l, ring, stores, acc);
     else st_clear<Cfg>(acc);
     const int next = L + (int)gridDim.x;
@@ -606,7 +641,7 @@ __device__ __forceinline__ void st_run_short(int total, char* ring, const UnitOf
   for (int U = first; U < total; U += G) {
     const auto u = unit(U);
     for (int j = 0; j < u.tiles; ++j) {
-      typename Cfg::Acc acc[Cfg::MT][8];
+      typename Cfg::Acc acc;
       st_clear<Cfg>(acc);
       if (u.nst > 0) {
         // this stage's copies; after them came the next stage's (at least its
@@ -624,7 +659,7 @@ __device__ __forceinline__ void st_run_short(int total, char* ring, const UnitOf
 #pragma unroll
         for (int mt = 0; mt < Cfg::MT; ++mt) F.x[mt] = st_frag<Cfg::LA>(as, l.ao, 0, mt);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) F.w[t] = st_frag<Cfg::LB>(bs, l.bo, 0, t);
+        for (int t = 0; t < Cfg::NT; ++t) F.w[t] = st_frag<Cfg::LB>(bs, l.bo, 0, t);
         int s = 0;
         for (; s + 1 < u.nst; ++s) {
           st_kstep<true>(p, l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, s, 1, F, F1, acc);

@@ -29,6 +29,14 @@ CASES = {
     "long_whole_k": ([513, 255, 256], 288, 544, "bf16", {}),
     "one_long": ([1100], 520, 264, "bf16", {}),
     "mid_k": ([70, 64], 96, 416, "bf16", {}),                        # 3 and 13 stages of K
+    # enough tiles for the 256-, 192- and 128-row kernels (fewer take 64 x 128
+    # tiles, as all the others here do), with and without K tails
+    "tall_many": ([300 + (37 * e) % 200 - 100 for e in range(64)], 264, 200, "bf16", dict(T=1200, k=16)),
+    "tall_many_whole_k": ([300 - (53 * e) % 200 + 100 for e in range(64)], 256, 192, "bf16", dict(T=1200, k=17)),
+    "mid_many": ([130 + (29 * e) % 140 - 70 for e in range(64)], 264, 328, "bf16", dict(T=520, k=16)),
+    "mid_many_whole_k": ([130 + (31 * e) % 140 - 70 for e in range(64)], 384, 320, "bf16", dict(T=520, k=17)),
+    "low_many": ([80 + (23 * e) % 90 - 45 if e % 7 else 0 for e in range(100)], 328, 264, "bf16", dict(T=320, k=25)),
+    "low_many_whole_k": ([80 + (19 * e) % 90 - 45 for e in range(100)], 384, 320, "bf16", dict(T=320, k=25)),
     "many_experts": ([(7 * e) % 5 for e in range(150)], 40, 48, "bf16", dict(T=40, k=8)),
     "no_rows": ([0, 0, 0], 64, 72, "bf16", dict(T=5, k=2)),
     "part_of_experts": ([9, 40, 0, 3], 72, 136, "bf16", dict(T=64, k=2, E=16)),
