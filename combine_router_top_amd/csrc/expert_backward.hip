@@ -291,41 +291,54 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
 }
 
 // ---------------------------------------------------------------------------
-// fp32: 64 x 64 tiles of 256 threads, 4 x 4 values each, K in steps of 16
-// through LDS, the next step's operands loaded while one is multiplied.  For
-// the small fp32 problems only.
+// fp32, for the small fp32 problems only: 32 x 32 tiles of eight waves that
+// split K.  Those problems have tens of tiles, so what counts is how many trips
+// to memory follow one another: each wave takes every eighth 16-deep slice of K
+// through its own LDS, the next slice's operands loaded while one is multiplied,
+// and the eight sums meet at the end, in a fixed order.
 // ---------------------------------------------------------------------------
-constexpr int F_K = 16, F_LD = 68;
+constexpr int F_K = 16, F_T = 32, F_LD = F_T + 4;   // slice depth, tile side, LDS row (16-byte aligned)
+constexpr int F_NW = 8;                             // waves
 
-// acc[a][b] += sum_k A(k, 4 ty + a) B(k, 4 tx + b) over k < K; A and B give 0
-// outside their operand and are called with tile indices 0 .. 63.
+struct F32Lds {
+  float a[F_NW][F_K * F_LD], b[F_NW][F_K * F_LD];
+  float sum[F_NW - 1][F_T * F_T];
+};
+
+// acc[p][r] of this lane: rows 4 ty + p, columns 4 tx + r (ty, tx = lane / 8,
+// lane % 8) of the sum over k < K of A(k, row) B(k, column), complete in wave 0.
+// A and B give 0 outside their operand; *_kfast: k is their contiguous index.
+// All waves call.
 template <class FA, class FB>
-__device__ __forceinline__ void f32_tile(const FA& A, bool a_kfast, const FB& B, bool b_kfast, int K, float* sa,
-                                         float* sb, float (&acc)[4][4]) {
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  float ra[4], rb[4];
-  // element v of a thread: (k, j) with the operand's contiguous index fastest over threads
-  auto ka = [&](int v) { return a_kfast ? tid & 15 : (tid >> 6) + 4 * v; };
-  auto ja = [&](int v) { return a_kfast ? (tid >> 4) + 16 * v : tid & 63; };
-  auto kb = [&](int v) { return b_kfast ? tid & 15 : (tid >> 6) + 4 * v; };
-  auto jb = [&](int v) { return b_kfast ? (tid >> 4) + 16 * v : tid & 63; };
+__device__ __forceinline__ void f32_tile(const FA& A, bool a_kfast, const FB& B, bool b_kfast, int K, F32Lds& s,
+                                         float (&acc)[4][4]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tx = lane & 7, ty = lane >> 3;
+  float* sa = s.a[wave];
+  float* sb = s.b[wave];
+  float ra[8], rb[8];
+  // element v of a lane: (k, j), the operand's contiguous index fastest over lanes
+  auto kk = [&](bool kfast, int v) { return kfast ? lane & 15 : (lane >> 5) + 2 * v; };
+  auto jj = [&](bool kfast, int v) { return kfast ? (lane >> 4) + 4 * v : lane & 31; };
   auto load = [&](int k0) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      ra[v] = k0 + ka(v) < K ? A(k0 + ka(v), ja(v)) : 0.f;
-      rb[v] = k0 + kb(v) < K ? B(k0 + kb(v), jb(v)) : 0.f;
+    for (int v = 0; v < 8; ++v) {
+      const int ka = k0 + kk(a_kfast, v), kb = k0 + kk(b_kfast, v);
+      ra[v] = ka < K ? A(ka, jj(a_kfast, v)) : 0.f;
+      rb[v] = kb < K ? B(kb, jj(b_kfast, v)) : 0.f;
     }
   };
-  load(0);
-  for (int k0 = 0; k0 < K; k0 += F_K) {
-    __syncthreads();
+  load(F_K * wave);
+  for (int k0 = F_K * wave; k0 < K; k0 += F_NW * F_K) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      sa[ka(v) * F_LD + ja(v)] = ra[v];
-      sb[kb(v) * F_LD + jb(v)] = rb[v];
+    for (int v = 0; v < 8; ++v) {
+      sa[kk(a_kfast, v) * F_LD + jj(a_kfast, v)] = ra[v];
+      sb[kk(b_kfast, v) * F_LD + jj(b_kfast, v)] = rb[v];
     }
-    __syncthreads();
-    if (k0 + F_K < K) load(k0 + F_K);
+    // this wave alone writes and reads its part: LDS operations of a wave stay in order
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (k0 + F_NW * F_K < K) load(k0 + F_NW * F_K);
 #pragma unroll
     for (int k = 0; k < F_K; ++k) {
       const f32x4 a = *reinterpret_cast<const f32x4*>(sa + k * F_LD + 4 * ty);
@@ -335,82 +348,119 @@ __device__ __forceinline__ void f32_tile(const FA& A, bool a_kfast, const FB& B,
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[p][r] = fmaf(a[p], b[r], acc[p][r]);
     }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
 }
 
-// Row block b of 64 rows, counted over all segments; false past the last.
+// Adds the other waves' sums to wave 0's.
+__device__ __forceinline__ void f32_join(F32Lds& s, float (&acc)[4][4]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (wave) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s.sum[wave - 1][(4 * p + r) * 64 + lane] = acc[p][r];
+  }
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 0; w < F_NW - 1; ++w)
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[p][r] += s.sum[w][(4 * p + r) * 64 + lane];
+  }
+}
+
+// Row block b of 32 rows, counted over all segments; false past the last.
 __device__ __forceinline__ bool f32_row_block(const int32_t* offsets, int n, int b, StTile& t) {
-  t = st_tile_at(b, offsets, n, 1, 64);
+  t = st_tile_at(b, offsets, n, 1, F_T);
   return t.R > 0;
 }
 
-__global__ __launch_bounds__(256) void gate_grad_f32(const float* __restrict__ dy, const int32_t* __restrict__ offsets,
+// Calls put(row, column, value) for this lane's values of the tile.
+template <class Put>
+__device__ __forceinline__ void f32_store(const float (&acc)[4][4], const Put& put) {
+  if (threadIdx.x >= 64) return;
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) put(4 * ty + p, 4 * tx + r, acc[p][r]);
+}
+
+__global__ __launch_bounds__(64 * F_NW) void gate_grad_f32(const float* __restrict__ dy, const int32_t* __restrict__ offsets,
                                                      int n, const float* __restrict__ w2, const float* __restrict__ g,
                                                      const float* __restrict__ u, float* __restrict__ dg,
                                                      float* __restrict__ du, int d, int f) {
-  __shared__ __attribute__((aligned(16))) float sa[F_K * F_LD], sb[F_K * F_LD];
+  __shared__ __attribute__((aligned(16))) F32Lds s;
   StTile t;
   if (!f32_row_block(offsets, n, blockIdx.x, t)) return;
-  const int c0 = blockIdx.y * 64;
+  const int c0 = blockIdx.y * F_T;
   const float* a = dy + (int64_t)t.r0 * d;
-  const float* b = w2 + (int64_t)t.e * f * d;
+  const float* b = w2 + ((int64_t)t.e * f + c0) * d;
   float acc[4][4] = {};
   f32_tile([&](int k, int j) { return j < t.R ? a[(int64_t)j * d + k] : 0.f; }, true,
-           [&](int k, int j) { return c0 + j < f ? b[(int64_t)(c0 + j) * d + k] : 0.f; }, true, d, sa, sb, acc);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int p = 0; p < 4; ++p)
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * ty + p, col = c0 + 4 * tx + r;
-      if (row >= t.R || col >= f) continue;
-      const int64_t at = (int64_t)(t.r0 + row) * f + col;
-      const float gv = g[at], s = 1.0f / (1.0f + expf(-gv));
-      dg[at] = acc[p][r] * u[at] * (s * (1.0f + gv * (1.0f - s)));
-      du[at] = acc[p][r] * (gv * s);
-    }
+           [&](int k, int j) { return c0 + j < f ? b[(int64_t)j * d + k] : 0.f; }, true, d, s, acc);
+  f32_join(s, acc);
+  f32_store(acc, [&](int row, int col, float dh) {
+    if (row >= t.R || c0 + col >= f) return;
+    const int64_t at = (int64_t)(t.r0 + row) * f + c0 + col;
+    const float gv = g[at], sg = 1.0f / (1.0f + expf(-gv));
+    dg[at] = dh * u[at] * (sg * (1.0f + gv * (1.0f - sg)));
+    du[at] = dh * (gv * sg);
+  });
 }
 
-__global__ __launch_bounds__(256) void input_grad_f32(const float* __restrict__ dg, const float* __restrict__ du,
+__global__ __launch_bounds__(64 * F_NW) void input_grad_f32(const float* __restrict__ dg, const float* __restrict__ du,
                                                       const int32_t* __restrict__ offsets, int n,
                                                       const float* __restrict__ w1, const float* __restrict__ w3,
                                                       float* __restrict__ dx, int d, int f) {
-  __shared__ __attribute__((aligned(16))) float sa[F_K * F_LD], sb[F_K * F_LD];
+  __shared__ __attribute__((aligned(16))) F32Lds s;
   StTile t;
   if (!f32_row_block(offsets, n, blockIdx.x, t)) return;
-  const int c0 = blockIdx.y * 64;
+  const int c0 = blockIdx.y * F_T;
+  const int64_t ar = (int64_t)t.r0 * f, br = ((int64_t)t.e * d + c0) * f;
   float acc[4][4] = {};
-  for (int half = 0; half < 2; ++half) {
-    const float* a = (half ? du : dg) + (int64_t)t.r0 * f;
-    const float* b = (half ? w3 : w1) + (int64_t)t.e * d * f;
-    f32_tile([&](int k, int j) { return j < t.R ? a[(int64_t)j * f + k] : 0.f; }, true,
-             [&](int k, int j) { return c0 + j < d ? b[(int64_t)(c0 + j) * f + k] : 0.f; }, true, f, sa, sb, acc);
-  }
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int p = 0; p < 4; ++p)
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * ty + p, col = c0 + 4 * tx + r;
-      if (row < t.R && col < d) dx[(int64_t)(t.r0 + row) * d + col] = acc[p][r];
-    }
+  // both products as one sum over 2 f
+  f32_tile([&](int k, int j) { return j < t.R ? (k < f ? dg + ar : du + ar - f)[(int64_t)j * f + k] : 0.f; }, true,
+           [&](int k, int j) { return c0 + j < d ? (k < f ? w1 + br : w3 + br - f)[(int64_t)j * f + k] : 0.f; }, true,
+           2 * f, s, acc);
+  f32_join(s, acc);
+  f32_store(acc, [&](int row, int col, float v) {
+    if (row < t.R && c0 + col < d) dx[(int64_t)(t.r0 + row) * d + c0 + col] = v;
+  });
 }
 
-// C_e [M][N] = P^T Q over the segment's rows; blockIdx.z is the expert.
-__global__ __launch_bounds__(256) void weight_grad_f32(const float* __restrict__ P, const float* __restrict__ Q,
-                                                       float* __restrict__ C, int M, int N,
-                                                       const int32_t* __restrict__ offsets) {
-  __shared__ __attribute__((aligned(16))) float sa[F_K * F_LD], sb[F_K * F_LD];
-  const int e = blockIdx.z, o = offsets[e], cnt = offsets[e + 1] - o;
-  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  const float* a = P + (int64_t)o * M;
-  const float* b = Q + (int64_t)o * N;
+// C_e [M][N] = P^T Q over the segment's rows, for up to three matrices: block z
+// is matrix z % nm of expert z / nm.
+struct WeightGradsF32 {
+  struct {
+    const float* P;
+    const float* Q;
+    float* C;
+    int M, N;
+  } m[3];
+};
+__global__ __launch_bounds__(64 * F_NW) void weight_grad_f32(WeightGradsF32 w, int nm,
+                                                             const int32_t* __restrict__ offsets) {
+  __shared__ __attribute__((aligned(16))) F32Lds s;
+  const int e = blockIdx.z / nm, k0 = blockIdx.z - e * nm;
+  const auto m = w.m[k0];
+  const int m0 = blockIdx.x * F_T, n0 = blockIdx.y * F_T;
+  if (m0 >= m.M || n0 >= m.N) return;
+  const int o = offsets[e], cnt = offsets[e + 1] - o;
+  const float* a = m.P + (int64_t)o * m.M + m0;
+  const float* b = m.Q + (int64_t)o * m.N + n0;
   float acc[4][4] = {};
-  if (cnt > 0)
-    f32_tile([&](int k, int j) { return m0 + j < M ? a[(int64_t)k * M + m0 + j] : 0.f; }, false,
-             [&](int k, int j) { return n0 + j < N ? b[(int64_t)k * N + n0 + j] : 0.f; }, false, cnt, sa, sb, acc);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int p = 0; p < 4; ++p)
-    for (int r = 0; r < 4; ++r) {
-      const int row = m0 + 4 * ty + p, col = n0 + 4 * tx + r;
-      if (row < M && col < N) C[((int64_t)e * M + row) * N + col] = acc[p][r];
-    }
+  f32_tile([&](int k, int j) { return m0 + j < m.M ? a[(int64_t)k * m.M + j] : 0.f; }, false,
+           [&](int k, int j) { return n0 + j < m.N ? b[(int64_t)k * m.N + j] : 0.f; }, false, cnt, s, acc);
+  f32_join(s, acc);
+  f32_store(acc, [&](int row, int col, float v) {
+    if (m0 + row < m.M && n0 + col < m.N) m.C[((int64_t)e * m.M + m0 + row) * m.N + n0 + col] = v;
+  });
 }
 
 // Zeros (the weight gradients of an empty batch): a kernel, so that a captured
@@ -446,24 +496,36 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
   char* dup = dgp + expert_backward_ws_bytes(p) / 2;
   const bool gate = dx || dw1 || dw3;
   if (p.dtype != 1) {
-    const unsigned rb = (unsigned)std::min<int64_t>((p.rows_max + 63) / 64 + p.n, p.rows_max);
-    const unsigned cf = (unsigned)((p.f + 63) / 64), cd = (unsigned)((p.d + 63) / 64);
+    const unsigned rb = (unsigned)std::min<int64_t>((p.rows_max + F_T - 1) / F_T + p.n, p.rows_max);
+    const unsigned cf = (unsigned)((p.f + F_T - 1) / F_T), cd = (unsigned)((p.d + F_T - 1) / F_T);
     if (gate) {
-      hipLaunchKernelGGL(gate_grad_f32, dim3(rb, cf), dim3(256), 0, st, (const float*)dy, offsets, p.n,
+      hipLaunchKernelGGL(gate_grad_f32, dim3(rb, cf), dim3(64 * F_NW), 0, st, (const float*)dy, offsets, p.n,
                          (const float*)w2, (const float*)g, (const float*)u, (float*)dgp, (float*)dup, p.d, p.f);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (dx) {
-      hipLaunchKernelGGL(input_grad_f32, dim3(rb, cd), dim3(256), 0, st, (const float*)dgp, (const float*)dup, offsets,
+      hipLaunchKernelGGL(input_grad_f32, dim3(rb, cd), dim3(64 * F_NW), 0, st, (const float*)dgp, (const float*)dup, offsets,
                          p.n, (const float*)w1, (const float*)w3, (float*)dx, p.d, p.f);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    const struct { const void *P, *Q; void* C; int M, N; } m[3] = {
-        {x, dgp, dw1, p.d, p.f}, {x, dup, dw3, p.d, p.f}, {h, dy, dw2, p.f, p.d}};
-    for (const auto& k : m) {
-      if (!k.C) continue;
-      hipLaunchKernelGGL(weight_grad_f32, dim3((k.M + 63) / 64, (k.N + 63) / 64, p.n), dim3(256), 0, st,
-                         (const float*)k.P, (const float*)k.Q, (float*)k.C, k.M, k.N, offsets);
+    WeightGradsF32 w{};
+    int nm = 0, M = 0, N = 0;
+    auto want = [&](const void* P, const void* Q, void* C, int m, int n) {
+      if (!C) return;
+      w.m[nm].P = (const float*)P;
+      w.m[nm].Q = (const float*)Q;
+      w.m[nm].C = (float*)C;
+      w.m[nm].M = m;
+      w.m[nm++].N = n;
+      M = std::max(M, m);
+      N = std::max(N, n);
+    };
+    want(x, dgp, dw1, p.d, p.f);
+    want(x, dup, dw3, p.d, p.f);
+    want(h, dy, dw2, p.f, p.d);
+    if (nm) {
+      hipLaunchKernelGGL(weight_grad_f32, dim3((M + F_T - 1) / F_T, (N + F_T - 1) / F_T, p.n * nm), dim3(64 * F_NW), 0,
+                         st, w, nm, offsets);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;

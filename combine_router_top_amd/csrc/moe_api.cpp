@@ -169,7 +169,7 @@ moe_status_t check_signal_shape(int32_t M, int32_t N, int32_t K) {
 // The backward pass addresses up to 256 rows of d or f elements, and a 2 GiB
 // run of rows in steps of 32, with 32-bit offsets.
 moe_status_t check_backward_widths(const moe::Prob& q) {
-  const int32_t lim = 1 << 21;
+  const int32_t lim = 1 << 20;
   if (q.d > lim || q.f > lim)
     return fail(MOE_ERR_UNSUPPORTED, "d=%d and f=%d must be at most %d", q.d, q.f, lim);
   return MOE_OK;
