@@ -21,7 +21,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "common.h"
 #include "kernels.h"
@@ -37,15 +36,15 @@ __device__ __forceinline__ void swiglu_grad(float dh, float g, float u, float& d
   du = dh * (g * s);
 }
 
-template <int MT, bool KT>
-using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, KT, (MT == 1 ? 4 : 8) * MT>;
-template <int MT, bool KT>
-using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, KT, (MT == 1 ? 2 : 4) * MT>;
+template <int MT>
+using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, (MT == 1 ? 4 : 8) * MT>;
+template <int MT>
+using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, (MT == 1 ? 2 : 4) * MT>;
 template <bool SHORT>
-using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, false, 16, SHORT>;
+using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, 16, SHORT>;
 
 // dh tiles: rows of dy against rows of W2 (its f rows are the output columns).
-template <int MT, bool KT>
+template <int MT>
 __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restrict__ dy,
                                                            const int32_t* __restrict__ offsets, int n,
                                                            const bf16_t* __restrict__ w2,
@@ -53,7 +52,7 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
                                                            const bf16_t* __restrict__ u,
                                                            bf16_t* __restrict__ dg, bf16_t* __restrict__ du,
                                                            int d, int f, int ntn) {
-  using Cfg = GateCfg<MT, KT>;
+  using Cfg = GateCfg<MT>;
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
   const int total = st_row_blocks(offsets, n, Cfg::BM) * ntn;
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
@@ -67,7 +66,6 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
         st_rows(c.a[0], dy + (int64_t)t.r0 * d, ld, t.R, ld);
         st_rows(c.b[0], w2 + ((int64_t)t.e * f + Cfg::BN * t.nt) * d, ld, min(Cfg::BN, f - Cfg::BN * t.nt), ld);
         c.nst = c.nst1 = (d + 63) / 64;
-        c.kvals = d;
         return t;
       },
       [&](const StTile& t, typename Cfg::Acc& acc) {
@@ -114,22 +112,7 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
       });
 }
 
-// bf16 rows of a finished tile: its columns from col0, those below N.
-template <int MT, int NT>
-__device__ __forceinline__ void store_tile(const StOut& o, const f32x4 (&acc)[MT][NT], int col0, int N) {
-  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int k = 0; k < NT / 2; ++k) {
-      const int col = col0 + 16 * NT * (wave >> 2) + 32 * k + 8 * q;
-      st_put(o, 16 * MT * (wave & 3) + 16 * mt + i, 2u * (uint32_t)col, col < N,
-             st_pack8(acc[mt][2 * k], acc[mt][2 * k + 1]));
-    }
-}
-
-// The same through a 4 KB staging area of this wave: a store then writes four
+// A finished tile through a 4 KB staging area of each wave: a store then writes four
 // rows of 256 bytes instead of sixteen pieces of 64, which cost the address
 // unit about 100 cycles an instruction and bounded tiles that mostly store.
 // Staged rows keep their 32-byte chunk c at c ^ (row & 7).
@@ -156,14 +139,14 @@ __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&ac
 }
 
 // dx tiles: [dg | du] against rows of W1, then of W3, in one accumulator.
-template <int MT, bool KT>
+template <int MT>
 __global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __restrict__ dg,
                                                             const bf16_t* __restrict__ du,
                                                             const int32_t* __restrict__ offsets, int n,
                                                             const bf16_t* __restrict__ w1,
                                                             const bf16_t* __restrict__ w3,
                                                             bf16_t* __restrict__ dx, int d, int f, int ntn) {
-  using Cfg = InputCfg<MT, KT>;
+  using Cfg = InputCfg<MT>;
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
   const int total = st_row_blocks(offsets, n, Cfg::BM) * ntn;
   st_run<Cfg>(
@@ -179,11 +162,10 @@ __global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __rest
         st_rows(c.b[1], w3 + brow, ld, cols, ld);
         c.nst1 = (f + 63) / 64;
         c.nst = 2 * c.nst1;
-        c.kvals = f;
         return t;
       },
       [&](const StTile& t, typename Cfg::Acc& acc) {
-        store_tile(st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R), acc, Cfg::BN * t.nt, d);
+        st_store_tile(st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R), acc, Cfg::BN * t.nt, d);
       });
 }
 
@@ -264,7 +246,6 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
   auto cols = [&](const Unit& r, StCtx<Cfg>& c) __attribute__((always_inline)) {
     st_panel(c.b[0], r.m.Q + (int64_t)r.o * r.m.N, (uint32_t)r.m.N * 2, r.cnt, 256 * r.tn, r.m.N);
     c.nst = c.nst1 = r.nst;
-    c.kvals = 0;
   };
   auto rows = [&](const Unit& r, int j, StCtx<Cfg>& c) __attribute__((always_inline)) {
     st_panel(c.a[0], r.m.P + (int64_t)r.o * r.m.M, (uint32_t)r.m.M * 2, r.cnt, 256 * (r.tm + j), r.m.M);
@@ -286,7 +267,7 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
           rows(r, 0, c);
           return r;
         },
-        [&](const Unit& r, f32x4 (&acc)[4][8]) { store_tile(out(r, 0), acc, 256 * r.tn, r.m.N); });
+        [&](const Unit& r, f32x4 (&acc)[4][8]) { st_store_tile(out(r, 0), acc, 256 * r.tn, r.m.N); });
   }
 }
 
@@ -530,46 +511,28 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
     }
     return hipSuccess;
   }
-  auto row_grid = [&](int bm, int ntn) {
-    const int64_t blocks = std::min<int64_t>(p.rows_max / bm + std::min<int64_t>(p.n, p.rows_max), p.rows_max);
-    return dim3(st_grid(blocks * ntn));
-  };
-  // Tile height from the expected segment: 256 rows where it fills them; below,
-  // the weights' stream bounds the product, and a height that holds a whole
-  // segment reads them once: 192 rows around a mean of 128.
-  const int64_t mean = p.tk() / p.E;
-  const int mt = mean >= 256 ? 4 : mean > 96 ? 3 : 2;
+  const int64_t mean = p.tk() / p.E;   // expected rows of a segment
   const bf16_t* DG = (const bf16_t*)dgp;
   const bf16_t* DU = (const bf16_t*)dup;
-  // the kernel of this product's tile and K tail
-  auto launch = [&](auto pick, int K, int N, auto... args) {
-    // 64 x 128 tiles where those make at most two rounds of workgroups: larger
-    // ones would leave most compute units idle
-    const int64_t small = (int64_t)p.n * std::max<int64_t>(1, (mean + 63) / 64) * ((N + 127) / 128);
-    const int h = small <= 2 * device_cus() ? 1 : mt;
-    const int bn = h == 1 ? 128 : 256, ntn = (N + bn - 1) / bn;
-    auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, row_grid(64 * h, ntn), dim3(ST_NT), 0, st, args..., ntn);
-      return hipGetLastError();
-    };
-    auto tail = [&](auto height) {
-      return K % 64 == 0 ? go(pick(height, std::false_type{})) : go(pick(height, std::true_type{}));
-    };
-    switch (h) {
-      case 1: return tail(std::integral_constant<int, 1>{});
-      case 2: return tail(std::integral_constant<int, 2>{});
-      case 3: return tail(std::integral_constant<int, 3>{});
-      default: return tail(std::integral_constant<int, 4>{});
-    }
-  };
   if (gate) {
-    e = launch([](auto h, auto kt) { return gate_grad_bf16<h(), kt()>; }, p.d, p.f, (const bf16_t*)dy, offsets, p.n,
-               (const bf16_t*)w2, (const bf16_t*)g, (const bf16_t*)u, (bf16_t*)dgp, (bf16_t*)dup, p.d, p.f);
+    e = st_with_height(st_height(p.n, mean, (int64_t)p.d * 2, p.f, 128), [&](auto h) {
+      constexpr int bn = GateCfg<h()>::BN;
+      const int ntn = (p.f + bn - 1) / bn;
+      hipLaunchKernelGGL(gate_grad_bf16<h()>, st_row_grid(p.rows_max, p.n, h(), ntn), dim3(ST_NT), 0, st,
+                         (const bf16_t*)dy, offsets, p.n, (const bf16_t*)w2, (const bf16_t*)g, (const bf16_t*)u,
+                         (bf16_t*)dgp, (bf16_t*)dup, p.d, p.f, ntn);
+      return hipGetLastError();
+    });
     if (e != hipSuccess) return e;
   }
   if (dx) {
-    e = launch([](auto h, auto kt) { return input_grad_bf16<h(), kt()>; }, p.f, p.d, DG, DU, offsets, p.n,
-               (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f);
+    e = st_with_height(st_height(p.n, mean, (int64_t)p.f * 4, p.d, 128), [&](auto h) {
+      constexpr int bn = InputCfg<h()>::BN;
+      const int ntn = (p.d + bn - 1) / bn;
+      hipLaunchKernelGGL(input_grad_bf16<h()>, st_row_grid(p.rows_max, p.n, h(), ntn), dim3(ST_NT), 0, st, DG, DU,
+                         offsets, p.n, (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn);
+      return hipGetLastError();
+    });
     if (e != hipSuccess) return e;
   }
   WeightGrads w{};

@@ -792,9 +792,9 @@ hipError_t launch_expert_gemm(const Prob& p, const void* x_packed, const int32_t
                              rscale, nullptr, nullptr);
 }
 
-hipError_t launch_expert_gemm_train(const Prob& p, const void* x_packed, const int32_t* offsets,
-                                    const void* w1, const void* w3, const void* w2, void* g, void* u,
-                                    void* h, void* y_packed, void* ws, hipStream_t st) {
+hipError_t launch_expert_gemm_keep(const Prob& p, const void* x_packed, const int32_t* offsets,
+                                   const void* w1, const void* w3, const void* w2, void* g, void* u,
+                                   void* h, void* y_packed, void* ws, hipStream_t st) {
   return launch_gemms<true>(p, x_packed, offsets, w1, w3, w2, h, y_packed, ws, 0, p.n, st, nullptr, nullptr,
                             g, u);
 }

@@ -241,7 +241,7 @@ __device__ __forceinline__ void i8_values(const i32x4& p1, const i32x4& p3, floa
 // Tiles of 64 MT rows x 256 weight columns, or 64 x 128 (GATED: half as many
 // output columns, of both matrices), for segments of more than `lo` rows.
 template <int MT, bool GATED, bool F32OUT>
-using I8Cfg = StCfg<MT, ST_ROWS, ST_PACK, i32x4, 1, GATED, false,
+using I8Cfg = StCfg<MT, ST_ROWS, ST_PACK, i32x4, 1, GATED,
                     MT * (MT == 1 ? 1 : 2) * (F32OUT ? 4 : 2) / (GATED ? 2 : 1)>;
 
 template <int MT, bool GATED, bool F32OUT>
@@ -264,7 +264,6 @@ __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
         st_pack<GATED>(c.b[0], p.b1 + eo, GATED ? p.b3 + eo : nullptr, (GATED ? Cfg::BN / 32 : Cfg::BN / 16) * t.nt,
                        p.ntiles, run);
         c.nst = c.nst1 = (p.kt + 1) / 2;   // an odd last block meets zeros past its run
-        c.kvals = 0;
         return t;
       },
       [&](const StTile& t, typename Cfg::Acc& acc) {
@@ -407,6 +406,10 @@ __global__ __launch_bounds__(64 * KS) void i8_stream(I8Args p) {
 constexpr int I8_THIN = 32;        // rows up to which a segment streams
 constexpr int I8_THIN_MEAN = 64;   // expected rows from which every segment takes a tile
 
+// Output columns of a tile of height h.
+template <bool GATED>
+constexpr int I8Cols(int h) { return (h == 1 ? 128 : 256) / (GATED ? 2 : 1); }
+
 // mean: expected rows of a segment; most: bound of one segment's rows.
 template <bool GATED, bool F32OUT>
 static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t rows_max, hipStream_t st) {
@@ -433,24 +436,15 @@ static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t r
     if (e != hipSuccess || most <= I8_THIN) return e;
   }
   p.lo = stream ? I8_THIN : 0;
-  // tile height from the expected segment, and small tiles, as in the backward pass
-  const int64_t small =
-      (int64_t)p.n * std::max<int64_t>(1, (mean + 63) / 64) * ((p.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
-  const int mt = small <= 2 * device_cus() ? 1 : mean >= 256 ? 4 : mean > 96 ? 3 : 2;
-  const int cols = (mt == 1 ? 128 : 256) / (GATED ? 2 : 1);
-  const int ntn = (p.N + cols - 1) / cols;
-  auto go = [&](auto kernel) {
-    const int bm = 64 * mt;
-    const int64_t blocks = std::min<int64_t>(rows_max / bm + std::min<int64_t>(p.n, rows_max), rows_max);
-    hipLaunchKernelGGL(kernel, dim3(st_grid(blocks * ntn)), dim3(ST_NT), 0, st, p, ntn);
+  auto blocks = [&](int h) { return (p.N + I8Cols<GATED>(h) - 1) / I8Cols<GATED>(h); };
+  const int wide = blocks(2);
+  const int h = st_height(p.n, mean, (p.kt + 1) / 2, {0, blocks(1), wide, wide, wide}, {0, 128, 256, 256, 256});
+  return st_with_height(h, [&](auto height) {
+    constexpr int H = height();
+    const int ntn = blocks(H);
+    hipLaunchKernelGGL((i8_tile<H, GATED, F32OUT>), st_row_grid(rows_max, p.n, H, ntn), dim3(ST_NT), 0, st, p, ntn);
     return hipGetLastError();
-  };
-  switch (mt) {
-    case 1: return go(i8_tile<1, GATED, F32OUT>);
-    case 2: return go(i8_tile<2, GATED, F32OUT>);
-    case 3: return go(i8_tile<3, GATED, F32OUT>);
-    default: return go(i8_tile<4, GATED, F32OUT>);
-  }
+  });
 }
 
 hipError_t launch_quantize_rows(const void* x, int dtype, int64_t rows, int K, int64_t ldq, void* q, float* s,

@@ -58,7 +58,12 @@ hipError_t launch_expert_gemm(const Prob& p, const void* x_packed, const int32_t
                               const void* w1, const void* w3, const void* w2, void* h,
                               void* y_packed, void* ws, int e_begin, int e_end, hipStream_t st,
                               const int32_t* perm = nullptr, const float* rscale = nullptr);
-// The same, keeping g = rnd(x W1) and u = rnd(x W3) for the backward pass.
+// The same over all local experts, keeping g = rnd(x W1) and u = rnd(x W3).
+hipError_t launch_expert_gemm_keep(const Prob& p, const void* x_packed, const int32_t* offsets,
+                                   const void* w1, const void* w3, const void* w2, void* g, void* u,
+                                   void* h, void* y_packed, void* ws, hipStream_t st);
+
+// expert_train.hip: the training forward pass.
 hipError_t launch_expert_gemm_train(const Prob& p, const void* x_packed, const int32_t* offsets,
                                     const void* w1, const void* w3, const void* w2, void* g, void* u,
                                     void* h, void* y_packed, void* ws, hipStream_t st);

@@ -45,10 +45,14 @@
 // multiplied.
 #pragma once
 
+#include <algorithm>
+#include <type_traits>
+
 #include "common.h"
 #include "gemm_core.h"
 #include "dma_tile.h"
 #include "dma_big.h"
+#include "kernels.h"
 
 namespace moe {
 
@@ -68,11 +72,14 @@ struct StOp {
   uint32_t v[L == ST_PANEL ? 2 : 1];             // lane source offsets at stage 0
   uint32_t ld;                                   // bytes between rows (ST_ROWS) or K-rows (ST_PANEL)
   uint32_t size;                                 // descriptor bytes (ST_ROWS, ST_PACK)
+  uint32_t kbytes;                               // ST_ROWS: bytes of a row
   int krows;                                     // ST_PANEL: valid K-rows
 };
 
-// ST_ROWS: `rows` valid rows (>= 1) of `ld` bytes from base, kbytes of each
-// read.  Rows past the last valid one lie outside the descriptor and read zeros.
+// ST_ROWS: `rows` valid rows (>= 1) of `ld` bytes from base, kbytes (a multiple
+// of 16) of each read.  Rows past the last valid one lie outside the descriptor
+// and read zeros; so do the pieces of the last stage past a row's end, whose
+// lanes are sent outside the descriptor.
 template <int W>
 __device__ __forceinline__ void st_rows(StOp<ST_ROWS, W>& o, const void* base, uint32_t ld, int rows,
                                         uint32_t kbytes) {
@@ -84,13 +91,15 @@ __device__ __forceinline__ void st_rows(StOp<ST_ROWS, W>& o, const void* base, u
   o.v[0] = (uint32_t)r * ld + 16u * (uint32_t)((lane & 7) ^ ((r >> 1) & 7));
   o.ld = ld;
   o.size = (uint32_t)(min(rows, W) - 1) * ld + kbytes;
+  o.kbytes = kbytes;
 }
 
 // ST_PANEL: K-rows [0, krows) of ld2 bytes from base, columns col0 .. col0 + W
-// - 1 of which those below ncols are read; K-rows past krows read zeros.
+// - 1 of which those below ncols are read; K-rows past krows read zeros.  With
+// base2 the two half-panels are columns col0 .. col0 + 127 of two matrices.
 template <int W>
 __device__ __forceinline__ void st_panel(StOp<ST_PANEL, W>& o, const void* base, uint32_t ld2,
-                                         int krows, int col0, int ncols) {
+                                         int krows, int col0, int ncols, const void* base2 = nullptr) {
   static_assert(W == 256, "two half-panels");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -99,11 +108,11 @@ __device__ __forceinline__ void st_panel(StOp<ST_PANEL, W>& o, const void* base,
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int sig = ((lane >> 4) & 3) | (h << 2);
-    const int col = col0 + 128 * (wave >> 2) + 8 * ((lane & 15) ^ (2 * sig));
+    const int col = col0 + (base2 ? 0 : 128 * (wave >> 2)) + 8 * ((lane & 15) ^ (2 * sig));
     const int j = 16 * (wave & 3) + 8 * h + (lane >> 4);
     o.v[h] = col < ncols ? (uint32_t)j * ld2 + 2u * (uint32_t)col : GC_OOR;
   }
-  o.base[0] = (const char*)base;
+  o.base[0] = (const char*)(base2 && (wave >> 2) ? base2 : base);
   o.ld = ld2;
   o.krows = krows;
   o.size = 0;
@@ -140,9 +149,12 @@ __device__ __forceinline__ void st_issue(const StOp<L, W>& o, uint32_t lds, int 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if constexpr (L == ST_ROWS) {
     const __amdgpu_buffer_rsrc_t r = gc_rsrc(o.base[0], o.size);
+    const int lane = threadIdx.x & 63;
+    const uint32_t piece = 16u * (uint32_t)((lane & 7) ^ (((8 * wave + (lane >> 3)) >> 1) & 7));
+    const uint32_t v = (uint32_t)st * ST_KB + piece < o.kbytes ? o.v[0] : GC_OOR;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      bd_copy16(r, lds + 1024 * (wave + 8 * c), o.v[0], (uint32_t)st * ST_KB + (uint32_t)(64 * c) * o.ld);
+      bd_copy16(r, lds + 1024 * (wave + 8 * c), v, (uint32_t)st * ST_KB + (uint32_t)(64 * c) * o.ld);
   } else if constexpr (L == ST_PANEL) {
     // a descriptor per stage: a segment may span more than 32 bits
     // (the saturated row count is formed on the vector unit; the descriptor is scalar)
@@ -178,7 +190,7 @@ __device__ __forceinline__ int st_lane(int t0) {
 template <int L>
 __device__ __forceinline__ u32x4 st_frag(const char* slot, int lane_off, int ks, int t) {
   if constexpr (L == ST_PANEL) {
-    const char* p = slot + (lane_off ^ (32 * t)) + 8192 * ks;
+    const char* p = slot + (lane_off ^ (32 * (t & 7))) + 16384 * (t >> 3) + 8192 * ks;
     const s16x4 lo = dt_tr16(p), hi = dt_tr16(p + 4 * BD_HPROW);
     return __builtin_bit_cast(u32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   } else if constexpr (L == ST_ROWS) {
@@ -196,27 +208,28 @@ __device__ __forceinline__ i32x4 st_mfma(const u32x4& a, const u32x4& b, const i
                                                0, 0, 0);
 }
 
-// Tile configuration.  MT = 1: the 64 x 128 tile.  NP phases of operands follow
+// Tile configuration.  MT = 1: the small tile, 64 x 128 (64 x 256 for a gated pair
+// of ST_PANEL matrices).  NP phases of operands follow
 // one another along K (the input gradient sums two products); all have the same
 // shape.  SPLIT: half of the columns are of one packed matrix, the others the
 // same columns of a second (gate and up products of one h column meet in one
-// lane: acc[mt][t] and acc[mt][t + NT / 2]).  KT: K is not a multiple of a stage;
-// the fragments past its end are zeroed (ST_ROWS reads there what follows the
-// row).  STORES: store instructions of a wave's epilogue, every one of them
+// lane: acc[mt][t] and acc[mt][t + NT / 2]).  STORES: store instructions of a wave's epilogue, every one of them
 // unconditional.  SHORT: two slots for each operand, for st_run_short.
-template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, bool KT_, int STORES_, bool SHORT_ = false>
+template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, int STORES_, bool SHORT_ = false,
+          int BN_ = MT_ == 1 ? 128 : 256>
 struct StCfg {
   static constexpr int MT = MT_, LA = LA_, LB = LB_, NP = NP_, STORES = STORES_;
-  static constexpr bool SPLIT = SPLIT_, KT = KT_;
-  static constexpr int BM = 64 * MT, BN = MT == 1 ? 128 : 256;
+  static constexpr bool SPLIT = SPLIT_;
+  static constexpr int BM = 64 * MT, BN = BN_;
   static constexpr int NT = BN / 32, WN = BN / 2;              // a wave's column tiles and columns
   typedef AccT_ Acc[MT][NT];
   typedef StOp<LA, BM> A;
   typedef StOp<LB, BN> B;
   // slots: the columns (weights, from HBM) three deep where LDS allows; small
-  // tiles, of which a compute unit may have one alone, six deep, since nothing
-  // else hides the latency of their loads
-  static constexpr int NA = MT == 1 ? 6 : BM == 128 && !SHORT_ ? 3 : 2, NB = MT == 1 ? 6 : SHORT_ ? 2 : 3;
+  // tiles, of which a compute unit may have one alone, as deep as LDS holds,
+  // since nothing else hides the latency of their loads
+  static constexpr int DEEP = BN == 128 ? 6 : 4;
+  static constexpr int NA = MT == 1 ? DEEP : BM == 128 && !SHORT_ ? 3 : 2, NB = MT == 1 ? DEEP : SHORT_ ? 2 : 3;
   static constexpr int AREG = NA * A::BYTES;                   // the column slots follow the row slots
   static constexpr int LDS = AREG + NB * B::BYTES;             // 128 to 160 KB (all there is)
   static constexpr int CA = A::C, CB = B::C;                   // copies per wave per stage
@@ -231,7 +244,6 @@ struct StCtx {
   typename Cfg::B b[Cfg::NP];
   int nst1;          // stages of a phase
   int nst;           // stages in all
-  int kvals;         // K of a phase in bf16 elements (KT only)
 };
 
 template <class Cfg>
@@ -249,15 +261,6 @@ template <class Cfg>
 __device__ __forceinline__ void st_issue_b(const StCtx<Cfg>& c, uint32_t at, int st) {
   if (Cfg::NP > 1 && st >= c.nst1) st_issue(c.b[Cfg::NP - 1], at, st - c.nst1);
   else st_issue(c.b[0], at, st);
-}
-
-// Whether this lane's k (8 bf16 from 8 g) of k-step ks lie past the end of
-// stage st's phase.
-template <class Cfg>
-__device__ __forceinline__ bool st_past(const StCtx<Cfg>& c, int st, int ks) {
-  if constexpr (!Cfg::KT) return false;
-  const int s = Cfg::NP > 1 && st >= c.nst1 ? st - c.nst1 : st;
-  return 64 * s + 32 * ks + 8 * (int)((threadIdx.x & 63) >> 4) >= c.kvals;
 }
 
 // Wait until at most N of this wave's copies and stores are outstanding and its
@@ -297,18 +300,13 @@ __device__ __forceinline__ constexpr int st_slot_tile(int t) {
 // pass 19.6 -> 18.7 ms, 4096 x 14336 x 4096 int8 product 241 -> 222 us; the
 // order of reads and products inside a k-step is left to the compiler).
 template <bool READ, class Cfg>
-__device__ __forceinline__ void st_kstep(const StCtx<Cfg>& c, const StLane<Cfg>& l, const char* as, const char* bs,
-                                         int st, int ks, const StFrag<Cfg>& F, StFrag<Cfg>& G,
-                                         typename Cfg::Acc& acc) {
+__device__ __forceinline__ void st_kstep(const StLane<Cfg>& l, const char* as, const char* bs, int ks,
+                                         const StFrag<Cfg>& F, StFrag<Cfg>& G, typename Cfg::Acc& acc) {
   constexpr int MT = Cfg::MT;
-  const bool zero = READ && st_past(c, st, ks);
   __builtin_amdgcn_sched_barrier(0);
   if (READ) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      G.x[mt] = st_frag<Cfg::LA>(as, l.ao, ks, mt);
-      if (Cfg::KT && zero) G.x[mt] = u32x4{0u, 0u, 0u, 0u};
-    }
+    for (int mt = 0; mt < MT; ++mt) G.x[mt] = st_frag<Cfg::LA>(as, l.ao, ks, mt);
   }
 #pragma unroll
   for (int t = 0; t < Cfg::NT; ++t) {
@@ -317,7 +315,6 @@ __device__ __forceinline__ void st_kstep(const StCtx<Cfg>& c, const StLane<Cfg>&
     if (t == 0) __builtin_amdgcn_s_setprio(1);
     if (READ) {
       G.w[t] = st_frag<Cfg::LB>(bs, l.bo, ks, st_slot_tile<Cfg>(t));
-      if (Cfg::KT && zero) G.w[t] = u32x4{0u, 0u, 0u, 0u};
     }
   }
   __builtin_amdgcn_s_setprio(0);
@@ -384,24 +381,15 @@ __device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, const StLane<Cfg>&
   if (stores) st_wait_first<Cfg::STORES, Cfg>(0, c.nst);
   else st_wait_first<0, Cfg>(0, c.nst);
   StFrag<Cfg> F, G;
-  {
-    const bool zero = st_past(c, 0, 0);
 #pragma unroll
-    for (int mt = 0; mt < Cfg::MT; ++mt) {
-      F.x[mt] = st_frag<Cfg::LA>(ring, l.ao, 0, mt);
-      if (Cfg::KT && zero) F.x[mt] = u32x4{0u, 0u, 0u, 0u};
-    }
+  for (int mt = 0; mt < Cfg::MT; ++mt) F.x[mt] = st_frag<Cfg::LA>(ring, l.ao, 0, mt);
 #pragma unroll
-    for (int t = 0; t < Cfg::NT; ++t) {
-      F.w[t] = st_frag<Cfg::LB>(ring + Cfg::AREG, l.bo, 0, st_slot_tile<Cfg>(t));
-      if (Cfg::KT && zero) F.w[t] = u32x4{0u, 0u, 0u, 0u};
-    }
-  }
+  for (int t = 0; t < Cfg::NT; ++t) F.w[t] = st_frag<Cfg::LB>(ring + Cfg::AREG, l.bo, 0, st_slot_tile<Cfg>(t));
   // slot offsets of stage s; stage s + NA (NB) takes the slot of stage s
   uint32_t as = 0, bs = Cfg::AREG;
   int s = 0;
   for (; s + 1 < c.nst; ++s) {
-    st_kstep<true>(c, l, ring + as, ring + bs, s, 1, F, G, acc);
+    st_kstep<true>(l, ring + as, ring + bs, 1, F, G, acc);
     if (s == 0) {
       if (stores) st_wait_first<Cfg::STORES, Cfg>(1, c.nst);
       else st_wait_first<0, Cfg>(1, c.nst);
@@ -418,13 +406,13 @@ __device__ __forceinline__ void st_accum(const StCtx<Cfg>& c, const StLane<Cfg>&
     if (Cfg::MT == 1 && s + Cfg::NB < c.nst) st_issue_b(c, l.lbase + free_b, s + Cfg::NB);
     as = as == (Cfg::NA - 1) * Cfg::A::BYTES ? 0 : as + Cfg::A::BYTES;
     bs = bs == Cfg::AREG + (Cfg::NB - 1) * Cfg::B::BYTES ? Cfg::AREG : bs + Cfg::B::BYTES;
-    st_kstep<true>(c, l, ring + as, ring + bs, s + 1, 0, G, F, acc);
+    st_kstep<true>(l, ring + as, ring + bs, 0, G, F, acc);
     // half a stage after the rows' copies, which spreads the requests
     if (Cfg::MT != 1 && s + Cfg::NB < c.nst) st_issue_b(c, l.lbase + free_b, s + Cfg::NB);
   }
-  st_kstep<true>(c, l, ring + as, ring + bs, s, 1, F, G, acc);
+  st_kstep<true>(l, ring + as, ring + bs, 1, F, G, acc);
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  st_kstep<false>(c, l, ring, ring, s, 0, G, F, acc);
+  st_kstep<false>(l, ring, ring, 0, G, F, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -473,6 +461,21 @@ __device__ __forceinline__ StOut st_out(void* base, int64_t ld, int rows) {
 template <bool NT = false>
 __device__ __forceinline__ void st_put(const StOut& o, int row, uint32_t byte, bool ok, const u32x4& v) {
   __builtin_amdgcn_raw_buffer_store_b128(v, o.r, ok ? (uint32_t)row * o.ld + byte : 0xFFFFFFF0u, 0, NT ? 2 : 0);
+}
+
+// bf16 rows of a finished tile: its columns from col0, those below N.
+template <int MT, int NT>
+__device__ __forceinline__ void st_store_tile(const StOut& o, const f32x4 (&acc)[MT][NT], int col0, int N) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int k = 0; k < NT / 2; ++k) {
+      const int col = col0 + 16 * NT * (wave >> 2) + 32 * k + 8 * q;
+      st_put(o, 16 * MT * (wave & 3) + 16 * mt + i, 2u * (uint32_t)col, col < N,
+             st_pack8(acc[mt][2 * k], acc[mt][2 * k + 1]));
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -662,22 +665,21 @@ __device__ __forceinline__ void st_run_short(int total, char* ring, const UnitOf
         for (int t = 0; t < Cfg::NT; ++t) F.w[t] = st_frag<Cfg::LB>(bs, l.bo, 0, t);
         int s = 0;
         for (; s + 1 < u.nst; ++s) {
-          st_kstep<true>(p, l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, s, 1, F, F1, acc);
+          st_kstep<true>(l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, 1, F, F1, acc);
           // the next stage was copied before the stores only if this is the first
           if (s == 0 && stores) st_sync<S>();
           else st_sync<0>();
           --ahead;
           copy_next(slot);
           slot ^= 1;
-          st_kstep<true>(p, l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, s + 1, 0, F1, F,
-                         acc);
+          st_kstep<true>(l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, 0, F1, F, acc);
         }
-        st_kstep<true>(p, l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, s, 1, F, F1, acc);
+        st_kstep<true>(l, ring + slot * Cfg::A::BYTES, ring + Cfg::AREG + slot * Cfg::B::BYTES, 1, F, F1, acc);
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         --ahead;
         copy_next(slot);
         slot ^= 1;
-        st_kstep<false>(p, l, ring, ring, s, 0, F1, F, acc);
+        st_kstep<false>(l, ring, ring, 0, F1, F, acc);
       }
       __builtin_amdgcn_sched_barrier(0);
       finish(u, j, acc);
@@ -686,6 +688,58 @@ __device__ __forceinline__ void st_run_short(int total, char* ring, const UnitOf
       stores = true;
     }
   }
+}
+
+// ---------------------------------------------------------------------------
+// host side: tile heights
+// ---------------------------------------------------------------------------
+// Height (in units of 64 rows) of the tiles for segments of about `mean` rows of
+// n experts: the one whose rounds of workgroups take the least time.  A stage of
+// a tile costs the copies of its rows and columns, at the 38 GB/s that a compute
+// unit sustains from L2, but at least about half a microsecond; a tile costs
+// about 4 us more (first loads, epilogue).  Segments are taken a quarter longer
+// than the mean unless there is one alone: a segment that does not fit its tile
+// reads all its columns again.  ntn[h]: column blocks for height h, each of
+// bn[h] operand columns; 0: no such tile.
+inline int st_height(int64_t n, int64_t mean, int stages, const int (&ntn)[5], const int (&bn)[5]) {
+  const int64_t seg = std::max<int64_t>(1, n > 1 ? mean + mean / 4 : mean);
+  const int64_t cus = device_cus();
+  int best = 0;
+  double least = 0;
+  for (int h = 4; h >= 1; --h) {
+    if (!ntn[h]) continue;
+    const int64_t tiles = n * ((seg + 64 * h - 1) / (64 * h)) * ntn[h];
+    const double stage = std::max(0.5, (64 * h + bn[h]) * 128 / 38e3);
+    const double us = (double)((tiles + cus - 1) / cus) * (stages * stage + 4.0);
+    if (!best || us < least) {
+      best = h;
+      least = us;
+    }
+  }
+  return best;
+}
+// The same for tiles of 256 columns and, at height 1, `small` columns.
+inline int st_height(int64_t n, int64_t mean, int64_t kbytes, int N, int small) {
+  const int wide = (N + 255) / 256;
+  return st_height(n, mean, (int)((kbytes + ST_KB - 1) / ST_KB), {0, (N + small - 1) / small, wide, wide, wide},
+                   {0, small, 256, 256, 256});
+}
+
+// Calls go with the height as a compile-time constant.
+template <class Go>
+inline hipError_t st_with_height(int h, const Go& go) {
+  switch (h) {
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    case 3: return go(std::integral_constant<int, 3>{});
+    default: return go(std::integral_constant<int, 4>{});
+  }
+}
+
+// Grid over the row blocks that a batch can have at most.
+inline dim3 st_row_grid(int64_t rows_max, int64_t n, int h, int ntn) {
+  const int64_t blocks = std::min<int64_t>(rows_max / (64 * h) + std::min<int64_t>(n, rows_max), rows_max);
+  return dim3(st_grid(blocks * ntn));
 }
 
 }  // namespace moe

@@ -272,8 +272,8 @@ moe_status_t moe_expert_gemm_padded(const moe_problem_t* p, int32_t capacity, co
  * two unactivated products for the backward pass.  For each local expert e and
  * its rows R:
  *   g[R] = rnd(x_packed[R] w1[e]),  u[R] = rnd(x_packed[R] w3[e])
- * and h, y_packed as moe_expert_gemm writes them (h from the unrounded
- * products).
+ * and h, y_packed by the formulas of moe_expert_gemm (h from the unrounded
+ * products; the fp32 sums may run in another order).
  *   g, u [rows_max,f]  dtype output (rows >= A untouched)
  *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_TRAIN) bytes
  * A dense gated block is the problem with E = k = n_local = 1 and offsets

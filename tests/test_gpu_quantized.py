@@ -70,7 +70,7 @@ SIZES = [(1, 8, 16), (1, 2048, 7168), (2, 24, 48), (15, 136, 64), (16, 512, 80),
          (32, 4096, 128), (33, 264, 144), (64, 72, 320), (129, 520, 592), (300, 264, 1040), (257, 1000, 128), (1, 20000, 64),
          (20, 20000, 192), (3, 8, 8192),
          # enough tiles for the 256-, 192- and 128-row kernels
-         (2000, 2200, 144), (2049, 2104, 64), (150, 22008, 80), (70, 33000, 208)]
+         (4096, 4096, 1040), (2049, 2104, 64), (180, 65528, 80), (70, 33000, 208)]
 
 
 @pytest.mark.parametrize("Mr,N,K", SIZES)
@@ -114,8 +114,8 @@ CASES = {
     "wide": ([3] * 40, 64, 1032, dict(T=20)),
     "no_rows": ([0, 0, 0], 64, 72, dict(T=5, k=2)),
     # enough tiles for the 256-, 192- and 128-row kernels
-    "tall_many": ([300 + (37 * e) % 200 - 100 for e in range(64)], 264, 200, dict(T=1200, k=16)),
-    "mid_many": ([130 + (29 * e) % 140 - 70 for e in range(64)], 328, 264, dict(T=520, k=16)),
+    "tall_many": ([400 + (37 * e) % 200 - 100 for e in range(64)], 264, 512, dict(T=1600, k=16)),
+    "mid_many": ([150 + (29 * e) % 140 - 70 for e in range(128)], 328, 200, dict(T=750, k=26)),
     "low_many": ([80 + (23 * e) % 90 - 45 if e % 7 else 0 for e in range(100)], 264, 328, dict(T=320, k=25)),
 }
 
