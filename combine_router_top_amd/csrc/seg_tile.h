@@ -214,12 +214,13 @@ __device__ __forceinline__ i32x4 st_mfma(const u32x4& a, const u32x4& b, const i
 // shape.  SPLIT: half of the columns are of one packed matrix, the others the
 // same columns of a second (gate and up products of one h column meet in one
 // lane: acc[mt][t] and acc[mt][t + NT / 2]).  STORES: store instructions of a wave's epilogue, every one of them
-// unconditional.  SHORT: two slots for each operand, for st_run_short.
+// unconditional.  SHORT: two slots for each operand, for st_run_short.  ROT: K
+// starts at stage ctx.rot and wraps around.
 template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, int STORES_, bool SHORT_ = false,
-          int BN_ = MT_ == 1 ? 128 : 256>
+          int BN_ = MT_ == 1 ? 128 : 256, bool ROT_ = false>
 struct StCfg {
   static constexpr int MT = MT_, LA = LA_, LB = LB_, NP = NP_, STORES = STORES_;
-  static constexpr bool SPLIT = SPLIT_;
+  static constexpr bool SPLIT = SPLIT_, ROT = ROT_;
   static constexpr int BM = 64 * MT, BN = BN_;
   static constexpr int NT = BN / 32, WN = BN / 2;              // a wave's column tiles and columns
   typedef AccT_ Acc[MT][NT];
@@ -244,6 +245,7 @@ struct StCtx {
   typename Cfg::B b[Cfg::NP];
   int nst1;          // stages of a phase
   int nst;           // stages in all
+  int rot;           // first stage (ROT)
 };
 
 template <class Cfg>
@@ -254,11 +256,19 @@ struct StFrag {
 // The copies of stage st into the slot at LDS address `at`.
 template <class Cfg>
 __device__ __forceinline__ void st_issue_a(const StCtx<Cfg>& c, uint32_t at, int st) {
+  if (Cfg::ROT) {
+    st += c.rot;
+    if (st >= c.nst) st -= c.nst;
+  }
   if (Cfg::NP > 1 && st >= c.nst1) st_issue(c.a[Cfg::NP - 1], at, st - c.nst1);
   else st_issue(c.a[0], at, st);
 }
 template <class Cfg>
 __device__ __forceinline__ void st_issue_b(const StCtx<Cfg>& c, uint32_t at, int st) {
+  if (Cfg::ROT) {
+    st += c.rot;
+    if (st >= c.nst) st -= c.nst;
+  }
   if (Cfg::NP > 1 && st >= c.nst1) st_issue(c.b[Cfg::NP - 1], at, st - c.nst1);
   else st_issue(c.b[0], at, st);
 }
