@@ -40,8 +40,11 @@ template <int MT>
 using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, (MT == 1 ? 4 : 8) * MT>;
 template <int MT>
 using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, (MT == 1 ? 2 : 4) * MT, false, MT == 1 ? 128 : 256, MT != 4>;
-template <bool SHORT>
-using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, 16, SHORT>;
+// How the weight gradients run: whole segments by st_run, short ones by
+// st_run_short, or long segments of few tiles split along their rows.
+enum { WG_LONG = 0, WG_SHORT = 1, WG_SPLIT = 2 };
+template <int MODE>
+using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, MODE == WG_SPLIT ? 32 : 16, MODE == WG_SHORT>;
 
 // dh tiles: rows of dy against rows of W2 (its f rows are the output columns).
 template <int MT>
@@ -188,11 +191,13 @@ struct WeightGrads {
 };
 
 // All tiles of all wanted weight gradients, expert by expert; a segment without
-// rows gives zeros.  SHORT: st_run_short over units of at most glen row blocks.
-template <bool SHORT>
-__global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int nm, int glen,
+// rows gives zeros.  WG_SHORT: units of at most `div` row blocks.  WG_SPLIT: each
+// tile's rows go to `div` workgroups, whose fp32 sums m[].C holds as [div][n][M][N].
+template <int MODE>
+__global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int nm, int div,
                                                              const int32_t* __restrict__ offsets, int n) {
-  using Cfg = WeightCfg<SHORT>;
+  using Cfg = WeightCfg<MODE>;
+  constexpr bool SHORT = MODE == WG_SHORT;
   __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS + (SHORT ? 8 * 4096 : 0)];
   // the table as values: a choice between its addresses would put it in scratch,
   // and what is read from there into vector registers
@@ -203,22 +208,24 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
   const WeightGrad m0 = held(w.m[0]), m1 = held(w.m[1]), m2 = held(w.m[2]);
   // column blocks, runs of row blocks and their length, and the tiles (SHORT:
   // units) of each matrix
-  auto runs_of = [&](int M) { return SHORT ? st_div((M + 255) / 256 + glen - 1, glen) : (M + 255) / 256; };
+  auto runs_of = [&](int M) { return max(1, SHORT ? st_div((M + 255) / 256 + div - 1, div) : (M + 255) / 256); };
   auto len_of = [&](int M, int runs) { return st_div((M + 255) / 256 + runs - 1, runs); };
   const int r0 = runs_of(m0.M), r1 = runs_of(m1.M), r2 = runs_of(m2.M);
   const int l0 = len_of(m0.M, r0), l1 = len_of(m1.M, r1), l2 = len_of(m2.M, r2);
   const int n0 = (m0.N + 255) / 256, n1 = (m1.N + 255) / 256, n2 = (m2.N + 255) / 256;
   const int c0 = n0 * r0, c1 = nm > 1 ? n1 * r1 : 0, c2 = nm > 2 ? n2 * r2 : 0;
-  const int per = c0 + c1 + c2;
+  const int all = c0 + c1 + c2, per = MODE == WG_SPLIT ? div * all : all;
   struct Unit {
     WeightGrad m;
     int e, tm, tn, tiles;   // row blocks tm .. tm + tiles - 1
-    int o, cnt, nst;
+    int o, cnt, nst, part;   // part (WG_SPLIT): which share of the rows
   };
   auto unit = [&](int L) __attribute__((always_inline)) {
     Unit r;
     r.e = st_div(L, per);
     int at = L - r.e * per;
+    r.part = MODE == WG_SPLIT ? st_div(at, all) : 0;
+    at -= r.part * all;
     const bool b1 = at >= c0, b2 = at >= c0 + c1;
     auto pick = [&](auto v0, auto v1, auto v2) { return b2 ? v2 : b1 ? v1 : v0; };
     at -= pick(0, c0, c0 + c1);
@@ -247,6 +254,12 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
     r.cnt = __builtin_amdgcn_readfirstlane(offsets[r.e + 1]) - r.o;
     r.nst = (r.cnt + 63) / 64;
     if (SHORT && r.nst == 1) r.nst = 2;
+    if (MODE == WG_SPLIT) {   // an equal share of the stages; the last ones may be empty
+      const int share = st_div(r.nst + div - 1, div), first = 64 * share * r.part;
+      r.o += first;
+      r.cnt = max(0, min(r.cnt - first, 64 * share));
+      r.nst = (r.cnt + 63) / 64;
+    }
     return r;
   };
   auto cols = [&](const Unit& r, StCtx<Cfg>& c) __attribute__((always_inline)) {
@@ -273,7 +286,44 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
           rows(r, 0, c);
           return r;
         },
-        [&](const Unit& r, f32x4 (&acc)[4][8]) { st_store_tile(out(r, 0), acc, 256 * r.tn, r.m.N); });
+        [&](const Unit& r, f32x4 (&acc)[4][8]) {
+          if constexpr (MODE == WG_SPLIT) {
+            const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            const int row0 = 256 * r.tm;
+            float* C = reinterpret_cast<float*>(r.m.C) + (((int64_t)r.part * n + r.e) * r.m.M + row0) * r.m.N;
+            const StOut o = st_out(C, (int64_t)r.m.N * 4, min(256, r.m.M - row0));
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+              for (int t = 0; t < 8; ++t) {
+                const int col = 256 * r.tn + 128 * (wave >> 2) + 16 * t + 4 * (lane >> 4);
+                st_put(o, 64 * (wave & 3) + 16 * mt + (lane & 15), 4u * (uint32_t)col, col < r.m.N,
+                       __builtin_bit_cast(u32x4, acc[mt][t]));
+              }
+          } else {
+            st_store_tile(out(r, 0), acc, 256 * r.tn, r.m.N);
+          }
+        });
+  }
+}
+
+// C = rnd(sum of the `div` parts), in their order; blockIdx.y is the matrix.
+struct WeightSums {
+  const float* part[3];
+  bf16_t* C[3];
+};
+__global__ __launch_bounds__(256) void weight_grad_sum(WeightSums w, int div, int64_t count) {
+  const float* p = w.part[blockIdx.y];
+  const int64_t n8 = count / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+    f32x4 a = reinterpret_cast<const f32x4*>(p)[2 * i], b = reinterpret_cast<const f32x4*>(p)[2 * i + 1];
+    for (int s = 1; s < div; ++s) {
+      const f32x4* q = reinterpret_cast<const f32x4*>(p + s * count) + 2 * i;
+      a += q[0];
+      b += q[1];
+    }
+    reinterpret_cast<u32x4*>(w.C[blockIdx.y])[i] =
+        u32x4{cvt_bf16x2(a[0], a[1]), cvt_bf16x2(a[2], a[3]), cvt_bf16x2(b[0], b[1]), cvt_bf16x2(b[2], b[3])};
   }
 }
 
@@ -457,11 +507,36 @@ __global__ __launch_bounds__(256) void fill_zero(u32x4* __restrict__ p, int64_t 
     p[i] = u32x4{0u, 0u, 0u, 0u};
 }
 
-constexpr int WG_SHORT = 512;   // expected rows up to which the weight gradients take st_run_short
+constexpr int WG_SHORT_ROWS = 512;   // expected rows up to which the weight gradients take st_run_short
+
+// Parts that the rows of the weight gradients are split into: as many as make
+// the least time by the rule of st_height, the fp32 parts written and read at
+// about 4 TB/s, at most 256 MB of them.  1: not split.
+static int weight_parts(const Prob& p) {
+  if (p.dtype != 1 || p.T == 0) return 1;
+  const int64_t mean = p.tk() / p.E, stages = (mean + 63) / 64, cus = device_cus();
+  const int64_t tiles = 3 * (int64_t)p.n * ((p.d + 255) / 256) * ((p.f + 255) / 256);
+  const double elems = 3.0 * p.n * p.d * p.f;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 32 && (s == 1 || (s * elems * 4 <= 256e6 && stages >= 4 * s)); ++s) {
+    const double us = (double)((tiles * s + cus - 1) / cus) * ((stages + s - 1) / s * 1.72 + 4) +
+                      (s > 1 ? 4 + elems * (8.0 * s + 2) / 4e6 : 0);
+    if (s == 1 || us < least) {
+      best = s;
+      least = us;
+    }
+  }
+  return best;
+}
+
+static size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
 
 size_t expert_backward_ws_bytes(const Prob& p) {
-  // dg and du, [rows_max, f] each
-  return 2 * (((size_t)p.rows_max * p.f * p.elem() + 255) / 256 * 256);
+  // dg and du, [rows_max, f] each, and the parts of split weight gradients
+  const int parts = weight_parts(p);
+  return 2 * pad256((size_t)p.rows_max * p.f * p.elem()) +
+         (parts > 1 ? 3 * pad256((size_t)parts * p.n * p.d * p.f * 4) : 0);
 }
 
 hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* offsets, const void* w1,
@@ -480,7 +555,7 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
     return hipSuccess;
   }
   char* dgp = (char*)ws;
-  char* dup = dgp + expert_backward_ws_bytes(p) / 2;
+  char* dup = dgp + pad256((size_t)p.rows_max * p.f * p.elem());
   const bool gate = dx || dw1 || dw3;
   if (p.dtype != 1) {
     const unsigned rb = (unsigned)std::min<int64_t>((p.rows_max + F_T - 1) / F_T + p.n, p.rows_max);
@@ -552,18 +627,33 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
   want(h, dy, dw2, p.f, p.d);
   want(x, DG, dw1, p.d, p.f);
   want(x, DU, dw3, p.d, p.f);
-  if (nm) {
+  if (!nm) return hipSuccess;
+  const int parts = weight_parts(p);
+  if (parts > 1) {
+    WeightSums sums{};
+    char* at = dup + pad256((size_t)p.rows_max * p.f * p.elem());
+    const int64_t count = (int64_t)p.n * p.d * p.f;
+    for (int k = 0; k < nm; ++k, at += pad256((size_t)parts * count * 4)) {
+      sums.part[k] = (const float*)at;
+      sums.C[k] = w.m[k].C;
+      w.m[k].C = (bf16_t*)at;
+    }
+    hipLaunchKernelGGL(weight_grad_bf16<WG_SPLIT>, dim3(st_grid(tiles * parts)), dim3(ST_NT), 0, st, w, nm, parts,
+                       offsets, p.n);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t blocks = (count / 8 + 255) / 256;
+    hipLaunchKernelGGL(weight_grad_sum, dim3((unsigned)std::min<int64_t>(blocks, 2048), nm), dim3(256), 0, st, sums,
+                       parts, count);
+  } else if (mean <= WG_SHORT_ROWS) {
     // runs of row blocks that share their columns: up to 4 (8, 2 and 1 measured
     // 864, 813 and 839 us against 808 on 32 experts of about 128 rows), fewer where that
     // would leave less than four units for each compute unit
-    const int glen = (int)std::min<int64_t>(4, std::max<int64_t>(1, tiles / (4 * (int64_t)device_cus())));
-    if (mean <= WG_SHORT)
-      hipLaunchKernelGGL(weight_grad_bf16<true>, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, glen, offsets, p.n);
-    else
-      hipLaunchKernelGGL(weight_grad_bf16<false>, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, 1, offsets, p.n);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int run = (int)std::min<int64_t>(4, std::max<int64_t>(1, tiles / (4 * (int64_t)device_cus())));
+    hipLaunchKernelGGL(weight_grad_bf16<WG_SHORT>, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, run, offsets, p.n);
+  } else {
+    hipLaunchKernelGGL(weight_grad_bf16<WG_LONG>, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, 1, offsets, p.n);
   }
-  return hipSuccess;
+  return hipGetLastError();
 }
 
 }  // namespace moe

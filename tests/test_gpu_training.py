@@ -151,7 +151,7 @@ def test_backward(name):
     _check_backward(p, r, v, g, u, h, dy, got)
 
 
-@pytest.mark.parametrize("name", ["ragged", "f32_ragged"])
+@pytest.mark.parametrize("name", ["ragged", "one_long", "f32_ragged"])
 @pytest.mark.parametrize("wanted", [(1, 0, 0, 0), (0, 1, 0, 0), (0, 0, 1, 0), (0, 0, 0, 1), (1, 0, 1, 1)])
 def test_backward_some_outputs(name, wanted):
     p, r, v = _case(name)
