@@ -305,20 +305,15 @@ __global__ __launch_bounds__(ST_NT, 1) void i8_tile(I8Args p, int ntn) {
       });
 }
 
-// Segments of at most 16 MT rows: a stream of the packed weights.  Workgroup
-// (task, e) owns NT 16-column tiles (GATED: NT / 2 of each matrix); its KS
-// waves split K evenly, each loads its blocks straight into MFMA operands, U
-// stages ahead of their use, and the int32 sums meet in LDS.  Rows of A come
-// through the caches.  Past its part of K a wave's weight descriptors read
-// zeros, so that the loop needs no tail.
+// Short segments: a stream of the packed weights.  Workgroup (task, e) owns NT
+// 16-column tiles (GATED: NT / 2 of each matrix); its KS waves split K evenly,
+// each loads its blocks straight into MFMA operands, U stages ahead of their
+// use, and the int32 sums meet in LDS.  Rows of A come through the caches.  Past
+// its part of K a wave's weight descriptors read zeros, so that the loop needs
+// no tail.  One call multiplies up to 16 MT rows, o .. o + R - 1.
 template <int MT, int NT, bool GATED, bool F32OUT, int KS, int U>
-__global__ __launch_bounds__(64 * KS) void i8_stream(I8Args p) {
+__device__ __forceinline__ void i8_stream_block(const I8Args& p, int e, int o, int R, i32x4* red, int stride) {
   constexpr int NH = GATED ? NT / 2 : NT;   // output column tiles
-  __shared__ __attribute__((aligned(16))) i32x4 red[KS][MT * NT][64];
-  const int e = blockIdx.y;
-  int o;
-  const int R = i8_rows(p, e, o);
-  if (R == 0) return;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tile0 = (int)blockIdx.x * NH;
@@ -378,17 +373,18 @@ __global__ __launch_bounds__(64 * KS) void i8_stream(I8Args p) {
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) red[wave][mt * NT + t][lane] = acc[mt][t];
+    for (int t = 0; t < NT; ++t) red[wave * stride + (mt * NT + t) * 64 + lane] = acc[mt][t];
   __syncthreads();
   const float* s1 = p.s1 + (int64_t)e * p.N;
   const float* s3 = GATED ? p.s3 + (int64_t)e * p.N : nullptr;
   for (int j = wave; j < MT * NH; j += KS) {
     const int mt = j / NH, t = j - mt * NH;
-    i32x4 p1 = red[0][mt * NT + t][lane], p3 = red[0][mt * NT + (GATED ? t + NH : t)][lane];
+    const i32x4* at = red + (mt * NT + t) * 64 + lane;
+    i32x4 p1 = at[0], p3 = at[GATED ? NH * 64 : 0];
 #pragma unroll
     for (int v = 1; v < KS; ++v) {
-      p1 += red[v][mt * NT + t][lane];
-      if (GATED) p3 += red[v][mt * NT + t + NH][lane];
+      p1 += at[v * stride];
+      if (GATED) p3 += at[v * stride + NH * 64];
     }
     const int row = 16 * mt + i, col = 16 * (tile0 + t) + 4 * g;
     if (row >= R || col >= p.N) continue;
@@ -400,11 +396,32 @@ __global__ __launch_bounds__(64 * KS) void i8_stream(I8Args p) {
   }
 }
 
+// All rows of a segment, 16 MT at a time (with MT = 2 a last block of up to 16
+// rows multiplies half as much); longer segments read their weights again for
+// each block, from the caches.  MT = 1, for batches of up to 16 rows, holds fewer
+// registers, hence more waves and loads in flight (8 rows, 4096 x 14336: 17
+// against 23 us with the quantiser).
+template <int MT, int NT, bool GATED, bool F32OUT, int KS, int U1, int U2>
+__global__ __launch_bounds__(64 * KS) void i8_stream(I8Args p) {
+  __shared__ __attribute__((aligned(16))) i32x4 red[KS][MT * NT][64];
+  const int e = blockIdx.y;
+  int o;
+  const int R = i8_rows(p, e, o);
+  constexpr int stride = MT * NT * 64;
+  for (int r0 = 0; r0 < R; r0 += 16 * MT) {
+    if (r0) __syncthreads();   // the sums before have been read
+    if (MT == 1 || R - r0 <= 16)
+      i8_stream_block<1, NT, GATED, F32OUT, KS, U1>(p, e, o + r0, min(16, R - r0), &red[0][0][0], stride);
+    else i8_stream_block<2, NT, GATED, F32OUT, KS, U2>(p, e, o + r0, min(32, R - r0), &red[0][0][0], stride);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
 constexpr int I8_THIN = 32;        // rows up to which a segment streams
 constexpr int I8_THIN_MEAN = 64;   // expected rows from which every segment takes a tile
+constexpr int I8_THIN_MOST = 128;  // longest possible segment for which all of them stream
 
 // Output columns of a tile of height h.
 template <bool GATED>
@@ -416,9 +433,13 @@ static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t r
   hipError_t e;
   const bool stream = mean <= I8_THIN_MEAN;
   if (stream) {
+    // a second launch for the segments that do not fit costs about 5 us even if
+    // there are none; short batches stream them in blocks of 32 rows instead (32
+    // experts, 128 tokens: 246 -> 241 us, with skewed routing 247 -> 203 us; with
+    // 256 tokens and skewed routing the tiles are faster, 75 against 123 us)
+    const bool alone = most <= I8_THIN_MOST;
     p.lo = 0;
-    p.hi = I8_THIN;
-    const bool one = most <= 16;   // 16-row tiles alone
+    p.hi = alone ? INT32_MAX : I8_THIN;
     // four tiles of 16 columns a workgroup where that still makes a workgroup
     // per compute unit, else one (gated: one of each matrix)
     const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
@@ -426,14 +447,14 @@ static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t r
       hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n), dim3(64 * ks), 0, st, p);
       return hipGetLastError();
     };
-    if (wide) {
-      e = one ? go(i8_stream<1, 4, GATED, F32OUT, 4, 4>, GATED ? 32 : 64, 4)
-              : go(i8_stream<2, 4, GATED, F32OUT, 4, 3>, GATED ? 32 : 64, 4);
-    } else {
-      constexpr int NT = GATED ? 2 : 1;
-      e = one ? go(i8_stream<1, NT, GATED, F32OUT, 8, 4>, 16, 8) : go(i8_stream<2, NT, GATED, F32OUT, 8, 4>, 16, 8);
-    }
-    if (e != hipSuccess || most <= I8_THIN) return e;
+    constexpr int NT = GATED ? 2 : 1;
+    if (most <= 16)
+      e = wide ? go(i8_stream<1, 4, GATED, F32OUT, 4, 4, 4>, GATED ? 32 : 64, 4)
+               : go(i8_stream<1, NT, GATED, F32OUT, 8, 4, 4>, 16, 8);
+    else
+      e = wide ? go(i8_stream<2, 4, GATED, F32OUT, 4, 4, 3>, GATED ? 32 : 64, 4)
+               : go(i8_stream<2, NT, GATED, F32OUT, 8, 4, 4>, 16, 8);
+    if (e != hipSuccess || alone) return e;
   }
   p.lo = stream ? I8_THIN : 0;
   auto blocks = [&](int h) { return (p.N + I8Cols<GATED>(h) - 1) / I8Cols<GATED>(h); };

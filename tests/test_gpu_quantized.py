@@ -108,6 +108,7 @@ CASES = {
     "narrow": ([3, 0, 2], 8, 8, {}),
     "streams": ([0, 5, 16, 1, 17, 32], 264, 200, {}),
     "streams_16": ([4, 0, 16, 1], 1032, 328, dict(T=16, k=4)),
+    "streams_long": ([0, 5, 128, 33, 1, 64], 264, 200, dict(T=128, k=2, E=48)),   # blocks of 32 rows
     "mixed": ([0, 5, 33, 130, 1, 257], 264, 200, dict(T=257, k=2, E=48)),   # streams and tiles in one call
     "tiles": ([100, 70, 0, 150], 328, 264, {}),
     "tall_tiles": ([700, 0, 300], 136, 72, {}),
