@@ -44,7 +44,7 @@ MOE_F_WRITE_LOGITS, MOE_F_OVERLAP, MOE_F_FOLD_WEIGHT = 1, 2, 4
 MOE_WS_H, MOE_WS_Y_PACKED = 0, 1
 MOE_CALL_ROUTE, MOE_CALL_DISPATCH, MOE_CALL_EXPERT_GEMM, MOE_CALL_COMBINE, MOE_CALL_LAYER = range(5)
 MOE_CALL_DISPATCH_PADDED, MOE_CALL_EXPERT_GEMM_PADDED = 5, 6
-MOE_CALL_EXPERT_GEMM_TRAIN, MOE_CALL_EXPERT_GEMM_BACKWARD, MOE_CALL_EXPERT_GEMM_QUANTIZED = 7, 8, 9
+MOE_CALL_EXPERT_GEMM_BACKWARD, MOE_CALL_EXPERT_GEMM_QUANTIZED = 7, 8
 MOE_SCOPE_AGENT, MOE_SCOPE_SYSTEM = 0, 1
 
 EXPORTED = ["moe_last_error", "moe_version", "moe_workspace_bytes", "moe_route", "moe_dispatch",
@@ -107,7 +107,7 @@ def lib() -> ctypes.CDLL:
         L.moe_gemm_signal.argtypes = [i32, i32, i32, vp, vp, vp, vp, u32, i32, vp]
         L.moe_tile_forward.argtypes = [i32, i32, vp, vp, vp, u32, u32, i32, vp, i32, vp]
         i64 = ctypes.c_int64
-        L.moe_expert_gemm_train.argtypes = [P] + [vp] * 10 + [sz, vp]
+        L.moe_expert_gemm_train.argtypes = [P] + [vp] * 10
         L.moe_expert_gemm_backward.argtypes = [P] + [vp] * 14 + [sz, vp]
         L.moe_combine_backward.argtypes = [P] + [vp] * 7
         L.moe_quantize_rows.argtypes = [i64, i32, i32, vp, vp, vp, vp]
@@ -399,7 +399,7 @@ def expert_gemm_padded(p: Spec, capacity: int, x_packed, offsets, w1, w3, w2, wo
 # ---------------------------------------------------------------------------
 # training
 # ---------------------------------------------------------------------------
-def expert_gemm_train(p: Spec, x_packed, offsets, w1, w3, w2, workspace=None, stream=None, out=None):
+def expert_gemm_train(p: Spec, x_packed, offsets, w1, w3, w2, stream=None, out=None):
     """``expert_gemm`` that also returns the unactivated products the backward
     pass reads: (g, u, h, y_packed).  ``out``: these four, written in place."""
     torch = _torch()
@@ -415,13 +415,12 @@ def expert_gemm_train(p: Spec, x_packed, offsets, w1, w3, w2, workspace=None, st
     g, u, h, yp = out
     for t, n, name in ((g, p.f, "g"), (u, p.f, "u"), (h, p.f, "h"), (yp, p.d, "y_packed")):
         _need(t, (p.rows_max, n), dt, name)
-    ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_TRAIN, dev)
     _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (w3, "w3"), (w2, "w2"), (g, "g"),
-          (u, "u"), (h, "h"), (yp, "y_packed"), (ws, "workspace"))
+          (u, "u"), (h, "h"), (yp, "y_packed"))
     pc = p.c()
     _check(lib().moe_expert_gemm_train(ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1),
                                        _ptr(w3), _ptr(w2), _ptr(g), _ptr(u), _ptr(h), _ptr(yp),
-                                       _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+                                       _stream(stream)))
     return g, u, h, yp
 
 

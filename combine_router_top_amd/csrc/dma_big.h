@@ -319,15 +319,13 @@ __device__ __forceinline__ void bd_accum(const bf16_t* __restrict__ A, int64_t l
 // multiples of 8.
 //   SWIGLU: C[r0 + r][128 nt + h] = rnd(SiLU(A W1) * (A W3)), B1/B3 = [E][K][N]
 //   else:   C[r0 + r][256 nt + n] = rnd(s (A W2)),             B1 = [E][K][N]
-// with s = rscale[r0 + r], or 1 when rscale is NULL.  KEEP (SWIGLU): the
-// rounded products A W1 and A W3 go to keep.g and keep.u as well.
-template <bool SWIGLU, int NW, bool KEEP = false>
+// with s = rscale[r0 + r], or 1 when rscale is NULL.
+template <bool SWIGLU, int NW>
 __device__ __forceinline__ void bd_tile(const bf16_t* __restrict__ A, const bf16_t* __restrict__ B1,
                                         const bf16_t* __restrict__ B3, int K, int N,
                                         bf16_t* __restrict__ C, int e, int r0, int R, int nt,
                                         const int32_t* __restrict__ rows, int rdiv, uint32_t abytes,
-                                        const float* __restrict__ rscale, char* ring,
-                                        KeepOut keep = KeepOut{}) {
+                                        const float* __restrict__ rscale, char* ring) {
   constexpr int MT = BdCfg<NW>::MT;
   const int64_t estride = (int64_t)K * N;
   f32x4 acc[MT][8];
@@ -353,14 +351,6 @@ __device__ __forceinline__ void bd_tile(const bf16_t* __restrict__ A, const bf16
       if (row < R && col < N)
         *reinterpret_cast<u32x2*>(C + (int64_t)(r0 + row) * N + col) =
             u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-      if constexpr (KEEP) {
-        if (row < R && col < N) {
-          const f32x4 a = acc[mt][t], b = acc[mt][t + 4];
-          const int64_t at = (int64_t)(r0 + row) * N + col;
-          *reinterpret_cast<u32x2*>(keep.g + at) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
-          *reinterpret_cast<u32x2*>(keep.u + at) = u32x2{pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
-        }
-      }
     }
   }
 }

@@ -82,12 +82,6 @@ __device__ __forceinline__ s16x4 dt_tr16(const char* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((dt_lds4_t*)p);
 }
 
-// Where a kept forward pass writes its unactivated products.
-struct KeepOut {
-  bf16_t* g = nullptr;
-  bf16_t* u = nullptr;
-};
-
 // The ring: one __shared__ array of DT_LDS bytes (weight slot j at j DT_WSLOT,
 // A slot j at DT_AREG + j DT_ASLOT).
 struct DtSlots {
@@ -224,15 +218,13 @@ __device__ __forceinline__ void dt_step(const DtCtx<MT>& c, const DtSlots& S, in
 // rows[r0 + r] / rdiv of the abytes-byte matrix A.  K and N multiples of 8.
 //   SWIGLU: C[r0 + r][h] = rnd(SiLU(A W1) * (A W3)),  B1/B3 = [E][K][N]
 //   else:   C[r0 + r][n] = rnd(s (A W2)),               B1 = [E][K][N]
-// with s = rscale[r0 + r], or 1 when rscale is NULL.  KEEP (SWIGLU): the
-// rounded products A W1 and A W3 go to keep.g and keep.u as well.
-template <bool SWIGLU, int MT, bool KEEP = false>
+// with s = rscale[r0 + r], or 1 when rscale is NULL.
+template <bool SWIGLU, int MT>
 __device__ __forceinline__ void dt_block(const bf16_t* __restrict__ A, const bf16_t* __restrict__ B1,
                                          const bf16_t* __restrict__ B3, int K, int N,
                                          bf16_t* __restrict__ C, int e, int r0, int R, int nb, int mcols,
                                          const int32_t* __restrict__ rows, int rdiv, uint32_t abytes,
-                                         const float* __restrict__ rscale, int wave, const DtSlots& S,
-                                         KeepOut keep = KeepOut{}) {
+                                         const float* __restrict__ rscale, int wave, const DtSlots& S) {
   const int lane = threadIdx.x & 63;
   const int i = lane & 15, g = lane >> 4;
   const int64_t estride = (int64_t)K * N;
@@ -346,15 +338,12 @@ __device__ __forceinline__ void dt_block(const bf16_t* __restrict__ A, const bf1
     const int rbase = 16 * MT * wm + 16 * mt;
     const float sc = !SWIGLU && rscale && rbase + i < R ? rscale[r0 + rbase + i] : 1.0f;
 #pragma unroll
-    for (int pass = 0; pass < (KEEP ? 3 : 1); ++pass) {
-    bf16_t* out = !KEEP || pass == 0 ? C : pass == 1 ? keep.g : keep.u;
-#pragma unroll
     for (int t = 0; t < WC / 16; ++t) {
       float o[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float a = acc[mt][t][r];
-        o[r] = SWIGLU ? (pass == 0 ? silu_mul(a, acc[mt][t + 4][r]) : pass == 1 ? a : acc[mt][t + 4][r]) : a * sc;
+        o[r] = SWIGLU ? silu_mul(a, acc[mt][t + 4][r]) : a * sc;
       }
       *reinterpret_cast<u32x2*>(stg + i * RB + 32 * (t ^ (i & (NCH - 1))) + 8 * g) =
           u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
@@ -368,10 +357,9 @@ __device__ __forceinline__ void dt_block(const bf16_t* __restrict__ A, const bf1
                                                       16 * (p & 1));
       const int col = colw + 8 * p;
       if (rbase + row < R && col < cend)
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + (int64_t)(r0 + rbase + row) * N + col));
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(C + (int64_t)(r0 + rbase + row) * N + col));
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
   }
 }
 

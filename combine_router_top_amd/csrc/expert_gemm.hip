@@ -86,7 +86,6 @@ struct RowMap {
   // is multiplied by scale[p] before its rounding (the routing weight of its
   // assignment, so that combine only sums).  nullptr: no scale.
   const float* scale = nullptr;
-  KeepOut keep = KeepOut{};   // GEMM-1 of a kept forward pass: its unactivated products
 };
 
 // Segments of at most XG_THIN_MAX rows stream through the thin tiles, larger
@@ -229,7 +228,7 @@ __device__ RowBlock schedule(const int32_t* __restrict__ offsets, int e_begin, i
   return rb;
 }
 
-template <class Cfg, bool SWIGLU, int MT, bool KEEP>
+template <class Cfg, bool SWIGLU, int MT>
 __device__ __forceinline__ void gemm_body(const bf16_t* __restrict__ A, const bf16_t* __restrict__ Bl,
                                           int K, int N, int col, bf16_t* __restrict__ C,
                                           const RowBlock& rb, const RowMap& rm, bf16_t* As,
@@ -250,8 +249,6 @@ __device__ __forceinline__ void gemm_body(const bf16_t* __restrict__ A, const bf
   // lower half holds x.W1 for; they hand them over through LDS (pairs
   // 0 .. NW/4 - 1 through xch0, the others through xch1).
   bool store_wave = true;
-  [[maybe_unused]] f32x4 up[KEEP ? MT : 1][CPL];   // the W3 products where they are kept
-  [[maybe_unused]] f32x4 gate[KEEP ? MT : 1][CPL];
   if (SWIGLU) {
     store_wave = wave < NW / 2;
     const int pair = wave % (NW / 2);
@@ -275,10 +272,6 @@ __device__ __forceinline__ void gemm_body(const bf16_t* __restrict__ A, const bf
             const float a = acc[mt][c][r];
             const float b = slot[((mt * CPL + c) * 4 + r) * 64];
             acc[mt][c][r] = silu_mul(a, b);
-            if constexpr (KEEP) {
-              gate[mt][c][r] = a;
-              up[mt][c][r] = b;
-            }
           }
     }
   }
@@ -301,13 +294,6 @@ __device__ __forceinline__ void gemm_body(const bf16_t* __restrict__ A, const bf
         } else {
           *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16x2(acc[mt][0][r], acc[mt][1][r]),
                                                  pack_bf16x2(acc[mt][2][r], acc[mt][3][r])};
-          if constexpr (KEEP) {
-            const int64_t at = (int64_t)(rb.r0 + row) * N + col;
-            *reinterpret_cast<u32x2*>(rm.keep.g + at) = u32x2{pack_bf16x2(gate[mt][0][r], gate[mt][1][r]),
-                                                              pack_bf16x2(gate[mt][2][r], gate[mt][3][r])};
-            *reinterpret_cast<u32x2*>(rm.keep.u + at) = u32x2{pack_bf16x2(up[mt][0][r], up[mt][1][r]),
-                                                              pack_bf16x2(up[mt][2][r], up[mt][3][r])};
-          }
         }
       }
     }
@@ -315,7 +301,7 @@ __device__ __forceinline__ void gemm_body(const bf16_t* __restrict__ A, const bf
 }
 
 // One streamed row block of class Cfg.
-template <class Cfg, bool SWIGLU, bool KEEP>
+template <class Cfg, bool SWIGLU>
 __device__ __forceinline__ void stream_block(const bf16_t* __restrict__ A, const bf16_t* __restrict__ B1,
                                              const bf16_t* __restrict__ B3, int K, int N,
                                              bf16_t* __restrict__ C, const RowBlock& rb,
@@ -336,7 +322,7 @@ __device__ __forceinline__ void stream_block(const bf16_t* __restrict__ A, const
   const int mt = (rb.R + 15) >> 4;
   switch (mt) {
 #define XG_CASE(n) \
-  case n: if constexpr (n <= Cfg::MTMAX) gemm_body<Cfg, SWIGLU, n, KEEP>(A, Bl, K, N, col, C, rb, rm, As, xch0, xch1); break;
+  case n: if constexpr (n <= Cfg::MTMAX) gemm_body<Cfg, SWIGLU, n>(A, Bl, K, N, col, C, rb, rm, As, xch0, xch1); break;
     XG_CASE(1) XG_CASE(2) XG_CASE(3) XG_CASE(4) XG_CASE(5)
     XG_CASE(6) XG_CASE(7) XG_CASE(8) XG_CASE(9) XG_CASE(10)
 #undef XG_CASE
@@ -437,7 +423,7 @@ static_assert(2 * (XG_MAXN + 1) * 4 <= DT_LDS, "the schedule's prefix sums fit t
 // else:   A = h [*, K = f], B1 = w2 [n][K][N = d], C = y_packed [*, d]
 // Segments with fewer than `th` rows; each picks its tile class by row count.
 // K and N tails are bounded by the buffer descriptors (gemm_core.h).
-template <bool SWIGLU, bool KEEP = false>
+template <bool SWIGLU>
 __global__ __launch_bounds__(64 * XGThin::NW) void grouped_gemm_bf16(const bf16_t* __restrict__ A,
                                                                      const int32_t* __restrict__ offsets,
                                                                      int e_begin, int e_end,
@@ -473,7 +459,7 @@ __global__ __launch_bounds__(64 * XGThin::NW) void grouped_gemm_bf16(const bf16_
   __syncthreads();         // every wave has read the prefix sums before the ring is written
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (rb.cls == 0) {
-    stream_block<XGThin, SWIGLU, KEEP>(A, B1, B3, K, N, C, rb, rm, wave, SWIGLU ? XGThin::COLS : tcols,
+    stream_block<XGThin, SWIGLU>(A, B1, B3, K, N, C, rb, rm, wave, SWIGLU ? XGThin::COLS : tcols,
                                  reinterpret_cast<bf16_t*>(ring), reinterpret_cast<float*>(ring + XG_TPART),
                                  reinterpret_cast<float*>(ring + 2 * XG_TPART));
     return;
@@ -482,8 +468,8 @@ __global__ __launch_bounds__(64 * XGThin::NW) void grouped_gemm_bf16(const bf16_
   switch ((rb.R + 31) >> 5) {
 #define XM_CASE(n)                                                                              \
   case n:                                                                                       \
-    dt_block<SWIGLU, n, KEEP>(A, B1, B3, K, N, C, rb.e, rb.r0, rb.R, rb.nb, mcols, rm.rows, rm.div,    \
-                        rm.bytes, rm.scale, wave, slots, rm.keep);                              \
+    dt_block<SWIGLU, n>(A, B1, B3, K, N, C, rb.e, rb.r0, rb.R, rb.nb, mcols, rm.rows, rm.div,    \
+                        rm.bytes, rm.scale, wave, slots);                                       \
     break;
     XM_CASE(1) XM_CASE(2) XM_CASE(3) XM_CASE(4) XM_CASE(5)
 #undef XM_CASE
@@ -501,7 +487,7 @@ __global__ __launch_bounds__(64 * XGThin::NW) void grouped_gemm_bf16(const bf16_
 // neighbouring tiles share operands in that XCD's L2.  The host sizes G to
 // cover every tile, so each workgroup takes at most one and the hardware
 // balances the compute units.
-template <bool SWIGLU, bool KEEP = false>
+template <bool SWIGLU>
 __global__ __launch_bounds__(64 * XB_NW, 1) void grouped_gemm_bf16_big(
     const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets, int e_begin, int e_end,
     const bf16_t* __restrict__ B1, const bf16_t* __restrict__ B3, int K, int N,
@@ -541,8 +527,8 @@ __global__ __launch_bounds__(64 * XB_NW, 1) void grouped_gemm_bf16_big(
     bt.R = __builtin_amdgcn_readfirstlane(bt.R);
     bt.nt = __builtin_amdgcn_readfirstlane(bt.nt);
     __syncthreads();   // every wave has read the table before the copies overwrite it
-    bd_tile<SWIGLU, XB_NW, KEEP>(A, B1, B3, K, N, C, bt.e, bt.r0, bt.R, bt.nt, rm.rows, rm.div, rm.bytes,
-                                 rm.scale, ring, rm.keep);
+    bd_tile<SWIGLU, XB_NW>(A, B1, B3, K, N, C, bt.e, bt.r0, bt.R, bt.nt, rm.rows, rm.div, rm.bytes,
+                           rm.scale, ring);
   }
 }
 
@@ -617,8 +603,7 @@ __global__ __launch_bounds__(256) void grouped_gemm_f32(const float* __restrict_
                                                         const float* __restrict__ B1,
                                                         const float* __restrict__ B3, int K, int N,
                                                         float* __restrict__ C,
-                                                        const float* __restrict__ rscale,
-                                                        float* __restrict__ keep_g, float* __restrict__ keep_u) {
+                                                        const float* __restrict__ rscale) {
   const int64_t p = (int64_t)offsets[e_begin] + blockIdx.x;
   if (p >= offsets[e_end]) return;
   const int n = blockIdx.y * 256 + threadIdx.x;
@@ -634,10 +619,6 @@ __global__ __launch_bounds__(256) void grouped_gemm_f32(const float* __restrict_
   for (int kk = 0; kk < K; ++kk) {
     s1 = fmaf(a[kk], B1[es + (int64_t)kk * N + n], s1);
     if (SWIGLU) s3 = fmaf(a[kk], B3[es + (int64_t)kk * N + n], s3);
-  }
-  if (SWIGLU && keep_g) {
-    keep_g[p * N + n] = s1;
-    keep_u[p * N + n] = s3;
   }
   C[p * N + n] = SWIGLU ? s1 / (1.0f + expf(-s1)) * s3 : (rscale ? s1 * rscale[p] : s1);
 }
@@ -661,17 +642,14 @@ int device_cus() { return big_cus(); }
 // the down projection's real workgroups per XCD (8 ints), written by GEMM-1
 size_t expert_gemm_ws_bytes(const Prob& p) { return p.dtype == 1 ? 256 : 0; }
 
-// KEEP: GEMM-1 also writes g = rnd(x W1) and u = rnd(x W3).
-template <bool KEEP>
-static hipError_t launch_gemms(const Prob& p, const void* x_packed, const int32_t* offsets,
-                               const void* w1, const void* w3, const void* w2, void* h,
-                               void* y_packed, void* ws, int e_begin, int e_end, hipStream_t st,
-                               const int32_t* perm, const float* rscale, void* g, void* u) {
+hipError_t launch_expert_gemm(const Prob& p, const void* x_packed, const int32_t* offsets,
+                              const void* w1, const void* w3, const void* w2, void* h,
+                              void* y_packed, void* ws, int e_begin, int e_end, hipStream_t st,
+                              const int32_t* perm, const float* rscale) {
   if (p.rows_max == 0 || e_end <= e_begin) return hipSuccess;
   if (p.dtype == 1) {
     // with perm, x_packed is x itself and GEMM-1 reads row perm[p] / k for packed row p
-    RowMap rm1 = perm ? RowMap{perm, p.k, (uint32_t)((int64_t)p.T * p.d * 2)} : RowMap{nullptr, 1, 0};
-    if (KEEP) rm1.keep = KeepOut{(bf16_t*)g, (bf16_t*)u};
+    const RowMap rm1 = perm ? RowMap{perm, p.k, (uint32_t)((int64_t)p.T * p.d * 2)} : RowMap{nullptr, 1, 0};
     const RowMap rm2{nullptr, 1, 0, rscale};
     // Dense-like routing (the mean segment reaches XB_TH rows, or every
     // segment does in the padded layout): experts with >= XB_TH rows go to the
@@ -748,13 +726,13 @@ static hipError_t launch_gemms(const Prob& p, const void* x_packed, const int32_
     hipError_t e;
     if (big) {
       const int ntn = (p.f + 127) / 128;
-      hipLaunchKernelGGL((grouped_gemm_bf16_big<true, KEEP>), dim3(big_grid(ntn)), dim3(64 * XB_NW), 0, st,
+      hipLaunchKernelGGL(grouped_gemm_bf16_big<true>, dim3(big_grid(ntn)), dim3(64 * XB_NW), 0, st,
                          (const bf16_t*)x_packed, offsets, e_begin, e_end, (const bf16_t*)w1,
                          (const bf16_t*)w3, p.d, p.f, (bf16_t*)h, ntn, rm1);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     int* xcnt = reinterpret_cast<int*>(ws);
-    hipLaunchKernelGGL((grouped_gemm_bf16<true, KEEP>), dim3(grid(2 * p.f, mc1, tc1)), dim3(64 * XGThin::NW), 0, st,
+    hipLaunchKernelGGL(grouped_gemm_bf16<true>, dim3(grid(2 * p.f, mc1, tc1)), dim3(64 * XGThin::NW), 0, st,
                        (const bf16_t*)x_packed, offsets, e_begin, e_end, (const bf16_t*)w1,
                        (const bf16_t*)w3, p.d, p.f, (bf16_t*)h, th, mc1, tc1, rm1, xcnt, p.d, mc2, tc2);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -774,29 +752,14 @@ static hipError_t launch_gemms(const Prob& p, const void* x_packed, const int32_
   dim3 g1((unsigned)p.rows_max, (p.f + 255) / 256);
   hipLaunchKernelGGL(grouped_gemm_f32<true>, g1, dim3(256), 0, st, (const float*)x_packed, offsets,
                      e_begin, e_end, (const float*)w1, (const float*)w3, p.d, p.f, (float*)h,
-                     (const float*)nullptr, KEEP ? (float*)g : nullptr, KEEP ? (float*)u : nullptr);
+                     (const float*)nullptr);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   dim3 g2((unsigned)p.rows_max, (p.d + 255) / 256);
   hipLaunchKernelGGL(grouped_gemm_f32<false>, g2, dim3(256), 0, st, (const float*)h, offsets,
                      e_begin, e_end, (const float*)w2, (const float*)nullptr, p.f, p.d,
-                     (float*)y_packed, rscale, (float*)nullptr, (float*)nullptr);
+                     (float*)y_packed, rscale);
   return hipGetLastError();
-}
-
-hipError_t launch_expert_gemm(const Prob& p, const void* x_packed, const int32_t* offsets,
-                              const void* w1, const void* w3, const void* w2, void* h,
-                              void* y_packed, void* ws, int e_begin, int e_end, hipStream_t st,
-                              const int32_t* perm, const float* rscale) {
-  return launch_gemms<false>(p, x_packed, offsets, w1, w3, w2, h, y_packed, ws, e_begin, e_end, st, perm,
-                             rscale, nullptr, nullptr);
-}
-
-hipError_t launch_expert_gemm_keep(const Prob& p, const void* x_packed, const int32_t* offsets,
-                                   const void* w1, const void* w3, const void* w2, void* g, void* u,
-                                   void* h, void* y_packed, void* ws, hipStream_t st) {
-  return launch_gemms<true>(p, x_packed, offsets, w1, w3, w2, h, y_packed, ws, 0, p.n, st, nullptr, nullptr,
-                            g, u);
 }
 
 }  // namespace moe

@@ -3,18 +3,20 @@
 //
 //   g = rnd(x W1), u = rnd(x W3), h = rnd(SiLU(x W1) (x W3)), y = rnd(h W2)
 //
-// Three regimes.  Where the weights' stream bounds the pass (tens to a few
-// hundred rows an expert, large weights) the streaming kernels of
-// expert_gemm.hip run with an epilogue that also stores g and u: a workgroup
-// there reads 512 weight columns for at most 160 rows.  Long segments (dense
-// routing, a dense block) and small problems take the tiles of seg_tile.h: the
-// former because the matrix cores bound them, the latter because those tiles
-// come small enough to occupy the compute units.
+// bf16: two launches over the tiles of seg_tile.h; W1 and W3 products of an h
+// column meet in one lane, so g, u and h leave from registers.  The launch pair
+// of expert_gemm.hip streams a set of weight columns past at most 160 rows and is
+// within 10% of this one where every segment is short (32 experts of 7168 x 2048,
+// about 80 rows each: 485 against 545 us); where any segment is longer it reads
+// those weights once more and in a second round of workgroups (about 128 rows each:
+// 719 against 568 us; 16 .. 96 rows each, skewed: 735 against 570 .. 660 us), and
+// training batches are of that kind.
 #include <stdint.h>
 
 #include <algorithm>
 
 #include "common.h"
+#include "f32_tile.h"
 #include "kernels.h"
 #include "seg_tile.h"
 
@@ -95,17 +97,65 @@ __global__ __launch_bounds__(ST_NT, 1) void keep_down_bf16(const bf16_t* __restr
       });
 }
 
+__global__ __launch_bounds__(64 * F_NW) void keep_up_f32(const float* __restrict__ x, const int32_t* __restrict__ offsets,
+                                                         int n, const float* __restrict__ w1,
+                                                         const float* __restrict__ w3, float* __restrict__ g,
+                                                         float* __restrict__ u, float* __restrict__ h, int d, int f) {
+  __shared__ __attribute__((aligned(16))) F32Lds s;
+  StTile t;
+  if (!f32_row_block(offsets, n, blockIdx.x, t)) return;
+  const int c0 = blockIdx.y * F_T;
+  const float* a = x + (int64_t)t.r0 * d;
+  const int64_t bo = (int64_t)t.e * d * f + c0;
+  auto rows = [&](int k, int j) { return j < t.R ? a[(int64_t)j * d + k] : 0.f; };
+  float gate[4][4] = {}, up[4][4] = {};
+  f32_tile(rows, true, [&](int k, int j) { return c0 + j < f ? w1[bo + (int64_t)k * f + j] : 0.f; }, false, d, s, gate);
+  f32_join(s, gate);
+  __syncthreads();   // the joined sums are read before the next ones arrive
+  f32_tile(rows, true, [&](int k, int j) { return c0 + j < f ? w3[bo + (int64_t)k * f + j] : 0.f; }, false, d, s, up);
+  f32_join(s, up);
+  f32_store(gate, up, [&](int row, int col, float gv, float uv) {
+    if (row >= t.R || c0 + col >= f) return;
+    const int64_t at = (int64_t)(t.r0 + row) * f + c0 + col;
+    g[at] = gv;
+    u[at] = uv;
+    h[at] = gv / (1.0f + expf(-gv)) * uv;
+  });
+}
+
+__global__ __launch_bounds__(64 * F_NW) void keep_down_f32(const float* __restrict__ h, const int32_t* __restrict__ offsets,
+                                                           int n, const float* __restrict__ w2, float* __restrict__ y,
+                                                           int d, int f) {
+  __shared__ __attribute__((aligned(16))) F32Lds s;
+  StTile t;
+  if (!f32_row_block(offsets, n, blockIdx.x, t)) return;
+  const int c0 = blockIdx.y * F_T;
+  const float* a = h + (int64_t)t.r0 * f;
+  const float* b = w2 + (int64_t)t.e * f * d + c0;
+  float acc[4][4] = {};
+  f32_tile([&](int k, int j) { return j < t.R ? a[(int64_t)j * f + k] : 0.f; }, true,
+           [&](int k, int j) { return c0 + j < d ? b[(int64_t)k * d + j] : 0.f; }, false, f, s, acc);
+  f32_join(s, acc);
+  f32_store(acc, [&](int row, int col, float v) {
+    if (row < t.R && c0 + col < d) y[(int64_t)(t.r0 + row) * d + c0 + col] = v;
+  });
+}
+
 hipError_t launch_expert_gemm_train(const Prob& p, const void* x_packed, const int32_t* offsets,
                                     const void* w1, const void* w3, const void* w2, void* g, void* u,
-                                    void* h, void* y_packed, void* ws, hipStream_t st) {
-  const int64_t mean = p.tk() / p.E;
+                                    void* h, void* y_packed, hipStream_t st) {
+  if (p.dtype != 1) {
+    const unsigned rb = f32_row_blocks(p);
+    hipLaunchKernelGGL(keep_up_f32, dim3(rb, (p.f + F_T - 1) / F_T), dim3(64 * F_NW), 0, st, (const float*)x_packed,
+                       offsets, p.n, (const float*)w1, (const float*)w3, (float*)g, (float*)u, (float*)h, p.d, p.f);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(keep_down_f32, dim3(rb, (p.d + F_T - 1) / F_T), dim3(64 * F_NW), 0, st, (const float*)h, offsets,
+                       p.n, (const float*)w2, (float*)y_packed, p.d, p.f);
+    return hipGetLastError();
+  }
   const int nup = (p.f + 127) / 128, ndown = (p.d + 255) / 256;
-  const int64_t small = (int64_t)p.n * std::max<int64_t>(1, (mean + 63) / 64) * std::max(nup, ndown);
-  const int cus = device_cus();
-  const bool wide = p.d > (1 << 20) || p.f > (1 << 20);   // beyond seg_tile.h's 32-bit offsets
-  if (p.dtype != 1 || wide || (mean < 320 && small > cus))
-    return launch_expert_gemm_keep(p, x_packed, offsets, w1, w3, w2, g, u, h, y_packed, ws, st);
-  const int64_t seg = std::max<int64_t>(1, mean);
+  const int64_t seg = std::max<int64_t>(1, p.tk() / p.E);   // expected rows of a segment
   hipError_t e = st_with_height(
       st_height(p.n, seg, (p.d + 63) / 64, {0, nup, nup, nup, nup}, {0, 256, 256, 256, 256}), [&](auto m) {
         hipLaunchKernelGGL(keep_up_bf16<m()>, st_row_grid(p.rows_max, p.n, m(), nup), dim3(ST_NT), 0, st,

@@ -1,0 +1,126 @@
+// fp32 products of the training calls: 32 x 32 tiles of eight waves that split K.
+// The fp32 problems of this library are small and have tens of tiles, so what
+// counts is how many trips to memory follow one another: each wave takes every
+// eighth 16-deep slice of K through its own LDS, the next slice's operands loaded
+// while one is multiplied, and the eight sums meet at the end, in a fixed order.
+#pragma once
+
+#include <algorithm>
+
+#include "common.h"
+#include "kernels.h"
+#include "seg_tile.h"
+
+namespace moe {
+
+constexpr int F_K = 16, F_T = 32, F_LD = F_T + 4;   // slice depth, tile side, LDS row (16-byte aligned)
+constexpr int F_NW = 8;                             // waves
+
+struct F32Lds {
+  float a[F_NW][F_K * F_LD], b[F_NW][F_K * F_LD];
+  float sum[F_NW - 1][F_T * F_T];
+};
+
+// acc[p][r] of this lane: rows 4 ty + p, columns 4 tx + r (ty, tx = lane / 8,
+// lane % 8) of the sum over k < K of A(k, row) B(k, column), complete in wave 0.
+// A and B give 0 outside their operand; *_kfast: k is their contiguous index.
+// All waves call.
+template <class FA, class FB>
+__device__ __forceinline__ void f32_tile(const FA& A, bool a_kfast, const FB& B, bool b_kfast, int K, F32Lds& s,
+                                         float (&acc)[4][4]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tx = lane & 7, ty = lane >> 3;
+  float* sa = s.a[wave];
+  float* sb = s.b[wave];
+  float ra[8], rb[8];
+  // element v of a lane: (k, j), the operand's contiguous index fastest over lanes
+  auto kk = [&](bool kfast, int v) { return kfast ? lane & 15 : (lane >> 5) + 2 * v; };
+  auto jj = [&](bool kfast, int v) { return kfast ? (lane >> 4) + 4 * v : lane & 31; };
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const int ka = k0 + kk(a_kfast, v), kb = k0 + kk(b_kfast, v);
+      ra[v] = ka < K ? A(ka, jj(a_kfast, v)) : 0.f;
+      rb[v] = kb < K ? B(kb, jj(b_kfast, v)) : 0.f;
+    }
+  };
+  load(F_K * wave);
+  for (int k0 = F_K * wave; k0 < K; k0 += F_NW * F_K) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      sa[kk(a_kfast, v) * F_LD + jj(a_kfast, v)] = ra[v];
+      sb[kk(b_kfast, v) * F_LD + jj(b_kfast, v)] = rb[v];
+    }
+    // this wave alone writes and reads its part: LDS operations of a wave stay in order
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (k0 + F_NW * F_K < K) load(k0 + F_NW * F_K);
+#pragma unroll
+    for (int k = 0; k < F_K; ++k) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(sa + k * F_LD + 4 * ty);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(sb + k * F_LD + 4 * tx);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[p][r] = fmaf(a[p], b[r], acc[p][r]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// Adds the other waves' sums to wave 0's.
+__device__ __forceinline__ void f32_join(F32Lds& s, float (&acc)[4][4]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (wave) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s.sum[wave - 1][(4 * p + r) * 64 + lane] = acc[p][r];
+  }
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 0; w < F_NW - 1; ++w)
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[p][r] += s.sum[w][(4 * p + r) * 64 + lane];
+  }
+}
+
+// Row block b of 32 rows, counted over all segments; false past the last.
+__device__ __forceinline__ bool f32_row_block(const int32_t* offsets, int n, int b, StTile& t) {
+  t = st_tile_at(b, offsets, n, 1, F_T);
+  return t.R > 0;
+}
+
+// Calls put(row, column, value) for this lane's values of the tile.
+template <class Put>
+__device__ __forceinline__ void f32_store(const float (&acc)[4][4], const Put& put) {
+  if (threadIdx.x >= 64) return;
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) put(4 * ty + p, 4 * tx + r, acc[p][r]);
+}
+
+// The same over two tiles: put(row, column, first, second).
+template <class Put>
+__device__ __forceinline__ void f32_store(const float (&a)[4][4], const float (&b)[4][4], const Put& put) {
+  if (threadIdx.x >= 64) return;
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) put(4 * ty + p, 4 * tx + r, a[p][r], b[p][r]);
+}
+
+// At most this many blocks of 32 rows, over all segments.
+inline unsigned f32_row_blocks(const Prob& p) {
+  return (unsigned)std::min<int64_t>((p.rows_max + F_T - 1) / F_T + p.n, p.rows_max);
+}
+
+}  // namespace moe

@@ -58,15 +58,11 @@ hipError_t launch_expert_gemm(const Prob& p, const void* x_packed, const int32_t
                               const void* w1, const void* w3, const void* w2, void* h,
                               void* y_packed, void* ws, int e_begin, int e_end, hipStream_t st,
                               const int32_t* perm = nullptr, const float* rscale = nullptr);
-// The same over all local experts, keeping g = rnd(x W1) and u = rnd(x W3).
-hipError_t launch_expert_gemm_keep(const Prob& p, const void* x_packed, const int32_t* offsets,
-                                   const void* w1, const void* w3, const void* w2, void* g, void* u,
-                                   void* h, void* y_packed, void* ws, hipStream_t st);
 
 // expert_train.hip: the training forward pass.
 hipError_t launch_expert_gemm_train(const Prob& p, const void* x_packed, const int32_t* offsets,
                                     const void* w1, const void* w3, const void* w2, void* g, void* u,
-                                    void* h, void* y_packed, void* ws, hipStream_t st);
+                                    void* h, void* y_packed, hipStream_t st);
 
 // expert_gemm.hip: GEMM C = rnd(A B) with a release flag per 256 x 256 tile
 int64_t gemm_signal_tiles(int M, int N);

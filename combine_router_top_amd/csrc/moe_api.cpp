@@ -121,8 +121,7 @@ size_t call_ws_bytes(const moe::Prob& p, int32_t call) {
     case MOE_CALL_COMBINE: return 0;
     case MOE_CALL_LAYER: return layer_ws(p).total;
     case MOE_CALL_DISPATCH_PADDED: return moe::dispatch_padded_ws_bytes(p);
-    case MOE_CALL_EXPERT_GEMM_PADDED:
-    case MOE_CALL_EXPERT_GEMM_TRAIN: return moe::expert_gemm_ws_bytes(p);
+    case MOE_CALL_EXPERT_GEMM_PADDED: return moe::expert_gemm_ws_bytes(p);
     case MOE_CALL_EXPERT_GEMM_BACKWARD: return moe::expert_backward_ws_bytes(p);
     case MOE_CALL_EXPERT_GEMM_QUANTIZED: return moe::expert_i8_ws_bytes(p);
     default: return 0;
@@ -166,9 +165,9 @@ moe_status_t check_signal_shape(int32_t M, int32_t N, int32_t K) {
   return MOE_OK;
 }
 
-// The backward pass addresses up to 256 rows of d or f elements, and a 2 GiB
+// The training calls address up to 256 rows of d or f elements, and a 2 GiB
 // run of rows in steps of 32, with 32-bit offsets.
-moe_status_t check_backward_widths(const moe::Prob& q) {
+moe_status_t check_training_widths(const moe::Prob& q) {
   const int32_t lim = 1 << 20;
   if (q.d > lim || q.f > lim)
     return fail(MOE_ERR_UNSUPPORTED, "d=%d and f=%d must be at most %d", q.d, q.f, lim);
@@ -436,10 +435,11 @@ moe_status_t moe_expert_gemm_padded(const moe_problem_t* p, int32_t capacity, co
 moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
                                    const int32_t* offsets, const void* w1, const void* w3,
                                    const void* w2, void* g, void* u, void* h, void* y_packed,
-                                   void* workspace, size_t workspace_bytes, void* stream) {
+                                   void* stream) {
   moe::Prob q;
   moe_status_t st = check_problem(p, &q);
   if (st != MOE_OK) return st;
+  if ((st = check_training_widths(q)) != MOE_OK) return st;
   NEED_PTR(offsets);
   NEED_PTR(w1);
   NEED_PTR(w3);
@@ -458,10 +458,9 @@ moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
   NEED_ALIGNED(u);
   NEED_ALIGNED(h);
   NEED_ALIGNED(y_packed);
-  if ((st = check_ws(q, MOE_CALL_EXPERT_GEMM_TRAIN, workspace, workspace_bytes)) != MOE_OK) return st;
   (void)hipGetLastError();
   return hip_status(moe::launch_expert_gemm_train(q, x_packed, offsets, w1, w3, w2, g, u, h, y_packed,
-                                                  workspace, (hipStream_t)stream),
+                                                  (hipStream_t)stream),
                     "moe_expert_gemm_train");
 }
 
@@ -474,7 +473,7 @@ moe_status_t moe_expert_gemm_backward(const moe_problem_t* p, const void* x_pack
   moe::Prob q;
   moe_status_t st = check_problem(p, &q);
   if (st != MOE_OK) return st;
-  if ((st = check_backward_widths(q)) != MOE_OK) return st;
+  if ((st = check_training_widths(q)) != MOE_OK) return st;
   NEED_PTR(offsets);
   NEED_PTR(w1);
   NEED_PTR(w3);

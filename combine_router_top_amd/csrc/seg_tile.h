@@ -1,14 +1,15 @@
 // Tiles of a product over expert segments whose two operands may lie in memory
-// in any of three ways (gfx950): the products of the experts' backward pass
-// (bf16) and of the 8-bit experts (int8) share this core.
+// in any of three ways (gfx950): the products of the experts' training forward
+// and backward passes (bf16) and of the 8-bit experts (int8) share this core.
 //
 // A workgroup of 8 waves computes (64 MT) x 256 tiles, MT = 2, 3 or 4, or, for
 // small problems, 64 x 128 tiles, in stages of 128 bytes of K (64 bf16 or 128
 // int8 values, two 16x16 MFMA k-steps).  Wave (wm, wn) = (w & 3, w >> 2)
-// multiplies 16 MT tile rows by half of the tile's columns.  Both operands of a stage are copied from memory straight into
-// LDS (16 bytes per lane and instruction), the rows into a ring of NA slots and
-// the columns into one of NB.  While a wave multiplies one k-step from
-// registers it reads the fragments of the next.  A stage costs one barrier, in
+// multiplies 16 MT tile rows by half of the tile's columns.  Both operands of a
+// stage are copied from memory straight into LDS (16 bytes per lane and
+// instruction), the rows into a ring of NA slots and the columns into one of NB.
+// While a wave multiplies one k-step from registers it reads the fragments of
+// the next.  A stage costs one barrier, in
 // its middle: by then every wave holds the stage's second half in registers,
 // so its slots may be refilled, and the wait before it has seen the next
 // stage's copies arrive.

@@ -94,9 +94,8 @@ enum {
   MOE_CALL_LAYER = 4,
   MOE_CALL_DISPATCH_PADDED = 5,
   MOE_CALL_EXPERT_GEMM_PADDED = 6,
-  MOE_CALL_EXPERT_GEMM_TRAIN = 7,
-  MOE_CALL_EXPERT_GEMM_BACKWARD = 8,
-  MOE_CALL_EXPERT_GEMM_QUANTIZED = 9
+  MOE_CALL_EXPERT_GEMM_BACKWARD = 7,
+  MOE_CALL_EXPERT_GEMM_QUANTIZED = 8
 };
 
 /*
@@ -275,14 +274,13 @@ moe_status_t moe_expert_gemm_padded(const moe_problem_t* p, int32_t capacity, co
  * and h, y_packed by the formulas of moe_expert_gemm (h from the unrounded
  * products; the fp32 sums may run in another order).
  *   g, u [rows_max,f]  dtype output (rows >= A untouched)
- *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_TRAIN) bytes
- * A dense gated block is the problem with E = k = n_local = 1 and offsets
- * {0, T}.
+ * d and f at most 2^20.  A dense gated block is the problem with E = k = n_local
+ * = 1 and offsets {0, T}.
  */
 moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
                                    const int32_t* offsets, const void* w1, const void* w3,
                                    const void* w2, void* g, void* u, void* h, void* y_packed,
-                                   void* workspace, size_t workspace_bytes, void* stream);
+                                   void* stream);
 
 /*
  * Backward pass of the local experts.  With the g, u, h that

@@ -324,12 +324,11 @@ def test_backward_captured():
     x, dyd = r.packed(v["x"]), r.packed(dy)
     n = len(r.counts)
     ws = M.alloc_workspace(p, M.MOE_CALL_EXPERT_GEMM_BACKWARD)
-    ws2 = M.alloc_workspace(p, M.MOE_CALL_EXPERT_GEMM_TRAIN)
     fw = tuple(r.out(w) for w in (p.f, p.f, p.f, p.d))
     bw = (r.out(p.d), *(torch.empty(s, dtype=r.dt, device="cuda") for s in ((n, p.d, p.f), (n, p.d, p.f), (n, p.f, p.d))))
 
     def step():
-        M.expert_gemm_train(p, x, off, *W, workspace=ws2, out=fw)
+        M.expert_gemm_train(p, x, off, *W, out=fw)
         M.expert_gemm_backward(p, x, off, *W, *fw[:3], dyd, workspace=ws, out=bw)
 
     s = torch.cuda.Stream()
