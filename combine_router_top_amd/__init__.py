@@ -30,6 +30,7 @@ Functions (same names as the C calls):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -225,6 +226,16 @@ def _here(*named):
             raise ValueError(f"{name} is on device {t.get_device()}, the current device is {cur}")
 
 
+_here_and_now = contextlib.nullcontext()
+
+
+def _alloc_on(stream):
+    """Context for what a call with ``stream=`` allocates: on that stream, so that
+    fills come before the call's kernels there and memory given back meets only
+    later work there."""
+    return _here_and_now if stream is None else _torch().cuda.stream(stream)
+
+
 def alloc_workspace(p: Spec, call: int = MOE_CALL_LAYER, device="cuda"):
     torch = _torch()
     n = workspace_bytes(p, call)
@@ -411,7 +422,8 @@ def expert_gemm_train(p: Spec, x_packed, offsets, w1, w3, w2, stream=None, out=N
     _need(w2, (p.n_local, p.f, p.d), dt, "w2")
     dev = x_packed.device
     if out is None:
-        out = tuple(torch.zeros((p.rows_max, n), dtype=dt, device=dev) for n in (p.f, p.f, p.f, p.d))
+        with _alloc_on(stream):
+            out = tuple(torch.zeros((p.rows_max, n), dtype=dt, device=dev) for n in (p.f, p.f, p.f, p.d))
     g, u, h, yp = out
     for t, n, name in ((g, p.f, "g"), (u, p.f, "u"), (h, p.f, "h"), (yp, p.d, "y_packed")):
         _need(t, (p.rows_max, n), dt, name)
@@ -439,14 +451,18 @@ def expert_gemm_backward(p: Spec, x_packed, offsets, w1, w3, w2, g, u, h, dy_pac
     _need(w2, (p.n_local, p.f, p.d), dt, "w2")
     dev = x_packed.device
     if out is None:
-        out = (torch.zeros((p.rows_max, p.d), dtype=dt, device=dev), torch.empty_like(w1),
-               torch.empty_like(w3), torch.empty_like(w2))
+        with _alloc_on(stream):
+            out = (torch.zeros((p.rows_max, p.d), dtype=dt, device=dev), torch.empty_like(w1),
+                   torch.empty_like(w3), torch.empty_like(w2))
     dx, dw1, dw3, dw2 = out
     for t, shape, name in ((dx, (p.rows_max, p.d), "dx_packed"), (dw1, (p.n_local, p.d, p.f), "dw1"),
                            (dw3, (p.n_local, p.d, p.f), "dw3"), (dw2, (p.n_local, p.f, p.d), "dw2")):
         if t is not None:
             _need(t, shape, dt, name)
-    ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_BACKWARD, dev)
+    ws = workspace
+    if ws is None:
+        with _alloc_on(stream):
+            ws = alloc_workspace(p, MOE_CALL_EXPERT_GEMM_BACKWARD, dev)
     _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (w3, "w3"), (w2, "w2"), (g, "g"),
           (u, "u"), (h, "h"), (dy_packed, "dy_packed"), (dx, "dx_packed"), (dw1, "dw1"), (dw3, "dw3"),
           (dw2, "dw2"), (ws, "workspace"))
@@ -471,8 +487,9 @@ def combine_backward(p: Spec, dy, y_packed, inv, topk_w, stream=None, out=None,
     if topk_w is not None:
         _need(topk_w, (p.T, p.k), torch.float32, "topk_w")
     if out is None:
-        out = (torch.zeros((n, p.d), dtype=dt, device=dy.device),
-               torch.empty((p.T, p.k), dtype=torch.float32, device=dy.device))
+        with _alloc_on(stream):
+            out = (torch.zeros((n, p.d), dtype=dt, device=dy.device),
+                   torch.empty((p.T, p.k), dtype=torch.float32, device=dy.device))
     dyp, dw = out
     _need(dyp, (n, p.d), dt, "dy_packed")
     if dw is not None:
@@ -504,8 +521,11 @@ def quantize_rows(x, stream=None, out=None):
     code = _dtype_code(x, "x")
     rows, K = x.shape
     _need(x, (rows, K), x.dtype, "x")
-    q, s = out if out is not None else (torch.empty((rows, K), dtype=torch.int8, device=x.device),
-                                        torch.empty(rows, dtype=torch.float32, device=x.device))
+    if out is None:
+        with _alloc_on(stream):
+            out = (torch.empty((rows, K), dtype=torch.int8, device=x.device),
+                   torch.empty(rows, dtype=torch.float32, device=x.device))
+    q, s = out
     _need(q, (rows, K), torch.int8, "q")
     _need(s, (rows,), torch.float32, "scale")
     _here((x, "x"), (q, "q"), (s, "scale"))
@@ -525,7 +545,7 @@ def packed_weights_bytes(n: int, K: int, N: int) -> int:
     return b
 
 
-def _packed_out(w, out):
+def _packed_out(w, out, stream):
     torch = _torch()
     lead, K, N = tuple(w.shape[:-2]), w.shape[-2], w.shape[-1]
     if len(lead) > 1:
@@ -533,14 +553,16 @@ def _packed_out(w, out):
     n = lead[0] if lead else 1
     packed_weights_bytes(n, K, N)
     shape = lead + packed_weights_shape(K, N)
-    packed = torch.empty(shape, dtype=torch.int8, device=w.device) if out is None else out
-    return n, K, N, lead, _need(packed, shape, torch.int8, "packed")
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(shape, dtype=torch.int8, device=w.device)
+    return n, K, N, lead, _need(out, shape, torch.int8, "packed")
 
 
 def pack_weights(w, stream=None, out=None):
     """int8 weights [n, K, N] or [K, N] in the order the 8-bit products read."""
     torch = _torch()
-    n, K, N, _, packed = _packed_out(w, out)
+    n, K, N, _, packed = _packed_out(w, out, stream)
     _need(w, w.shape, torch.int8, "w")
     _here((w, "w"), (packed, "packed"))
     _check(lib().moe_pack_weights(n, K, N, _ptr(w), _ptr(packed), _stream(stream)))
@@ -552,9 +574,10 @@ def quantize_weights(w, stream=None, out=None):
     per output channel."""
     torch = _torch()
     code = _dtype_code(w, "w")
-    n, K, N, lead, packed = _packed_out(w, None if out is None else out[0])
+    n, K, N, lead, packed = _packed_out(w, None if out is None else out[0], stream)
     _need(w, w.shape, w.dtype, "w")
-    s = torch.empty(lead + (N,), dtype=torch.float32, device=w.device) if out is None else out[1]
+    with _alloc_on(stream):
+        s = torch.empty(lead + (N,), dtype=torch.float32, device=w.device) if out is None else out[1]
     _need(s, lead + (N,), torch.float32, "scale")
     _here((w, "w"), (packed, "packed"), (s, "scale"))
     _check(lib().moe_quantize_weights(n, K, N, code, _ptr(w), _ptr(packed), _ptr(s), _stream(stream)))
@@ -573,7 +596,8 @@ def gemm_quantized(a, a_scale, packed, b_scale, dtype=None, stream=None, out=Non
     _need(packed, packed_weights_shape(K, N), torch.int8, "packed")
     _need(b_scale, (N,), torch.float32, "b_scale")
     if out is None:
-        out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
+        with _alloc_on(stream):
+            out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
     _need(out, (M, N), dtype or out.dtype, "out")
     _here((a, "a"), (a_scale, "a_scale"), (packed, "packed"), (b_scale, "b_scale"), (out, "out"))
     _check(lib().moe_gemm_quantized(M, N, K, _ptr(a), _ptr(a_scale), _ptr(packed), _ptr(b_scale),
@@ -594,12 +618,16 @@ def expert_gemm_quantized(p: Spec, x_packed, offsets, w1, s1, w3, s3, w2, s2, wo
         _need(s, (p.n_local, N), torch.float32, "s" + name)
     dev = x_packed.device
     if out is None:
-        out = (torch.zeros((p.rows_max, p.f), dtype=dt, device=dev),
-               torch.zeros((p.rows_max, p.d), dtype=dt, device=dev))
+        with _alloc_on(stream):
+            out = (torch.zeros((p.rows_max, p.f), dtype=dt, device=dev),
+                   torch.zeros((p.rows_max, p.d), dtype=dt, device=dev))
     h, yp = out
     _need(h, (p.rows_max, p.f), dt, "h")
     _need(yp, (p.rows_max, p.d), dt, "y_packed")
-    ws = workspace if workspace is not None else alloc_workspace(p, MOE_CALL_EXPERT_GEMM_QUANTIZED, dev)
+    ws = workspace
+    if ws is None:
+        with _alloc_on(stream):
+            ws = alloc_workspace(p, MOE_CALL_EXPERT_GEMM_QUANTIZED, dev)
     _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (s1, "s1"), (w3, "w3"), (s3, "s3"),
           (w2, "w2"), (s2, "s2"), (h, "h"), (yp, "y_packed"), (ws, "workspace"))
     pc = p.c()

@@ -32,13 +32,20 @@ namespace moe {
 // ---------------------------------------------------------------------------
 // Factor of a row or channel with maximum `top`: 127 (1 / top), each operation
 // rounded to fp32.  Below 2^-119 the factor would leave the fp32 range: such a
-// row counts as zeros.
+// row counts as zeros.  A row with an infinity or a NaN has the factor 0 and that
+// value as its scale: every product with it is then NaN instead of a plausible
+// number.
 constexpr float Q_TINY = 0x1p-119f;
 __device__ __forceinline__ float quant_factor(float top) { return top >= Q_TINY ? 127.0f * (1.0f / top) : 0.f; }
-__device__ __forceinline__ float quant_scale(float top) { return top >= Q_TINY ? top / 127.0f : 0.f; }
+__device__ __forceinline__ float quant_scale(float top) { return top < Q_TINY ? 0.f : top / 127.0f; }
+
+// max |v| by the bits, which order magnitudes as integers with NaN above infinity
+// (a float maximum would drop a NaN).
+__device__ __forceinline__ uint32_t top_of(uint32_t top, float v) { return max(top, __float_as_uint(v) & 0x7FFFFFFFu); }
 
 // Four values q = rint(v inv) in the bytes of a word (|v inv| <= 127 up to one
-// rounding, so the result fits int8).
+// rounding, so the result fits int8; the conversion takes NaN, 0 times an infinity,
+// to 0).
 __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float inv) {
   const uint32_t q0 = (uint32_t)(int)rintf(a * inv) & 255u, q1 = (uint32_t)(int)rintf(b * inv) & 255u;
   const uint32_t q2 = (uint32_t)(int)rintf(c * inv) & 255u, q3 = (uint32_t)(int)rintf(d * inv) & 255u;
@@ -79,14 +86,14 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int K,
                                                             int64_t ldq, int8_t* __restrict__ q,
                                                             float* __restrict__ s, const int32_t* __restrict__ limit) {
-  __shared__ float part[2][4];
+  __shared__ uint32_t part[2][4];
   const int nv = K / 8;
   if (limit) rows = min(rows, (int64_t)*limit);
   int flip = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
     const char* src = reinterpret_cast<const char*>(x) + row * K * (BF16 ? 2 : 4);
     F8 keep[QR_U];
-    float top = 0.f;
+    uint32_t bits = 0;
 #pragma unroll
     for (int u = 0; u < QR_U; ++u) {
       const int v = threadIdx.x + 256 * u;
@@ -96,17 +103,17 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restri
     for (int u = 0; u < QR_U; ++u)
       if ((int)threadIdx.x + 256 * u < nv)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(keep[u].v[j]));
+        for (int j = 0; j < 8; ++j) bits = top_of(bits, keep[u].v[j]);
     for (int v = threadIdx.x + 256 * QR_U; v < nv; v += 256) {
       const F8 o = load8<BF16>(src, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(o.v[j]));
+      for (int j = 0; j < 8; ++j) bits = top_of(bits, o.v[j]);
     }
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    if ((threadIdx.x & 63) == 0) part[flip][threadIdx.x >> 6] = top;
+    for (int off = 32; off > 0; off >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, off));
+    if ((threadIdx.x & 63) == 0) part[flip][threadIdx.x >> 6] = bits;
     __syncthreads();   // alternating halves: the next row's writes meet no reader of this one
-    top = fmaxf(fmaxf(part[flip][0], part[flip][1]), fmaxf(part[flip][2], part[flip][3]));
+    const float top = __uint_as_float(max(max(part[flip][0], part[flip][1]), max(part[flip][2], part[flip][3])));
     const float inv = quant_factor(top);
     if (threadIdx.x == 0) s[row] = quant_scale(top);
     u32x2* dst = reinterpret_cast<u32x2*>(q + row * ldq);
@@ -133,17 +140,17 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
 template <bool BF16>
 __global__ __launch_bounds__(256) void channel_max_kernel(const void* __restrict__ w, int K, int N,
                                                             float* __restrict__ s) {
-  __shared__ float part[4][64];
+  __shared__ uint32_t part[4][64];
   const int col = blockIdx.x * 64 + (threadIdx.x & 63), grp = threadIdx.x >> 6;
   const int64_t base = (int64_t)blockIdx.y * K * N;
-  float top = 0.f;
+  uint32_t top = 0;
   if (col < N)
-    for (int k = grp; k < K; k += 4) top = fmaxf(top, fabsf(load1<BF16>(w, base + (int64_t)k * N + col)));
+    for (int k = grp; k < K; k += 4) top = top_of(top, load1<BF16>(w, base + (int64_t)k * N + col));
   part[grp][threadIdx.x & 63] = top;
   __syncthreads();
   if (grp == 0 && col < N) {
-    top = fmaxf(fmaxf(part[0][threadIdx.x], part[1][threadIdx.x]), fmaxf(part[2][threadIdx.x], part[3][threadIdx.x]));
-    s[(int64_t)blockIdx.y * N + col] = top;
+    top = max(max(part[0][threadIdx.x], part[1][threadIdx.x]), max(part[2][threadIdx.x], part[3][threadIdx.x]));
+    s[(int64_t)blockIdx.y * N + col] = __uint_as_float(top);
   }
 }
 

@@ -165,8 +165,7 @@ moe_status_t check_signal_shape(int32_t M, int32_t N, int32_t K) {
   return MOE_OK;
 }
 
-// The training calls address up to 256 rows of d or f elements, and a 2 GiB
-// run of rows in steps of 32, with 32-bit offsets.
+// The training calls address up to 256 rows of d or f elements with 32-bit offsets.
 moe_status_t check_training_widths(const moe::Prob& q) {
   const int32_t lim = 1 << 20;
   if (q.d > lim || q.f > lim)
@@ -177,6 +176,8 @@ moe_status_t check_training_widths(const moe::Prob& q) {
 // Widths of the 8-bit products: K below 131072 keeps every int32 sum exact
 // (131071 products of at most 128 * 128).
 constexpr int32_t kMaxQuantK = 131072;
+// 256 output rows of N fp32 values are addressed with 32-bit offsets.
+constexpr int32_t kMaxQuantN = 1 << 21;
 
 moe_status_t check_packed(int32_t n, int32_t K, int32_t N) {
   if (n <= 0 || K <= 0 || N <= 0)
@@ -184,6 +185,7 @@ moe_status_t check_packed(int32_t n, int32_t K, int32_t N) {
   if (n > 1024) return fail(MOE_ERR_UNSUPPORTED, "n=%d > 1024 not supported", n);
   if (K >= kMaxQuantK) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be below %d", K, kMaxQuantK);
   if (N % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "N=%d must be a multiple of 8", N);
+  if (N > kMaxQuantN) return fail(MOE_ERR_UNSUPPORTED, "N=%d must be at most %d", N, kMaxQuantN);
   if ((int64_t)K * N >= ((int64_t)1 << 31))
     return fail(MOE_ERR_UNSUPPORTED, "a weight matrix exceeds 2 GiB (K=%d N=%d)", K, N);
   return MOE_OK;
@@ -568,6 +570,8 @@ moe_status_t moe_gemm_quantized(int32_t M, int32_t N, int32_t K, const int8_t* A
   if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M=%d must be >= 0", M);
   if ((st = check_packed(1, K, N)) != MOE_OK) return st;
   if (K % 16 != 0) return fail(MOE_ERR_UNSUPPORTED, "K=%d must be a multiple of 16", K);
+  if (M > 1 << 30)   // row blocks are counted in 32 bits
+    return fail(MOE_ERR_UNSUPPORTED, "M=%d must be at most %d", M, 1 << 30);
   if ((st = check_dtype(out_dtype)) != MOE_OK) return st;
   NEED_PTR(packed);
   NEED_PTR(b_scale);

@@ -316,7 +316,7 @@ moe_status_t moe_expert_gemm_backward(const moe_problem_t* p, const void* x_pack
  *   dy_packed[p] = rnd(topk_w[a] * dy[t]),  dtopk_w[a] = sum_i dy[t,i] y_packed[p,i]
  * and dtopk_w[a] = 0 where inv[a] < 0.  Rows of dy_packed that inv does not
  * name are left untouched; the entries of inv must be distinct where not
- * negative.  topk_w = NULL: unit weights.
+ * negative.  topk_w = NULL: unit weights.  Outputs must not overlap inputs.
  *   dy       [T,d] dtype;  y_packed as moe_combine read it (may be NULL with dtopk_w NULL)
  *   dy_packed      dtype output, as many rows as y_packed
  *   dtopk_w  [T,k] fp32 output, or NULL
@@ -329,7 +329,8 @@ moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dy, const 
  * Rows to 8 bits, one scale each: with m = max_k |x[r,k]|
  *   scale[r] = m / 127,  q[r,k] = rint(x[r,k] * (127 * (1 / m)))   (ties to even)
  * in fp32 arithmetic, each operation rounded; a row with m < 2^-119 (zeros
- * among them) gets scale 0 and zeros.
+ * among them) gets scale 0 and zeros, one with an infinity or a NaN that as its
+ * scale and zeros (so that every product with it is NaN).
  *   x [rows,K] of dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32;  q [rows,K] int8
  * K a multiple of 8, x 16-byte and q 8-byte aligned; rows >= 0.
  */
@@ -345,7 +346,8 @@ moe_status_t moe_quantize_rows(int64_t rows, int32_t K, int32_t dtype, const voi
  * moe_pack_weights:      packs int8 w [n,K,N].
  * moe_quantize_weights:  quantises w [n,K,N] of `dtype` per output channel
  *   (scale[e,j] = max_k |w[e,k,j]| / 127, values as moe_quantize_rows) and packs.
- * n 1..1024, K < 131072, N a multiple of 8; packed 16-byte aligned.
+ * n 1..1024, K < 131072, N a multiple of 8 and at most 2^21; packed 16-byte
+ * aligned.
  */
 size_t moe_packed_weights_bytes(int32_t n, int32_t K, int32_t N);
 moe_status_t moe_pack_weights(int32_t n, int32_t K, int32_t N, const int8_t* w, void* packed,
@@ -360,7 +362,7 @@ moe_status_t moe_quantize_weights(int32_t n, int32_t K, int32_t N, int32_t dtype
  * (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
  *   A [M,K] int8 row-major, K a multiple of 16;  packed: one matrix [K,N] of
  *   moe_pack_weights or moe_quantize_weights;  C [M,N], N a multiple of 8.
- * A, packed, b_scale and C 16-byte aligned.  M = 0 launches nothing.
+ * A, packed, b_scale and C 16-byte aligned.  M = 0 launches nothing; M at most 2^30.
  */
 moe_status_t moe_gemm_quantized(int32_t M, int32_t N, int32_t K, const int8_t* A,
                                 const float* a_scale, const void* packed, const float* b_scale,

@@ -126,7 +126,7 @@ def test_packed_weights_arguments():
     L = M.lib()
     assert L.moe_packed_weights_bytes(1, 64, 16) == 1024
     assert L.moe_packed_weights_bytes(3, 65, 24) == 3 * 2 * 2 * 1024
-    for n, K, N in ((0, 64, 16), (1, 0, 16), (1, 64, 0), (1025, 64, 16), (1, 131072, 16), (1, 64, 12), (1, 131064, 16392)):
+    for n, K, N in ((0, 64, 16), (1, 0, 16), (1, 64, 0), (1025, 64, 16), (1, 131072, 16), (1, 64, 12), (1, 131064, 16392), (1, 8, (1 << 21) + 8)):
         assert L.moe_packed_weights_bytes(n, K, N) == 0 and L.moe_last_error()
         assert L.moe_pack_weights(n, K, N, FAKE, FAKE, None) in (INV, UNS)
         assert L.moe_quantize_weights(n, K, N, M.MOE_DTYPE_BF16, FAKE, FAKE, FAKE, None) in (INV, UNS)
@@ -141,7 +141,7 @@ def test_gemm_quantized_arguments():
     def g(Mr=4, N=16, K=64, a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, c=FAKE, dt=M.MOE_DTYPE_BF16):
         return M.lib().moe_gemm_quantized(Mr, N, K, a, sa, b, sb, c, dt, None)
     assert g(Mr=-1) == INV and g(N=0) == INV and g(K=0) == INV
-    assert g(K=24) == UNS and g(N=12) == UNS and g(K=131072) == UNS and g(dt=9) == UNS
+    assert g(Mr=(1 << 30) + 1) == UNS and g(N=(1 << 21) + 8) == UNS and g(K=24) == UNS and g(N=12) == UNS and g(K=131072) == UNS and g(dt=9) == UNS
     for name in ("a", "sa", "b", "sb", "c"):
         assert g(**{name: None}) == INV, name
     for name in ("a", "b", "sb", "c"):

@@ -200,3 +200,111 @@ def test_quantized_captured():
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, out))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [272, 8208])
+def test_not_finite_rows_and_channels(dtype, K):
+    """A row or channel with an infinity or a NaN: that as its scale and zeros, and
+    NaN in every product with it; its neighbours as without it."""
+    r = Rows(spec([6], 8, 8, "bf16"), [6], seed=K)
+    x = torch.randn((6, K), generator=r.gen).to(dtype)
+    rq, rs = _quant(x.float().numpy())
+    x[1, 3], x[2, K - 1], x[4, 0], x[4, 7] = float("nan"), float("-inf"), float("inf"), float("nan")
+    q, s = M.quantize_rows(x.cuda())
+    q, s = q.cpu(), s.cpu()
+    assert bool(torch.isnan(s[[1, 4]]).all()) and float(s[2]) == float("inf") and not bool(q[[1, 2, 4]].any())
+    for row in (0, 3, 5):
+        assert np.array_equal(q[row].numpy(), rq[row]) and float(s[row]) == float(rs[row])
+    w = torch.randn((K, 24), generator=r.gen).to(dtype)
+    packed, sw = M.quantize_weights(w.cuda())
+    bad = w.clone()
+    bad[5, 2], bad[K - 1, 17] = float("nan"), float("inf")
+    bad_packed, bad_sw = M.quantize_weights(bad.cuda())
+    a, sa = M.quantize_rows(x[[0, 3, 5]].contiguous().cuda())
+    one, two = M.gemm_quantized(a, sa, packed, sw), M.gemm_quantized(a, sa, bad_packed, bad_sw)
+    keep = [c for c in range(24) if c not in (2, 17)]
+    assert torch.equal(one[:, keep], two[:, keep]) and bool(torch.isnan(two[:, [2, 17]]).all())
+    assert torch.isnan(bad_sw[2]) and torch.isinf(bad_sw[17])
+
+
+def _experts(counts, d, f, seed, **kw):
+    p = spec(counts, d, f, "bf16", **kw)
+    r = Rows(p, counts, seed=seed)
+    w = [t for s in ((d, f), (d, f), (f, d)) for t in M.quantize_weights(r.dev(r.draw(len(counts), *s, scale=s[0] ** -0.5)))]
+    return p, r, w, r.draw(r.A, d), offsets_of(counts)
+
+
+@pytest.mark.parametrize("name", ["streams", "mixed", "tiles"])
+def test_expert_rows_that_are_not_finite(name):
+    """They give NaN rows and leave every other row as it was."""
+    counts, d, f, kw = CASES[name]
+    p, r, w, x, off = _experts(counts, d, f, 11, **kw)
+    ref = M.expert_gemm_quantized(p, r.packed(x), off, *w)
+    xd = r.packed(x)
+    hit = [0, r.A // 2, r.A - 1]
+    xd[hit[0], 1], xd[hit[1], 0], xd[hit[2], d - 1] = float("nan"), float("inf"), float("-inf")
+    got = M.expert_gemm_quantized(p, xd, off, *w)
+    torch.cuda.synchronize()
+    rest = [i for i in range(r.A) if i not in hit]
+    for a, b in zip(ref, got):
+        assert torch.equal(a[rest], b[rest]) and bool(torch.isnan(b[hit]).all())
+
+
+def test_quantized_on_a_given_stream_and_two_at_once():
+    jobs = []
+    for seed, (counts, d, f, kw) in enumerate((CASES["mixed"], CASES["tiles"])):
+        p, r, w, x, off = _experts(counts, d, f, seed, **kw)
+        args = (r.packed(x), off, *w)
+        jobs.append((p, args, M.expert_gemm_quantized(p, *args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for p, args, ref, s in jobs:
+        with torch.cuda.stream(s):   # still busy when the calls return
+            a = torch.ones((4096, 4096), device="cuda")
+            for _ in range(8):
+                a = a @ a * 1e-4
+    got = [M.expert_gemm_quantized(p, *args, stream=s) for p, args, _, s in jobs]
+    rows = [M.quantize_rows(args[0], stream=s) for _, args, _, s in jobs]
+    spoil = [torch.full((M.workspace_bytes(p, M.MOE_CALL_EXPERT_GEMM_QUANTIZED),), 0x7F, dtype=torch.uint8, device="cuda")
+             for p, *_ in jobs for _ in range(3)]
+    torch.cuda.synchronize()
+    del spoil
+    for (p, args, ref, _), out, (q, sc) in zip(jobs, got, rows):
+        assert all(torch.equal(a, b) for a, b in zip(ref, out))
+        rq, rs = M.quantize_rows(args[0])
+        assert torch.equal(q, rq) and torch.equal(sc.view(torch.int32), rs.view(torch.int32))
+
+
+def test_offsets_beyond_32_bits():
+    """Rows more than 4 GiB into their buffers: the sums are exact, so they equal
+    the same rows in a small call bit by bit."""
+    K, N, rows = 8192, 4104, 530_000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    some = torch.randn((70, K), generator=g, device="cuda").bfloat16()
+    x = some[:1].repeat(rows, 1)
+    x[-70:] = some
+    q, s = M.quantize_rows(x)
+    del x
+    q1, s1 = M.quantize_rows(some)
+    assert torch.equal(q[-70:], q1) and torch.equal(s[-70:], s1) and q.numel() > 2 ** 32
+    packed, sw = M.quantize_weights(torch.randn((K, N), generator=g, device="cuda").bfloat16())
+    c = M.gemm_quantized(q, s, packed, sw)
+    assert torch.equal(c[-70:], M.gemm_quantized(q1, s1, packed, sw)) and torch.equal(c[0], c[rows // 2])
+
+
+def test_experts_beyond_32_bits():
+    d, f, counts = 8192, 40, [299_950, 0, 10]
+    p = spec(counts, d, f, "bf16", k=2)
+    few = Rows(spec([50, 0, 10], d, f, "bf16"), [50, 0, 10], seed=8)
+    w = [t for s in ((d, f), (d, f), (f, d)) for t in M.quantize_weights(few.dev(few.draw(3, *s, scale=s[0] ** -0.5)))]
+    x = few.packed(few.draw(60, d))
+    ref = M.expert_gemm_quantized(few.p, x, offsets_of([50, 0, 10]), *w)
+    A = sum(counts)
+    big = torch.ones((p.rows_max, d), dtype=torch.bfloat16, device="cuda")
+    big[A - 60 : A] = x[:60]
+    big[A:] = float("nan")
+    out = tuple(torch.full((p.rows_max, n), -77.0, dtype=torch.bfloat16, device="cuda") for n in (f, d))
+    M.expert_gemm_quantized(p, big, offsets_of(counts), *w, out=out)
+    torch.cuda.synchronize()
+    for a, b in zip(ref, out):
+        assert torch.equal(a[:60], b[A - 60 : A]) and bool((b[A:] == -77.0).all())
