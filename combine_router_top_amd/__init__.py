@@ -153,13 +153,19 @@ class Spec:
         return self.T * min(self.k, self.n_local)
 
     def c(self) -> Problem:
-        """The C structure (made once: the fields of a Spec do not change)."""
-        pc = self.__dict__.get("_c")
-        if pc is None:
-            pc = Problem(self.T, self.d, self.E, self.k, self.f, self.expert_lo, self.n_local,
-                         MOE_DTYPE_BF16 if self.dtype == "bf16" else MOE_DTYPE_F32, self.flags)
-            object.__setattr__(self, "_c", pc)
-        return pc
+        return Problem(self.T, self.d, self.E, self.k, self.f, self.expert_lo, self.n_local,
+                       MOE_DTYPE_BF16 if self.dtype == "bf16" else MOE_DTYPE_F32, self.flags)
+
+    def ref(self):
+        """The C structure by reference, made once: the fields of a Spec do not change."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
+
+    def __reduce__(self):   # copies and pickles without the reference
+        return Spec, (self.T, self.d, self.E, self.k, self.f, self.expert_lo, self.n_local, self.dtype, self.flags)
 
     @staticmethod
     def of(w, flags: int = 0) -> "Spec":
@@ -168,8 +174,7 @@ class Spec:
 
 
 def workspace_bytes(p: Spec, call: int = MOE_CALL_LAYER) -> int:
-    pc = p.c()
-    n = lib().moe_workspace_bytes(ctypes.byref(pc), call)
+    n = lib().moe_workspace_bytes(p.ref(), call)
     if n == 0 and lib().moe_last_error():
         raise MoeError(MOE_ERR_INVALID_ARG, lib().moe_last_error().decode())
     return int(n)
@@ -217,13 +222,42 @@ def _need(t, shape, dtype, name):
     return t
 
 
-def _here(*named):
-    """Refuses tensors of another device than the current one, on whose stream
-    the call would run: (tensor or None, name) pairs."""
-    cur = _torch()._C._cuda_getDevice()
-    for t, name in named:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"{name} is on device {t.get_device()}, the current device is {cur}")
+def _current() -> int:
+    """The current device; without any, a number that no tensor has."""
+    try:
+        return _torch()._C._cuda_getDevice()
+    except RuntimeError:
+        return -2
+
+
+def _at(cur, t, shape, dtype, name) -> int:
+    """Address of a tensor that ``_need`` accepts and that lies on the current
+    device ``cur``, on whose stream the call runs."""
+    if t is not None and t.get_device() == cur and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, shape, dtype, name)
+    raise ValueError(f"{name} is on device {t.get_device()}, the current device is {cur}")
+
+
+def _stream_at(cur, stream) -> int:
+    if stream is None:
+        # what torch.cuda.current_stream().cuda_stream gives, without the Stream object
+        return _torch()._C._cuda_getCurrentRawStream(cur)
+    if stream.device_index != cur:
+        raise ValueError(f"the stream is on device {stream.device_index}, the current device is {cur}")
+    return stream.cuda_stream
+
+
+def _workspace_at(cur, p, call, workspace, stream):
+    """(tensor, address, bytes) of the given workspace or of a new one."""
+    if workspace is None:
+        with _alloc_on(stream):
+            workspace = alloc_workspace(p, call, f"cuda:{cur}")
+        if workspace is None:
+            return None, None, 0
+    if workspace.get_device() != cur:
+        raise ValueError(f"workspace is on device {workspace.get_device()}, the current device is {cur}")
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 _here_and_now = contextlib.nullcontext()
@@ -414,25 +448,17 @@ def expert_gemm_train(p: Spec, x_packed, offsets, w1, w3, w2, stream=None, out=N
     """``expert_gemm`` that also returns the unactivated products the backward
     pass reads: (g, u, h, y_packed).  ``out``: these four, written in place."""
     torch = _torch()
-    dt = _dt(p)
-    _need(x_packed, (p.rows_max, p.d), dt, "x_packed")
-    _need(offsets, (p.n_local + 1,), torch.int32, "offsets")
-    _need(w1, (p.n_local, p.d, p.f), dt, "w1")
-    _need(w3, (p.n_local, p.d, p.f), dt, "w3")
-    _need(w2, (p.n_local, p.f, p.d), dt, "w2")
-    dev = x_packed.device
+    dt, cur, rows = _dt(p), _current(), p.rows_max
+    wide, tall, up = (rows, p.d), (rows, p.f), (p.n_local, p.d, p.f)
+    ins = (_at(cur, x_packed, wide, dt, "x_packed"), _at(cur, offsets, (p.n_local + 1,), torch.int32, "offsets"),
+           _at(cur, w1, up, dt, "w1"), _at(cur, w3, up, dt, "w3"), _at(cur, w2, (p.n_local, p.f, p.d), dt, "w2"))
     if out is None:
         with _alloc_on(stream):
-            out = tuple(torch.zeros((p.rows_max, n), dtype=dt, device=dev) for n in (p.f, p.f, p.f, p.d))
+            out = tuple(torch.zeros(n, dtype=dt, device=x_packed.device) for n in (tall, tall, tall, wide))
     g, u, h, yp = out
-    for t, n, name in ((g, p.f, "g"), (u, p.f, "u"), (h, p.f, "h"), (yp, p.d, "y_packed")):
-        _need(t, (p.rows_max, n), dt, name)
-    _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (w3, "w3"), (w2, "w2"), (g, "g"),
-          (u, "u"), (h, "h"), (yp, "y_packed"))
-    pc = p.c()
-    _check(lib().moe_expert_gemm_train(ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1),
-                                       _ptr(w3), _ptr(w2), _ptr(g), _ptr(u), _ptr(h), _ptr(yp),
-                                       _stream(stream)))
+    _check(lib().moe_expert_gemm_train(p.ref(), *ins, _at(cur, g, tall, dt, "g"), _at(cur, u, tall, dt, "u"),
+                                       _at(cur, h, tall, dt, "h"), _at(cur, yp, wide, dt, "y_packed"),
+                                       _stream_at(cur, stream)))
     return g, u, h, yp
 
 
@@ -441,36 +467,23 @@ def expert_gemm_backward(p: Spec, x_packed, offsets, w1, w3, w2, g, u, h, dy_pac
     """Gradients (dx_packed, dw1, dw3, dw2) of ``expert_gemm_train``.  ``out``:
     these four, written in place; a None among them is not computed."""
     torch = _torch()
-    dt = _dt(p)
-    for t, n, name in ((x_packed, p.d, "x_packed"), (g, p.f, "g"), (u, p.f, "u"), (h, p.f, "h"),
-                       (dy_packed, p.d, "dy_packed")):
-        _need(t, (p.rows_max, n), dt, name)
-    _need(offsets, (p.n_local + 1,), torch.int32, "offsets")
-    _need(w1, (p.n_local, p.d, p.f), dt, "w1")
-    _need(w3, (p.n_local, p.d, p.f), dt, "w3")
-    _need(w2, (p.n_local, p.f, p.d), dt, "w2")
-    dev = x_packed.device
+    dt, cur, rows = _dt(p), _current(), p.rows_max
+    wide, tall, up, down = (rows, p.d), (rows, p.f), (p.n_local, p.d, p.f), (p.n_local, p.f, p.d)
+    ins = (_at(cur, x_packed, wide, dt, "x_packed"), _at(cur, offsets, (p.n_local + 1,), torch.int32, "offsets"),
+           _at(cur, w1, up, dt, "w1"), _at(cur, w3, up, dt, "w3"), _at(cur, w2, down, dt, "w2"),
+           _at(cur, g, tall, dt, "g"), _at(cur, u, tall, dt, "u"), _at(cur, h, tall, dt, "h"),
+           _at(cur, dy_packed, wide, dt, "dy_packed"))
     if out is None:
         with _alloc_on(stream):
-            out = (torch.zeros((p.rows_max, p.d), dtype=dt, device=dev), torch.empty_like(w1),
+            out = (torch.zeros(wide, dtype=dt, device=x_packed.device), torch.empty_like(w1),
                    torch.empty_like(w3), torch.empty_like(w2))
     dx, dw1, dw3, dw2 = out
-    for t, shape, name in ((dx, (p.rows_max, p.d), "dx_packed"), (dw1, (p.n_local, p.d, p.f), "dw1"),
-                           (dw3, (p.n_local, p.d, p.f), "dw3"), (dw2, (p.n_local, p.f, p.d), "dw2")):
-        if t is not None:
-            _need(t, shape, dt, name)
-    ws = workspace
-    if ws is None:
-        with _alloc_on(stream):
-            ws = alloc_workspace(p, MOE_CALL_EXPERT_GEMM_BACKWARD, dev)
-    _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (w3, "w3"), (w2, "w2"), (g, "g"),
-          (u, "u"), (h, "h"), (dy_packed, "dy_packed"), (dx, "dx_packed"), (dw1, "dw1"), (dw3, "dw3"),
-          (dw2, "dw2"), (ws, "workspace"))
-    pc = p.c()
-    _check(lib().moe_expert_gemm_backward(
-        ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(g), _ptr(u),
-        _ptr(h), _ptr(dy_packed), _ptr(dx), _ptr(dw1), _ptr(dw3), _ptr(dw2), _ptr(ws),
-        0 if ws is None else ws.numel(), _stream(stream)))
+    outs = (None if dx is None else _at(cur, dx, wide, dt, "dx_packed"),
+            None if dw1 is None else _at(cur, dw1, up, dt, "dw1"),
+            None if dw3 is None else _at(cur, dw3, up, dt, "dw3"),
+            None if dw2 is None else _at(cur, dw2, down, dt, "dw2"))
+    ws, at, size = _workspace_at(cur, p, MOE_CALL_EXPERT_GEMM_BACKWARD, workspace, stream)
+    _check(lib().moe_expert_gemm_backward(p.ref(), *ins, *outs, at, size, _stream_at(cur, stream)))
     return dx, dw1, dw3, dw2
 
 
@@ -480,27 +493,20 @@ def combine_backward(p: Spec, dy, y_packed, inv, topk_w, stream=None, out=None,
     ``topk_w=None``: unit weights.  ``out``: the two, written in place; with
     dtopk_w None it is not computed and ``y_packed`` may be None."""
     torch = _torch()
-    dt = _dt(p)
-    n = p.rows_max if rows is None else rows
-    _need(dy, (p.T, p.d), dt, "dy")
-    _need(inv, (p.T * p.k,), torch.int32, "inv")
-    if topk_w is not None:
-        _need(topk_w, (p.T, p.k), torch.float32, "topk_w")
+    dt, cur = _dt(p), _current()
+    packed, slots = (p.rows_max if rows is None else rows, p.d), (p.T, p.k)
+    pdy = _at(cur, dy, (p.T, p.d), dt, "dy")
     if out is None:
         with _alloc_on(stream):
-            out = (torch.zeros((n, p.d), dtype=dt, device=dy.device),
-                   torch.empty((p.T, p.k), dtype=torch.float32, device=dy.device))
+            out = (torch.zeros(packed, dtype=dt, device=dy.device),
+                   torch.empty(slots, dtype=torch.float32, device=dy.device))
     dyp, dw = out
-    _need(dyp, (n, p.d), dt, "dy_packed")
-    if dw is not None:
-        _need(dw, (p.T, p.k), torch.float32, "dtopk_w")
-    if dw is not None or y_packed is not None:
-        _need(y_packed, (n, p.d), dt, "y_packed")
-    _here((dy, "dy"), (y_packed, "y_packed"), (inv, "inv"), (topk_w, "topk_w"), (dyp, "dy_packed"),
-          (dw, "dtopk_w"))
-    pc = p.c()
-    _check(lib().moe_combine_backward(ctypes.byref(pc), _ptr(dy), _ptr(y_packed), _ptr(inv),
-                                      _ptr(topk_w), _ptr(dyp), _ptr(dw), _stream(stream)))
+    _check(lib().moe_combine_backward(
+        p.ref(), pdy, None if dw is None and y_packed is None else _at(cur, y_packed, packed, dt, "y_packed"),
+        _at(cur, inv, (p.T * p.k,), torch.int32, "inv"),
+        None if topk_w is None else _at(cur, topk_w, slots, torch.float32, "topk_w"),
+        _at(cur, dyp, packed, dt, "dy_packed"),
+        None if dw is None else _at(cur, dw, slots, torch.float32, "dtopk_w"), _stream_at(cur, stream)))
     return dyp, dw
 
 
@@ -509,27 +515,27 @@ def combine_backward(p: Spec, dy, y_packed, inv, topk_w, stream=None, out=None,
 # ---------------------------------------------------------------------------
 def _dtype_code(t, name):
     torch = _torch()
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
-    return MOE_DTYPE_BF16 if t.dtype == torch.bfloat16 else MOE_DTYPE_F32
+    if t.dtype is torch.bfloat16:
+        return MOE_DTYPE_BF16
+    if t.dtype is torch.float32:
+        return MOE_DTYPE_F32
+    raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
 def quantize_rows(x, stream=None, out=None):
     """(q int8, scale fp32) of the rows of x [rows, K] (bf16 or fp32):
     scale = max|x| / 127, q = rint(x * (127 * (1 / max|x|)))."""
     torch = _torch()
-    code = _dtype_code(x, "x")
+    code, cur = _dtype_code(x, "x"), _current()
     rows, K = x.shape
-    _need(x, (rows, K), x.dtype, "x")
+    px = _at(cur, x, (rows, K), x.dtype, "x")
     if out is None:
         with _alloc_on(stream):
             out = (torch.empty((rows, K), dtype=torch.int8, device=x.device),
-                   torch.empty(rows, dtype=torch.float32, device=x.device))
+                   torch.empty((rows,), dtype=torch.float32, device=x.device))
     q, s = out
-    _need(q, (rows, K), torch.int8, "q")
-    _need(s, (rows,), torch.float32, "scale")
-    _here((x, "x"), (q, "q"), (s, "scale"))
-    _check(lib().moe_quantize_rows(rows, K, code, _ptr(x), _ptr(q), _ptr(s), _stream(stream)))
+    _check(lib().moe_quantize_rows(rows, K, code, px, _at(cur, q, (rows, K), torch.int8, "q"),
+                                   _at(cur, s, (rows,), torch.float32, "scale"), _stream_at(cur, stream)))
     return q, s
 
 
@@ -552,20 +558,20 @@ def _packed_out(w, out, stream):
         raise ValueError(f"w: expected [n, K, N] or [K, N], got {tuple(w.shape)}")
     n = lead[0] if lead else 1
     packed_weights_bytes(n, K, N)
-    shape = lead + packed_weights_shape(K, N)
     if out is None:
         with _alloc_on(stream):
-            out = torch.empty(shape, dtype=torch.int8, device=w.device)
-    return n, K, N, lead, _need(out, shape, torch.int8, "packed")
+            out = torch.empty(lead + packed_weights_shape(K, N), dtype=torch.int8, device=w.device)
+    return n, K, N, lead, out
 
 
 def pack_weights(w, stream=None, out=None):
     """int8 weights [n, K, N] or [K, N] in the order the 8-bit products read."""
     torch = _torch()
-    n, K, N, _, packed = _packed_out(w, out, stream)
-    _need(w, w.shape, torch.int8, "w")
-    _here((w, "w"), (packed, "packed"))
-    _check(lib().moe_pack_weights(n, K, N, _ptr(w), _ptr(packed), _stream(stream)))
+    cur = _current()
+    n, K, N, lead, packed = _packed_out(w, out, stream)
+    _check(lib().moe_pack_weights(n, K, N, _at(cur, w, w.shape, torch.int8, "w"),
+                                  _at(cur, packed, lead + packed_weights_shape(K, N), torch.int8, "packed"),
+                                  _stream_at(cur, stream)))
     return packed
 
 
@@ -573,14 +579,14 @@ def quantize_weights(w, stream=None, out=None):
     """(packed, scale) of bf16 or fp32 weights [n, K, N] or [K, N], one scale
     per output channel."""
     torch = _torch()
-    code = _dtype_code(w, "w")
+    code, cur = _dtype_code(w, "w"), _current()
     n, K, N, lead, packed = _packed_out(w, None if out is None else out[0], stream)
-    _need(w, w.shape, w.dtype, "w")
+    pw = _at(cur, w, w.shape, w.dtype, "w")
     with _alloc_on(stream):
         s = torch.empty(lead + (N,), dtype=torch.float32, device=w.device) if out is None else out[1]
-    _need(s, lead + (N,), torch.float32, "scale")
-    _here((w, "w"), (packed, "packed"), (s, "scale"))
-    _check(lib().moe_quantize_weights(n, K, N, code, _ptr(w), _ptr(packed), _ptr(s), _stream(stream)))
+    _check(lib().moe_quantize_weights(
+        n, K, N, code, pw, _at(cur, packed, lead + packed_weights_shape(K, N), torch.int8, "packed"),
+        _at(cur, s, lead + (N,), torch.float32, "scale"), _stream_at(cur, stream)))
     return packed, s
 
 
@@ -589,19 +595,18 @@ def gemm_quantized(a, a_scale, packed, b_scale, dtype=None, stream=None, out=Non
     [K, N] matrix, a scale per row and per output channel; ``dtype`` (default
     torch.bfloat16, or that of ``out``) is C's."""
     torch = _torch()
+    cur = _current()
     M, K = a.shape
     N = b_scale.shape[0]
-    _need(a, (M, K), torch.int8, "a")
-    _need(a_scale, (M,), torch.float32, "a_scale")
-    _need(packed, packed_weights_shape(K, N), torch.int8, "packed")
-    _need(b_scale, (N,), torch.float32, "b_scale")
+    pa = _at(cur, a, (M, K), torch.int8, "a")
     if out is None:
         with _alloc_on(stream):
             out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
-    _need(out, (M, N), dtype or out.dtype, "out")
-    _here((a, "a"), (a_scale, "a_scale"), (packed, "packed"), (b_scale, "b_scale"), (out, "out"))
-    _check(lib().moe_gemm_quantized(M, N, K, _ptr(a), _ptr(a_scale), _ptr(packed), _ptr(b_scale),
-                                    _ptr(out), _dtype_code(out, "out"), _stream(stream)))
+    _check(lib().moe_gemm_quantized(
+        M, N, K, pa, _at(cur, a_scale, (M,), torch.float32, "a_scale"),
+        _at(cur, packed, packed_weights_shape(K, N), torch.int8, "packed"),
+        _at(cur, b_scale, (N,), torch.float32, "b_scale"), _at(cur, out, (M, N), dtype or out.dtype, "out"),
+        _dtype_code(out, "out"), _stream_at(cur, stream)))
     return out
 
 
@@ -610,31 +615,21 @@ def expert_gemm_quantized(p: Spec, x_packed, offsets, w1, s1, w3, s3, w2, s2, wo
     """``expert_gemm`` with packed 8-bit weights [n_local, ...] and their channel
     scales, and rows quantised on the way: (h, y_packed)."""
     torch = _torch()
-    dt = _dt(p)
-    _need(x_packed, (p.rows_max, p.d), dt, "x_packed")
-    _need(offsets, (p.n_local + 1,), torch.int32, "offsets")
-    for w, s, K, N, name in ((w1, s1, p.d, p.f, "1"), (w3, s3, p.d, p.f, "3"), (w2, s2, p.f, p.d, "2")):
-        _need(w, (p.n_local,) + packed_weights_shape(K, N), torch.int8, "w" + name)
-        _need(s, (p.n_local, N), torch.float32, "s" + name)
-    dev = x_packed.device
+    dt, cur, n = _dt(p), _current(), (p.n_local,)
+    wide, tall = (p.rows_max, p.d), (p.rows_max, p.f)
+    up, down = n + packed_weights_shape(p.d, p.f), n + packed_weights_shape(p.f, p.d)
+    f32, i8 = torch.float32, torch.int8
+    ins = (_at(cur, x_packed, wide, dt, "x_packed"), _at(cur, offsets, (p.n_local + 1,), torch.int32, "offsets"),
+           _at(cur, w1, up, i8, "w1"), _at(cur, s1, n + (p.f,), f32, "s1"),
+           _at(cur, w3, up, i8, "w3"), _at(cur, s3, n + (p.f,), f32, "s3"),
+           _at(cur, w2, down, i8, "w2"), _at(cur, s2, n + (p.d,), f32, "s2"))
     if out is None:
         with _alloc_on(stream):
-            out = (torch.zeros((p.rows_max, p.f), dtype=dt, device=dev),
-                   torch.zeros((p.rows_max, p.d), dtype=dt, device=dev))
+            out = tuple(torch.zeros(v, dtype=dt, device=x_packed.device) for v in (tall, wide))
     h, yp = out
-    _need(h, (p.rows_max, p.f), dt, "h")
-    _need(yp, (p.rows_max, p.d), dt, "y_packed")
-    ws = workspace
-    if ws is None:
-        with _alloc_on(stream):
-            ws = alloc_workspace(p, MOE_CALL_EXPERT_GEMM_QUANTIZED, dev)
-    _here((x_packed, "x_packed"), (offsets, "offsets"), (w1, "w1"), (s1, "s1"), (w3, "w3"), (s3, "s3"),
-          (w2, "w2"), (s2, "s2"), (h, "h"), (yp, "y_packed"), (ws, "workspace"))
-    pc = p.c()
-    _check(lib().moe_expert_gemm_quantized(
-        ctypes.byref(pc), _ptr(x_packed), _ptr(offsets), _ptr(w1), _ptr(s1), _ptr(w3), _ptr(s3),
-        _ptr(w2), _ptr(s2), _ptr(h), _ptr(yp), _ptr(ws), 0 if ws is None else ws.numel(),
-        _stream(stream)))
+    outs = (_at(cur, h, tall, dt, "h"), _at(cur, yp, wide, dt, "y_packed"))
+    ws, at, size = _workspace_at(cur, p, MOE_CALL_EXPERT_GEMM_QUANTIZED, workspace, stream)
+    _check(lib().moe_expert_gemm_quantized(p.ref(), *ins, *outs, at, size, _stream_at(cur, stream)))
     return h, yp
 
 

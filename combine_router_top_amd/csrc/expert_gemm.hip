@@ -637,8 +637,6 @@ static int big_cus() {
   return n;
 }
 
-int device_cus() { return big_cus(); }
-
 // the down projection's real workgroups per XCD (8 ints), written by GEMM-1
 size_t expert_gemm_ws_bytes(const Prob& p) { return p.dtype == 1 ? 256 : 0; }
 

@@ -22,6 +22,17 @@
 
 namespace moe {
 
+int device_cus() {
+  static const int n = [] {
+    int dev = 0, c = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || c <= 0)
+      c = 256;   // no device here: the part this is written for
+    return c;
+  }();
+  return n;
+}
+
 template <int MT>
 using UpCfg = StCfg<MT, ST_ROWS, ST_PANEL, f32x4, 1, true, 6 * MT, false, 256>;
 template <int MT>

@@ -82,7 +82,8 @@ hipError_t launch_combine(const Prob& p, const void* y_packed, const int32_t* in
 hipError_t launch_combine_backward(const Prob& p, const void* dy, const void* y_packed, const int32_t* inv,
                                    const float* w, void* dy_packed, float* dw, hipStream_t st);
 
-// Compute units of the current device, and the grid of a persistent kernel over
+// Compute units of the device (the first one asked about: one process drives one
+// kind), and the grid of a persistent kernel over
 // `tiles` tiles: a multiple of 8 (one share per XCD) of at most that many.
 int device_cus();
 inline unsigned st_grid(int64_t tiles) {

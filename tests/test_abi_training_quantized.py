@@ -170,3 +170,16 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         M.pack_weights(z(1, 1, 16, 16, dt=torch.int8))
     with pytest.raises(ValueError, match="a must be|a: expected"):
         M.gemm_quantized(z(2, 16, dt=torch.int8), z(2, dt=torch.float32), z(1, 1, 4, 16, 16, dt=torch.int8), z(8, dt=torch.float32))
+
+
+def test_a_used_problem_can_be_copied_and_pickled():
+    import copy
+    import pickle
+    p = M.Spec(4, 16, 2, 1, 8, 0, 2, "bf16", 0)
+    need = M.workspace_bytes(p, M.MOE_CALL_EXPERT_GEMM_BACKWARD)
+    for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+        assert q == p and M.workspace_bytes(q, M.MOE_CALL_EXPERT_GEMM_BACKWARD) == need
+    # the structure a caller gets is its own
+    c = p.c()
+    c.T = 400
+    assert p.c().T == 4 and M.workspace_bytes(p, M.MOE_CALL_EXPERT_GEMM_BACKWARD) == need

@@ -528,3 +528,17 @@ def test_combine_backward_beyond_32_bits():
         assert_within(dyp[rows.cuda()], ref, (HALF["bf16"] + 2.0 ** -23) * ref.abs(), "dy_packed")
         each = dy[t].cpu().double() * yp[:8].flip(0).cpu().double()
         assert_within(dw[t], each.sum(1), d * 2.0 ** -23 * each.abs().sum(1), "dtopk_w")
+
+
+def test_tensors_and_streams_of_another_device_are_refused(monkeypatch):
+    """A call runs on the current device; here another number stands for it."""
+    p, r, v = _case("one_row")
+    x, off, W = r.packed(v["x"]), offsets_of(r.counts), [r.dev(v[k]) for k in ("w1", "w3", "w2")]
+    s = torch.cuda.Stream()
+    monkeypatch.setattr(M, "_current", lambda: 1)
+    with pytest.raises(ValueError, match="x_packed is on device 0, the current device is 1"):
+        M.expert_gemm_train(p, x, off, *W)
+    with pytest.raises(ValueError, match="x is on device 0"):
+        M.quantize_rows(x)
+    with pytest.raises(ValueError, match="the stream is on device 0"):
+        M._stream_at(1, s)
