@@ -119,7 +119,9 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
 // A finished tile through a 4 KB staging area of each wave: a store then writes four
 // rows of 256 bytes instead of sixteen pieces of 64, which cost the address
 // unit about 100 cycles an instruction and bounded tiles that mostly store.
-// Staged rows keep their 32-byte chunk c at c ^ (row & 7).
+// Staged rows keep their 32-byte chunk c at c ^ (row & 7), rows 8 .. 15 with its
+// halves exchanged, so that 32 lanes' writes meet 64 distinct banks (sparse
+// weight gradients 825 -> 789 us).
 __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&acc)[4][8], int col0, int N, char* stage) {
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -130,13 +132,13 @@ __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&ac
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       const f32x4 v = acc[mt][t];
-      *reinterpret_cast<u32x2*>(stg + i * 256 + 32 * (t ^ (i & 7)) + 8 * q) =
+      *reinterpret_cast<u32x2*>(stg + i * 256 + 32 * (t ^ (i & 7)) + 8 * (q ^ (2 * (i >> 3)))) =
           u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int row = 4 * k + q;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * 256 + 32 * ((p >> 1) ^ (row & 7)) + 16 * (p & 1));
+      const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * 256 + 32 * ((p >> 1) ^ (row & 7)) + 16 * ((p & 1) ^ (row >> 3)));
       st_put<true>(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
     }
   }
