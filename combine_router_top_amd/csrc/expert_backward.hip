@@ -7,7 +7,7 @@
 //   dx    = rnd(dg W1^T + du W3^T)            (one fp32 sum over both products)
 //   dW1_e = rnd(x^T dg), dW3_e = rnd(x^T du), dW2_e = rnd(h^T dy)
 //
-// Three launches: the gate gradient (dh with its epilogue), the input gradient,
+// Two launches: the gate gradient (dh with its epilogue), then the input gradient
 // and all weight gradients.  The one rounding inside is that of dg and du to
 // the storage type, which the matrix cores need of their operands: it costs
 // 2^-9 relative once per value, as the rounding of h does in the forward pass.
@@ -144,16 +144,27 @@ __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&ac
   }
 }
 
-// dx tiles: [dg | du] against rows of W1, then of W3, in one accumulator.
+// The input gradient: [dg | du] against rows of W1, then of W3, in one accumulator.
+struct InputGrad {
+  const bf16_t* dg;
+  const bf16_t* du;
+  const bf16_t* w1;
+  const bf16_t* w3;
+  bf16_t* dx;   // NULL: not wanted
+  int d, f, ntn;
+};
+
+// Its tiles; returns their number.
 template <int MT>
-__global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __restrict__ dg,
-                                                            const bf16_t* __restrict__ du,
-                                                            const int32_t* __restrict__ offsets, int n,
-                                                            const bf16_t* __restrict__ w1,
-                                                            const bf16_t* __restrict__ w3,
-                                                            bf16_t* __restrict__ dx, int d, int f, int ntn) {
+__device__ __forceinline__ int input_tiles(const InputGrad& p, const int32_t* __restrict__ offsets, int n, char* ring) {
   using Cfg = InputCfg<MT>;
-  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
+  if (!p.dx) return 0;
+  const bf16_t* __restrict__ dg = p.dg;
+  const bf16_t* __restrict__ du = p.du;
+  const bf16_t* __restrict__ w1 = p.w1;
+  const bf16_t* __restrict__ w3 = p.w3;
+  bf16_t* __restrict__ dx = p.dx;
+  const int d = p.d, f = p.f, ntn = p.ntn;
   const int total = st_row_blocks(offsets, n, Cfg::BM) * ntn;
   st_run<Cfg>(
       total, ring,
@@ -179,6 +190,7 @@ __global__ __launch_bounds__(ST_NT, 1) void input_grad_bf16(const bf16_t* __rest
       [&](const StTile& t, typename Cfg::Acc& acc) {
         st_store_tile(st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R), acc, Cfg::BN * t.nt, d);
       });
+  return total;
 }
 
 // One weight gradient C_e [M][N] = P^T Q over the segment's rows, P [rows][M],
@@ -196,12 +208,12 @@ struct WeightGrads {
 // All tiles of all wanted weight gradients, expert by expert; a segment without
 // rows gives zeros.  WG_SHORT: units of at most `div` row blocks.  WG_SPLIT: each
 // tile's rows go to `div` workgroups, whose fp32 sums m[].C holds as [div][n][M][N].
+// first: this workgroup's first tile (unit).
 template <int MODE>
-__global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int nm, int div,
-                                                             const int32_t* __restrict__ offsets, int n) {
+__device__ __forceinline__ void weight_tiles(const WeightGrads& w, int nm, int div, const int32_t* __restrict__ offsets,
+                                             int n, char* ring, int start) {
   using Cfg = WeightCfg<MODE>;
   constexpr bool SHORT = MODE == WG_SHORT;
-  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS + (SHORT ? 8 * 4096 : 0)];
   // the table as values: a choice between its addresses would put it in scratch,
   // and what is read from there into vector registers
   auto held = [&](WeightGrad m) {
@@ -279,7 +291,7 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
   if constexpr (SHORT) {
     st_run_short<Cfg>(n * per, ring, unit, cols, rows, [&](const Unit& r, int j, f32x4 (&acc)[4][8]) {
       store_tile_rows(out(r, j), acc, 256 * r.tn, r.m.N, ring + Cfg::LDS);
-    });
+    }, start);
   } else {
     st_run<Cfg>(
         n * per, ring,
@@ -306,8 +318,22 @@ __global__ __launch_bounds__(ST_NT, 1) void weight_grad_bf16(WeightGrads w, int 
           } else {
             st_store_tile(out(r, 0), acc, 256 * r.tn, r.m.N);
           }
-        });
+        },
+        start);
   }
+}
+
+// Both in one launch: neither needs the other, and in small problems neither has a
+// tile for every compute unit (backward pass of 64 tokens, 4 experts of 512 x 512
+// 28.5 -> 20.8 us, one token and 8 experts of 2048 x 1024 59 -> 50, 32 x 128 rows
+// 1445 -> 1430, 8 dense experts 18.9 -> 19.1 ms).
+template <int MT, int MODE>
+__global__ __launch_bounds__(ST_NT, 1) void input_weight_grad_bf16(InputGrad in, WeightGrads w, int nm, int div,
+                                                                   const int32_t* __restrict__ offsets, int n) {
+  constexpr int LI = InputCfg<MT>::LDS, LW = WeightCfg<MODE>::LDS + (MODE == WG_SHORT ? 8 * 4096 : 0);
+  __shared__ __attribute__((aligned(16))) char ring[LI > LW ? LI : LW];
+  const int before = input_tiles<MT>(in, offsets, n, ring);
+  if (nm) weight_tiles<MODE>(w, nm, div, offsets, n, ring, st_second_tile(before));
 }
 
 // C = rnd(sum of the `div` parts), in their order; blockIdx.y is the matrix.
@@ -341,66 +367,97 @@ __global__ __launch_bounds__(64 * F_NW) void gate_grad_f32(const float* __restri
   const int c0 = blockIdx.y * F_T;
   const float* a = dy + (int64_t)t.r0 * d;
   const float* b = w2 + ((int64_t)t.e * f + c0) * d;
+  // g and u of this lane's values, on their way while the product runs
+  const int row = f32_row(), col = c0 + f32_col();
+  const bool live = row < t.R && col < f;
+  const int64_t at = (int64_t)(t.r0 + row) * f + col;
+  f32x2 gv = {0.f, 0.f}, uv = {0.f, 0.f};
+  if (live) {
+    gv = *reinterpret_cast<const f32x2*>(g + at);
+    uv = *reinterpret_cast<const f32x2*>(u + at);
+  }
   float acc[4][4] = {};
   f32_tile([&](int k, int j) { return j < t.R ? a[(int64_t)j * d + k] : 0.f; }, true,
            [&](int k, int j) { return c0 + j < f ? b[(int64_t)j * d + k] : 0.f; }, true, d, s, acc);
-  f32_join(s, acc);
-  f32_store(acc, [&](int row, int col, float dh) {
-    if (row >= t.R || c0 + col >= f) return;
-    const int64_t at = (int64_t)(t.r0 + row) * f + c0 + col;
-    const float gv = g[at], sg = 1.0f / (1.0f + expf(-gv));
-    dg[at] = dh * u[at] * (sg * (1.0f + gv * (1.0f - sg)));
-    du[at] = dh * (gv * sg);
-  });
+  const f32x2 dh = f32_join(s, acc);
+  if (!live) return;
+  f32x2 vg, vu;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float sg = 1.0f / (1.0f + expf(-gv[r]));
+    vg[r] = dh[r] * uv[r] * (sg * (1.0f + gv[r] * (1.0f - sg)));
+    vu[r] = dh[r] * (gv[r] * sg);
+  }
+  *reinterpret_cast<f32x2*>(dg + at) = vg;
+  *reinterpret_cast<f32x2*>(du + at) = vu;
 }
 
-__global__ __launch_bounds__(64 * F_NW) void input_grad_f32(const float* __restrict__ dg, const float* __restrict__ du,
-                                                      const int32_t* __restrict__ offsets, int n,
-                                                      const float* __restrict__ w1, const float* __restrict__ w3,
-                                                      float* __restrict__ dx, int d, int f) {
-  __shared__ __attribute__((aligned(16))) F32Lds s;
-  StTile t;
-  if (!f32_row_block(offsets, n, blockIdx.x, t)) return;
-  const int c0 = blockIdx.y * F_T;
-  const int64_t ar = (int64_t)t.r0 * f, br = ((int64_t)t.e * d + c0) * f;
-  float acc[4][4] = {};
-  // both products as one sum over 2 f
-  f32_tile([&](int k, int j) { return j < t.R ? (k < f ? dg + ar : du + ar - f)[(int64_t)j * f + k] : 0.f; }, true,
-           [&](int k, int j) { return c0 + j < d ? (k < f ? w1 + br : w3 + br - f)[(int64_t)j * f + k] : 0.f; }, true,
-           2 * f, s, acc);
-  f32_join(s, acc);
-  f32_store(acc, [&](int row, int col, float v) {
-    if (row < t.R && c0 + col < d) dx[(int64_t)(t.r0 + row) * d + c0 + col] = v;
-  });
-}
-
-// C_e [M][N] = P^T Q over the segment's rows, for up to three matrices: block z
-// is matrix z % nm of expert z / nm.
-struct WeightGradsF32 {
+// The input and weight gradients that are wanted: C_e [M][N] = P^T Q over the
+// segment's rows for up to three matrices, and dx; a 32 x 32 tile for each workgroup,
+// in one launch (64 tokens, 8 experts of 128 x 256: whole pass 33.7 -> 17.5 us with
+// the shared join and the gate's early loads).
+struct GradsF32 {
+  const float* dg;
+  const float* du;
+  const float* w1;
+  const float* w3;
+  float* dx;
+  int d, f;
+  int64_t in_tiles;   // row blocks * ceil(d / 32), or 0
+  int row_blocks;
   struct {
     const float* P;
     const float* Q;
     float* C;
     int M, N;
   } m[3];
+  int nm;
+  int64_t tiles;      // in_tiles + n * nm * ceil(d / 32) * ceil(f / 32)
 };
-__global__ __launch_bounds__(64 * F_NW) void weight_grad_f32(WeightGradsF32 w, int nm,
-                                                             const int32_t* __restrict__ offsets) {
-  __shared__ __attribute__((aligned(16))) F32Lds s;
-  const int e = blockIdx.z / nm, k0 = blockIdx.z - e * nm;
-  const auto m = w.m[k0];
-  const int m0 = blockIdx.x * F_T, n0 = blockIdx.y * F_T;
-  if (m0 >= m.M || n0 >= m.N) return;
+
+__device__ __forceinline__ void input_tile_f32(const GradsF32& p, int64_t tile, const int32_t* __restrict__ offsets,
+                                               int n, F32Lds& s) {
+  const int d = p.d, f = p.f;
+  StTile t;
+  const int c = (int)(tile / p.row_blocks);
+  if (!f32_row_block(offsets, n, (int)(tile - (int64_t)c * p.row_blocks), t)) return;
+  const int c0 = c * F_T;
+  const int64_t ar = (int64_t)t.r0 * f, br = ((int64_t)t.e * d + c0) * f;
+  float acc[4][4] = {};
+  // both products as one sum over 2 f
+  f32_tile([&](int k, int j) { return j < t.R ? (k < f ? p.dg + ar : p.du + ar - f)[(int64_t)j * f + k] : 0.f; }, true,
+           [&](int k, int j) { return c0 + j < d ? (k < f ? p.w1 + br : p.w3 + br - f)[(int64_t)j * f + k] : 0.f; }, true,
+           2 * f, s, acc);
+  const f32x2 v = f32_join(s, acc);
+  const int row = f32_row(), col = c0 + f32_col();
+  if (row < t.R && col < d) *reinterpret_cast<f32x2*>(p.dx + (int64_t)(t.r0 + row) * d + col) = v;
+}
+
+__device__ __forceinline__ void weight_tile_f32(const GradsF32& p, int64_t tile, const int32_t* __restrict__ offsets,
+                                                F32Lds& s) {
+  const int64_t each = (p.tiles - p.in_tiles) / p.nm;   // n * tiles of a matrix, alike for all of them
+  const int k0 = (int)(tile / each);
+  const auto m = k0 == 0 ? p.m[0] : k0 == 1 ? p.m[1] : p.m[2];
+  tile -= k0 * each;
+  const int nm = (m.M + F_T - 1) / F_T, nn = (m.N + F_T - 1) / F_T;
+  const int e = (int)(tile / ((int64_t)nm * nn)), at = (int)(tile - (int64_t)e * nm * nn);
+  const int m0 = at / nn * F_T, n0 = at % nn * F_T;
   const int o = offsets[e], cnt = offsets[e + 1] - o;
   const float* a = m.P + (int64_t)o * m.M + m0;
   const float* b = m.Q + (int64_t)o * m.N + n0;
   float acc[4][4] = {};
   f32_tile([&](int k, int j) { return m0 + j < m.M ? a[(int64_t)k * m.M + j] : 0.f; }, false,
            [&](int k, int j) { return n0 + j < m.N ? b[(int64_t)k * m.N + j] : 0.f; }, false, cnt, s, acc);
-  f32_join(s, acc);
-  f32_store(acc, [&](int row, int col, float v) {
-    if (m0 + row < m.M && n0 + col < m.N) m.C[((int64_t)e * m.M + m0 + row) * m.N + n0 + col] = v;
-  });
+  const f32x2 v = f32_join(s, acc);
+  const int row = m0 + f32_row(), col = n0 + f32_col();
+  if (row < m.M && col < m.N) *reinterpret_cast<f32x2*>(m.C + ((int64_t)e * m.M + row) * m.N + col) = v;
+}
+
+__global__ __launch_bounds__(64 * F_NW) void input_weight_grad_f32(GradsF32 p, const int32_t* __restrict__ offsets, int n) {
+  __shared__ __attribute__((aligned(16))) F32Lds s;
+  const int64_t tile = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (tile < p.in_tiles) input_tile_f32(p, tile, offsets, n, s);
+  else if (tile < p.tiles) weight_tile_f32(p, tile - p.in_tiles, offsets, s);
 }
 
 // Zeros (the weight gradients of an empty batch): a kernel, so that a captured
@@ -468,29 +525,27 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
                          (const float*)w2, (const float*)g, (const float*)u, (float*)dgp, (float*)dup, p.d, p.f);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (dx) {
-      hipLaunchKernelGGL(input_grad_f32, dim3(rb, cd), dim3(64 * F_NW), 0, st, (const float*)dgp, (const float*)dup, offsets,
-                         p.n, (const float*)w1, (const float*)w3, (float*)dx, p.d, p.f);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    WeightGradsF32 w{};
-    int nm = 0, M = 0, N = 0;
-    auto want = [&](const void* P, const void* Q, void* C, int m, int n) {
+    GradsF32 q{(const float*)dgp, (const float*)dup, (const float*)w1, (const float*)w3, (float*)dx, p.d, p.f};
+    q.row_blocks = (int)rb;
+    q.in_tiles = dx ? (int64_t)rb * cd : 0;
+    q.tiles = q.in_tiles;
+    auto want = [&](const void* P, const void* Q, void* C, int M, int N) {
       if (!C) return;
-      w.m[nm].P = (const float*)P;
-      w.m[nm].Q = (const float*)Q;
-      w.m[nm].C = (float*)C;
-      w.m[nm].M = m;
-      w.m[nm++].N = n;
-      M = std::max(M, m);
-      N = std::max(N, n);
+      auto& m = q.m[q.nm++];
+      m.P = (const float*)P;
+      m.Q = (const float*)Q;
+      m.C = (float*)C;
+      m.M = M;
+      m.N = N;
+      q.tiles += (int64_t)p.n * cd * cf;
     };
     want(x, dgp, dw1, p.d, p.f);
     want(x, dup, dw3, p.d, p.f);
     want(h, dy, dw2, p.f, p.d);
-    if (nm) {
-      hipLaunchKernelGGL(weight_grad_f32, dim3((M + F_T - 1) / F_T, (N + F_T - 1) / F_T, p.n * nm), dim3(64 * F_NW), 0,
-                         st, w, nm, offsets);
+    if (q.tiles) {
+      const int64_t gx = std::min<int64_t>(q.tiles, 1 << 16);
+      hipLaunchKernelGGL(input_weight_grad_f32, dim3((unsigned)gx, (unsigned)((q.tiles + gx - 1) / gx)), dim3(64 * F_NW),
+                         0, st, q, offsets, p.n);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;
@@ -509,16 +564,6 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
     });
     if (e != hipSuccess) return e;
   }
-  if (dx) {
-    e = st_with_height(st_height(p.n, mean, (int64_t)p.f * 4, p.d, 128), [&](auto h) {
-      constexpr int bn = InputCfg<h()>::BN;
-      const int ntn = (p.d + bn - 1) / bn;
-      hipLaunchKernelGGL(input_grad_bf16<h()>, st_row_grid(p.rows_max, p.n, h(), ntn), dim3(ST_NT), 0, st, DG, DU,
-                         offsets, p.n, (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn);
-      return hipGetLastError();
-    });
-    if (e != hipSuccess) return e;
-  }
   WeightGrads w{};
   int nm = 0;
   int64_t tiles = 0;
@@ -530,9 +575,20 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
   want(h, dy, dw2, p.f, p.d);
   want(x, DG, dw1, p.d, p.f);
   want(x, DU, dw3, p.d, p.f);
-  if (!nm) return hipSuccess;
+  const int tall = st_height(p.n, mean, (int64_t)p.f * 4, p.d, 128);
+  auto go = [&](auto mode, int div, int64_t units) {
+    return st_with_height(dx ? tall : 4, [&](auto height) {
+      constexpr int bn = InputCfg<height()>::BN;
+      const int ntn = (p.d + bn - 1) / bn;
+      const InputGrad in{DG, DU, (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn};
+      const unsigned gi = dx ? st_row_grid(p.rows_max, p.n, height(), ntn).x : 0, gw = nm ? st_grid(units) : 0;
+      hipLaunchKernelGGL((input_weight_grad_bf16<height(), mode()>), dim3(std::min(gi + gw, st_grid(INT32_MAX))),
+                         dim3(ST_NT), 0, st, in, w, nm, div, offsets, p.n);
+      return hipGetLastError();
+    });
+  };
   const int parts = weight_parts(p);
-  if (parts > 1) {
+  if (nm && parts > 1) {
     WeightSums sums{};
     char* at = dup + pad256((size_t)p.rows_max * p.f * p.elem());
     const int64_t count = (int64_t)p.n * p.d * p.f;
@@ -541,22 +597,20 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
       sums.C[k] = w.m[k].C;
       w.m[k].C = (bf16_t*)at;
     }
-    hipLaunchKernelGGL(weight_grad_bf16<WG_SPLIT>, dim3(st_grid(tiles * parts)), dim3(ST_NT), 0, st, w, nm, parts,
-                       offsets, p.n);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = go(std::integral_constant<int, WG_SPLIT>{}, parts, tiles * parts)) != hipSuccess) return e;
     const int64_t blocks = (count / 8 + 255) / 256;
     hipLaunchKernelGGL(weight_grad_sum, dim3((unsigned)std::min<int64_t>(blocks, 2048), nm), dim3(256), 0, st, sums,
                        parts, count);
-  } else if (mean <= WG_SHORT_ROWS) {
+    return hipGetLastError();
+  }
+  if (mean <= WG_SHORT_ROWS) {
     // runs of row blocks that share their columns: up to 4 (8, 2 and 1 measured
     // 864, 813 and 839 us against 808 on 32 experts of about 128 rows), fewer where that
     // would leave less than four units for each compute unit
     const int run = (int)std::min<int64_t>(4, std::max<int64_t>(1, tiles / (4 * (int64_t)device_cus())));
-    hipLaunchKernelGGL(weight_grad_bf16<WG_SHORT>, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, run, offsets, p.n);
-  } else {
-    hipLaunchKernelGGL(weight_grad_bf16<WG_LONG>, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, w, nm, 1, offsets, p.n);
+    return go(std::integral_constant<int, WG_SHORT>{}, run, tiles);
   }
-  return hipGetLastError();
+  return go(std::integral_constant<int, WG_LONG>{}, 1, tiles);
 }
 
 }  // namespace moe

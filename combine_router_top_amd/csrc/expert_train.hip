@@ -119,19 +119,25 @@ __global__ __launch_bounds__(64 * F_NW) void keep_up_f32(const float* __restrict
   const float* a = x + (int64_t)t.r0 * d;
   const int64_t bo = (int64_t)t.e * d * f + c0;
   auto rows = [&](int k, int j) { return j < t.R ? a[(int64_t)j * d + k] : 0.f; };
-  float gate[4][4] = {}, up[4][4] = {};
-  f32_tile(rows, true, [&](int k, int j) { return c0 + j < f ? w1[bo + (int64_t)k * f + j] : 0.f; }, false, d, s, gate);
-  f32_join(s, gate);
-  __syncthreads();   // the joined sums are read before the next ones arrive
-  f32_tile(rows, true, [&](int k, int j) { return c0 + j < f ? w3[bo + (int64_t)k * f + j] : 0.f; }, false, d, s, up);
-  f32_join(s, up);
-  f32_store(gate, up, [&](int row, int col, float gv, float uv) {
-    if (row >= t.R || c0 + col >= f) return;
-    const int64_t at = (int64_t)(t.r0 + row) * f + c0 + col;
-    g[at] = gv;
-    u[at] = uv;
-    h[at] = gv / (1.0f + expf(-gv)) * uv;
-  });
+  float acc[4][4] = {};
+  f32_tile(rows, true, [&](int k, int j) { return c0 + j < f ? w1[bo + (int64_t)k * f + j] : 0.f; }, false, d, s, acc);
+  const f32x2 gate = f32_join(s, acc);
+  __syncthreads();   // the joined sums are read before the next slices arrive
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[p][r] = 0.f;
+  f32_tile(rows, true, [&](int k, int j) { return c0 + j < f ? w3[bo + (int64_t)k * f + j] : 0.f; }, false, d, s, acc);
+  const f32x2 up = f32_join(s, acc);
+  const int row = f32_row(), col = c0 + f32_col();
+  if (row >= t.R || col >= f) return;
+  const int64_t at = (int64_t)(t.r0 + row) * f + col;
+  f32x2 act;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) act[r] = gate[r] / (1.0f + expf(-gate[r])) * up[r];
+  *reinterpret_cast<f32x2*>(g + at) = gate;
+  *reinterpret_cast<f32x2*>(u + at) = up;
+  *reinterpret_cast<f32x2*>(h + at) = act;
 }
 
 __global__ __launch_bounds__(64 * F_NW) void keep_down_f32(const float* __restrict__ h, const int32_t* __restrict__ offsets,
@@ -146,10 +152,9 @@ __global__ __launch_bounds__(64 * F_NW) void keep_down_f32(const float* __restri
   float acc[4][4] = {};
   f32_tile([&](int k, int j) { return j < t.R ? a[(int64_t)j * f + k] : 0.f; }, true,
            [&](int k, int j) { return c0 + j < d ? b[(int64_t)k * d + j] : 0.f; }, false, f, s, acc);
-  f32_join(s, acc);
-  f32_store(acc, [&](int row, int col, float v) {
-    if (row < t.R && c0 + col < d) y[(int64_t)(t.r0 + row) * d + c0 + col] = v;
-  });
+  const f32x2 v = f32_join(s, acc);
+  const int row = f32_row(), col = c0 + f32_col();
+  if (row < t.R && col < d) *reinterpret_cast<f32x2*>(y + (int64_t)(t.r0 + row) * d + col) = v;
 }
 
 hipError_t launch_expert_gemm_train(const Prob& p, const void* x_packed, const int32_t* offsets,

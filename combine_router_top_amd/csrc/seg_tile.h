@@ -571,13 +571,22 @@ __device__ __forceinline__ int st_first_tile() {
   return (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
 }
 
+// First tile of a second walk in the same launch, after one over `before` tiles:
+// the workgroups that the first walk's last round left without a tile come first.
+__device__ __forceinline__ int st_second_tile(int before) {
+  const int G = (int)gridDim.x;
+  const int at = st_first_tile() - (before - st_div(before, G) * G);
+  return at < 0 ? at + G : at;
+}
+
 // The persistent loop.  setup(L, ctx) describes tile L and returns what
 // finish(tile, acc) needs to store it, with exactly Cfg::STORES stores per wave.
-// setup may leave ctx.nst = 0 (a tile of zeros).
+// setup may leave ctx.nst = 0 (a tile of zeros).  first: this workgroup's first tile.
 template <class Cfg, class Setup, class Finish>
-__device__ __forceinline__ void st_run(int total, char* ring, const Setup& setup, const Finish& finish) {
+__device__ __forceinline__ void st_run(int total, char* ring, const Setup& setup, const Finish& finish,
+                                       int first = st_first_tile()) {
   const StLane<Cfg> l = st_lanes<Cfg>(ring);
-  int L = st_first_tile();
+  int L = first;
   if (L >= total) return;
   StCtx<Cfg> c;
   auto tile = setup(L, c);
@@ -616,15 +625,15 @@ __device__ __forceinline__ void st_run(int total, char* ring, const Setup& setup
 //     columns of stage s stay in theirs from tile to tile.
 // unit(U) gives a Unit with nst (stages, 0 or >= 2) and tiles; cols(unit, ctx)
 // and rows(unit, j, ctx) describe its operands for row block j; finish(unit, j,
-// acc) stores with exactly Cfg::STORES stores per wave.
+// acc) stores with exactly Cfg::STORES stores per wave.  first: this workgroup's
+// first unit.
 template <class Cfg, class UnitOf, class Cols, class Rows, class Finish>
 __device__ __forceinline__ void st_run_short(int total, char* ring, const UnitOf& unit, const Cols& cols,
-                                             const Rows& rows, const Finish& finish) {
+                                             const Rows& rows, const Finish& finish, int first = st_first_tile()) {
   static_assert(Cfg::NA == 2 && Cfg::NB == 2 && Cfg::NP == 1, "two slots, one phase");
   constexpr int CA = Cfg::CA, S = Cfg::STORES;
   const StLane<Cfg> l = st_lanes<Cfg>(ring);
   const int G = (int)gridDim.x;
-  const int first = st_first_tile();
   if (first >= total) return;
   // the copies' place: unit Up, its row block jp, that block's next stage sp
   int Up = first - G, jp = 0, sp = 0;

@@ -308,3 +308,43 @@ def test_experts_beyond_32_bits():
     torch.cuda.synchronize()
     for a, b in zip(ref, out):
         assert torch.equal(a[:60], b[A - 60 : A]) and bool((b[A:] == -77.0).all())
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_layer_served_in_8_bits(T):
+    """Route, dispatch, the 8-bit experts and combine, as a server runs them after
+    quantising its weights once, against the layer in 64 bits on the same routing;
+    and the experts' call against the same steps through the single products."""
+    d, f, E, k, lo, n = 512, 256, 8, 3, 2, 4
+    p = M.Spec(T, d, E, k, f, lo, n, "bf16")
+    r = Rows(p, [0], seed=T)
+    x, wg = r.draw(T, d), r.draw(d, E, scale=d ** -0.5)
+    w1, w3, w2 = (r.draw(n, *s, scale=s[0] ** -0.5) for s in ((d, f), (d, f), (f, d)))
+    weights = [M.quantize_weights(r.dev(w)) for w in (w1, w3, w2)]
+    idx, wt = M.route(p, r.dev(x), r.dev(wg))
+    D = M.dispatch(p, idx, r.dev(x))
+    h, yp = M.expert_gemm_quantized(p, D["x_packed"], D["offsets"], *(t for pair in weights for t in pair))
+    y = M.combine(p, yp, D["inv"], wt)
+    torch.cuda.synchronize()
+    ref = torch.zeros(T, d, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            e = int(idx[t, j]) - lo
+            if 0 <= e < n:
+                a = x[t] @ w1[e]
+                ref[t] += float(wt[t, j]) * ((a * torch.sigmoid(a) * (x[t] @ w3[e])) @ w2[e])
+    if float(ref.norm()) == 0:
+        assert not bool(y.any())
+        return
+    # steps of a row or channel whose largest value is c sigma put c / 127 / sqrt(12)
+    # on an operand: x (c up to 4.5, in both factors of h) 2%, W1, W3 and W2 (3.3)
+    # 0.75% each, h (heavy tails, 9) 2%: 3.2% in quadrature, half as much again
+    # for what single rows deviate
+    assert float((y.cpu().double() - ref).norm() / ref.norm()) < 0.048
+    # the same through the single products: y_packed from the stored h, bit by bit
+    off = D["offsets"].cpu().tolist()
+    for e in range(n):
+        if off[e + 1] > off[e]:
+            hq, sh = M.quantize_rows(h[off[e] : off[e + 1]])
+            one = M.gemm_quantized(hq, sh, weights[2][0][e], weights[2][1][e])
+            assert torch.equal(one, yp[off[e] : off[e + 1]])
