@@ -326,7 +326,7 @@ __device__ __forceinline__ void weight_tiles(const WeightGrads& w, int nm, int d
 // Both in one launch: neither needs the other, and in small problems neither has a
 // tile for every compute unit (backward pass of 64 tokens, 4 experts of 512 x 512
 // 28.5 -> 20.8 us, one token and 8 experts of 2048 x 1024 59 -> 50, 32 x 128 rows
-// 1445 -> 1430, 8 dense experts 18.9 -> 19.1 ms).
+// 1445 -> 1430).
 template <int MT, int MODE>
 __global__ __launch_bounds__(ST_NT, 1) void input_weight_grad_bf16(InputGrad in, WeightGrads w, int nm, int div,
                                                                    const int32_t* __restrict__ offsets, int n) {
@@ -580,8 +580,18 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
     return st_with_height(dx ? tall : 4, [&](auto height) {
       constexpr int bn = InputCfg<height()>::BN;
       const int ntn = (p.d + bn - 1) / bn;
-      const InputGrad in{DG, DU, (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn};
-      const unsigned gi = dx ? st_row_grid(p.rows_max, p.n, height(), ntn).x : 0, gw = nm ? st_grid(units) : 0;
+      InputGrad in{DG, DU, (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn};
+      unsigned gi = dx ? st_row_grid(p.rows_max, p.n, height(), ntn).x : 0, gw = nm ? st_grid(units) : 0;
+      // Apart where both have many rounds of long tiles: workgroups that finish the
+      // first walk at different times no longer share operands in an L2 in the
+      // second (8 dense experts: 18.62 ms against 18.87 in one launch).
+      if (gi && gw && mode() == WG_LONG && units >= 8 * (int64_t)device_cus()) {
+        hipLaunchKernelGGL((input_weight_grad_bf16<height(), mode()>), dim3(gi), dim3(ST_NT), 0, st, in, w, 0, div,
+                           offsets, p.n);
+        if (hipError_t e1 = hipGetLastError(); e1 != hipSuccess) return e1;
+        in.dx = nullptr;
+        gi = 0;
+      }
       hipLaunchKernelGGL((input_weight_grad_bf16<height(), mode()>), dim3(std::min(gi + gw, st_grid(INT32_MAX))),
                          dim3(ST_NT), 0, st, in, w, nm, div, offsets, p.n);
       return hipGetLastError();

@@ -38,6 +38,8 @@ CASES = {
     "low_many": ([80 + (23 * e) % 90 - 45 if e % 7 else 0 for e in range(100)], 328, 264, "bf16", dict(T=320, k=25)),
     "low_many_whole_k": ([80 + (19 * e) % 90 - 45 for e in range(100)], 384, 320, "bf16", dict(T=320, k=25)),
     "one_wide": ([2000], 2312, 2568, "bf16", {}),
+    # rounds of long tiles: input and weight gradients apart
+    "long_many": ([500 + (31 * e) % 41 for e in range(172)], 264, 264, "bf16", dict(T=2800, k=32)),
     "one_deep": ([2000], 4360, 1416, "bf16", {}),
     "many_experts": ([(7 * e) % 5 for e in range(150)], 40, 48, "bf16", dict(T=40, k=8)),
     "no_rows": ([0, 0, 0], 64, 72, "bf16", dict(T=5, k=2)),
