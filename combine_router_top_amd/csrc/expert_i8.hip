@@ -403,8 +403,8 @@ __device__ __forceinline__ void i8_stream_block(const I8Args& p, int e, int o, i
   }
 }
 
-// All rows of a segment, 16 MT at a time (with MT = 2 a last block of up to 16
-// rows multiplies half as much); longer segments read their weights again for
+// All rows of a segment, 16 MT at a time, the blocks dealt out over gridDim.z
+// workgroups (with MT = 2 a last block of up to 16 rows multiplies half as much); longer segments read their weights again for
 // each block, from the caches.  MT = 1, for batches of up to 16 rows, holds fewer
 // registers, hence more waves and loads in flight (8 rows, 4096 x 14336: 17
 // against 23 us with the quantiser).
@@ -415,8 +415,9 @@ __global__ __launch_bounds__(64 * KS) void i8_stream(I8Args p) {
   int o;
   const int R = i8_rows(p, e, o);
   constexpr int stride = MT * NT * 64;
-  for (int r0 = 0; r0 < R; r0 += 16 * MT) {
-    if (r0) __syncthreads();   // the sums before have been read
+  const int step = 16 * MT * (int)gridDim.z;
+  for (int r0 = 16 * MT * (int)blockIdx.z; r0 < R; r0 += step) {
+    if (r0 >= step) __syncthreads();   // the sums before have been read
     if (MT == 1 || R - r0 <= 16)
       i8_stream_block<1, NT, GATED, F32OUT, KS, U1>(p, e, o + r0, min(16, R - r0), &red[0][0][0], stride);
     else i8_stream_block<2, NT, GATED, F32OUT, KS, U2>(p, e, o + r0, min(32, R - r0), &red[0][0][0], stride);
@@ -426,32 +427,57 @@ __global__ __launch_bounds__(64 * KS) void i8_stream(I8Args p) {
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-constexpr int I8_THIN = 32;        // rows up to which a segment streams
-constexpr int I8_THIN_MEAN = 64;   // expected rows from which every segment takes a tile
+constexpr int I8_THIN = 32;        // rows up to which a segment may stream beside a launch of tiles
+constexpr int I8_THIN_MEAN = 64;   // expected rows of a segment from which all of them take tiles
 constexpr int I8_THIN_MOST = 128;  // longest possible segment for which all of them stream
 
 // Output columns of a tile of height h.
 template <bool GATED>
 constexpr int I8Cols(int h) { return (h == 1 ? 128 : 256) / (GATED ? 2 : 1); }
 
-// mean: expected rows of a segment; most: bound of one segment's rows.
+// Whether the stream takes less time than the tiles, by what both measured: a
+// round of tiles about 4 us and 0.36 for each stage of 128 K; a round of narrow
+// stream workgroups, one for each 16 columns and 32 rows, about 4 us and 0.05 for
+// each 64 K; weights in bulk 4.7 and 6 TB/s.  5 us for a second launch.  E.g.
+// (K x N, rows: tiles, stream in us) 5824 x 368, 128: 20.4, 9.1; 7168 x 2048, 64:
+// 24.8, 12.2; 512 x 512, 64: 5.0, 7.8; 4096 x 14336, 64: 18.5, 44.2.
+template <bool GATED>
+static bool i8_streams(const I8Args& p, int64_t rows, int64_t act, bool wide, bool alone) {   // act: experts with rows
+  auto rounds = [](int64_t wgs) { return (double)((wgs + device_cus() - 1) / device_cus()); };
+  const double mb = act * (p.kt * 1024e-6) * p.ntiles * (GATED ? 2 : 1);
+  const int64_t cols = (p.N + I8Cols<GATED>(1) - 1) / I8Cols<GATED>(1);
+  const double tiles = std::max(mb / 4.7, rounds(act * ((rows + 63) / 64) * cols) * (4 + 0.18 * p.kt));
+  const int64_t blocks = (rows + 31) / 32;
+  const double stream =
+      wide ? 2 + blocks * mb / 6 : std::max(mb / 6, 2 + rounds(act * blocks * p.ntiles) * (4 + 0.05 * p.kt));
+  return stream + (alone ? 0 : 5) <= tiles;
+}
+
+// mean: expected rows of a segment; all: of all segments; most: bound of one
+// segment's rows.
 template <bool GATED, bool F32OUT>
-static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t rows_max, hipStream_t st) {
+static hipError_t launch_product(I8Args p, int64_t mean, int64_t all, int64_t most, int64_t rows_max, hipStream_t st) {
   hipError_t e;
-  const bool stream = mean <= I8_THIN_MEAN;
+  // four tiles of 16 columns a workgroup where that still makes a workgroup
+  // per compute unit, else one (gated: one of each matrix)
+  const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
+  // a second launch for the segments that do not fit costs about 5 us even if
+  // there are none; short batches stream them in blocks of 32 rows instead (32
+  // experts, 128 tokens: 246 -> 241 us, with skewed routing 247 -> 203 us; with
+  // 256 tokens and skewed routing the tiles are faster, 75 against 123 us)
+  const bool alone = !p.offsets || most <= I8_THIN_MOST;
+  const int64_t rows = std::max<int64_t>(1, mean), act = std::min<int64_t>(p.n, std::max<int64_t>(1, all));
+  const bool stream = (!p.offsets || mean <= I8_THIN_MEAN) && i8_streams<GATED>(p, rows, act, wide, alone);
   if (stream) {
-    // a second launch for the segments that do not fit costs about 5 us even if
-    // there are none; short batches stream them in blocks of 32 rows instead (32
-    // experts, 128 tokens: 246 -> 241 us, with skewed routing 247 -> 203 us; with
-    // 256 tokens and skewed routing the tiles are faster, 75 against 123 us)
-    const bool alone = most <= I8_THIN_MOST;
     p.lo = 0;
     p.hi = alone ? INT32_MAX : I8_THIN;
-    // four tiles of 16 columns a workgroup where that still makes a workgroup
-    // per compute unit, else one (gated: one of each matrix)
-    const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
+    // A segment's blocks of 32 rows go to workgroups of their own: all of them for a
+    // single product, up to 4 for segments (100 tokens, skewed over 16 experts of
+    // 2048 x 768: whole call 53.7 -> 42.4 us; 128 even rows over 32 experts 243.8,
+    // 243.7).
+    const unsigned zb = (unsigned)std::min<int64_t>((most + 31) / 32, p.offsets ? 4 : 1024);
     auto go = [&](auto kernel, int cols, int ks) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n), dim3(64 * ks), 0, st, p);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n, zb), dim3(64 * ks), 0, st, p);
       return hipGetLastError();
     };
     constexpr int NT = GATED ? 2 : 1;
@@ -465,8 +491,8 @@ static hipError_t launch_product(I8Args p, int64_t mean, int64_t most, int64_t r
   }
   p.lo = stream ? I8_THIN : 0;
   auto blocks = [&](int h) { return (p.N + I8Cols<GATED>(h) - 1) / I8Cols<GATED>(h); };
-  const int wide = blocks(2);
-  const int h = st_height(p.n, mean, (p.kt + 1) / 2, {0, blocks(1), wide, wide, wide}, {0, 128, 256, 256, 256});
+  const int ncol = blocks(2);
+  const int h = st_height(p.n, mean, (p.kt + 1) / 2, {0, blocks(1), ncol, ncol, ncol}, {0, 128, 256, 256, 256});
   return st_with_height(h, [&](auto height) {
     constexpr int H = height();
     const int ntn = blocks(H);
@@ -530,10 +556,7 @@ hipError_t launch_gemm_i8(int M, int N, int K, const void* a, const float* sa, c
   p.N = N;
   p.kt = (K + 63) / 64;
   p.ntiles = (N + 15) / 16;
-  // the row count is known: the stream or the tiles, never both
-  const int64_t mean = M <= I8_THIN ? M : std::max(M, I8_THIN_MEAN + 1);
-  return out_dtype == 1 ? launch_product<false, false>(p, mean, M, M, st)
-                        : launch_product<false, true>(p, mean, M, M, st);
+  return out_dtype == 1 ? launch_product<false, false>(p, M, M, M, M, st) : launch_product<false, true>(p, M, M, M, M, st);
 }
 
 static size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
@@ -554,7 +577,7 @@ hipError_t launch_expert_i8(const Prob& p, const void* x, const int32_t* offsets
   float* sx = (float*)(at += pad256((size_t)p.rows_max * pad64(p.f)));
   float* sh = (float*)(at += pad256((size_t)p.rows_max * 4));
   const int32_t* rows = offsets + p.n;   // rows behind the last segment are not read
-  const int64_t mean = p.tk() / p.E;
+  const int64_t mean = p.tk() / p.E, all = p.tk() * p.n / p.E;
   I8Args a{};
   a.offsets = offsets;
   a.n = p.n;
@@ -571,7 +594,7 @@ hipError_t launch_expert_i8(const Prob& p, const void* x, const int32_t* offsets
   a.N = p.f;
   a.kt = pad64(p.d) / 64;
   a.ntiles = (p.f + 15) / 16;
-  if ((e = launch_product<true, false>(a, mean, p.T, p.rows_max, st)) != hipSuccess) return e;
+  if ((e = launch_product<true, false>(a, mean, all, p.T, p.rows_max, st)) != hipSuccess) return e;
   if ((e = launch_quantize_rows(h, 1, p.rows_max, p.f, pad64(p.f), hq, sh, rows, st)) != hipSuccess) return e;
   a.a = hq;
   a.sa = sh;
@@ -584,7 +607,7 @@ hipError_t launch_expert_i8(const Prob& p, const void* x, const int32_t* offsets
   a.N = p.d;
   a.kt = pad64(p.f) / 64;
   a.ntiles = (p.d + 15) / 16;
-  return launch_product<false, false>(a, mean, p.T, p.rows_max, st);
+  return launch_product<false, false>(a, mean, all, p.T, p.rows_max, st);
 }
 
 }  // namespace moe
