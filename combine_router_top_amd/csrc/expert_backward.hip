@@ -121,11 +121,15 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
 // unit about 100 cycles an instruction and bounded tiles that mostly store.
 // Staged rows keep their 32-byte chunk c at c ^ (row & 7), rows 8 .. 15 with its
 // halves exchanged, so that 32 lanes' writes meet 64 distinct banks (sparse
-// weight gradients 825 -> 789 us).
+// weight gradients 825 -> 789 us).  The stores pass L2 by, except for narrow rows
+// that do not start on cache lines, whose pieces L2 merges (30 experts of 64 rows,
+// rows of 784 bytes: 378 -> 313 us; of 768: 237 past L2, 269 through it; four
+// column blocks of 2000 bytes: 142 and 171).
 __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&acc)[4][8], int col0, int N, char* stage) {
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   char* stg = stage + 4096 * wave;
+  const bool merge = N <= 512 && (N & 63) != 0;
   const int p = lane & 15, col = col0 + 128 * (wave >> 2) + 8 * p;
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
@@ -139,7 +143,8 @@ __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&ac
     for (int k = 0; k < 4; ++k) {
       const int row = 4 * k + q;
       const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * 256 + 32 * ((p >> 1) ^ (row & 7)) + 16 * ((p & 1) ^ (row >> 3)));
-      st_put<true>(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
+      if (merge) st_put(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
+      else st_put<true>(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
     }
   }
 }
