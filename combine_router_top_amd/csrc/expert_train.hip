@@ -39,7 +39,8 @@ template <int MT>
 using DownCfg = StCfg<MT, ST_ROWS, ST_PANEL, f32x4, 1, false, 4 * MT, false, 256>;
 
 // Both products of 128 h columns in one tile; W1 and W3 products of a column
-// meet in a lane.
+// meet in a lane.  32 experts of about 128 rows, 7168 x 2048: 390 us, 5.0 TB/s; 2000
+// rows of a dense block, 4104 x 1416: 69 us, the copy rate of 192 busy compute units.
 template <int MT>
 __global__ __launch_bounds__(ST_NT, 1) void keep_up_bf16(const bf16_t* __restrict__ x,
                                                          const int32_t* __restrict__ offsets, int n,

@@ -35,9 +35,9 @@
 // The MFMA takes the column operand first, so a product lane holds 4
 // consecutive columns of one row: lane (i, g) = (l % 16, l / 16) of wave
 // (wm, wn) holds in acc[mt][t] row 16 MT wm + 16 mt + i, columns WN wn + 16 t
-// + 4 g .. + 3 (WN: the columns of a wave).  st_swap_pair exchanges two column tiles between lane groups so
-// that a lane holds 8 consecutive columns: 16-byte stores, whole 64-byte
-// sectors per row.
+// + 4 g .. + 3 (WN: the columns of a wave).  st_swap_pair exchanges two column
+// tiles between lane groups so that a lane holds 8 consecutive columns: 16-byte
+// stores, whole 64-byte sectors per row.
 //
 // Workgroups are persistent (one per compute unit).  The first stages of the
 // next tile are copied before the epilogue of this one, and its first waits
@@ -210,11 +210,11 @@ __device__ __forceinline__ i32x4 st_mfma(const u32x4& a, const u32x4& b, const i
 }
 
 // Tile configuration.  MT = 1: the small tile, 64 x 128 (64 x 256 for a gated pair
-// of ST_PANEL matrices).  NP phases of operands follow
-// one another along K (the input gradient sums two products); all have the same
-// shape.  SPLIT: half of the columns are of one packed matrix, the others the
-// same columns of a second (gate and up products of one h column meet in one
-// lane: acc[mt][t] and acc[mt][t + NT / 2]).  STORES: store instructions of a wave's epilogue, every one of them
+// of ST_PANEL matrices).  NP phases of operands follow one another along K (the
+// input gradient sums two products); all have the same shape.  SPLIT: half of the
+// columns are of one matrix, the others the same columns of a second (gate and up
+// products of one h column meet in one lane: acc[mt][t] and acc[mt][t + NT / 2]).
+// STORES: store instructions of a wave's epilogue, every one of them
 // unconditional.  SHORT: two slots for each operand, for st_run_short.  ROT: K
 // starts at stage ctx.rot and wraps around.
 template <int MT_, int LA_, int LB_, typename AccT_, int NP_, bool SPLIT_, int STORES_, bool SHORT_ = false,
