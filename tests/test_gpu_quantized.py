@@ -70,7 +70,9 @@ SIZES = [(1, 8, 16), (1, 2048, 7168), (2, 24, 48), (15, 136, 64), (16, 512, 80),
          (32, 4096, 128), (33, 264, 144), (64, 72, 320), (129, 520, 592), (300, 264, 1040), (257, 1000, 128), (1, 20000, 64),
          (20, 20000, 192), (3, 8, 8192),
          # enough tiles for the 256-, 192- and 128-row kernels
-         (4096, 4096, 1040), (2049, 2104, 64), (180, 65528, 80), (70, 33000, 208)]
+         (4096, 4096, 1040), (2049, 2104, 64), (180, 65528, 80), (70, 33000, 208),
+         # deep and narrow: blocks of 32 rows on workgroups of their own, a short one last
+         (49, 72, 8208), (100, 136, 2064), (128, 520, 4112), (250, 8, 16400)]
 
 
 @pytest.mark.parametrize("Mr,N,K", SIZES)
