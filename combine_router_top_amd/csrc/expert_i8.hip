@@ -223,13 +223,14 @@ __device__ __forceinline__ int i8_rows(const I8Args& p, int e, int& o) {
   return cnt > p.lo && cnt <= p.hi ? cnt : 0;
 }
 
-// Four neighbouring columns of one output row.
+// Four neighbouring columns of one output row.  Rounded by the hardware's conversion,
+// as in the tiles: it keeps a NaN of any payload a NaN (a scale may hold any).
 template <bool F32OUT>
 __device__ __forceinline__ void i8_store(void* c, int64_t at, const float (&o)[4]) {
   if (F32OUT) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(c) + at) = f32x4{o[0], o[1], o[2], o[3]};
   else
     *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(c) + at) =
-        u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+        u32x2{cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3])};
 }
 
 template <bool GATED>

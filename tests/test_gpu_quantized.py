@@ -350,3 +350,56 @@ def test_layer_served_in_8_bits(T):
             hq, sh = M.quantize_rows(h[off[e] : off[e + 1]])
             one = M.gemm_quantized(hq, sh, weights[2][0][e], weights[2][1][e])
             assert torch.equal(one, yp[off[e] : off[e + 1]])
+
+
+def _nan(bits, *shape):
+    """fp32 NaN of the given bits; memory filled with 0xFF bytes holds 0xFFFFFFFF."""
+    return torch.full(shape, bits - (bits >> 31 << 32), dtype=torch.int32).view(torch.float32)
+
+
+@pytest.mark.parametrize("bits", [0x7FFFFFFF, 0xFFFFFFFF, 0x7FFF8000, 0x7F800001])
+@pytest.mark.parametrize("Mr,N,K", [(6, 24, 8208), (40, 24, 8208), (300, 1040, 1040)])   # the stream, and the tiles
+def test_every_nan_gives_nan_products(bits, Mr, N, K):
+    """A NaN of any payload, in a row, in a channel or in a given scale, is NaN in
+    the bf16 and the fp32 output, and in these rows and columns alone."""
+    g = torch.Generator().manual_seed(bits & 0xFFFF)
+    x, w = torch.randn((Mr, K), generator=g), torch.randn((K, N), generator=g)
+    x[1, 5], w[7, 3] = _nan(bits), _nan(bits)
+    q, s = M.quantize_rows(x.cuda())
+    packed, sw = M.quantize_weights(w.cuda())
+    assert torch.isnan(s[1]) and torch.isnan(sw[3])
+    s[4] = _nan(bits).cuda()
+    sw[N - 1] = _nan(bits).cuda()
+    want = torch.zeros((Mr, N), dtype=torch.bool, device="cuda")
+    want[[1, 4]] = True
+    want[:, [3, N - 1]] = True
+    for dtype in (torch.bfloat16, torch.float32):
+        assert torch.equal(torch.isnan(M.gemm_quantized(q, s, packed, sw, dtype=dtype)), want)
+
+
+@pytest.mark.parametrize("bits", [0x7FFFFFFF, 0xFFFFFFFF])
+@pytest.mark.parametrize("name", ["wide", "tiles"])   # the stream, and the tiles
+def test_every_nan_scale_gives_nan_rows(bits, name):
+    counts, d, f, kw = CASES[name]
+    p, r, w, x, off = _experts(counts, d, f, 12, **kw)
+    xd = r.packed(x)
+    ref = M.expert_gemm_quantized(p, xd, off, *w)
+    e, seg = next((e, s) for e, s in r.segments() if s.start < s.stop)
+    # channel 5 of the down projection: that column of y alone
+    s2 = w[5].clone()
+    s2[e, 5] = _nan(bits).cuda()
+    h, y = M.expert_gemm_quantized(p, xd, off, *w[:5], s2)
+    assert torch.equal(h, ref[0])
+    want = torch.zeros((p.rows_max, d), dtype=torch.bool, device="cuda")
+    want[seg, 5] = True
+    assert torch.equal(torch.isnan(y[: r.A]), want[: r.A])
+    # channel 6 of either gated product: that column of h, and then every column of y
+    for k in (1, 3):
+        scales = list(w)
+        scales[k] = w[k].clone()
+        scales[k][e, 6] = _nan(bits).cuda()
+        h, y = M.expert_gemm_quantized(p, xd, off, *scales)
+        want = torch.zeros((p.rows_max, f), dtype=torch.bool, device="cuda")
+        want[seg, 6] = True
+        assert torch.equal(torch.isnan(h[: r.A]), want[: r.A])
+        assert bool(torch.isnan(y[seg]).all()) and torch.equal(y[: r.A][seg.stop :], ref[1][: r.A][seg.stop :])
