@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const u32x4* __re
           if (BF16) {
             dot = fmaf(g[u][2 * q], bf16_lo(val[u][q]), dot);
             dot = fmaf(g[u][2 * q + 1], bf16_hi(val[u][q]), dot);
-            o[q] = pack_bf16x2(wt * g[u][2 * q], wt * g[u][2 * q + 1]);
+            o[q] = cvt_bf16x2(wt * g[u][2 * q], wt * g[u][2 * q + 1]);   // a NaN weight may have any payload
           } else {
             dot = fmaf(g[u][q], __uint_as_float(val[u][q]), dot);
             o[q] = __float_as_uint(wt * g[u][q]);

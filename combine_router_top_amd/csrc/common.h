@@ -37,6 +37,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
 
+// As pack_bf16x2, by the hardware's packed conversion (one instruction a pair),
+// which keeps a NaN of any payload a NaN.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // SiLU(a) * b = a / (1 + e^-a) * b for the bf16 GEMM epilogues, with the
 // hardware's base-2 exponential and reciprocal (v_exp_f32, v_rcp_f32: each
 // within about one fp32 ulp, e^-a as 2^(-a log2 e)); the result is rounded to

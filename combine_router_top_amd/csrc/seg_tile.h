@@ -445,12 +445,6 @@ __device__ __forceinline__ void st_swap_pair(float& x, float& y) {
   y = __uint_as_float(b);
 }
 
-// As pack_bf16x2, by the hardware's packed conversion (one instruction a pair).
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
 // Values of column tiles t and t + 1 as bf16: 8 consecutive columns per lane,
 // 16 t + 8 g .. + 7 (g the lane group).
 __device__ __forceinline__ u32x4 st_pack8(const float (&x)[4], const float (&y)[4]) {

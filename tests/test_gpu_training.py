@@ -544,3 +544,20 @@ def test_tensors_and_streams_of_another_device_are_refused(monkeypatch):
         M.quantize_rows(x)
     with pytest.raises(ValueError, match="the stream is on device 0"):
         M._stream_at(1, s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bits", [0x7FFFFFFF, 0xFFFFFFFF, 0x7FFF8000, 0x7FC00000])
+def test_combine_backward_weights_that_are_no_number(dtype, bits):
+    """A NaN weight, of any payload, makes its slot's row NaN and no other."""
+    T, k, d = 5, 3, 264
+    p = M.Spec(T, d, k, k, 8, 0, k, dtype)
+    r = Rows(p, [T * k], seed=2)
+    dy, yp = r.dev(r.draw(T, d)), r.dev(r.draw(T * k, d))
+    inv = torch.arange(T * k, dtype=torch.int32).flip(0)
+    w = torch.rand((T, k), generator=r.gen)
+    w[2, 1] = torch.tensor(bits - (bits >> 31 << 32), dtype=torch.int32).view(torch.float32)
+    dyp, dw = M.combine_backward(p, dy, yp, inv.cuda(), w.cuda())
+    want = torch.zeros((T * k, d), dtype=torch.bool)
+    want[int(inv[2 * k + 1])] = True
+    assert torch.equal(torch.isnan(dyp).cpu(), want) and bool(torch.isfinite(dw).all())
