@@ -483,7 +483,7 @@ moe_status_t moe_expert_gemm_backward(const moe_problem_t* p, const void* x_pack
   NEED_ALIGNED(w1);
   NEED_ALIGNED(w3);
   NEED_ALIGNED(w2);
-  if (!dx_packed && !dw1 && !dw3 && !dw2)
+  if (q.T > 0 && !dx_packed && !dw1 && !dw3 && !dw2)   // an empty batch's dx_packed may be NULL
     return fail(MOE_ERR_INVALID_ARG, "dx_packed, dw1, dw3 and dw2 are all NULL");
   NEED_ALIGNED(dw1);
   NEED_ALIGNED(dw3);

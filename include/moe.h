@@ -297,7 +297,7 @@ moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
  *   dx_packed [rows_max,d]              dtype output (rows >= A untouched), or NULL
  *   dw1, dw3  [n_local,d,f]             dtype outputs, each may be NULL
  *   dw2       [n_local,f,d]             dtype output, or NULL
- * A NULL output is not computed; at least one must be given.  Outputs must not
+ * A NULL output is not computed; at least one must be given unless T = 0.  Outputs must not
  * overlap inputs.  d and f at most 2^20.
  *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_BACKWARD) bytes
  * moe_combine(p, dx_packed, inv, NULL, dx) sums dx_packed back to token order

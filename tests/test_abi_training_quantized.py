@@ -183,3 +183,10 @@ def test_a_used_problem_can_be_copied_and_pickled():
     c = p.c()
     c.T = 400
     assert p.c().T == 4 and M.workspace_bytes(p, M.MOE_CALL_EXPERT_GEMM_BACKWARD) == need
+
+
+def test_backward_of_an_empty_batch_may_have_no_pointer_for_its_rows():
+    """T = 0: an array with a T-sized dimension may be NULL, also the only wanted one."""
+    args = [None, FAKE, FAKE, FAKE, FAKE] + [None] * 8
+    assert _call("moe_expert_gemm_backward", _p(T=0), args, ws=None, wsb=0) == M.MOE_OK
+    assert _call("moe_expert_gemm_backward", _p(), [FAKE] * 9 + [None] * 4) == INV

@@ -210,6 +210,15 @@ def test_backward_empty_batch():
         assert all(bool((o == 0).all()) for o in outs[1:])
 
 
+def test_backward_empty_batch_rows_alone():
+    """Only dx_packed wanted of an empty batch: nothing to do, and no refusal."""
+    p = M.Spec(0, 64, 4, 2, 40, 0, 3, "bf16")
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    out = M.expert_gemm_backward(p, z(0, 64), torch.zeros(4, dtype=torch.int32, device="cuda"), z(3, 64, 40), z(3, 64, 40),
+                                 z(3, 40, 64), z(0, 40), z(0, 40), z(0, 40), z(0, 64), out=(z(0, 64), None, None, None))
+    assert out[0].shape == (0, 64) and out[1:] == (None, None, None)
+
+
 def _slots(T, k, n, E, seed):
     rng = np.random.default_rng(seed)
     inv = np.full((T, k), -1, dtype=np.int32)
