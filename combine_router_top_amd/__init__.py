@@ -135,6 +135,13 @@ def _check(st: int):
         raise MoeError(st, lib().moe_last_error().decode())
 
 
+def _fits(bits: int, what: str) -> None:
+    """``bits``: sizes or-ed together.  ctypes would pass them modulo 2^32; small
+    negative ones are the library's to refuse."""
+    if not -(1 << 31) <= bits < 1 << 31:
+        raise ValueError(f"{what} does not fit 32 bits")
+
+
 @dataclass(frozen=True)
 class Spec:
     """Problem description (mirrors moe_problem_t)."""
@@ -153,6 +160,7 @@ class Spec:
         return self.T * min(self.k, self.n_local)
 
     def c(self) -> Problem:
+        _fits(self.T | self.d | self.E | self.k | self.f | self.expert_lo | self.n_local, "a size of the problem")
         return Problem(self.T, self.d, self.E, self.k, self.f, self.expert_lo, self.n_local,
                        MOE_DTYPE_BF16 if self.dtype == "bf16" else MOE_DTYPE_F32, self.flags)
 
@@ -528,6 +536,7 @@ def quantize_rows(x, stream=None, out=None):
     torch = _torch()
     code, cur = _dtype_code(x, "x"), _current()
     rows, K = x.shape
+    _fits(K, "a row of x")
     px = _at(cur, x, (rows, K), x.dtype, "x")
     if out is None:
         with _alloc_on(stream):
@@ -545,6 +554,7 @@ def packed_weights_shape(K: int, N: int):
 
 
 def packed_weights_bytes(n: int, K: int, N: int) -> int:
+    _fits(int(n) | int(K) | int(N), "a size of the weights")
     b = int(lib().moe_packed_weights_bytes(int(n), int(K), int(N)))
     if b == 0:
         raise MoeError(MOE_ERR_INVALID_ARG, lib().moe_last_error().decode())
@@ -598,6 +608,7 @@ def gemm_quantized(a, a_scale, packed, b_scale, dtype=None, stream=None, out=Non
     cur = _current()
     M, K = a.shape
     N = b_scale.shape[0]
+    _fits(M | N | K, "a size of the product")
     pa = _at(cur, a, (M, K), torch.int8, "a")
     if out is None:
         with _alloc_on(stream):

@@ -190,3 +190,30 @@ def test_backward_of_an_empty_batch_may_have_no_pointer_for_its_rows():
     args = [None, FAKE, FAKE, FAKE, FAKE] + [None] * 8
     assert _call("moe_expert_gemm_backward", _p(T=0), args, ws=None, wsb=0) == M.MOE_OK
     assert _call("moe_expert_gemm_backward", _p(), [FAKE] * 9 + [None] * 4) == INV
+
+
+def test_sizes_beyond_32_bits_are_refused_not_cut_off():
+    """Sizes that the C structure and arguments would hold modulo 2^32."""
+    meta = lambda *s, dt=torch.int8: torch.empty(s, dtype=dt, device="meta")  # noqa: E731
+    wide = 2 ** 32 + 16
+    for field in ("T", "d", "f", "E"):
+        kw = dict(T=4, d=16, E=2, k=1, f=8, expert_lo=0, n_local=2, dtype="bf16")
+        kw[field] = wide
+        with pytest.raises(ValueError, match="32 bits"):
+            M.workspace_bytes(M.Spec(**kw), M.MOE_CALL_EXPERT_GEMM_BACKWARD)
+    with pytest.raises(M.MoeError):   # small negative sizes are the library's to refuse
+        M.workspace_bytes(M.Spec(-1, 16, 2, 1, 8, 0, 2, "bf16"), M.MOE_CALL_EXPERT_GEMM_BACKWARD)
+    for n, K, N in ((wide, 64, 16), (1, wide, 16), (1, 64, wide)):
+        with pytest.raises(ValueError, match="32 bits"):
+            M.packed_weights_bytes(n, K, N)
+        with pytest.raises(ValueError, match="32 bits"):
+            M.pack_weights(meta(n, K, N))
+        with pytest.raises(ValueError, match="32 bits"):
+            M.quantize_weights(meta(n, K, N, dt=torch.bfloat16))
+    with pytest.raises(ValueError, match="32 bits"):
+        M.quantize_rows(meta(2, wide, dt=torch.bfloat16))
+    f32 = torch.float32
+    with pytest.raises(ValueError, match="32 bits"):
+        M.gemm_quantized(meta(wide, 16), meta(wide, dt=f32), meta(1, 1, 4, 16, 16), meta(8, dt=f32))
+    with pytest.raises(ValueError, match="32 bits"):
+        M.gemm_quantized(meta(2, wide), meta(2, dt=f32), meta(1, 1, 4, 16, 16), meta(8, dt=f32))
