@@ -570,3 +570,23 @@ def test_combine_backward_weights_that_are_no_number(dtype, bits):
     want = torch.zeros((T * k, d), dtype=torch.bool)
     want[int(inv[2 * k + 1])] = True
     assert torch.equal(torch.isnan(dyp).cpu(), want) and bool(torch.isfinite(dw).all())
+
+
+def test_combine_backward_of_many_tokens():
+    """More tokens than workgroups of 256 fit one grid dimension (2^24)."""
+    T, d = 2 ** 24 + 3, 8
+    p = M.Spec(T, d, 2, 1, 8, 0, 1, "bf16")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    dy = torch.randn((T, d), generator=g, device="cuda").bfloat16()
+    inv = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    inv[5] = -1   # its row T - 6 is named by no slot
+    w = torch.full((T, 1), 0.5, device="cuda")
+    out = (torch.full((T, d), SENTINEL, dtype=torch.bfloat16, device="cuda"), torch.full((T, 1), 9.0, device="cuda"))
+    dyp, dw = M.combine_backward(p, dy, dy, inv, w, out=out)
+    ref = 0.5 * dy.flip(0)   # exact
+    ref[T - 6] = SENTINEL
+    assert torch.equal(dyp, ref)
+    dot = (dy.double() * dy.flip(0).double()).sum(1)
+    dot[5] = 0
+    each = (dy.double() * dy.flip(0).double()).abs().sum(1)
+    assert bool(((dw[:, 0].double() - dot).abs() <= d * 2.0 ** -23 * each).all())
