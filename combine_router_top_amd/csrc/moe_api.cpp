@@ -165,11 +165,15 @@ moe_status_t check_signal_shape(int32_t M, int32_t N, int32_t K) {
   return MOE_OK;
 }
 
-// The training calls address up to 256 rows of d or f elements with 32-bit offsets.
-moe_status_t check_training_widths(const moe::Prob& q) {
+// The training calls address up to 256 rows of d or f elements with 32-bit offsets,
+// and the fp32 ones have a workgroup of 512 for each 32 rows in one grid dimension,
+// which holds fewer than 2^32 work-items.
+moe_status_t check_training_sizes(const moe::Prob& q) {
   const int32_t lim = 1 << 20;
   if (q.d > lim || q.f > lim)
     return fail(MOE_ERR_UNSUPPORTED, "d=%d and f=%d must be at most %d", q.d, q.f, lim);
+  if (q.dtype == MOE_DTYPE_F32 && q.rows_max > (int64_t)1 << 27)
+    return fail(MOE_ERR_UNSUPPORTED, "T*min(k, n_local)=%lld fp32 rows, at most %d", (long long)q.rows_max, 1 << 27);
   return MOE_OK;
 }
 
@@ -441,7 +445,7 @@ moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
   moe::Prob q;
   moe_status_t st = check_problem(p, &q);
   if (st != MOE_OK) return st;
-  if ((st = check_training_widths(q)) != MOE_OK) return st;
+  if ((st = check_training_sizes(q)) != MOE_OK) return st;
   NEED_PTR(offsets);
   NEED_PTR(w1);
   NEED_PTR(w3);
@@ -475,7 +479,7 @@ moe_status_t moe_expert_gemm_backward(const moe_problem_t* p, const void* x_pack
   moe::Prob q;
   moe_status_t st = check_problem(p, &q);
   if (st != MOE_OK) return st;
-  if ((st = check_training_widths(q)) != MOE_OK) return st;
+  if ((st = check_training_sizes(q)) != MOE_OK) return st;
   NEED_PTR(offsets);
   NEED_PTR(w1);
   NEED_PTR(w3);

@@ -274,8 +274,8 @@ moe_status_t moe_expert_gemm_padded(const moe_problem_t* p, int32_t capacity, co
  * and h, y_packed by the formulas of moe_expert_gemm (h from the unrounded
  * products; the fp32 sums may run in another order).
  *   g, u [rows_max,f]  dtype output (rows >= A untouched)
- * d and f at most 2^20.  A dense gated block is the problem with E = k = n_local
- * = 1 and offsets {0, T}.
+ * d and f at most 2^20, rows_max at most 2^27 in fp32.  A dense gated block is the
+ * problem with E = k = n_local = 1 and offsets {0, T}.
  */
 moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
                                    const int32_t* offsets, const void* w1, const void* w3,
@@ -298,7 +298,7 @@ moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
  *   dw1, dw3  [n_local,d,f]             dtype outputs, each may be NULL
  *   dw2       [n_local,f,d]             dtype output, or NULL
  * A NULL output is not computed; at least one must be given unless T = 0.  Outputs must not
- * overlap inputs.  d and f at most 2^20.
+ * overlap inputs.  Sizes as for moe_expert_gemm_train.
  *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_BACKWARD) bytes
  * moe_combine(p, dx_packed, inv, NULL, dx) sums dx_packed back to token order
  * (the backward pass of dispatch's row gather).

@@ -217,3 +217,11 @@ def test_sizes_beyond_32_bits_are_refused_not_cut_off():
         M.gemm_quantized(meta(wide, 16), meta(wide, dt=f32), meta(1, 1, 4, 16, 16), meta(8, dt=f32))
     with pytest.raises(ValueError, match="32 bits"):
         M.gemm_quantized(meta(2, wide), meta(2, dt=f32), meta(1, 1, 4, 16, 16), meta(8, dt=f32))
+
+
+def test_fp32_rows_of_the_training_calls_are_bounded():
+    """Refused as unsupported before anything is launched, not by a failed launch."""
+    p = _p(T=(1 << 27) + 1, d=8, f=8, E=1, k=1, n_local=1, dtype=M.MOE_DTYPE_F32)
+    assert _call("moe_expert_gemm_train", p, [FAKE] * len(TRAIN), has_ws=False) == UNS
+    assert _call("moe_expert_gemm_backward", p, [FAKE] * len(BACK)) == UNS
+    assert b"rows" in M.lib().moe_last_error()
