@@ -41,9 +41,6 @@ template <int MT>
 using GateCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, (MT == 1 ? 4 : 8) * MT>;
 template <int MT>
 using InputCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 2, false, (MT == 1 ? 2 : 4) * MT, false, MT == 1 ? 128 : 256, MT != 4>;
-// How the weight gradients run: whole segments by st_run, short ones by
-// st_run_short, or long segments of few tiles split along their rows.
-enum { WG_LONG = 0, WG_SHORT = 1, WG_SPLIT = 2 };
 template <int MODE>
 using WeightCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, MODE == WG_SPLIT ? 32 : 16, MODE == WG_SHORT>;
 
@@ -475,34 +472,11 @@ __global__ __launch_bounds__(256) void fill_zero(u32x4* __restrict__ p, int64_t 
     p[i] = u32x4{0u, 0u, 0u, 0u};
 }
 
-constexpr int WG_SHORT_ROWS = 512;   // expected rows up to which the weight gradients take st_run_short
-
-// Parts that the rows of the weight gradients are split into: as many as make
-// the least time by the rule of st_height, the fp32 parts written and read at
-// about 4 TB/s, at most 256 MB of them.  1: not split.
-static int weight_parts(const Prob& p) {
-  if (p.dtype != 1 || p.T == 0) return 1;
-  const int64_t mean = p.tk() / p.E, stages = (mean + 63) / 64, cus = device_cus();
-  const int64_t tiles = 3 * (int64_t)p.n * ((p.d + 255) / 256) * ((p.f + 255) / 256);
-  const double elems = 3.0 * p.n * p.d * p.f;
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= 32 && (s == 1 || (s * elems * 4 <= 256e6 && stages >= 4 * s)); ++s) {
-    const double us = (double)((tiles * s + cus - 1) / cus) * ((stages + s - 1) / s * 1.72 + 4) +
-                      (s > 1 ? 4 + elems * (8.0 * s + 2) / 4e6 : 0);
-    if (s == 1 || us < least) {
-      best = s;
-      least = us;
-    }
-  }
-  return best;
-}
-
 static size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
 
 size_t expert_backward_ws_bytes(const Prob& p) {
   // dg and du, [rows_max, f] each, and the parts of split weight gradients
-  const int parts = weight_parts(p);
+  const int parts = p.dtype == 1 && p.T > 0 ? weight_parts(device_cus(), p.tk(), p.E, p.n, p.d, p.f) : 1;
   return 2 * pad256((size_t)p.rows_max * p.f * p.elem()) +
          (parts > 1 ? 3 * pad256((size_t)parts * p.n * p.d * p.f * 4) : 0);
 }
@@ -558,11 +532,12 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
     }
     return hipSuccess;
   }
-  const int64_t mean = p.tk() / p.E;   // expected rows of a segment
+  const BackwardPlan plan =
+      backward_plan(device_cus(), p.tk(), p.E, p.n, p.d, p.f, dx, (dw1 != nullptr) + (dw3 != nullptr) + (dw2 != nullptr));
   const bf16_t* DG = (const bf16_t*)dgp;
   const bf16_t* DU = (const bf16_t*)dup;
   if (gate) {
-    e = st_with_height(st_height(p.n, mean, (int64_t)p.d * 2, p.f, 128), [&](auto h) {
+    e = st_with_height(plan.gate, [&](auto h) {
       constexpr int bn = GateCfg<h()>::BN;
       const int ntn = (p.f + bn - 1) / bn;
       hipLaunchKernelGGL(gate_grad_bf16<h()>, st_row_grid(p.rows_max, p.n, h(), ntn), dim3(ST_NT), 0, st,
@@ -574,39 +549,33 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
   }
   WeightGrads w{};
   int nm = 0;
-  int64_t tiles = 0;
   auto want = [&](const void* P, const void* Q, void* C, int M, int N) {
     if (!C) return;
     w.m[nm++] = WeightGrad{(const bf16_t*)P, (const bf16_t*)Q, (bf16_t*)C, M, N};
-    tiles += (int64_t)((M + 255) / 256) * ((N + 255) / 256) * p.n;
   };
   want(h, dy, dw2, p.f, p.d);
   want(x, DG, dw1, p.d, p.f);
   want(x, DU, dw3, p.d, p.f);
-  const int tall = st_height(p.n, mean, (int64_t)p.f * 4, p.d, 128);
-  auto go = [&](auto mode, int div, int64_t units) {
-    return st_with_height(dx ? tall : 4, [&](auto height) {
+  auto go = [&](auto mode) {
+    return st_with_height(plan.input, [&](auto height) {
       constexpr int bn = InputCfg<height()>::BN;
       const int ntn = (p.d + bn - 1) / bn;
       InputGrad in{DG, DU, (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)dx, p.d, p.f, ntn};
-      unsigned gi = dx ? st_row_grid(p.rows_max, p.n, height(), ntn).x : 0, gw = nm ? st_grid(units) : 0;
-      // Apart where both have many rounds of long tiles: workgroups that finish the
-      // first walk at different times no longer share operands in an L2 in the
-      // second (8 dense experts: 18.62 ms against 18.87 in one launch).
-      if (gi && gw && mode() == WG_LONG && units >= 8 * (int64_t)device_cus()) {
-        hipLaunchKernelGGL((input_weight_grad_bf16<height(), mode()>), dim3(gi), dim3(ST_NT), 0, st, in, w, 0, div,
+      unsigned gi = dx ? st_row_grid(p.rows_max, p.n, height(), ntn).x : 0, gw = nm ? st_grid(plan.units) : 0;
+      if (plan.apart) {
+        hipLaunchKernelGGL((input_weight_grad_bf16<height(), mode()>), dim3(gi), dim3(ST_NT), 0, st, in, w, 0, plan.div,
                            offsets, p.n);
         if (hipError_t e1 = hipGetLastError(); e1 != hipSuccess) return e1;
         in.dx = nullptr;
         gi = 0;
       }
       hipLaunchKernelGGL((input_weight_grad_bf16<height(), mode()>), dim3(std::min(gi + gw, st_grid(INT32_MAX))),
-                         dim3(ST_NT), 0, st, in, w, nm, div, offsets, p.n);
+                         dim3(ST_NT), 0, st, in, w, nm, plan.div, offsets, p.n);
       return hipGetLastError();
     });
   };
-  const int parts = weight_parts(p);
-  if (nm && parts > 1) {
+  if (plan.mode == WG_SPLIT) {
+    const int parts = plan.div;
     WeightSums sums{};
     char* at = dup + pad256((size_t)p.rows_max * p.f * p.elem());
     const int64_t count = (int64_t)p.n * p.d * p.f;
@@ -615,20 +584,14 @@ hipError_t launch_expert_backward(const Prob& p, const void* x, const int32_t* o
       sums.C[k] = w.m[k].C;
       w.m[k].C = (bf16_t*)at;
     }
-    if ((e = go(std::integral_constant<int, WG_SPLIT>{}, parts, tiles * parts)) != hipSuccess) return e;
+    if ((e = go(std::integral_constant<int, WG_SPLIT>{})) != hipSuccess) return e;
     const int64_t blocks = (count / 8 + 255) / 256;
     hipLaunchKernelGGL(weight_grad_sum, dim3((unsigned)std::min<int64_t>(blocks, 2048), nm), dim3(256), 0, st, sums,
                        parts, count);
     return hipGetLastError();
   }
-  if (mean <= WG_SHORT_ROWS) {
-    // runs of row blocks that share their columns: up to 4 (8, 2 and 1 measured
-    // 864, 813 and 839 us against 808 on 32 experts of about 128 rows), fewer where that
-    // would leave less than four units for each compute unit
-    const int run = (int)std::min<int64_t>(4, std::max<int64_t>(1, tiles / (4 * (int64_t)device_cus())));
-    return go(std::integral_constant<int, WG_SHORT>{}, run, tiles);
-  }
-  return go(std::integral_constant<int, WG_LONG>{}, 1, tiles);
+  if (plan.mode == WG_SHORT) return go(std::integral_constant<int, WG_SHORT>{});
+  return go(std::integral_constant<int, WG_LONG>{});
 }
 
 }  // namespace moe

@@ -431,75 +431,32 @@ __global__ __launch_bounds__(64 * KS) void i8_stream(I8Args p) {
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-constexpr int I8_THIN = 32;        // rows up to which a segment may stream beside a launch of tiles
-constexpr int I8_THIN_MEAN = 64;   // expected rows of a segment from which all of them take tiles
-constexpr int I8_THIN_MOST = 128;  // longest possible segment for which all of them stream
-
-// Output columns of a tile of height h.
-template <bool GATED>
-constexpr int I8Cols(int h) { return (h == 1 ? 128 : 256) / (GATED ? 2 : 1); }
-
-// Whether the stream takes less time than the tiles, by what both measured: a
-// round of tiles about 4 us and 0.36 for each stage of 128 K; a round of narrow
-// stream workgroups, one for each 16 columns and 32 rows, about 4 us and 0.05 for
-// each 64 K; weights in bulk 4.7 and 6 TB/s.  5 us for a second launch.  E.g.
-// (K x N, rows: tiles, stream in us) 5824 x 368, 128: 20.4, 9.1; 7168 x 2048, 64:
-// 24.8, 12.2; 512 x 512, 64: 5.0, 7.8; 4096 x 14336, 64: 18.5, 44.2.
-template <bool GATED>
-static bool i8_streams(const I8Args& p, int64_t rows, int64_t act, bool wide, bool alone) {   // act: experts with rows
-  auto rounds = [](int64_t wgs) { return (double)((wgs + device_cus() - 1) / device_cus()); };
-  const double mb = act * (p.kt * 1024e-6) * p.ntiles * (GATED ? 2 : 1);
-  const int64_t cols = (p.N + I8Cols<GATED>(1) - 1) / I8Cols<GATED>(1);
-  const double tiles = std::max(mb / 4.7, rounds(act * ((rows + 63) / 64) * cols) * (4 + 0.18 * p.kt));
-  const int64_t blocks = (rows + 31) / 32;
-  const double stream =
-      wide ? 2 + blocks * mb / 6 : std::max(mb / 6, 2 + rounds(act * blocks * p.ntiles) * (4 + 0.05 * p.kt));
-  return stream + (alone ? 0 : 5) <= tiles;
-}
-
-// mean: expected rows of a segment; all: of all segments; most: bound of one
-// segment's rows.
+// What i8_plan says for a product of these rows.
 template <bool GATED, bool F32OUT>
 static hipError_t launch_product(I8Args p, int64_t mean, int64_t all, int64_t most, int64_t rows_max, hipStream_t st) {
-  hipError_t e;
-  // four tiles of 16 columns a workgroup where that still makes a workgroup
-  // per compute unit, else one (gated: one of each matrix)
-  const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
-  // a second launch for the segments that do not fit costs about 5 us even if
-  // there are none; short batches stream them in blocks of 32 rows instead (32
-  // experts, 128 tokens: 246 -> 241 us, with skewed routing 247 -> 203 us; with
-  // 256 tokens and skewed routing the tiles are faster, 75 against 123 us)
-  const bool alone = !p.offsets || most <= I8_THIN_MOST;
-  const int64_t rows = std::max<int64_t>(1, mean), act = std::min<int64_t>(p.n, std::max<int64_t>(1, all));
-  const bool stream = (!p.offsets || mean <= I8_THIN_MEAN) && i8_streams<GATED>(p, rows, act, wide, alone);
-  if (stream) {
+  const I8Plan plan = i8_plan(device_cus(), I8Shape{GATED, p.offsets != nullptr, p.n, p.N, p.kt, mean, all, most});
+  if (plan.stream) {
     p.lo = 0;
-    p.hi = alone ? INT32_MAX : I8_THIN;
-    // A segment's blocks of 32 rows go to workgroups of their own: all of them for a
-    // single product, up to 4 for segments (100 tokens, skewed over 16 experts of
-    // 2048 x 768: whole call 53.7 -> 42.4 us; 128 even rows over 32 experts 243.8,
-    // 243.7).
-    const unsigned zb = (unsigned)std::min<int64_t>((most + 31) / 32, p.offsets ? 4 : 1024);
+    p.hi = plan.tiles ? I8_THIN : INT32_MAX;
     auto go = [&](auto kernel, int cols, int ks) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n, zb), dim3(64 * ks), 0, st, p);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n, (unsigned)plan.blocks),
+                         dim3(64 * ks), 0, st, p);
       return hipGetLastError();
     };
     constexpr int NT = GATED ? 2 : 1;
-    if (most <= 16)
-      e = wide ? go(i8_stream<1, 4, GATED, F32OUT, 4, 4, 4>, GATED ? 32 : 64, 4)
-               : go(i8_stream<1, NT, GATED, F32OUT, 8, 4, 4>, 16, 8);
+    hipError_t e;
+    if (plan.low)
+      e = plan.wide ? go(i8_stream<1, 4, GATED, F32OUT, 4, 4, 4>, GATED ? 32 : 64, 4)
+                    : go(i8_stream<1, NT, GATED, F32OUT, 8, 4, 4>, 16, 8);
     else
-      e = wide ? go(i8_stream<2, 4, GATED, F32OUT, 4, 4, 3>, GATED ? 32 : 64, 4)
-               : go(i8_stream<2, NT, GATED, F32OUT, 8, 4, 4>, 16, 8);
-    if (e != hipSuccess || alone) return e;
+      e = plan.wide ? go(i8_stream<2, 4, GATED, F32OUT, 4, 4, 3>, GATED ? 32 : 64, 4)
+                    : go(i8_stream<2, NT, GATED, F32OUT, 8, 4, 4>, 16, 8);
+    if (e != hipSuccess || !plan.tiles) return e;
   }
-  p.lo = stream ? I8_THIN : 0;
-  auto blocks = [&](int h) { return (p.N + I8Cols<GATED>(h) - 1) / I8Cols<GATED>(h); };
-  const int ncol = blocks(2);
-  const int h = st_height(p.n, mean, (p.kt + 1) / 2, {0, blocks(1), ncol, ncol, ncol}, {0, 128, 256, 256, 256});
-  return st_with_height(h, [&](auto height) {
-    constexpr int H = height();
-    const int ntn = blocks(H);
+  p.lo = plan.stream ? I8_THIN : 0;
+  return st_with_height(plan.height, [&](auto height) {
+    constexpr int H = height(), cols = i8_cols(GATED, H);
+    const int ntn = (p.N + cols - 1) / cols;
     hipLaunchKernelGGL((i8_tile<H, GATED, F32OUT>), st_row_grid(rows_max, p.n, H, ntn), dim3(ST_NT), 0, st, p, ntn);
     return hipGetLastError();
   });

@@ -13,8 +13,6 @@
 // training batches are of that kind.
 #include <stdint.h>
 
-#include <algorithm>
-
 #include "common.h"
 #include "f32_tile.h"
 #include "kernels.h"
@@ -172,16 +170,15 @@ hipError_t launch_expert_gemm_train(const Prob& p, const void* x_packed, const i
     return hipGetLastError();
   }
   const int nup = (p.f + 127) / 128, ndown = (p.d + 255) / 256;
-  const int64_t seg = std::max<int64_t>(1, p.tk() / p.E);   // expected rows of a segment
-  hipError_t e = st_with_height(
-      st_height(p.n, seg, (p.d + 63) / 64, {0, nup, nup, nup, nup}, {0, 256, 256, 256, 256}), [&](auto m) {
-        hipLaunchKernelGGL(keep_up_bf16<m()>, st_row_grid(p.rows_max, p.n, m(), nup), dim3(ST_NT), 0, st,
-                           (const bf16_t*)x_packed, offsets, p.n, (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)g,
-                           (bf16_t*)u, (bf16_t*)h, p.d, p.f, nup);
-        return hipGetLastError();
-      });
+  const TrainPlan plan = train_plan(device_cus(), p.tk(), p.E, p.n, p.d, p.f);
+  hipError_t e = st_with_height(plan.up, [&](auto m) {
+    hipLaunchKernelGGL(keep_up_bf16<m()>, st_row_grid(p.rows_max, p.n, m(), nup), dim3(ST_NT), 0, st,
+                       (const bf16_t*)x_packed, offsets, p.n, (const bf16_t*)w1, (const bf16_t*)w3, (bf16_t*)g,
+                       (bf16_t*)u, (bf16_t*)h, p.d, p.f, nup);
+    return hipGetLastError();
+  });
   if (e != hipSuccess) return e;
-  return st_with_height(st_height(p.n, seg, (int64_t)p.f * 2, p.d, 256), [&](auto m) {
+  return st_with_height(plan.down, [&](auto m) {
     hipLaunchKernelGGL(keep_down_bf16<m()>, st_row_grid(p.rows_max, p.n, m(), ndown), dim3(ST_NT), 0, st,
                        (const bf16_t*)h, offsets, p.n, (const bf16_t*)w2, (bf16_t*)y_packed, p.d, p.f, ndown);
     return hipGetLastError();

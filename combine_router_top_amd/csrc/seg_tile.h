@@ -54,6 +54,7 @@
 #include "dma_tile.h"
 #include "dma_big.h"
 #include "kernels.h"
+#include "tile_rules.h"
 
 namespace moe {
 
@@ -61,7 +62,6 @@ enum { ST_ROWS = 0, ST_PANEL = 1, ST_PACK = 2 };
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int ST_KB = 128;     // bytes of K per stage
 constexpr int ST_NT = 512;     // threads
 
 // One operand of W tile rows (or columns): state of its copies.
@@ -711,40 +711,8 @@ __device__ __forceinline__ void st_run_short(int total, char* ring, const UnitOf
 }
 
 // ---------------------------------------------------------------------------
-// host side: tile heights
+// host side: launches by tile height (tile_rules.h chooses it)
 // ---------------------------------------------------------------------------
-// Height (in units of 64 rows) of the tiles for segments of about `mean` rows of
-// n experts: the one whose rounds of workgroups take the least time.  A stage of
-// a tile costs the copies of its rows and columns, at the 38 GB/s that a compute
-// unit sustains from L2, but at least about half a microsecond; a tile costs
-// about 4 us more (first loads, epilogue).  Segments are taken a quarter longer
-// than the mean unless there is one alone: a segment that does not fit its tile
-// reads all its columns again.  ntn[h]: column blocks for height h, each of
-// bn[h] operand columns; 0: no such tile.
-inline int st_height(int64_t n, int64_t mean, int stages, const int (&ntn)[5], const int (&bn)[5]) {
-  const int64_t seg = std::max<int64_t>(1, n > 1 ? mean + mean / 4 : mean);
-  const int64_t cus = device_cus();
-  int best = 0;
-  double least = 0;
-  for (int h = 4; h >= 1; --h) {
-    if (!ntn[h]) continue;
-    const int64_t tiles = n * ((seg + 64 * h - 1) / (64 * h)) * ntn[h];
-    const double stage = std::max(0.5, (64 * h + bn[h]) * 128 / 38e3);
-    const double us = (double)((tiles + cus - 1) / cus) * (stages * stage + 4.0);
-    if (!best || us < least) {
-      best = h;
-      least = us;
-    }
-  }
-  return best;
-}
-// The same for tiles of 256 columns and, at height 1, `small` columns.
-inline int st_height(int64_t n, int64_t mean, int64_t kbytes, int N, int small) {
-  const int wide = (N + 255) / 256;
-  return st_height(n, mean, (int)((kbytes + ST_KB - 1) / ST_KB), {0, (N + small - 1) / small, wide, wide, wide},
-                   {0, small, 256, 256, 256});
-}
-
 // Calls go with the height as a compile-time constant.
 template <class Go>
 inline hipError_t st_with_height(int h, const Go& go) {
