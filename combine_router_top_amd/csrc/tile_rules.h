@@ -183,8 +183,8 @@ inline I8Plan i8_plan(int64_t cus, const I8Shape& p) {
   // A segment's blocks of 32 rows go to workgroups of their own: all of them for a
   // single product, up to 4 for segments (100 tokens, skewed over 16 experts of
   // 2048 x 768: whole call 53.7 -> 42.4 us; 128 even rows over 32 experts 243.8,
-  // 243.7).
-  r.blocks = (int)std::min<int64_t>((p.most + 31) / 32, p.segments ? 4 : 1024);
+  // 243.7).  Beside tiles a segment that streams has one block.
+  r.blocks = r.tiles ? 1 : (int)std::min<int64_t>((p.most + 31) / 32, p.segments ? 4 : 1024);
   auto cols = [&](int h) { return (p.N + i8_cols(p.gated, h) - 1) / i8_cols(p.gated, h); };
   const int ncol = cols(2);
   if (r.tiles)

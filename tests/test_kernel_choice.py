@@ -72,3 +72,11 @@ def test_every_8_bit_kernel_has_a_case():
     for plans in (gated, down):
         assert {(p.wide, p.tiles) for p in plans if p.stream} == {(0, 0), (0, 1), (1, 0), (1, 1)}
         assert {p.wide for p in plans if p.stream and not p.tiles and p.blocks > 1} == {0, 1}
+
+
+def test_no_workgroups_without_work():
+    """Beside tiles a streamed segment has one block of 32 rows: one workgroup for it."""
+    for case in C.QUANTIZED.values():
+        for plan in R.experts(C.problem(case)):
+            if plan.stream and plan.tiles:
+                assert plan.blocks == 1
