@@ -64,6 +64,15 @@ __device__ __forceinline__ uint32_t f32_order_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// What this wave's lanes wrote to LDS is read by other lanes of the same wave, or read
+// before it is written again: LDS operations of a wave stay in order, the compiler
+// has to leave them so.
+__device__ __forceinline__ void lds_wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 
 // Exclusive/inclusive wave-wide helpers on 64-lane wavefronts.

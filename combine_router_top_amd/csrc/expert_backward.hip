@@ -139,6 +139,7 @@ __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&ac
       *reinterpret_cast<u32x2*>(stg + i * 256 + 32 * (t ^ (i & 7)) + 8 * (q ^ (2 * (i >> 3)))) =
           u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
     }
+    lds_wave_order();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int row = 4 * k + q;
@@ -146,6 +147,7 @@ __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&ac
       if (merge) st_put(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
       else st_put<true>(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
     }
+    lds_wave_order();
   }
 }
 

@@ -55,10 +55,7 @@ __device__ __forceinline__ void f32_tile(const FA& A, bool a_kfast, const FB& B,
       sa[kk(a_kfast, v) * F_LD + jj(a_kfast, v)] = ra[v];
       sb[kk(b_kfast, v) * F_LD + jj(b_kfast, v)] = rb[v];
     }
-    // this wave alone writes and reads its part: LDS operations of a wave stay in order
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    lds_wave_order();   // this wave alone writes and reads its part
     if (k0 + F_NW * F_K < K) load(k0 + F_NW * F_K);
 #pragma unroll
     for (int k = 0; k < F_K; ++k) {
@@ -69,9 +66,7 @@ __device__ __forceinline__ void f32_tile(const FA& A, bool a_kfast, const FB& B,
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[p][r] = fmaf(a[p], b[r], acc[p][r]);
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    lds_wave_order();
   }
 }
 
