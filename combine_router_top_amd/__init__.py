@@ -27,6 +27,11 @@ Functions (same names as the C calls):
     expert_gemm_quantized(p, x_packed, offsets, w1, s1, w3, s3, w2, s2) -> (h, y_packed)
     gemm_signal(A, B, flags, epoch) -> C          (C = rnd(A B), a flag per 256 x 256 tile)
     tile_forward(C, dst, flags, epoch, spin_limit, timeouts, workgroups)
+
+The training and 8-bit calls take tensors and streams of the current device only.
+With ``stream=`` they order nothing against the current stream, and what they allocate
+belongs to the given one: wait for it before reading the outputs elsewhere, and
+``record_stream`` outputs that outlive such a use.
 """
 from __future__ import annotations
 

@@ -9,9 +9,9 @@
 //
 // Two launches: the gate gradient (dh with its epilogue), then the input gradient
 // and all weight gradients.  The one rounding inside is that of dg and du to
-// the storage type, which the matrix cores need of their operands: it costs
-// 2^-9 relative once per value, as the rounding of h does in the forward pass.
-// Every other sum stays in fp32.
+// the storage type, which the matrix cores need of their operands: in bf16 it costs
+// up to 2^-8 relative once per value, as the rounding of h does in the forward pass;
+// in fp32 there is none.  Every other sum stays in fp32.
 //
 // bf16: tiles of seg_tile.h.  The first two products contract over a dimension
 // that both operands hold contiguously (dy and rows of W2; dg and rows of W1),
@@ -124,7 +124,10 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_grad_bf16(const bf16_t* __restr
 // weight gradients 825 -> 789 us).  The stores pass L2 by, except for narrow rows
 // that do not start on cache lines, whose pieces L2 merges (30 experts of 64 rows,
 // rows of 784 bytes: 378 -> 313 us; of 768: 237 past L2, 269 through it; four
-// column blocks of 2000 bytes: 142 and 171).
+// column blocks of 2000 bytes: 142 and 171).  Where exactly wider rows change sides is
+// not known: with M = 7168 and 30 experts of 64 rows, going through L2 was faster up to
+// the widest tried (rows of 976 bytes 412 past, 354 through; 1040: 487, 450; 1424:
+// 613, 521; 2000: 778, 682; 2448: 997, 892).
 __device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&acc)[4][8], int col0, int N, char* stage) {
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -5,12 +5,13 @@
 //
 // bf16: two launches over the tiles of seg_tile.h; W1 and W3 products of an h
 // column meet in one lane, so g, u and h leave from registers.  The launch pair
-// of expert_gemm.hip streams a set of weight columns past at most 160 rows and is
-// within 10% of this one where every segment is short (32 experts of 7168 x 2048,
-// about 80 rows each: 485 against 545 us); where any segment is longer it reads
-// those weights once more and in a second round of workgroups (about 128 rows each:
-// 719 against 568 us; 16 .. 96 rows each, skewed: 735 against 570 .. 660 us), and
-// training batches are of that kind.
+// of expert_gemm.hip streams a set of weight columns past at most 160 rows and would
+// be faster where every segment is short (32 experts of 7168 x 2048, about 80 rows
+// each: 485 against 545 us); where any segment is longer it reads those weights once
+// more and in a second round of workgroups (about 128 rows each: 719 against 568 us;
+// 16 .. 96 rows each, skewed: 735 against 570 .. 660 us).  Training batches are of
+// that kind, and a host that knows the expected length alone cannot tell them apart, so
+// the tiles take every size.
 #include <stdint.h>
 
 #include "common.h"

@@ -43,7 +43,10 @@
 // next tile are copied before the epilogue of this one, and its first waits
 // count the epilogue's stores as outstanding (loads and stores retire in
 // order), so that the stores of a tile drain while the next is loaded and
-// multiplied.
+// multiplied.  An epilogue that loads itself (g and u of the gate gradient, the
+// scales of the 8-bit tiles, a spilled register: keep_up_bf16<4>, keep_down_bf16<4>
+// and the gated i8_tile<4> have 16 to 36 bytes of scratch a lane) waits for those first
+// copies too, for the same reason.
 #pragma once
 
 #include <algorithm>

@@ -42,7 +42,8 @@
  *     device or the host.
  *   - Validation is host-side and shape-only.  On error nothing is launched,
  *     a status is returned and moe_last_error() describes it.  Data-dependent
- *     conditions are not checked: NaN/Inf inputs, expert indices outside
+ *     conditions are not checked: NaN/Inf inputs (unless a call says below
+ *     what it gives for them), expert indices outside
  *     [0, E) in a caller-supplied topk_idx, and a topk_idx row that names the
  *     same expert twice are undefined behaviour (the buffers sized from
  *     rows_max hold T*min(k, n_local) rows only because the k experts of a
@@ -274,7 +275,9 @@ moe_status_t moe_expert_gemm_padded(const moe_problem_t* p, int32_t capacity, co
  * and h, y_packed by the formulas of moe_expert_gemm (h from the unrounded
  * products; the fp32 sums may run in another order).
  *   g, u [rows_max,f]  dtype output (rows >= A untouched)
- * d and f at most 2^20, rows_max at most 2^27 in fp32.  A dense gated block is the
+ * Outputs must not overlap inputs or one another.  NaN and infinities in one
+ * expert's rows reach no other expert's.  d and f at most 2^20, rows_max at most
+ * 2^27 in fp32.  A dense gated block is the
  * problem with E = k = n_local = 1 and offsets {0, T}.
  */
 moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
@@ -297,8 +300,8 @@ moe_status_t moe_expert_gemm_train(const moe_problem_t* p, const void* x_packed,
  *   dx_packed [rows_max,d]              dtype output (rows >= A untouched), or NULL
  *   dw1, dw3  [n_local,d,f]             dtype outputs, each may be NULL
  *   dw2       [n_local,f,d]             dtype output, or NULL
- * A NULL output is not computed; at least one must be given unless T = 0.  Outputs must not
- * overlap inputs.  Sizes as for moe_expert_gemm_train.
+ * A NULL output is not computed; at least one must be given unless T = 0.
+ * Overlaps, NaN and infinities, and sizes as for moe_expert_gemm_train.
  *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_BACKWARD) bytes
  * moe_combine(p, dx_packed, inv, NULL, dx) sums dx_packed back to token order
  * (the backward pass of dispatch's row gather).
@@ -316,7 +319,8 @@ moe_status_t moe_expert_gemm_backward(const moe_problem_t* p, const void* x_pack
  *   dy_packed[p] = rnd(topk_w[a] * dy[t]),  dtopk_w[a] = sum_i dy[t,i] y_packed[p,i]
  * and dtopk_w[a] = 0 where inv[a] < 0.  Rows of dy_packed that inv does not
  * name are left untouched; the entries of inv must be distinct where not
- * negative.  topk_w = NULL: unit weights.  Outputs must not overlap inputs.
+ * negative.  topk_w = NULL: unit weights.  Outputs must not overlap inputs.  A NaN
+ * in dy or topk_w is one in the rows computed from it.
  *   dy       [T,d] dtype;  y_packed as moe_combine read it (may be NULL with dtopk_w NULL)
  *   dy_packed      dtype output, as many rows as y_packed
  *   dtopk_w  [T,k] fp32 output, or NULL
@@ -332,7 +336,8 @@ moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dy, const 
  * among them) gets scale 0 and zeros, one with an infinity or a NaN that as its
  * scale and zeros (so that every product with it is NaN).
  *   x [rows,K] of dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32;  q [rows,K] int8
- * K a multiple of 8, x 16-byte and q 8-byte aligned; rows >= 0.
+ * K a multiple of 8, x 16-byte and q 8-byte aligned; rows >= 0; x, q and scale do
+ * not overlap.
  */
 moe_status_t moe_quantize_rows(int64_t rows, int32_t K, int32_t dtype, const void* x, int8_t* q,
                                float* scale, void* stream);
@@ -362,7 +367,8 @@ moe_status_t moe_quantize_weights(int32_t n, int32_t K, int32_t N, int32_t dtype
  * (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
  *   A [M,K] int8 row-major, K a multiple of 16;  packed: one matrix [K,N] of
  *   moe_pack_weights or moe_quantize_weights;  C [M,N], N a multiple of 8.
- * A, packed, b_scale and C 16-byte aligned.  M = 0 launches nothing; M at most 2^30.
+ * A, packed, b_scale and C 16-byte aligned; C overlaps none of the others.  A NaN
+ * scale gives NaN in its row or column.  M = 0 launches nothing; M at most 2^30.
  */
 moe_status_t moe_gemm_quantized(int32_t M, int32_t N, int32_t K, const int8_t* A,
                                 const float* a_scale, const void* packed, const float* b_scale,
@@ -379,6 +385,8 @@ moe_status_t moe_gemm_quantized(int32_t M, int32_t N, int32_t K, const int8_t* A
  *   s1, s3 [n_local,f], s2 [n_local,d] fp32 channel scales;  d, f < 131072
  *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_QUANTIZED) bytes
  * Rows >= A of x_packed are not read, those of h and y_packed are left untouched.
+ * Outputs must not overlap inputs or one another.  A row with a NaN or an infinity
+ * gives NaN rows of h and y_packed, and changes no other row.
  */
 moe_status_t moe_expert_gemm_quantized(const moe_problem_t* p, const void* x_packed,
                                        const int32_t* offsets, const void* w1, const float* s1,
