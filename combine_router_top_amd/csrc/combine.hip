@@ -142,13 +142,12 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const u32x4* __re
                                                                const u32x4* __restrict__ yp,
                                                                const int32_t* __restrict__ inv,
                                                                const float* __restrict__ w,
-                                                               u32x4* __restrict__ dyp, float* __restrict__ dw, int T,
-                                                               int k, int nvec) {
+                                                               u32x4* __restrict__ dyp, float* __restrict__ dw, int k,
+                                                               int nvec) {
   __shared__ int s_row[32], s_slot[32];
   __shared__ float s_w[32], s_dot[4][32];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-  if (t >= T) return;
+  const int64_t t = blockIdx.x;
   if (wave == 0) {
     int row = -1;
     float wt = 0.f;
@@ -233,16 +232,22 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const u32x4* __re
 hipError_t launch_combine_backward(const Prob& p, const void* dy, const void* y_packed, const int32_t* inv,
                                    const float* w, void* dy_packed, float* dw, hipStream_t st) {
   const int nvec = (int)((int64_t)p.d * p.elem() / 16);
-  // a dimension of a grid holds fewer than 2^32 work-items: many tokens take two
-  const unsigned gx = (unsigned)std::min(p.T, 1 << 20);
-  const dim3 grid(gx, (unsigned)(((int64_t)p.T + gx - 1) / gx));
-  if (p.dtype == 1)
-    hipLaunchKernelGGL(combine_backward_kernel<true>, grid, dim3(256), 0, st, (const u32x4*)dy,
-                       (const u32x4*)y_packed, inv, w, (u32x4*)dy_packed, dw, p.T, p.k, nvec);
-  else
-    hipLaunchKernelGGL(combine_backward_kernel<false>, grid, dim3(256), 0, st, (const u32x4*)dy,
-                       (const u32x4*)y_packed, inv, w, (u32x4*)dy_packed, dw, p.T, p.k, nvec);
-  return hipGetLastError();
+  // a grid's dimension holds fewer than 2^32 work-items: more tokens take more launches
+  for (int64_t t0 = 0; t0 < p.T; t0 += 1 << 23) {
+    const dim3 grid((unsigned)std::min<int64_t>(p.T - t0, 1 << 23));
+    const u32x4* g = (const u32x4*)dy + t0 * nvec;
+    const int32_t* at = inv + t0 * p.k;
+    const float* wt = w ? w + t0 * p.k : nullptr;
+    float* dwt = dw ? dw + t0 * p.k : nullptr;
+    if (p.dtype == 1)
+      hipLaunchKernelGGL(combine_backward_kernel<true>, grid, dim3(256), 0, st, g, (const u32x4*)y_packed, at, wt,
+                         (u32x4*)dy_packed, dwt, p.k, nvec);
+    else
+      hipLaunchKernelGGL(combine_backward_kernel<false>, grid, dim3(256), 0, st, g, (const u32x4*)y_packed, at, wt,
+                         (u32x4*)dy_packed, dwt, p.k, nvec);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe
