@@ -165,9 +165,10 @@ class Spec:
         return self.T * min(self.k, self.n_local)
 
     def c(self) -> Problem:
-        _fits(self.T | self.d | self.E | self.k | self.f | self.expert_lo | self.n_local, "a size of the problem")
-        return Problem(self.T, self.d, self.E, self.k, self.f, self.expert_lo, self.n_local,
-                       MOE_DTYPE_BF16 if self.dtype == "bf16" else MOE_DTYPE_F32, self.flags)
+        T, d, E, k, f, lo, n = self.T, self.d, self.E, self.k, self.f, self.expert_lo, self.n_local
+        if (T | d | E | k | f | lo | n) >> 31:
+            _fits(T | d | E | k | f | lo | n, "a size of the problem")
+        return Problem(T, d, E, k, f, lo, n, MOE_DTYPE_BF16 if self.dtype == "bf16" else MOE_DTYPE_F32, self.flags)
 
     def ref(self):
         """The C structure by reference, made once: the fields of a Spec do not change."""
