@@ -25,10 +25,20 @@ Functions (same names as the C calls):
     pack_weights(w) -> packed;  quantize_weights(w) -> (packed, scale)   (w [n,K,N] or [K,N])
     gemm_quantized(a, a_scale, packed, b_scale) -> C
     expert_gemm_quantized(p, x_packed, offsets, w1, s1, w3, s3, w2, s2) -> (h, y_packed)
+    select(p, gate, logits, balance=None) -> (topk_idx, topk_w)      (gate: a Gate)
+    route_scored(p, gate, x, w_gate, bias=None, balance=None, want_logits=False)
+        -> (topk_idx, topk_w[, logits])
+    route_backward(p, gate, x, w_gate, logits, topk_idx, dtopk_w, dx_add=None)
+        -> (dlogits, dx, dw_gate, dbias)
+    pack_weights_4bit(q) -> packed;  quantize_weights_4bit(w, group=128, zero=False)
+        -> (packed, scale, zero or None)                             (w [n,K,N] or [K,N])
+    gemm_4bit(a, packed, scale, zero=None, group=128) -> C
+    expert_gemm_4bit(p, x_packed, offsets, w1, s1, z1, w3, s3, z3, w2, s2, z2, group=128)
+        -> (h, y_packed)
     gemm_signal(A, B, flags, epoch) -> C          (C = rnd(A B), a flag per 256 x 256 tile)
     tile_forward(C, dst, flags, epoch, spin_limit, timeouts, workgroups)
 
-The training and 8-bit calls take tensors and streams of the current device only.
+The training, scored-routing, 8-bit and 4-bit calls take tensors and streams of the current device only.
 With ``stream=`` they order nothing against the current stream, and what they allocate
 belongs to the given one: wait for it before reading the outputs elsewhere, and
 ``record_stream`` outputs that outlive such a use.
@@ -51,6 +61,8 @@ MOE_WS_H, MOE_WS_Y_PACKED = 0, 1
 MOE_CALL_ROUTE, MOE_CALL_DISPATCH, MOE_CALL_EXPERT_GEMM, MOE_CALL_COMBINE, MOE_CALL_LAYER = range(5)
 MOE_CALL_DISPATCH_PADDED, MOE_CALL_EXPERT_GEMM_PADDED = 5, 6
 MOE_CALL_EXPERT_GEMM_BACKWARD, MOE_CALL_EXPERT_GEMM_QUANTIZED = 7, 8
+MOE_CALL_ROUTE_SCORED, MOE_CALL_ROUTE_BACKWARD = 9, 10
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_SCOPE_AGENT, MOE_SCOPE_SYSTEM = 0, 1
 
 EXPORTED = ["moe_last_error", "moe_version", "moe_workspace_bytes", "moe_route", "moe_dispatch",
@@ -59,7 +71,9 @@ EXPORTED = ["moe_last_error", "moe_version", "moe_workspace_bytes", "moe_route",
             "moe_dispatch_noalloc", "moe_layer_ws_offset", "moe_layer_set_gemm_events",
             "moe_expert_gemm_train", "moe_expert_gemm_backward", "moe_combine_backward",
             "moe_quantize_rows", "moe_packed_weights_bytes", "moe_pack_weights",
-            "moe_quantize_weights", "moe_gemm_quantized", "moe_expert_gemm_quantized"]
+            "moe_quantize_weights", "moe_gemm_quantized", "moe_expert_gemm_quantized",
+            "moe_select", "moe_route_scored", "moe_route_backward", "moe_packed_weights_4bit_bytes",
+            "moe_pack_weights_4bit", "moe_quantize_weights_4bit", "moe_gemm_4bit", "moe_expert_gemm_4bit"]
 
 
 class MoeError(RuntimeError):
@@ -77,6 +91,11 @@ class Problem(ctypes.Structure):
 class RoutingOut(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("topk_idx", "topk_w", "logits", "counts_all", "offsets", "perm", "inv")]
+
+
+class GateRule(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "groups", "topk_groups", "group_top", "renorm")] + [
+        ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -123,6 +142,19 @@ def lib() -> ctypes.CDLL:
         L.moe_quantize_weights.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp]
         L.moe_gemm_quantized.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i32, vp]
         L.moe_expert_gemm_quantized.argtypes = [P] + [vp] * 11 + [sz, vp]
+        G = ctypes.POINTER(GateRule)
+        L.moe_select.argtypes = [P, G] + [vp] * 5
+        L.moe_route_scored.argtypes = [P, G] + [vp] * 8 + [sz, vp]
+        L.moe_route_backward.argtypes = [P, G] + [vp] * 11 + [sz, vp]
+        L.moe_packed_weights_4bit_bytes.argtypes = [i32, i32, i32]
+        L.moe_packed_weights_4bit_bytes.restype = sz
+        L.moe_pack_weights_4bit.argtypes = [i32, i32, i32, vp, vp, vp]
+        L.moe_quantize_weights_4bit.argtypes = [i32] * 5 + [vp] * 5
+        L.moe_gemm_4bit.argtypes = [i32] * 4 + [vp] * 5 + [i32, vp]
+        L.moe_expert_gemm_4bit.argtypes = [P, i32] + [vp] * 14
+        for n in ("moe_select", "moe_route_scored", "moe_route_backward", "moe_pack_weights_4bit",
+                  "moe_quantize_weights_4bit", "moe_gemm_4bit", "moe_expert_gemm_4bit"):
+            getattr(L, n).restype = i32
         for n in ("moe_expert_gemm_train", "moe_expert_gemm_backward", "moe_combine_backward",
                   "moe_quantize_rows", "moe_pack_weights", "moe_quantize_weights",
                   "moe_gemm_quantized", "moe_expert_gemm_quantized"):
@@ -185,6 +217,39 @@ class Spec:
     def of(w, flags: int = 0) -> "Spec":
         """From any object with T, d, E, k, f, expert_lo, n_local, dtype fields."""
         return Spec(w.T, w.d, w.E, w.k, w.f, w.expert_lo, w.n_local, w.dtype, flags)
+
+
+@dataclass(frozen=True)
+class Gate:
+    """How tokens choose experts from their logits (mirrors moe_gate_t): ``score``
+    "softmax" or "sigmoid"; of ``groups`` groups of neighbouring experts the
+    ``topk_groups`` best stay, a group's value being the sum of its ``group_top`` (1 or
+    2) best experts'; ``renorm``: a token's weights sum to ``scale``."""
+    score: str = "softmax"
+    groups: int = 1
+    topk_groups: int = 1
+    group_top: int = 1
+    renorm: bool = True
+    scale: float = 1.0
+
+    def c(self) -> GateRule:
+        if self.score not in ("softmax", "sigmoid"):
+            raise ValueError(f"score: expected 'softmax' or 'sigmoid', got {self.score!r}")
+        for v in (self.groups, self.topk_groups, self.group_top):
+            _fits(v, "a size of the gate")
+        return GateRule(MOE_SCORE_SIGMOID if self.score == "sigmoid" else MOE_SCORE_SOFTMAX, self.groups,
+                        self.topk_groups, self.group_top, int(bool(self.renorm)), self.scale)
+
+    def ref(self):
+        """The C structure by reference, made once: the fields of a Gate do not change."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
+
+    def __reduce__(self):   # copies and pickles without the reference
+        return Gate, (self.score, self.groups, self.topk_groups, self.group_top, self.renorm, self.scale)
 
 
 def workspace_bytes(p: Spec, call: int = MOE_CALL_LAYER) -> int:
@@ -647,6 +712,188 @@ def expert_gemm_quantized(p: Spec, x_packed, offsets, w1, s1, w3, s3, w2, s2, wo
     outs = (_at(cur, h, tall, dt, "h"), _at(cur, yp, wide, dt, "y_packed"))
     ws, at, size = _workspace_at(cur, p, MOE_CALL_EXPERT_GEMM_QUANTIZED, workspace, stream)
     _check(lib().moe_expert_gemm_quantized(p.ref(), *ins, *outs, at, size, _stream_at(cur, stream)))
+    return h, yp
+
+
+# ---------------------------------------------------------------------------
+# scored routing
+# ---------------------------------------------------------------------------
+def _choice_out(p, device, out, stream):
+    torch = _torch()
+    if out is None:
+        with _alloc_on(stream):
+            out = (torch.empty((p.T, p.k), dtype=torch.int32, device=device),
+                   torch.empty((p.T, p.k), dtype=torch.float32, device=device))
+    return out
+
+
+def select(p: Spec, gate: Gate, logits, balance=None, stream=None, out=None):
+    """(topk_idx, topk_w) from fp32 logits [T, E] by the rule of ``gate``; ``balance`` [E]
+    is added to the scores for the choice alone.  ``out``: the two, written in place."""
+    torch = _torch()
+    cur, slots, f32 = _current(), (p.T, p.k), torch.float32
+    pl = _at(cur, logits, (p.T, p.E), f32, "logits")
+    pb = None if balance is None else _at(cur, balance, (p.E,), f32, "balance")
+    idx, w = _choice_out(p, logits.device, out, stream)
+    _check(lib().moe_select(p.ref(), gate.ref(), pl, pb, _at(cur, idx, slots, torch.int32, "topk_idx"),
+                            _at(cur, w, slots, f32, "topk_w"), _stream_at(cur, stream)))
+    return idx, w
+
+
+def route_scored(p: Spec, gate: Gate, x, w_gate, bias=None, balance=None, want_logits: bool = False,
+                 workspace=None, stream=None, out=None):
+    """``route`` by the rule of ``gate``: (topk_idx, topk_w[, logits]).  ``bias`` is part
+    of the logits, ``balance`` of the choice alone."""
+    torch = _torch()
+    dt, cur, slots, f32 = _dt(p), _current(), (p.T, p.k), torch.float32
+    px, pw = _at(cur, x, (p.T, p.d), dt, "x"), _at(cur, w_gate, (p.d, p.E), dt, "w_gate")
+    pb = None if bias is None else _at(cur, bias, (p.E,), f32, "bias")
+    pc = None if balance is None else _at(cur, balance, (p.E,), f32, "balance")
+    idx, w = _choice_out(p, x.device, out, stream)
+    with _alloc_on(stream):
+        logits = torch.empty((p.T, p.E), dtype=f32, device=x.device) if want_logits else None
+    ws, at, size = _workspace_at(cur, p, MOE_CALL_ROUTE_SCORED, workspace, stream)
+    _check(lib().moe_route_scored(p.ref(), gate.ref(), px, pw, pb, pc, _ptr(logits),
+                                  _at(cur, idx, slots, torch.int32, "topk_idx"), _at(cur, w, slots, f32, "topk_w"),
+                                  at, size, _stream_at(cur, stream)))
+    return (idx, w, logits) if want_logits else (idx, w)
+
+
+def route_backward(p: Spec, gate: Gate, x, w_gate, logits, topk_idx, dtopk_w, dx_add=None, workspace=None,
+                   stream=None, out=None):
+    """Gradients (dlogits, dx, dw_gate, dbias) of ``route_scored`` and ``select``;
+    ``dx_add`` is added to dx.  ``out``: these four, written in place; a None among them
+    is not computed (without dx, ``w_gate`` may be None; without dw_gate, ``x``)."""
+    torch = _torch()
+    dt, cur, slots, f32 = _dt(p), _current(), (p.T, p.k), torch.float32
+    wide, gates, all_e = (p.T, p.d), (p.d, p.E), (p.T, p.E)
+    pl = _at(cur, logits, all_e, f32, "logits")
+    ins = (_at(cur, topk_idx, slots, torch.int32, "topk_idx"), _at(cur, dtopk_w, slots, f32, "dtopk_w"),
+           None if dx_add is None else _at(cur, dx_add, wide, dt, "dx_add"))
+    if out is None:
+        with _alloc_on(stream):
+            dev = logits.device
+            out = (torch.empty(all_e, dtype=f32, device=dev), torch.empty(wide, dtype=dt, device=dev),
+                   torch.empty(gates, dtype=dt, device=dev), torch.empty((p.E,), dtype=f32, device=dev))
+    dl, dx, dwg, db = out
+    px = None if x is None and dwg is None else _at(cur, x, wide, dt, "x")
+    pw = None if w_gate is None and dx is None else _at(cur, w_gate, gates, dt, "w_gate")
+    outs = (None if dl is None else _at(cur, dl, all_e, f32, "dlogits"),
+            None if dx is None else _at(cur, dx, wide, dt, "dx"),
+            None if dwg is None else _at(cur, dwg, gates, dt, "dw_gate"),
+            None if db is None else _at(cur, db, (p.E,), f32, "dbias"))
+    ws, at, size = _workspace_at(cur, p, MOE_CALL_ROUTE_BACKWARD, workspace, stream)
+    _check(lib().moe_route_backward(p.ref(), gate.ref(), px, pw, pl, *ins, *outs, at, size, _stream_at(cur, stream)))
+    return dl, dx, dwg, db
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights
+# ---------------------------------------------------------------------------
+def packed_weights_4bit_shape(K: int, N: int):
+    """Shape of one packed [K, N] matrix of int32 words: (N/16, K/128, 64, 4), rounded up."""
+    return (-(-N // 16), -(-K // 128), 64, 4)
+
+
+def packed_weights_4bit_bytes(n: int, K: int, N: int) -> int:
+    _fits(int(n) | int(K) | int(N), "a size of the weights")
+    b = int(lib().moe_packed_weights_4bit_bytes(int(n), int(K), int(N)))
+    if b == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, lib().moe_last_error().decode())
+    return b
+
+
+def _groups(K: int, group: int) -> int:
+    if group not in (32, 64, 128):
+        raise ValueError(f"group: expected 32, 64 or 128, got {group}")
+    return -(-K // group)
+
+
+def _matrices(w):
+    lead, K, N = tuple(w.shape[:-2]), w.shape[-2], w.shape[-1]
+    if len(lead) > 1:
+        raise ValueError(f"w: expected [n, K, N] or [K, N], got {tuple(w.shape)}")
+    n = lead[0] if lead else 1
+    packed_weights_4bit_bytes(n, K, N)
+    return n, K, N, lead
+
+
+def pack_weights_4bit(q, stream=None, out=None):
+    """uint8 values 0 .. 15 [n, K, N] or [K, N] in the order the 4-bit products read."""
+    torch = _torch()
+    cur = _current()
+    n, K, N, lead = _matrices(q)
+    shape = lead + packed_weights_4bit_shape(K, N)
+    pq = _at(cur, q, q.shape, torch.uint8, "q")
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(shape, dtype=torch.int32, device=q.device)
+    _check(lib().moe_pack_weights_4bit(n, K, N, pq, _at(cur, out, shape, torch.int32, "packed"),
+                                       _stream_at(cur, stream)))
+    return out
+
+
+def quantize_weights_4bit(w, group: int = 128, zero: bool = False, stream=None, out=None):
+    """(packed, scale, zero) of bf16 or fp32 weights [n, K, N] or [K, N]: a bf16 scale, and
+    with ``zero`` a zero point (else None: 8), for each group of K in each column."""
+    torch = _torch()
+    code, cur = _dtype_code(w, "w"), _current()
+    n, K, N, lead = _matrices(w)
+    shape, rows = lead + packed_weights_4bit_shape(K, N), lead + (_groups(K, group), N)
+    pw = _at(cur, w, w.shape, w.dtype, "w")
+    if out is None:
+        with _alloc_on(stream):
+            out = (torch.empty(shape, dtype=torch.int32, device=w.device),
+                   torch.empty(rows, dtype=torch.bfloat16, device=w.device),
+                   torch.empty(rows, dtype=torch.uint8, device=w.device) if zero else None)
+    packed, s, z = out
+    _check(lib().moe_quantize_weights_4bit(
+        n, K, N, group, code, pw, _at(cur, packed, shape, torch.int32, "packed"), _at(cur, s, rows, torch.bfloat16, "scale"),
+        _at(cur, z, rows, torch.uint8, "zero") if zero else None, _stream_at(cur, stream)))
+    return packed, s, z if zero else None
+
+
+def gemm_4bit(a, packed, scale, zero=None, group: int = 128, dtype=None, stream=None, out=None):
+    """C = rnd(a W): bf16 a [M, K], packed 4-bit weights of one [K, N] matrix with their
+    scales and zero points (None: 8); ``dtype`` (default torch.bfloat16, or that of
+    ``out``) is C's."""
+    torch = _torch()
+    cur = _current()
+    M, K = a.shape
+    N = scale.shape[-1]
+    _fits(M | N | K, "a size of the product")
+    rows = (_groups(K, group), N)
+    pa = _at(cur, a, (M, K), torch.bfloat16, "a")
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
+    _check(lib().moe_gemm_4bit(
+        M, N, K, group, pa, _at(cur, packed, packed_weights_4bit_shape(K, N), torch.int32, "packed"),
+        _at(cur, scale, rows, torch.bfloat16, "scale"),
+        None if zero is None else _at(cur, zero, rows, torch.uint8, "zero"),
+        _at(cur, out, (M, N), dtype or out.dtype, "out"), _dtype_code(out, "out"), _stream_at(cur, stream)))
+    return out
+
+
+def expert_gemm_4bit(p: Spec, x_packed, offsets, w1, s1, z1, w3, s3, z3, w2, s2, z2, group: int = 128,
+                     stream=None, out=None):
+    """``expert_gemm`` with packed 4-bit weights [n_local, ...], their scales and zero
+    points (each None or not): (h, y_packed)."""
+    torch = _torch()
+    dt, cur, n = _dt(p), _current(), (p.n_local,)
+    wide, tall, i32, bf, u8 = (p.rows_max, p.d), (p.rows_max, p.f), torch.int32, torch.bfloat16, torch.uint8
+    up, down = n + packed_weights_4bit_shape(p.d, p.f), n + packed_weights_4bit_shape(p.f, p.d)
+    gu, gd = n + (_groups(p.d, group), p.f), n + (_groups(p.f, group), p.d)
+    ins = (_at(cur, x_packed, wide, dt, "x_packed"), _at(cur, offsets, (p.n_local + 1,), i32, "offsets"),
+           _at(cur, w1, up, i32, "w1"), _at(cur, s1, gu, bf, "s1"), None if z1 is None else _at(cur, z1, gu, u8, "z1"),
+           _at(cur, w3, up, i32, "w3"), _at(cur, s3, gu, bf, "s3"), None if z3 is None else _at(cur, z3, gu, u8, "z3"),
+           _at(cur, w2, down, i32, "w2"), _at(cur, s2, gd, bf, "s2"), None if z2 is None else _at(cur, z2, gd, u8, "z2"))
+    if out is None:
+        with _alloc_on(stream):
+            out = tuple(torch.zeros(v, dtype=dt, device=x_packed.device) for v in (tall, wide))
+    h, yp = out
+    _check(lib().moe_expert_gemm_4bit(p.ref(), group, *ins, _at(cur, h, tall, dt, "h"),
+                                      _at(cur, yp, wide, dt, "y_packed"), _stream_at(cur, stream)))
     return h, yp
 
 

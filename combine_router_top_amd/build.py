@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libmoe.so")
 ARCH = "gfx950"
 
 SOURCES = ["route.hip", "dispatch.hip", "expert_gemm.hip", "combine.hip", "tile_forward.hip",
-           "expert_train.hip", "expert_backward.hip", "expert_i8.hip", "moe_api.cpp"]
+           "expert_train.hip", "expert_backward.hip", "expert_i8.hip", "select.hip",
+           "route_backward.hip", "expert_4bit.hip", "moe_api.cpp"]
 # measurement-only streaming-read probe, linked into a library of its own
 PROBE_SOURCE = "hbm_read_probe.hip"
 PROBE_LIB = os.path.join(PKG, "libhbm_probe.so")

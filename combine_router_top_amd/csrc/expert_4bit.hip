@@ -1,0 +1,424 @@
+// Products of bf16 rows with 4-bit weights that have a scale, and perhaps a zero
+// point, for each group of 32, 64 or 128 along K in each output channel, and the
+// SwiGLU expert FFNs built from them.
+//
+//   W[k,j] = (q[k,j] - z[k/G,j]) s[k/G,j]         q, z in 0 .. 15 (z = 8 without zero points)
+//   gemm   C = rnd(A W)
+//   expert h = rnd(SiLU(x W1) (x W3)), y = rnd(h W2)
+//
+// A group's part of a sum is  s (sum x q - z sum x).  The matrix cores take q as the
+// bf16 number 16 + q, which is exact and costs one masked or of the packed bits (q is
+// the upper mantissa of a number in 16 .. 32), so that with X = sum x over the group
+//
+//   part = sum x (16 + q),   C += s (part - (16 + z) X)
+//
+// X is one more product, with ones.  All of it is fp32: no weight is ever rounded.  The
+// offset makes the terms of a part about five times larger than those of the result,
+// two bits of fp32's 24.
+//
+// Packed weights: blocks of 16 columns x 128 K, 1 KB, one 16-byte load per lane and an
+// operand of four MFMA k-steps after the masked ors: [N/16][K/128][64 lanes][4 words],
+// lane 16 a + c holding column c, word s its k = 32 s + 8 a .. + 7, value 2 p + h at
+// bits 16 h + 4 p, the word then rotated left by 3 bits to where the mantissas want it.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "common.h"
+#include "kernels.h"
+#include "seg_tile.h"
+
+namespace moe {
+
+constexpr int W4_KB = 128;   // K of a packed block
+
+// ---------------------------------------------------------------------------
+// quantiser and packing (once per set of weights)
+// ---------------------------------------------------------------------------
+template <bool BF16>
+__device__ __forceinline__ float w4_load(const void* p, int64_t i) {
+  return BF16 ? bf16_to_f32(reinterpret_cast<const bf16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
+}
+
+// Scales and zero points, one thread per group and column.  A group that holds an
+// infinity or a NaN gets that as its scale, so that its products are no plausible numbers.
+template <bool BF16>
+__global__ __launch_bounds__(256) void w4_scales(const void* __restrict__ w, int K, int N, int G, int groups,
+                                                 bf16_t* __restrict__ scale, uint8_t* __restrict__ zero) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= (int64_t)groups * N) return;
+  const int grp = (int)(id / N), col = (int)(id - (int64_t)grp * N);
+  const int64_t base = (int64_t)blockIdx.y * K * N + col;
+  float lo = 0.f, hi = 0.f;
+  uint32_t top = 0;
+  for (int k = grp * G; k < min(K, grp * G + G); ++k) {
+    const float v = w4_load<BF16>(w, base + (int64_t)k * N);
+    top = max(top, __float_as_uint(v) & 0x7FFFFFFFu);
+    lo = fminf(lo, v);
+    hi = fmaxf(hi, v);
+  }
+  const int64_t at = (int64_t)blockIdx.y * groups * N + id;
+  const float big = __uint_as_float(top);
+  float s = zero ? (hi - lo) / 15.0f : big / 7.0f;
+  if (top >= 0x7F800000u) s = big;
+  scale[at] = (bf16_t)cvt_bf16x2(s, 0.f);
+  if (zero) {
+    s = bf16_to_f32(scale[at]);
+    zero[at] = s > 0.f && s < INFINITY ? (uint8_t)fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : (uint8_t)8;
+  }
+}
+
+// One packed block per wave.  MODE 0: values 0 .. 15 as bytes [n][K][N] (higher bits are
+// dropped); 1: bf16, 2: fp32 weights, quantised with the scales and zero points.
+template <int MODE>
+__global__ __launch_bounds__(256) void w4_pack(const void* __restrict__ w, const bf16_t* __restrict__ scale,
+                                               const uint8_t* __restrict__ zero, int K, int N, int G, int groups,
+                                               int kb, int nt, u32x4* __restrict__ out) {
+  const int lane = threadIdx.x & 63, c = lane & 15, a = lane >> 4;
+  const int64_t blk = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (blk >= (int64_t)kb * nt) return;
+  const int tn = (int)(blk / kb), tk = (int)(blk - (int64_t)tn * kb);
+  const int col = 16 * tn + c;
+  const int64_t base = (int64_t)blockIdx.y * K * N + col, gbase = (int64_t)blockIdx.y * groups * N + col;
+  u32x4 o;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    uint32_t word = 0;
+    const int k0 = W4_KB * tk + 32 * s + 8 * a;
+    if (col < N && k0 < K) {   // K is a multiple of 8, a group of 32
+      float sc = 0.f, z = 8.f;
+      if (MODE) {
+        const int64_t g = gbase + (int64_t)(k0 / G) * N;
+        sc = bf16_to_f32(scale[g]);
+        if (zero) z = zero[g];
+      }
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        uint32_t q;
+        if (MODE == 0) {
+          q = reinterpret_cast<const uint8_t*>(w)[base + (int64_t)(k0 + v) * N] & 15u;
+        } else if (sc > 0.f && sc < INFINITY) {
+          const float r = rintf(w4_load<MODE == 1>(w, base + (int64_t)(k0 + v) * N) / sc) + z;
+          q = (uint32_t)fminf(fmaxf(r, zero ? 0.f : 1.f), 15.f);
+        } else {
+          q = (uint32_t)z;
+        }
+        word |= q << (16 * (v & 1) + 4 * (v >> 1));
+      }
+    }
+    o[s] = (word << 3) | (word >> 29);
+  }
+  out[((int64_t)blockIdx.y * kb * nt + blk) * 64 + lane] = o;
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+// Segments: rows [offsets[e], offsets[e+1]) of expert e, or, without offsets, one
+// segment of rows [0, M).
+struct W4Args {
+  const bf16_t* a;         // [*][K]
+  const char* b1;          // packed weights [n][ntiles][kb] blocks
+  const char* b3;          // second matrix of a gated product
+  const bf16_t* s1;        // [n][groups][N]
+  const bf16_t* s3;
+  const uint8_t* z1;       // [n][groups][N] or NULL
+  const uint8_t* z3;
+  void* c;                 // [*][N]
+  const int32_t* offsets;
+  int n, M;
+  int K, N, kb, ntiles, groups;
+};
+
+__device__ __forceinline__ int w4_rows(const W4Args& p, int e, int& o) {
+  int cnt = p.M;
+  o = 0;
+  if (p.offsets) {
+    o = p.offsets[e];
+    cnt = p.offsets[e + 1] - o;
+  }
+  o = __builtin_amdgcn_readfirstlane(o);
+  return __builtin_amdgcn_readfirstlane(cnt);
+}
+
+// The eight numbers 16 + q of a packed word.
+__device__ __forceinline__ u32x4 w4_unpack(uint32_t w) {
+  u32x4 o;
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    o[p] = ((p ? __builtin_amdgcn_alignbit(w, w, 4 * p) : w) & 0x00780078u) | 0x41804180u;
+  return o;
+}
+
+template <bool F32OUT>
+__device__ __forceinline__ void w4_store(void* c, int64_t at, const float (&o)[4]) {
+  if (F32OUT) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(c) + at) = f32x4{o[0], o[1], o[2], o[3]};
+  else
+    *reinterpret_cast<u32x2*>(reinterpret_cast<bf16_t*>(c) + at) =
+        u32x2{cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3])};
+}
+
+// Up to 16 MT rows o .. o + R - 1 against NT 16-column tiles (GATED: NT / 2 of each
+// matrix).  The KS waves split K evenly by blocks; each loads its blocks straight into
+// registers, one ahead of its use, and the fp32 sums meet in LDS in wave order.
+// GPB: groups of a block.
+template <int MT, int NT, bool GATED, bool F32OUT, int KS, int GPB>
+__device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, int R, f32x4* red, int stride) {
+  constexpr int NH = GATED ? NT / 2 : NT, SPG = 4 / GPB;   // k-steps of a group
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile0 = (int)blockIdx.x * NH;
+  const uint32_t run = (uint32_t)p.kb * 1024u;
+  const int per = (p.kb + KS - 1) / KS, s0 = wave * per, ns = max(0, min(per, p.kb - s0));
+  const int64_t ge = (int64_t)e * p.groups * p.N;
+  const uint32_t gsize = (uint32_t)p.groups * (uint32_t)p.N;
+  __amdgpu_buffer_rsrc_t rb[NT], rs[GATED ? 2 : 1], rz[GATED ? 2 : 1];
+  uint32_t vs[NH];   // a lane's four columns of each tile
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const char* base = GATED && t >= NH ? p.b3 : p.b1;
+    const int nt = min(tile0 + t % NH, p.ntiles - 1);
+    rb[t] = gc_rsrc(base + ((int64_t)e * p.ntiles + nt) * run + (int64_t)s0 * 1024, (uint32_t)ns * 1024u);
+  }
+#pragma unroll
+  for (int m = 0; m < (GATED ? 2 : 1); ++m) {
+    const uint8_t* z = m ? p.z3 : p.z1;
+    rs[m] = gc_rsrc((m ? p.s3 : p.s1) + ge, gsize * 2u);
+    rz[m] = gc_rsrc(z ? z + ge : (const uint8_t*)p.a, z ? gsize : 0u);
+  }
+#pragma unroll
+  for (int t = 0; t < NH; ++t) {
+    const int col = 16 * (tile0 + t) + 4 * g;
+    vs[t] = col < p.N ? (uint32_t)col : GC_OOR >> 1;
+  }
+  const __amdgpu_buffer_rsrc_t ra = gc_rsrc(p.a + (int64_t)o * p.K, (uint32_t)R * (uint32_t)p.K * 2u);
+  uint32_t va[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+    va[mt] = 16 * mt + i < R ? ((uint32_t)(16 * mt + i) * (uint32_t)p.K + 8u * (uint32_t)g) * 2u : GC_OOR;
+  const uint32_t vb = 16u * (uint32_t)lane;
+  // what is subtracted from 16 + q: the zero point, 8 where there are none
+  const float zb1 = p.z1 ? -16.f : -24.f, zb3 = GATED && p.z3 ? -16.f : -24.f;
+
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 w[2][NT], x[2][MT][4];
+  u32x2 sc[2][NT][GPB];
+  uint32_t zp[2][NT][GPB];
+  auto load = [&](int h, int b) {   // block b of this wave; one past its last reads zeros
+#pragma unroll
+    for (int t = 0; t < NT; ++t) w[h][t] = __builtin_amdgcn_raw_buffer_load_b128(rb[t], vb, b * 1024, 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = (s0 + b) * W4_KB + 32 * q;
+      const bool in = k + 8 * g < p.K;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        x[h][mt][q] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? va[mt] : GC_OOR, (uint32_t)k * 2u, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int u = 0; u < GPB; ++u) {
+        const int m = GATED && t >= NH;
+        const uint32_t row = (uint32_t)((s0 + b) * GPB + u) * (uint32_t)p.N;
+        sc[h][t][u] = __builtin_amdgcn_raw_buffer_load_b64(rs[m], vs[t % NH] * 2u, row * 2u, 0);
+        zp[h][t][u] = __builtin_amdgcn_raw_buffer_load_b32(rz[m], vs[t % NH], row, 0);
+      }
+  };
+  auto multiply = [&](int h) {
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+#pragma unroll
+    for (int u = 0; u < GPB; ++u) {
+      f32x4 X[MT], part[MT][NT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        X[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) part[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int q = u * SPG; q < (u + 1) * SPG; ++q) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) X[mt] = mfma16(ones, __builtin_bit_cast(bf16x8, x[h][mt][q]), X[mt]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const u32x4 f = w4_unpack(w[h][t][q]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) part[mt][t] = st_mfma(f, x[h][mt][q], part[mt][t]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const u32x2 s2 = sc[h][t][u];
+        const float s[4] = {bf16_lo(s2[0]), bf16_hi(s2[0]), bf16_lo(s2[1]), bf16_hi(s2[1])};
+        const float zb = GATED && t >= NH ? zb3 : zb1;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float z = zb - (float)((zp[h][t][u] >> (8 * r)) & 255u);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) acc[mt][t][r] = fmaf(s[r], fmaf(z, X[mt][r], part[mt][t][r]), acc[mt][t][r]);
+        }
+      }
+    }
+  };
+  if (ns > 0) {
+    load(0, 0);
+    for (int b = 0; b < ns; b += 2) {
+      load(1, b + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (b + 1 == ns) break;
+      load(0, b + 2);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) red[wave * stride + (mt * NT + t) * 64 + lane] = acc[mt][t];
+  __syncthreads();
+  for (int j = wave; j < MT * NH; j += KS) {
+    const int mt = j / NH, t = j - mt * NH;
+    const f32x4* at = red + (mt * NT + t) * 64 + lane;
+    f32x4 p1 = at[0], p3 = at[GATED ? NH * 64 : 0];
+#pragma unroll
+    for (int v = 1; v < KS; ++v) {
+      p1 += at[v * stride];
+      if (GATED) p3 += at[v * stride + NH * 64];
+    }
+    const int row = 16 * mt + i, col = 16 * (tile0 + t) + 4 * g;
+    if (row >= R || col >= p.N) continue;
+    float v4[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v4[r] = GATED ? silu_mul(p1[r], p3[r]) : p1[r];
+    w4_store<F32OUT>(p.c, (int64_t)(o + row) * p.N + col, v4);
+  }
+}
+
+// All rows of a segment, 16 MT at a time, the blocks dealt out over gridDim.z
+// workgroups; longer segments read their weights again for each block, from the caches.
+template <int MT, int NT, bool GATED, bool F32OUT, int KS, int GPB>
+__global__ __launch_bounds__(64 * KS) void w4_stream(W4Args p) {
+  __shared__ __attribute__((aligned(16))) f32x4 red[KS][MT * NT][64];
+  const int e = blockIdx.y;
+  int o;
+  const int R = w4_rows(p, e, o);
+  constexpr int stride = MT * NT * 64;
+  const int step = 16 * MT * (int)gridDim.z;
+  for (int r0 = 16 * MT * (int)blockIdx.z; r0 < R; r0 += step) {
+    if (r0 >= step) __syncthreads();   // the sums before have been read
+    if (MT == 1 || R - r0 <= 16)
+      w4_stream_block<1, NT, GATED, F32OUT, KS, GPB>(p, e, o + r0, min(16, R - r0), &red[0][0][0], stride);
+    else w4_stream_block<MT, NT, GATED, F32OUT, KS, GPB>(p, e, o + r0, min(16 * MT, R - r0), &red[0][0][0], stride);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+template <bool GATED, bool F32OUT, int GPB>
+static hipError_t launch_4bit_group(const W4Args& p, int64_t mean, int64_t most, hipStream_t st) {
+  const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
+  const int64_t blocks = std::min<int64_t>((most + 31) / 32, p.offsets ? 4 : 1024);
+  auto go = [&](auto kernel, int cols, int ks) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n, (unsigned)blocks), dim3(64 * ks), 0,
+                       st, p);
+    return hipGetLastError();
+  };
+  constexpr int NT = GATED ? 2 : 1;
+  if (most <= 16)
+    return wide ? go(w4_stream<1, 4, GATED, F32OUT, 4, GPB>, GATED ? 32 : 64, 4)
+                : go(w4_stream<1, NT, GATED, F32OUT, 8, GPB>, 16, 8);
+  return wide ? go(w4_stream<2, 4, GATED, F32OUT, 4, GPB>, GATED ? 32 : 64, 4)
+              : go(w4_stream<2, NT, GATED, F32OUT, 8, GPB>, 16, 8);
+}
+
+template <bool GATED, bool F32OUT>
+static hipError_t launch_4bit(const W4Args& p, int group, int64_t mean, int64_t most, hipStream_t st) {
+  return group == 32   ? launch_4bit_group<GATED, F32OUT, 4>(p, mean, most, st)
+         : group == 64 ? launch_4bit_group<GATED, F32OUT, 2>(p, mean, most, st)
+                       : launch_4bit_group<GATED, F32OUT, 1>(p, mean, most, st);
+}
+
+size_t packed_4bit_bytes(int n, int K, int N) {
+  return (size_t)n * ((K + W4_KB - 1) / W4_KB) * ((N + 15) / 16) * 1024;
+}
+
+hipError_t launch_pack_4bit(int n, int K, int N, const void* w, void* packed, hipStream_t st) {
+  const int kb = (K + W4_KB - 1) / W4_KB, nt = (N + 15) / 16;
+  hipLaunchKernelGGL(w4_pack<0>, dim3((unsigned)(((int64_t)kb * nt + 3) / 4), (unsigned)n), dim3(256), 0, st, w,
+                     (const bf16_t*)nullptr, (const uint8_t*)nullptr, K, N, 32, 0, kb, nt, (u32x4*)packed);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_4bit(int n, int K, int N, int group, int dtype, const void* w, void* packed, void* scale,
+                                void* zero, hipStream_t st) {
+  const int kb = (K + W4_KB - 1) / W4_KB, nt = (N + 15) / 16, groups = (K + group - 1) / group;
+  const dim3 g1((unsigned)(((int64_t)groups * N + 255) / 256), (unsigned)n);
+  const dim3 g2((unsigned)(((int64_t)kb * nt + 3) / 4), (unsigned)n);
+  auto scales = dtype == 1 ? w4_scales<true> : w4_scales<false>;
+  auto pack = dtype == 1 ? w4_pack<1> : w4_pack<2>;
+  hipLaunchKernelGGL(scales, g1, dim3(256), 0, st, w, K, N, group, groups, (bf16_t*)scale, (uint8_t*)zero);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(pack, g2, dim3(256), 0, st, w, (const bf16_t*)scale, (const uint8_t*)zero, K, N, group, groups, kb, nt,
+                     (u32x4*)packed);
+  return hipGetLastError();
+}
+
+static W4Args w4_args(int n, int K, int N, int group) {
+  W4Args p{};
+  p.n = n;
+  p.K = K;
+  p.N = N;
+  p.kb = (K + W4_KB - 1) / W4_KB;
+  p.ntiles = (N + 15) / 16;
+  p.groups = (K + group - 1) / group;
+  return p;
+}
+
+hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const void* packed, const void* scale,
+                            const void* zero, void* c, int out_dtype, hipStream_t st) {
+  W4Args p = w4_args(1, K, N, group);
+  p.M = M;
+  p.a = (const bf16_t*)a;
+  p.b1 = (const char*)packed;
+  p.s1 = (const bf16_t*)scale;
+  p.z1 = (const uint8_t*)zero;
+  p.c = c;
+  return out_dtype == 1 ? launch_4bit<false, false>(p, group, M, M, st) : launch_4bit<false, true>(p, group, M, M, st);
+}
+
+hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int32_t* offsets, const Weights4& w1,
+                              const Weights4& w3, const Weights4& w2, void* h, void* y, hipStream_t st) {
+  const int64_t mean = p.tk() / p.E;
+  W4Args a = w4_args(p.n, p.d, p.f, group);
+  a.offsets = offsets;
+  a.a = (const bf16_t*)x;
+  a.b1 = (const char*)w1.w;
+  a.s1 = (const bf16_t*)w1.scale;
+  a.z1 = (const uint8_t*)w1.zero;
+  a.b3 = (const char*)w3.w;
+  a.s3 = (const bf16_t*)w3.scale;
+  a.z3 = (const uint8_t*)w3.zero;
+  a.c = h;
+  const hipError_t e = launch_4bit<true, false>(a, group, mean, p.T, st);
+  if (e != hipSuccess) return e;
+  W4Args b = w4_args(p.n, p.f, p.d, group);
+  b.offsets = offsets;
+  b.a = (const bf16_t*)h;
+  b.b1 = (const char*)w2.w;
+  b.s1 = (const bf16_t*)w2.scale;
+  b.z1 = (const uint8_t*)w2.zero;
+  b.c = y;
+  return launch_4bit<false, false>(b, group, mean, p.T, st);
+}
+
+}  // namespace moe

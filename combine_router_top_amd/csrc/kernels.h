@@ -19,6 +19,29 @@ hipError_t launch_route(const Prob& p, const void* x, const void* wg, const floa
                         int32_t* chunk_hist = nullptr, int64_t hist_elems = 0,
                         bool* hist_done = nullptr);
 
+// The router's product alone: fp32 sums [splits][T][E] into ws (route_ws_bytes).
+int route_splits(const Prob& p);
+hipError_t launch_route_product(const Prob& p, const void* x, const void* wg, void* ws, hipStream_t st);
+
+// select.hip: how experts are chosen from their logits.
+struct SelectRule {
+  int softmax;       // scores: softmax, else sigmoid
+  int groups, topk_groups, group_top;
+  int renorm;
+  int by_logit;      // softmax without a bias: the logits order the experts
+  int lanes;         // lanes that work on a group: 64 / groups, down to a power of two
+  float scale;
+};
+// part: fp32 sums [nsplit][T][E]; logits (or NULL) receives their total plus bias.
+hipError_t launch_select(const Prob& p, const SelectRule& r, const float* part, int nsplit, const float* bias,
+                         const float* balance, float* logits, int32_t* idx, float* w, hipStream_t st);
+
+// route_backward.hip: gradients of the router; any output may be NULL.
+size_t route_backward_ws_bytes(const Prob& p);
+hipError_t launch_route_backward(const Prob& p, const SelectRule& r, const void* x, const void* wg, const float* logits,
+                                 const int32_t* idx, const float* dw, const void* dx_add, float* dlogits, void* dx,
+                                 void* dwg, float* dbias, void* ws, hipStream_t st);
+
 // dispatch.hip
 size_t dispatch_ws_bytes(const Prob& p);
 // hist_ready: ws already holds the chunk histograms (filled by top-k), so the
@@ -113,5 +136,21 @@ size_t expert_i8_ws_bytes(const Prob& p);
 hipError_t launch_expert_i8(const Prob& p, const void* x, const int32_t* offsets, const void* q1, const float* s1,
                             const void* q3, const float* s3, const void* q2, const float* s2, void* h, void* y,
                             void* ws, hipStream_t st);
+
+// expert_4bit.hip: products with 4-bit weights in groups of `group` along K; zero
+// points may be NULL (8).
+size_t packed_4bit_bytes(int n, int K, int N);
+hipError_t launch_pack_4bit(int n, int K, int N, const void* w, void* packed, hipStream_t st);
+hipError_t launch_quantize_4bit(int n, int K, int N, int group, int dtype, const void* w, void* packed, void* scale,
+                                void* zero, hipStream_t st);
+hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const void* packed, const void* scale,
+                            const void* zero, void* c, int out_dtype, hipStream_t st);
+struct Weights4 {
+  const void* w;      // packed [n]
+  const void* scale;  // bf16 [n][groups][N]
+  const void* zero;   // uint8 [n][groups][N] or NULL
+};
+hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int32_t* offsets, const Weights4& w1,
+                              const Weights4& w3, const Weights4& w2, void* h, void* y, hipStream_t st);
 
 }  // namespace moe

@@ -3,6 +3,7 @@
 // rejected (and testable) on a machine without a GPU.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -124,6 +125,8 @@ size_t call_ws_bytes(const moe::Prob& p, int32_t call) {
     case MOE_CALL_EXPERT_GEMM_PADDED: return moe::expert_gemm_ws_bytes(p);
     case MOE_CALL_EXPERT_GEMM_BACKWARD: return moe::expert_backward_ws_bytes(p);
     case MOE_CALL_EXPERT_GEMM_QUANTIZED: return moe::expert_i8_ws_bytes(p);
+    case MOE_CALL_ROUTE_SCORED: return moe::route_ws_bytes(p);
+    case MOE_CALL_ROUTE_BACKWARD: return moe::route_backward_ws_bytes(p);
     default: return 0;
   }
 }
@@ -192,6 +195,55 @@ moe_status_t check_packed(int32_t n, int32_t K, int32_t N) {
   if (N > kMaxQuantN) return fail(MOE_ERR_UNSUPPORTED, "N=%d must be at most %d", N, kMaxQuantN);
   if ((int64_t)K * N >= ((int64_t)1 << 31))
     return fail(MOE_ERR_UNSUPPORTED, "a weight matrix exceeds 2 GiB (K=%d N=%d)", K, N);
+  return MOE_OK;
+}
+
+// Rules of the scored routing calls for a valid problem.
+moe_status_t check_gate(const moe_gate_t* g, const moe::Prob& p, bool balance, moe::SelectRule* out) {
+  if (!g) return fail(MOE_ERR_INVALID_ARG, "gate is NULL");
+  if (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARG, "score %d is neither MOE_SCORE_SOFTMAX nor MOE_SCORE_SIGMOID", g->score);
+  if (g->groups <= 0 || p.E % g->groups != 0)
+    return fail(MOE_ERR_INVALID_ARG, "groups=%d must divide E=%d", g->groups, p.E);
+  if (g->groups > 64) return fail(MOE_ERR_UNSUPPORTED, "groups=%d > 64 not supported", g->groups);
+  const int per = p.E / g->groups;
+  if (g->topk_groups <= 0 || g->topk_groups > g->groups)
+    return fail(MOE_ERR_INVALID_ARG, "topk_groups=%d outside [1, groups=%d]", g->topk_groups, g->groups);
+  if (g->group_top < 1 || g->group_top > 2 || (g->groups > 1 && g->group_top > per))
+    return fail(MOE_ERR_INVALID_ARG, "group_top=%d must be 1 or 2 and at most E/groups=%d", g->group_top, per);
+  if (p.k > g->topk_groups * per)
+    return fail(MOE_ERR_INVALID_ARG, "k=%d exceeds the %d experts of topk_groups=%d", p.k, g->topk_groups * per,
+                g->topk_groups);
+  if (g->renorm != 0 && g->renorm != 1) return fail(MOE_ERR_INVALID_ARG, "renorm=%d must be 0 or 1", g->renorm);
+  if (!std::isfinite(g->scale)) return fail(MOE_ERR_INVALID_ARG, "scale must be finite");
+  out->softmax = g->score == MOE_SCORE_SOFTMAX;
+  out->groups = g->groups;
+  out->topk_groups = g->topk_groups;
+  out->group_top = g->group_top;
+  out->renorm = g->renorm;
+  out->by_logit = out->softmax && !balance;
+  out->lanes = 64;
+  while (out->lanes * g->groups > 64) out->lanes /= 2;
+  out->scale = g->scale;
+  return MOE_OK;
+}
+
+// 4-bit weights: K bounded so that 32 rows of it are addressed with 32-bit offsets.
+moe_status_t check_packed_4bit(int32_t n, int32_t K, int32_t N) {
+  if (n <= 0 || K <= 0 || N <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "n=%d K=%d N=%d must be positive", n, K, N);
+  if (n > 1024) return fail(MOE_ERR_UNSUPPORTED, "n=%d > 1024 not supported", n);
+  if (K % 8 != 0 || N % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "K=%d and N=%d must be multiples of 8", K, N);
+  if (K > 1 << 20 || N > kMaxQuantN)
+    return fail(MOE_ERR_UNSUPPORTED, "K=%d must be at most %d and N=%d at most %d", K, 1 << 20, N, kMaxQuantN);
+  if ((int64_t)K * N >= ((int64_t)1 << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "a weight matrix has 2^31 elements or more (K=%d N=%d)", K, N);
+  return MOE_OK;
+}
+
+moe_status_t check_group(int32_t group) {
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MOE_ERR_UNSUPPORTED, "group=%d must be 32, 64 or 128", group);
   return MOE_OK;
 }
 
@@ -264,7 +316,7 @@ size_t moe_layer_ws_offset(const moe_problem_t* p, int32_t what) {
 size_t moe_workspace_bytes(const moe_problem_t* p, int32_t call) {
   moe::Prob q;
   if (check_problem(p, &q) != MOE_OK) return 0;
-  if (call < MOE_CALL_ROUTE || call > MOE_CALL_EXPERT_GEMM_QUANTIZED) {
+  if (call < MOE_CALL_ROUTE || call > MOE_CALL_ROUTE_BACKWARD) {
     fail(MOE_ERR_INVALID_ARG, "unknown call %d", call);
     return 0;
   }
@@ -630,6 +682,186 @@ moe_status_t moe_expert_gemm_quantized(const moe_problem_t* p, const void* x_pac
   return hip_status(moe::launch_expert_i8(q, x_packed, offsets, w1, s1, w3, s3, w2, s2, h, y_packed,
                                           workspace, (hipStream_t)stream),
                     "moe_expert_gemm_quantized");
+}
+
+moe_status_t moe_select(const moe_problem_t* p, const moe_gate_t* gate, const float* logits,
+                        const float* balance, int32_t* topk_idx, float* topk_w, void* stream) {
+  moe::Prob q;
+  moe::SelectRule r;
+  moe_status_t st = check_problem(p, &q);
+  if (st != MOE_OK) return st;
+  if ((st = check_gate(gate, q, balance != nullptr, &r)) != MOE_OK) return st;
+  if (q.T == 0) return ok();  // empty batch: nothing to choose
+  NEED_PTR(logits);
+  NEED_PTR(topk_idx);
+  NEED_PTR(topk_w);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_select(q, r, logits, 1, nullptr, balance, nullptr, topk_idx, topk_w,
+                                       (hipStream_t)stream),
+                    "moe_select");
+}
+
+moe_status_t moe_route_scored(const moe_problem_t* p, const moe_gate_t* gate, const void* x,
+                              const void* w_gate, const float* bias, const float* balance,
+                              float* logits, int32_t* topk_idx, float* topk_w, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  moe::Prob q;
+  moe::SelectRule r;
+  moe_status_t st = check_problem(p, &q);
+  if (st != MOE_OK) return st;
+  if ((st = check_gate(gate, q, balance != nullptr, &r)) != MOE_OK) return st;
+  NEED_PTR(w_gate);
+  NEED_ALIGNED(w_gate);
+  if (q.T == 0) return ok();  // empty batch: nothing to route
+  NEED_PTR(x);
+  NEED_PTR(topk_idx);
+  NEED_PTR(topk_w);
+  NEED_ALIGNED(x);
+  if ((st = check_ws(q, MOE_CALL_ROUTE_SCORED, workspace, workspace_bytes)) != MOE_OK) return st;
+  (void)hipGetLastError();
+  hipError_t e = moe::launch_route_product(q, x, w_gate, workspace, (hipStream_t)stream);
+  if (e == hipSuccess)
+    e = moe::launch_select(q, r, static_cast<const float*>(workspace), moe::route_splits(q), bias, balance, logits,
+                           topk_idx, topk_w, (hipStream_t)stream);
+  return hip_status(e, "moe_route_scored");
+}
+
+moe_status_t moe_route_backward(const moe_problem_t* p, const moe_gate_t* gate, const void* x,
+                                const void* w_gate, const float* logits, const int32_t* topk_idx,
+                                const float* dtopk_w, const void* dx_add, float* dlogits, void* dx,
+                                void* dw_gate, float* dbias, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  moe::Prob q;
+  moe::SelectRule r;
+  moe_status_t st = check_problem(p, &q);
+  if (st != MOE_OK) return st;
+  if ((st = check_gate(gate, q, true, &r)) != MOE_OK) return st;
+  if (q.d > 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "d=%d must be at most %d", q.d, 1 << 20);
+  if (q.dtype == MOE_DTYPE_F32 && q.T > 1 << 27)
+    return fail(MOE_ERR_UNSUPPORTED, "T=%d fp32 rows, at most %d", q.T, 1 << 27);
+  if (q.T > 0 && !dlogits && !dx && !dw_gate && !dbias)   // an empty batch's dlogits and dx may be NULL
+    return fail(MOE_ERR_INVALID_ARG, "dlogits, dx, dw_gate and dbias are all NULL");
+  if (dx) NEED_PTR(w_gate);
+  if (dx_add && !dx && q.T > 0) return fail(MOE_ERR_INVALID_ARG, "dx_add without dx");
+  NEED_ALIGNED(w_gate);
+  NEED_ALIGNED(dw_gate);
+  if (q.T > 0) {  // an empty batch only zeroes dw_gate and dbias
+    NEED_PTR(logits);
+    NEED_PTR(topk_idx);
+    NEED_PTR(dtopk_w);
+    if (dw_gate) NEED_PTR(x);
+    NEED_ALIGNED(x);
+    NEED_ALIGNED(dx_add);
+    NEED_ALIGNED(dx);
+  }
+  if ((st = check_ws(q, MOE_CALL_ROUTE_BACKWARD, workspace, workspace_bytes)) != MOE_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(moe::launch_route_backward(q, r, x, w_gate, logits, topk_idx, dtopk_w, dx_add, dlogits, dx,
+                                               dw_gate, dbias, workspace, (hipStream_t)stream),
+                    "moe_route_backward");
+}
+
+size_t moe_packed_weights_4bit_bytes(int32_t n, int32_t K, int32_t N) {
+  if (check_packed_4bit(n, K, N) != MOE_OK) return 0;
+  ok();
+  return moe::packed_4bit_bytes(n, K, N);
+}
+
+moe_status_t moe_pack_weights_4bit(int32_t n, int32_t K, int32_t N, const uint8_t* q, void* packed,
+                                   void* stream) {
+  moe_status_t st;
+  if ((st = check_packed_4bit(n, K, N)) != MOE_OK) return st;
+  NEED_PTR(q);
+  NEED_PTR(packed);
+  NEED_ALIGNED(packed);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_pack_4bit(n, K, N, q, packed, (hipStream_t)stream), "moe_pack_weights_4bit");
+}
+
+#define NEED_GROUPS(scale, zero)                                                                \
+  do {                                                                                          \
+    NEED_PTR(scale);                                                                            \
+    if ((reinterpret_cast<uintptr_t>(scale) & 7u) != 0)                                         \
+      return fail(MOE_ERR_UNSUPPORTED, "%s is not 8-byte aligned", #scale);                     \
+    if ((reinterpret_cast<uintptr_t>(zero) & 3u) != 0)                                          \
+      return fail(MOE_ERR_UNSUPPORTED, "%s is not 4-byte aligned", #zero);                      \
+  } while (0)
+
+moe_status_t moe_quantize_weights_4bit(int32_t n, int32_t K, int32_t N, int32_t group,
+                                       int32_t dtype, const void* w, void* packed, void* scale,
+                                       uint8_t* zero, void* stream) {
+  moe_status_t st;
+  if ((st = check_packed_4bit(n, K, N)) != MOE_OK) return st;
+  if ((st = check_group(group)) != MOE_OK) return st;
+  if ((st = check_dtype(dtype)) != MOE_OK) return st;
+  NEED_PTR(w);
+  NEED_PTR(packed);
+  NEED_GROUPS(scale, zero);
+  NEED_ALIGNED(w);
+  NEED_ALIGNED(packed);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_quantize_4bit(n, K, N, group, dtype, w, packed, scale, zero, (hipStream_t)stream),
+                    "moe_quantize_weights_4bit");
+}
+
+moe_status_t moe_gemm_4bit(int32_t M, int32_t N, int32_t K, int32_t group, const void* A,
+                           const void* packed, const void* scale, const uint8_t* zero, void* C,
+                           int32_t out_dtype, void* stream) {
+  moe_status_t st;
+  if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M=%d must be >= 0", M);
+  if ((st = check_packed_4bit(1, K, N)) != MOE_OK) return st;
+  if ((st = check_group(group)) != MOE_OK) return st;
+  if (M > 1 << 30)   // row blocks are counted in 32 bits
+    return fail(MOE_ERR_UNSUPPORTED, "M=%d must be at most %d", M, 1 << 30);
+  if ((st = check_dtype(out_dtype)) != MOE_OK) return st;
+  NEED_PTR(packed);
+  NEED_ALIGNED(packed);
+  NEED_GROUPS(scale, zero);
+  if (M == 0) return ok();
+  NEED_PTR(A);
+  NEED_PTR(C);
+  NEED_ALIGNED(A);
+  NEED_ALIGNED(C);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_gemm_4bit(M, N, K, group, A, packed, scale, zero, C, out_dtype, (hipStream_t)stream),
+                    "moe_gemm_4bit");
+}
+
+moe_status_t moe_expert_gemm_4bit(const moe_problem_t* p, int32_t group, const void* x_packed,
+                                  const int32_t* offsets, const void* w1, const void* s1,
+                                  const uint8_t* z1, const void* w3, const void* s3,
+                                  const uint8_t* z3, const void* w2, const void* s2,
+                                  const uint8_t* z2, void* h, void* y_packed, void* stream) {
+  moe::Prob q;
+  moe_status_t st = check_problem(p, &q);
+  if (st != MOE_OK) return st;
+  if (q.dtype != MOE_DTYPE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "4-bit experts take bf16 rows (dtype %d)", q.dtype);
+  if ((st = check_group(group)) != MOE_OK) return st;
+  if ((st = check_packed_4bit(q.n, q.d, q.f)) != MOE_OK) return st;
+  if ((st = check_packed_4bit(q.n, q.f, q.d)) != MOE_OK) return st;
+  NEED_PTR(offsets);
+  NEED_PTR(w1);
+  NEED_PTR(w3);
+  NEED_PTR(w2);
+  NEED_ALIGNED(w1);
+  NEED_ALIGNED(w3);
+  NEED_ALIGNED(w2);
+  NEED_GROUPS(s1, z1);
+  NEED_GROUPS(s3, z3);
+  NEED_GROUPS(s2, z2);
+  if (q.T == 0) return ok();  // empty batch: no rows
+  NEED_PTR(x_packed);
+  NEED_PTR(h);
+  NEED_PTR(y_packed);
+  NEED_ALIGNED(x_packed);
+  NEED_ALIGNED(h);
+  NEED_ALIGNED(y_packed);
+  (void)hipGetLastError();
+  return hip_status(moe::launch_expert_4bit(q, group, x_packed, offsets, moe::Weights4{w1, s1, z1},
+                                            moe::Weights4{w3, s3, z3}, moe::Weights4{w2, s2, z2}, h, y_packed,
+                                            (hipStream_t)stream),
+                    "moe_expert_gemm_4bit");
 }
 
 int64_t moe_gemm_signal_tiles(int32_t M, int32_t N) {

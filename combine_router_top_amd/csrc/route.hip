@@ -751,7 +751,7 @@ static int route_mt(const Prob& p) {
   return rw_blocks(p, RW_MT_LONG) * rw_splits(p, RW_MT_LONG) >= 128 ? RW_MT_LONG : RW_MT_SHORT;
 }
 
-static int route_splits(const Prob& p) {
+int route_splits(const Prob& p) {
   switch (route_kind(p)) {
     case ROUTE_DMA: return rd_splits(p);
     case ROUTE_WIDE: return rw_splits(p, route_mt(p));
@@ -769,15 +769,9 @@ size_t route_ws_bytes(const Prob& p) {
   return (size_t)route_splits(p) * p.T * p.E * sizeof(float);
 }
 
-hipError_t launch_route(const Prob& p, const void* x, const void* wg, const float* bias,
-                        float* logits, int32_t* idx, float* w, void* ws, hipStream_t st,
-                        int32_t* chunk_hist, int64_t hist_elems, bool* hist_done) {
-  float* part = reinterpret_cast<float*>(ws);
-  const RouteKind kind = route_kind(p);
-  const int S = route_splits(p);
-  // the chunk histograms are filled by top-k only behind router_dma, which clears them first
-  int32_t* hist = (kind == ROUTE_DMA && chunk_hist && hist_elems > 0) ? chunk_hist : nullptr;
-  if (hist_done) *hist_done = hist != nullptr;
+// The product; hist[0 .. hist_elems) is cleared by router_dma (or NULL).
+static hipError_t launch_product(const Prob& p, RouteKind kind, int S, const void* x, const void* wg, float* part,
+                                 int32_t* hist, int64_t hist_elems, hipStream_t st) {
   if (kind == ROUTE_DMA) {
     const int kc = route_kchunk(p, S, RD_KS);
     const int ncb = (int)rd_col_blocks(p);
@@ -806,7 +800,23 @@ hipError_t launch_route(const Prob& p, const void* x, const void* wg, const floa
       hipLaunchKernelGGL(router_plain<float>, grid, dim3(256), 0, st, (const float*)x,
                          (const float*)wg, part, p.T, p.d, p.E);
   }
-  hipError_t e = hipGetLastError();
+  return hipGetLastError();
+}
+
+hipError_t launch_route_product(const Prob& p, const void* x, const void* wg, void* ws, hipStream_t st) {
+  return launch_product(p, route_kind(p), route_splits(p), x, wg, (float*)ws, nullptr, 0, st);
+}
+
+hipError_t launch_route(const Prob& p, const void* x, const void* wg, const float* bias,
+                        float* logits, int32_t* idx, float* w, void* ws, hipStream_t st,
+                        int32_t* chunk_hist, int64_t hist_elems, bool* hist_done) {
+  float* part = reinterpret_cast<float*>(ws);
+  const RouteKind kind = route_kind(p);
+  const int S = route_splits(p);
+  // the chunk histograms are filled by top-k only behind router_dma, which clears them first
+  int32_t* hist = (kind == ROUTE_DMA && chunk_hist && hist_elems > 0) ? chunk_hist : nullptr;
+  if (hist_done) *hist_done = hist != nullptr;
+  const hipError_t e = launch_product(p, kind, S, x, wg, part, hist, hist_elems, st);
   if (e != hipSuccess) return e;
   const int nv = (p.E + 63) / 64;
   if (S >= TK_MULTI_MIN_SPLITS) {

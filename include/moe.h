@@ -23,6 +23,12 @@
  *   moe_quantize_rows, moe_quantize_weights, moe_pack_weights,
  *   moe_gemm_quantized, moe_expert_gemm_quantized
  *                    the experts served with 8-bit weights and activations
+ *   moe_select, moe_route_scored, moe_route_backward
+ *                    routing by softmax or sigmoid scores with a balance bias and
+ *                    groups of experts, and the router's gradients
+ *   moe_quantize_weights_4bit, moe_pack_weights_4bit, moe_gemm_4bit,
+ *   moe_expert_gemm_4bit
+ *                    the experts served with 4-bit weights in groups along K
  *   moe_gemm_signal, moe_tile_forward
  *                    GEMM with per-tile completion flags and their consumer
  *                    (the local half of the pages' GEMM + AllGather)
@@ -96,7 +102,9 @@ enum {
   MOE_CALL_DISPATCH_PADDED = 5,
   MOE_CALL_EXPERT_GEMM_PADDED = 6,
   MOE_CALL_EXPERT_GEMM_BACKWARD = 7,
-  MOE_CALL_EXPERT_GEMM_QUANTIZED = 8
+  MOE_CALL_EXPERT_GEMM_QUANTIZED = 8,
+  MOE_CALL_ROUTE_SCORED = 9,
+  MOE_CALL_ROUTE_BACKWARD = 10
 };
 
 /*
@@ -167,6 +175,87 @@ size_t moe_workspace_bytes(const moe_problem_t* p, int32_t call);
 moe_status_t moe_route(const moe_problem_t* p, const void* x, const void* w_gate,
                        const float* bias, float* logits, int32_t* topk_idx, float* topk_w,
                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * How moe_select, moe_route_scored and moe_route_backward turn logits into experts and
+ * weights.
+ *   score        MOE_SCORE_SOFTMAX: s = softmax over all E; MOE_SCORE_SIGMOID: each
+ *                expert's s = 1 / (1 + exp(-l))
+ *   groups       groups of E / groups neighbouring experts (a divisor of E, 1..64);
+ *                1: no groups
+ *   topk_groups  groups that a token chooses from, 1..groups; k at most
+ *                topk_groups * E / groups
+ *   group_top    a group's value is the sum of its 1 or 2 best experts' (with groups > 1
+ *                at most E / groups)
+ *   renorm       0 or 1: a token's k weights sum to `scale`
+ *   scale        factor of all weights, finite
+ * groups = topk_groups = group_top = renorm = 1, scale = 1 and softmax scores are
+ * moe_route's rule.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct moe_gate_t {
+  int32_t score, groups, topk_groups, group_top, renorm;
+  float scale;
+} moe_gate_t;
+
+/*
+ * Experts and weights of every token from its logits l.  With c = s + balance:
+ * of the groups, the topk_groups of largest value (ties to the lower group) stay; of
+ * their experts the k of largest c, descending, ties to the lower expert index, are
+ * the token's; its weights are w_j = scale * s_j, with renorm scale * s_j / sum_i s_i.
+ * The order is that of c in 64 bits (softmax scores without a balance bias: that of
+ * the logits).  balance moves the choice alone, not the weights.
+ * An expert whose logit or balance is -inf comes after every other one of the groups
+ * that stay, and a score of 0 gives weight 0 (all k of them zero under renorm too).  A
+ * row with a NaN logit, or under softmax a logit of +inf, gives NaN weights where its
+ * scores are NaN; topk_idx holds k distinct experts in [0, E) for any input.
+ * Only T, E and k of p are used (the others have to be valid).
+ *   logits   [T,E] fp32
+ *   balance  [E]   fp32, or NULL (zeros)
+ *   topk_idx [T,k] int32 output;  topk_w [T,k] fp32 output
+ */
+moe_status_t moe_select(const moe_problem_t* p, const moe_gate_t* gate, const float* logits,
+                        const float* balance, int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
+ * moe_route with that rule: logits[t,e] = sum_i x[t,i] * w_gate[i,e] (+ bias[e]) as
+ * there, then moe_select.  bias is part of the logits, balance is not.
+ *   workspace of moe_workspace_bytes(p, MOE_CALL_ROUTE_SCORED) bytes
+ */
+moe_status_t moe_route_scored(const moe_problem_t* p, const moe_gate_t* gate, const void* x,
+                              const void* w_gate, const float* bias, const float* balance,
+                              float* logits, int32_t* topk_idx, float* topk_w, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Backward pass of moe_route_scored (and, with its rule, of moe_route): from dtopk_w,
+ * as moe_combine_backward gives it, with the logits and topk_idx of the forward pass.
+ * The choice itself has no gradient.  With sums over the token's k experts e_j, g_j =
+ * scale * dtopk_w[t,j], p_j = s_j / sum_i s_i and m = sum_i g_i p_i:
+ *   sigmoid          dlogits[t,e_j] = g_j s_j (1 - s_j)
+ *   sigmoid, renorm  dlogits[t,e_j] = p_j (1 - s_j) (g_j - m)
+ *   softmax, renorm  dlogits[t,e_j] = p_j (g_j - m)        each 0 for other experts
+ *   softmax          dlogits[t,e]   = s_e ((e = e_j ? g_j : 0) - sum_i g_i s_i), all e
+ * and with dl = rnd(dlogits)
+ *   dx = rnd(dx_add + dl w_gate^T),  dw_gate = rnd(x^T dl),  dbias = sum_t dlogits[t]
+ * with fp32 accumulation.  Every element of the outputs is written (zeros of dw_gate
+ * and dbias for T = 0 too).  d at most 2^20, in fp32 T at most 2^27.
+ *   logits [T,E] fp32;  topk_idx [T,k], distinct in a row;  dtopk_w [T,k] fp32
+ *   dx_add  [T,d] dtype, added to dx (the gradient that reaches x through the
+ *           experts), or NULL; may be dx itself
+ *   dlogits [T,E] fp32 output, or NULL
+ *   dx      [T,d] dtype output, or NULL (then w_gate may be NULL too)
+ *   dw_gate [d,E] dtype output, or NULL (then x may be NULL too)
+ *   dbias   [E] fp32 output, or NULL
+ * At least one output has to be given; but for dx_add, they overlap neither inputs nor
+ * one another.
+ *   workspace of moe_workspace_bytes(p, MOE_CALL_ROUTE_BACKWARD) bytes
+ */
+moe_status_t moe_route_backward(const moe_problem_t* p, const moe_gate_t* gate, const void* x,
+                                const void* w_gate, const float* logits, const int32_t* topk_idx,
+                                const float* dtopk_w, const void* dx_add, float* dlogits, void* dx,
+                                void* dw_gate, float* dbias, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /*
  * Dispatch (CUCo, Table 4, "MoE Dispatch/Combine": variable-size per-peer
@@ -393,6 +482,61 @@ moe_status_t moe_expert_gemm_quantized(const moe_problem_t* p, const void* x_pac
                                        const void* w3, const float* s3, const void* w2,
                                        const float* s2, void* h, void* y_packed, void* workspace,
                                        size_t workspace_bytes, void* stream);
+
+/*
+ * 4-bit weights.  A matrix [K,N] has values q in 0 .. 15, a bf16 scale and perhaps a zero
+ * point in 0 .. 15 for each `group` (32, 64 or 128) consecutive k of a column; the last
+ * group of a column may be short.  The weight is (q - zero) * scale, exactly; without
+ * zero points zero = 8.
+ *   packed   n matrices in the order the matrix cores read them: 1 KB blocks of 16 columns
+ *            x 128 k, [n][ceil(N/16)][ceil(K/128)][64][4] words of 32 bits.  Word s of
+ *            entry 16 a + c holds column c, k = 32 s + 8 a + v for v = 0 .. 7 at bits
+ *            16 (v % 2) + 4 (v / 2) .. + 3, and is then rotated left by 3 bits.
+ *   scale    [n, ceil(K/group), N] bf16
+ *   zero     [n, ceil(K/group), N] uint8, or NULL
+ * moe_packed_weights_4bit_bytes(n, K, N): size of packed, 0 for invalid sizes.
+ * moe_pack_weights_4bit:      packs q [n,K,N], a value 0 .. 15 in each byte.
+ * moe_quantize_weights_4bit:  quantises w [n,K,N] of `dtype` and packs, in fp32 steps:
+ *   zero NULL: scale = rnd(max|w| / 7),            q = clamp(rint(w / scale) + 8, 1, 15)
+ *   else       scale = rnd((hi - lo) / 15),        hi = max(w, 0), lo = min(w, 0),
+ *              zero = clamp(rint(-lo / scale)),    q = clamp(rint(w / scale) + zero)
+ *   (clamp: to 0 .. 15).  Where the scale is 0, q = zero = 8; a group with an infinity or
+ *   a NaN gets that as its scale.
+ * n 1..1024, K at most 2^20, K and N multiples of 8; packed 16-byte, scale 8-byte and zero
+ * 4-byte aligned; outputs do not overlap inputs or one another.
+ */
+size_t moe_packed_weights_4bit_bytes(int32_t n, int32_t K, int32_t N);
+moe_status_t moe_pack_weights_4bit(int32_t n, int32_t K, int32_t N, const uint8_t* q, void* packed,
+                                   void* stream);
+moe_status_t moe_quantize_weights_4bit(int32_t n, int32_t K, int32_t N, int32_t group,
+                                       int32_t dtype, const void* w, void* packed, void* scale,
+                                       uint8_t* zero, void* stream);
+
+/*
+ * Product with 4-bit weights: C = rnd(A W), W one matrix [K,N] as above, with fp32
+ * accumulation; no weight is rounded.  A row of A with an infinity or a NaN gives a row
+ * of NaN, a NaN scale a column of NaN, and neither reaches others.
+ *   A [M,K] bf16 row-major, 16-byte aligned;  C [M,N] of out_dtype, 16-byte aligned,
+ *   overlaps none of the others.  M = 0 launches nothing; M at most 2^30.
+ */
+moe_status_t moe_gemm_4bit(int32_t M, int32_t N, int32_t K, int32_t group, const void* A,
+                           const void* packed, const void* scale, const uint8_t* zero, void* C,
+                           int32_t out_dtype, void* stream);
+
+/*
+ * moe_expert_gemm with 4-bit weights.  For each local expert e and its rows R
+ *   h[R] = rnd(SiLU(x_packed[R] w1[e]) * (x_packed[R] w3[e])),  y_packed[R] = rnd(h[R] w2[e])
+ * with the weights of packed [n_local][d,f] (w1, w3) and [n_local][f,d] (w2), their
+ * scales s1, s3, s2 and zero points z1, z3, z2 (each NULL or not).  bf16 only.
+ * Rows >= A of x_packed are not read, those of h and y_packed are left untouched.  Outputs
+ * must not overlap inputs or one another.  A row with an infinity or a NaN gives NaN rows
+ * of h and y_packed, and changes no other row.
+ */
+moe_status_t moe_expert_gemm_4bit(const moe_problem_t* p, int32_t group, const void* x_packed,
+                                  const int32_t* offsets, const void* w1, const void* s1,
+                                  const uint8_t* z1, const void* w3, const void* s3,
+                                  const uint8_t* z3, const void* w2, const void* s2,
+                                  const uint8_t* z2, void* h, void* y_packed, void* stream);
 
 /*
  * GEMM with per-tile completion signals: the local compute half of the pages'
