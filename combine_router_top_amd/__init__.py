@@ -6,7 +6,7 @@ status codes into exceptions.  Every step of the layer runs in the library's
 HIP kernels; there is no fallback.  If ``libmoe.so`` has not been built, every
 call raises.
 
-Functions (same names as the C calls):
+Functions (same names as the C calls, which spell 4bit as fourbit):
     route(p, x, w_gate, bias=None, want_logits=False) -> (topk_idx, topk_w[, logits])
     dispatch(p, topk_idx, x) -> dict(counts_all, offsets, perm, inv, x_packed)
     dispatch_noalloc(p, topk_idx, x) -> the same, with no workspace (static scratch)
@@ -72,8 +72,8 @@ EXPORTED = ["moe_last_error", "moe_version", "moe_workspace_bytes", "moe_route",
             "moe_expert_gemm_train", "moe_expert_gemm_backward", "moe_combine_backward",
             "moe_quantize_rows", "moe_packed_weights_bytes", "moe_pack_weights",
             "moe_quantize_weights", "moe_gemm_quantized", "moe_expert_gemm_quantized",
-            "moe_select", "moe_route_scored", "moe_route_backward", "moe_packed_weights_4bit_bytes",
-            "moe_pack_weights_4bit", "moe_quantize_weights_4bit", "moe_gemm_4bit", "moe_expert_gemm_4bit"]
+            "moe_select", "moe_route_scored", "moe_route_backward", "moe_packed_weights_fourbit_bytes",
+            "moe_pack_weights_fourbit", "moe_quantize_weights_fourbit", "moe_gemm_fourbit", "moe_expert_gemm_fourbit"]
 
 
 class MoeError(RuntimeError):
@@ -146,14 +146,14 @@ def lib() -> ctypes.CDLL:
         L.moe_select.argtypes = [P, G] + [vp] * 5
         L.moe_route_scored.argtypes = [P, G] + [vp] * 8 + [sz, vp]
         L.moe_route_backward.argtypes = [P, G] + [vp] * 11 + [sz, vp]
-        L.moe_packed_weights_4bit_bytes.argtypes = [i32, i32, i32]
-        L.moe_packed_weights_4bit_bytes.restype = sz
-        L.moe_pack_weights_4bit.argtypes = [i32, i32, i32, vp, vp, vp]
-        L.moe_quantize_weights_4bit.argtypes = [i32] * 5 + [vp] * 5
-        L.moe_gemm_4bit.argtypes = [i32] * 4 + [vp] * 5 + [i32, vp]
-        L.moe_expert_gemm_4bit.argtypes = [P, i32] + [vp] * 14
-        for n in ("moe_select", "moe_route_scored", "moe_route_backward", "moe_pack_weights_4bit",
-                  "moe_quantize_weights_4bit", "moe_gemm_4bit", "moe_expert_gemm_4bit"):
+        L.moe_packed_weights_fourbit_bytes.argtypes = [i32, i32, i32]
+        L.moe_packed_weights_fourbit_bytes.restype = sz
+        L.moe_pack_weights_fourbit.argtypes = [i32, i32, i32, vp, vp, vp]
+        L.moe_quantize_weights_fourbit.argtypes = [i32] * 5 + [vp] * 5
+        L.moe_gemm_fourbit.argtypes = [i32] * 4 + [vp] * 5 + [i32, vp]
+        L.moe_expert_gemm_fourbit.argtypes = [P, i32] + [vp] * 14
+        for n in ("moe_select", "moe_route_scored", "moe_route_backward", "moe_pack_weights_fourbit",
+                  "moe_quantize_weights_fourbit", "moe_gemm_fourbit", "moe_expert_gemm_fourbit"):
             getattr(L, n).restype = i32
         for n in ("moe_expert_gemm_train", "moe_expert_gemm_backward", "moe_combine_backward",
                   "moe_quantize_rows", "moe_pack_weights", "moe_quantize_weights",
@@ -797,7 +797,7 @@ def packed_weights_4bit_shape(K: int, N: int):
 
 def packed_weights_4bit_bytes(n: int, K: int, N: int) -> int:
     _fits(int(n) | int(K) | int(N), "a size of the weights")
-    b = int(lib().moe_packed_weights_4bit_bytes(int(n), int(K), int(N)))
+    b = int(lib().moe_packed_weights_fourbit_bytes(int(n), int(K), int(N)))
     if b == 0:
         raise MoeError(MOE_ERR_INVALID_ARG, lib().moe_last_error().decode())
     return b
@@ -828,7 +828,7 @@ def pack_weights_4bit(q, stream=None, out=None):
     if out is None:
         with _alloc_on(stream):
             out = torch.empty(shape, dtype=torch.int32, device=q.device)
-    _check(lib().moe_pack_weights_4bit(n, K, N, pq, _at(cur, out, shape, torch.int32, "packed"),
+    _check(lib().moe_pack_weights_fourbit(n, K, N, pq, _at(cur, out, shape, torch.int32, "packed"),
                                        _stream_at(cur, stream)))
     return out
 
@@ -847,7 +847,7 @@ def quantize_weights_4bit(w, group: int = 128, zero: bool = False, stream=None, 
                    torch.empty(rows, dtype=torch.bfloat16, device=w.device),
                    torch.empty(rows, dtype=torch.uint8, device=w.device) if zero else None)
     packed, s, z = out
-    _check(lib().moe_quantize_weights_4bit(
+    _check(lib().moe_quantize_weights_fourbit(
         n, K, N, group, code, pw, _at(cur, packed, shape, torch.int32, "packed"), _at(cur, s, rows, torch.bfloat16, "scale"),
         _at(cur, z, rows, torch.uint8, "zero") if zero else None, _stream_at(cur, stream)))
     return packed, s, z if zero else None
@@ -867,7 +867,7 @@ def gemm_4bit(a, packed, scale, zero=None, group: int = 128, dtype=None, stream=
     if out is None:
         with _alloc_on(stream):
             out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
-    _check(lib().moe_gemm_4bit(
+    _check(lib().moe_gemm_fourbit(
         M, N, K, group, pa, _at(cur, packed, packed_weights_4bit_shape(K, N), torch.int32, "packed"),
         _at(cur, scale, rows, torch.bfloat16, "scale"),
         None if zero is None else _at(cur, zero, rows, torch.uint8, "zero"),
@@ -892,7 +892,7 @@ def expert_gemm_4bit(p: Spec, x_packed, offsets, w1, s1, z1, w3, s3, z3, w2, s2,
         with _alloc_on(stream):
             out = tuple(torch.zeros(v, dtype=dt, device=x_packed.device) for v in (tall, wide))
     h, yp = out
-    _check(lib().moe_expert_gemm_4bit(p.ref(), group, *ins, _at(cur, h, tall, dt, "h"),
+    _check(lib().moe_expert_gemm_fourbit(p.ref(), group, *ins, _at(cur, h, tall, dt, "h"),
                                       _at(cur, yp, wide, dt, "y_packed"), _stream_at(cur, stream)))
     return h, yp
 

@@ -761,13 +761,13 @@ moe_status_t moe_route_backward(const moe_problem_t* p, const moe_gate_t* gate, 
                     "moe_route_backward");
 }
 
-size_t moe_packed_weights_4bit_bytes(int32_t n, int32_t K, int32_t N) {
+size_t moe_packed_weights_fourbit_bytes(int32_t n, int32_t K, int32_t N) {
   if (check_packed_4bit(n, K, N) != MOE_OK) return 0;
   ok();
   return moe::packed_4bit_bytes(n, K, N);
 }
 
-moe_status_t moe_pack_weights_4bit(int32_t n, int32_t K, int32_t N, const uint8_t* q, void* packed,
+moe_status_t moe_pack_weights_fourbit(int32_t n, int32_t K, int32_t N, const uint8_t* q, void* packed,
                                    void* stream) {
   moe_status_t st;
   if ((st = check_packed_4bit(n, K, N)) != MOE_OK) return st;
@@ -775,7 +775,7 @@ moe_status_t moe_pack_weights_4bit(int32_t n, int32_t K, int32_t N, const uint8_
   NEED_PTR(packed);
   NEED_ALIGNED(packed);
   (void)hipGetLastError();
-  return hip_status(moe::launch_pack_4bit(n, K, N, q, packed, (hipStream_t)stream), "moe_pack_weights_4bit");
+  return hip_status(moe::launch_pack_4bit(n, K, N, q, packed, (hipStream_t)stream), "moe_pack_weights_fourbit");
 }
 
 #define NEED_GROUPS(scale, zero)                                                                \
@@ -787,7 +787,7 @@ moe_status_t moe_pack_weights_4bit(int32_t n, int32_t K, int32_t N, const uint8_
       return fail(MOE_ERR_UNSUPPORTED, "%s is not 4-byte aligned", #zero);                      \
   } while (0)
 
-moe_status_t moe_quantize_weights_4bit(int32_t n, int32_t K, int32_t N, int32_t group,
+moe_status_t moe_quantize_weights_fourbit(int32_t n, int32_t K, int32_t N, int32_t group,
                                        int32_t dtype, const void* w, void* packed, void* scale,
                                        uint8_t* zero, void* stream) {
   moe_status_t st;
@@ -801,10 +801,10 @@ moe_status_t moe_quantize_weights_4bit(int32_t n, int32_t K, int32_t N, int32_t 
   NEED_ALIGNED(packed);
   (void)hipGetLastError();
   return hip_status(moe::launch_quantize_4bit(n, K, N, group, dtype, w, packed, scale, zero, (hipStream_t)stream),
-                    "moe_quantize_weights_4bit");
+                    "moe_quantize_weights_fourbit");
 }
 
-moe_status_t moe_gemm_4bit(int32_t M, int32_t N, int32_t K, int32_t group, const void* A,
+moe_status_t moe_gemm_fourbit(int32_t M, int32_t N, int32_t K, int32_t group, const void* A,
                            const void* packed, const void* scale, const uint8_t* zero, void* C,
                            int32_t out_dtype, void* stream) {
   moe_status_t st;
@@ -824,10 +824,10 @@ moe_status_t moe_gemm_4bit(int32_t M, int32_t N, int32_t K, int32_t group, const
   NEED_ALIGNED(C);
   (void)hipGetLastError();
   return hip_status(moe::launch_gemm_4bit(M, N, K, group, A, packed, scale, zero, C, out_dtype, (hipStream_t)stream),
-                    "moe_gemm_4bit");
+                    "moe_gemm_fourbit");
 }
 
-moe_status_t moe_expert_gemm_4bit(const moe_problem_t* p, int32_t group, const void* x_packed,
+moe_status_t moe_expert_gemm_fourbit(const moe_problem_t* p, int32_t group, const void* x_packed,
                                   const int32_t* offsets, const void* w1, const void* s1,
                                   const uint8_t* z1, const void* w3, const void* s3,
                                   const uint8_t* z3, const void* w2, const void* s2,
@@ -861,7 +861,7 @@ moe_status_t moe_expert_gemm_4bit(const moe_problem_t* p, int32_t group, const v
   return hip_status(moe::launch_expert_4bit(q, group, x_packed, offsets, moe::Weights4{w1, s1, z1},
                                             moe::Weights4{w3, s3, z3}, moe::Weights4{w2, s2, z2}, h, y_packed,
                                             (hipStream_t)stream),
-                    "moe_expert_gemm_4bit");
+                    "moe_expert_gemm_fourbit");
 }
 
 int64_t moe_gemm_signal_tiles(int32_t M, int32_t N) {

@@ -26,8 +26,8 @@
  *   moe_select, moe_route_scored, moe_route_backward
  *                    routing by softmax or sigmoid scores with a balance bias and
  *                    groups of experts, and the router's gradients
- *   moe_quantize_weights_4bit, moe_pack_weights_4bit, moe_gemm_4bit,
- *   moe_expert_gemm_4bit
+ *   moe_quantize_weights_fourbit, moe_pack_weights_fourbit, moe_gemm_fourbit,
+ *   moe_expert_gemm_fourbit
  *                    the experts served with 4-bit weights in groups along K
  *   moe_gemm_signal, moe_tile_forward
  *                    GEMM with per-tile completion flags and their consumer
@@ -494,9 +494,9 @@ moe_status_t moe_expert_gemm_quantized(const moe_problem_t* p, const void* x_pac
  *            16 (v % 2) + 4 (v / 2) .. + 3, and is then rotated left by 3 bits.
  *   scale    [n, ceil(K/group), N] bf16
  *   zero     [n, ceil(K/group), N] uint8, or NULL
- * moe_packed_weights_4bit_bytes(n, K, N): size of packed, 0 for invalid sizes.
- * moe_pack_weights_4bit:      packs q [n,K,N], a value 0 .. 15 in each byte.
- * moe_quantize_weights_4bit:  quantises w [n,K,N] of `dtype` and packs, in fp32 steps:
+ * moe_packed_weights_fourbit_bytes(n, K, N): size of packed, 0 for invalid sizes.
+ * moe_pack_weights_fourbit:      packs q [n,K,N], a value 0 .. 15 in each byte.
+ * moe_quantize_weights_fourbit:  quantises w [n,K,N] of `dtype` and packs, in fp32 steps:
  *   zero NULL: scale = rnd(max|w| / 7),            q = clamp(rint(w / scale) + 8, 1, 15)
  *   else       scale = rnd((hi - lo) / 15),        hi = max(w, 0), lo = min(w, 0),
  *              zero = clamp(rint(-lo / scale)),    q = clamp(rint(w / scale) + zero)
@@ -505,10 +505,10 @@ moe_status_t moe_expert_gemm_quantized(const moe_problem_t* p, const void* x_pac
  * n 1..1024, K at most 2^20, K and N multiples of 8; packed 16-byte, scale 8-byte and zero
  * 4-byte aligned; outputs do not overlap inputs or one another.
  */
-size_t moe_packed_weights_4bit_bytes(int32_t n, int32_t K, int32_t N);
-moe_status_t moe_pack_weights_4bit(int32_t n, int32_t K, int32_t N, const uint8_t* q, void* packed,
+size_t moe_packed_weights_fourbit_bytes(int32_t n, int32_t K, int32_t N);
+moe_status_t moe_pack_weights_fourbit(int32_t n, int32_t K, int32_t N, const uint8_t* q, void* packed,
                                    void* stream);
-moe_status_t moe_quantize_weights_4bit(int32_t n, int32_t K, int32_t N, int32_t group,
+moe_status_t moe_quantize_weights_fourbit(int32_t n, int32_t K, int32_t N, int32_t group,
                                        int32_t dtype, const void* w, void* packed, void* scale,
                                        uint8_t* zero, void* stream);
 
@@ -519,7 +519,7 @@ moe_status_t moe_quantize_weights_4bit(int32_t n, int32_t K, int32_t N, int32_t 
  *   A [M,K] bf16 row-major, 16-byte aligned;  C [M,N] of out_dtype, 16-byte aligned,
  *   overlaps none of the others.  M = 0 launches nothing; M at most 2^30.
  */
-moe_status_t moe_gemm_4bit(int32_t M, int32_t N, int32_t K, int32_t group, const void* A,
+moe_status_t moe_gemm_fourbit(int32_t M, int32_t N, int32_t K, int32_t group, const void* A,
                            const void* packed, const void* scale, const uint8_t* zero, void* C,
                            int32_t out_dtype, void* stream);
 
@@ -532,7 +532,7 @@ moe_status_t moe_gemm_4bit(int32_t M, int32_t N, int32_t K, int32_t group, const
  * must not overlap inputs or one another.  A row with an infinity or a NaN gives NaN rows
  * of h and y_packed, and changes no other row.
  */
-moe_status_t moe_expert_gemm_4bit(const moe_problem_t* p, int32_t group, const void* x_packed,
+moe_status_t moe_expert_gemm_fourbit(const moe_problem_t* p, int32_t group, const void* x_packed,
                                   const int32_t* offsets, const void* w1, const void* s1,
                                   const uint8_t* z1, const void* w3, const void* s3,
                                   const uint8_t* z3, const void* w2, const void* s2,

@@ -20,7 +20,7 @@ ROUTE = ["x", "w_gate", "bias", "balance", "logits", "topk_idx", "topk_w"]
 BACK = ["x", "w_gate", "logits", "topk_idx", "dtopk_w", "dx_add", "dlogits", "dx", "dw_gate", "dbias"]
 EXPERTS = ["x_packed", "offsets", "w1", "s1", "z1", "w3", "s3", "z3", "w2", "s2", "z2", "h", "y_packed"]
 CALLS = {"moe_select": (SELECT, False), "moe_route_scored": (ROUTE, True), "moe_route_backward": (BACK, True),
-         "moe_expert_gemm_4bit": (EXPERTS, False)}
+         "moe_expert_gemm_fourbit": (EXPERTS, False)}
 OPTIONAL = {"balance", "bias", "dx_add", "dlogits", "dx", "dw_gate", "dbias", "z1", "z3", "z2"}
 RULE = M.GateRule(M.MOE_SCORE_SIGMOID, 2, 1, 2, 1, 1.0)
 
@@ -30,7 +30,7 @@ def _call(name, p=None, args=None, rule=RULE, group=64, ws=FAKE, wsb=BIG, **name
     args = [FAKE] * len(names) if args is None else args
     args = [named.get(n, a) for n, a in zip(names, args)]
     p = _p() if p is None else p
-    second = group if name == "moe_expert_gemm_4bit" else (None if rule is None else ctypes.byref(rule))
+    second = group if name == "moe_expert_gemm_fourbit" else (None if rule is None else ctypes.byref(rule))
     return getattr(M.lib(), name)(ctypes.byref(p), second, *args, *((ws, wsb, None) if has_ws else (None,)))
 
 
@@ -104,37 +104,37 @@ def test_empty_batches_launch_nothing():
     assert _call("moe_select", p, [None] * 4) == M.MOE_OK
     assert _call("moe_route_scored", p, [None, FAKE] + [None] * 5, **nothing) == M.MOE_OK
     assert _call("moe_route_backward", p, [None] * 10, **nothing) == M.MOE_OK
-    assert _call("moe_expert_gemm_4bit", p, x_packed=None, h=None, y_packed=None) == M.MOE_OK
-    assert M.lib().moe_gemm_4bit(0, 64, 64, 32, None, FAKE, FAKE, None, None, M.MOE_DTYPE_BF16, None) == M.MOE_OK
+    assert _call("moe_expert_gemm_fourbit", p, x_packed=None, h=None, y_packed=None) == M.MOE_OK
+    assert M.lib().moe_gemm_fourbit(0, 64, 64, 32, None, FAKE, FAKE, None, None, M.MOE_DTYPE_BF16, None) == M.MOE_OK
 
 
 def test_experts_take_bf16_rows_and_known_groups():
-    assert _call("moe_expert_gemm_4bit", _p(dtype=M.MOE_DTYPE_F32)) == UNS
+    assert _call("moe_expert_gemm_fourbit", _p(dtype=M.MOE_DTYPE_F32)) == UNS
     for group in (0, 16, 96, 256, -32):
-        assert _call("moe_expert_gemm_4bit", group=group) == UNS, group
-    assert _call("moe_expert_gemm_4bit", _p(d=(1 << 20) + 8, f=8)) == UNS
-    assert _call("moe_expert_gemm_4bit", _p(f=(1 << 20) + 8, d=8)) == UNS
+        assert _call("moe_expert_gemm_fourbit", group=group) == UNS, group
+    assert _call("moe_expert_gemm_fourbit", _p(d=(1 << 20) + 8, f=8)) == UNS
+    assert _call("moe_expert_gemm_fourbit", _p(f=(1 << 20) + 8, d=8)) == UNS
 
 
 def test_packed_weights_arguments():
     L = M.lib()
-    assert L.moe_packed_weights_4bit_bytes(1, 128, 16) == 1024
-    assert L.moe_packed_weights_4bit_bytes(3, 136, 24) == 3 * 2 * 2 * 1024
+    assert L.moe_packed_weights_fourbit_bytes(1, 128, 16) == 1024
+    assert L.moe_packed_weights_fourbit_bytes(3, 136, 24) == 3 * 2 * 2 * 1024
     for n, K, N in ((0, 64, 16), (1, 0, 16), (1, 64, 0), (1025, 64, 16), (1, 12, 16), (1, 64, 12), (1, (1 << 20) + 8, 8),
                     (1, 8, (1 << 21) + 8), (1, 1 << 20, 2048)):
-        assert L.moe_packed_weights_4bit_bytes(n, K, N) == 0 and L.moe_last_error()
-        assert L.moe_pack_weights_4bit(n, K, N, FAKE, FAKE, None) in (INV, UNS)
-        assert L.moe_quantize_weights_4bit(n, K, N, 32, M.MOE_DTYPE_BF16, FAKE, FAKE, FAKE, FAKE, None) in (INV, UNS)
-    assert L.moe_pack_weights_4bit(1, 64, 16, None, FAKE, None) == INV
-    assert L.moe_pack_weights_4bit(1, 64, 16, FAKE, ODD, None) == UNS
-    q = lambda g=32, dt=M.MOE_DTYPE_F32, w=FAKE, o=FAKE, s=FAKE, z=FAKE: L.moe_quantize_weights_4bit(1, 64, 16, g, dt, w, o, s, z, None)  # noqa: E731
+        assert L.moe_packed_weights_fourbit_bytes(n, K, N) == 0 and L.moe_last_error()
+        assert L.moe_pack_weights_fourbit(n, K, N, FAKE, FAKE, None) in (INV, UNS)
+        assert L.moe_quantize_weights_fourbit(n, K, N, 32, M.MOE_DTYPE_BF16, FAKE, FAKE, FAKE, FAKE, None) in (INV, UNS)
+    assert L.moe_pack_weights_fourbit(1, 64, 16, None, FAKE, None) == INV
+    assert L.moe_pack_weights_fourbit(1, 64, 16, FAKE, ODD, None) == UNS
+    q = lambda g=32, dt=M.MOE_DTYPE_F32, w=FAKE, o=FAKE, s=FAKE, z=FAKE: L.moe_quantize_weights_fourbit(1, 64, 16, g, dt, w, o, s, z, None)  # noqa: E731
     assert q(g=48) == UNS and q(dt=3) == UNS and q(w=ODD) == UNS and q(o=ODD) == UNS and q(s=FAKE + 4) == UNS and q(z=FAKE + 1) == UNS
     assert q(w=None) == INV and q(o=None) == INV and q(s=None) == INV
 
 
 def test_gemm_4bit_arguments():
     def g(Mr=4, N=16, K=64, G=32, a=FAKE, b=FAKE, s=FAKE, z=FAKE, c=FAKE, dt=M.MOE_DTYPE_BF16):
-        return M.lib().moe_gemm_4bit(Mr, N, K, G, a, b, s, z, c, dt, None)
+        return M.lib().moe_gemm_fourbit(Mr, N, K, G, a, b, s, z, c, dt, None)
     assert g(Mr=-1) == INV and g(N=0) == INV and g(K=0) == INV
     assert g(Mr=(1 << 30) + 1) == UNS and g(N=(1 << 21) + 8) == UNS and g(K=20) == UNS and g(N=12) == UNS and g(dt=9) == UNS
     assert g(G=0) == UNS and g(G=65) == UNS
