@@ -23,7 +23,8 @@ ARCH = "gfx950"
 
 SOURCES = ["route.hip", "dispatch.hip", "expert_gemm.hip", "combine.hip", "tile_forward.hip",
            "expert_train.hip", "expert_backward.hip", "expert_i8.hip", "select.hip",
-           "route_backward.hip", "expert_4bit.hip", "moe_api.cpp"]
+           "route_backward.hip", "expert_4bit.hip", "expert_4bit_up.hip", "expert_4bit_down.hip",
+           "moe_api.cpp"]
 # measurement-only streaming-read probe, linked into a library of its own
 PROBE_SOURCE = "hbm_read_probe.hip"
 PROBE_LIB = os.path.join(PKG, "libhbm_probe.so")

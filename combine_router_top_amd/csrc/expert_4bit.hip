@@ -26,11 +26,9 @@
 
 #include "common.h"
 #include "kernels.h"
-#include "seg_tile.h"
+#include "w4.h"
 
 namespace moe {
-
-constexpr int W4_KB = 128;   // K of a packed block
 
 // ---------------------------------------------------------------------------
 // quantiser and packing (once per set of weights)
@@ -112,44 +110,8 @@ __global__ __launch_bounds__(256) void w4_pack(const void* __restrict__ w, const
 }
 
 // ---------------------------------------------------------------------------
-// products
+// streams
 // ---------------------------------------------------------------------------
-// Segments: rows [offsets[e], offsets[e+1]) of expert e, or, without offsets, one
-// segment of rows [0, M).
-struct W4Args {
-  const bf16_t* a;         // [*][K]
-  const char* b1;          // packed weights [n][ntiles][kb] blocks
-  const char* b3;          // second matrix of a gated product
-  const bf16_t* s1;        // [n][groups][N]
-  const bf16_t* s3;
-  const uint8_t* z1;       // [n][groups][N] or NULL
-  const uint8_t* z3;
-  void* c;                 // [*][N]
-  const int32_t* offsets;
-  int n, M;
-  int K, N, kb, ntiles, groups;
-};
-
-__device__ __forceinline__ int w4_rows(const W4Args& p, int e, int& o) {
-  int cnt = p.M;
-  o = 0;
-  if (p.offsets) {
-    o = p.offsets[e];
-    cnt = p.offsets[e + 1] - o;
-  }
-  o = __builtin_amdgcn_readfirstlane(o);
-  return __builtin_amdgcn_readfirstlane(cnt);
-}
-
-// The eight numbers 16 + q of a packed word.
-__device__ __forceinline__ u32x4 w4_unpack(uint32_t w) {
-  u32x4 o;
-#pragma unroll
-  for (int p = 0; p < 4; ++p)
-    o[p] = ((p ? __builtin_amdgcn_alignbit(w, w, 4 * p) : w) & 0x00780078u) | 0x41804180u;
-  return o;
-}
-
 template <bool F32OUT>
 __device__ __forceinline__ void w4_store(void* c, int64_t at, const float (&o)[4]) {
   if (F32OUT) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(c) + at) = f32x4{o[0], o[1], o[2], o[3]};
@@ -324,7 +286,7 @@ __global__ __launch_bounds__(64 * KS) void w4_stream(W4Args p) {
 // launches
 // ---------------------------------------------------------------------------
 template <bool GATED, bool F32OUT, int GPB>
-static hipError_t launch_4bit_group(const W4Args& p, int64_t mean, int64_t most, hipStream_t st) {
+static hipError_t launch_4bit_stream(const W4Args& p, int64_t most, hipStream_t st) {
   const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
   const int64_t blocks = std::min<int64_t>((most + 31) / 32, p.offsets ? 4 : 1024);
   auto go = [&](auto kernel, int cols, int ks) {
@@ -341,10 +303,16 @@ static hipError_t launch_4bit_group(const W4Args& p, int64_t mean, int64_t most,
 }
 
 template <bool GATED, bool F32OUT>
-static hipError_t launch_4bit(const W4Args& p, int group, int64_t mean, int64_t most, hipStream_t st) {
-  return group == 32   ? launch_4bit_group<GATED, F32OUT, 4>(p, mean, most, st)
-         : group == 64 ? launch_4bit_group<GATED, F32OUT, 2>(p, mean, most, st)
-                       : launch_4bit_group<GATED, F32OUT, 1>(p, mean, most, st);
+static hipError_t launch_4bit(W4Args p, int group, int64_t mean, int64_t most, int64_t rows_max, hipStream_t st) {
+  const bool tiles = mean > 64;
+  p.lo = 0;
+  p.hi = INT32_MAX;
+  if (tiles)
+    return GATED ? launch_4bit_tiles_up(p, group, mean > 64 ? 2 : 1, rows_max, st)
+                 : launch_4bit_tiles_down(p, group, mean > 64 ? 2 : 1, rows_max, F32OUT, st);
+  return group == 32   ? launch_4bit_stream<GATED, F32OUT, 4>(p, most, st)
+         : group == 64 ? launch_4bit_stream<GATED, F32OUT, 2>(p, most, st)
+                       : launch_4bit_stream<GATED, F32OUT, 1>(p, most, st);
 }
 
 size_t packed_4bit_bytes(int n, int K, int N) {
@@ -393,7 +361,7 @@ hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const
   p.s1 = (const bf16_t*)scale;
   p.z1 = (const uint8_t*)zero;
   p.c = c;
-  return out_dtype == 1 ? launch_4bit<false, false>(p, group, M, M, st) : launch_4bit<false, true>(p, group, M, M, st);
+  return out_dtype == 1 ? launch_4bit<false, false>(p, group, M, M, M, st) : launch_4bit<false, true>(p, group, M, M, M, st);
 }
 
 hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int32_t* offsets, const Weights4& w1,
@@ -409,7 +377,7 @@ hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int
   a.s3 = (const bf16_t*)w3.scale;
   a.z3 = (const uint8_t*)w3.zero;
   a.c = h;
-  const hipError_t e = launch_4bit<true, false>(a, group, mean, p.T, st);
+  const hipError_t e = launch_4bit<true, false>(a, group, mean, p.T, p.rows_max, st);
   if (e != hipSuccess) return e;
   W4Args b = w4_args(p.n, p.f, p.d, group);
   b.offsets = offsets;
@@ -418,7 +386,7 @@ hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int
   b.s1 = (const bf16_t*)w2.scale;
   b.z1 = (const uint8_t*)w2.zero;
   b.c = y;
-  return launch_4bit<false, false>(b, group, mean, p.T, st);
+  return launch_4bit<false, false>(b, group, mean, p.T, p.rows_max, st);
 }
 
 }  // namespace moe

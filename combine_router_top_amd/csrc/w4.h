@@ -1,0 +1,57 @@
+// What the kernels of the 4-bit products share: their arguments, the rows of a
+// segment, the masked or that makes bf16 numbers of packed values.  See expert_4bit.hip
+// for the mathematics and the layout.
+#pragma once
+
+#include "common.h"
+#include "kernels.h"
+#include "seg_tile.h"
+
+namespace moe {
+
+constexpr int W4_KB = 128;   // K of a packed block
+
+// Segments: rows [offsets[e], offsets[e+1]) of expert e, or, without offsets, one
+// segment of rows [0, M).
+struct W4Args {
+  const bf16_t* a;         // [*][K]
+  const char* b1;          // packed weights [n][ntiles][kb] blocks
+  const char* b3;          // second matrix of a gated product
+  const bf16_t* s1;        // [n][groups][N]
+  const bf16_t* s3;
+  const uint8_t* z1;       // [n][groups][N] or NULL
+  const uint8_t* z3;
+  void* c;                 // [*][N]
+  const int32_t* offsets;
+  int n, M;
+  int K, N, kb, ntiles, groups;
+  int lo, hi;              // this launch takes segments with lo < rows <= hi (tiles: no upper bound)
+};
+
+__device__ __forceinline__ int w4_rows(const W4Args& p, int e, int& o) {
+  int cnt = p.M;
+  o = 0;
+  if (p.offsets) {
+    o = p.offsets[e];
+    cnt = p.offsets[e + 1] - o;
+  }
+  o = __builtin_amdgcn_readfirstlane(o);
+  cnt = __builtin_amdgcn_readfirstlane(cnt);
+  return cnt > p.lo && cnt <= p.hi ? cnt : 0;
+}
+
+// The eight numbers 16 + q of a packed word.
+__device__ __forceinline__ u32x4 w4_unpack(uint32_t w) {
+  u32x4 o;
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    o[p] = ((p ? __builtin_amdgcn_alignbit(w, w, 4 * p) : w) & 0x00780078u) | 0x41804180u;
+  return o;
+}
+
+// expert_4bit_up.hip, expert_4bit_down.hip: the products on tiles of `height` (1 or 2)
+// times 64 rows, for the segments of more than p.lo rows.
+hipError_t launch_4bit_tiles_up(const W4Args& p, int group, int height, int64_t rows_max, hipStream_t st);
+hipError_t launch_4bit_tiles_down(const W4Args& p, int group, int height, int64_t rows_max, bool f32out, hipStream_t st);
+
+}  // namespace moe
