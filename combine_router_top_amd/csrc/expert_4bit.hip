@@ -162,6 +162,7 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
   // what is subtracted from 16 + q: the zero point, 8 where there are none
   const float zb1 = p.z1 ? -16.f : -24.f, zb3 = GATED && p.z3 ? -16.f : -24.f;
 
+  const uint32_t mask = w4_mask(), bits = w4_bits();
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -208,7 +209,7 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
         for (int mt = 0; mt < MT; ++mt) X[mt] = mfma16(ones, __builtin_bit_cast(bf16x8, x[h][mt][q]), X[mt]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const u32x4 f = w4_unpack(w[h][t][q]);
+          const u32x4 f = w4_unpack(w[h][t][q], mask, bits);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) part[mt][t] = st_mfma(f, x[h][mt][q], part[mt][t]);
         }

@@ -40,13 +40,24 @@ __device__ __forceinline__ int w4_rows(const W4Args& p, int e, int& o) {
   return cnt > p.lo && cnt <= p.hi ? cnt : 0;
 }
 
-// The eight numbers 16 + q of a packed word.
-__device__ __forceinline__ u32x4 w4_unpack(uint32_t w) {
+// The eight numbers 16 + q of a packed word.  mask and bits are w4_mask() and w4_bits():
+// as constants that the compiler knows they would be literals, of which a masked or
+// takes none (then it is two instructions); it takes one scalar register.
+__device__ __forceinline__ u32x4 w4_unpack(uint32_t w, uint32_t mask, uint32_t bits) {
   u32x4 o;
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
-    o[p] = ((p ? __builtin_amdgcn_alignbit(w, w, 4 * p) : w) & 0x00780078u) | 0x41804180u;
+  for (int p = 0; p < 4; ++p) o[p] = ((p ? __builtin_amdgcn_alignbit(w, w, 4 * p) : w) & mask) | bits;
   return o;
+}
+__device__ __forceinline__ uint32_t w4_mask() {
+  uint32_t v;
+  asm("v_mov_b32 %0, 0x780078" : "=v"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t w4_bits() {
+  uint32_t v;
+  asm("s_mov_b32 %0, 0x41804180" : "=s"(v));
+  return v;
 }
 
 // expert_4bit_up.hip, expert_4bit_down.hip: the products on tiles of `height` (1 or 2)
