@@ -162,6 +162,11 @@ struct W4Wave {
         for (int mt = 0; mt < MT; ++mt)
           v[mt] = mfma16(ones, __builtin_bit_cast(bf16x8, x[mt][q]), q == u * SPG ? f32x4{0.f, 0.f, 0.f, 0.f} : v[mt]);
       flush(acc, 1, NT - 1, u * MT / GPB, (u + 1) * MT / GPB);
+#pragma unroll
+      for (int k = 0; k < MT * SPG; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+      }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -272,6 +277,9 @@ __global__ __launch_bounds__(ST_NT, 1) void w4_tile(W4Args p, int ntn) {
     return t;
   };
   auto prologue = [&]() {
+    // what setup loaded is here: else the compiler waits for it inside the loop over the
+    // stages, and there for every copy as well
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
 #pragma unroll
     for (int s = 0; s < C::NS - 1; ++s) w4_issue(p, c, lbase + s * C::SLOT, s);
   };
