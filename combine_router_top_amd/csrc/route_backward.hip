@@ -18,57 +18,79 @@
 #include "f32_tile.h"
 #include "kernels.h"
 #include "seg_tile.h"
+#include "wave_reduce.h"
 
 namespace moe {
 
-constexpr int RB_TOK = 16;        // tokens of a workgroup of the logit gradients
+constexpr int RB_TOK = 8;         // tokens of a workgroup of the logit gradients
 constexpr int RB_MOST = 512;      // workgroups of it
 
 static int rb_blocks(const Prob& p) { return (int)std::min<int64_t>(((int64_t)p.T + RB_TOK - 1) / RB_TOK, RB_MOST); }
 static int rb_pad(const Prob& p) { return (p.E + 7) / 8 * 8; }
 
 __device__ __forceinline__ float rb_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+  return wave_reduce(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float rb_max(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
+  return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// Logit gradients, one wave per token, lane l holds experts l + 64 j.  dl, dlb [T][Ep]
-// (either NULL): the fp32 values, those rounded to bf16 with zero columns from E on.
-// colsum: this workgroup's sums over its tokens, [gridDim.x][E], or NULL.
+// Logit gradients, one wave per token, lane l holds experts NV l .. NV l + NV - 1.  dl
+// [T][E], dlb [T][Ep] (either NULL): the fp32 values, those rounded to bf16 with zero
+// columns from E on.  colsum: this workgroup's sums over its tokens, [gridDim.x][E], or NULL.
 template <int NV>
 __global__ __launch_bounds__(256) void logit_grad(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                                                   const float* __restrict__ dw, int T, int E, int Ep, int k,
                                                   SelectRule r, float* __restrict__ dl, bf16_t* __restrict__ dlb,
                                                   float* __restrict__ colsum) {
   __shared__ float red[4][64 * NV];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e0 = NV * lane;
+  const bool quads = NV % 4 == 0 && E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dl)) & 15) == 0;
   float sum[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) sum[j] = 0.f;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < T; t += (int64_t)gridDim.x * 4) {
+  const int64_t step = (int64_t)gridDim.x * 4;
+  // the next token's values are on their way while one is worked on
+  float nl[NV], nw = 0.f;
+  int ni = -1;
+  auto load = [&](int64_t t) {
+    ni = lane < k ? idx[t * k + lane] : -1;
+    nw = lane < k ? dw[t * k + lane] : 0.f;
+    const float* p = logits + t * E + e0;
+    if (quads) {
+#pragma unroll
+      for (int j = 0; j < NV; j += 4) {
+        f32x4 v = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (e0 + j < E) v = *reinterpret_cast<const f32x4*>(p + j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < NV) nl[j + i] = v[i];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) nl[j] = e0 + j < E ? p[j] : -INFINITY;
+    }
+  };
+  int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  if (t < T) load(t);
+  for (; t < T; t += step) {
     float l[NV], g[NV];
     bool in[NV];
-    const int my = lane < k ? idx[t * k + lane] : -1;
-    const float mw = lane < k ? dw[t * k + lane] * r.scale : 0.f;
+    const int my = ni;
+    const float mw = nw * r.scale;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = lane + 64 * j;
-      l[j] = e < E ? logits[t * E + e] : -INFINITY;
+      l[j] = nl[j];
       g[j] = 0.f;
       in[j] = false;
     }
+    if (t + step < T) load(t + step);
     for (int q = 0; q < k; ++q) {
-      const int e = __builtin_amdgcn_readlane(my, q);
+      const int e = __builtin_amdgcn_readlane(my, q) - e0;
       const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mw), q));
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (e == lane + 64 * j) {
+        if (e == j) {
           g[j] += v;
           in[j] = true;
         }
@@ -85,9 +107,14 @@ __global__ __launch_bounds__(256) void logit_grad(const float* __restrict__ logi
     float s[NV], slope[NV], total = 0.f, dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const float z = expf(-fabsf(l[j]));
-      slope[j] = r.softmax ? 1.f : (l[j] > 0.f ? z : 1.f) / (1.f + z);   // sigmoid(-l)
-      s[j] = r.softmax ? expf(l[j] - top) : expf(fminf(l[j], 0.f) - top) / (1.f + z);
+      if (r.softmax) {
+        slope[j] = 1.f;
+        s[j] = expf(l[j] - top);
+      } else {
+        const float z = expf(-fabsf(l[j])), inv = 1.f / (1.f + z);
+        slope[j] = (l[j] > 0.f ? z : 1.f) * inv;   // sigmoid(-l)
+        s[j] = r.renorm ? expf(fminf(l[j], 0.f) - top) * inv : (l[j] > 0.f ? 1.f : z) * inv;
+      }
       if (l[j] == -INFINITY) s[j] = 0.f;
       if (!r.renorm || in[j]) total += s[j];
       dot += g[j] * s[j];
@@ -99,21 +126,41 @@ __global__ __launch_bounds__(256) void logit_grad(const float* __restrict__ logi
     }
     const float inv = !shared ? 1.f : total == 0.f ? 0.f : 1.f / total;
     const float mean = shared ? dot * inv : 0.f;
+    float v[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = lane + 64 * j;
-      const bool live = in[j] || (r.softmax && !r.renorm);
-      const float v = live ? s[j] * inv * slope[j] * (g[j] - mean) : 0.f;
-      if (e < E) {
-        if (dl) dl[t * E + e] = v;
-        sum[j] += v;
+      const bool live = e0 + j < E && (in[j] || (r.softmax && !r.renorm));
+      v[j] = live ? s[j] * inv * slope[j] * (g[j] - mean) : 0.f;
+      sum[j] += v[j];
+    }
+    if (dl) {
+      float* p = dl + t * E + e0;
+      if (quads) {
+#pragma unroll
+        for (int j = 0; j < NV; j += 4)
+          if (e0 + j < E) *reinterpret_cast<f32x4*>(p + j) = f32x4{v[j], v[(j + 1) % NV], v[(j + 2) % NV], v[(j + 3) % NV]};
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (e0 + j < E) p[j] = v[j];
       }
-      if (dlb && e < Ep) dlb[t * Ep + e] = (bf16_t)(cvt_bf16x2(e < E ? v : 0.f, 0.f));
+    }
+    if (dlb) {   // Ep is a multiple of 8
+      bf16_t* p = dlb + t * Ep + e0;
+      if constexpr (NV % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < NV; j += 4)
+          if (e0 + j < Ep) *reinterpret_cast<u32x2*>(p + j) = u32x2{cvt_bf16x2(v[j], v[j + 1]), cvt_bf16x2(v[j + 2], v[j + 3])};
+      } else if constexpr (NV == 2) {
+        if (e0 < Ep) *reinterpret_cast<uint32_t*>(p) = cvt_bf16x2(v[0], v[1]);
+      } else {
+        if (e0 < Ep) p[0] = (bf16_t)cvt_bf16x2(v[0], 0.f);
+      }
     }
   }
   if (!colsum) return;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) red[wave][lane + 64 * j] = sum[j];
+  for (int j = 0; j < NV; ++j) red[wave][e0 + j] = sum[j];
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += 256)
     colsum[(int64_t)blockIdx.x * E + e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
@@ -238,18 +285,50 @@ __global__ __launch_bounds__(ST_NT, 1) void gate_weight_grad(const bf16_t* __res
       });
 }
 
-// What remains of dWg and db: the parts' sums, in their order.
-__global__ __launch_bounds__(256) void gate_sums(const float* __restrict__ part, int shares, int64_t d, int E, int Ep,
-                                                 bf16_t* __restrict__ dwg, const float* __restrict__ colsum, int rows,
-                                                 float* __restrict__ db) {
-  if (db && blockIdx.x == 0)
-    for (int e = threadIdx.x; e < E; e += 256) {
+// What remains of dWg and db, the parts' sums in their order.  The first ceil(E / 64)
+// workgroups sum db if it is wanted: 64 experts, the rows dealt out over 16 waves.
+__global__ __launch_bounds__(1024) void gate_sums(const float* __restrict__ part, int shares, int64_t d, int E, int Ep,
+                                                  bf16_t* __restrict__ dwg, const float* __restrict__ colsum, int rows,
+                                                  float* __restrict__ db) {
+  __shared__ float red[16][64];
+  int first = 0;
+  if (db) {
+    first = (E + 63) / 64;
+    if ((int)blockIdx.x < first) {
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = 64 * blockIdx.x + lane;
       float s = 0.f;
-      for (int b = 0; b < rows; ++b) s += colsum[(int64_t)b * E + e];
-      db[e] = s;
+      for (int b = wave; b < rows; b += 256) {   // sixteen loads together
+        float v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) v[u] = e < E && b + 16 * u < rows ? colsum[(int64_t)(b + 16 * u) * E + e] : 0.f;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) s += v[u];
+      }
+      red[wave][lane] = s;
+      __syncthreads();
+      if (wave == 0 && e < E) {
+        s = red[0][lane];
+        for (int u = 1; u < 16; ++u) s += red[u][lane];
+        db[e] = s;
+      }
+      return;
     }
-  if (!dwg) return;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < d * E; i += (int64_t)gridDim.x * 256) {
+  }
+  const int64_t at0 = ((int64_t)blockIdx.x - first) * 1024 + threadIdx.x, step = ((int64_t)gridDim.x - first) * 1024;
+  if (E == Ep) {   // 8 values of a row together
+    for (int64_t i = at0; i < d * E / 8; i += step) {
+      f32x4 a = f32x4{0.f, 0.f, 0.f, 0.f}, b = a;
+      for (int q = 0; q < shares; ++q) {
+        const f32x4* v = reinterpret_cast<const f32x4*>(part + q * d * Ep) + 2 * i;
+        a += v[0];
+        b += v[1];
+      }
+      reinterpret_cast<u32x4*>(dwg)[i] =
+          u32x4{cvt_bf16x2(a[0], a[1]), cvt_bf16x2(a[2], a[3]), cvt_bf16x2(b[0], b[1]), cvt_bf16x2(b[2], b[3])};
+    }
+    return;
+  }
+  for (int64_t i = at0; i < d * E; i += step) {
     const int64_t row = i / E, at = row * Ep + (i - row * E);
     float s = 0.f;
     for (int q = 0; q < shares; ++q) s += part[q * d * Ep + at];
@@ -370,7 +449,7 @@ hipError_t launch_route_backward(const Prob& p, const SelectRule& r, const void*
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (dbias)
-      hipLaunchKernelGGL(gate_sums, dim3(1), dim3(256), 0, st, (const float*)nullptr, 0, (int64_t)p.d, p.E, Ep,
+      hipLaunchKernelGGL(gate_sums, dim3((unsigned)((p.E + 63) / 64)), dim3(1024), 0, st, (const float*)nullptr, 0, (int64_t)p.d, p.E, Ep,
                          (bf16_t*)nullptr, (const float*)colsum, rb_blocks(p), dbias);
     return hipGetLastError();
   }
@@ -400,8 +479,9 @@ hipError_t launch_route_backward(const Prob& p, const SelectRule& r, const void*
                        part, p.T, p.d, Ep, shares);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const int64_t blocks = dwg ? std::min<int64_t>(((int64_t)p.d * p.E + 255) / 256, 4096) : 1;
-  hipLaunchKernelGGL(gate_sums, dim3((unsigned)blocks), dim3(256), 0, st, (const float*)part, shares, (int64_t)p.d, p.E, Ep,
+  const int64_t count = !dwg ? 0 : p.E == Ep ? (int64_t)p.d * p.E / 8 : (int64_t)p.d * p.E;
+  const int64_t blocks = std::min<int64_t>((count + 1023) / 1024, 1024) + (dbias ? (p.E + 63) / 64 : 0);
+  hipLaunchKernelGGL(gate_sums, dim3((unsigned)blocks), dim3(1024), 0, st, (const float*)part, shares, (int64_t)p.d, p.E, Ep,
                      (bf16_t*)dwg, (const float*)colsum, rb_blocks(p), dbias);
   return hipGetLastError();
 }
