@@ -177,36 +177,59 @@ __global__ __launch_bounds__(256) void pad_rows(const bf16_t* __restrict__ w, in
   }
 }
 
-template <int MT>
-using RowCfg = StCfg<MT, ST_ROWS, ST_ROWS, f32x4, 1, false, (MT == 1 ? 2 : 4) * MT>;
+// dx and the parts of dWg, in one launch of one workgroup per compute unit: half of the
+// workgroups begin with the one, half with the other, so that what is mostly read (x)
+// and what is mostly written (dx) share the memory.
+//
+// dx: tiles of seg_tile.h, rows of dl against rows of Wg.  K is E, a few stages, and a tile
+// is mostly its store: whole rows leave through LDS, except where dx_add joins the sum
+// before it is rounded, and on the small tiles of few tokens.
+// dWg: a unit is 128 rows of d, 256 experts and a share of the tokens, both operands
+// panels of 64 tokens in a ring of three slots, transposed by the LDS read.
+struct RouteGrad {
+  const bf16_t* x;
+  const bf16_t* wg;     // [d][Ep]
+  const bf16_t* dl;     // [T][Ep]
+  const bf16_t* add;
+  bf16_t* dx;           // or NULL
+  float* part;          // [shares][d][Ep], or NULL
+  int T, d, Ep;
+  int shares;
+};
 
-// dx tiles: rows of dl against rows of Wg.
-template <int MT>
-__global__ __launch_bounds__(ST_NT, 1) void row_grad(const bf16_t* __restrict__ dl, const bf16_t* __restrict__ wg,
-                                                     const bf16_t* add, bf16_t* dx, int T,
-                                                     int d, int Ep, int ntn) {
-  using Cfg = RowCfg<MT>;
-  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
-  const int blocks = (T + Cfg::BM - 1) / Cfg::BM;
+enum { RG_FEW = 0, RG_ROWS = 1, RG_ADD = 2 };   // small tiles, whole rows, with dx_add
+template <int KIND>
+using RowCfg = StCfg<KIND == RG_FEW ? 1 : 4, ST_ROWS, ST_ROWS, f32x4, 1, false, KIND == RG_FEW ? 2 : 16, KIND == RG_ROWS>;
+
+// Tiles of dx.
+template <int KIND>
+__device__ __forceinline__ void row_tiles(const RouteGrad& p, char* ring) {
+  using Cfg = RowCfg<KIND>;
+  constexpr int MT = Cfg::MT;
+  const int blocks = (p.T + Cfg::BM - 1) / Cfg::BM, ntn = (p.d + Cfg::BN - 1) / Cfg::BN;
   const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   st_run<Cfg>(
       blocks * ntn, ring,
       [&](int L, StCtx<Cfg>& c) {
-        const StTile t = st_tile_of(L, 0, T, blocks, ntn, Cfg::BM);
-        const uint32_t ld = (uint32_t)Ep * 2;
-        st_rows(c.a[0], dl + (int64_t)t.r0 * Ep, ld, t.R, ld);
-        st_rows(c.b[0], wg + (int64_t)Cfg::BN * t.nt * Ep, ld, min(Cfg::BN, d - Cfg::BN * t.nt), ld);
-        c.nst = c.nst1 = (Ep + 63) / 64;
+        const StTile t = st_tile_of(L, 0, p.T, blocks, ntn, Cfg::BM);
+        const uint32_t ld = (uint32_t)p.Ep * 2;
+        st_rows(c.a[0], p.dl + (int64_t)t.r0 * p.Ep, ld, t.R, ld);
+        st_rows(c.b[0], p.wg + (int64_t)Cfg::BN * t.nt * p.Ep, ld, min(Cfg::BN, p.d - Cfg::BN * t.nt), ld);
+        c.nst = c.nst1 = (p.Ep + 63) / 64;
         return t;
       },
       [&](const StTile& t, typename Cfg::Acc& acc) {
-        const StOut o = st_out(dx + (int64_t)t.r0 * d, (int64_t)d * 2, t.R);
-        if (!add) {
-          st_store_tile(o, acc, Cfg::BN * t.nt, d);
+        const StOut o = st_out(p.dx + (int64_t)t.r0 * p.d, (int64_t)p.d * 2, t.R);
+        if constexpr (KIND == RG_ROWS) {
+          store_tile_rows(o, acc, Cfg::BN * t.nt, p.d, ring + Cfg::LDS);
           return;
         }
-        const __amdgpu_buffer_rsrc_t ra = gc_rsrc(add + (int64_t)t.r0 * d, (uint32_t)t.R * (uint32_t)d * 2);
+        if (KIND == RG_FEW && !p.add) {
+          st_store_tile(o, acc, Cfg::BN * t.nt, p.d);
+          return;
+        }
+        const __amdgpu_buffer_rsrc_t ra = gc_rsrc(p.add + (int64_t)t.r0 * p.d, (uint32_t)t.R * (uint32_t)p.d * 2);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const int row = 16 * MT * (wave & 3) + 16 * mt + i;
@@ -215,7 +238,7 @@ __global__ __launch_bounds__(ST_NT, 1) void row_grad(const bf16_t* __restrict__ 
           for (int k = 0; k < Cfg::NT / 2; ++k) {
             const int col = Cfg::BN * t.nt + Cfg::WN * (wave >> 2) + 32 * k + 8 * q;
             av[k] = __builtin_amdgcn_raw_buffer_load_b128(
-                ra, col < d ? ((uint32_t)row * (uint32_t)d + (uint32_t)col) * 2u : 0xFFFFFFF0u, 0, 0);
+                ra, col < p.d ? ((uint32_t)row * (uint32_t)p.d + (uint32_t)col) * 2u : 0xFFFFFFF0u, 0, 0);
           }
 #pragma unroll
           for (int k = 0; k < Cfg::NT / 2; ++k) {
@@ -233,56 +256,99 @@ __global__ __launch_bounds__(ST_NT, 1) void row_grad(const bf16_t* __restrict__ 
               const float* z = h < 2 ? x + 2 * h : y + 2 * (h - 2);
               v[h] = cvt_bf16x2(z[0] + bf16_lo(av[k][h]), z[1] + bf16_hi(av[k][h]));
             }
-            st_put(o, row, 2u * (uint32_t)col, col < d, v);
+            st_put(o, row, 2u * (uint32_t)col, col < p.d, v);
           }
         }
       });
 }
 
-using GateWCfg = StCfg<4, ST_PANEL, ST_PANEL, f32x4, 1, false, 32>;
+constexpr int RG_XB = 64 * 256, RG_SLOT = 3 * RG_XB;   // a stage's 64 x 128 of x, with 64 x 256 of dl
+constexpr int RG_LDS = 3 * RG_SLOT;
 
-// Parts of dWg: tile (256 rows of d) x (256 experts) over an equal share of the
-// tokens, fp32 sums at part[share][d][Ep].
-__global__ __launch_bounds__(ST_NT, 1) void gate_weight_grad(const bf16_t* __restrict__ x,
-                                                             const bf16_t* __restrict__ dl, float* __restrict__ part,
-                                                             int T, int d, int Ep, int shares) {
-  using Cfg = GateWCfg;
-  __shared__ __attribute__((aligned(16))) char ring[Cfg::LDS];
-  const int nm = (d + 255) / 256, nn = (Ep + 255) / 256;
-  const int stages = (T + 63) / 64, each = (stages + shares - 1) / shares;
-  struct Unit {
-    int m, n, s, rows, nst;
-  };
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ void weight_unit(const RouteGrad& p, int u, char* lds) {
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  st_run<Cfg>(
-      nm * nn * shares, ring,
-      [&](int L, StCtx<Cfg>& c) {
-        Unit u;
-        u.s = st_div(L, nm * nn);
-        const int at = L - u.s * nm * nn;
-        u.m = st_div(at, nn);
-        u.n = at - u.m * nn;
-        const int64_t first = (int64_t)64 * each * u.s;
-        u.rows = (int)max((int64_t)0, min((int64_t)T - first, (int64_t)64 * each));
-        u.rows = __builtin_amdgcn_readfirstlane(u.rows);
-        st_panel(c.a[0], x + first * d, (uint32_t)d * 2, u.rows, 256 * u.m, d);
-        st_panel(c.b[0], dl + first * Ep, (uint32_t)Ep * 2, u.rows, 256 * u.n, Ep);
-        c.nst = c.nst1 = u.nst = (u.rows + 63) / 64;
-        return u;
-      },
-      [&](const Unit& u, typename Cfg::Acc& acc) {
-        const int row0 = 256 * u.m;
-        const StOut o = st_out(part + ((int64_t)u.s * d + row0) * Ep, (int64_t)Ep * 4, min(256, d - row0));
+  const int wm = wave & 1, wn = wave >> 1;
+  const int nn = (p.Ep + 255) / 256, stages = (p.T + 63) / 64, each = (stages + p.shares - 1) / p.shares;
+  // the shares of a block of rows run far apart, neighbours share their dl in an L2
+  const int md = st_div(u, nn * p.shares), rest = u - md * nn * p.shares, share = st_div(rest, nn), nb = rest - share * nn;
+  const int64_t first = (int64_t)64 * each * share;
+  const int rows = __builtin_amdgcn_readfirstlane((int)max((int64_t)0, min((int64_t)p.T - first, (int64_t)64 * each)));
+  const int nst = (rows + 63) / 64;
+  const uint32_t lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)lds);
+  // x: copy c of wave w holds K-rows 8 w + 4 c .. + 3 of the half-panel
+  const uint32_t ldx = (uint32_t)p.d * 2u;
+  const int sig = (lane >> 4) | ((wave & 1) << 2);
+  const int xcol = 128 * md + 8 * ((lane & 15) ^ (2 * sig));
+  const uint32_t vx = xcol < p.d ? (uint32_t)(8 * wave + (lane >> 4)) * ldx + 2u * (uint32_t)xcol : GC_OOR;
+  const char* xb = (const char*)(p.x + first * p.d);
+  StOp<ST_PANEL, 256> q;
+  st_panel(q, p.dl + first * p.Ep, (uint32_t)p.Ep * 2u, rows, 256 * nb, p.Ep);
+  auto issue = [&](int slot, int st) {
+    const uint32_t at = lbase + slot * RG_SLOT;
+    const int left = __builtin_amdgcn_readfirstlane(max(0, min(64, rows - 64 * st)));
+    const __amdgpu_buffer_rsrc_t r = gc_rsrc(xb + (int64_t)st * 64 * ldx, (uint32_t)left * ldx);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+    for (int c = 0; c < 2; ++c) bd_copy16(r, at + 2048 * wave + 1024 * c, vx, (uint32_t)(4 * c) * ldx);
+    st_issue(q, at + RG_XB, st);
+  };
+  f32x4 acc[4][4];
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const int col = 256 * u.n + 128 * (wave >> 2) + 16 * t + 4 * (lane >> 4);
-            st_put(o, 64 * (wave & 3) + 16 * mt + (lane & 15), 4u * (uint32_t)col, col < Ep,
-                   __builtin_bit_cast(u32x4, acc[mt][t]));
-          }
-      });
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int xo = st_lane<ST_PANEL>(4 * wm), lo = st_lane<ST_PANEL>(4 * wn);
+  if (nst > 0) issue(0, 0);
+  if (nst > 1) issue(1, 1);
+  int slot = 0;
+  for (int s = 0; s < nst; ++s) {
+    // this stage has arrived in every wave, all are done with the one before
+    if (s + 1 < nst) st_sync<6>();
+    else st_sync<0>();
+    const int third = slot == 0 ? 2 : slot - 1;
+    if (s + 2 < nst) issue(third, s + 2);
+    const char* at = lds + slot * RG_SLOT;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4 xf[4], lf[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        xf[t] = st_frag<ST_PANEL>(at, xo, ks, t);
+        lf[t] = st_frag<ST_PANEL>(at + RG_XB, lo, ks, t);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) acc[mt][t] = st_mfma(lf[t], xf[mt], acc[mt][t]);
+    }
+    slot = slot == 2 ? 0 : slot + 1;
+  }
+  const int row0 = 128 * md;
+  const StOut o = st_out(p.part + ((int64_t)share * p.d + row0) * p.Ep, (int64_t)p.Ep * 4, min(128, p.d - row0));
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int col = 256 * nb + 64 * wn + 16 * t + 4 * g;
+      st_put(o, 64 * wm + 16 * mt + i, 4u * (uint32_t)col, col < p.Ep, __builtin_bit_cast(u32x4, acc[mt][t]));
+    }
+  __syncthreads();   // before LDS is written again
+}
+
+template <int KIND>
+__global__ __launch_bounds__(512, 1) void route_grad(RouteGrad p) {
+  constexpr int LR = RowCfg<KIND>::LDS + (KIND == RG_ROWS ? 8 * 4096 : 0);
+  __shared__ __attribute__((aligned(16))) char lds[LR > RG_LDS ? LR : RG_LDS];
+  for (int phase = 0; phase < 2; ++phase) {
+    if ((((int)blockIdx.x >> 3) + phase) & 1) {
+      if (p.dx) row_tiles<KIND>(p, lds);
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // all are done with LDS
+    } else if (p.part) {
+      const int units = (p.d + 127) / 128 * ((p.Ep + 255) / 256) * p.shares;
+      // from the other end, so that a workgroup with a tile less of dx has a unit more
+      for (int u = (int)gridDim.x - 1 - st_first_tile(); u < units; u += (int)gridDim.x) weight_unit(p, u, lds);
+    }
+  }
 }
 
 // What remains of dWg and db, the parts' sums in their order.  The first ceil(E / 64)
@@ -388,10 +454,10 @@ __global__ __launch_bounds__(256) void clear_grads(char* __restrict__ a, int64_t
 
 static size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Shares of the tokens that the tiles of dWg are split into: as many as give every
+// Shares of the tokens that the units of dWg are split into: as many as give every
 // compute unit one, each of at least four stages.
 static int rb_shares(const Prob& p) {
-  const int64_t tiles = (int64_t)((p.d + 255) / 256) * ((p.E + 255) / 256), stages = ((int64_t)p.T + 63) / 64;
+  const int64_t tiles = (int64_t)((p.d + 127) / 128) * ((p.E + 255) / 256), stages = ((int64_t)p.T + 63) / 64;
   return (int)std::max<int64_t>(1, std::min<int64_t>(device_cus() / tiles, stages / 4));
 }
 
@@ -453,32 +519,27 @@ hipError_t launch_route_backward(const Prob& p, const SelectRule& r, const void*
                          (bf16_t*)nullptr, (const float*)colsum, rb_blocks(p), dbias);
     return hipGetLastError();
   }
-  if (dx) {
+  if (!products && !dbias) return hipSuccess;
+  const int shares = rb_shares(p);
+  float* part = (float*)(at + L.part);
+  if (products) {
     const bf16_t* w = (const bf16_t*)wg;
-    if (p.E % 8) {
+    if (dx && p.E % 8) {
       w = (const bf16_t*)(at + L.wg);
       hipLaunchKernelGGL(pad_rows, dim3((unsigned)std::min<int64_t>(((int64_t)p.d * Ep + 255) / 256, 4096)), dim3(256), 0, st,
                          (const bf16_t*)wg, (int64_t)p.d, p.E, Ep, (bf16_t*)(at + L.wg));
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    e = st_with_height(st_height(device_cus(), 1, p.T, (int64_t)Ep * 2, p.d, 128), [&](auto h) {
-      constexpr int bn = RowCfg<h()>::BN;
-      const int ntn = (p.d + bn - 1) / bn;
-      hipLaunchKernelGGL(row_grad<h()>, st_row_grid(p.T, 1, h(), ntn), dim3(ST_NT), 0, st, (const bf16_t*)dlb, w,
-                         (const bf16_t*)dx_add, (bf16_t*)dx, p.T, p.d, Ep, ntn);
-      return hipGetLastError();
-    });
-    if (e != hipSuccess) return e;
-  }
-  if (!dwg && !dbias) return hipSuccess;
-  const int shares = rb_shares(p);
-  float* part = (float*)(at + L.part);
-  if (dwg) {
-    const int64_t tiles = (int64_t)((p.d + 255) / 256) * ((Ep + 255) / 256) * shares;
-    hipLaunchKernelGGL(gate_weight_grad, dim3(st_grid(tiles)), dim3(ST_NT), 0, st, (const bf16_t*)x, (const bf16_t*)dlb,
-                       part, p.T, p.d, Ep, shares);
+    RouteGrad q{(const bf16_t*)x, w, dlb, (const bf16_t*)dx_add, (bf16_t*)dx, dwg ? part : nullptr, p.T, p.d, Ep, shares};
+    const int64_t tiles = (((int64_t)p.T + 255) / 256) * ((p.d + 255) / 256);
+    const bool few = tiles < device_cus() / 2;   // less than half a round of 256 x 256 tiles: 64 x 128
+    int64_t units = dwg ? (int64_t)((p.d + 127) / 128) * ((Ep + 255) / 256) * shares : 0;
+    if (dx) units += few ? (((int64_t)p.T + 63) / 64) * ((p.d + 127) / 128) : tiles;
+    auto kern = few ? route_grad<RG_FEW> : dx_add ? route_grad<RG_ADD> : route_grad<RG_ROWS>;
+    hipLaunchKernelGGL(kern, dim3(st_grid(units)), dim3(512), 0, st, q);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
+  if (!dwg && !dbias) return hipSuccess;
   const int64_t count = !dwg ? 0 : p.E == Ep ? (int64_t)p.d * p.E / 8 : (int64_t)p.d * p.E;
   const int64_t blocks = std::min<int64_t>((count + 1023) / 1024, 1024) + (dbias ? (p.E + 63) / 64 : 0);
   hipLaunchKernelGGL(gate_sums, dim3((unsigned)blocks), dim3(1024), 0, st, (const float*)part, shares, (int64_t)p.d, p.E, Ep,

@@ -492,6 +492,44 @@ __device__ __forceinline__ void st_store_tile(const StOut& o, const f32x4 (&acc)
     }
 }
 
+// A finished tile through a 4 KB staging area of each wave: a store then writes four
+// rows of 256 bytes instead of sixteen pieces of 64, which cost the address
+// unit about 100 cycles an instruction and bounded tiles that mostly store.
+// Staged rows keep their 32-byte chunk c at c ^ (row & 7), rows 8 .. 15 with its
+// halves exchanged, so that 32 lanes' writes meet 64 distinct banks (sparse
+// weight gradients 825 -> 789 us).  The stores pass L2 by, except for narrow rows
+// that do not start on cache lines, whose pieces L2 merges (30 experts of 64 rows,
+// rows of 784 bytes: 378 -> 313 us; of 768: 237 past L2, 269 through it; four
+// column blocks of 2000 bytes: 142 and 171).  Where exactly wider rows change sides is
+// not known: with M = 7168 and 30 experts of 64 rows, going through L2 was faster up to
+// the widest tried (rows of 976 bytes 412 past, 354 through; 1040: 487, 450; 1424:
+// 613, 521; 2000: 778, 682; 2448: 997, 892).
+__device__ __forceinline__ void store_tile_rows(const StOut& o, const f32x4 (&acc)[4][8], int col0, int N, char* stage) {
+  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char* stg = stage + 4096 * wave;
+  const bool merge = N <= 512 && (N & 63) != 0;
+  const int p = lane & 15, col = col0 + 128 * (wave >> 2) + 8 * p;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const f32x4 v = acc[mt][t];
+      *reinterpret_cast<u32x2*>(stg + i * 256 + 32 * (t ^ (i & 7)) + 8 * (q ^ (2 * (i >> 3)))) =
+          u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+    }
+    lds_wave_order();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 4 * k + q;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * 256 + 32 * ((p >> 1) ^ (row & 7)) + 16 * ((p & 1) ^ (row >> 3)));
+      if (merge) st_put(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
+      else st_put<true>(o, 64 * (wave & 3) + 16 * mt + row, 2u * (uint32_t)col, col < N, v);
+    }
+    lds_wave_order();
+  }
+}
+
 // ---------------------------------------------------------------------------
 // row blocks of expert segments
 // ---------------------------------------------------------------------------
