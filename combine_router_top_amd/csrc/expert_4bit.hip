@@ -120,11 +120,26 @@ __device__ __forceinline__ void w4_store(void* c, int64_t at, const float (&o)[4
         u32x2{cvt_bf16x2(o[0], o[1]), cvt_bf16x2(o[2], o[3])};
 }
 
+// The value of lane N of a row of 16 lanes in all of them; n is a constant after unrolling.
+__device__ __forceinline__ uint32_t row_lane(uint32_t v, int n) {
+  switch (n) {
+#define ROW_LANE(N) \
+  case N: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xf, 0xf, false);
+    ROW_LANE(0) ROW_LANE(1) ROW_LANE(2) ROW_LANE(3) ROW_LANE(4) ROW_LANE(5) ROW_LANE(6) ROW_LANE(7)
+    ROW_LANE(8) ROW_LANE(9) ROW_LANE(10) ROW_LANE(11) ROW_LANE(12) ROW_LANE(13) ROW_LANE(14)
+#undef ROW_LANE
+    default: return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x15F, 0xf, 0xf, false);
+  }
+}
+
 // Up to 16 MT rows o .. o + R - 1 against NT 16-column tiles (GATED: NT / 2 of each
-// matrix).  The KS waves split K evenly by blocks; each loads its blocks straight into
-// registers, one ahead of its use, and the fp32 sums meet in LDS in wave order.
-// GPB: groups of a block.
-template <int MT, int NT, bool GATED, bool F32OUT, int KS, int GPB>
+// matrix).  The KS waves split K evenly by blocks; each loads its blocks straight into a
+// ring of RB sets of registers, RB - 1 ahead of their use, and the fp32 sums meet in LDS in
+// wave order.  GPB: groups of a block.  A lane needs the scales of four columns of each tile
+// and group, the same for 16 lanes: each of the 16 loads another tile's or group's, and
+// DPP hands them round (a load instruction occupies the address unit 16 cycles, whatever
+// its lanes share).
+template <int MT, int NT, bool GATED, bool F32OUT, int KS, int GPB, bool ZERO, int RB>
 __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, int R, f32x4* red, int stride) {
   constexpr int NH = GATED ? NT / 2 : NT, SPG = 4 / GPB;   // k-steps of a group
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -132,10 +147,11 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
   const int tile0 = (int)blockIdx.x * NH;
   const uint32_t run = (uint32_t)p.kb * 1024u;
   const int per = (p.kb + KS - 1) / KS, s0 = wave * per, ns = max(0, min(per, p.kb - s0));
+  const int kend = min(p.K, (s0 + ns) * W4_KB);   // rows read zeros from there on
   const int64_t ge = (int64_t)e * p.groups * p.N;
   const uint32_t gsize = (uint32_t)p.groups * (uint32_t)p.N;
   __amdgpu_buffer_rsrc_t rb[NT], rs[GATED ? 2 : 1], rz[GATED ? 2 : 1];
-  uint32_t vs[NH];   // a lane's four columns of each tile
+  constexpr int MATS = GATED ? 2 : 1;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const char* base = GATED && t >= NH ? p.b3 : p.b1;
@@ -143,23 +159,22 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
     rb[t] = gc_rsrc(base + ((int64_t)e * p.ntiles + nt) * run + (int64_t)s0 * 1024, (uint32_t)ns * 1024u);
   }
 #pragma unroll
-  for (int m = 0; m < (GATED ? 2 : 1); ++m) {
+  for (int m = 0; m < MATS; ++m) {
     const uint8_t* z = m ? p.z3 : p.z1;
     rs[m] = gc_rsrc((m ? p.s3 : p.s1) + ge, gsize * 2u);
     rz[m] = gc_rsrc(z ? z + ge : (const uint8_t*)p.a, z ? gsize : 0u);
   }
-#pragma unroll
-  for (int t = 0; t < NH; ++t) {
-    const int col = 16 * (tile0 + t) + 4 * g;
-    vs[t] = col < p.N ? (uint32_t)col : GC_OOR >> 1;
-  }
+  // lane i of a row loads tile i / GPB and group i % GPB
+  static_assert(NH * GPB <= 16, "a lane for each tile and group");
+  const int scol = 16 * (tile0 + min(i / GPB, NH - 1)) + 4 * g;
+  const uint32_t vs = scol < p.N ? (uint32_t)(i % GPB) * (uint32_t)p.N + (uint32_t)scol : GC_OOR >> 1;
   const __amdgpu_buffer_rsrc_t ra = gc_rsrc(p.a + (int64_t)o * p.K, (uint32_t)R * (uint32_t)p.K * 2u);
   uint32_t va[MT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
     va[mt] = 16 * mt + i < R ? ((uint32_t)(16 * mt + i) * (uint32_t)p.K + 8u * (uint32_t)g) * 2u : GC_OOR;
   const uint32_t vb = 16u * (uint32_t)lane;
-  // what is subtracted from 16 + q: the zero point, 8 where there are none
+  // what is subtracted from 16 + q: the zero point, 8 where there are none (they read as zeros)
   const float zb1 = p.z1 ? -16.f : -24.f, zb3 = GATED && p.z3 ? -16.f : -24.f;
 
   const uint32_t mask = w4_mask(), bits = w4_bits();
@@ -168,29 +183,26 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  u32x4 w[2][NT], x[2][MT][4];
-  u32x2 sc[2][NT][GPB];
-  uint32_t zp[2][NT][GPB];
-  auto load = [&](int h, int b) {   // block b of this wave; one past its last reads zeros
+  u32x4 w[RB][NT], x[RB][MT][4];
+  u32x2 sc[RB][MATS];
+  uint32_t zp[RB][MATS];
+  auto load = [&](int h, int b) {   // block b of this wave; of one past its last, rows and weights are zeros
 #pragma unroll
     for (int t = 0; t < NT; ++t) w[h][t] = __builtin_amdgcn_raw_buffer_load_b128(rb[t], vb, b * 1024, 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int k = (s0 + b) * W4_KB + 32 * q;
-      const bool in = k + 8 * g < p.K;
+      const bool in = k + 8 * g < kend;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
         x[h][mt][q] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? va[mt] : GC_OOR, (uint32_t)k * 2u, 0);
     }
+    const uint32_t row = (uint32_t)((s0 + b) * GPB) * (uint32_t)p.N;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int u = 0; u < GPB; ++u) {
-        const int m = GATED && t >= NH;
-        const uint32_t row = (uint32_t)((s0 + b) * GPB + u) * (uint32_t)p.N;
-        sc[h][t][u] = __builtin_amdgcn_raw_buffer_load_b64(rs[m], vs[t % NH] * 2u, row * 2u, 0);
-        zp[h][t][u] = __builtin_amdgcn_raw_buffer_load_b32(rz[m], vs[t % NH], row, 0);
-      }
+    for (int m = 0; m < MATS; ++m) {
+      sc[h][m] = __builtin_amdgcn_raw_buffer_load_b64(rs[m], vs * 2u, row * 2u, 0);
+      if (ZERO) zp[h][m] = __builtin_amdgcn_raw_buffer_load_b32(rz[m], vs, row, 0);
+    }
   };
   auto multiply = [&](int h) {
     const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
@@ -216,12 +228,14 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const u32x2 s2 = sc[h][t][u];
+        const int m = GATED && t >= NH, from = t % NH * GPB + u;
+        const u32x2 s2 = u32x2{row_lane(sc[h][m][0], from), row_lane(sc[h][m][1], from)};
+        const uint32_t zq = ZERO ? row_lane(zp[h][m], from) : 0u;
         const float s[4] = {bf16_lo(s2[0]), bf16_hi(s2[0]), bf16_lo(s2[1]), bf16_hi(s2[1])};
         const float zb = GATED && t >= NH ? zb3 : zb1;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float z = zb - (float)((zp[h][t][u] >> (8 * r)) & 255u);
+          const float z = ZERO ? zb - (float)((zq >> (8 * r)) & 255u) : -24.f;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) acc[mt][t][r] = fmaf(s[r], fmaf(z, X[mt][r], part[mt][t][r]), acc[mt][t][r]);
         }
@@ -229,17 +243,16 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
     }
   };
   if (ns > 0) {
-    load(0, 0);
-    for (int b = 0; b < ns; b += 2) {
-      load(1, b + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(0);
-      __builtin_amdgcn_sched_barrier(0);
-      if (b + 1 == ns) break;
-      load(0, b + 2);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(1);
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int h = 0; h + 1 < RB; ++h) load(h, h);
+    for (int b = 0; b < ns; b += RB) {
+#pragma unroll
+      for (int h = 0; h < RB; ++h) {
+        load((h + RB - 1) % RB, b + h + RB - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(h);   // a block past the last adds zeros
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
 #pragma unroll
@@ -267,7 +280,7 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
 
 // All rows of a segment, 16 MT at a time, the blocks dealt out over gridDim.z
 // workgroups; longer segments read their weights again for each block, from the caches.
-template <int MT, int NT, bool GATED, bool F32OUT, int KS, int GPB>
+template <int MT, int NT, bool GATED, bool F32OUT, int KS, int GPB, bool ZERO, int RB>
 __global__ __launch_bounds__(64 * KS) void w4_stream(W4Args p) {
   __shared__ __attribute__((aligned(16))) f32x4 red[KS][MT * NT][64];
   const int e = blockIdx.y;
@@ -278,29 +291,30 @@ __global__ __launch_bounds__(64 * KS) void w4_stream(W4Args p) {
   for (int r0 = 16 * MT * (int)blockIdx.z; r0 < R; r0 += step) {
     if (r0 >= step) __syncthreads();   // the sums before have been read
     if (MT == 1 || R - r0 <= 16)
-      w4_stream_block<1, NT, GATED, F32OUT, KS, GPB>(p, e, o + r0, min(16, R - r0), &red[0][0][0], stride);
-    else w4_stream_block<MT, NT, GATED, F32OUT, KS, GPB>(p, e, o + r0, min(16 * MT, R - r0), &red[0][0][0], stride);
+      w4_stream_block<1, NT, GATED, F32OUT, KS, GPB, ZERO, RB>(p, e, o + r0, min(16, R - r0), &red[0][0][0], stride);
+    else w4_stream_block<MT, NT, GATED, F32OUT, KS, GPB, ZERO, RB>(p, e, o + r0, min(16 * MT, R - r0), &red[0][0][0], stride);
   }
 }
 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-template <bool GATED, bool F32OUT, int GPB>
-static hipError_t launch_4bit_stream(const W4Args& p, int64_t most, hipStream_t st) {
+template <bool GATED, bool F32OUT, int GPB, bool ZERO>
+static hipError_t launch_4bit_stream(const W4Args& p, int64_t mean, int64_t most, hipStream_t st) {
   const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
-  const int64_t blocks = std::min<int64_t>((most + 31) / 32, p.offsets ? 4 : 1024);
+  const bool low = most <= 16 || mean <= 8;
+  const int64_t blocks = std::min<int64_t>(low ? (most + 15) / 16 : (most + 31) / 32, p.offsets ? 4 : 1024);
   auto go = [&](auto kernel, int cols, int ks) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n, (unsigned)blocks), dim3(64 * ks), 0,
                        st, p);
     return hipGetLastError();
   };
   constexpr int NT = GATED ? 2 : 1;
-  if (most <= 16)
-    return wide ? go(w4_stream<1, 4, GATED, F32OUT, 4, GPB>, GATED ? 32 : 64, 4)
-                : go(w4_stream<1, NT, GATED, F32OUT, 8, GPB>, 16, 8);
-  return wide ? go(w4_stream<2, 4, GATED, F32OUT, 4, GPB>, GATED ? 32 : 64, 4)
-              : go(w4_stream<2, NT, GATED, F32OUT, 8, GPB>, 16, 8);
+  if (low)
+    return wide ? go(w4_stream<1, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, GATED ? 32 : 64, 4)
+                : go(w4_stream<1, NT, GATED, F32OUT, 8, GPB, ZERO, 2>, 16, 8);
+  return wide ? go(w4_stream<2, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, GATED ? 32 : 64, 4)
+              : go(w4_stream<2, NT, GATED, F32OUT, 8, GPB, ZERO, 2>, 16, 8);
 }
 
 template <bool GATED, bool F32OUT>
@@ -311,9 +325,14 @@ static hipError_t launch_4bit(W4Args p, int group, int64_t mean, int64_t most, i
   if (tiles)
     return GATED ? launch_4bit_tiles_up(p, group, mean > 64 ? 2 : 1, rows_max, st)
                  : launch_4bit_tiles_down(p, group, mean > 64 ? 2 : 1, rows_max, F32OUT, st);
-  return group == 32   ? launch_4bit_stream<GATED, F32OUT, 4>(p, most, st)
-         : group == 64 ? launch_4bit_stream<GATED, F32OUT, 2>(p, most, st)
-                       : launch_4bit_stream<GATED, F32OUT, 1>(p, most, st);
+  const bool zero = p.z1 || (GATED && p.z3);
+  auto with = [&](auto gpb) {
+    return zero ? launch_4bit_stream<GATED, F32OUT, gpb(), true>(p, mean, most, st)
+                : launch_4bit_stream<GATED, F32OUT, gpb(), false>(p, mean, most, st);
+  };
+  return group == 32   ? with(std::integral_constant<int, 4>{})
+         : group == 64 ? with(std::integral_constant<int, 2>{})
+                       : with(std::integral_constant<int, 1>{});
 }
 
 size_t packed_4bit_bytes(int n, int K, int N) {
