@@ -61,7 +61,7 @@ MOE_WS_H, MOE_WS_Y_PACKED = 0, 1
 MOE_CALL_ROUTE, MOE_CALL_DISPATCH, MOE_CALL_EXPERT_GEMM, MOE_CALL_COMBINE, MOE_CALL_LAYER = range(5)
 MOE_CALL_DISPATCH_PADDED, MOE_CALL_EXPERT_GEMM_PADDED = 5, 6
 MOE_CALL_EXPERT_GEMM_BACKWARD, MOE_CALL_EXPERT_GEMM_QUANTIZED = 7, 8
-MOE_CALL_ROUTE_SCORED, MOE_CALL_ROUTE_BACKWARD = 9, 10
+MOE_CALL_ROUTE_SCORED, MOE_CALL_ROUTE_BACKWARD, MOE_CALL_EXPERT_GEMM_FOURBIT = 9, 10, 11
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_SCOPE_AGENT, MOE_SCOPE_SYSTEM = 0, 1
 
@@ -73,7 +73,8 @@ EXPORTED = ["moe_last_error", "moe_version", "moe_workspace_bytes", "moe_route",
             "moe_quantize_rows", "moe_packed_weights_bytes", "moe_pack_weights",
             "moe_quantize_weights", "moe_gemm_quantized", "moe_expert_gemm_quantized",
             "moe_select", "moe_route_scored", "moe_route_backward", "moe_packed_weights_fourbit_bytes",
-            "moe_pack_weights_fourbit", "moe_quantize_weights_fourbit", "moe_gemm_fourbit", "moe_expert_gemm_fourbit"]
+            "moe_pack_weights_fourbit", "moe_quantize_weights_fourbit", "moe_gemm_fourbit",
+            "moe_gemm_fourbit_workspace_bytes", "moe_expert_gemm_fourbit"]
 
 
 class MoeError(RuntimeError):
@@ -150,8 +151,10 @@ def lib() -> ctypes.CDLL:
         L.moe_packed_weights_fourbit_bytes.restype = sz
         L.moe_pack_weights_fourbit.argtypes = [i32, i32, i32, vp, vp, vp]
         L.moe_quantize_weights_fourbit.argtypes = [i32] * 5 + [vp] * 5
-        L.moe_gemm_fourbit.argtypes = [i32] * 4 + [vp] * 5 + [i32, vp]
-        L.moe_expert_gemm_fourbit.argtypes = [P, i32] + [vp] * 14
+        L.moe_gemm_fourbit_workspace_bytes.argtypes = [i32] * 3
+        L.moe_gemm_fourbit_workspace_bytes.restype = sz
+        L.moe_gemm_fourbit.argtypes = [i32] * 4 + [vp] * 5 + [i32, vp, sz, vp]
+        L.moe_expert_gemm_fourbit.argtypes = [P, i32] + [vp] * 14 + [sz, vp]
         for n in ("moe_select", "moe_route_scored", "moe_route_backward", "moe_pack_weights_fourbit",
                   "moe_quantize_weights_fourbit", "moe_gemm_fourbit", "moe_expert_gemm_fourbit"):
             getattr(L, n).restype = i32
@@ -853,7 +856,16 @@ def quantize_weights_4bit(w, group: int = 128, zero: bool = False, stream=None, 
     return packed, s, z if zero else None
 
 
-def gemm_4bit(a, packed, scale, zero=None, group: int = 128, dtype=None, stream=None, out=None):
+def gemm_4bit_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of scratch of ``gemm_4bit`` (0 for few rows)."""
+    _fits(M | N | K, "a size of the product")
+    n = int(lib().moe_gemm_fourbit_workspace_bytes(M, N, K))
+    if n == 0 and lib().moe_last_error():
+        raise MoeError(MOE_ERR_INVALID_ARG, lib().moe_last_error().decode())
+    return n
+
+
+def gemm_4bit(a, packed, scale, zero=None, group: int = 128, dtype=None, workspace=None, stream=None, out=None):
     """C = rnd(a W): bf16 a [M, K], packed 4-bit weights of one [K, N] matrix with their
     scales and zero points (None: 8); ``dtype`` (default torch.bfloat16, or that of
     ``out``) is C's."""
@@ -867,16 +879,24 @@ def gemm_4bit(a, packed, scale, zero=None, group: int = 128, dtype=None, stream=
     if out is None:
         with _alloc_on(stream):
             out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
-    _check(lib().moe_gemm_fourbit(
-        M, N, K, group, pa, _at(cur, packed, packed_weights_4bit_shape(K, N), torch.int32, "packed"),
-        _at(cur, scale, rows, torch.bfloat16, "scale"),
-        None if zero is None else _at(cur, zero, rows, torch.uint8, "zero"),
-        _at(cur, out, (M, N), dtype or out.dtype, "out"), _dtype_code(out, "out"), _stream_at(cur, stream)))
+    ins = (_at(cur, packed, packed_weights_4bit_shape(K, N), torch.int32, "packed"),
+           _at(cur, scale, rows, torch.bfloat16, "scale"),
+           None if zero is None else _at(cur, zero, rows, torch.uint8, "zero"),
+           _at(cur, out, (M, N), dtype or out.dtype, "out"), _dtype_code(out, "out"))
+    if workspace is None:
+        need = gemm_4bit_workspace_bytes(M, N, K)
+        if need:
+            with _alloc_on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+    elif workspace.get_device() != cur:
+        raise ValueError(f"workspace is on device {workspace.get_device()}, the current device is {cur}")
+    _check(lib().moe_gemm_fourbit(M, N, K, group, pa, *ins, _ptr(workspace),
+                                  0 if workspace is None else workspace.numel(), _stream_at(cur, stream)))
     return out
 
 
 def expert_gemm_4bit(p: Spec, x_packed, offsets, w1, s1, z1, w3, s3, z3, w2, s2, z2, group: int = 128,
-                     stream=None, out=None):
+                     workspace=None, stream=None, out=None):
     """``expert_gemm`` with packed 4-bit weights [n_local, ...], their scales and zero
     points (each None or not): (h, y_packed)."""
     torch = _torch()
@@ -892,8 +912,9 @@ def expert_gemm_4bit(p: Spec, x_packed, offsets, w1, s1, z1, w3, s3, z3, w2, s2,
         with _alloc_on(stream):
             out = tuple(torch.zeros(v, dtype=dt, device=x_packed.device) for v in (tall, wide))
     h, yp = out
-    _check(lib().moe_expert_gemm_fourbit(p.ref(), group, *ins, _at(cur, h, tall, dt, "h"),
-                                      _at(cur, yp, wide, dt, "y_packed"), _stream_at(cur, stream)))
+    outs = (_at(cur, h, tall, dt, "h"), _at(cur, yp, wide, dt, "y_packed"))
+    ws, at, size = _workspace_at(cur, p, MOE_CALL_EXPERT_GEMM_FOURBIT, workspace, stream)
+    _check(lib().moe_expert_gemm_fourbit(p.ref(), group, *ins, *outs, at, size, _stream_at(cur, stream)))
     return h, yp
 
 

@@ -300,39 +300,140 @@ __global__ __launch_bounds__(64 * KS) void w4_stream(W4Args p) {
 // launches
 // ---------------------------------------------------------------------------
 template <bool GATED, bool F32OUT, int GPB, bool ZERO>
-static hipError_t launch_4bit_stream(const W4Args& p, int64_t mean, int64_t most, hipStream_t st) {
-  const bool wide = (int64_t)((p.N + (GATED ? 31 : 63)) / (GATED ? 32 : 64)) * p.n >= device_cus();
-  const bool low = most <= 16 || mean <= 8;
-  const int64_t blocks = std::min<int64_t>(low ? (most + 15) / 16 : (most + 31) / 32, p.offsets ? 4 : 1024);
+static hipError_t launch_4bit_stream(const W4Args& p, const W4Plan& plan, hipStream_t st) {
   auto go = [&](auto kernel, int cols, int ks) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n, (unsigned)blocks), dim3(64 * ks), 0,
-                       st, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + cols - 1) / cols), (unsigned)p.n, (unsigned)plan.blocks), dim3(64 * ks),
+                       0, st, p);
     return hipGetLastError();
   };
   constexpr int NT = GATED ? 2 : 1;
-  if (low)
-    return wide ? go(w4_stream<1, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, GATED ? 32 : 64, 4)
-                : go(w4_stream<1, NT, GATED, F32OUT, 8, GPB, ZERO, 2>, 16, 8);
-  return wide ? go(w4_stream<2, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, GATED ? 32 : 64, 4)
-              : go(w4_stream<2, NT, GATED, F32OUT, 8, GPB, ZERO, 2>, 16, 8);
+  if (plan.low)
+    return plan.wide ? go(w4_stream<1, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, GATED ? 32 : 64, 4)
+                     : go(w4_stream<1, NT, GATED, F32OUT, 8, GPB, ZERO, 2>, 16, 8);
+  return plan.wide ? go(w4_stream<2, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, GATED ? 32 : 64, 4)
+                   : go(w4_stream<2, NT, GATED, F32OUT, 8, GPB, ZERO, 2>, 16, 8);
 }
 
+// What a plan says, for the shape it was made for.
 template <bool GATED, bool F32OUT>
-static hipError_t launch_4bit(W4Args p, int group, int64_t mean, int64_t most, int64_t rows_max, hipStream_t st) {
-  const bool tiles = mean > 64;
-  p.lo = 0;
-  p.hi = INT32_MAX;
-  if (tiles)
-    return GATED ? launch_4bit_tiles_up(p, group, mean > 64 ? 2 : 1, rows_max, st)
-                 : launch_4bit_tiles_down(p, group, mean > 64 ? 2 : 1, rows_max, F32OUT, st);
+static hipError_t launch_4bit(const W4Args& p, const W4Plan& plan, int group, int64_t rows_max, hipStream_t st) {
+  if (plan.tiles)
+    return GATED ? launch_4bit_tiles_up(p, group, plan.bm, rows_max, st)
+                 : launch_4bit_tiles_down(p, group, plan.bm, rows_max, F32OUT, st);
   const bool zero = p.z1 || (GATED && p.z3);
   auto with = [&](auto gpb) {
-    return zero ? launch_4bit_stream<GATED, F32OUT, gpb(), true>(p, mean, most, st)
-                : launch_4bit_stream<GATED, F32OUT, gpb(), false>(p, mean, most, st);
+    return zero ? launch_4bit_stream<GATED, F32OUT, gpb(), true>(p, plan, st)
+                : launch_4bit_stream<GATED, F32OUT, gpb(), false>(p, plan, st);
   };
   return group == 32   ? with(std::integral_constant<int, 4>{})
          : group == 64 ? with(std::integral_constant<int, 2>{})
                        : with(std::integral_constant<int, 1>{});
+}
+
+// ---------------------------------------------------------------------------
+// what the tiles take: rows in fp16, exponents of rows and columns
+// ---------------------------------------------------------------------------
+// Exponent k that puts |v| in 2^(top-1) .. 2^top; 0 for zero, an infinity or a NaN.
+__device__ __forceinline__ int w4_exponent(uint32_t bits, int top) {
+  if (bits == 0 || bits >= 0x7F800000u) return 0;
+  return top - __builtin_amdgcn_frexp_expf(__uint_as_float(bits));
+}
+
+struct W4Columns {
+  const bf16_t* s;   // [n][groups][N]
+  int32_t* k;        // [n][N]
+  int groups, N;
+};
+struct W4Prepare {
+  const bf16_t* a;
+  bf16_t* out;            // fp16 bits
+  int32_t* kr;
+  int64_t rows;
+  const int32_t* limit;   // device row count, or NULL
+  int K, n;
+  W4Columns m[3];
+  int64_t columns;        // n * sum of N over the matrices given
+};
+
+constexpr int WP_U = 4;   // 8-value pieces a thread keeps between the two passes
+
+// The last workgroups take the columns, a thread for each, the others rows (grid-stride).
+// A row with an infinity or a NaN holds a NaN afterwards, and so does every product of it.
+__global__ __launch_bounds__(256) void w4_prepare(W4Prepare p, int row_blocks) {
+  if ((int)blockIdx.x >= row_blocks) {
+    for (int64_t c = ((int64_t)blockIdx.x - row_blocks) * 256 + threadIdx.x; c < p.columns;
+         c += ((int64_t)gridDim.x - row_blocks) * 256) {
+      int64_t at = c;
+      W4Columns m = p.m[0];
+      if (at >= (int64_t)p.n * m.N) {
+        at -= (int64_t)p.n * m.N;
+        m = p.m[1];
+        if (at >= (int64_t)p.n * m.N) {
+          at -= (int64_t)p.n * m.N;
+          m = p.m[2];
+        }
+      }
+      const int64_t e = at / m.N;
+      const bf16_t* s = m.s + e * m.groups * m.N + (at - e * m.N);
+      uint32_t top = 0;
+      for (int g = 0; g < m.groups; ++g) top = max(top, (uint32_t)s[(int64_t)g * m.N] & 0x7FFFu);
+      m.k[at] = w4_exponent(top << 16, 11);
+    }
+    return;
+  }
+  __shared__ uint32_t part[2][4];
+  const int nv = p.K / 8;
+  const int64_t rows = p.limit ? min(p.rows, (int64_t)*p.limit) : p.rows;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += row_blocks, flip ^= 1) {
+    const u32x4* src = reinterpret_cast<const u32x4*>(p.a + row * p.K);
+    u32x4 keep[WP_U];
+    uint32_t top = 0;   // largest magnitude, as bf16 bits in either half
+    auto see = [&](const u32x4& v) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
+    };
+#pragma unroll
+    for (int u = 0; u < WP_U; ++u)
+      if ((int)threadIdx.x + 256 * u < nv) keep[u] = src[threadIdx.x + 256 * u];
+#pragma unroll
+    for (int u = 0; u < WP_U; ++u)
+      if ((int)threadIdx.x + 256 * u < nv) see(keep[u]);
+    for (int v = threadIdx.x + 256 * WP_U; v < nv; v += 256) see(src[v]);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+    if ((threadIdx.x & 63) == 0) part[flip][threadIdx.x >> 6] = top;
+    __syncthreads();   // alternating halves: the next row's writes meet no reader of this one
+    top = max(max(part[flip][0], part[flip][1]), max(part[flip][2], part[flip][3]));
+    const int k = w4_exponent(top << 16, 15);
+    const bool bad = top >= 0x7F80u;
+    if (threadIdx.x == 0) p.kr[row] = k;
+    u32x4* dst = reinterpret_cast<u32x4*>(p.out + row * p.K);
+    auto convert = [&](const u32x4& v) {
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a = __builtin_ldexpf(bf16_lo(v[j]), k), b = __builtin_ldexpf(bf16_hi(v[j]), k);
+        if (bad) a = b = NAN;
+        o[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+      }
+      return o;
+    };
+#pragma unroll
+    for (int u = 0; u < WP_U; ++u)
+      if ((int)threadIdx.x + 256 * u < nv) dst[threadIdx.x + 256 * u] = convert(keep[u]);
+    for (int v = threadIdx.x + 256 * WP_U; v < nv; v += 256) dst[v] = convert(src[v]);
+  }
+}
+
+static hipError_t launch_prepare(W4Prepare p, hipStream_t st) {
+  int64_t all = 0;
+  for (const W4Columns& m : p.m) all += (int64_t)p.n * m.N;
+  p.columns = all;
+  const int rows = (int)std::min<int64_t>(p.rows, 8 * (int64_t)device_cus());
+  const int cols = (int)std::min<int64_t>((all + 255) / 256, 4 * (int64_t)device_cus());
+  hipLaunchKernelGGL(w4_prepare, dim3((unsigned)(rows + cols)), dim3(256), 0, st, p, rows);
+  return hipGetLastError();
 }
 
 size_t packed_4bit_bytes(int n, int K, int N) {
@@ -372,8 +473,20 @@ static W4Args w4_args(int n, int K, int N, int group) {
   return p;
 }
 
+static size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
+
+static W4Plan gemm_plan(int M, int N, int K) {
+  return w4_plan(device_cus(), W4Shape{false, false, 1, N, (K + W4_KB - 1) / W4_KB, M, M, M});
+}
+
+size_t gemm_4bit_ws_bytes(int M, int N, int K) {
+  if (M == 0 || !gemm_plan(M, N, K).tiles) return 0;
+  return pad256((size_t)M * K * 2) + pad256((size_t)M * 4) + pad256((size_t)N * 4);
+}
+
 hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const void* packed, const void* scale,
-                            const void* zero, void* c, int out_dtype, hipStream_t st) {
+                            const void* zero, void* c, int out_dtype, void* ws, hipStream_t st) {
+  const W4Plan plan = gemm_plan(M, N, K);
   W4Args p = w4_args(1, K, N, group);
   p.M = M;
   p.a = (const bf16_t*)a;
@@ -381,12 +494,53 @@ hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const
   p.s1 = (const bf16_t*)scale;
   p.z1 = (const uint8_t*)zero;
   p.c = c;
-  return out_dtype == 1 ? launch_4bit<false, false>(p, group, M, M, M, st) : launch_4bit<false, true>(p, group, M, M, M, st);
+  if (plan.tiles) {
+    bf16_t* rows = (bf16_t*)ws;
+    int32_t* kr = (int32_t*)((char*)ws + pad256((size_t)M * K * 2));
+    int32_t* kc = (int32_t*)((char*)kr + pad256((size_t)M * 4));
+    const hipError_t e = launch_prepare(
+        W4Prepare{p.a, rows, kr, M, nullptr, K, 1, {W4Columns{p.s1, kc, p.groups, N}, W4Columns{}, W4Columns{}}, 0}, st);
+    if (e != hipSuccess) return e;
+    p.a = rows;
+    p.kr = kr;
+    p.k1 = kc;
+  }
+  return out_dtype == 1 ? launch_4bit<false, false>(p, plan, group, M, st) : launch_4bit<false, true>(p, plan, group, M, st);
 }
 
+struct W4Expert {
+  W4Plan up, down;
+  size_t x, h, krx, krh, k1, k3, k2, total;   // places in the workspace
+};
+static W4Expert expert_plan(const Prob& p) {
+  W4Expert w;
+  const int64_t mean = p.tk() / p.E, all = p.tk() * p.n / p.E;
+  w.up = w4_plan(device_cus(), W4Shape{true, true, p.n, p.f, (p.d + W4_KB - 1) / W4_KB, mean, all, p.T});
+  w.down = w4_plan(device_cus(), W4Shape{false, true, p.n, p.d, (p.f + W4_KB - 1) / W4_KB, mean, all, p.T});
+  size_t o = 0;
+  auto take = [&](bool wanted, size_t bytes) {
+    const size_t at = o;
+    o += wanted ? pad256(bytes) : 0;
+    return at;
+  };
+  w.x = take(w.up.tiles, (size_t)p.rows_max * p.d * 2);
+  w.krx = take(w.up.tiles, (size_t)p.rows_max * 4);
+  w.k1 = take(w.up.tiles, (size_t)p.n * p.f * 4);
+  w.k3 = take(w.up.tiles, (size_t)p.n * p.f * 4);
+  w.h = take(w.down.tiles, (size_t)p.rows_max * p.f * 2);
+  w.krh = take(w.down.tiles, (size_t)p.rows_max * 4);
+  w.k2 = take(w.down.tiles, (size_t)p.n * p.d * 4);
+  w.total = o;
+  return w;
+}
+size_t expert_4bit_ws_bytes(const Prob& p) { return expert_plan(p).total; }
+
 hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int32_t* offsets, const Weights4& w1,
-                              const Weights4& w3, const Weights4& w2, void* h, void* y, hipStream_t st) {
-  const int64_t mean = p.tk() / p.E;
+                              const Weights4& w3, const Weights4& w2, void* h, void* y, void* ws, hipStream_t st) {
+  const W4Expert w = expert_plan(p);
+  char* at = (char*)ws;
+  const int32_t* rows = offsets + p.n;   // rows behind the last segment are not read
+  hipError_t e;
   W4Args a = w4_args(p.n, p.d, p.f, group);
   a.offsets = offsets;
   a.a = (const bf16_t*)x;
@@ -397,8 +551,6 @@ hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int
   a.s3 = (const bf16_t*)w3.scale;
   a.z3 = (const uint8_t*)w3.zero;
   a.c = h;
-  const hipError_t e = launch_4bit<true, false>(a, group, mean, p.T, p.rows_max, st);
-  if (e != hipSuccess) return e;
   W4Args b = w4_args(p.n, p.f, p.d, group);
   b.offsets = offsets;
   b.a = (const bf16_t*)h;
@@ -406,7 +558,25 @@ hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int
   b.s1 = (const bf16_t*)w2.scale;
   b.z1 = (const uint8_t*)w2.zero;
   b.c = y;
-  return launch_4bit<false, false>(b, group, mean, p.T, p.rows_max, st);
+  if (w.up.tiles) {
+    a.kr = (const int32_t*)(at + w.krx);
+    a.k1 = (const int32_t*)(at + w.k1);
+    a.k3 = (const int32_t*)(at + w.k3);
+    W4Prepare q{a.a, (bf16_t*)(at + w.x), (int32_t*)(at + w.krx), p.rows_max, rows, p.d, p.n,
+                {W4Columns{a.s1, (int32_t*)(at + w.k1), a.groups, p.f}, W4Columns{a.s3, (int32_t*)(at + w.k3), a.groups, p.f}, W4Columns{}}, 0};
+    if ((e = launch_prepare(q, st)) != hipSuccess) return e;
+    a.a = q.out;
+  }
+  if ((e = launch_4bit<true, false>(a, w.up, group, p.rows_max, st)) != hipSuccess) return e;
+  if (w.down.tiles) {
+    b.kr = (const int32_t*)(at + w.krh);
+    b.k1 = (const int32_t*)(at + w.k2);
+    W4Prepare q{b.a, (bf16_t*)(at + w.h), (int32_t*)(at + w.krh), p.rows_max, rows, p.f, p.n,
+                {W4Columns{b.s1, (int32_t*)(at + w.k2), b.groups, p.d}, W4Columns{}, W4Columns{}}, 0};
+    if ((e = launch_prepare(q, st)) != hipSuccess) return e;
+    b.a = q.out;
+  }
+  return launch_4bit<false, false>(b, w.down, group, p.rows_max, st);
 }
 
 }  // namespace moe

@@ -3,8 +3,8 @@
 
 namespace moe {
 
-hipError_t launch_4bit_tiles_up(const W4Args& p, int group, int height, int64_t rows_max, hipStream_t st) {
-  return launch_w4_tiles<true, false>(p, group, height, rows_max, st);
+hipError_t launch_4bit_tiles_up(const W4Args& p, int group, int bm, int64_t rows_max, hipStream_t st) {
+  return launch_w4_tiles<true, false>(p, group, bm, rows_max, st);
 }
 
 }  // namespace moe

@@ -143,14 +143,16 @@ size_t packed_4bit_bytes(int n, int K, int N);
 hipError_t launch_pack_4bit(int n, int K, int N, const void* w, void* packed, hipStream_t st);
 hipError_t launch_quantize_4bit(int n, int K, int N, int group, int dtype, const void* w, void* packed, void* scale,
                                 void* zero, hipStream_t st);
+size_t gemm_4bit_ws_bytes(int M, int N, int K);
 hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const void* packed, const void* scale,
-                            const void* zero, void* c, int out_dtype, hipStream_t st);
+                            const void* zero, void* c, int out_dtype, void* ws, hipStream_t st);
 struct Weights4 {
   const void* w;      // packed [n]
   const void* scale;  // bf16 [n][groups][N]
   const void* zero;   // uint8 [n][groups][N] or NULL
 };
+size_t expert_4bit_ws_bytes(const Prob& p);
 hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int32_t* offsets, const Weights4& w1,
-                              const Weights4& w3, const Weights4& w2, void* h, void* y, hipStream_t st);
+                              const Weights4& w3, const Weights4& w2, void* h, void* y, void* ws, hipStream_t st);
 
 }  // namespace moe

@@ -127,12 +127,12 @@ size_t call_ws_bytes(const moe::Prob& p, int32_t call) {
     case MOE_CALL_EXPERT_GEMM_QUANTIZED: return moe::expert_i8_ws_bytes(p);
     case MOE_CALL_ROUTE_SCORED: return moe::route_ws_bytes(p);
     case MOE_CALL_ROUTE_BACKWARD: return moe::route_backward_ws_bytes(p);
+    case MOE_CALL_EXPERT_GEMM_FOURBIT: return moe::expert_4bit_ws_bytes(p);
     default: return 0;
   }
 }
 
-moe_status_t check_ws(const moe::Prob& p, int32_t call, const void* ws, size_t bytes) {
-  const size_t need = call_ws_bytes(p, call);
+moe_status_t check_ws(size_t need, const void* ws, size_t bytes) {
   if (need == 0) return MOE_OK;
   if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL, %zu bytes needed", need);
   if (bytes < need)
@@ -140,6 +140,9 @@ moe_status_t check_ws(const moe::Prob& p, int32_t call, const void* ws, size_t b
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
   return MOE_OK;
+}
+moe_status_t check_ws(const moe::Prob& p, int32_t call, const void* ws, size_t bytes) {
+  return check_ws(call_ws_bytes(p, call), ws, bytes);
 }
 
 // Capacity of the padded layout: 1 <= capacity <= T (no expert receives more
@@ -241,6 +244,13 @@ moe_status_t check_packed_4bit(int32_t n, int32_t K, int32_t N) {
   return MOE_OK;
 }
 
+moe_status_t check_gemm_4bit(int32_t M, int32_t N, int32_t K) {
+  if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M=%d must be >= 0", M);
+  if (M > 1 << 30)   // row blocks are counted in 32 bits
+    return fail(MOE_ERR_UNSUPPORTED, "M=%d must be at most %d", M, 1 << 30);
+  return check_packed_4bit(1, K, N);
+}
+
 moe_status_t check_group(int32_t group) {
   if (group != 32 && group != 64 && group != 128)
     return fail(MOE_ERR_UNSUPPORTED, "group=%d must be 32, 64 or 128", group);
@@ -316,7 +326,7 @@ size_t moe_layer_ws_offset(const moe_problem_t* p, int32_t what) {
 size_t moe_workspace_bytes(const moe_problem_t* p, int32_t call) {
   moe::Prob q;
   if (check_problem(p, &q) != MOE_OK) return 0;
-  if (call < MOE_CALL_ROUTE || call > MOE_CALL_ROUTE_BACKWARD) {
+  if (call < MOE_CALL_ROUTE || call > MOE_CALL_EXPERT_GEMM_FOURBIT) {
     fail(MOE_ERR_INVALID_ARG, "unknown call %d", call);
     return 0;
   }
@@ -804,15 +814,19 @@ moe_status_t moe_quantize_weights_fourbit(int32_t n, int32_t K, int32_t N, int32
                     "moe_quantize_weights_fourbit");
 }
 
+size_t moe_gemm_fourbit_workspace_bytes(int32_t M, int32_t N, int32_t K) {
+  if (check_gemm_4bit(M, N, K) != MOE_OK) return 0;
+  ok();
+  return moe::gemm_4bit_ws_bytes(M, N, K);
+}
+
 moe_status_t moe_gemm_fourbit(int32_t M, int32_t N, int32_t K, int32_t group, const void* A,
                            const void* packed, const void* scale, const uint8_t* zero, void* C,
-                           int32_t out_dtype, void* stream) {
+                           int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
   moe_status_t st;
-  if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M=%d must be >= 0", M);
-  if ((st = check_packed_4bit(1, K, N)) != MOE_OK) return st;
+  if ((st = check_gemm_4bit(M, N, K)) != MOE_OK) return st;
   if ((st = check_group(group)) != MOE_OK) return st;
-  if (M > 1 << 30)   // row blocks are counted in 32 bits
-    return fail(MOE_ERR_UNSUPPORTED, "M=%d must be at most %d", M, 1 << 30);
   if ((st = check_dtype(out_dtype)) != MOE_OK) return st;
   NEED_PTR(packed);
   NEED_ALIGNED(packed);
@@ -822,8 +836,10 @@ moe_status_t moe_gemm_fourbit(int32_t M, int32_t N, int32_t K, int32_t group, co
   NEED_PTR(C);
   NEED_ALIGNED(A);
   NEED_ALIGNED(C);
+  if ((st = check_ws(moe::gemm_4bit_ws_bytes(M, N, K), workspace, workspace_bytes)) != MOE_OK) return st;
   (void)hipGetLastError();
-  return hip_status(moe::launch_gemm_4bit(M, N, K, group, A, packed, scale, zero, C, out_dtype, (hipStream_t)stream),
+  return hip_status(moe::launch_gemm_4bit(M, N, K, group, A, packed, scale, zero, C, out_dtype, workspace,
+                                          (hipStream_t)stream),
                     "moe_gemm_fourbit");
 }
 
@@ -831,7 +847,8 @@ moe_status_t moe_expert_gemm_fourbit(const moe_problem_t* p, int32_t group, cons
                                   const int32_t* offsets, const void* w1, const void* s1,
                                   const uint8_t* z1, const void* w3, const void* s3,
                                   const uint8_t* z3, const void* w2, const void* s2,
-                                  const uint8_t* z2, void* h, void* y_packed, void* stream) {
+                                     const uint8_t* z2, void* h, void* y_packed, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
   moe::Prob q;
   moe_status_t st = check_problem(p, &q);
   if (st != MOE_OK) return st;
@@ -857,10 +874,11 @@ moe_status_t moe_expert_gemm_fourbit(const moe_problem_t* p, int32_t group, cons
   NEED_ALIGNED(x_packed);
   NEED_ALIGNED(h);
   NEED_ALIGNED(y_packed);
+  if ((st = check_ws(q, MOE_CALL_EXPERT_GEMM_FOURBIT, workspace, workspace_bytes)) != MOE_OK) return st;
   (void)hipGetLastError();
   return hip_status(moe::launch_expert_4bit(q, group, x_packed, offsets, moe::Weights4{w1, s1, z1},
                                             moe::Weights4{w3, s3, z3}, moe::Weights4{w2, s2, z2}, h, y_packed,
-                                            (hipStream_t)stream),
+                                            workspace, (hipStream_t)stream),
                     "moe_expert_gemm_fourbit");
 }
 

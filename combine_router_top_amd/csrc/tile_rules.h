@@ -192,4 +192,49 @@ inline I8Plan i8_plan(int64_t cus, const I8Shape& p) {
   return r;
 }
 
+// ---------------------------------------------------------------------------
+// 4-bit products
+// ---------------------------------------------------------------------------
+// A product of rows with packed 4-bit weights [n][K][N] (gated: two of them side by
+// side), kb blocks of 128 K; rows as in I8Shape.
+struct W4Shape {
+  bool gated, segments;
+  int n, N, kb;
+  int64_t mean, all, most;
+};
+struct W4Plan {
+  bool tiles;    // w4_tile, else w4_stream
+  int bm;        // tiles: rows of a block, a multiple of 64 up to 192
+  bool wide;     // stream: four column tiles of 16 a workgroup, else one (gated: of each matrix)
+  bool low;      // stream: 16 rows at a time, else 32
+  int blocks;    // stream: workgroups that a segment's blocks of rows are dealt out to
+};
+
+inline W4Plan w4_plan(int64_t cus, const W4Shape& p) {
+  W4Plan r{};
+  const int64_t act = std::min<int64_t>(p.n, std::max<int64_t>(1, p.all));   // experts with rows
+  const int64_t seg = std::max<int64_t>(1, p.segments && p.n > 1 ? p.mean + p.mean / 4 : p.mean);
+  const double mb = act * (p.kb * 1024e-6) * ((p.N + 15) / 16) * (p.gated ? 2 : 1);
+  const int64_t cols = (p.N + (p.gated ? 127 : 255)) / (p.gated ? 128 : 256);
+  auto rounds = [&](int64_t wgs) { return (double)((wgs + cus - 1) / cus); };
+  // tiles: a block of 128 K takes 0.6 us and 0.33 for each 64 rows, a tile about 6 us more,
+  // the preparation of the rows 6
+  double tiles = 0;
+  for (int h = 3; h >= 1; --h) {
+    const int64_t full = seg / (64 * h), rest = (seg % (64 * h) + 63) / 64;
+    const double us = std::max(mb / 5.2, rounds(act * (full + (rest ? 1 : 0)) * cols) * (p.kb * (0.6 + 0.33 * h) + 6)) + 6;
+    if (!r.bm || us < tiles) {
+      r.bm = 64 * h;
+      tiles = us;
+    }
+  }
+  r.wide = (int64_t)((p.N + (p.gated ? 31 : 63)) / (p.gated ? 32 : 64)) * p.n >= cus;
+  r.low = p.most <= 16 || p.mean <= 8;
+  const int64_t rows = r.low ? 16 : 32, passes = (seg + rows - 1) / rows;
+  r.blocks = (int)std::min<int64_t>((p.most + rows - 1) / rows, p.segments ? 4 : 1024);
+  const double stream = 4 + passes * std::max(mb / (r.low ? 5.2 : 3.2), 0.02 * p.kb);
+  r.tiles = stream > tiles;
+  return r;
+}
+
 }  // namespace moe

@@ -25,7 +25,9 @@ struct W4Args {
   const int32_t* offsets;
   int n, M;
   int K, N, kb, ntiles, groups;
-  int lo, hi;              // this launch takes segments with lo < rows <= hi (tiles: no upper bound)
+  const int32_t* kr;       // tiles: exponents of the rows and of the columns [n][N]
+  const int32_t* k1;
+  const int32_t* k3;
 };
 
 __device__ __forceinline__ int w4_rows(const W4Args& p, int e, int& o) {
@@ -37,7 +39,7 @@ __device__ __forceinline__ int w4_rows(const W4Args& p, int e, int& o) {
   }
   o = __builtin_amdgcn_readfirstlane(o);
   cnt = __builtin_amdgcn_readfirstlane(cnt);
-  return cnt > p.lo && cnt <= p.hi ? cnt : 0;
+  return cnt;
 }
 
 // The eight numbers 16 + q of a packed word.  mask and bits are w4_mask() and w4_bits():
@@ -60,9 +62,9 @@ __device__ __forceinline__ uint32_t w4_bits() {
   return v;
 }
 
-// expert_4bit_up.hip, expert_4bit_down.hip: the products on tiles of `height` (1 or 2)
-// times 64 rows, for the segments of more than p.lo rows.
-hipError_t launch_4bit_tiles_up(const W4Args& p, int group, int height, int64_t rows_max, hipStream_t st);
-hipError_t launch_4bit_tiles_down(const W4Args& p, int group, int height, int64_t rows_max, bool f32out, hipStream_t st);
+// expert_4bit_up.hip, expert_4bit_down.hip: the products on tiles, blocks of bm rows (64 to
+// 256).  a: fp16 rows.
+hipError_t launch_4bit_tiles_up(const W4Args& p, int group, int bm, int64_t rows_max, hipStream_t st);
+hipError_t launch_4bit_tiles_down(const W4Args& p, int group, int bm, int64_t rows_max, bool f32out, hipStream_t st);
 
 }  // namespace moe

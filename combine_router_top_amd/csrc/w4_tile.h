@@ -1,49 +1,56 @@
-// Tiles of the 4-bit products (gfx950): 64 WM rows x 256 columns (gated: 128 of each
-// matrix), 8 waves in a WM x (8 / WM) grid, each 64 rows by 16 NT columns, in stages of
-// 128 K.
+// Tiles of the 4-bit products (gfx950): up to 256 rows x 256 columns (gated: 128 of each
+// matrix), 8 waves in a 2 x 4 grid.
 //
-// The rows of a stage (two halves of 64 K in the ST_ROWS layout of seg_tile.h), its
-// packed blocks and its scales are copied from memory straight into a ring of LDS slots.
-// A wave holds its rows' fragments of a whole stage in registers and goes through its
-// column tiles one by one: a tile's packed words become MFMA operands in registers (8
-// values in 7 instructions, shared by the wave's four row tiles), a group's sums are
-// scaled and added to the accumulators in fp32.  The group sums of the rows, which the
-// offset of the operands needs, are a product with ones.
+// On this part a wave's vector instructions do not run beside its matrix instructions,
+// nor beside those of the other wave of its SIMD: a 16 x 16 x 32 product takes 7.1 ns of a
+// SIMD and a vector instruction about 1.0, one after the other.  So what counts is how few
+// of the latter there are for each product.  The tiles therefore work in fp16, where a
+// weight is made complete before it is multiplied, and no sum is scaled later:
+//   - rows come with a power of two that puts their largest value in 2^14 .. 2^15, so
+//     that every bf16 value within 2^-29 of it is exact in fp16 (smaller ones are off by
+//     at most 2^-40 of it); scales likewise, by columns, with their largest in
+//     2^10 .. 2^11.  The epilogue takes both powers out again.
+//   - without zero points, q becomes the fp16 number 16 + q by one masked or (two values),
+//     and one packed fma with s and -24 s gives (q - 8) s: exactly, since 8-bit scales times
+//     -8 .. 7 and times 24 fit fp16's 11 bits.  With zero points, 128 + q, an exact
+//     subtraction and a product, which rounds odd multiples above 8 to 11 bits (by
+//     2^-12 relative, once per weight; a bf16 output is rounded sixteen times as coarsely).
+// An operand of 8 weights costs 12 (15) instructions and serves up to 8 row tiles.
+//
+// Wave (wm, wn) = (w & 1, w >> 1) has the row tiles 2 m + wm, m < L, so that a short tile's
+// rows are shared evenly, and four column tiles.  L (2, 4, 6, 8) is chosen for each tile by
+// its actual rows.  K runs in steps of 64: rows in a ring of three slots, packed blocks of
+// 128 K with their scales in a ring of two, all copied from memory straight into LDS.
+// While a k-step of 32 is multiplied, the operands of the next are made, and a row
+// fragment's registers take its successor as soon as they are free.  One barrier per step,
+// in its middle: by then every wave holds the step's second half.
 #pragma once
 
 #include "w4.h"
 
 namespace moe {
 
-template <int WM_, int GPB_, bool ZERO_, bool GATED_, bool F32OUT_>
-struct W4Cfg {
-  static constexpr int WM = WM_, WN = 8 / WM, GPB = GPB_, MT = 4, BM = 64 * WM;
-  static constexpr bool ZERO = ZERO_, GATED = GATED_, F32OUT = F32OUT_;
-  static constexpr int NT = 16 / WN, NH = GATED ? NT / 2 : NT;   // a wave's weight and output tiles
-  static constexpr int COLS = GATED ? 128 : 256;                 // output columns of a tile
-  static constexpr int XH = BM * 128;                            // bytes of half a stage's rows
-  static constexpr int WOFF = 2 * XH, SOFF = WOFF + 16 * 1024;   // packed blocks, then scales, zero points
-  // a group's scales (512 bytes) and zero points (256, gated: 256 of each matrix, half of them used)
-  static constexpr int ZROW = GATED ? 512 : 256, ZOFF = SOFF + GPB * 512;
-  static constexpr int SLOT = ZOFF + (ZERO ? GPB * ZROW : 0);
-  static constexpr int NS = WM == 1 ? 4 : 3;                     // slots
-  // copies of a wave per stage: rows, packed blocks, and pieces of 256 bytes of scales and
-  // zero points dealt out over the waves (some twice, so that every wave issues as many)
-  static constexpr int SP = 2 * GPB, PIECES = SP + (ZERO ? (GATED ? 2 : 1) * GPB : 0);
-  static constexpr int CS = (PIECES + 7) / 8, COPIES = 2 * WM + 2 + CS;
-  static constexpr int STORES = MT * (F32OUT ? NH : (NH + 1) / 2);
-  typedef StOp<ST_ROWS, BM> X;
-};
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-template <class C>
-struct W4Ctx {
-  typename C::X x;
-  const char* w[2];        // packed runs of this wave's two blocks
-  const char* s[C::CS];    // this wave's pieces of scales or zero points of the first stage
-  uint32_t ssize[C::CS];   // bytes from there to the end of the matrix's, 0 for zero points that it has not
-  uint32_t sstep[C::CS];   // bytes between stages
-  uint32_t sdst[C::CS];    // where in a slot
-  int nst;
+template <int GPB_, bool ZERO_, bool GATED_, bool F32OUT_>
+struct W4Cfg {
+  static constexpr int GPB = GPB_;
+  static constexpr bool ZERO = ZERO_, GATED = GATED_, F32OUT = F32OUT_;
+  static constexpr int NT = 4, NH = GATED ? 2 : 4;      // a wave's weight and output tiles
+  static constexpr int COLS = GATED ? 128 : 256;        // output columns of a tile
+  static constexpr int XSLOT = 256 * 128;               // 64 K of 256 rows
+  static constexpr int WOFF = 3 * XSLOT;                // the packed blocks' ring
+  // a slot of it: 16 blocks, a group's scales (512 bytes), its zero points (256, gated: 256 of
+  // each matrix, half of them used)
+  static constexpr int SOFF = 16 * 1024, ZROW = GATED ? 512 : 256, ZOFF = SOFF + GPB * 512;
+  static constexpr int WSLOT = ZOFF + (ZERO ? GPB * ZROW : 0);
+  static constexpr int LDS = WOFF + 2 * WSLOT;
+  // copies of a wave: packed blocks, and pieces of 256 bytes of scales and zero points dealt
+  // out over the waves (some twice, so that every wave issues as many)
+  static constexpr int SP = 2 * GPB, PIECES = SP + (ZERO ? (GATED ? 2 : 1) * GPB : 0);
+  static constexpr int CS = (PIECES + 7) / 8, W = 2 + CS;
+  static_assert(LDS <= 160 * 1024, "LDS");
 };
 
 // As bd_copy16, 4 bytes per lane.
@@ -57,7 +64,7 @@ __device__ __forceinline__ void bd_copy4(__amdgpu_buffer_rsrc_t r, uint32_t lds,
       : "memory");
 }
 
-// A 256-byte piece of a stage's scales or zero points: group u, matrix or half of the columns hm.
+// A 256-byte piece of a block's scales or zero points: group u, matrix or half of the columns hm.
 struct W4Piece {
   int u, hm, dst;
   bool zero;
@@ -74,316 +81,285 @@ __device__ __forceinline__ W4Piece w4_piece(int at) {
   return q;
 }
 
-// The copies of stage st into the slot at LDS address `slot`.
+// What a wave copies of the weights of a tile.
 template <class C>
-__device__ __forceinline__ void w4_issue(const W4Args& p, const W4Ctx<C>& c, uint32_t slot, int st) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  st_issue(c.x, slot, 2 * st);
-  st_issue(c.x, slot + C::XH, 2 * st + 1);
-  const uint32_t run = (uint32_t)p.kb * 1024u;
-#pragma unroll
-  for (int v = 0; v < 2; ++v)
-    bd_copy16(gc_rsrc(c.w[v], run), slot + C::WOFF + 1024 * (wave + 8 * v), 16u * (uint32_t)lane, (uint32_t)st * 1024u);
-#pragma unroll
-  for (int v = 0; v < C::CS; ++v) {
-    bd_copy4(gc_rsrc(c.s[v], c.ssize[v]), slot + c.sdst[v], 4u * (uint32_t)lane, (uint32_t)st * c.sstep[v]);
-  }
-}
-
-// What a wave holds while it goes through its column tiles.  The group whose products
-// are complete is scaled and added ("flushed") between the products of the next one, so
-// that neither the matrix cores nor the vector unit waits for the other.
-template <class C>
-struct W4Wave {
-  static constexpr int MT = C::MT, NT = C::NT, NH = C::NH, GPB = C::GPB, SPG = 4 / GPB;
-  // Without zero points and with one group a stage, products start at -24 X instead of 0.
-  static constexpr bool INIT = !C::ZERO && GPB == 1;
-  int xo, wn;
-  uint32_t mask, bits;     // of w4_unpack
-  u32x4 x[MT][4];          // rows of the stage
-  typename std::conditional<INIT, f32x4, float>::type X[MT][GPB];   // their group sums (INIT: times -24)
-  f32x4 part[2][MT];       // products of a group, and of the one before
-  u32x4 w, f;              // packed words of the tile, operand of the next k-step
-  // the group to flush: scales, zero points, sums
-  u32x2 sc;
-  uint32_t zp;
-  float z0, Xp[MT];
-
-  __device__ __forceinline__ void clear() {
-    sc = u32x2{0u, 0u};
-    zp = 0;
-    z0 = 0.f;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      Xp[mt] = 0.f;
-      part[1][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-  }
-  __device__ __forceinline__ void read_x(const char* slot, int q) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) x[mt][q] = st_frag<ST_ROWS>(slot + (q >> 1) * C::XH, xo, q & 1, mt);
-  }
-  static constexpr int tile_of(int t, int& m) {
-    m = C::GATED ? t / NH : 0;
-    return C::GATED ? t % NH : t;
-  }
-  __device__ __forceinline__ u32x4 read_w(const char* slot, int t) const {
-    int m = 0;
-    const int at = NH * wn + tile_of(t, m);
-    return *reinterpret_cast<const u32x4*>(slot + C::WOFF + 1024 * (at + 8 * m) + 16 * (threadIdx.x & 63));
-  }
-  __device__ __forceinline__ f32x4 start(int mt, int u) const {
-    if constexpr (INIT) return X[mt][u];
-    else return f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  // Elements [k0, k1) of MT of the pending group's row tiles, products in part[b].
-  __device__ __forceinline__ void flush(float (&acc)[MT][NT][4], int b, int t, int k0, int k1) {
-    const float s[4] = {bf16_lo(sc[0]), bf16_hi(sc[0]), bf16_lo(sc[1]), bf16_hi(sc[1])};
-#pragma unroll
-    for (int mt = k0; mt < k1; ++mt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float z = C::ZERO ? z0 - (float)((zp >> (8 * r)) & 255u) : -24.f;
-        const float v = INIT ? part[b][mt][r] : fmaf(z, Xp[mt], part[b][mt][r]);
-        acc[mt][t][r] = fmaf(s[r], v, acc[mt][t][r]);
-      }
-  }
-  // The group sums, and the last flush of the stage before.
-  __device__ __forceinline__ void sums(float (&acc)[MT][NT][4]) {
-    const uint32_t one = INIT ? 0xC1C0C1C0u : 0x3F803F80u;
-    const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{one, one, one, one});
-#pragma unroll
-    for (int u = 0; u < GPB; ++u) {
-      f32x4 v[MT];
-#pragma unroll
-      for (int q = u * SPG; q < (u + 1) * SPG; ++q)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          v[mt] = mfma16(ones, __builtin_bit_cast(bf16x8, x[mt][q]), q == u * SPG ? f32x4{0.f, 0.f, 0.f, 0.f} : v[mt]);
-      flush(acc, 1, NT - 1, u * MT / GPB, (u + 1) * MT / GPB);
-#pragma unroll
-      for (int k = 0; k < MT * SPG; ++k) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        if constexpr (INIT) X[mt][u] = v[mt];
-        else X[mt][u] = v[mt][0];
-    }
-  }
-  // Tile t of the stage; NEXT: the following stage's rows are read once they are no longer needed.
-  template <bool NEXT>
-  __device__ __forceinline__ void tile(const W4Args& p, const char* slot, const char* next, int t, float (&acc)[MT][NT][4]) {
-    int m = 0;
-    const int at = NH * wn + tile_of(t, m);
-    const int col = C::COLS * m + 16 * at + 4 * ((threadIdx.x & 63) >> 4);
-    u32x4 wn4 = w;
-    if (t + 1 < NT) wn4 = read_w(slot, t + 1);
-#pragma unroll
-    for (int u = 0; u < GPB; ++u) {
-      constexpr int total = NT * GPB;
-      const int b = (t * GPB + u) & 1;
-      static_assert(total % 2 == 0, "the parts alternate across stages");
-      const u32x2 nsc = *reinterpret_cast<const u32x2*>(slot + C::SOFF + u * 512 + 2 * col);
-      const uint32_t nzp =
-          C::ZERO ? *reinterpret_cast<const uint32_t*>(slot + C::ZOFF + u * C::ZROW + col + (C::GATED ? 128 * m : 0)) : 0u;
-      const int before = u ? t : t - 1;   // the tile to flush (t = 0, u = 0: done by sums)
-#pragma unroll
-      for (int j = 0; j < SPG; ++j) {
-        const int q = u * SPG + j;
-        const u32x4 now = f;
-        if (q < 3) f = w4_unpack(w[q + 1], mask, bits);
-        else if (t + 1 < NT) f = w4_unpack(wn4[0], mask, bits);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          part[b][mt] = st_mfma(now, x[mt][q], j ? part[b][mt] : start(mt, u));
-        if (before >= 0) flush(acc, b ^ 1, before, j * MT / SPG, (j + 1) * MT / SPG);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, C::ZERO ? 5 : 3, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (NEXT) read_x(next, q);   // into the registers just used
-      }
-      sc = nsc;
-      zp = nzp;
-      // a matrix without zero points reads zeros
-      z0 = !C::ZERO ? -24.f : !C::GATED || (m ? p.z3 : p.z1) ? -16.f : -24.f;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        if constexpr (!INIT) Xp[mt] = X[mt][u];
-    }
-    w = wn4;
-  }
-  __device__ __forceinline__ void first_tiles(const W4Args& p, const char* slot, float (&acc)[MT][NT][4]) {
-    w = read_w(slot, 0);
-    sums(acc);
-    f = w4_unpack(w[0], mask, bits);
-#pragma unroll
-    for (int t = 0; t + 1 < NT; ++t) tile<false>(p, slot, slot, t, acc);
-  }
-  __device__ __forceinline__ void last_tile(const W4Args& p, const char* slot, const char* next, float (&acc)[MT][NT][4]) {
-    tile<true>(p, slot, next, NT - 1, acc);
-  }
-  __device__ __forceinline__ void flush_pending(float (&acc)[MT][NT][4]) { flush(acc, 1, NT - 1, 0, MT); }
+struct W4Ctx {
+  const char* w[2];        // packed runs of its two tiles
+  const char* s[C::CS];    // its pieces of scales or zero points of the first block
+  uint32_t ssize[C::CS];   // bytes from there to the end of the matrix's, 0 for zero points that it has not
+  uint32_t sstep[C::CS];   // bytes between blocks
+  uint32_t sdst[C::CS];    // where in a slot
+  uint32_t run;
 };
 
+__device__ __forceinline__ const char* w4_scalar(const char* p) {   // descriptors are made of it
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const char*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at) |
+                                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32);
+}
+
 template <class C>
-__global__ __launch_bounds__(ST_NT, 1) void w4_tile(W4Args p, int ntn) {
-  __shared__ __attribute__((aligned(16))) char ring[C::NS * C::SLOT];
-  constexpr int MT = C::MT, NT = C::NT, NH = C::NH, GPB = C::GPB;
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void w4_setup(const W4Args& p, const StTile& t, W4Ctx<C>& c) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave % C::WM, wn = wave / C::WM;
-  const int total = (p.offsets ? st_row_blocks(p.offsets, p.n, C::BM, p.lo) : (p.M + C::BM - 1) / C::BM) * ntn;
-  int L = st_first_tile();
-  if (L >= total) return;
-  const uint32_t lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
-  const uint32_t run = (uint32_t)p.kb * 1024u;
-  const int xo = st_lane<ST_ROWS>(MT * wm);
-  W4Ctx<C> c;
-  c.nst = p.kb;
-  auto setup = [&](int at) {
-    const StTile t = p.offsets ? st_tile_at(at, p.offsets, p.n, ntn, C::BM, p.lo)
-                               : st_tile_of(at, 0, p.M, (p.M + C::BM - 1) / C::BM, ntn, C::BM);
-    st_rows(c.x, p.a + (int64_t)t.r0 * p.K, (uint32_t)p.K * 2, t.R, (uint32_t)p.K * 2);
-    const int64_t eo = (int64_t)t.e * p.ntiles;
+  c.run = (uint32_t)p.kb * 1024u;
+  const int64_t eo = (int64_t)t.e * p.ntiles;
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {   // packed blocks wave and wave + 8 (gated: the second matrix)
-      const int tile = C::COLS / 16 * t.nt + (C::GATED ? wave : wave + 8 * v);
-      c.w[v] = (C::GATED && v ? p.b3 : p.b1) + (eo + min(tile, p.ntiles - 1)) * run;
-    }
-    const int64_t go = (int64_t)t.e * p.groups * p.N + C::COLS * t.nt;
+  for (int v = 0; v < 2; ++v) {   // packed tiles wave and wave + 8 (gated: the second matrix)
+    const int tile = C::COLS / 16 * t.nt + (C::GATED ? wave : wave + 8 * v);
+    c.w[v] = w4_scalar((C::GATED && v ? p.b3 : p.b1) + (eo + min(tile, p.ntiles - 1)) * c.run);
+  }
+  const int64_t go = (int64_t)t.e * p.groups * p.N + C::COLS * t.nt;
 #pragma unroll
-    for (int v = 0; v < C::CS; ++v) {
-      const W4Piece q = w4_piece<C>(wave + 8 * v);
-      const bool m = C::GATED && q.hm;
-      const uint8_t* zp = m ? p.z3 : p.z1;
-      const uint32_t row = (uint32_t)p.N * (q.zero ? 1u : 2u);   // bytes of a group
-      const uint32_t skip = row * (uint32_t)q.u + (C::GATED || q.zero ? 0u : 256u * (uint32_t)q.hm);
-      const uint32_t size = q.zero && !zp ? 0u : (uint32_t)p.groups * row;
-      const char* from = (q.zero ? (const char*)(zp + go) : (const char*)((m ? p.s3 : p.s1) + go)) + skip;
-      const uint64_t at = reinterpret_cast<uint64_t>(from);   // scalar: descriptors are made of it
-      c.s[v] = reinterpret_cast<const char*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at) |
-                                             (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32);
-      c.ssize[v] = __builtin_amdgcn_readfirstlane(size > skip ? size - skip : 0u);
-      c.sstep[v] = __builtin_amdgcn_readfirstlane(row * (uint32_t)GPB);
-      c.sdst[v] = __builtin_amdgcn_readfirstlane(q.dst);
-    }
-    return t;
-  };
-  auto prologue = [&]() {
-    // what setup loaded is here: else the compiler waits for it inside the loop over the
-    // stages, and there for every copy as well
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-#pragma unroll
-    for (int s = 0; s < C::NS - 1; ++s) w4_issue(p, c, lbase + s * C::SLOT, s);
-  };
-  StTile tile = setup(L);
-  prologue();
-  bool stores = false;
-  for (;;) {
-    float acc[MT][NT][4];   // single values: as vectors they are moved about at every branch
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[mt][t][r] = 0.f;
-    // the first stage; newer are the other stages of the prologue and the stores of the tile before
-    if (stores) st_sync<(C::NS - 2) * C::COPIES + C::STORES>();
-    else st_sync<(C::NS - 2) * C::COPIES>();
-    W4Wave<C> v;
-    v.xo = xo;
-    v.wn = wn;
-    v.mask = w4_mask();
-    v.bits = w4_bits();
-    v.clear();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v.read_x(ring, q);
-    uint32_t so = 0;   // slot offset of stage s
-    for (int s = 0; s < c.nst; ++s) {
-      v.first_tiles(p, ring + so, acc);
-      // the next stage has arrived in every wave, and all are done with the one before;
-      // stages past the last read zeros, so that the loop has no branches
-      st_sync<(C::NS - 3) * C::COPIES>();
-      w4_issue(p, c, lbase + (so == 0 ? (C::NS - 1) * C::SLOT : so - C::SLOT), s + C::NS - 1);
-      const uint32_t to = so == (C::NS - 1) * C::SLOT ? 0 : so + C::SLOT;
-      v.last_tile(p, ring + so, ring + to, acc);
-      so = to;
-    }
-    v.flush_pending(acc);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave is done with the ring
-    const int next = L + (int)gridDim.x;
-    const StTile done = tile;
-    if (next < total) {
-      tile = setup(next);
-      prologue();
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    constexpr int ES = C::F32OUT ? 4 : 2;
-    const StOut out = st_out((char*)p.c + (int64_t)done.r0 * p.N * ES, (int64_t)p.N * ES, done.R);
-    const int col0 = C::COLS * done.nt + 16 * NH * wn;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int row = 64 * wm + 16 * mt + i;
-      f32x4 v[NH];
-#pragma unroll
-      for (int t = 0; t < NH; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[t][r] = C::GATED ? silu_mul(acc[mt][t][r], acc[mt][t + NT - NH][r]) : acc[mt][t][r];
-      if constexpr (C::F32OUT) {
-#pragma unroll
-        for (int t = 0; t < NH; ++t) {
-          const int at = col0 + 16 * t + 4 * g;
-          st_put(out, row, 4u * (uint32_t)at, at < p.N, __builtin_bit_cast(u32x4, v[t]));
-        }
-      } else if constexpr (NH == 1) {   // 4 columns a lane
-        const int at = col0 + 4 * g;
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{cvt_bf16x2(v[0][0], v[0][1]), cvt_bf16x2(v[0][2], v[0][3])}, out.r,
-                                              at < p.N ? (uint32_t)row * out.ld + 2u * (uint32_t)at : 0xFFFFFFF0u, 0, 0);
-      } else {
-#pragma unroll
-        for (int t = 0; t < NH; t += 2) {
-          const int at = col0 + 16 * t + 8 * g;
-          st_put(out, row, 2u * (uint32_t)at, at < p.N, st_pack8(v[t], v[t + 1]));
-        }
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-    if (next >= total) return;
-    L = next;
-    stores = true;
+  for (int v = 0; v < C::CS; ++v) {
+    const W4Piece q = w4_piece<C>(wave + 8 * v);
+    const bool m = C::GATED && q.hm;
+    const uint8_t* zp = m ? p.z3 : p.z1;
+    const uint32_t row = (uint32_t)p.N * (q.zero ? 1u : 2u);   // bytes of a group
+    const uint32_t skip = row * (uint32_t)q.u + (C::GATED || q.zero ? 0u : 256u * (uint32_t)q.hm);
+    const uint32_t size = q.zero && !zp ? 0u : (uint32_t)p.groups * row - (uint32_t)(C::COLS * t.nt) * (q.zero ? 1u : 2u);
+    c.s[v] = w4_scalar((q.zero ? (const char*)(zp + go) : (const char*)((m ? p.s3 : p.s1) + go)) + skip);
+    c.ssize[v] = __builtin_amdgcn_readfirstlane(size > skip ? size - skip : 0u);
+    c.sstep[v] = __builtin_amdgcn_readfirstlane(row * (uint32_t)C::GPB);
+    c.sdst[v] = __builtin_amdgcn_readfirstlane(q.dst);
   }
 }
 
-template <bool GATED, bool F32OUT, int WM, int GPB, bool ZERO>
-static hipError_t launch_w4_tile(const W4Args& p, int64_t rows_max, hipStream_t st) {
-  using C = W4Cfg<WM, GPB, ZERO, GATED, F32OUT>;
+// The copies of block b into the slot at LDS address `slot`; blocks past the last read zeros.
+template <class C>
+__device__ __forceinline__ void w4_issue(const W4Ctx<C>& c, uint32_t slot, int b) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+    bd_copy16(gc_rsrc(c.w[v], c.run), slot + 1024 * (wave + 8 * v), 16u * (uint32_t)lane, (uint32_t)b * 1024u);
+#pragma unroll
+  for (int v = 0; v < C::CS; ++v)
+    bd_copy4(gc_rsrc(c.s[v], c.ssize[v]), slot + c.sdst[v], 4u * (uint32_t)lane, (uint32_t)b * c.sstep[v]);
+}
+
+__device__ __forceinline__ uint32_t w4_vreg(uint32_t v) {   // a constant that is no literal (w4_unpack)
+  asm("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t w4_sreg(uint32_t v) {
+  asm("" : "+s"(v));
+  return v;
+}
+
+// A tile's product for L row tiles a wave.  x: copies of the rows (fp16).
+template <class C, int L>
+struct W4Wave {
+  static constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, SPG = 4 / GPB, X = L / 2;
+  f32x4 acc[L][NT];
+  u32x4 x[L];              // rows of a k-step
+  u32x4 w[NT];             // packed words of a block
+  u32x4 f[2][NT];          // operands of a k-step and of the next
+  uint32_t S[NT], Z[NT];   // scale and addend of the group that operands are made of, twice each
+  int k[NT];               // exponents of this lane's columns
+  uint32_t mask, bits, zmul, zbase[2];
+  int xo, at0;             // lane offsets in a slot: rows, and the wave's first column tile
+
+  static __device__ __forceinline__ int matrix(int t) { return C::GATED ? t / NH : 0; }
+  __device__ __forceinline__ int tile(int t) const { return at0 + (C::GATED ? t % NH + 8 * (t / NH) : t); }   // of the slot's 16
+
+  __device__ __forceinline__ void read_x(const char* slot, int ks, int m) {
+    x[m] = st_frag<ST_ROWS>(slot, xo, ks, 2 * m);
+  }
+  __device__ __forceinline__ void read_w(const char* slot) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) w[t] = *reinterpret_cast<const u32x4*>(slot + 1024 * tile(t) + 16 * (threadIdx.x & 63));
+  }
+  // Scales and addends of the block's group u.
+  __device__ __forceinline__ void scales(const char* slot, int u) {
+    const int i = threadIdx.x & 15;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int col = 16 * tile(t) + i;   // of the slot's 256
+      const uint32_t raw = *reinterpret_cast<const uint16_t*>(slot + C::SOFF + 512 * u + 2 * col);
+      const float s = __builtin_ldexpf(__uint_as_float(raw << 16), k[t]);
+      S[t] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(s, s));   // exact: 8 bits
+      if constexpr (C::ZERO) {
+        const uint32_t z = *reinterpret_cast<const uint8_t*>(slot + C::ZOFF + C::ZROW * u + col + (C::GATED ? 128 * matrix(t) : 0));
+        Z[t] = z * zmul + zbase[matrix(t)];   // -(128 + z), twice
+      } else {
+        const f16x2 m24 = f16x2{(_Float16)-24, (_Float16)-24};
+        Z[t] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, S[t]) * m24);
+      }
+    }
+  }
+  __device__ __forceinline__ u32x4 operand(uint32_t word, int t) const {
+    const f16x2 s = __builtin_bit_cast(f16x2, S[t]), z = __builtin_bit_cast(f16x2, Z[t]);
+    u32x4 o;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int r = (C::ZERO ? 4 * p : 4 * p + 29) & 31;
+      const f16x2 v = __builtin_bit_cast(f16x2, ((r ? __builtin_amdgcn_alignbit(word, word, r) : word) & mask) | bits);
+      o[p] = __builtin_bit_cast(uint32_t, C::ZERO ? (v + z) * s : __builtin_elementwise_fma(v, s, z));
+    }
+    return o;
+  }
+  // k-step q of a block: products with f[q & 1]; meanwhile the operands of the next from
+  // the words w, and the rows of the next from (next, ks).
+  template <int Q>
+  __device__ __forceinline__ void kstep(const char* next, int ks) {
+    constexpr int b = Q & 1, n = (Q + 1) & 3;
+#pragma unroll
+    for (int m = 0; m < L; ++m) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, f[b][t]), __builtin_bit_cast(f16x8, x[m]),
+                                                           acc[m][t], 0, 0, 0);
+      // the second half of the row tiles makes the operands: scales and words have arrived
+      constexpr int H = L / 2;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (m >= H && t >= (m - H) * NT / (L - H) && t < (m - H + 1) * NT / (L - H)) f[b ^ 1][t] = operand(w[t][n], t);
+      __builtin_amdgcn_sched_barrier(0);
+      read_x(next, ks, m);   // into the registers just used
+    }
+  }
+};
+
+template <class C, int L>
+__device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t, char* ring, W4Ctx<C>& c) {
+  constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, SPG = 4 / GPB, X = L / 2;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const uint32_t lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
+  StOp<ST_ROWS, 32 * L> xr;
+  st_rows(xr, p.a + (int64_t)t.r0 * p.K, (uint32_t)p.K * 2, t.R, (uint32_t)p.K * 2);
+  W4Wave<C, L> v;
+  v.xo = st_lane<ST_ROWS>(wm);
+  v.at0 = NH * wn;
+  v.mask = w4_vreg(C::ZERO ? 0x00780078u : 0x03C003C0u);
+  v.bits = w4_sreg(C::ZERO ? 0x58005800u : 0x4C004C00u);
+  v.zmul = w4_sreg(0x00080008u);
+  v.zbase[0] = w4_vreg(p.z1 ? 0xD800D800u : 0xD840D840u);   // without zero points: 8
+  v.zbase[1] = w4_vreg(p.z3 ? 0xD800D800u : 0xD840D840u);
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int col = C::COLS * t.nt + 16 * (v.at0 + (C::GATED ? q % NH : q)) + i;
+    v.k[q] = col < p.N ? (C::GATED && q >= NH ? p.k3 : p.k1)[(int64_t)t.e * p.N + col] : 0;
+  }
+#pragma unroll
+  for (int m = 0; m < L; ++m)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) v.acc[m][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): or the compiler waits for these loads in the loop
+  auto xslot = [&](int j) { return lbase + (uint32_t)(j * C::XSLOT); };
+  w4_issue(c, lbase + C::WOFF, 0);
+  st_issue(xr, xslot(0), 0);
+  st_issue(xr, xslot(1), 1);
+  w4_issue(c, lbase + C::WOFF + C::WSLOT, 1);
+  st_issue(xr, xslot(2), 2);
+  st_sync<2 * X + C::W>();
+  const char* ws = ring + C::WOFF;   // slot of this block
+#pragma unroll
+  for (int m = 0; m < L; ++m) v.read_x(ring, 0, m);
+  v.read_w(ws);
+  v.scales(ws, 0);
+#pragma unroll
+  for (int q = 0; q < NT; ++q) v.f[0][q] = v.operand(v.w[q][0], q);
+  uint32_t x0 = 0, x1 = C::XSLOT, x2 = 2 * C::XSLOT;   // slots of this step, the next and the one after
+  uint32_t wo = 0;                                     // offset of this block's slot
+  for (int b = 0; b < p.kb; ++b) {
+    ws = ring + C::WOFF + wo;
+    if (GPB == 4) v.scales(ws, 1);
+    v.template kstep<0>(ring + x0, 1);
+    // the next step's rows have arrived, this step's are in registers: their slot is refilled
+    st_sync<C::W + X>();
+    st_issue(xr, lbase + x0, 2 * b + 3);
+    if (SPG <= 2) v.scales(ws, SPG == 2 ? 1 : 2);
+    v.template kstep<1>(ring + x1, 0);
+    if (GPB == 4) v.scales(ws, 3);
+    v.template kstep<2>(ring + x1, 1);
+    st_sync<X>();
+    w4_issue(c, lbase + C::WOFF + wo, b + 2);
+    st_issue(xr, lbase + x1, 2 * b + 4);
+    wo = C::WSLOT - wo;
+    v.read_w(ring + C::WOFF + wo);
+    v.scales(ring + C::WOFF + wo, 0);
+    v.template kstep<3>(ring + x2, 0);
+    const uint32_t keep = x0;
+    x0 = x2;
+    x2 = x1;
+    x1 = keep;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave is done with the ring
+
+  constexpr int ES = C::F32OUT ? 4 : 2;
+  const StOut out = st_out((char*)p.c + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
+  const int col0 = C::COLS * t.nt + 16 * NH * wn;
+  int kc[NT][4];   // exponents of the columns that this lane stores
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int col = min(col0 + 16 * (C::GATED ? q % NH : q) + 4 * g, p.N - 4);
+    const i32x4 e = *reinterpret_cast<const i32x4*>((C::GATED && q >= NH ? p.k3 : p.k1) + (int64_t)t.e * p.N + col);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) kc[q][r] = e[r];
+  }
+#pragma unroll
+  for (int m = 0; m < L; ++m) {
+    const int row = 16 * (2 * m + wm) + i;
+    const int kr = p.kr[t.r0 + min(row, t.R - 1)];
+    f32x4 o[NH];
+#pragma unroll
+    for (int q = 0; q < NH; ++q)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float a = __builtin_ldexpf(v.acc[m][q][r], -(kr + kc[q][r]));
+        if constexpr (C::GATED) o[q][r] = silu_mul(a, __builtin_ldexpf(v.acc[m][q + NT - NH][r], -(kr + kc[q + NT - NH][r])));
+        else o[q][r] = a;
+      }
+    if constexpr (C::F32OUT) {
+#pragma unroll
+      for (int q = 0; q < NH; ++q) {
+        const int at = col0 + 16 * q + 4 * g;
+        st_put(out, row, 4u * (uint32_t)at, at < p.N, __builtin_bit_cast(u32x4, o[q]));
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < NH; q += 2) {
+        const int at = col0 + 16 * q + 8 * g;
+        st_put(out, row, 2u * (uint32_t)at, at < p.N, st_pack8(o[q], o[q + 1]));
+      }
+    }
+  }
+}
+
+template <class C>
+__global__ __launch_bounds__(ST_NT, 1) void w4_tile(W4Args p, int ntn, int bm) {
+  __shared__ __attribute__((aligned(16))) char ring[C::LDS];
+  const int blocks = p.offsets ? st_row_blocks(p.offsets, p.n, bm) : (p.M + bm - 1) / bm;
+  for (int L = st_first_tile(); L < blocks * ntn; L += (int)gridDim.x) {
+    const StTile t = p.offsets ? st_tile_at(L, p.offsets, p.n, ntn, bm) : st_tile_of(L, 0, p.M, blocks, ntn, bm);
+    W4Ctx<C> c;
+    w4_setup<C>(p, t, c);
+    if (t.R <= 64) w4_tile_product<C, 2>(p, t, ring, c);
+    else if (t.R <= 128) w4_tile_product<C, 4>(p, t, ring, c);
+    else w4_tile_product<C, 6>(p, t, ring, c);
+  }
+}
+
+template <bool GATED, bool F32OUT, int GPB, bool ZERO>
+static hipError_t launch_w4_tile(const W4Args& p, int bm, int64_t rows_max, hipStream_t st) {
+  using C = W4Cfg<GPB, ZERO, GATED, F32OUT>;
   const int ntn = (p.N + C::COLS - 1) / C::COLS;
-  hipLaunchKernelGGL(w4_tile<C>, st_row_grid(rows_max, p.n, WM, ntn), dim3(ST_NT), 0, st, p, ntn);
+  hipLaunchKernelGGL(w4_tile<C>, st_row_grid(rows_max, p.n, bm / 64, ntn), dim3(ST_NT), 0, st, p, ntn, bm);
   return hipGetLastError();
 }
 
 template <bool GATED, bool F32OUT>
-static hipError_t launch_w4_tiles(const W4Args& p, int group, int height, int64_t rows_max, hipStream_t st) {
+static hipError_t launch_w4_tiles(const W4Args& p, int group, int bm, int64_t rows_max, hipStream_t st) {
   const bool zero = p.z1 || (GATED && p.z3);
-  auto with = [&](auto gpb, auto z) {
-    return height == 1 ? launch_w4_tile<GATED, F32OUT, 1, gpb(), z()>(p, rows_max, st)
-                       : launch_w4_tile<GATED, F32OUT, 2, gpb(), z()>(p, rows_max, st);
+  auto with = [&](auto gpb) {
+    return zero ? launch_w4_tile<GATED, F32OUT, gpb(), true>(p, bm, rows_max, st)
+                : launch_w4_tile<GATED, F32OUT, gpb(), false>(p, bm, rows_max, st);
   };
-  auto grouped = [&](auto gpb) {
-    return zero ? with(gpb, std::true_type{}) : with(gpb, std::false_type{});
-  };
-  return group == 32   ? grouped(std::integral_constant<int, 4>{})
-         : group == 64 ? grouped(std::integral_constant<int, 2>{})
-                       : grouped(std::integral_constant<int, 1>{});
+  return group == 32   ? with(std::integral_constant<int, 4>{})
+         : group == 64 ? with(std::integral_constant<int, 2>{})
+                       : with(std::integral_constant<int, 1>{});
 }
 
 }  // namespace moe

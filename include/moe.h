@@ -104,7 +104,8 @@ enum {
   MOE_CALL_EXPERT_GEMM_BACKWARD = 7,
   MOE_CALL_EXPERT_GEMM_QUANTIZED = 8,
   MOE_CALL_ROUTE_SCORED = 9,
-  MOE_CALL_ROUTE_BACKWARD = 10
+  MOE_CALL_ROUTE_BACKWARD = 10,
+  MOE_CALL_EXPERT_GEMM_FOURBIT = 11
 };
 
 /*
@@ -514,29 +515,38 @@ moe_status_t moe_quantize_weights_fourbit(int32_t n, int32_t K, int32_t N, int32
 
 /*
  * Product with 4-bit weights: C = rnd(A W), W one matrix [K,N] as above, with fp32
- * accumulation; no weight is rounded.  A row of A with an infinity or a NaN gives a row
+ * accumulation.  No weight is rounded, except that products of many rows take odd multiples
+ * |q - zero| above 8 of a scale rounded to 11 bits (2^-12 relative), and scales 2^-25 below
+ * the largest of their column with fewer.  A row of A with an infinity or a NaN gives a row
  * of NaN, a NaN scale a column of NaN, and neither reaches others.
  *   A [M,K] bf16 row-major, 16-byte aligned;  C [M,N] of out_dtype, 16-byte aligned,
  *   overlaps none of the others.  M = 0 launches nothing; M at most 2^30.
+ *   workspace of moe_gemm_fourbit_workspace_bytes(M, N, K) bytes (0 for few rows, or for
+ *   sizes that moe_gemm_fourbit refuses), 256-byte aligned
  */
+size_t moe_gemm_fourbit_workspace_bytes(int32_t M, int32_t N, int32_t K);
 moe_status_t moe_gemm_fourbit(int32_t M, int32_t N, int32_t K, int32_t group, const void* A,
-                           const void* packed, const void* scale, const uint8_t* zero, void* C,
-                           int32_t out_dtype, void* stream);
+                              const void* packed, const void* scale, const uint8_t* zero, void* C,
+                              int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /*
  * moe_expert_gemm with 4-bit weights.  For each local expert e and its rows R
  *   h[R] = rnd(SiLU(x_packed[R] w1[e]) * (x_packed[R] w3[e])),  y_packed[R] = rnd(h[R] w2[e])
  * with the weights of packed [n_local][d,f] (w1, w3) and [n_local][f,d] (w2), their
- * scales s1, s3, s2 and zero points z1, z3, z2 (each NULL or not).  bf16 only.
+ * scales s1, s3, s2 and zero points z1, z3, z2 (each NULL or not); weights as exact as in
+ * moe_gemm_fourbit.  bf16 only.
  * Rows >= A of x_packed are not read, those of h and y_packed are left untouched.  Outputs
  * must not overlap inputs or one another.  A row with an infinity or a NaN gives NaN rows
  * of h and y_packed, and changes no other row.
+ *   workspace of moe_workspace_bytes(p, MOE_CALL_EXPERT_GEMM_FOURBIT) bytes
  */
 moe_status_t moe_expert_gemm_fourbit(const moe_problem_t* p, int32_t group, const void* x_packed,
-                                  const int32_t* offsets, const void* w1, const void* s1,
-                                  const uint8_t* z1, const void* w3, const void* s3,
-                                  const uint8_t* z3, const void* w2, const void* s2,
-                                  const uint8_t* z2, void* h, void* y_packed, void* stream);
+                                     const int32_t* offsets, const void* w1, const void* s1,
+                                     const uint8_t* z1, const void* w3, const void* s3,
+                                     const uint8_t* z3, const void* w2, const void* s2,
+                                     const uint8_t* z2, void* h, void* y_packed, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /*
  * GEMM with per-tile completion signals: the local compute half of the pages'

@@ -20,7 +20,7 @@ ROUTE = ["x", "w_gate", "bias", "balance", "logits", "topk_idx", "topk_w"]
 BACK = ["x", "w_gate", "logits", "topk_idx", "dtopk_w", "dx_add", "dlogits", "dx", "dw_gate", "dbias"]
 EXPERTS = ["x_packed", "offsets", "w1", "s1", "z1", "w3", "s3", "z3", "w2", "s2", "z2", "h", "y_packed"]
 CALLS = {"moe_select": (SELECT, False), "moe_route_scored": (ROUTE, True), "moe_route_backward": (BACK, True),
-         "moe_expert_gemm_fourbit": (EXPERTS, False)}
+         "moe_expert_gemm_fourbit": (EXPERTS, True)}
 OPTIONAL = {"balance", "bias", "dx_add", "dlogits", "dx", "dw_gate", "dbias", "z1", "z3", "z2"}
 RULE = M.GateRule(M.MOE_SCORE_SIGMOID, 2, 1, 2, 1, 1.0)
 
@@ -77,9 +77,10 @@ def test_no_rule(name):
 
 
 @pytest.mark.parametrize("name,call", [("moe_route_scored", M.MOE_CALL_ROUTE_SCORED),
-                                       ("moe_route_backward", M.MOE_CALL_ROUTE_BACKWARD)])
+                                       ("moe_route_backward", M.MOE_CALL_ROUTE_BACKWARD),
+                                       ("moe_expert_gemm_fourbit", M.MOE_CALL_EXPERT_GEMM_FOURBIT)])
 def test_workspace(name, call):
-    p = _p()
+    p = _p(T=4096, d=1024, f=1024)   # long segments: also the 4-bit experts have some
     need = M.lib().moe_workspace_bytes(ctypes.byref(p), call)
     assert need > 0
     assert _call(name, p, ws=None) == WS
@@ -104,8 +105,8 @@ def test_empty_batches_launch_nothing():
     assert _call("moe_select", p, [None] * 4) == M.MOE_OK
     assert _call("moe_route_scored", p, [None, FAKE] + [None] * 5, **nothing) == M.MOE_OK
     assert _call("moe_route_backward", p, [None] * 10, **nothing) == M.MOE_OK
-    assert _call("moe_expert_gemm_fourbit", p, x_packed=None, h=None, y_packed=None) == M.MOE_OK
-    assert M.lib().moe_gemm_fourbit(0, 64, 64, 32, None, FAKE, FAKE, None, None, M.MOE_DTYPE_BF16, None) == M.MOE_OK
+    assert _call("moe_expert_gemm_fourbit", p, x_packed=None, h=None, y_packed=None, **nothing) == M.MOE_OK
+    assert M.lib().moe_gemm_fourbit(0, 64, 64, 32, None, FAKE, FAKE, None, None, M.MOE_DTYPE_BF16, None, 0, None) == M.MOE_OK
 
 
 def test_experts_take_bf16_rows_and_known_groups():
@@ -133,8 +134,8 @@ def test_packed_weights_arguments():
 
 
 def test_gemm_4bit_arguments():
-    def g(Mr=4, N=16, K=64, G=32, a=FAKE, b=FAKE, s=FAKE, z=FAKE, c=FAKE, dt=M.MOE_DTYPE_BF16):
-        return M.lib().moe_gemm_fourbit(Mr, N, K, G, a, b, s, z, c, dt, None)
+    def g(Mr=4, N=16, K=64, G=32, a=FAKE, b=FAKE, s=FAKE, z=FAKE, c=FAKE, dt=M.MOE_DTYPE_BF16, ws=FAKE, wsb=BIG):
+        return M.lib().moe_gemm_fourbit(Mr, N, K, G, a, b, s, z, c, dt, ws, wsb, None)
     assert g(Mr=-1) == INV and g(N=0) == INV and g(K=0) == INV
     assert g(Mr=(1 << 30) + 1) == UNS and g(N=(1 << 21) + 8) == UNS and g(K=20) == UNS and g(N=12) == UNS and g(dt=9) == UNS
     assert g(G=0) == UNS and g(G=65) == UNS
@@ -143,6 +144,14 @@ def test_gemm_4bit_arguments():
     for name in ("a", "b", "c"):
         assert g(**{name: ODD}) == UNS, name
     assert g(s=FAKE + 4) == UNS and g(z=FAKE + 2) == UNS
+    many = dict(Mr=4096, N=1024, K=1024)
+    need = M.gemm_4bit_workspace_bytes(4096, 1024, 1024)
+    assert need >= 4096 * 1024 * 2
+    assert g(ws=None, wsb=0, **many) == WS and g(wsb=need - 1, **many) == WS and g(ws=FAKE + 16, **many) == WS
+    assert M.gemm_4bit_workspace_bytes(1, 1024, 1024) == 0 and M.gemm_4bit_workspace_bytes(0, 8, 8) == 0
+    for sizes in ((-1, 8, 8), (8, 12, 8), (8, 8, 12)):
+        with pytest.raises(M.MoeError):
+            M.gemm_4bit_workspace_bytes(*sizes)
 
 
 def test_binding_refuses_host_tensors_and_wrong_shapes():
