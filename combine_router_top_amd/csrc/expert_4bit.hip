@@ -351,41 +351,61 @@ struct W4Prepare {
   int64_t rows;
   const int32_t* limit;   // device row count, or NULL
   int K, n;
-  W4Columns m[3];
-  int64_t columns;        // n * sum of N over the matrices given
+  W4Columns m[2];
 };
 
 constexpr int WP_U = 4;   // 8-value pieces a thread keeps between the two passes
+constexpr int WP_COLS = 256;   // columns of a workgroup
 
-// The last workgroups take the columns, a thread for each, the others rows (grid-stride).
-// A row with an infinity or a NaN holds a NaN afterwards, and so does every product of it.
-__global__ __launch_bounds__(256) void w4_prepare(W4Prepare p, int row_blocks) {
-  if ((int)blockIdx.x >= row_blocks) {
-    for (int64_t c = ((int64_t)blockIdx.x - row_blocks) * 256 + threadIdx.x; c < p.columns;
-         c += ((int64_t)gridDim.x - row_blocks) * 256) {
-      int64_t at = c;
-      W4Columns m = p.m[0];
-      if (at >= (int64_t)p.n * m.N) {
-        at -= (int64_t)p.n * m.N;
-        m = p.m[1];
-        if (at >= (int64_t)p.n * m.N) {
-          at -= (int64_t)p.n * m.N;
-          m = p.m[2];
-        }
+// Columns [c, c + WP_COLS) of an expert: thread (lane of 32, part of 8) takes 8 of them and
+// every 8th group.
+__device__ __forceinline__ void w4_columns(const W4Columns& m, int64_t e, int c, uint32_t (*part)[WP_COLS]) {
+  const int lane = threadIdx.x & 31, by = threadIdx.x >> 5, col = c + 8 * lane;
+  uint32_t top[8] = {};
+  if (col < m.N) {
+    const bf16_t* s = m.s + e * m.groups * m.N + col;
+#pragma unroll 4
+    for (int g = by; g < m.groups; g += 8) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(s + (int64_t)g * m.N);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        top[2 * j] = max(top[2 * j], v[j] & 0x7FFFu);
+        top[2 * j + 1] = max(top[2 * j + 1], (v[j] >> 16) & 0x7FFFu);
       }
-      const int64_t e = at / m.N;
-      const bf16_t* s = m.s + e * m.groups * m.N + (at - e * m.N);
-      uint32_t top = 0;
-      for (int g = 0; g < m.groups; ++g) top = max(top, (uint32_t)s[(int64_t)g * m.N] & 0x7FFFu);
-      m.k[at] = w4_exponent(top << 16, 11);
     }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[by][8 * lane + j] = top[j];
+  __syncthreads();
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) most = max(most, part[j][threadIdx.x]);
+  if (c + (int)threadIdx.x < m.N) m.k[e * m.N + c + threadIdx.x] = w4_exponent(most << 16, 11);
+}
+
+// The first workgroups take the columns, the others rows (grid-stride).
+// A row with an infinity or a NaN holds a NaN afterwards, and so does every product of it.
+__global__ __launch_bounds__(256) void w4_prepare(W4Prepare p, int col_blocks) {
+  if ((int)blockIdx.x < col_blocks) {
+    __shared__ uint32_t part[8][WP_COLS];
+    int64_t at = blockIdx.x;
+    int i = 0;
+    for (; i < 2; ++i) {
+      const int64_t here = (int64_t)p.n * ((p.m[i].N + WP_COLS - 1) / WP_COLS);
+      if (at < here) break;
+      at -= here;
+    }
+    const W4Columns m = p.m[i];
+    const int per = (m.N + WP_COLS - 1) / WP_COLS;
+    w4_columns(m, at / per, (int)(at % per) * WP_COLS, part);
     return;
   }
+  const int first = (int)blockIdx.x - col_blocks, row_blocks = (int)gridDim.x - col_blocks;
   __shared__ uint32_t part[2][4];
   const int nv = p.K / 8;
   const int64_t rows = p.limit ? min(p.rows, (int64_t)*p.limit) : p.rows;
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += row_blocks, flip ^= 1) {
+  for (int64_t row = first; row < rows; row += row_blocks, flip ^= 1) {
     const u32x4* src = reinterpret_cast<const u32x4*>(p.a + row * p.K);
     u32x4 keep[WP_U];
     uint32_t top = 0;   // largest magnitude, as bf16 bits in either half
@@ -427,12 +447,10 @@ __global__ __launch_bounds__(256) void w4_prepare(W4Prepare p, int row_blocks) {
 }
 
 static hipError_t launch_prepare(W4Prepare p, hipStream_t st) {
-  int64_t all = 0;
-  for (const W4Columns& m : p.m) all += (int64_t)p.n * m.N;
-  p.columns = all;
+  int64_t cols = 0;
+  for (const W4Columns& m : p.m) cols += (int64_t)p.n * ((m.N + WP_COLS - 1) / WP_COLS);
   const int rows = (int)std::min<int64_t>(p.rows, 8 * (int64_t)device_cus());
-  const int cols = (int)std::min<int64_t>((all + 255) / 256, 4 * (int64_t)device_cus());
-  hipLaunchKernelGGL(w4_prepare, dim3((unsigned)(rows + cols)), dim3(256), 0, st, p, rows);
+  hipLaunchKernelGGL(w4_prepare, dim3((unsigned)(rows + cols)), dim3(256), 0, st, p, (int)cols);
   return hipGetLastError();
 }
 
@@ -499,7 +517,7 @@ hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const
     int32_t* kr = (int32_t*)((char*)ws + pad256((size_t)M * K * 2));
     int32_t* kc = (int32_t*)((char*)kr + pad256((size_t)M * 4));
     const hipError_t e = launch_prepare(
-        W4Prepare{p.a, rows, kr, M, nullptr, K, 1, {W4Columns{p.s1, kc, p.groups, N}, W4Columns{}, W4Columns{}}, 0}, st);
+        W4Prepare{p.a, rows, kr, M, nullptr, K, 1, {W4Columns{p.s1, kc, p.groups, N}, W4Columns{}}}, st);
     if (e != hipSuccess) return e;
     p.a = rows;
     p.kr = kr;
@@ -563,7 +581,7 @@ hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int
     a.k1 = (const int32_t*)(at + w.k1);
     a.k3 = (const int32_t*)(at + w.k3);
     W4Prepare q{a.a, (bf16_t*)(at + w.x), (int32_t*)(at + w.krx), p.rows_max, rows, p.d, p.n,
-                {W4Columns{a.s1, (int32_t*)(at + w.k1), a.groups, p.f}, W4Columns{a.s3, (int32_t*)(at + w.k3), a.groups, p.f}, W4Columns{}}, 0};
+                {W4Columns{a.s1, (int32_t*)(at + w.k1), a.groups, p.f}, W4Columns{a.s3, (int32_t*)(at + w.k3), a.groups, p.f}}};
     if ((e = launch_prepare(q, st)) != hipSuccess) return e;
     a.a = q.out;
   }
@@ -572,7 +590,7 @@ hipError_t launch_expert_4bit(const Prob& p, int group, const void* x, const int
     b.kr = (const int32_t*)(at + w.krh);
     b.k1 = (const int32_t*)(at + w.k2);
     W4Prepare q{b.a, (bf16_t*)(at + w.h), (int32_t*)(at + w.krh), p.rows_max, rows, p.f, p.n,
-                {W4Columns{b.s1, (int32_t*)(at + w.k2), b.groups, p.d}, W4Columns{}, W4Columns{}}, 0};
+                {W4Columns{b.s1, (int32_t*)(at + w.k2), b.groups, p.d}, W4Columns{}}};
     if ((e = launch_prepare(q, st)) != hipSuccess) return e;
     b.a = q.out;
   }
