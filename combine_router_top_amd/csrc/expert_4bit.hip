@@ -356,6 +356,7 @@ struct W4Prepare {
 
 constexpr int WP_U = 4;   // 8-value pieces a thread keeps between the two passes
 constexpr int WP_COLS = 256;   // columns of a workgroup
+typedef uint32_t u32x4_by8 __attribute__((ext_vector_type(4), aligned(8)));   // scales begin at 8 bytes
 
 // Columns [c, c + WP_COLS) of an expert: thread (lane of 32, part of 8) takes 8 of them and
 // every 8th group.
@@ -366,7 +367,7 @@ __device__ __forceinline__ void w4_columns(const W4Columns& m, int64_t e, int c,
     const bf16_t* s = m.s + e * m.groups * m.N + col;
 #pragma unroll 4
     for (int g = by; g < m.groups; g += 8) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(s + (int64_t)g * m.N);
+      const u32x4_by8 v = *reinterpret_cast<const u32x4_by8*>(s + (int64_t)g * m.N);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         top[2 * j] = max(top[2 * j], v[j] & 0x7FFFu);

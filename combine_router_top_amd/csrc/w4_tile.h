@@ -28,6 +28,9 @@
 
 #include "w4.h"
 
+#ifndef W4_S0
+#define W4_S0 (L > 4)
+#endif
 namespace moe {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -37,6 +40,7 @@ template <int GPB_, bool ZERO_, bool GATED_, bool F32OUT_>
 struct W4Cfg {
   static constexpr int GPB = GPB_;
   static constexpr bool ZERO = ZERO_, GATED = GATED_, F32OUT = F32OUT_;
+  static constexpr int WAVES = 4;
   static constexpr int NT = 4, NH = GATED ? 2 : 4;      // a wave's weight and output tiles
   static constexpr int COLS = GATED ? 128 : 256;        // output columns of a tile
   static constexpr int XSLOT = 256 * 128;               // 64 K of 256 rows
@@ -49,7 +53,7 @@ struct W4Cfg {
   // copies of a wave: packed blocks, and pieces of 256 bytes of scales and zero points dealt
   // out over the waves (some twice, so that every wave issues as many)
   static constexpr int SP = 2 * GPB, PIECES = SP + (ZERO ? (GATED ? 2 : 1) * GPB : 0);
-  static constexpr int CS = (PIECES + 7) / 8, W = 2 + CS;
+  static constexpr int WB = 16 / WAVES, CS = (PIECES + WAVES - 1) / WAVES, W = WB + CS;
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
@@ -84,7 +88,7 @@ __device__ __forceinline__ W4Piece w4_piece(int at) {
 // What a wave copies of the weights of a tile.
 template <class C>
 struct W4Ctx {
-  const char* w[2];        // packed runs of its two tiles
+  const char* w[C::WB];    // packed runs of its tiles
   const char* s[C::CS];    // its pieces of scales or zero points of the first block
   uint32_t ssize[C::CS];   // bytes from there to the end of the matrix's, 0 for zero points that it has not
   uint32_t sstep[C::CS];   // bytes between blocks
@@ -104,14 +108,15 @@ __device__ __forceinline__ void w4_setup(const W4Args& p, const StTile& t, W4Ctx
   c.run = (uint32_t)p.kb * 1024u;
   const int64_t eo = (int64_t)t.e * p.ntiles;
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {   // packed tiles wave and wave + 8 (gated: the second matrix)
-    const int tile = C::COLS / 16 * t.nt + (C::GATED ? wave : wave + 8 * v);
-    c.w[v] = w4_scalar((C::GATED && v ? p.b3 : p.b1) + (eo + min(tile, p.ntiles - 1)) * c.run);
+  for (int v = 0; v < C::WB; ++v) {   // packed tiles wave, wave + 4, .. (gated: the second half of the second matrix)
+    const int at = wave + C::WAVES * v;
+    const int tile = C::COLS / 16 * t.nt + (C::GATED ? at % 8 : at);
+    c.w[v] = w4_scalar((C::GATED && v >= C::WB / 2 ? p.b3 : p.b1) + (eo + min(tile, p.ntiles - 1)) * c.run);
   }
   const int64_t go = (int64_t)t.e * p.groups * p.N + C::COLS * t.nt;
 #pragma unroll
   for (int v = 0; v < C::CS; ++v) {
-    const W4Piece q = w4_piece<C>(wave + 8 * v);
+    const W4Piece q = w4_piece<C>(wave + C::WAVES * v);
     const bool m = C::GATED && q.hm;
     const uint8_t* zp = m ? p.z3 : p.z1;
     const uint32_t row = (uint32_t)p.N * (q.zero ? 1u : 2u);   // bytes of a group
@@ -130,8 +135,8 @@ __device__ __forceinline__ void w4_issue(const W4Ctx<C>& c, uint32_t slot, int b
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-  for (int v = 0; v < 2; ++v)
-    bd_copy16(gc_rsrc(c.w[v], c.run), slot + 1024 * (wave + 8 * v), 16u * (uint32_t)lane, (uint32_t)b * 1024u);
+  for (int v = 0; v < C::WB; ++v)
+    bd_copy16(gc_rsrc(c.w[v], c.run), slot + 1024 * (wave + C::WAVES * v), 16u * (uint32_t)lane, (uint32_t)b * 1024u);
 #pragma unroll
   for (int v = 0; v < C::CS; ++v)
     bd_copy4(gc_rsrc(c.s[v], c.ssize[v]), slot + c.sdst[v], 4u * (uint32_t)lane, (uint32_t)b * c.sstep[v]);
@@ -146,10 +151,46 @@ __device__ __forceinline__ uint32_t w4_sreg(uint32_t v) {
   return v;
 }
 
-// A tile's product for L row tiles a wave.  x: copies of the rows (fp16).
+// The rows' copies (fp16), 8 rows of 64 K each: copy c of wave w takes rows 32 c + 8 w .. + 7.
+// Rows past the last one and pieces past a row's end lie outside the descriptor and read zeros.
+struct W4Rows {
+  const char* base;
+  uint32_t voff, ld, size;
+};
+__device__ __forceinline__ W4Rows w4_row_copies(const bf16_t* a, int K, int rows) {
+  const int r = 8 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + ((threadIdx.x & 63) >> 3);
+  W4Rows o;
+  o.base = (const char*)a;
+  o.ld = (uint32_t)K * 2;
+  o.voff = (uint32_t)r * o.ld + 16u * (uint32_t)((threadIdx.x & 7) ^ ((r >> 1) & 7));
+  o.size = (uint32_t)rows * o.ld;
+  return o;
+}
+template <int X>
+__device__ __forceinline__ void w4_issue_rows(const W4Rows& o, uint32_t slot, int st) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = 8 * wave + ((threadIdx.x & 63) >> 3);
+  const uint32_t piece = 16u * (uint32_t)((threadIdx.x & 7) ^ ((r >> 1) & 7));
+  const uint32_t v = (uint32_t)st * ST_KB + piece < o.ld ? o.voff : GC_OOR;
+  const __amdgpu_buffer_rsrc_t d = gc_rsrc(o.base, o.size);
+#pragma unroll
+  for (int c = 0; c < X; ++c)
+    bd_copy16(d, slot + 1024 * (wave + 4 * c), v, (uint32_t)st * ST_KB + (uint32_t)(32 * c) * o.ld);
+}
+
+// As __builtin_amdgcn_mfma_f32_16x16x32_f16, with the sum held in place: of so many sums the
+// compiler moves some at every turn of the loop.  What it would see to is seen to here: a
+// vector instruction that writes an operand has two others between it and its product, and a
+// sum is read only after w4_mfma_done().
+__device__ __forceinline__ void w4_mfma(const u32x4& a, const u32x4& b, f32x4& c) {
+  asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void w4_mfma_done() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
+// A tile's product for L row tiles a wave.
 template <class C, int L>
 struct W4Wave {
-  static constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, SPG = 4 / GPB, X = L / 2;
+  static constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, X = L / 2;
   f32x4 acc[L][NT];
   u32x4 x[L];              // rows of a k-step
   u32x4 w[NT];             // packed words of a block
@@ -163,75 +204,82 @@ struct W4Wave {
   __device__ __forceinline__ int tile(int t) const { return at0 + (C::GATED ? t % NH + 8 * (t / NH) : t); }   // of the slot's 16
 
   __device__ __forceinline__ void read_x(const char* slot, int ks, int m) {
-    x[m] = st_frag<ST_ROWS>(slot, xo, ks, 2 * m);
+    x[m] = st_frag<ST_ROWS>(slot, xo, ks, m);
   }
   __device__ __forceinline__ void read_w(const char* slot) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) w[t] = *reinterpret_cast<const u32x4*>(slot + 1024 * tile(t) + 16 * (threadIdx.x & 63));
   }
-  // Scales and addends of the block's group u.
-  __device__ __forceinline__ void scales(const char* slot, int u) {
-    const int i = threadIdx.x & 15;
+  // Scales and zero points of the block's group u, as they are, and the operands' made of them.
+  __device__ __forceinline__ void read_scales(const char* slot, int u) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int col = 16 * tile(t) + i;   // of the slot's 256
-      const uint32_t raw = *reinterpret_cast<const uint16_t*>(slot + C::SOFF + 512 * u + 2 * col);
-      const float s = __builtin_ldexpf(__uint_as_float(raw << 16), k[t]);
-      S[t] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(s, s));   // exact: 8 bits
-      if constexpr (C::ZERO) {
-        const uint32_t z = *reinterpret_cast<const uint8_t*>(slot + C::ZOFF + C::ZROW * u + col + (C::GATED ? 128 * matrix(t) : 0));
-        Z[t] = z * zmul + zbase[matrix(t)];   // -(128 + z), twice
-      } else {
-        const f16x2 m24 = f16x2{(_Float16)-24, (_Float16)-24};
-        Z[t] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, S[t]) * m24);
-      }
+      const int col = 16 * tile(t) + (int)(threadIdx.x & 15);   // of the slot's 256
+      S[t] = *reinterpret_cast<const uint16_t*>(slot + C::SOFF + 512 * u + 2 * col);
+      if constexpr (C::ZERO)
+        Z[t] = *reinterpret_cast<const uint8_t*>(slot + C::ZOFF + C::ZROW * u + col + (C::GATED ? 128 * matrix(t) : 0));
     }
   }
-  __device__ __forceinline__ u32x4 operand(uint32_t word, int t) const {
-    const f16x2 s = __builtin_bit_cast(f16x2, S[t]), z = __builtin_bit_cast(f16x2, Z[t]);
-    u32x4 o;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int r = (C::ZERO ? 4 * p : 4 * p + 29) & 31;
-      const f16x2 v = __builtin_bit_cast(f16x2, ((r ? __builtin_amdgcn_alignbit(word, word, r) : word) & mask) | bits);
-      o[p] = __builtin_bit_cast(uint32_t, C::ZERO ? (v + z) * s : __builtin_elementwise_fma(v, s, z));
-    }
-    return o;
+  __device__ __forceinline__ void make_scale(int t) {
+    const float s = __builtin_ldexpf(__uint_as_float(S[t] << 16), k[t]);
+    S[t] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(s, s));   // exact: 8 bits
+    if constexpr (C::ZERO) Z[t] = Z[t] * zmul + zbase[matrix(t)];            // -(128 + z), twice
+    else Z[t] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, S[t]) * f16x2{(_Float16)-24, (_Float16)-24});
   }
-  // k-step q of a block: products with f[q & 1]; meanwhile the operands of the next from
-  // the words w, and the rows of the next from (next, ks).
-  template <int Q>
-  __device__ __forceinline__ void kstep(const char* next, int ks) {
+  // Two of the eight weights of a packed word, the numbers at places p and p + 4, in two
+  // halves of two instructions.
+  __device__ __forceinline__ uint32_t pick(uint32_t word, int p) const {
+    const int r = (C::ZERO ? 4 * p : 4 * p + 29) & 31;
+    return ((r ? __builtin_amdgcn_alignbit(word, word, r) : word) & mask) | bits;
+  }
+  __device__ __forceinline__ uint32_t weigh(uint32_t q, int t) const {
+    const f16x2 v = __builtin_bit_cast(f16x2, q), s = __builtin_bit_cast(f16x2, S[t]), z = __builtin_bit_cast(f16x2, Z[t]);
+    return __builtin_bit_cast(uint32_t, C::ZERO ? (v + z) * s : __builtin_elementwise_fma(v, s, z));
+  }
+  // k-step Q of a block: products with f[Q & 1]; meanwhile the operands of the next from
+  // the words w (SCALES: scales that were just read), and the rows of the next from (next, ks),
+  // after `sync`, which comes once the first products are under way.  A product leaves room
+  // for one or two vector instructions of its wave, more in a row hold up the next: so they
+  // are dealt out, in a fixed order.
+  template <int Q, bool SCALES, class Sync>
+  __device__ __forceinline__ void kstep(const char* next, int ks, const Sync& sync) {
     constexpr int b = Q & 1, n = (Q + 1) & 3;
+    constexpr int S0 = W4_S0, MS = S0 + 1 + (L > 8), M0 = MS + 1, M1 = L - (L > 4);
+    constexpr int H = 8 * NT, A = M0 * NT, B = M1 * NT;   // halves, and the products beside which they are made
 #pragma unroll
     for (int m = 0; m < L; ++m) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, f[b][t]), __builtin_bit_cast(f16x8, x[m]),
-                                                           acc[m][t], 0, 0, 0);
-      // the second half of the row tiles makes the operands: scales and words have arrived
-      constexpr int H = L / 2;
+      for (int t = 0; t < NT; ++t) {
+        w4_mfma(f[b][t], x[m], acc[m][t]);
+        if (SCALES && m == MS) make_scale(t);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (m >= H && t >= (m - H) * NT / (L - H) && t < (m - H + 1) * NT / (L - H)) f[b ^ 1][t] = operand(w[t][n], t);
-      __builtin_amdgcn_sched_barrier(0);
-      read_x(next, ks, m);   // into the registers just used
+        for (int h = 0; h < H; ++h)
+          if (A + h * (B - A) / H == m * NT + t) {
+            const int t = h / 8, p = h % 8 / 2;
+            f[b ^ 1][t][p] = h & 1 ? weigh(f[b ^ 1][t][p], t) : pick(w[t][n], p);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (m == S0) {
+        sync();
+#pragma unroll
+        for (int j = 0; j <= S0; ++j) read_x(next, ks, j);
+      }
+      if (m > S0) read_x(next, ks, m);   // into the registers just used
     }
   }
 };
 
 template <class C, int L>
 __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t, char* ring, W4Ctx<C>& c) {
-  constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, SPG = 4 / GPB, X = L / 2;
+  constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, X = L / 2;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
   const uint32_t lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
-  StOp<ST_ROWS, 32 * L> xr;
-  st_rows(xr, p.a + (int64_t)t.r0 * p.K, (uint32_t)p.K * 2, t.R, (uint32_t)p.K * 2);
+  const W4Rows xr = w4_row_copies(p.a + (int64_t)t.r0 * p.K, p.K, min(t.R, 16 * L));
   W4Wave<C, L> v;
-  v.xo = st_lane<ST_ROWS>(wm);
-  v.at0 = NH * wn;
+  v.xo = st_lane<ST_ROWS>(0);
+  v.at0 = NH * wave;
   v.mask = w4_vreg(C::ZERO ? 0x00780078u : 0x03C003C0u);
   v.bits = w4_sreg(C::ZERO ? 0x58005800u : 0x4C004C00u);
   v.zmul = w4_sreg(0x00080008u);
@@ -249,48 +297,53 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): or the compiler waits for these loads in the loop
   auto xslot = [&](int j) { return lbase + (uint32_t)(j * C::XSLOT); };
   w4_issue(c, lbase + C::WOFF, 0);
-  st_issue(xr, xslot(0), 0);
-  st_issue(xr, xslot(1), 1);
+  w4_issue_rows<X>(xr, xslot(0), 0);
+  w4_issue_rows<X>(xr, xslot(1), 1);
   w4_issue(c, lbase + C::WOFF + C::WSLOT, 1);
-  st_issue(xr, xslot(2), 2);
+  w4_issue_rows<X>(xr, xslot(2), 2);
   st_sync<2 * X + C::W>();
   const char* ws = ring + C::WOFF;   // slot of this block
 #pragma unroll
   for (int m = 0; m < L; ++m) v.read_x(ring, 0, m);
   v.read_w(ws);
-  v.scales(ws, 0);
+  v.read_scales(ws, 0);
 #pragma unroll
-  for (int q = 0; q < NT; ++q) v.f[0][q] = v.operand(v.w[q][0], q);
+  for (int q = 0; q < NT; ++q) v.make_scale(q);
+#pragma unroll
+  for (int u = 0; u < 4 * NT; ++u) v.f[0][u / 4][u % 4] = v.weigh(v.pick(v.w[u / 4][0], u % 4), u / 4);
   uint32_t x0 = 0, x1 = C::XSLOT, x2 = 2 * C::XSLOT;   // slots of this step, the next and the one after
   uint32_t wo = 0;                                     // offset of this block's slot
   for (int b = 0; b < p.kb; ++b) {
     ws = ring + C::WOFF + wo;
-    if (GPB == 4) v.scales(ws, 1);
-    v.template kstep<0>(ring + x0, 1);
-    // the next step's rows have arrived, this step's are in registers: their slot is refilled
-    st_sync<C::W + X>();
-    st_issue(xr, lbase + x0, 2 * b + 3);
-    if (SPG <= 2) v.scales(ws, SPG == 2 ? 1 : 2);
-    v.template kstep<1>(ring + x1, 0);
-    if (GPB == 4) v.scales(ws, 3);
-    v.template kstep<2>(ring + x1, 1);
-    st_sync<X>();
-    w4_issue(c, lbase + C::WOFF + wo, b + 2);
-    st_issue(xr, lbase + x1, 2 * b + 4);
-    wo = C::WSLOT - wo;
-    v.read_w(ring + C::WOFF + wo);
-    v.scales(ring + C::WOFF + wo, 0);
-    v.template kstep<3>(ring + x2, 0);
+    if (GPB == 4) v.read_scales(ws, 1);
+    v.template kstep<0, GPB == 4>(ring + x0, 1, [] {});
+    if (GPB >= 2) v.read_scales(ws, GPB == 2 ? 1 : 2);
+    v.template kstep<1, GPB >= 2>(ring + x1, 0, [&] {
+      // the next step's rows have arrived, this step's are in registers: their slot is refilled
+      st_sync<C::W + X>();
+      w4_issue_rows<X>(xr, lbase + x0, 2 * b + 3);
+    });
+    if (GPB == 4) v.read_scales(ws, 3);
+    v.template kstep<2, GPB == 4>(ring + x1, 1, [] {});
+    v.template kstep<3, true>(ring + x2, 0, [&] {
+      st_sync<X>();
+      w4_issue(c, lbase + C::WOFF + wo, b + 2);
+      w4_issue_rows<X>(xr, lbase + x1, 2 * b + 4);
+      wo = C::WSLOT - wo;
+      v.read_w(ring + C::WOFF + wo);
+      v.read_scales(ring + C::WOFF + wo, 0);
+    });
     const uint32_t keep = x0;
     x0 = x2;
     x2 = x1;
     x1 = keep;
   }
+  w4_mfma_done();
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave is done with the ring
 
   constexpr int ES = C::F32OUT ? 4 : 2;
   const StOut out = st_out((char*)p.c + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
-  const int col0 = C::COLS * t.nt + 16 * NH * wn;
+  const int col0 = C::COLS * t.nt + 16 * NH * wave;
   int kc[NT][4];   // exponents of the columns that this lane stores
 #pragma unroll
   for (int q = 0; q < NT; ++q) {
@@ -301,7 +354,7 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
   }
 #pragma unroll
   for (int m = 0; m < L; ++m) {
-    const int row = 16 * (2 * m + wm) + i;
+    const int row = 16 * m + i;
     const int kr = p.kr[t.r0 + min(row, t.R - 1)];
     f32x4 o[NH];
 #pragma unroll
@@ -329,16 +382,16 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
 }
 
 template <class C>
-__global__ __launch_bounds__(ST_NT, 1) void w4_tile(W4Args p, int ntn, int bm) {
+__global__ __launch_bounds__(64 * C::WAVES, 1) void w4_tile(W4Args p, int ntn, int bm) {
   __shared__ __attribute__((aligned(16))) char ring[C::LDS];
   const int blocks = p.offsets ? st_row_blocks(p.offsets, p.n, bm) : (p.M + bm - 1) / bm;
   for (int L = st_first_tile(); L < blocks * ntn; L += (int)gridDim.x) {
     const StTile t = p.offsets ? st_tile_at(L, p.offsets, p.n, ntn, bm) : st_tile_of(L, 0, p.M, blocks, ntn, bm);
     W4Ctx<C> c;
     w4_setup<C>(p, t, c);
-    if (t.R <= 64) w4_tile_product<C, 2>(p, t, ring, c);
-    else if (t.R <= 128) w4_tile_product<C, 4>(p, t, ring, c);
-    else w4_tile_product<C, 6>(p, t, ring, c);
+    if (t.R <= 64) w4_tile_product<C, 4>(p, t, ring, c);
+    else if (t.R <= 128) w4_tile_product<C, 8>(p, t, ring, c);
+    else w4_tile_product<C, 12>(p, t, ring, c);
   }
 }
 
@@ -346,7 +399,7 @@ template <bool GATED, bool F32OUT, int GPB, bool ZERO>
 static hipError_t launch_w4_tile(const W4Args& p, int bm, int64_t rows_max, hipStream_t st) {
   using C = W4Cfg<GPB, ZERO, GATED, F32OUT>;
   const int ntn = (p.N + C::COLS - 1) / C::COLS;
-  hipLaunchKernelGGL(w4_tile<C>, st_row_grid(rows_max, p.n, bm / 64, ntn), dim3(ST_NT), 0, st, p, ntn, bm);
+  hipLaunchKernelGGL(w4_tile<C>, st_row_grid(rows_max, p.n, bm / 64, ntn), dim3(64 * C::WAVES), 0, st, p, ntn, bm);
   return hipGetLastError();
 }
 
