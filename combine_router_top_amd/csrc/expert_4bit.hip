@@ -346,7 +346,7 @@ struct W4Columns {
 };
 struct W4Prepare {
   const bf16_t* a;
-  bf16_t* out;            // fp16 bits
+  bf16_t* out;            // fp16 bits, K padded with zeros to whole blocks
   int32_t* kr;
   int64_t rows;
   const int32_t* limit;   // device row count, or NULL
@@ -429,7 +429,8 @@ __global__ __launch_bounds__(256) void w4_prepare(W4Prepare p, int col_blocks) {
     const int k = w4_exponent(top << 16, 15);
     const bool bad = top >= 0x7F80u;
     if (threadIdx.x == 0) p.kr[row] = k;
-    u32x4* dst = reinterpret_cast<u32x4*>(p.out + row * p.K);
+    const int nvp = (p.K + W4_KB - 1) / W4_KB * (W4_KB / 8);
+    u32x4* dst = reinterpret_cast<u32x4*>(p.out + row * (8 * (int64_t)nvp));
     auto convert = [&](const u32x4& v) {
       u32x4 o;
 #pragma unroll
@@ -444,6 +445,7 @@ __global__ __launch_bounds__(256) void w4_prepare(W4Prepare p, int col_blocks) {
     for (int u = 0; u < WP_U; ++u)
       if ((int)threadIdx.x + 256 * u < nv) dst[threadIdx.x + 256 * u] = convert(keep[u]);
     for (int v = threadIdx.x + 256 * WP_U; v < nv; v += 256) dst[v] = convert(src[v]);
+    if ((int)threadIdx.x < nvp - nv) dst[nv + threadIdx.x] = u32x4{0, 0, 0, 0};
   }
 }
 
@@ -493,6 +495,7 @@ static W4Args w4_args(int n, int K, int N, int group) {
 }
 
 static size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
+static size_t w4_row_bytes(int64_t rows, int K) { return (size_t)rows * ((K + W4_KB - 1) / W4_KB) * (2 * W4_KB); }
 
 static W4Plan gemm_plan(int M, int N, int K) {
   return w4_plan(device_cus(), W4Shape{false, false, 1, N, (K + W4_KB - 1) / W4_KB, M, M, M});
@@ -500,7 +503,7 @@ static W4Plan gemm_plan(int M, int N, int K) {
 
 size_t gemm_4bit_ws_bytes(int M, int N, int K) {
   if (M == 0 || !gemm_plan(M, N, K).tiles) return 0;
-  return pad256((size_t)M * K * 2) + pad256((size_t)M * 4) + pad256((size_t)N * 4);
+  return pad256(w4_row_bytes(M, K)) + pad256((size_t)M * 4) + pad256((size_t)N * 4);
 }
 
 hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const void* packed, const void* scale,
@@ -515,7 +518,7 @@ hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const
   p.c = c;
   if (plan.tiles) {
     bf16_t* rows = (bf16_t*)ws;
-    int32_t* kr = (int32_t*)((char*)ws + pad256((size_t)M * K * 2));
+    int32_t* kr = (int32_t*)((char*)ws + pad256(w4_row_bytes(M, K)));
     int32_t* kc = (int32_t*)((char*)kr + pad256((size_t)M * 4));
     const hipError_t e = launch_prepare(
         W4Prepare{p.a, rows, kr, M, nullptr, K, 1, {W4Columns{p.s1, kc, p.groups, N}, W4Columns{}}}, st);
@@ -542,11 +545,11 @@ static W4Expert expert_plan(const Prob& p) {
     o += wanted ? pad256(bytes) : 0;
     return at;
   };
-  w.x = take(w.up.tiles, (size_t)p.rows_max * p.d * 2);
+  w.x = take(w.up.tiles, w4_row_bytes(p.rows_max, p.d));
   w.krx = take(w.up.tiles, (size_t)p.rows_max * 4);
   w.k1 = take(w.up.tiles, (size_t)p.n * p.f * 4);
   w.k3 = take(w.up.tiles, (size_t)p.n * p.f * 4);
-  w.h = take(w.down.tiles, (size_t)p.rows_max * p.f * 2);
+  w.h = take(w.down.tiles, w4_row_bytes(p.rows_max, p.f));
   w.krh = take(w.down.tiles, (size_t)p.rows_max * 4);
   w.k2 = take(w.down.tiles, (size_t)p.n * p.d * 4);
   w.total = o;

@@ -57,15 +57,15 @@ struct W4Cfg {
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-// As bd_copy16, 4 bytes per lane.
-__device__ __forceinline__ void bd_copy4(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  uint32_t keep;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-      "buffer_load_dword %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
-      : "=&s"(keep)
-      : "s"(lds), "v"(voff), "s"(r), "s"(soff)
-      : "memory");
+// 16 (4) bytes per lane from descriptor r at voff + soff to LDS at `lds` + at + 16 (4) lane.
+template <int BYTES>
+__device__ __forceinline__ void w4_copy(__amdgpu_buffer_rsrc_t r, uint32_t lds, int at, uint32_t voff, uint32_t soff) {
+  if constexpr (BYTES == 16)
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
+                 :: "s"(lds), "i"(at), "v"(voff), "s"(r), "s"(soff) : "memory", "m0", "scc");
+  else
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dword %2, %3, %4 offen lds"
+                 :: "s"(lds), "i"(at), "v"(voff), "s"(r), "s"(soff) : "memory", "m0", "scc");
 }
 
 // A 256-byte piece of a block's scales or zero points: group u, matrix or half of the columns hm.
@@ -88,12 +88,13 @@ __device__ __forceinline__ W4Piece w4_piece(int at) {
 // What a wave copies of the weights of a tile.
 template <class C>
 struct W4Ctx {
-  const char* w[C::WB];    // packed runs of its tiles
+  const char* w[2];        // packed runs of the tile's first columns (gated: of each matrix)
+  uint32_t wsize;          // bytes from there to the end of the expert's
+  uint32_t woff[C::WB];    // lane offsets of its runs
   const char* s[C::CS];    // its pieces of scales or zero points of the first block
   uint32_t ssize[C::CS];   // bytes from there to the end of the matrix's, 0 for zero points that it has not
   uint32_t sstep[C::CS];   // bytes between blocks
   uint32_t sdst[C::CS];    // where in a slot
-  uint32_t run;
 };
 
 __device__ __forceinline__ const char* w4_scalar(const char* p) {   // descriptors are made of it
@@ -105,13 +106,16 @@ __device__ __forceinline__ const char* w4_scalar(const char* p) {   // descripto
 template <class C>
 __device__ __forceinline__ void w4_setup(const W4Args& p, const StTile& t, W4Ctx<C>& c) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  c.run = (uint32_t)p.kb * 1024u;
-  const int64_t eo = (int64_t)t.e * p.ntiles;
+  const uint32_t run = (uint32_t)p.kb * 1024u;
+  const int first = C::COLS / 16 * t.nt, most = p.ntiles - 1 - first;
+  const int64_t eo = ((int64_t)t.e * p.ntiles + first) * run;
+  c.w[0] = w4_scalar(p.b1 + eo);
+  c.w[1] = w4_scalar((C::GATED ? p.b3 : p.b1) + eo);
+  c.wsize = __builtin_amdgcn_readfirstlane((uint32_t)min((int64_t)(most + 1) * run, (int64_t)UINT32_MAX));
 #pragma unroll
   for (int v = 0; v < C::WB; ++v) {   // packed tiles wave, wave + 4, .. (gated: the second half of the second matrix)
     const int at = wave + C::WAVES * v;
-    const int tile = C::COLS / 16 * t.nt + (C::GATED ? at % 8 : at);
-    c.w[v] = w4_scalar((C::GATED && v >= C::WB / 2 ? p.b3 : p.b1) + (eo + min(tile, p.ntiles - 1)) * c.run);
+    c.woff[v] = (uint32_t)min(C::GATED ? at % 8 : at, most) * run + 16u * (threadIdx.x & 63);
   }
   const int64_t go = (int64_t)t.e * p.groups * p.N + C::COLS * t.nt;
 #pragma unroll
@@ -129,17 +133,17 @@ __device__ __forceinline__ void w4_setup(const W4Args& p, const StTile& t, W4Ctx
   }
 }
 
-// The copies of block b into the slot at LDS address `slot`; blocks past the last read zeros.
+// Copy v (of W) of block b into the slot at LDS address `slot` (of this wave: slot + 1024
+// wave).  What is past the last block is in the expert's matrix or reads zeros.
 template <class C>
-__device__ __forceinline__ void w4_issue(const W4Ctx<C>& c, uint32_t slot, int b) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-#pragma unroll
-  for (int v = 0; v < C::WB; ++v)
-    bd_copy16(gc_rsrc(c.w[v], c.run), slot + 1024 * (wave + C::WAVES * v), 16u * (uint32_t)lane, (uint32_t)b * 1024u);
-#pragma unroll
-  for (int v = 0; v < C::CS; ++v)
-    bd_copy4(gc_rsrc(c.s[v], c.ssize[v]), slot + c.sdst[v], 4u * (uint32_t)lane, (uint32_t)b * c.sstep[v]);
+__device__ __forceinline__ void w4_issue(const W4Ctx<C>& c, uint32_t slot, int b, int v) {
+  if (v < C::WB) {
+    const __amdgpu_buffer_rsrc_t r = gc_rsrc(c.w[C::GATED && v >= C::WB / 2 ? 1 : 0], c.wsize);
+    w4_copy<16>(r, slot + 1024 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), 1024 * C::WAVES * v, c.woff[v], (uint32_t)b * 1024u);
+  } else {
+    const int u = v - C::WB;
+    w4_copy<4>(gc_rsrc(c.s[u], c.ssize[u]), slot + c.sdst[u], 0, 4u * (threadIdx.x & 63), (uint32_t)b * c.sstep[u]);
+  }
 }
 
 __device__ __forceinline__ uint32_t w4_vreg(uint32_t v) {   // a constant that is no literal (w4_unpack)
@@ -151,32 +155,25 @@ __device__ __forceinline__ uint32_t w4_sreg(uint32_t v) {
   return v;
 }
 
-// The rows' copies (fp16), 8 rows of 64 K each: copy c of wave w takes rows 32 c + 8 w .. + 7.
-// Rows past the last one and pieces past a row's end lie outside the descriptor and read zeros.
+// The rows' copies (fp16, of K padded to whole blocks), 8 rows of 64 K each: copy c of wave w
+// takes rows 32 c + 8 w .. + 7.  Rows past the last one lie outside the descriptor and read
+// zeros; steps past the last read rows that follow, or zeros, and are not multiplied.
+template <int X>
 struct W4Rows {
   const char* base;
-  uint32_t voff, ld, size;
-};
-__device__ __forceinline__ W4Rows w4_row_copies(const bf16_t* a, int K, int rows) {
-  const int r = 8 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + ((threadIdx.x & 63) >> 3);
-  W4Rows o;
-  o.base = (const char*)a;
-  o.ld = (uint32_t)K * 2;
-  o.voff = (uint32_t)r * o.ld + 16u * (uint32_t)((threadIdx.x & 7) ^ ((r >> 1) & 7));
-  o.size = (uint32_t)rows * o.ld;
-  return o;
-}
-template <int X>
-__device__ __forceinline__ void w4_issue_rows(const W4Rows& o, uint32_t slot, int st) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = 8 * wave + ((threadIdx.x & 63) >> 3);
-  const uint32_t piece = 16u * (uint32_t)((threadIdx.x & 7) ^ ((r >> 1) & 7));
-  const uint32_t v = (uint32_t)st * ST_KB + piece < o.ld ? o.voff : GC_OOR;
-  const __amdgpu_buffer_rsrc_t d = gc_rsrc(o.base, o.size);
+  uint32_t voff[X], size;
+  __device__ __forceinline__ void of(const bf16_t* a, uint32_t ld, int rows) {
+    const int r = 8 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + ((threadIdx.x & 63) >> 3);
+    base = w4_scalar((const char*)a);
 #pragma unroll
-  for (int c = 0; c < X; ++c)
-    bd_copy16(d, slot + 1024 * (wave + 4 * c), v, (uint32_t)st * ST_KB + (uint32_t)(32 * c) * o.ld);
-}
+    for (int c = 0; c < X; ++c) voff[c] = (uint32_t)(r + 32 * c) * ld + 16u * (uint32_t)((threadIdx.x & 7) ^ ((r >> 1) & 7));
+    size = __builtin_amdgcn_readfirstlane((uint32_t)rows * ld);
+  }
+  __device__ __forceinline__ void issue(uint32_t slot, int st, int c) const {   // slot: of this wave
+    w4_copy<16>(gc_rsrc(base, size), slot + 1024 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), 4096 * c, voff[c],
+                (uint32_t)st * ST_KB);
+  }
+};
 
 // As __builtin_amdgcn_mfma_f32_16x16x32_f16, with the sum held in place: of so many sums the
 // compiler moves some at every turn of the loop.  What it would see to is seen to here: a
@@ -226,38 +223,52 @@ struct W4Wave {
     if constexpr (C::ZERO) Z[t] = Z[t] * zmul + zbase[matrix(t)];            // -(128 + z), twice
     else Z[t] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, S[t]) * f16x2{(_Float16)-24, (_Float16)-24});
   }
-  // Two of the eight weights of a packed word, the numbers at places p and p + 4, in two
-  // halves of two instructions.
-  __device__ __forceinline__ uint32_t pick(uint32_t word, int p) const {
+  // Numbers p and p + 4 of the packed word of k-step n, as operand values of buffer b, in steps.
+  __device__ __forceinline__ void pick(int b, int t, int n, int p) {
+    const uint32_t word = w[t][n];
     const int r = (C::ZERO ? 4 * p : 4 * p + 29) & 31;
-    return ((r ? __builtin_amdgcn_alignbit(word, word, r) : word) & mask) | bits;
+    f[b][t][p] = ((r ? __builtin_amdgcn_alignbit(word, word, r) : word) & mask) | bits;
   }
-  __device__ __forceinline__ uint32_t weigh(uint32_t q, int t) const {
-    const f16x2 v = __builtin_bit_cast(f16x2, q), s = __builtin_bit_cast(f16x2, S[t]), z = __builtin_bit_cast(f16x2, Z[t]);
-    return __builtin_bit_cast(uint32_t, C::ZERO ? (v + z) * s : __builtin_elementwise_fma(v, s, z));
+  __device__ __forceinline__ void less(int b, int t, int p) {
+    f[b][t][p] = __builtin_bit_cast(uint32_t, half2(f[b][t][p]) + half2(Z[t]));
+  }
+  __device__ __forceinline__ void weigh(int b, int t, int p) {
+    const f16x2 v = half2(f[b][t][p]), s = half2(S[t]);
+    f[b][t][p] = __builtin_bit_cast(uint32_t, C::ZERO ? v * s : __builtin_elementwise_fma(v, s, half2(Z[t])));
+  }
+  static __device__ __forceinline__ f16x2 half2(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
+  // Step h of PARTS for two pairs of numbers, two instructions each (a sum is not
+  // followed at once by the product that takes it, which would wait).
+  static constexpr int PARTS = C::ZERO ? 4 : 3;
+  __device__ __forceinline__ void part(int b, int n, int h) {
+    const int t = h / (2 * PARTS), p = h / PARTS % 2 * 2;
+    switch (h % PARTS) {
+      case 0: pick(b, t, n, p); break;
+      case 1: pick(b, t, n, p + 1); break;
+      case PARTS - 1: weigh(b, t, p); weigh(b, t, p + 1); break;
+      default: less(b, t, p); less(b, t, p + 1);
+    }
   }
   // k-step Q of a block: products with f[Q & 1]; meanwhile the operands of the next from
   // the words w (SCALES: scales that were just read), and the rows of the next from (next, ks),
   // after `sync`, which comes once the first products are under way.  A product leaves room
   // for one or two vector instructions of its wave, more in a row hold up the next: so they
-  // are dealt out, in a fixed order.
-  template <int Q, bool SCALES, class Sync>
-  __device__ __forceinline__ void kstep(const char* next, int ks, const Sync& sync) {
+  // are dealt out, in a fixed order, and so are the COPIES copies, copy(0), copy(1), ..
+  template <int Q, bool SCALES, int COPIES, class Sync, class Copy>
+  __device__ __forceinline__ void kstep(const char* next, int ks, const Sync& sync, const Copy& copy) {
     constexpr int b = Q & 1, n = (Q + 1) & 3;
     constexpr int S0 = W4_S0, MS = S0 + 1 + (L > 8), M0 = MS + 1, M1 = L - (L > 4);
-    constexpr int H = 8 * NT, A = M0 * NT, B = M1 * NT;   // halves, and the products beside which they are made
+    constexpr int H = 2 * PARTS * NT, A = M0 * NT, B = M1 * NT;   // halves, and the products beside which they are made
 #pragma unroll
     for (int m = 0; m < L; ++m) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         w4_mfma(f[b][t], x[m], acc[m][t]);
+        __builtin_amdgcn_sched_barrier(0);
         if (SCALES && m == MS) make_scale(t);
 #pragma unroll
         for (int h = 0; h < H; ++h)
-          if (A + h * (B - A) / H == m * NT + t) {
-            const int t = h / 8, p = h % 8 / 2;
-            f[b ^ 1][t][p] = h & 1 ? weigh(f[b ^ 1][t][p], t) : pick(w[t][n], p);
-          }
+          if (A + h * (B - A) / H == m * NT + t) part(b ^ 1, n, h);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (m == S0) {
@@ -265,7 +276,12 @@ struct W4Wave {
 #pragma unroll
         for (int j = 0; j <= S0; ++j) read_x(next, ks, j);
       }
-      if (m > S0) read_x(next, ks, m);   // into the registers just used
+      if (m > S0) {
+        read_x(next, ks, m);   // into the registers just used
+#pragma unroll
+        for (int c = 0; c < COPIES; ++c)
+          if (S0 + 1 + c * (L - 1 - S0) / (COPIES ? COPIES : 1) == m) copy(c);
+      }
     }
   }
 };
@@ -276,7 +292,9 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
-  const W4Rows xr = w4_row_copies(p.a + (int64_t)t.r0 * p.K, p.K, min(t.R, 16 * L));
+  const uint32_t ld = (uint32_t)p.kb * (2 * W4_KB);   // bytes of a row
+  W4Rows<X> xr;
+  xr.of(p.a + (int64_t)t.r0 * (p.kb * W4_KB), ld, min(t.R, 16 * L));
   W4Wave<C, L> v;
   v.xo = st_lane<ST_ROWS>(0);
   v.at0 = NH * wave;
@@ -296,11 +314,19 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
     for (int q = 0; q < NT; ++q) v.acc[m][q] = f32x4{0.f, 0.f, 0.f, 0.f};
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): or the compiler waits for these loads in the loop
   auto xslot = [&](int j) { return lbase + (uint32_t)(j * C::XSLOT); };
-  w4_issue(c, lbase + C::WOFF, 0);
-  w4_issue_rows<X>(xr, xslot(0), 0);
-  w4_issue_rows<X>(xr, xslot(1), 1);
-  w4_issue(c, lbase + C::WOFF + C::WSLOT, 1);
-  w4_issue_rows<X>(xr, xslot(2), 2);
+  auto block = [&](uint32_t slot, int b) {
+#pragma unroll
+    for (int u = 0; u < C::W; ++u) w4_issue(c, lbase + C::WOFF + slot, b, u);
+  };
+  auto rows = [&](int j) {
+#pragma unroll
+    for (int u = 0; u < X; ++u) xr.issue(xslot(j), j, u);
+  };
+  block(0, 0);
+  rows(0);
+  rows(1);
+  block(C::WSLOT, 1);
+  rows(2);
   st_sync<2 * X + C::W>();
   const char* ws = ring + C::WOFF;   // slot of this block
 #pragma unroll
@@ -310,29 +336,29 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
 #pragma unroll
   for (int q = 0; q < NT; ++q) v.make_scale(q);
 #pragma unroll
-  for (int u = 0; u < 4 * NT; ++u) v.f[0][u / 4][u % 4] = v.weigh(v.pick(v.w[u / 4][0], u % 4), u / 4);
+  for (int h = 0; h < 2 * NT * v.PARTS; ++h) v.part(0, 0, h);
   uint32_t x0 = 0, x1 = C::XSLOT, x2 = 2 * C::XSLOT;   // slots of this step, the next and the one after
   uint32_t wo = 0;                                     // offset of this block's slot
   for (int b = 0; b < p.kb; ++b) {
     ws = ring + C::WOFF + wo;
+    auto nothing = [](auto...) {};
     if (GPB == 4) v.read_scales(ws, 1);
-    v.template kstep<0, GPB == 4>(ring + x0, 1, [] {});
+    v.template kstep<0, GPB == 4, 0>(ring + x0, 1, nothing, nothing);
     if (GPB >= 2) v.read_scales(ws, GPB == 2 ? 1 : 2);
-    v.template kstep<1, GPB >= 2>(ring + x1, 0, [&] {
-      // the next step's rows have arrived, this step's are in registers: their slot is refilled
-      st_sync<C::W + X>();
-      w4_issue_rows<X>(xr, lbase + x0, 2 * b + 3);
-    });
+    // the next step's rows have arrived, this step's are in registers: their slot is refilled
+    v.template kstep<1, GPB >= 2, X>(ring + x1, 0, [] { st_sync<C::W + X>(); },
+                                     [&](int u) { xr.issue(lbase + x0, 2 * b + 3, u); });
     if (GPB == 4) v.read_scales(ws, 3);
-    v.template kstep<2, GPB == 4>(ring + x1, 1, [] {});
-    v.template kstep<3, true>(ring + x2, 0, [&] {
+    v.template kstep<2, GPB == 4, 0>(ring + x1, 1, nothing, nothing);
+    v.template kstep<3, true, C::W + X>(ring + x2, 0, [&] {
       st_sync<X>();
-      w4_issue(c, lbase + C::WOFF + wo, b + 2);
-      w4_issue_rows<X>(xr, lbase + x1, 2 * b + 4);
-      wo = C::WSLOT - wo;
-      v.read_w(ring + C::WOFF + wo);
-      v.read_scales(ring + C::WOFF + wo, 0);
+      v.read_w(ring + C::WOFF + C::WSLOT - wo);
+      v.read_scales(ring + C::WOFF + C::WSLOT - wo, 0);
+    }, [&](int u) {
+      if (u < C::W) w4_issue(c, lbase + C::WOFF + wo, b + 2, u);
+      else xr.issue(lbase + x1, 2 * b + 4, u - C::W);
     });
+    wo = C::WSLOT - wo;
     const uint32_t keep = x0;
     x0 = x2;
     x2 = x1;
