@@ -184,6 +184,28 @@ __device__ __forceinline__ void w4_mfma(const u32x4& a, const u32x4& b, f32x4& c
 }
 __device__ __forceinline__ void w4_mfma_done() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
+// Row tiles of a tile of `rows` rows.
+__device__ __forceinline__ int w4_height(int rows) { return rows <= 64 ? 4 : min(2 * ((rows + 31) / 32), 12); }
+
+// The first copies of a tile: two blocks of the weights, three steps of the rows.
+template <class C>
+__device__ __forceinline__ void w4_begin(const W4Args& p, const StTile& t, const W4Ctx<C>& c, uint32_t lbase) {
+  const uint32_t ld = (uint32_t)p.kb * (2 * W4_KB);
+  const int X = w4_height(t.R) / 2;
+  W4Rows<1> x;
+  x.of(p.a + (int64_t)t.r0 * (p.kb * W4_KB), ld, t.R);
+  const __amdgpu_buffer_rsrc_t r = gc_rsrc(x.base, x.size);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int u = 0; u < C::W; ++u) w4_issue(c, lbase + C::WOFF + b * C::WSLOT, b, u);
+  for (int u = 0; u < X; ++u)
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      w4_copy<16>(r, lbase + 1024 * wave + 4096 * u, j * C::XSLOT, x.voff[0] + (uint32_t)(32 * u) * ld, (uint32_t)j * ST_KB);
+}
+
 // A tile's product for L row tiles a wave.
 template <class C, int L>
 struct W4Wave {
@@ -286,8 +308,11 @@ struct W4Wave {
   }
 };
 
-template <class C, int L>
-__device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t, char* ring, W4Ctx<C>& c) {
+// Product of a tile whose first copies are under way; `after` begins the next one, once the
+// ring is free, before this one's stores.
+template <class C, int L, class After>
+__device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile t, char* ring, const W4Ctx<C>& c,
+                                                const After& after) {
   constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, X = L / 2;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -313,21 +338,7 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
 #pragma unroll
     for (int q = 0; q < NT; ++q) v.acc[m][q] = f32x4{0.f, 0.f, 0.f, 0.f};
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): or the compiler waits for these loads in the loop
-  auto xslot = [&](int j) { return lbase + (uint32_t)(j * C::XSLOT); };
-  auto block = [&](uint32_t slot, int b) {
-#pragma unroll
-    for (int u = 0; u < C::W; ++u) w4_issue(c, lbase + C::WOFF + slot, b, u);
-  };
-  auto rows = [&](int j) {
-#pragma unroll
-    for (int u = 0; u < X; ++u) xr.issue(xslot(j), j, u);
-  };
-  block(0, 0);
-  rows(0);
-  rows(1);
-  block(C::WSLOT, 1);
-  rows(2);
-  st_sync<2 * X + C::W>();
+  st_sync<0>();
   const char* ws = ring + C::WOFF;   // slot of this block
 #pragma unroll
   for (int m = 0; m < L; ++m) v.read_x(ring, 0, m);
@@ -367,8 +378,6 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
   w4_mfma_done();
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // every wave is done with the ring
 
-  constexpr int ES = C::F32OUT ? 4 : 2;
-  const StOut out = st_out((char*)p.c + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
   const int col0 = C::COLS * t.nt + 16 * NH * wave;
   int kc[NT][4];   // exponents of the columns that this lane stores
 #pragma unroll
@@ -378,17 +387,24 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile& t
 #pragma unroll
     for (int r = 0; r < 4; ++r) kc[q][r] = e[r];
   }
+  int kr[L];
+#pragma unroll
+  for (int m = 0; m < L; ++m) kr[m] = p.kr[t.r0 + min(16 * m + i, t.R - 1)];
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): not after the copies that follow
+  after();
+
+  constexpr int ES = C::F32OUT ? 4 : 2;
+  const StOut out = st_out((char*)p.c + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
 #pragma unroll
   for (int m = 0; m < L; ++m) {
     const int row = 16 * m + i;
-    const int kr = p.kr[t.r0 + min(row, t.R - 1)];
     f32x4 o[NH];
 #pragma unroll
     for (int q = 0; q < NH; ++q)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float a = __builtin_ldexpf(v.acc[m][q][r], -(kr + kc[q][r]));
-        if constexpr (C::GATED) o[q][r] = silu_mul(a, __builtin_ldexpf(v.acc[m][q + NT - NH][r], -(kr + kc[q + NT - NH][r])));
+        const float a = __builtin_ldexpf(v.acc[m][q][r], -(kr[m] + kc[q][r]));
+        if constexpr (C::GATED) o[q][r] = silu_mul(a, __builtin_ldexpf(v.acc[m][q + NT - NH][r], -(kr[m] + kc[q + NT - NH][r])));
         else o[q][r] = a;
       }
     if constexpr (C::F32OUT) {
@@ -411,13 +427,33 @@ template <class C>
 __global__ __launch_bounds__(64 * C::WAVES, 1) void w4_tile(W4Args p, int ntn, int bm) {
   __shared__ __attribute__((aligned(16))) char ring[C::LDS];
   const int blocks = p.offsets ? st_row_blocks(p.offsets, p.n, bm) : (p.M + bm - 1) / bm;
-  for (int L = st_first_tile(); L < blocks * ntn; L += (int)gridDim.x) {
-    const StTile t = p.offsets ? st_tile_at(L, p.offsets, p.n, ntn, bm) : st_tile_of(L, 0, p.M, blocks, ntn, bm);
-    W4Ctx<C> c;
-    w4_setup<C>(p, t, c);
-    if (t.R <= 64) w4_tile_product<C, 4>(p, t, ring, c);
-    else if (t.R <= 128) w4_tile_product<C, 8>(p, t, ring, c);
-    else w4_tile_product<C, 12>(p, t, ring, c);
+  const uint32_t lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
+  auto tile = [&](int L) {
+    return p.offsets ? st_tile_at(L, p.offsets, p.n, ntn, bm) : st_tile_of(L, 0, p.M, blocks, ntn, bm);
+  };
+  int L = st_first_tile();
+  if (L >= blocks * ntn) return;
+  W4Ctx<C> c;
+  StTile t = tile(L);
+  w4_setup<C>(p, t, c);
+  w4_begin(p, t, c, lbase);
+  for (;;) {
+    const StTile now = t;
+    L += (int)gridDim.x;
+    auto after = [&] {
+      if (L >= blocks * ntn) return;
+      t = tile(L);
+      w4_setup<C>(p, t, c);
+      w4_begin(p, t, c, lbase);
+    };
+    switch (w4_height(now.R)) {
+      case 4: w4_tile_product<C, 4>(p, now, ring, c, after); break;
+      case 6: w4_tile_product<C, 6>(p, now, ring, c, after); break;
+      case 8: w4_tile_product<C, 8>(p, now, ring, c, after); break;
+      case 10: w4_tile_product<C, 10>(p, now, ring, c, after); break;
+      default: w4_tile_product<C, 12>(p, now, ring, c, after);
+    }
+    if (L >= blocks * ntn) return;
   }
 }
 
