@@ -483,6 +483,18 @@ hipError_t launch_quantize_4bit(int n, int K, int N, int group, int dtype, const
   return hipGetLastError();
 }
 
+// The products of the parts of K, summed in their order.
+template <bool F32OUT>
+__global__ __launch_bounds__(256) void w4_join(const f32x4* __restrict__ sums, void* __restrict__ c, int64_t vecs, int parts) {
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (v >= vecs) return;
+  f32x4 a = sums[v];
+#pragma unroll 4
+  for (int s = 1; s < parts; ++s) a += sums[v + s * vecs];
+  if constexpr (F32OUT) ((f32x4*)c)[v] = a;
+  else ((u32x2*)c)[v] = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+}
+
 static W4Args w4_args(int n, int K, int N, int group) {
   W4Args p{};
   p.n = n;
@@ -491,6 +503,8 @@ static W4Args w4_args(int n, int K, int N, int group) {
   p.kb = (K + W4_KB - 1) / W4_KB;
   p.ntiles = (N + 15) / 16;
   p.groups = (K + group - 1) / group;
+  p.parts = 1;
+  p.per = p.kb;
   return p;
 }
 
@@ -502,8 +516,10 @@ static W4Plan gemm_plan(int M, int N, int K) {
 }
 
 size_t gemm_4bit_ws_bytes(int M, int N, int K) {
-  if (M == 0 || !gemm_plan(M, N, K).tiles) return 0;
-  return pad256(w4_row_bytes(M, K)) + pad256((size_t)M * 4) + pad256((size_t)N * 4);
+  const W4Plan plan = gemm_plan(M, N, K);
+  const int parts = plan.parts;
+  if (M == 0 || !plan.tiles) return 0;
+  return pad256(w4_row_bytes(M, K)) + pad256((size_t)M * 4) + pad256((size_t)N * 4) + (parts > 1 ? (size_t)parts * M * N * 4 : 0);
 }
 
 hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const void* packed, const void* scale,
@@ -526,6 +542,19 @@ hipError_t launch_gemm_4bit(int M, int N, int K, int group, const void* a, const
     p.a = rows;
     p.kr = kr;
     p.k1 = kc;
+    if (plan.parts > 1) {
+      char* sums = (char*)kc + pad256((size_t)N * 4);
+      p.parts = plan.parts;
+      p.per = plan.per;
+      p.part = (int64_t)M * N * 4;
+      p.c = sums;
+      const hipError_t t = launch_4bit_tiles_down(p, group, plan.bm, M, true, st);
+      if (t != hipSuccess) return t;
+      const int64_t vecs = (int64_t)M * N / 4;
+      auto join = out_dtype == 1 ? w4_join<false> : w4_join<true>;
+      hipLaunchKernelGGL(join, dim3((unsigned)((vecs + 255) / 256)), dim3(256), 0, st, (const f32x4*)sums, c, vecs, plan.parts);
+      return hipGetLastError();
+    }
   }
   return out_dtype == 1 ? launch_4bit<false, false>(p, plan, group, M, st) : launch_4bit<false, true>(p, plan, group, M, st);
 }

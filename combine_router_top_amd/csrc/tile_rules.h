@@ -203,37 +203,67 @@ struct W4Shape {
   int64_t mean, all, most;
 };
 struct W4Plan {
-  bool tiles;    // w4_tile, else w4_stream
-  int bm;        // tiles: rows of a block, a multiple of 64 up to 192
-  bool wide;     // stream: four column tiles of 16 a workgroup, else one (gated: of each matrix)
-  bool low;      // stream: 16 rows at a time, else 32
-  int blocks;    // stream: workgroups that a segment's blocks of rows are dealt out to
+  bool tiles;        // w4_tile, else w4_stream
+  int bm;            // tiles: rows of a block, a multiple of 64 up to 192
+  int parts, per;    // tiles of a single product: parts of K, blocks of 128 K in each
+  bool wide;         // stream: four column tiles of 16 a workgroup, else one (gated: of each matrix)
+  bool low;          // stream: 16 rows at a time, else 32
+  int blocks;        // stream: workgroups that a segment's blocks of rows are dealt out to
 };
 
+// What the kernels take, in us, by what they measured, all with K x N, rows:
+//   - a wide stream workgroup takes 0.6 us for each 4 blocks of 128 K, 0.034 a row from 18
+//     rows on; a narrow one 0.9 and 0.4 + 0.047 a row for each 8 blocks.  There is one at a time
+//     on a compute unit.  Weights in bulk 5.2 and 4 TB/s.  (wide, narrow: 4096 x 14336, 1: 9.5, 13.4; 16: 9.9,
+//     20.6; 32: 13.7, 36.6; 7168 x 2048, 1: 11.2, 5.9; 32: 18.1, 16.7; 2048 x 7168, 1: 5.6, 4.9; 16: 5.8,
+//     7.5; 14336 x 4096, 64: 34, 58; 32 experts of
+//     7168 x 2048, 2 rows each, whole call: 111, 137)
+//   - a tile of 64 h rows takes 0.72 + 0.5 h for each block and 2.5 more; preparing the rows 6
+//     and what their bytes take.  (64, 128, 192 rows a tile: 4096 x 14336, 256: 50, 62, 71; 512: 91, 67,
+//     75; 2048: 288, 238, 233)
+//   - K in parts, where tiles leave compute units idle: 3 more and the bytes of their sums.
 inline W4Plan w4_plan(int64_t cus, const W4Shape& p) {
   W4Plan r{};
   const int64_t act = std::min<int64_t>(p.n, std::max<int64_t>(1, p.all));   // experts with rows
   const int64_t seg = std::max<int64_t>(1, p.segments && p.n > 1 ? p.mean + p.mean / 4 : p.mean);
   const double mb = act * (p.kb * 1024e-6) * ((p.N + 15) / 16) * (p.gated ? 2 : 1);
+  const double kept = std::max<double>(1, p.segments ? (double)p.all : (double)p.mean);   // rows in all
   const int64_t cols = (p.N + (p.gated ? 127 : 255)) / (p.gated ? 128 : 256);
   auto rounds = [&](int64_t wgs) { return (double)((wgs + cus - 1) / cus); };
-  // tiles: a block of 128 K takes 0.6 us and 0.33 for each 64 rows, a tile about 6 us more,
-  // the preparation of the rows 6
   double tiles = 0;
+  const double rows_us = 6 + kept * p.kb * (128 * 4e-6 / 4);
   for (int h = 3; h >= 1; --h) {
     const int64_t full = seg / (64 * h), rest = (seg % (64 * h) + 63) / 64;
-    const double us = std::max(mb / 5.2, rounds(act * (full + (rest ? 1 : 0)) * cols) * (p.kb * (0.6 + 0.33 * h) + 6)) + 6;
-    if (!r.bm || us < tiles) {
-      r.bm = 64 * h;
-      tiles = us;
+    const int64_t wgs = act * (full + (rest ? 1 : 0)) * cols;
+    for (int parts = 1; parts <= 16; parts *= 2) {
+      if (parts > 1 && (p.segments || wgs * parts > cus || p.kb < 4 * parts)) break;
+      const int per = (p.kb + parts - 1) / parts, used = (p.kb + per - 1) / per;
+      double us = std::max(mb / 5.2, rounds(wgs * used) * (per * (0.72 + 0.5 * h) + 2.5)) + rows_us;
+      if (used > 1) us += 3 + (used + 1) * kept * p.N * (4e-6 / 4);
+      if (!r.bm || us < tiles) {
+        r.bm = 64 * h;
+        r.parts = used;
+        r.per = per;
+        tiles = us;
+      }
     }
   }
-  r.wide = (int64_t)((p.N + (p.gated ? 31 : 63)) / (p.gated ? 32 : 64)) * p.n >= cus;
+  // stream: passes of 32 rows, the last of up to 16 or 32
   r.low = p.most <= 16 || p.mean <= 8;
-  const int64_t rows = r.low ? 16 : 32, passes = (seg + rows - 1) / rows;
-  r.blocks = (int)std::min<int64_t>((p.most + rows - 1) / rows, p.segments ? 4 : 1024);
-  const double stream = 4 + passes * std::max(mb / (r.low ? 5.2 : 3.2), 0.02 * p.kb);
-  r.tiles = stream > tiles;
+  const int64_t pass = r.low ? 16 : 32, passes = (seg + pass - 1) / pass;
+  r.blocks = (int)std::min<int64_t>((p.most + pass - 1) / pass, p.segments ? 4 : 1024);
+  auto stream = [&](bool wide) {
+    const int64_t per = wide ? (p.gated ? 32 : 64) : 16, wgs = act * ((p.N + per - 1) / per);
+    const int64_t last = seg - (passes - 1) * pass;
+    auto block = [&](int64_t rows) { return wide ? std::max(0.6, 0.034 * (double)rows) : 0.4 + 0.047 * (double)rows; };
+    const double steps = (double)((p.kb + (wide ? 3 : 7)) / (wide ? 4 : 8)), more = wide ? 0 : 0.9;
+    const double work = ((passes - 1) * block(pass) + block(last)) * steps + more * (double)passes;
+    const double one = block(std::min(seg, pass)) * steps + more;
+    return (wide ? 3 : 1.3) + std::max(mb / (wide ? 5.2 : 4), std::max(one, work * (double)wgs / (double)cus));
+  };
+  const double narrow = stream(false), wide = stream(true);
+  r.wide = wide < narrow;
+  r.tiles = std::min(wide, narrow) > tiles;
   return r;
 }
 

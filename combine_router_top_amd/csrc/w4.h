@@ -28,6 +28,8 @@ struct W4Args {
   const int32_t* kr;       // tiles: exponents of the rows and of the columns [n][N]
   const int32_t* k1;
   const int32_t* k3;
+  int parts, per;          // tiles: parts of K, and blocks of 128 K of each (the last may have fewer)
+  int64_t part;            // bytes between the parts' products
 };
 
 __device__ __forceinline__ int w4_rows(const W4Args& p, int e, int& o) {

@@ -85,6 +85,11 @@ __device__ __forceinline__ W4Piece w4_piece(int at) {
   return q;
 }
 
+// A tile: rows and columns, and the blocks of 128 K that are multiplied.
+struct W4Tile : StTile {
+  int b0, nb, part;   // first block, their number, which part of K that is
+};
+
 // What a wave copies of the weights of a tile.
 template <class C>
 struct W4Ctx {
@@ -104,14 +109,14 @@ __device__ __forceinline__ const char* w4_scalar(const char* p) {   // descripto
 }
 
 template <class C>
-__device__ __forceinline__ void w4_setup(const W4Args& p, const StTile& t, W4Ctx<C>& c) {
+__device__ __forceinline__ void w4_setup(const W4Args& p, const W4Tile& t, W4Ctx<C>& c) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t run = (uint32_t)p.kb * 1024u;
   const int first = C::COLS / 16 * t.nt, most = p.ntiles - 1 - first;
-  const int64_t eo = ((int64_t)t.e * p.ntiles + first) * run;
+  const int64_t eo = ((int64_t)t.e * p.ntiles + first) * run + 1024 * t.b0;
   c.w[0] = w4_scalar(p.b1 + eo);
   c.w[1] = w4_scalar((C::GATED ? p.b3 : p.b1) + eo);
-  c.wsize = __builtin_amdgcn_readfirstlane((uint32_t)min((int64_t)(most + 1) * run, (int64_t)UINT32_MAX));
+  c.wsize = __builtin_amdgcn_readfirstlane((uint32_t)min((int64_t)(most + 1) * run, (int64_t)UINT32_MAX) - 1024u * (uint32_t)t.b0);
 #pragma unroll
   for (int v = 0; v < C::WB; ++v) {   // packed tiles wave, wave + 4, .. (gated: the second half of the second matrix)
     const int at = wave + C::WAVES * v;
@@ -124,7 +129,7 @@ __device__ __forceinline__ void w4_setup(const W4Args& p, const StTile& t, W4Ctx
     const bool m = C::GATED && q.hm;
     const uint8_t* zp = m ? p.z3 : p.z1;
     const uint32_t row = (uint32_t)p.N * (q.zero ? 1u : 2u);   // bytes of a group
-    const uint32_t skip = row * (uint32_t)q.u + (C::GATED || q.zero ? 0u : 256u * (uint32_t)q.hm);
+    const uint32_t skip = row * (uint32_t)(q.u + t.b0 * C::GPB) + (C::GATED || q.zero ? 0u : 256u * (uint32_t)q.hm);
     const uint32_t size = q.zero && !zp ? 0u : (uint32_t)p.groups * row - (uint32_t)(C::COLS * t.nt) * (q.zero ? 1u : 2u);
     c.s[v] = w4_scalar((q.zero ? (const char*)(zp + go) : (const char*)((m ? p.s3 : p.s1) + go)) + skip);
     c.ssize[v] = __builtin_amdgcn_readfirstlane(size > skip ? size - skip : 0u);
@@ -162,12 +167,13 @@ template <int X>
 struct W4Rows {
   const char* base;
   uint32_t voff[X], size;
-  __device__ __forceinline__ void of(const bf16_t* a, uint32_t ld, int rows) {
+  __device__ __forceinline__ void of(const W4Args& p, const W4Tile& t, int rows) {
+    const uint32_t ld = (uint32_t)p.kb * (2 * W4_KB);   // bytes of a row
     const int r = 8 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + ((threadIdx.x & 63) >> 3);
-    base = w4_scalar((const char*)a);
+    base = w4_scalar((const char*)(p.a + (int64_t)t.r0 * (p.kb * W4_KB) + t.b0 * W4_KB));
 #pragma unroll
     for (int c = 0; c < X; ++c) voff[c] = (uint32_t)(r + 32 * c) * ld + 16u * (uint32_t)((threadIdx.x & 7) ^ ((r >> 1) & 7));
-    size = __builtin_amdgcn_readfirstlane((uint32_t)rows * ld);
+    size = __builtin_amdgcn_readfirstlane((uint32_t)rows * ld - 2u * W4_KB * (uint32_t)t.b0);
   }
   __device__ __forceinline__ void issue(uint32_t slot, int st, int c) const {   // slot: of this wave
     w4_copy<16>(gc_rsrc(base, size), slot + 1024 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), 4096 * c, voff[c],
@@ -189,11 +195,11 @@ __device__ __forceinline__ int w4_height(int rows) { return rows <= 64 ? 4 : min
 
 // The first copies of a tile: two blocks of the weights, three steps of the rows.
 template <class C>
-__device__ __forceinline__ void w4_begin(const W4Args& p, const StTile& t, const W4Ctx<C>& c, uint32_t lbase) {
+__device__ __forceinline__ void w4_begin(const W4Args& p, const W4Tile& t, const W4Ctx<C>& c, uint32_t lbase) {
   const uint32_t ld = (uint32_t)p.kb * (2 * W4_KB);
   const int X = w4_height(t.R) / 2;
   W4Rows<1> x;
-  x.of(p.a + (int64_t)t.r0 * (p.kb * W4_KB), ld, t.R);
+  x.of(p, t, t.R);
   const __amdgpu_buffer_rsrc_t r = gc_rsrc(x.base, x.size);
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
@@ -311,15 +317,14 @@ struct W4Wave {
 // Product of a tile whose first copies are under way; `after` begins the next one, once the
 // ring is free, before this one's stores.
 template <class C, int L, class After>
-__device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile t, char* ring, const W4Ctx<C>& c,
+__device__ __forceinline__ void w4_tile_product(const W4Args& p, const W4Tile t, char* ring, const W4Ctx<C>& c,
                                                 const After& after) {
   constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, X = L / 2;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
-  const uint32_t ld = (uint32_t)p.kb * (2 * W4_KB);   // bytes of a row
   W4Rows<X> xr;
-  xr.of(p.a + (int64_t)t.r0 * (p.kb * W4_KB), ld, min(t.R, 16 * L));
+  xr.of(p, t, min(t.R, 16 * L));
   W4Wave<C, L> v;
   v.xo = st_lane<ST_ROWS>(0);
   v.at0 = NH * wave;
@@ -350,7 +355,7 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile t,
   for (int h = 0; h < 2 * NT * v.PARTS; ++h) v.part(0, 0, h);
   uint32_t x0 = 0, x1 = C::XSLOT, x2 = 2 * C::XSLOT;   // slots of this step, the next and the one after
   uint32_t wo = 0;                                     // offset of this block's slot
-  for (int b = 0; b < p.kb; ++b) {
+  for (int b = 0; b < t.nb; ++b) {
     ws = ring + C::WOFF + wo;
     auto nothing = [](auto...) {};
     if (GPB == 4) v.read_scales(ws, 1);
@@ -394,7 +399,7 @@ __device__ __forceinline__ void w4_tile_product(const W4Args& p, const StTile t,
   after();
 
   constexpr int ES = C::F32OUT ? 4 : 2;
-  const StOut out = st_out((char*)p.c + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
+  const StOut out = st_out((char*)p.c + t.part * p.part + (int64_t)t.r0 * p.N * ES, (int64_t)p.N * ES, t.R);
 #pragma unroll
   for (int m = 0; m < L; ++m) {
     const int row = 16 * m + i;
@@ -428,20 +433,27 @@ __global__ __launch_bounds__(64 * C::WAVES, 1) void w4_tile(W4Args p, int ntn, i
   __shared__ __attribute__((aligned(16))) char ring[C::LDS];
   const int blocks = p.offsets ? st_row_blocks(p.offsets, p.n, bm) : (p.M + bm - 1) / bm;
   const uint32_t lbase = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(dt_lds_t*)ring);
+  const int tiles = blocks * ntn, total = tiles * p.parts;
   auto tile = [&](int L) {
-    return p.offsets ? st_tile_at(L, p.offsets, p.n, ntn, bm) : st_tile_of(L, 0, p.M, blocks, ntn, bm);
+    W4Tile t;
+    t.part = p.parts > 1 ? st_div(L, tiles) : 0;
+    L -= t.part * tiles;
+    static_cast<StTile&>(t) = p.offsets ? st_tile_at(L, p.offsets, p.n, ntn, bm) : st_tile_of(L, 0, p.M, blocks, ntn, bm);
+    t.b0 = t.part * p.per;
+    t.nb = min(p.per, p.kb - t.b0);
+    return t;
   };
   int L = st_first_tile();
-  if (L >= blocks * ntn) return;
+  if (L >= total) return;
   W4Ctx<C> c;
-  StTile t = tile(L);
+  W4Tile t = tile(L);
   w4_setup<C>(p, t, c);
   w4_begin(p, t, c, lbase);
   for (;;) {
-    const StTile now = t;
+    const W4Tile now = t;
     L += (int)gridDim.x;
     auto after = [&] {
-      if (L >= blocks * ntn) return;
+      if (L >= total) return;
       t = tile(L);
       w4_setup<C>(p, t, c);
       w4_begin(p, t, c, lbase);
@@ -453,7 +465,7 @@ __global__ __launch_bounds__(64 * C::WAVES, 1) void w4_tile(W4Args p, int ntn, i
       case 10: w4_tile_product<C, 10>(p, now, ring, c, after); break;
       default: w4_tile_product<C, 12>(p, now, ring, c, after);
     }
-    if (L >= blocks * ntn) return;
+    if (L >= total) return;
   }
 }
 
@@ -461,7 +473,7 @@ template <bool GATED, bool F32OUT, int GPB, bool ZERO>
 static hipError_t launch_w4_tile(const W4Args& p, int bm, int64_t rows_max, hipStream_t st) {
   using C = W4Cfg<GPB, ZERO, GATED, F32OUT>;
   const int ntn = (p.N + C::COLS - 1) / C::COLS;
-  hipLaunchKernelGGL(w4_tile<C>, st_row_grid(rows_max, p.n, bm / 64, ntn), dim3(64 * C::WAVES), 0, st, p, ntn, bm);
+  hipLaunchKernelGGL(w4_tile<C>, st_row_grid(rows_max, p.n, bm / 64, ntn * p.parts), dim3(64 * C::WAVES), 0, st, p, ntn, bm);
   return hipGetLastError();
 }
 
