@@ -211,17 +211,19 @@ struct W4Plan {
   int blocks;        // stream: workgroups that a segment's blocks of rows are dealt out to
 };
 
-// What the kernels take, in us, by what they measured, all with K x N, rows:
-//   - a wide stream workgroup takes 0.6 us for each 4 blocks of 128 K, 0.034 a row from 18
-//     rows on; a narrow one 0.9 and 0.4 + 0.047 a row for each 8 blocks.  There is one at a time
-//     on a compute unit.  Weights in bulk 5.2 and 4 TB/s.  (wide, narrow: 4096 x 14336, 1: 9.5, 13.4; 16: 9.9,
-//     20.6; 32: 13.7, 36.6; 7168 x 2048, 1: 11.2, 5.9; 32: 18.1, 16.7; 2048 x 7168, 1: 5.6, 4.9; 16: 5.8,
-//     7.5; 14336 x 4096, 64: 34, 58; 32 experts of
-//     7168 x 2048, 2 rows each, whole call: 111, 137)
-//   - a tile of 64 h rows takes 0.72 + 0.5 h for each block and 2.5 more; preparing the rows 6
-//     and what their bytes take.  (64, 128, 192 rows a tile: 4096 x 14336, 256: 50, 62, 71; 512: 91, 67,
-//     75; 2048: 288, 238, 233)
-//   - K in parts, where tiles leave compute units idle: 3 more and the bytes of their sums.
+// What the kernels take, in us, by what they measured (K x N, rows: us of either side):
+//   - wide stream: 2.4, and a workgroup 0.6 and, for each 4 blocks of 128 K, 0.6 or 0.034 a row;
+//     narrow: 1.3, and 0.9 and, for each 8 blocks, 0.4 + 0.047 a row.  One workgroup at a time on
+//     a compute unit; weights in bulk 5.2 and 4 TB/s.  Wide, narrow: 4096 x 14336, 1: 9.5, 13.4;
+//     16: 9.9, 20.6; 32: 13.7, 36.6; 7168 x 2048, 1: 11.2, 5.9; 32: 18.1, 16.7; 2048 x 7168, 1: 5.6,
+//     4.9; 16: 5.8, 7.5; 14336 x 4096, 64: 34, 58; 32 experts of 7168 x 2048 with 2 rows each, the
+//     whole call: 111, 137.
+//   - tiles: 0.72 + 0.5 h for each block of a tile of 64 h rows and 2.5 more; the rows'
+//     preparation 6 and its bytes.  64, 128, 192 rows: 4096 x 14336, 256: 50, 62, 71; 512: 91,
+//     67, 75; 2048: 288, 238, 233.  Wide stream and tiles: 1024 x 1024, 2048: 15, 22; 4096: 26,
+//     25; 8192: 47, 33; 368 x 5824, 256: 9.9, 12.4; 512: 15.4, 13.1.
+//   - K in parts: 3 more and the bytes of their sums.  One part, several: 7168 x 2048, 256: 74,
+//     19; 512: 75, 33.
 inline W4Plan w4_plan(int64_t cus, const W4Shape& p) {
   W4Plan r{};
   const int64_t act = std::min<int64_t>(p.n, std::max<int64_t>(1, p.all));   // experts with rows
@@ -256,10 +258,10 @@ inline W4Plan w4_plan(int64_t cus, const W4Shape& p) {
     const int64_t per = wide ? (p.gated ? 32 : 64) : 16, wgs = act * ((p.N + per - 1) / per);
     const int64_t last = seg - (passes - 1) * pass;
     auto block = [&](int64_t rows) { return wide ? std::max(0.6, 0.034 * (double)rows) : 0.4 + 0.047 * (double)rows; };
-    const double steps = (double)((p.kb + (wide ? 3 : 7)) / (wide ? 4 : 8)), more = wide ? 0 : 0.9;
+    const double steps = (double)((p.kb + (wide ? 3 : 7)) / (wide ? 4 : 8)), more = wide ? 0.6 : 0.9;
     const double work = ((passes - 1) * block(pass) + block(last)) * steps + more * (double)passes;
     const double one = block(std::min(seg, pass)) * steps + more;
-    return (wide ? 3 : 1.3) + std::max(mb / (wide ? 5.2 : 4), std::max(one, work * (double)wgs / (double)cus));
+    return (wide ? 2.4 : 1.3) + std::max(mb / (wide ? 5.2 : 4), std::max(one, work * (double)wgs / (double)cus));
   };
   const double narrow = stream(false), wide = stream(true);
   r.wide = wide < narrow;
