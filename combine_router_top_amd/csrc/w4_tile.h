@@ -1,36 +1,37 @@
-// Tiles of the 4-bit products (gfx950): up to 256 rows x 256 columns (gated: 128 of each
-// matrix), 8 waves in a 2 x 4 grid.
+// Tiles of the 4-bit products (gfx950): up to 192 rows x 256 columns (gated: 128 of each
+// matrix), four waves, one on each SIMD, each with all rows of 64 columns.
 //
-// On this part a wave's vector instructions do not run beside its matrix instructions,
-// nor beside those of the other wave of its SIMD: a 16 x 16 x 32 product takes 7.1 ns of a
-// SIMD and a vector instruction about 1.0, one after the other.  So what counts is how few
-// of the latter there are for each product.  The tiles therefore work in fp16, where a
-// weight is made complete before it is multiplied, and no sum is scaled later:
-//   - rows come with a power of two that puts their largest value in 2^14 .. 2^15, so
-//     that every bf16 value within 2^-29 of it is exact in fp16 (smaller ones are off by
-//     at most 2^-40 of it); scales likewise, by columns, with their largest in
-//     2^10 .. 2^11.  The epilogue takes both powers out again.
+// What bounds them is how much else than matrix products a wave issues, and the power the
+// products draw: a 16 x 16 x 32 product takes 9 to 10 ns of a SIMD under load, one vector
+// instruction beside it is nearly free, each further one of the same wave costs 1 to 2 ns
+// (products alone 380 us of 4096 x 4096 x 14336, the whole tile kernel 410 to 490 us, by how
+// long it has run, where 563 us were taken by eight waves of 96 x 64, which make every weight
+// twice).  So:
+//   - the tiles work in fp16, where a weight is made complete before it is multiplied, and no
+//     sum is scaled later.  Rows come with a power of two that puts their largest value in
+//     2^14 .. 2^15: every bf16 value within 2^-31 of it is exact in fp16, smaller ones are off by
+//     less than 2^-38 of it.  Scales likewise, by columns, with their largest in 2^10 .. 2^11:
+//     exact within 2^-27 of it, else off by less than 2^-34 of it.  The epilogue takes both
+//     powers out again.
 //   - without zero points, q becomes the fp16 number 16 + q by one masked or (two values),
 //     and one packed fma with s and -24 s gives (q - 8) s: exactly, since 8-bit scales times
 //     -8 .. 7 and times 24 fit fp16's 11 bits.  With zero points, 128 + q, an exact
-//     subtraction and a product, which rounds odd multiples above 8 to 11 bits (by
-//     2^-12 relative, once per weight; a bf16 output is rounded sixteen times as coarsely).
-// An operand of 8 weights costs 12 (15) instructions and serves up to 8 row tiles.
+//     subtraction and a product, which rounds odd multiples above 8 to 11 bits (by up to
+//     2^-11 relative, once per weight; a bf16 output is rounded by up to 2^-8).
+//   - an operand of 8 weights costs 12 (15) instructions and serves all row tiles, and these
+//     instructions, the copies and the reads are dealt out between the products.
 //
-// Wave (wm, wn) = (w & 1, w >> 1) has the row tiles 2 m + wm, m < L, so that a short tile's
-// rows are shared evenly, and four column tiles.  L (2, 4, 6, 8) is chosen for each tile by
-// its actual rows.  K runs in steps of 64: rows in a ring of three slots, packed blocks of
-// 128 K with their scales in a ring of two, all copied from memory straight into LDS.
-// While a k-step of 32 is multiplied, the operands of the next are made, and a row
-// fragment's registers take its successor as soon as they are free.  One barrier per step,
-// in its middle: by then every wave holds the step's second half.
+// Heights are 64, 96, 128, 160 or 192 rows, for each tile by its actual rows.  K runs in steps of
+// 64: rows in a ring of three slots, packed blocks of 128 K with their scales in a ring of two,
+// all copied from memory straight into LDS.  While a k-step of 32 is multiplied, the operands of
+// the next are made, and a row fragment's registers take its successor as soon as they are
+// free.  One barrier per step, once the first products of its second half are under way: by
+// then every wave holds that half.  The next tile's first copies are issued before this
+// one's stores.
 #pragma once
 
 #include "w4.h"
 
-#ifndef W4_S0
-#define W4_S0 (L > 4)
-#endif
 namespace moe {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -285,7 +286,7 @@ struct W4Wave {
   template <int Q, bool SCALES, int COPIES, class Sync, class Copy>
   __device__ __forceinline__ void kstep(const char* next, int ks, const Sync& sync, const Copy& copy) {
     constexpr int b = Q & 1, n = (Q + 1) & 3;
-    constexpr int S0 = W4_S0, MS = S0 + 1 + (L > 8), M0 = MS + 1, M1 = L - (L > 4);
+    constexpr int S0 = L > 4, MS = S0 + 1 + (L > 8), M0 = MS + 1, M1 = L - (L > 4);
     constexpr int H = 2 * PARTS * NT, A = M0 * NT, B = M1 * NT;   // halves, and the products beside which they are made
 #pragma unroll
     for (int m = 0; m < L; ++m) {

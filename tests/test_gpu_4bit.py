@@ -65,12 +65,13 @@ def _slack(x, s, z, G, w):
     terms of up to 31 |x| each, (16 + z) X is one more rounding; then two per group and the
     waves' join.  Many rows: one sum of x W, K / 32 products of 32 terms (K / 32 + 36 roundings
     cover both), whose weights are exact without zero points and otherwise rounded to 11 bits
-    where |q - z| is odd and above 8."""
+    where |q - z| is odd and above 8: (q - z) s is a whole number of at most 15 * 255 < 2^12 times a
+    power of two, so from 2^11 on, where not every one has 11 bits, it moves by at most 1, 2^-11 of it."""
     K = x.shape[1]
     per = s.double().abs().repeat_interleave(G, 0)[:K]
     size = x.abs() @ w.abs()
     few = (2 * min(G, K) + 4) * EPS * 31 * (x.abs() @ per) + (2 * s.shape[0] + 20) * EPS * size
-    return few + (K / 32 + 36) * EPS * size + (0 if z is None else 2.0 ** -12) * size
+    return few + (K / 32 + 36) * EPS * size + (0 if z is None else 2.0 ** -11) * size
 
 
 @pytest.mark.parametrize("K,N", [(8, 8), (32, 16), (40, 24), (128, 16), (136, 40), (1000, 56)])
