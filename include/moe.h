@@ -515,10 +515,13 @@ moe_status_t moe_quantize_weights_fourbit(int32_t n, int32_t K, int32_t N, int32
 
 /*
  * Product with 4-bit weights: C = rnd(A W), W one matrix [K,N] as above, with fp32
- * accumulation.  No weight is rounded, except that products of many rows take odd multiples
- * |q - zero| above 8 of a scale rounded to 11 bits (2^-12 relative), and scales 2^-25 below
- * the largest of their column with fewer.  A row of A with an infinity or a NaN gives a row
- * of NaN, a NaN scale a column of NaN, and neither reaches others.
+ * accumulation.  Which kernel runs goes by the sizes, so a row's result may differ in its last
+ * bits with the number of rows beside it.  For few rows nothing is rounded but the sums; for
+ * many, odd multiples |q - zero| above 8 of a scale are rounded to 11 bits where there are zero
+ * points (by up to 2^-11), values of A more than 2^-31 below the largest of their row to multiples of
+ * 2^-38 of it, scales more than 2^-27 below the largest of their column to multiples of 2^-34 of it.
+ * A row of A with an infinity or a NaN gives a row of NaN, a NaN scale a column of NaN, and
+ * neither reaches others.
  *   A [M,K] bf16 row-major, 16-byte aligned;  C [M,N] of out_dtype, 16-byte aligned,
  *   overlaps none of the others.  M = 0 launches nothing; M at most 2^30.
  *   workspace of moe_gemm_fourbit_workspace_bytes(M, N, K) bytes (0 for few rows, or for
