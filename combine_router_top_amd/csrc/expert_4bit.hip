@@ -310,12 +310,18 @@ static hipError_t launch_4bit_stream(const W4Args& p, const W4Plan& plan, hipStr
                        0, st, p);
     return hipGetLastError();
   };
-  constexpr int NT = GATED ? 2 : 1;
+  constexpr int NT = GATED ? 2 : 1, WIDE = GATED ? 32 : 64;
+  if constexpr (!GATED)
+    if (plan.ahead)
+      return plan.low ? go(w4_stream<1, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, WIDE, 4)
+                      : go(w4_stream<2, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, WIDE, 4);
+  if (plan.wide)
+    return plan.low ? go(w4_stream<1, 4, GATED, F32OUT, 8, GPB, ZERO, 1>, WIDE, 8)
+                    : go(w4_stream<2, 4, GATED, F32OUT, 4, GPB, ZERO, 1>, WIDE, 4);
   if (plan.low)
-    return plan.wide ? go(w4_stream<1, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, GATED ? 32 : 64, 4)
-                     : go(w4_stream<1, NT, GATED, F32OUT, 8, GPB, ZERO, 2>, 16, 8);
-  return plan.wide ? go(w4_stream<2, 4, GATED, F32OUT, 4, GPB, ZERO, 2>, GATED ? 32 : 64, 4)
-                   : go(w4_stream<2, NT, GATED, F32OUT, 8, GPB, ZERO, 2>, 16, 8);
+    return plan.waves == 16 ? go(w4_stream<1, NT, GATED, F32OUT, 16, GPB, ZERO, 1>, 16, 16)
+                            : go(w4_stream<1, NT, GATED, F32OUT, 8, GPB, ZERO, 1>, 16, 8);
+  return go(w4_stream<2, NT, GATED, F32OUT, 8, GPB, ZERO, 1>, 16, 8);
 }
 
 // What a plan says, for the shape it was made for.

@@ -209,6 +209,8 @@ struct W4Plan {
   bool wide;         // stream: four column tiles of 16 a workgroup, else one (gated: of each matrix)
   bool low;          // stream: 16 rows at a time, else 32
   int blocks;        // stream: workgroups that a segment's blocks of rows are dealt out to
+  int waves;         // stream: waves of a workgroup, among which K is dealt out
+  bool ahead;        // stream: a wave loads its next block of K before it multiplies one
 };
 
 // What the kernels take, in us, by what they measured (K x N, rows: us of either side):
@@ -266,6 +268,15 @@ inline W4Plan w4_plan(int64_t cus, const W4Shape& p) {
   const double narrow = stream(false), wide = stream(true);
   r.wide = wide < narrow;
   r.tiles = std::min(wide, narrow) > tiles;
+  // With several workgroups for each compute unit the waves beside one another hide its
+  // loads, and registers for a block in advance only keep waves out (32 experts of 7168 x 2048,
+  // 4 rows each: 4 waves with it 140 us, 8 without 126; 24 rows: 224, 222; 16 of 2048 x 768, 24 rows:
+  // 25.6, 23.5); with one it pays (4096 x 14336, 8 rows: 9.5, 12.5; 24 rows: 12.6, 18.8).
+  const int64_t wgs = (p.N + 63) / 64 * (int64_t)r.blocks;
+  r.ahead = r.wide && !p.segments && wgs <= cus && p.kb > 4;
+  // narrow ones for up to 16 rows take 16 waves where K lasts (7168 x 2048, one row: 8 waves 6.4 us, 16
+  // 5.6; 8 experts of 512 x 512: 8.0, 8.9)
+  r.waves = r.wide ? (r.low && !r.ahead ? 8 : 4) : r.low && p.kb >= 32 ? 16 : 8;
   return r;
 }
 

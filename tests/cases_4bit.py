@@ -3,12 +3,14 @@ library's rules say of them).  tests/test_4bit_choice.py holds the two together.
 
 # M, K, N, group; what tests/rules_4bit.py's plan has
 PRODUCTS = {
-    "narrow, 16 rows": ((5, 136, 24, 32), dict(tiles=False, wide=False, low=True, blocks=1)),
-    "narrow, long": ((9, 4104, 72, 64), dict(tiles=False, wide=False, low=True, blocks=1)),
+    "narrow, 16 rows": ((5, 136, 24, 32), dict(tiles=False, wide=False, low=True, waves=8)),
+    "narrow, long": ((9, 4104, 72, 64), dict(tiles=False, wide=False, low=True, waves=16)),
     "narrow, 32 rows": ((24, 520, 40, 128), dict(tiles=False, wide=False, low=False, blocks=1)),
     "narrow, blocks of rows": ((50, 2056, 136, 64), dict(tiles=False, wide=False, low=False, blocks=2)),
-    "wide, 16 rows": ((7, 264, 8200, 128), dict(tiles=False, wide=True, low=True, blocks=1)),
-    "wide, 32 rows": ((30, 392, 8200, 32), dict(tiles=False, wide=True, low=False, blocks=1)),
+    "wide, 16 rows": ((7, 264, 8200, 128), dict(tiles=False, wide=True, low=True, ahead=False, waves=8)),
+    "wide, 32 rows": ((30, 392, 8200, 32), dict(tiles=False, wide=True, low=False, ahead=False, waves=4)),
+    "wide, 16 rows, a block ahead": ((6, 1032, 8200, 64), dict(tiles=False, wide=True, low=True, ahead=True, waves=4)),
+    "wide, 32 rows, a block ahead": ((20, 1160, 8200, 32), dict(tiles=False, wide=True, low=False, ahead=True, waves=4)),
     "wide, blocks of rows": ((100, 264, 1032, 64), dict(tiles=False, wide=True, low=False, blocks=4)),
     "tiles of 64, one block": ((1092, 8, 2056, 32), dict(tiles=True, bm=64, parts=1)),
     "tiles of 64": ((286, 520, 8200, 128), dict(tiles=True, bm=64, parts=1)),

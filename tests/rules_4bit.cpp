@@ -12,4 +12,6 @@ extern "C" void rules_w4(int64_t cus, int gated, int segments, int n, int N, int
   out[4] = p.wide;
   out[5] = p.low;
   out[6] = p.blocks;
+  out[7] = p.waves;
+  out[8] = p.ahead;
 }

@@ -18,6 +18,8 @@ class Plan(NamedTuple):
     wide: bool
     low: bool
     blocks: int
+    waves: int
+    ahead: bool
 
 
 @functools.lru_cache(None)
@@ -28,11 +30,11 @@ def _lib():
 
 
 def _plan(gated, segments, n, N, K, mean, rows, most):
-    out = (ctypes.c_int64 * 7)()
+    out = (ctypes.c_int64 * 9)()
     i64 = ctypes.c_int64
     _lib().rules_w4(i64(CUS), gated, segments, n, N, -(-K // 128), i64(mean), i64(rows), i64(most), out)
     p = Plan(*out)
-    return p._replace(tiles=bool(p.tiles), wide=bool(p.wide), low=bool(p.low))
+    return p._replace(tiles=bool(p.tiles), wide=bool(p.wide), low=bool(p.low), ahead=bool(p.ahead))
 
 
 def product(M, K, N):

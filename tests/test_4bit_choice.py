@@ -29,7 +29,9 @@ def test_experts(name):
 
 def test_every_kernel_has_a_case():
     plans = [(R.product(*s[:3]), s) for s, _ in C.PRODUCTS.values()]
-    assert {(p.wide, p.low) for p, _ in plans if not p.tiles} == {(w, l) for w in (False, True) for l in (False, True)}
+    assert {(p.wide, p.low, p.waves, p.ahead) for p, _ in plans if not p.tiles} == {
+        (False, True, 8, False), (False, True, 16, False), (False, False, 8, False), (True, True, 8, False),
+        (True, False, 4, False), (True, True, 4, True), (True, False, 4, True)}
     for wide in (False, True):
         assert {s[3] for p, s in plans if not p.tiles and p.wide == wide} == {32, 64, 128}
     tiles = [(p, s) for p, s in plans if p.tiles]
