@@ -721,13 +721,15 @@ def expert_gemm_quantized(p: Spec, x_packed, offsets, w1, s1, w3, s3, w2, s2, wo
 # ---------------------------------------------------------------------------
 # scored routing
 # ---------------------------------------------------------------------------
-def _choice_out(p, device, out, stream):
-    torch = _torch()
+def _choice_out(cur, p, like, out, stream):
+    """(topk_idx, topk_w) of ``out``, or new ones beside ``like``, and their addresses."""
+    torch, slots = _torch(), (p.T, p.k)
     if out is None:
         with _alloc_on(stream):
-            out = (torch.empty((p.T, p.k), dtype=torch.int32, device=device),
-                   torch.empty((p.T, p.k), dtype=torch.float32, device=device))
-    return out
+            idx, w = like.new_empty(slots, dtype=torch.int32), like.new_empty(slots, dtype=torch.float32)
+        return idx, w, idx.data_ptr(), w.data_ptr()
+    idx, w = out
+    return idx, w, _at(cur, idx, slots, torch.int32, "topk_idx"), _at(cur, w, slots, torch.float32, "topk_w")
 
 
 def select(p: Spec, gate: Gate, logits, balance=None, stream=None, out=None):
@@ -737,9 +739,8 @@ def select(p: Spec, gate: Gate, logits, balance=None, stream=None, out=None):
     cur, slots, f32 = _current(), (p.T, p.k), torch.float32
     pl = _at(cur, logits, (p.T, p.E), f32, "logits")
     pb = None if balance is None else _at(cur, balance, (p.E,), f32, "balance")
-    idx, w = _choice_out(p, logits.device, out, stream)
-    _check(lib().moe_select(p.ref(), gate.ref(), pl, pb, _at(cur, idx, slots, torch.int32, "topk_idx"),
-                            _at(cur, w, slots, f32, "topk_w"), _stream_at(cur, stream)))
+    idx, w, pi, pw = _choice_out(cur, p, logits, out, stream)
+    _check(lib().moe_select(p.ref(), gate.ref(), pl, pb, pi, pw, _stream_at(cur, stream)))
     return idx, w
 
 
@@ -752,13 +753,12 @@ def route_scored(p: Spec, gate: Gate, x, w_gate, bias=None, balance=None, want_l
     px, pw = _at(cur, x, (p.T, p.d), dt, "x"), _at(cur, w_gate, (p.d, p.E), dt, "w_gate")
     pb = None if bias is None else _at(cur, bias, (p.E,), f32, "bias")
     pc = None if balance is None else _at(cur, balance, (p.E,), f32, "balance")
-    idx, w = _choice_out(p, x.device, out, stream)
+    idx, w, pi, pv = _choice_out(cur, p, x, out, stream)
     with _alloc_on(stream):
         logits = torch.empty((p.T, p.E), dtype=f32, device=x.device) if want_logits else None
     ws, at, size = _workspace_at(cur, p, MOE_CALL_ROUTE_SCORED, workspace, stream)
     _check(lib().moe_route_scored(p.ref(), gate.ref(), px, pw, pb, pc, _ptr(logits),
-                                  _at(cur, idx, slots, torch.int32, "topk_idx"), _at(cur, w, slots, f32, "topk_w"),
-                                  at, size, _stream_at(cur, stream)))
+                                  pi, pv, at, size, _stream_at(cur, stream)))
     return (idx, w, logits) if want_logits else (idx, w)
 
 
@@ -774,17 +774,18 @@ def route_backward(p: Spec, gate: Gate, x, w_gate, logits, topk_idx, dtopk_w, dx
     ins = (_at(cur, topk_idx, slots, torch.int32, "topk_idx"), _at(cur, dtopk_w, slots, f32, "dtopk_w"),
            None if dx_add is None else _at(cur, dx_add, wide, dt, "dx_add"))
     if out is None:
-        with _alloc_on(stream):
-            dev = logits.device
-            out = (torch.empty(all_e, dtype=f32, device=dev), torch.empty(wide, dtype=dt, device=dev),
-                   torch.empty(gates, dtype=dt, device=dev), torch.empty((p.E,), dtype=f32, device=dev))
-    dl, dx, dwg, db = out
-    px = None if x is None and dwg is None else _at(cur, x, wide, dt, "x")
-    pw = None if w_gate is None and dx is None else _at(cur, w_gate, gates, dt, "w_gate")
-    outs = (None if dl is None else _at(cur, dl, all_e, f32, "dlogits"),
-            None if dx is None else _at(cur, dx, wide, dt, "dx"),
-            None if dwg is None else _at(cur, dwg, gates, dt, "dw_gate"),
-            None if db is None else _at(cur, db, (p.E,), f32, "dbias"))
+        px, pw = _at(cur, x, wide, dt, "x"), _at(cur, w_gate, gates, dt, "w_gate")
+        with _alloc_on(stream):   # of the inputs' sizes, which were checked
+            dl, dx, dwg, db = torch.empty_like(logits), torch.empty_like(x), torch.empty_like(w_gate), logits.new_empty((p.E,))
+        outs = (dl.data_ptr(), dx.data_ptr(), dwg.data_ptr(), db.data_ptr())
+    else:
+        dl, dx, dwg, db = out
+        px = None if x is None and dwg is None else _at(cur, x, wide, dt, "x")
+        pw = None if w_gate is None and dx is None else _at(cur, w_gate, gates, dt, "w_gate")
+        outs = (None if dl is None else _at(cur, dl, all_e, f32, "dlogits"),
+                None if dx is None else _at(cur, dx, wide, dt, "dx"),
+                None if dwg is None else _at(cur, dwg, gates, dt, "dw_gate"),
+                None if db is None else _at(cur, db, (p.E,), f32, "dbias"))
     ws, at, size = _workspace_at(cur, p, MOE_CALL_ROUTE_BACKWARD, workspace, stream)
     _check(lib().moe_route_backward(p.ref(), gate.ref(), px, pw, pl, *ins, *outs, at, size, _stream_at(cur, stream)))
     return dl, dx, dwg, db
