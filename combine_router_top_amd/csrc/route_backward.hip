@@ -246,6 +246,9 @@ __global__ __launch_bounds__(256) void pad_rows(const bf16_t* __restrict__ w, in
 // before it is rounded, and on the small tiles of few tokens.
 // dWg: a unit is 128 rows of d, 256 experts and a share of the tokens, both operands
 // panels of 64 tokens in a ring of three slots, transposed by the LDS read.
+// 4096 x 7168 x 256: 45 us (dx alone 26, the parts of dWg alone 23; two launches 49), at 59 MB of
+// x, as much of dx and 29 MB of parts; a workgroup's stores and the loads of its next tile
+// bound it, with one workgroup on a compute unit.
 struct RouteGrad {
   const bf16_t* x;
   const bf16_t* wg;     // [d][Ep]

@@ -202,7 +202,9 @@ __device__ __forceinline__ int choose_exact(const float (&l)[NV], const float* _
   return mye;
 }
 
-// One wave per token.  Lane l holds the NV experts NV l .. NV l + NV - 1.
+// One wave per token.  Lane l holds the NV experts NV l .. NV l + NV - 1.  A round of the
+// choice is a maximum over the wave, six dependent steps and a way through scalar
+// registers, and k + 1 rounds bound it: 256 experts, 8 of them, one token 6.0 us, 4096 12.0.
 template <int NV>
 __global__ __launch_bounds__(256) void select_kernel(const float* __restrict__ part, int nsplit,
                                                      const float* __restrict__ bias,
