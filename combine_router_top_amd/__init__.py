@@ -879,16 +879,19 @@ def gemm_4bit(a, packed, scale, zero=None, group: int = 128, dtype=None, workspa
     pa = _at(cur, a, (M, K), torch.bfloat16, "a")
     if out is None:
         with _alloc_on(stream):
-            out = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=a.device)
+            out = a.new_empty((M, N), dtype=dtype or torch.bfloat16)
+        po = out.data_ptr()
+    else:
+        po = _at(cur, out, (M, N), dtype or out.dtype, "out")
     ins = (_at(cur, packed, packed_weights_4bit_shape(K, N), torch.int32, "packed"),
            _at(cur, scale, rows, torch.bfloat16, "scale"),
            None if zero is None else _at(cur, zero, rows, torch.uint8, "zero"),
-           _at(cur, out, (M, N), dtype or out.dtype, "out"), _dtype_code(out, "out"))
+           po, _dtype_code(out, "out"))
     if workspace is None:
         need = gemm_4bit_workspace_bytes(M, N, K)
         if need:
             with _alloc_on(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+                workspace = a.new_empty(need, dtype=torch.uint8)
     elif workspace.get_device() != cur:
         raise ValueError(f"workspace is on device {workspace.get_device()}, the current device is {cur}")
     _check(lib().moe_gemm_fourbit(M, N, K, group, pa, *ins, _ptr(workspace),
