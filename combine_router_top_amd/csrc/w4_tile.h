@@ -44,7 +44,7 @@ struct W4Cfg {
   static constexpr int WAVES = 4;
   static constexpr int NT = 4, NH = GATED ? 2 : 4;      // a wave's weight and output tiles
   static constexpr int COLS = GATED ? 128 : 256;        // output columns of a tile
-  static constexpr int XSLOT = 256 * 128;               // 64 K of 256 rows
+  static constexpr int XSLOT = 192 * 128;               // 64 K of 192 rows
   static constexpr int WOFF = 3 * XSLOT;                // the packed blocks' ring
   // a slot of it: 16 blocks, a group's scales (512 bytes), its zero points (256, gated: 256 of
   // each matrix, half of them used)
@@ -216,7 +216,7 @@ __device__ __forceinline__ void w4_begin(const W4Args& p, const W4Tile& t, const
 // A tile's product for L row tiles a wave.
 template <class C, int L>
 struct W4Wave {
-  static constexpr int NT = C::NT, NH = C::NH, GPB = C::GPB, X = L / 2;
+  static constexpr int NT = C::NT, NH = C::NH;
   f32x4 acc[L][NT];
   u32x4 x[L];              // rows of a k-step
   u32x4 w[NT];             // packed words of a block

@@ -2,6 +2,7 @@
 import ctypes
 import functools
 import os
+import shutil
 import subprocess
 import tempfile
 from typing import NamedTuple
@@ -24,9 +25,12 @@ class Plan(NamedTuple):
 
 @functools.lru_cache(None)
 def _lib():
-    out = os.path.join(tempfile.mkdtemp(prefix="rules_4bit_"), "rules.so")
-    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-o", out, os.path.join(HERE, "rules_4bit.cpp")], check=True)
-    return ctypes.CDLL(out)
+    cxx = next((c for c in ("g++", "clang++", "/opt/rocm/llvm/bin/clang++") if shutil.which(c)), None)
+    assert cxx, "no host C++ compiler"
+    with tempfile.TemporaryDirectory() as tmp:
+        out = os.path.join(tmp, "rules.so")
+        subprocess.run([cxx, "-O1", "-std=c++17", "-shared", "-fPIC", "-o", out, os.path.join(HERE, "rules_4bit.cpp")], check=True)
+        return ctypes.CDLL(out)   # stays mapped after the file is gone
 
 
 def _plan(gated, segments, n, N, K, mean, rows, most):
