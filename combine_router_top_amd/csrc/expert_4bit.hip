@@ -164,8 +164,9 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
   const int kend = min(p.K, (s0 + ns) * W4_KB);   // rows read zeros from there on
   const int64_t ge = (int64_t)e * p.groups * p.N;
   const uint32_t gsize = (uint32_t)p.groups * (uint32_t)p.N;
-  __amdgpu_buffer_rsrc_t rb[NT], rs[GATED ? 2 : 1], rz[GATED ? 2 : 1];
   constexpr int MATS = GATED ? 2 : 1;
+  __amdgpu_buffer_rsrc_t rb[NT], rs[MATS], rz[MATS];
+  uint32_t zsize[MATS];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const char* base = GATED && t >= NH ? p.b3 : p.b1;
@@ -176,13 +177,15 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
   for (int m = 0; m < MATS; ++m) {
     const uint8_t* z = m ? p.z3 : p.z1;
     rs[m] = gc_rsrc((m ? p.s3 : p.s1) + ge, gsize * 2u);
-    rz[m] = gc_rsrc(z ? z + ge : (const uint8_t*)p.a, z ? gsize : 0u);
+    zsize[m] = z ? gsize : 0u;
+    rz[m] = gc_rsrc(z ? z + ge : (const uint8_t*)p.a, zsize[m]);
   }
   // lane i of a row loads tile i / GPB and group i % GPB
   static_assert(NH * GPB <= 16, "a lane for each tile and group");
   const int scol = 16 * (tile0 + min(i / GPB, NH - 1)) + 4 * g;
   const uint32_t vs = scol < p.N ? (uint32_t)(i % GPB) * (uint32_t)p.N + (uint32_t)scol : GC_OOR >> 1;
-  const __amdgpu_buffer_rsrc_t ra = gc_rsrc(p.a + (int64_t)o * p.K, (uint32_t)R * (uint32_t)p.K * 2u);
+  const uint32_t asize = (uint32_t)R * (uint32_t)p.K * 2u;
+  const __amdgpu_buffer_rsrc_t ra = gc_rsrc(p.a + (int64_t)o * p.K, asize);
   uint32_t va[MT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -202,20 +205,21 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
   uint32_t zp[RB][MATS];
   auto load = [&](int h, int b) {   // block b of this wave; of one past its last, rows and weights are zeros
 #pragma unroll
-    for (int t = 0; t < NT; ++t) w[h][t] = __builtin_amdgcn_raw_buffer_load_b128(rb[t], vb, b * 1024, 0);
+    for (int t = 0; t < NT; ++t)
+      w[h][t] = __builtin_amdgcn_raw_buffer_load_b128(rb[t], vb, st_offset((uint32_t)b * 1024u, (uint32_t)ns * 1024u), 0);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int k = (s0 + b) * W4_KB + 32 * q;
       const bool in = k + 8 * g < kend;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
-        x[h][mt][q] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? va[mt] : GC_OOR, (uint32_t)k * 2u, 0);
+        x[h][mt][q] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? va[mt] : GC_OOR, st_offset((uint32_t)k * 2u, asize), 0);
     }
     const uint32_t row = (uint32_t)((s0 + b) * GPB) * (uint32_t)p.N;
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
-      sc[h][m] = __builtin_amdgcn_raw_buffer_load_b64(rs[m], vs * 2u, row * 2u, 0);
-      if (ZERO) zp[h][m] = __builtin_amdgcn_raw_buffer_load_b32(rz[m], vs, row, 0);
+      sc[h][m] = __builtin_amdgcn_raw_buffer_load_b64(rs[m], vs * 2u, st_offset(row * 2u, gsize * 2u), 0);
+      if (ZERO) zp[h][m] = __builtin_amdgcn_raw_buffer_load_b32(rz[m], vs, st_offset(row, zsize[m]), 0);
     }
   };
   auto multiply = [&](int h) {

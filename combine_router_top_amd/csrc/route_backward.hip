@@ -352,7 +352,8 @@ __device__ __forceinline__ void weight_unit(const RouteGrad& p, int u, char* lds
     const int left = __builtin_amdgcn_readfirstlane(max(0, min(64, rows - 64 * st)));
     const __amdgpu_buffer_rsrc_t r = gc_rsrc(xb + (int64_t)st * 64 * ldx, (uint32_t)left * ldx);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) bd_copy16(r, at + 2048 * wave + 1024 * c, vx, (uint32_t)(4 * c) * ldx);
+    for (int c = 0; c < 2; ++c)
+      bd_copy16(r, at + 2048 * wave + 1024 * c, vx, st_offset((uint32_t)(4 * c) * ldx, (uint32_t)left * ldx));
     st_issue(q, at + RG_XB, st);
   };
   f32x4 acc[4][4];

@@ -14,6 +14,12 @@ namespace moe {
 // ---------------------------------------------------------------------------
 constexpr int ST_KB = 128;     // bytes of K per stage
 
+// The scalar offset of a load from a buffer of `size` bytes.  What lies past the end (blocks
+// ahead of the last, groups that the last block has not, absent zero points, rows that a
+// share has not) is asked for at the end, where the range check drops every lane: it
+// compares lane offsets with the size less the scalar offset, which is not to pass zero.
+constexpr uint32_t st_offset(uint32_t off, uint32_t size) { return off < size ? off : size; }
+
 // Height (in units of 64 rows) of the tiles for segments of about `mean` rows of
 // n experts: the one whose rounds of workgroups take the least time.  A stage of
 // a tile costs the copies of its rows and columns, at the 38 GB/s that a compute

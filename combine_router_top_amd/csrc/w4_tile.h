@@ -145,10 +145,12 @@ template <class C>
 __device__ __forceinline__ void w4_issue(const W4Ctx<C>& c, uint32_t slot, int b, int v) {
   if (v < C::WB) {
     const __amdgpu_buffer_rsrc_t r = gc_rsrc(c.w[C::GATED && v >= C::WB / 2 ? 1 : 0], c.wsize);
-    w4_copy<16>(r, slot + 1024 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), 1024 * C::WAVES * v, c.woff[v], (uint32_t)b * 1024u);
+    w4_copy<16>(r, slot + 1024 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), 1024 * C::WAVES * v, c.woff[v],
+                st_offset((uint32_t)b * 1024u, c.wsize));
   } else {
     const int u = v - C::WB;
-    w4_copy<4>(gc_rsrc(c.s[u], c.ssize[u]), slot + c.sdst[u], 0, 4u * (threadIdx.x & 63), (uint32_t)b * c.sstep[u]);
+    w4_copy<4>(gc_rsrc(c.s[u], c.ssize[u]), slot + c.sdst[u], 0, 4u * (threadIdx.x & 63),
+               st_offset((uint32_t)b * c.sstep[u], c.ssize[u]));
   }
 }
 
@@ -178,7 +180,7 @@ struct W4Rows {
   }
   __device__ __forceinline__ void issue(uint32_t slot, int st, int c) const {   // slot: of this wave
     w4_copy<16>(gc_rsrc(base, size), slot + 1024 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), 4096 * c, voff[c],
-                (uint32_t)st * ST_KB);
+                st_offset((uint32_t)st * ST_KB, size));
   }
 };
 
@@ -210,7 +212,8 @@ __device__ __forceinline__ void w4_begin(const W4Args& p, const W4Tile& t, const
   for (int u = 0; u < X; ++u)
 #pragma unroll
     for (int j = 0; j < 3; ++j)
-      w4_copy<16>(r, lbase + 1024 * wave + 4096 * u, j * C::XSLOT, x.voff[0] + (uint32_t)(32 * u) * ld, (uint32_t)j * ST_KB);
+      w4_copy<16>(r, lbase + 1024 * wave + 4096 * u, j * C::XSLOT, x.voff[0] + (uint32_t)(32 * u) * ld,
+                  st_offset((uint32_t)j * ST_KB, x.size));
 }
 
 // A tile's product for L row tiles a wave.
