@@ -72,9 +72,10 @@ __device__ __forceinline__ Top2<T> merge(const Top2<T>& p, const Top2<T>& q) {
 
 // Groups that stay, as a mask with bit g L of each (L = r.lanes): the groups with fewer than
 // topk_groups better ones, or as good and before them; `mine` is the value of the group of
-// lanes g L .. g L + L - 1.
+// lanes g L .. g L + L - 1.  In fp32, that value may be off by `error`, in proportion to the sizes
+// of its members (they may cancel), and `close` is set where that could change what stays.
 template <class T>
-__device__ __forceinline__ uint64_t open_groups(T mine, const SelectRule& r, float slack, bool& close) {
+__device__ __forceinline__ uint64_t open_groups(T mine, const SelectRule& r, float error, bool& close) {
   const int g = (threadIdx.x & 63) / r.lanes;
   int better = 0;
   for (int q = 0; q < r.groups; ++q) {
@@ -84,10 +85,11 @@ __device__ __forceinline__ uint64_t open_groups(T mine, const SelectRule& r, flo
     better += v > mine || (v == mine && q < g);
   }
   const bool in = g < r.groups, stay = in && better < r.topk_groups;
-  if constexpr (sizeof(T) == 4) {   // the worst that stays against the best that does not
-    const float worst = -reduce_max(stay ? -mine : -INFINITY), best = reduce_max(in && !stay ? mine : -INFINITY);
-    close |= !(worst - best > slack * (1.0f + fabsf(worst)));
-  }
+  if constexpr (sizeof(T) == 4)
+    if (r.topk_groups < r.groups) {   // the least that one that stays can be, the most that another can
+      const float worst = -reduce_max(stay ? error - mine : -INFINITY), best = reduce_max(in && !stay ? mine + error : -INFINITY);
+      close |= !(worst > best);
+    }
   return __ballot(stay);
 }
 
@@ -262,7 +264,10 @@ __global__ __launch_bounds__(256) void select_kernel(const float* __restrict__ p
       if (r.lanes > 2) v = merge(v, Top2<float>{dpp<0x4E>(v.a), dpp<0x4E>(v.b)});
       if (r.lanes > 4) v = merge(v, Top2<float>{dpp<0x141>(v.a), dpp<0x141>(v.b)});
       if (r.lanes > 8) v = merge(v, Top2<float>{dpp<0x140>(v.a), dpp<0x140>(v.b)});
-      open = open_groups<float>(r.group_top == 2 ? fmaxf(v.a + v.b, SEL_LOW_F) : v.a, r, 2 * slack, close);
+      const bool two = r.group_top == 2;
+      // each member is off by up to slack / 2 (1 + |c|), their sum by 2^-24 of itself more
+      const float error = slack + slack * fabsf(v.a) + (two ? slack * fabsf(v.b) : 0.f);
+      open = open_groups<float>(two ? fmaxf(v.a + v.b, SEL_LOW_F) : v.a, r, error, close);
     } else if (r.groups > 1) {
       close = true;   // odd groups: in fp64
     }
