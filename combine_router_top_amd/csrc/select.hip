@@ -27,7 +27,7 @@ namespace moe {
 // in 500 with 256 experts; all of 4096 tokens in fp64 took 17.6 us.  Comparisons of
 // logits are exact.
 constexpr double SEL_LOW = -1e300;        // experts that come last, in fp64
-constexpr float SEL_LOW_F = -3.402823466e38f;   // and in fp32
+constexpr float SEL_LOW_F = -3.402823466e38f;   // in fp32 sums of groups; single experts that come last have -inf
 
 __device__ __forceinline__ uint64_t order_key(double v) {
   const uint64_t u = __double_as_longlong(v + 0.0);
@@ -73,9 +73,10 @@ __device__ __forceinline__ Top2<T> merge(const Top2<T>& p, const Top2<T>& q) {
 // Groups that stay, as a mask with bit g L of each (L = r.lanes): the groups with fewer than
 // topk_groups better ones, or as good and before them; `mine` is the value of the group of
 // lanes g L .. g L + L - 1.  In fp32, that value may be off by `error`, in proportion to the sizes
-// of its members (they may cancel), and `close` is set where that could change what stays.
+// of its members (they may cancel), and `close` is set where that could change what stays;
+// `masked`: a member comes last, and the value may be any lower.
 template <class T>
-__device__ __forceinline__ uint64_t open_groups(T mine, const SelectRule& r, float error, bool& close) {
+__device__ __forceinline__ uint64_t open_groups(T mine, const SelectRule& r, float error, bool masked, bool& close) {
   const int g = (threadIdx.x & 63) / r.lanes;
   int better = 0;
   for (int q = 0; q < r.groups; ++q) {
@@ -87,7 +88,8 @@ __device__ __forceinline__ uint64_t open_groups(T mine, const SelectRule& r, flo
   const bool in = g < r.groups, stay = in && better < r.topk_groups;
   if constexpr (sizeof(T) == 4)
     if (r.topk_groups < r.groups) {   // the least that one that stays can be, the most that another can
-      const float worst = -reduce_max(stay ? error - mine : -INFINITY), best = reduce_max(in && !stay ? mine + error : -INFINITY);
+      const float worst = -reduce_max(!stay ? -INFINITY : masked ? INFINITY : error - mine);
+      const float best = reduce_max(in && !stay ? mine + error : -INFINITY);
       close |= !(worst > best);
     }
   return __ballot(stay);
@@ -172,7 +174,7 @@ __device__ __forceinline__ int choose_exact(const float (&l)[NV], const float* _
       for (int i = lane % r.lanes; i < per; i += r.lanes) v = merge(v, Top2<double>{value[g * per + i], -INFINITY});
     for (int off = 1; off < r.lanes; off <<= 1) v = merge(v, Top2<double>{__shfl_xor(v.a, off), __shfl_xor(v.b, off)});
     bool close = false;
-    open = open_groups<double>(r.group_top == 2 ? v.a + v.b : v.a, r, 0.f, close);
+    open = open_groups<double>(r.group_top == 2 ? v.a + v.b : v.a, r, 0.f, false, close);
   }
   uint64_t key[NV];
 #pragma unroll
@@ -251,15 +253,15 @@ __global__ __launch_bounds__(256) void select_kernel(const float* __restrict__ p
       for (int j = 0; j < NV; ++j) {
         if (r.softmax) c[j] *= inv;
         c[j] += b[j];
-        if (l[j] == -INFINITY || !(c[j] >= SEL_LOW_F)) c[j] = SEL_LOW_F;
+        if (l[j] == -INFINITY || !(c[j] >= SEL_LOW_F)) c[j] = -INFINITY;
       }
     }
     bool close = false;
     uint64_t open = 0;
     if (rows) {
-      Top2<float> v{c[0], SEL_LOW_F};
+      Top2<float> v{fmaxf(c[0], SEL_LOW_F), SEL_LOW_F};
 #pragma unroll
-      for (int j = 1; j < NV; ++j) v = merge(v, Top2<float>{c[j], SEL_LOW_F});
+      for (int j = 1; j < NV; ++j) v = merge(v, Top2<float>{c[j], SEL_LOW_F});   // -inf: below both
       if (r.lanes > 1) v = merge(v, Top2<float>{dpp<0xB1>(v.a), dpp<0xB1>(v.b)});
       if (r.lanes > 2) v = merge(v, Top2<float>{dpp<0x4E>(v.a), dpp<0x4E>(v.b)});
       if (r.lanes > 4) v = merge(v, Top2<float>{dpp<0x141>(v.a), dpp<0x141>(v.b)});
@@ -267,14 +269,14 @@ __global__ __launch_bounds__(256) void select_kernel(const float* __restrict__ p
       const bool two = r.group_top == 2;
       // each member is off by up to slack / 2 (1 + |c|), their sum by 2^-24 of itself more
       const float error = slack + slack * fabsf(v.a) + (two ? slack * fabsf(v.b) : 0.f);
-      open = open_groups<float>(two ? fmaxf(v.a + v.b, SEL_LOW_F) : v.a, r, error, close);
+      open = open_groups<float>(two ? fmaxf(v.a + v.b, SEL_LOW_F) : v.a, r, error, two && v.b == SEL_LOW_F, close);
     } else if (r.groups > 1) {
       close = true;   // odd groups: in fp64
     }
     uint32_t key[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const float v = r.by_logit ? (l[j] >= SEL_LOW_F ? l[j] : SEL_LOW_F) : c[j];
+      const float v = r.by_logit ? (l[j] == l[j] ? l[j] : -INFINITY) : c[j];
       const bool in = e0 + j < E && (r.groups == 1 || ((open >> (lane & -r.lanes)) & 1));
       key[j] = in ? f32_order_key(v) : 0u;
     }
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(256) void select_kernel(const float* __restrict__ p
         if (!r.by_logit) {
           const float v = __uint_as_float((m & 0x80000000u) ? (m & 0x7FFFFFFFu) : ~m);
           // the last ones are alike by definition; m = 0: nothing is left
-          const bool near = m != 0 && v != SEL_LOW_F && !(before - v > slack * (1.0f + fabsf(v)));
+          const bool near = m != 0 && v != -INFINITY && !(before - v > slack * (1.0f + fabsf(v)));
           if (q >= k && !near) break;
           again |= near;
           before = v;
@@ -406,7 +408,7 @@ __global__ __launch_bounds__(256) void select_rows(const float* __restrict__ par
       }
       bad |= l[j] != l[j] || l[j] == INFINITY;
       top = fmaxf(top, l[j]);
-      key[j] = e < E ? f32_order_key(l[j] >= SEL_LOW_F ? l[j] : SEL_LOW_F) : 0u;
+      key[j] = e < E ? f32_order_key(l[j] == l[j] ? l[j] : -INFINITY) : 0u;
     }
     top = row_reduce(top, fmax2);
     float total = 1.f;

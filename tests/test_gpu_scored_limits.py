@@ -7,7 +7,7 @@ import torch
 
 import combine_router_top_amd as M
 from tests.segments import assert_within
-from tests.test_gpu_scored import EPS, _choose, _logits, _scores, _spec
+from tests.test_gpu_scored import EPS, _check_select, _choose, _logits, _scores, _spec
 
 
 def _choose_all(gate, k, l, balance):
@@ -43,3 +43,42 @@ def test_groups_whose_two_best_cancel(score, E, groups, topk_groups, k, size):
     idx, w = M.select(_spec(T, E, k), gate, l.cuda(), b.cuda())
     assert np.array_equal(idx.cpu().numpy(), ri)
     assert_within(w, rw, (k + 60) * EPS * rw + 1e-37, "weights")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score,groups,group_top", [("softmax", 1, 1), ("sigmoid", 1, 1), ("softmax", 8, 1), ("softmax", 8, 2), ("sigmoid", 8, 2)])
+@pytest.mark.parametrize("E", [24, 64, 120, 256, 1000])
+@pytest.mark.parametrize("where", ["logits", "balance", "both"])
+def test_masks_of_the_lowest_value(score, groups, group_top, E, where):
+    """Values of the type's lowest come before -inf and after everything else, also where k reaches them."""
+    T, k, lowest = 70, 9, torch.finfo(torch.float32).min
+    gate = M.Gate(score, groups, max(1, groups // 2), group_top, False)
+    g = torch.Generator().manual_seed(E)
+    l, b = _logits(T, E, E + 3), None
+    if where != "balance":
+        pick = torch.rand((T, E), generator=g)
+        l[pick < 0.9] = lowest
+        l[pick < 0.4] = -math.inf
+        l[0], l[1, 1:] = lowest, lowest
+    if where != "logits":
+        pick = torch.rand(E, generator=g)
+        b = torch.randn(E, generator=g) * 0.2
+        b[pick < 0.9] = lowest
+        b[pick < 0.4] = -math.inf
+    idx, w = M.select(_spec(T, E, k), gate, l.cuda(), None if b is None else b.cuda())
+    _check_select(gate, k, l, b, idx, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,group_top", [(64, 32, 2), (64, 32, 1), (256, 8, 2), (24, 1, 1)])
+def test_balances_of_every_size(score, E, groups, group_top):
+    T, k = 40, 8
+    gate = M.Gate(score, groups, max(1, groups // 3), group_top, False)
+    sizes = torch.tensor([3e38, 1e38, 1.0, 0.0, -1.0, -1e38, -3e38, torch.finfo(torch.float32).min, -math.inf])
+    for seed in range(12):
+        g = torch.Generator().manual_seed(seed)
+        b = sizes[torch.randint(0, sizes.numel(), (E,), generator=g)]
+        l = _logits(T, E, seed, "masked" if seed % 3 == 0 else "normal")
+        idx, w = M.select(_spec(T, E, k), gate, l.cuda(), b.cuda())
+        _check_select(gate, k, l, b, idx, w)
