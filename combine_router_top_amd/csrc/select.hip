@@ -222,7 +222,7 @@ __global__ __launch_bounds__(256) void select_kernel(const float* __restrict__ p
   // groups of whole lanes, 2^n up to 16 of them: their two best by DPP
   const bool rows = r.groups > 1 && per % NV == 0 && per / NV <= 16 && ((per / NV) & (per / NV - 1)) == 0 &&
                     per / NV == r.lanes;
-  const bool sums = r.softmax && (!r.renorm || !r.by_logit || r.groups > 1);   // the sum over all experts is needed
+  const bool sums = r.softmax && (!r.renorm || !r.by_logit || r.groups > 1);   // scores of all experts are needed
   const float slack = r.softmax ? 0x1p-18f : 0x1p-20f;
   float b[NV];
 #pragma unroll
@@ -345,7 +345,11 @@ __global__ __launch_bounds__(256) void select_kernel(const float* __restrict__ p
     float s = 0.f;
     {
       if (r.softmax) {
-        s = expf(mine - top) * inv;
+        // renorm: by the best of the chosen, which a balance may take from far below the row's
+        // best, where fp32 holds no scores but their ratios are the weights all the same
+        const float from = r.renorm ? reduce_max(lane < k ? mine : -INFINITY) : top;
+        s = expf(mine - from);
+        if (!r.renorm) s *= inv;
         if (mine == -INFINITY) s = 0.f;   // also where every logit is
       } else {
         // renorm: all by exp(-shift), so that the ratio of tiny scores is theirs

@@ -207,9 +207,11 @@ typedef struct moe_gate_t {
  * The order is that of c in 64 bits (softmax scores without a balance bias: that of
  * the logits).  balance moves the choice alone, not the weights.
  * An expert whose logit or balance is -inf comes after every other one of the groups
- * that stay, and a score of 0 gives weight 0 (all k of them zero under renorm too).  A
- * row with a NaN logit, or under softmax a logit of +inf, gives NaN weights where its
- * scores are NaN; topk_idx holds k distinct experts in [0, E) for any input.
+ * that stay, and a score of 0, of a logit of -inf, gives weight 0 (all k of them zero under
+ * renorm too).  Under renorm the weights are the chosen scores' ratios, also where a balance
+ * takes experts whose scores fp32 does not hold.  A row with a NaN logit, or under softmax
+ * a logit of +inf, gives NaN weights where its scores are NaN; topk_idx holds k distinct
+ * experts in [0, E) for any input.
  * Only T, E and k of p are used (the others have to be valid).
  *   logits   [T,E] fp32
  *   balance  [E]   fp32, or NULL (zeros)

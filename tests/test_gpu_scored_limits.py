@@ -82,3 +82,22 @@ def test_balances_of_every_size(score, E, groups, group_top):
         l = _logits(T, E, seed, "masked" if seed % 3 == 0 else "normal")
         idx, w = M.select(_spec(T, E, k), gate, l.cuda(), b.cuda())
         _check_select(gate, k, l, b, idx, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("far", [20.0, 80.0, 95.0, 104.0, 200.0])
+@pytest.mark.parametrize("groups", [1, 8])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_chosen_far_below_the_best(score, groups, far):
+    """The balance chooses experts whose scores fp32 does not hold; under renorm only their ratios count."""
+    T, E, k = 300, 64, 6
+    l = _logits(T, E, 11) * 0.5
+    l[:, : E // 2] += far if score == "softmax" else 0.0
+    l[:, E // 2:] -= 0.0 if score == "softmax" else far
+    b = torch.zeros(E)
+    b[E // 2:] = 4.0
+    b += torch.randn(E, generator=torch.Generator().manual_seed(2)) * 0.1
+    gate = M.Gate(score, groups, max(1, groups // 2), min(2, groups), True, 2.5)
+    idx, w = M.select(_spec(T, E, k), gate, l.cuda(), b.cuda())
+    assert int(idx.min()) >= E // 2
+    _check_select(gate, k, l, b, idx, w)
