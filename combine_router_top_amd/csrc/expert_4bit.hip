@@ -8,16 +8,18 @@
 //
 // Two forms of the product, by what either takes (w4_plan).  Streams, for few rows, read
 // every weight once, straight into registers.  A group's part of a sum is
-// s (sum x q - z sum x).  The matrix cores take q as the bf16 number (16 + q) / 32, which is
+// s (sum x q - z sum x).  The matrix cores take q as the bf16 number (16 + q) / 4096, which is
 // exact and costs one masked or of the packed bits (q is the upper mantissa of a number in
-// 1/2 .. 1), so that with X = sum x / 32 over the group
+// 2^-8 .. 2^-7), so that with X = sum x / 4096 over the group
 //
-//   part = sum x (16 + q) / 32,   C = 32 sum s (part - (16 + z) X)
+//   part = sum x (16 + q) / 4096,   C = 4096 sum s (part - (16 + z) X)
 //
-// X is one more product, with 1/32.  All of it is fp32: no weight is ever rounded.  The
+// X is one more product, with 1/4096.  All of it is fp32: no weight is ever rounded.  The
 // offset makes the terms of a part about five times larger than those of the result, two
-// bits of fp32's 24; the 1/32 keeps them below the rows' own size, so that nothing overflows
-// that x does not.  Tiles, for many rows: w4_tile.h.
+// bits of fp32's 24.  The 1/4096 keeps both of a group's sums, of up to 128 terms of 31 |x|,
+// below the largest |x|, so that no part overflows; every bf16 x times (16 + q) / 4096 is a
+// multiple of 2^-145, which fp32 holds, and what is summed last are multiples of 2^-149, so
+// that results are off by up to 2^-137 for each group.  Tiles, for many rows: w4_tile.h.
 //
 // Packed weights: blocks of 16 columns x 128 K, 1 KB, one 16-byte load per lane and an
 // operand of four MFMA k-steps after the masked ors: [N/16][K/128][64 lanes][4 words],
@@ -191,7 +193,7 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
   for (int mt = 0; mt < MT; ++mt)
     va[mt] = 16 * mt + i < R ? ((uint32_t)(16 * mt + i) * (uint32_t)p.K + 8u * (uint32_t)g) * 2u : GC_OOR;
   const uint32_t vb = 16u * (uint32_t)lane;
-  // what is subtracted, 32 X times: 16 and the zero point, 8 where there are none (they read as zeros)
+  // what is subtracted, X times: 16 and the zero point, 8 where there are none (they read as zeros)
   const float zb1 = p.z1 ? -16.f : -24.f, zb3 = GATED && p.z3 ? -16.f : -24.f;
 
   const uint32_t mask = w4_mask(), bits = w4_bits();
@@ -223,8 +225,8 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
     }
   };
   auto multiply = [&](int h) {
-    const bf16x8 unit =   // 1/32
-        __builtin_bit_cast(bf16x8, u32x4{0x3D003D00u, 0x3D003D00u, 0x3D003D00u, 0x3D003D00u});
+    const bf16x8 unit =   // 1/4096
+        __builtin_bit_cast(bf16x8, u32x4{0x39803980u, 0x39803980u, 0x39803980u, 0x39803980u});
 #pragma unroll
     for (int u = 0; u < GPB; ++u) {
       f32x4 X[MT], part[MT][NT];
@@ -292,7 +294,7 @@ __device__ __forceinline__ void w4_stream_block(const W4Args& p, int e, int o, i
     if (row >= R || col >= p.N) continue;
     float v4[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v4[r] = GATED ? silu_mul(32.f * p1[r], 32.f * p3[r]) : 32.f * p1[r];
+    for (int r = 0; r < 4; ++r) v4[r] = GATED ? silu_mul(4096.f * p1[r], 4096.f * p3[r]) : 4096.f * p1[r];
     w4_store<F32OUT>(p.c, (int64_t)(o + row) * p.N + col, v4);
   }
 }

@@ -44,7 +44,7 @@ __device__ __forceinline__ int w4_rows(const W4Args& p, int e, int& o) {
   return cnt;
 }
 
-// The eight numbers (16 + q) / 32 of a packed word.  mask and bits are w4_mask() and w4_bits():
+// The eight numbers (16 + q) / 4096 of a packed word.  mask and bits are w4_mask() and w4_bits():
 // as constants that the compiler knows they would be literals, of which a masked or
 // takes none (then it is two instructions); it takes one scalar register.
 __device__ __forceinline__ u32x4 w4_unpack(uint32_t w, uint32_t mask, uint32_t bits) {
@@ -60,7 +60,7 @@ __device__ __forceinline__ uint32_t w4_mask() {
 }
 __device__ __forceinline__ uint32_t w4_bits() {
   uint32_t v;
-  asm("s_mov_b32 %0, 0x3F003F00" : "=s"(v));
+  asm("s_mov_b32 %0, 0x3B803B80" : "=s"(v));
   return v;
 }
 

@@ -518,10 +518,11 @@ moe_status_t moe_quantize_weights_fourbit(int32_t n, int32_t K, int32_t N, int32
 /*
  * Product with 4-bit weights: C = rnd(A W), W one matrix [K,N] as above, with fp32
  * accumulation.  Which kernel runs goes by the sizes, so a row's result may differ in its last
- * bits with the number of rows beside it.  For few rows nothing is rounded but the sums; for
- * many, odd multiples |q - zero| above 8 of a scale are rounded to 11 bits where there are zero
- * points (by up to 2^-11), values of A more than 2^-31 below the largest of their row to multiples of
- * 2^-38 of it, scales more than 2^-27 below the largest of their column to multiples of 2^-34 of it.
+ * bits with the number of rows beside it.  For few rows nothing is rounded but the sums (to
+ * which a group adds multiples of 2^-137); for many, odd multiples |q - zero| above 8 of a scale
+ * are rounded to 11 bits where there are zero points (by up to 2^-11), values of A more than 2^-31
+ * below the largest of their row to multiples of 2^-38 of it, scales more than 2^-27 below the
+ * largest of their column to multiples of 2^-34 of it.
  * A row of A with an infinity or a NaN gives a row of NaN, a NaN scale a column of NaN, and
  * neither reaches others.
  *   A [M,K] bf16 row-major, 16-byte aligned;  C [M,N] of out_dtype, 16-byte aligned,
