@@ -68,7 +68,9 @@ __global__ __launch_bounds__(256) void w4_scales(const void* __restrict__ w, int
   }
   const int64_t at = (int64_t)blockIdx.y * groups * N + id;
   const float big = __uint_as_float(top);
-  float s = zero ? (hi - lo) / 15.0f : big / 7.0f;
+  // (a range past fp32's largest value by halves: elsewhere it is the one step documented)
+  const float range = hi - lo;
+  float s = !zero ? big / 7.0f : range < INFINITY ? range / 15.0f : (0.5f * hi - 0.5f * lo) / 7.5f;
   if (top >= 0x7F800000u) s = big;
   scale[at] = (bf16_t)cvt_bf16x2(s, 0.f);
   if (zero) {

@@ -503,8 +503,8 @@ moe_status_t moe_expert_gemm_quantized(const moe_problem_t* p, const void* x_pac
  *   zero NULL: scale = rnd(max|w| / 7),            q = clamp(rint(w / scale) + 8, 1, 15)
  *   else       scale = rnd((hi - lo) / 15),        hi = max(w, 0), lo = min(w, 0),
  *              zero = clamp(rint(-lo / scale)),    q = clamp(rint(w / scale) + zero)
- *   (clamp: to 0 .. 15).  Where the scale is 0, q = zero = 8; a group with an infinity or
- *   a NaN gets that as its scale.
+ *   (clamp: to 0 .. 15; hi - lo as if fp32 had no largest value).  Where the scale is 0,
+ *   q = zero = 8; a group with an infinity or a NaN gets that as its scale.
  * n 1..1024, K at most 2^20, K and N multiples of 8; packed 16-byte, scale 8-byte and zero
  * 4-byte aligned; outputs do not overlap inputs or one another.
  */

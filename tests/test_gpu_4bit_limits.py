@@ -54,3 +54,18 @@ def test_dense_rows_of_one_sign(name, zero, exponent):
     for dtype, half in ((torch.bfloat16, HALF["bf16"]), (torch.float32, HALF["f32"])):
         got = M.gemm_4bit(*args, group=G, dtype=dtype)
         assert_within(got, ref, slack * (1 + half) + half * ref.abs(), str(dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantiser_at_the_largest_weights(dtype):
+    """With zero points a group's range can pass fp32's largest value; its scale does not."""
+    K, N, G = 136, 24, 64
+    top = torch.finfo(torch.bfloat16).max
+    w = ((torch.rand((K, N), generator=torch.Generator().manual_seed(3)) * 2 - 1) * top).to(dtype)
+    w[0], w[1], w[64], w[65], w[128], w[129] = top, -top, top, -top, top, -top
+    p, s, z = M.quantize_weights_4bit(w.cuda(), G, True)
+    step = torch.tensor(2 * top / 15, dtype=torch.float64).to(torch.bfloat16)
+    assert bool((s.cpu() == step).all())
+    assert bool((z.cpu() == torch.round(top / step.float())).all())
+    values = torch.clamp(torch.round(w.float() / step.float()) + z.cpu().float()[0], 0, 15).to(torch.uint8)
+    assert torch.equal(p, M.pack_weights_4bit(values.cuda()))
