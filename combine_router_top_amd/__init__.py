@@ -839,8 +839,11 @@ def pack_weights_4bit(q, stream=None, out=None):
 
 def quantize_weights_4bit(w, group: int = 128, zero: bool = False, stream=None, out=None):
     """(packed, scale, zero) of bf16 or fp32 weights [n, K, N] or [K, N]: a bf16 scale, and
-    with ``zero`` a zero point (else None: 8), for each group of K in each column."""
+    with ``zero`` a zero point (else None: 8), for each group of K in each column.  ``out``:
+    the three, written in place; zero points among them only with ``zero``."""
     torch = _torch()
+    if out is not None and out[2] is not None and not zero:
+        raise ValueError("out has zero points, which are not made without zero=True")
     code, cur = _dtype_code(w, "w"), _current()
     n, K, N, lead = _matrices(w)
     shape, rows = lead + packed_weights_4bit_shape(K, N), lead + (_groups(K, group), N)
