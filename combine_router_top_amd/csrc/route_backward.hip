@@ -536,12 +536,7 @@ __global__ __launch_bounds__(256) void clear_grads(char* __restrict__ a, int64_t
 
 static size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Shares of the tokens that the units of dWg are split into: as many as give every
-// compute unit one, each of at least four stages.
-static int rb_shares(const Prob& p) {
-  const int64_t tiles = (int64_t)((p.d + 127) / 128) * ((p.E + 255) / 256), stages = ((int64_t)p.T + 63) / 64;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(device_cus() / tiles, stages / 4));
-}
+static int rb_shares(const Prob& p) { return route_shares(device_cus(), p.T, p.d, p.E); }
 
 struct RouteBackWs {
   size_t dl, wg, part, colsum, total;
@@ -621,7 +616,7 @@ hipError_t launch_route_backward(const Prob& p, const SelectRule& r, const void*
     }
     RouteGrad q{(const bf16_t*)x, w, dlb, (const bf16_t*)dx_add, (bf16_t*)dx, dwg ? part : nullptr, p.T, p.d, Ep, shares};
     const int64_t tiles = (((int64_t)p.T + 255) / 256) * ((p.d + 255) / 256);
-    const bool few = tiles < device_cus() / 2;   // less than half a round of 256 x 256 tiles: 64 x 128
+    const bool few = route_few(device_cus(), p.T, p.d);
     int64_t units = dwg ? (int64_t)((p.d + 127) / 128) * ((Ep + 255) / 256) * shares : 0;
     if (dx) units += few ? (((int64_t)p.T + 63) / 64) * ((p.d + 127) / 128) : tiles;
     auto kern = few ? route_grad<RG_FEW> : dx_add ? route_grad<RG_ADD> : route_grad<RG_ROWS>;

@@ -1,4 +1,4 @@
-// Which kernels a training or 8-bit call takes: rules on sizes and the number of
+// Which kernels a call of the experts, the router's gradients or the 8- and 4-bit products takes: rules on sizes and the number of
 // compute units alone, without device code, so that any host compiler can evaluate
 // them.  The launchers do what a plan says and decide nothing themselves.
 #pragma once
@@ -126,6 +126,18 @@ inline BackwardPlan backward_plan(int64_t cus, int64_t tk, int E, int n, int d, 
   // second (8 dense experts: 18.62 ms against 18.87 in one launch).
   p.apart = input && wants && p.mode == WG_LONG && p.units >= 8 * cus;
   return p;
+}
+
+// ---------------------------------------------------------------------------
+// the router's gradients, bf16
+// ---------------------------------------------------------------------------
+// Tiles of dx are 64 x 128 where 256 x 256 ones would make less than half a round.
+inline bool route_few(int64_t cus, int64_t T, int d) { return (T + 255) / 256 * ((d + 255) / 256) < cus / 2; }
+// Shares of the tokens that the units of dWg are split into: as many as give every
+// compute unit one, each of at least four stages.
+inline int route_shares(int64_t cus, int64_t T, int d, int E) {
+  const int64_t tiles = (int64_t)((d + 127) / 128) * ((E + 255) / 256), stages = (T + 63) / 64;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(cus / tiles, stages / 4));
 }
 
 // ---------------------------------------------------------------------------
