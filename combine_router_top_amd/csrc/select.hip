@@ -267,8 +267,8 @@ __global__ __launch_bounds__(256) void select_kernel(const float* __restrict__ p
       if (r.lanes > 4) v = merge(v, Top2<float>{dpp<0x141>(v.a), dpp<0x141>(v.b)});
       if (r.lanes > 8) v = merge(v, Top2<float>{dpp<0x140>(v.a), dpp<0x140>(v.b)});
       const bool two = r.group_top == 2;
-      // each member is off by up to slack / 2 (1 + |c|), their sum by 2^-24 of itself more
-      const float error = slack + slack * fabsf(v.a) + (two ? slack * fabsf(v.b) : 0.f);
+      // each member is off by up to slack / 2 (1 + |c|), their sum by 2^-24 <= slack / 16 of itself more
+      const float part = 0.5625f * slack, error = two ? slack + part * fabsf(v.a) + part * fabsf(v.b) : part + part * fabsf(v.a);
       open = open_groups<float>(two ? fmaxf(v.a + v.b, SEL_LOW_F) : v.a, r, error, two && v.b == SEL_LOW_F, close);
     } else if (r.groups > 1) {
       close = true;   // odd groups: in fp64
