@@ -19,6 +19,8 @@ constexpr int ST_KB = 128;     // bytes of K per stage
 // share has not) is asked for at the end, where the range check drops every lane: it
 // compares lane offsets with the size less the scalar offset, which is not to pass zero.
 constexpr uint32_t st_offset(uint32_t off, uint32_t size) { return off < size ? off : size; }
+// The block or step of n that a copy ahead of its use takes: past the last one, that again.
+constexpr int st_upto(int i, int n) { return i < n ? i : n - 1; }
 
 // Height (in units of 64 rows) of the tiles for segments of about `mean` rows of
 // n experts: the one whose rounds of workgroups take the least time.  A stage of
