@@ -905,7 +905,8 @@ def gemm_4bit(a, packed, scale, zero=None, group: int = 128, dtype=None, workspa
 def expert_gemm_4bit(p: Spec, x_packed, offsets, w1, s1, z1, w3, s3, z3, w2, s2, z2, group: int = 128,
                      workspace=None, stream=None, out=None):
     """``expert_gemm`` with packed 4-bit weights [n_local, ...], their scales and zero
-    points (each None or not): (h, y_packed)."""
+    points (each None or not): (h, y_packed).  Without ``out`` both are made, and zeroed at
+    their full size, by each call."""
     torch = _torch()
     dt, cur, n = _dt(p), _current(), (p.n_local,)
     wide, tall, i32, bf, u8 = (p.rows_max, p.d), (p.rows_max, p.f), torch.int32, torch.bfloat16, torch.uint8
