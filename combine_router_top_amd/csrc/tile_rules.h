@@ -1,6 +1,7 @@
-// Which kernels a call of the experts, the router's gradients or the 8- and 4-bit products takes: rules on sizes and the number of
-// compute units alone, without device code, so that any host compiler can evaluate
-// them.  The launchers do what a plan says and decide nothing themselves.
+// Which kernels a training call, the router's gradients or an 8- or 4-bit call takes: rules
+// on sizes and the number of compute units alone, without device code, so that any host
+// compiler can evaluate them.  The launchers do what a plan says and decide nothing
+// themselves.
 #pragma once
 
 #include <stdint.h>
